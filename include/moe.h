@@ -34,7 +34,8 @@
  *     recorded in the workspace's status word and read with moe_status_read.
  *   - No call throws across this boundary; all are safe to call from any host thread as
  *     long as concurrent calls use different workspaces and outputs.
- *   - T = 0 (an empty batch) is valid: the call enqueues nothing and returns MOE_OK.
+ *   - T = 0 (an empty batch) is valid: the call enqueues nothing and returns MOE_OK (the
+ *     training calls clear what is summed over the batch).
  *
  * Supported shapes: E <= 1024, k in {1, 2}, k <= E.  MOE_F16 (tensor-core path): d, f and
  * f_res multiples of 128.  MOE_F32 (SIMT path): d and f multiples of 4.  Every pointer
@@ -216,9 +217,9 @@ MOE_API moe_status moe_layer_forward(const void* tokens, const float* Wg, const 
 
 /*
  * Synchronises `stream`, then returns the device-side status word of the most recent
- * moe_expert_ffn / moe_layer_forward call on this workspace (MOE_OK, MOE_ERR_TIMEOUT or
- * MOE_ERR_DEVICE_BOUNDS), or MOE_ERR_CUDA if the synchronisation or the read failed.
- * The word is cleared at the start of each of those calls.
+ * moe_expert_ffn / moe_layer_forward / moe_adapter_forward / moe_adapter_backward call on this
+ * workspace (MOE_OK, MOE_ERR_TIMEOUT or MOE_ERR_DEVICE_BOUNDS), or MOE_ERR_CUDA if the
+ * synchronisation or the read failed.  Each of those calls sets the word anew.
  */
 MOE_API moe_status moe_status_read(const void* workspace, moe_stream_t stream);
 
@@ -253,6 +254,132 @@ MOE_API moe_status moe_set_stage_events(void* const* events, int n_events);
  * difference across a capture is the number of kernels per replay.  Never fails.
  */
 MOE_API unsigned long long moe_kernel_launches(void);
+
+/*
+ * ---- Training the router and low-rank adapters of a layer whose experts stay as they are ----
+ *
+ * The pages have no counterpart of the calls from here to moe_adapter_backward: they are the
+ * gradients of moe_gate_topk and moe_combine, the losses that keep a router balanced, and
+ * low-rank adapters of many requests beside the layer (or any projection of its tokens).
+ * An empty batch (T = 0) is valid for each: outputs with a row per token or slot have none, and
+ * what is summed over the batch (counts, losses, dWg, dA, dB) is written as zeros.
+ * Deterministic: equal calls give equal bits.  All sums are in float32 or wider.
+ */
+
+/* Bytes of workspace of moe_balance_loss.  Host only; writes *bytes. */
+MOE_API moe_status moe_balance_workspace_size(int T, int E, size_t* bytes);
+
+/*
+ * Router losses and per-expert counts of a batch routed by moe_gate_topk:
+ *   p = softmax(logits[t, :]),  n = number of tokens that count,
+ *   counts[e]    = #{(t, j): t counts, topk_idx[t, j] = e}    (before any capacity cut),
+ *   prob_mean[e] = 1/n sum_t p[t, e],
+ *   losses[0]    = E sum_e counts[e] / (n k) prob_mean[e]     (balance; 1 for a uniform router),
+ *   losses[1]    = 1/n sum_t (log sum_e exp logits[t, e])^2   (z).
+ *   logits     [T, E] float32, topk_idx [T, k] int32 (an index outside [0, E) is not counted).
+ *   token_mask nullable [T] bytes: tokens with 0 (padding) do not count; what their rows hold
+ *              (infinities, NaN) has no effect.
+ *   n_valid    [1] int32: n.  n = 0 gives zero losses.
+ * A row of -infinity only adds nothing to prob_mean and to the z loss, but counts in n.
+ *   workspace: moe_balance_workspace_size bytes; contents need no initialisation.
+ */
+MOE_API moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx,
+                                    const uint8_t* token_mask, int T, int E, int k, int32_t* counts,
+                                    float* prob_mean, float* losses, int32_t* n_valid,
+                                    void* workspace, size_t ws_bytes, moe_stream_t stream);
+
+/* Bytes of workspace of moe_gate_topk_backward when it takes the gradient to Wg or the tokens. */
+MOE_API moe_status moe_gate_backward_workspace_size(int T, int d, int E, moe_dtype dtype,
+                                                    size_t* bytes);
+
+/*
+ * Gradient of moe_gate_topk's gate weights and of moe_balance_loss's losses:
+ *   dlogits [T, E] = d/dlogits ( sum dtopk_w . topk_w + dlosses[0] balance + dlosses[1] z ),
+ * with topk_idx and counts held constant, and from it
+ *   dWg [d, E]     = tokens^T dlogits                               (float32),
+ *   dtokens [T, d] = dtokens_in + dlogits Wg^T                      (`dtype`, rounded once).
+ *   logits, topk_idx  as given to / written by moe_gate_topk (indices outside [0, E), or a pair
+ *                     of equal ones, carry no gradient of their weights).
+ *   dtopk_w    nullable [T, k] float32.
+ *   dlosses    nullable [2] float32 (device): gradients of the two losses (their coefficients
+ *              times what comes from above).  With it, counts [E] and n_valid [1] as
+ *              moe_balance_loss wrote them; for a batch spread over several callers, both
+ *              summed over the callers first.  NULL: counts and n_valid are not read.
+ *   token_mask nullable [T]: rows of tokens with 0 are zero (dtokens: dtokens_in).
+ *   dWg nullable (then tokens is not read), dtokens nullable (then Wg is not read), dtokens_in
+ *   nullable (zero; may be dtokens itself).
+ *   workspace: moe_gate_backward_workspace_size bytes; may be NULL when dWg and dtokens are.
+ * Shapes: those of moe_gate_topk, and for dWg / dtokens d a multiple of 8 (MOE_F16) or 4.
+ */
+MOE_API moe_status moe_gate_topk_backward(const float* logits, const int32_t* topk_idx,
+                                          const float* dtopk_w, const float* dlosses,
+                                          const int32_t* counts, const int32_t* n_valid,
+                                          const uint8_t* token_mask, const void* tokens,
+                                          const float* Wg, moe_dtype dtype, int T, int d, int E,
+                                          int k, float* dlogits, float* dWg, const void* dtokens_in,
+                                          void* dtokens, void* workspace, size_t ws_bytes,
+                                          moe_stream_t stream);
+
+/*
+ * Gradient of moe_combine.  For every assignment with s = slot_of[t, j] in [0, S_max):
+ *   dexpert_out[s, :] = topk_w[t, j] dout[t, :]           (`dtype`, rounded once),
+ *   dtopk_w[t, j]     = sum_i dout[t, i] expert_out[s, i] (float32; 0 for a dropped assignment).
+ *   dout [T, d], expert_out and dexpert_out [S_max, d] in `dtype`.  Slots that no assignment
+ *   names are left as they were.  dexpert_out nullable (then topk_w is not read), dtopk_w
+ *   nullable (then expert_out is not read); not both.  residual_in's gradient is dout itself.
+ */
+MOE_API moe_status moe_combine_backward(const void* dout, const void* expert_out,
+                                        const int32_t* slot_of, const float* topk_w, moe_dtype dtype,
+                                        int T, int d, int k, int S_max, void* dexpert_out,
+                                        float* dtopk_w, moe_stream_t stream);
+
+/* Bytes of workspace that moe_adapter_forward and moe_adapter_backward need for this shape. */
+MOE_API moe_status moe_adapter_workspace_size(int T, int d_in, int d_out, int r, int N, int S_max,
+                                              moe_dtype dtype, size_t* bytes);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection.  For every slot s of adapter n
+ * (offsets[n] <= s < offsets[n+1]) and its token t = perm[s]:
+ *   hidden[s, :] = tokens[t, :] A[n]                         (float32),
+ *   out[t, :]    = base[t, :] + scale[n] (hidden[s, :] B[n]) (`dtype`, rounded once).
+ *   perm, offsets: as moe_dispatch writes them for the adapter index of each token in place of
+ *   topk_idx (k = 1, E = N, capacity_factor = +INFINITY); an index outside [0, N) gives a token
+ *   no adapter.  One plan serves every projection of a step.
+ *   tokens [T, d_in], A [N, d_in, r], B [N, r, d_out], base (nullable: zero) and out [T, d_out]
+ *   in `dtype`; scale [N] float32.  base may be out itself (the shared projection's result, in
+ *   place).  Rows of out whose token has no adapter are left as they were.  Otherwise out
+ *   overlaps no input.  A token named by more than one slot gets one of their results.
+ *   hidden nullable [S_max, r] float32, for the backward pass; rows >= offsets[N] are not written.
+ *   Bounds: as moe_expert_ffn's: no slot >= S_max is used, and offsets outside [0, S_max] or
+ *   decreasing and perm entries outside [0, T) are skipped and recorded as
+ *   MOE_ERR_DEVICE_BOUNDS in the workspace's status word.
+ *   workspace: moe_adapter_workspace_size bytes; contents need no initialisation.
+ * Shapes: N <= 1024; r a multiple of 8, at most 128 (adapters of different ranks are padded with
+ * zeros); d_in, d_out multiples of 8 (MOE_F16) or 4 (MOE_F32).
+ */
+MOE_API moe_status moe_adapter_forward(const void* tokens, const int32_t* perm,
+                                       const int32_t* offsets, const void* A, const void* B,
+                                       const float* scale, const void* base, moe_dtype dtype, int T,
+                                       int d_in, int d_out, int r, int N, int S_max, void* out,
+                                       float* hidden, void* workspace, size_t ws_bytes,
+                                       moe_stream_t stream);
+
+/*
+ * Gradient of moe_adapter_forward, with dh[s, :] = dout[perm[s], :] B[n]^T:
+ *   dtokens[t, :] = dtokens_in[t, :] + scale[n] (dh[s, :] A[n]^T)   (`dtype`, rounded once),
+ *   dA[n] = scale[n] sum_s tokens[perm[s], :]^T dh[s, :],   dB[n] = scale[n] sum_s hidden[s, :]^T
+ *   dout[perm[s], :]   (float32 [N, d_in, r] and [N, r, d_out]; zero for an adapter without slots).
+ *   hidden: as moe_adapter_forward wrote it.  dtokens nullable; dtokens_in nullable (zero) and
+ *   may be dtokens itself; dA nullable (then tokens is not read), dB nullable (then hidden is
+ *   not read); not all three.  base's gradient is dout itself.
+ *   Everything else as moe_adapter_forward.
+ */
+MOE_API moe_status moe_adapter_backward(const void* dout, const void* tokens, const float* hidden,
+                                        const int32_t* perm, const int32_t* offsets, const void* A,
+                                        const void* B, const float* scale, const void* dtokens_in,
+                                        moe_dtype dtype, int T, int d_in, int d_out, int r, int N,
+                                        int S_max, void* dtokens, float* dA, float* dB,
+                                        void* workspace, size_t ws_bytes, moe_stream_t stream);
 
 /*
  * Allocation-free variant of moe_expert_ffn (the pages have no counterpart).

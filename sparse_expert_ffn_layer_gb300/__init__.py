@@ -22,7 +22,10 @@ MOE_MLP_STANDARD, MOE_MLP_RESIDUAL = 0, 1
 EXPORTED = ("moe_capacity", "moe_workspace_size", "moe_gate_topk", "moe_dispatch",
             "moe_expert_ffn", "moe_combine", "moe_layer_forward", "moe_status_read",
             "moe_status_string", "moe_selftest_wait", "moe_set_stage_events",
-            "moe_expert_ffn_noalloc", "moe_dispatch_sharded", "moe_kernel_launches")
+            "moe_expert_ffn_noalloc", "moe_dispatch_sharded", "moe_kernel_launches",
+            "moe_balance_workspace_size", "moe_balance_loss", "moe_gate_backward_workspace_size",
+            "moe_gate_topk_backward", "moe_combine_backward", "moe_adapter_workspace_size",
+            "moe_adapter_forward", "moe_adapter_backward")
 
 _lib = None
 MOE_STAGE_EVENTS = 7
@@ -55,6 +58,14 @@ def get_lib():
         "moe_expert_ffn_noalloc": ([P, P, P, P, P, I, I, I, I, I, I, P, P], I),
         "moe_dispatch_sharded": ([P, I, I, I, F, I, P, I, I, P, P, P, P, P, P], I),
         "moe_kernel_launches": ([], ctypes.c_ulonglong),
+        "moe_balance_workspace_size": ([I, I, ctypes.POINTER(S)], I),
+        "moe_balance_loss": ([P, P, P, I, I, I, P, P, P, P, P, S, P], I),
+        "moe_gate_backward_workspace_size": ([I, I, I, I, ctypes.POINTER(S)], I),
+        "moe_gate_topk_backward": ([P, P, P, P, P, P, P, P, P, I, I, I, I, I, P, P, P, P, P, S, P], I),
+        "moe_combine_backward": ([P, P, P, P, I, I, I, I, I, P, P, P], I),
+        "moe_adapter_workspace_size": ([I, I, I, I, I, I, I, ctypes.POINTER(S)], I),
+        "moe_adapter_forward": ([P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, P, P, S, P], I),
+        "moe_adapter_backward": ([P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, P, P, P, S, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -209,3 +220,196 @@ def moe_expert_ffn_noalloc(tokens, perm, offsets, W1, W2, S_max, expert_out, str
                                             _ptr(W2), _dtype(tokens), T, d, f, E, S_max,
                                             _ptr(expert_out), _stream(stream)),
            "moe_expert_ffn_noalloc")
+
+
+# ---------------------------------------------------------------- training and adapters
+def _given(where, dev, **tensors):
+    """Checks name=(tensor or None, dtype, shape) and returns the device all of them are on.
+
+    dtype None: any of the layer's two.  The kernels read dense row-major memory, so anything
+    else is refused here rather than read wrongly."""
+    import torch
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{where}: {name} must be a tensor")
+        if dtype is None:
+            _dtype(t)
+        elif t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+            raise TypeError(f"{where}: {name} is {t.dtype}, expected {dtype}")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous")
+        if dev is not None and t.device != dev:
+            raise ValueError(f"{where}: {name} is on {t.device}, expected {dev}")
+        dev = t.device
+    if dev is not None and dev.type != "cuda":
+        raise ValueError(f"{where}: tensors must be on a CUDA device, not {dev}")
+    return dev
+
+
+def _required(where, **tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{where}: {name} is required")
+
+
+def _ws(workspace):
+    return (_ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
+
+
+def _code(dtype) -> int:
+    """MOE_F32 / MOE_F16 of a torch dtype (or of a code itself)."""
+    if isinstance(dtype, int):
+        return dtype
+    import torch
+    if dtype not in (torch.float16, torch.float32):
+        raise TypeError(f"unsupported dtype {dtype}")
+    return MOE_F16 if dtype == torch.float16 else MOE_F32
+
+
+def _on(dev, stream):
+    """Context with `dev` current, so that the launch and the default stream are that device's."""
+    import torch
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.device(dev)
+
+
+def moe_balance_workspace_size(T, E) -> int:
+    n = ctypes.c_size_t(0)
+    _check(get_lib().moe_balance_workspace_size(T, E, ctypes.byref(n)), "moe_balance_workspace_size")
+    return n.value
+
+
+def moe_balance_loss(logits, topk_idx, counts, prob_mean, losses, n_valid, workspace,
+                     token_mask=None, stream=None):
+    import torch
+    where = "moe_balance_loss"
+    T, E = logits.shape
+    k = topk_idx.shape[1]
+    f32, i32 = torch.float32, torch.int32
+    dev = _given(where, None, logits=(logits, f32, (T, E)), topk_idx=(topk_idx, i32, (T, k)),
+                 counts=(counts, i32, (E,)), prob_mean=(prob_mean, f32, (E,)),
+                 losses=(losses, f32, (2,)), n_valid=(n_valid, i32, (1,)),
+                 workspace=(workspace, torch.uint8, None),
+                 token_mask=(token_mask, (torch.bool, torch.uint8), (T,)))
+    with _on(dev, stream):
+        _check(get_lib().moe_balance_loss(_ptr(logits), _ptr(topk_idx), _ptr(token_mask), T, E, k,
+                                          _ptr(counts), _ptr(prob_mean), _ptr(losses), _ptr(n_valid),
+                                          *_ws(workspace), _stream(stream)), where)
+
+
+def moe_gate_backward_workspace_size(T, d, E, dtype) -> int:
+    n = ctypes.c_size_t(0)
+    _check(get_lib().moe_gate_backward_workspace_size(T, d, E, _code(dtype), ctypes.byref(n)),
+           "moe_gate_backward_workspace_size")
+    return n.value
+
+
+def moe_gate_topk_backward(logits, topk_idx, dlogits, dtopk_w=None, dlosses=None, counts=None,
+                           n_valid=None, token_mask=None, tokens=None, Wg=None, dWg=None,
+                           dtokens=None, dtokens_in=None, workspace=None, stream=None):
+    import torch
+    where = "moe_gate_topk_backward"
+    T, E = logits.shape
+    k = topk_idx.shape[1]
+    f32, i32 = torch.float32, torch.int32
+    if dWg is not None:
+        _required(where, tokens=tokens)
+        d, like = tokens.shape[1], tokens
+    elif dtokens is not None:
+        d, like = dtokens.shape[1], dtokens
+    else:
+        d, like = 8, None
+    if dtokens is not None:
+        _required(where, Wg=Wg)
+    if dlosses is not None:
+        _required(where, counts=counts, n_valid=n_valid)
+    el = like.dtype if like is not None else None
+    dev = _given(where, None, logits=(logits, f32, (T, E)), topk_idx=(topk_idx, i32, (T, k)),
+                 dlogits=(dlogits, f32, (T, E)), dtopk_w=(dtopk_w, f32, (T, k)),
+                 dlosses=(dlosses, f32, (2,)), counts=(counts, i32, (E,)), n_valid=(n_valid, i32, (1,)),
+                 token_mask=(token_mask, (torch.bool, torch.uint8), (T,)),
+                 workspace=(workspace, torch.uint8, None))
+    if like is not None:
+        _given(where, dev, tokens=(tokens if dWg is not None else None, el, (T, d)),
+               Wg=(Wg if dtokens is not None else None, f32, (d, E)), dWg=(dWg, f32, (d, E)),
+               dtokens=(dtokens, el, (T, d)), dtokens_in=(dtokens_in, el, (T, d)))
+    with _on(dev, stream):
+        _check(get_lib().moe_gate_topk_backward(
+            _ptr(logits), _ptr(topk_idx), _ptr(dtopk_w), _ptr(dlosses), _ptr(counts), _ptr(n_valid),
+            _ptr(token_mask), _ptr(tokens), _ptr(Wg), MOE_F32 if like is None else _dtype(like), T, d,
+            E, k, _ptr(dlogits), _ptr(dWg), _ptr(dtokens_in), _ptr(dtokens), *_ws(workspace),
+            _stream(stream)), where)
+
+
+def moe_combine_backward(dout, expert_out, slot_of, topk_w, dexpert_out=None, dtopk_w=None,
+                         stream=None):
+    import torch
+    where = "moe_combine_backward"
+    T, d = dout.shape
+    k = slot_of.shape[1]
+    f32, i32 = torch.float32, torch.int32
+    rows = expert_out if expert_out is not None else dexpert_out
+    S_max = rows.shape[0] if rows is not None else 0
+    dev = _given(where, None, dout=(dout, None, (T, d)), slot_of=(slot_of, i32, (T, k)),
+                 expert_out=(expert_out, dout.dtype, (S_max, d)), topk_w=(topk_w, f32, (T, k)),
+                 dexpert_out=(dexpert_out, dout.dtype, (S_max, d)), dtopk_w=(dtopk_w, f32, (T, k)))
+    with _on(dev, stream):
+        _check(get_lib().moe_combine_backward(_ptr(dout), _ptr(expert_out), _ptr(slot_of), _ptr(topk_w),
+                                              _dtype(dout), T, d, k, S_max, _ptr(dexpert_out),
+                                              _ptr(dtopk_w), _stream(stream)), where)
+
+
+def moe_adapter_workspace_size(T, d_in, d_out, r, N, S_max, dtype) -> int:
+    n = ctypes.c_size_t(0)
+    _check(get_lib().moe_adapter_workspace_size(T, d_in, d_out, r, N, S_max, _code(dtype),
+                                                ctypes.byref(n)), "moe_adapter_workspace_size")
+    return n.value
+
+
+def moe_adapter_forward(tokens, perm, offsets, A, B, scale, out, workspace, base=None, hidden=None,
+                        stream=None):
+    """out[t] = base[t] + scale[n] (tokens[t] A[n]) B[n] for every slot of perm / offsets."""
+    import torch
+    where = "moe_adapter_forward"
+    T, d_in = tokens.shape
+    N, _, r = A.shape
+    d_out = B.shape[2]
+    S_max = perm.shape[0]
+    el, f32, i32 = tokens.dtype, torch.float32, torch.int32
+    dev = _given(where, None, tokens=(tokens, None, (T, d_in)), perm=(perm, i32, (S_max,)),
+                 offsets=(offsets, i32, (N + 1,)), A=(A, el, (N, d_in, r)), B=(B, el, (N, r, d_out)),
+                 scale=(scale, f32, (N,)), out=(out, el, (T, d_out)), base=(base, el, (T, d_out)),
+                 hidden=(hidden, f32, (S_max, r)), workspace=(workspace, torch.uint8, None))
+    with _on(dev, stream):
+        _check(get_lib().moe_adapter_forward(_ptr(tokens), _ptr(perm), _ptr(offsets), _ptr(A), _ptr(B),
+                                             _ptr(scale), _ptr(base), _dtype(tokens), T, d_in, d_out, r,
+                                             N, S_max, _ptr(out), _ptr(hidden), *_ws(workspace),
+                                             _stream(stream)), where)
+
+
+def moe_adapter_backward(dout, tokens, hidden, perm, offsets, A, B, scale, workspace, dtokens=None,
+                         dtokens_in=None, dA=None, dB=None, stream=None):
+    """Gradients of moe_adapter_forward: dtokens (added to dtokens_in), dA and dB in float32."""
+    import torch
+    where = "moe_adapter_backward"
+    T, d_out = dout.shape
+    N, d_in, r = A.shape
+    S_max = perm.shape[0]
+    el, f32, i32 = dout.dtype, torch.float32, torch.int32
+    dev = _given(where, None, dout=(dout, None, (T, d_out)), tokens=(tokens, el, (T, d_in)),
+                 hidden=(hidden, f32, (S_max, r)), perm=(perm, i32, (S_max,)),
+                 offsets=(offsets, i32, (N + 1,)), A=(A, el, (N, d_in, r)), B=(B, el, (N, r, d_out)),
+                 scale=(scale, f32, (N,)), dtokens=(dtokens, el, (T, d_in)),
+                 dtokens_in=(dtokens_in, el, (T, d_in)), dA=(dA, f32, (N, d_in, r)),
+                 dB=(dB, f32, (N, r, d_out)), workspace=(workspace, torch.uint8, None))
+    with _on(dev, stream):
+        _check(get_lib().moe_adapter_backward(_ptr(dout), _ptr(tokens), _ptr(hidden), _ptr(perm),
+                                              _ptr(offsets), _ptr(A), _ptr(B), _ptr(scale),
+                                              _ptr(dtokens_in), _dtype(dout), T, d_in, d_out, r, N,
+                                              S_max, _ptr(dtokens), _ptr(dA), _ptr(dB), *_ws(workspace),
+                                              _stream(stream)), where)

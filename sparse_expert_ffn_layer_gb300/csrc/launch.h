@@ -180,6 +180,33 @@ cudaError_t launch_finalize(const float* acc32, const float* r32, int T, int d, 
 cudaError_t launch_combine(const void* expert_out, const int32_t* slot_of, const float* topk_w,
                            const void* residual_in, int dtype_f16, int T, int d, int k, void* out,
                            cudaStream_t s);
+// Router losses and the logits' gradient (router_loss.cu).
+size_t balance_records_bytes(int E);
+cudaError_t launch_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* mask,
+                                int T, int E, int k, int32_t* counts, float* prob_mean,
+                                float* losses, int32_t* n_valid, float* records, cudaStream_t s);
+cudaError_t launch_dlogits(const float* logits, const int32_t* topk_idx, const float* dtopk_w,
+                           const float* dlosses, const int32_t* counts, const int32_t* n_valid,
+                           const uint8_t* mask, int T, int E, int k, float* dlogits,
+                           cudaStream_t s);
+// Sums over token rows for up to two jobs G[n][i][j] = scale_n sum_s x[row(s)][i] h[s][j]
+// (transposed: G[n][j][i]); G0 or G1 may be null (grad.cu).
+cudaError_t launch_row_sums(const void* x0, const float* h0, float* G0, int di0, int dj0, int tr0,
+                            const void* x1, const float* h1, float* G1, int di1, int dj1, int tr1,
+                            const float* scale, const int32_t* perm, const int32_t* offsets,
+                            const uint8_t* mask, int dtype_f16, int T, int S_max, int N,
+                            cudaStream_t s);
+cudaError_t launch_gate_dx(const float* dlogits, const float* Wg, const void* in, int dtype_f16, int T,
+                           int d, int E, void* out, cudaStream_t s);
+cudaError_t launch_combine_backward(const void* dout, const void* expert_out, const int32_t* slot_of,
+                                    const float* topk_w, int dtype_f16, int T, int d, int k, int S_max,
+                                    void* dexpert_out, float* dtopk_w, cudaStream_t s);
+// Low-rank adapters (adapter.cu): y[t] = base[t] + scale_n (x[t] P_n) Q_n; transposed: P, Q are
+// given as [N, r, dk] and [N, dn, r].  hidden [S_max, r] receives x P when not null.
+cudaError_t launch_adapter(const void* x, const void* P, const void* Q, const void* base, void* y,
+                           float* hidden, const float* scale, const int32_t* perm,
+                           const int32_t* offsets, int* status, int dtype_f16, bool transposed,
+                           int T, int dk, int dn, int r, int N, int S_max, cudaStream_t s);
 cudaError_t launch_selftest_wait(int* status, uint64_t timeout_ns, cudaStream_t s);
 // split-K reductions (fixed chunk order): first GEMM -> GeLU -> H / Hres; second GEMM -> the
 // combine of the given mode / r32

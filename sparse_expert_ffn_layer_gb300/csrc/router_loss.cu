@@ -1,0 +1,497 @@
+// Router losses over the gate's logits, and the gradient of the logits.
+//
+//   p = softmax(x_t),  lse_t = log sum_e exp(x_te),  n = tokens that count
+//   counts[e] = #{(t, j): token t counts, topk_idx[t,j] = e},   P[e] = 1/n sum_t p_te
+//   balance = E sum_e counts[e] / (n k) P[e],   z = 1/n sum_t lse_t^2
+//
+//   dx_te = p_te (a_e - sum_e' a_e' p_te') + 2 g_z / n lse_t p_te       (tokens that count)
+//         + gradient of the gate weights at the chosen experts  (0 for tokens that do not count),
+//   a_e = g_balance E counts[e] / (n^2 k)
+//
+// Both are one pass over [T, E] in 32 bits, bound by DRAM (4 bytes read per element, 4 more
+// written by the gradient).  A row is held in registers by LANES lanes with 16 (E > 512: 32)
+// values each, so that a warp has 64 bytes per lane in flight and a row's reductions are
+// log2(LANES) shuffles instead of five; the columns of a lane never change, so column sums
+// (forward) and a_e (backward) stay in registers too.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "launch.h"
+
+namespace cg = cooperative_groups;
+
+namespace moe {
+namespace {
+
+constexpr int kRowThreads = 512;
+constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kCluster = 8;
+constexpr int kFinalThreads = 1024;
+
+template <int LANES>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+template <int LANES>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Element e of value (j, v) in lane l of a row's group.
+template <int LANES, int VEC>
+__device__ __forceinline__ int col_of(int j, int l) { return (j * LANES + l) * VEC; }
+
+// One row's values (columns beyond E and rows that do not count: -inf).
+template <int LANES, int VEC, int J>
+__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, int l, bool on,
+                                         float (&x)[VEC * J]) {
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int c = col_of<LANES, VEC>(j, l);
+    if (on && c < E) {
+      if (VEC == 4) {
+        const float4 q = *reinterpret_cast<const float4*>(row + c);
+        x[4 * j + 0] = q.x; x[4 * j + 1] = q.y; x[4 * j + 2] = q.z; x[4 * j + 3] = q.w;
+      } else {
+        x[j] = row[c];
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) x[VEC * j + v] = -INFINITY;
+    }
+  }
+}
+
+// Softmax in place: x becomes p; returns lse.  A row of -inf only has p = 0 and lse = 0 (it
+// adds nothing to either loss); NaN and +inf give NaN as the formula does.
+template <int LANES, int N>
+__device__ __forceinline__ float softmax_row(float (&x)[N]) {
+  float m = x[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
+  m = group_max<LANES>(m);
+  if (m == -INFINITY) m = 0.f;
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] = expf(x[i] - m);
+    s += x[i];
+  }
+  s = group_sum<LANES>(s);
+  const bool empty = s == 0.f;
+  const float inv = empty ? 0.f : 1.f / s;
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] *= inv;
+  return empty ? 0.f : m + logf(s);
+}
+
+// Sum of v over the block, in a fixed order; the result is valid in thread 0.
+__device__ __forceinline__ float block_sum(float v, float* scratch) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float r = 0.f;
+  if (threadIdx.x == 0)
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) r += scratch[w];
+  return r;
+}
+
+struct LossOut {
+  int32_t* counts;
+  float* prob_mean;
+  float* losses;
+  int32_t* n_valid;
+};
+
+// Per-block partial sums, one record per block: probability sums [E], counts [E], then the sum
+// of lse^2 and the number of tokens.
+__host__ __device__ inline size_t record_words(int E) { return 2 * (size_t)E + 4; }
+
+// Joins nb records (rec(b) is record b) into the outputs.  Runs in one cluster of kCluster
+// blocks: block c owns the columns [c Ec, (c + 1) Ec); its threads sum each column in
+// blockDim / Ec parts, always in the same order, and rank 0 adds the blocks' shares of the
+// balance loss through distributed shared memory.
+template <typename Rec>
+__device__ __forceinline__ void join_records(Rec rec, int nb, int E, int k, LossOut o, float* sh_f,
+                                             int* sh_i, float* share) {
+  cg::cluster_group cl = cg::this_cluster();
+  const int c = (int)cl.block_rank();
+  const int Ec = (E + kCluster - 1) / kCluster;
+  const int parts = max(1, (int)blockDim.x / Ec);
+  const int col = threadIdx.x % Ec, part = threadIdx.x / Ec;
+  const int e = c * Ec + col;
+  float ps = 0.f;
+  int cs = 0, n = 0;
+  if (part < parts && e < E) {
+#pragma unroll 8
+    for (int b = part; b < nb; b += parts) {
+      const float* r = rec(b);
+      ps += r[e];
+      cs += __float_as_int(r[E + e]);
+    }
+  }
+  // every block needs n; only rank 0 needs the sum of lse^2
+  float z = 0.f;
+  for (int b = threadIdx.x; b < nb; b += blockDim.x) {
+    const float* r = rec(b);
+    z += r[2 * E];
+    n += __float_as_int(r[2 * E + 1]);
+  }
+  if (part < parts) {
+    sh_f[threadIdx.x] = ps;
+    sh_i[threadIdx.x] = cs;
+  }
+  __shared__ int n_sh;
+  __shared__ float scratch[kFinalThreads / 32];
+  if (threadIdx.x == 0) n_sh = 0;
+  __syncthreads();
+  if (n) atomicAdd(&n_sh, n);
+  z = block_sum(z, scratch);                        // its barriers publish n_sh and sh_*
+  const float nf = (float)max(n_sh, 1);
+  float mine = 0.f;
+  if (threadIdx.x < (unsigned)Ec && e < E) {
+    float p = 0.f;
+    int cnt = 0;
+    for (int q = 0; q < parts; ++q) {
+      p += sh_f[q * Ec + col];
+      cnt += sh_i[q * Ec + col];
+    }
+    p /= nf;
+    o.prob_mean[e] = p;
+    o.counts[e] = cnt;
+    mine = (float)cnt * p;
+  }
+  mine = block_sum(mine, scratch);
+  if (threadIdx.x == 0) cl.map_shared_rank(share, 0)[c] = mine;
+  cl.sync();
+  if (c == 0 && threadIdx.x == 0) {
+    float s = 0.f;
+    for (int q = 0; q < kCluster; ++q) s += share[q];
+    o.losses[0] = (float)E * (s / (nf * (float)k));
+    o.losses[1] = z / nf;
+    *o.n_valid = n_sh;
+  }
+}
+
+// kOne: the grid is one cluster, which keeps its records in shared memory and joins them itself
+// (small batches: one launch).  Otherwise records go to the workspace and balance_join_kernel
+// follows.
+template <int LANES, int VEC, int J, bool kOne>
+__global__ void __launch_bounds__(kRowThreads, 2) balance_rows_kernel(
+    const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
+    const uint8_t* __restrict__ mask, int T, int E, int k, float* __restrict__ records, LossOut o) {
+  constexpr int V = VEC * J;
+  constexpr int RPW = 32 / LANES;
+  extern __shared__ float sm[];
+  float* red = sm;                                            // [kRowWarps][E]
+  int* hist = reinterpret_cast<int*>(sm + kRowWarps * E);     // [E]
+  float* rec_s = sm + (kRowWarps + 1) * E;                    // kOne: this block's record
+  __shared__ float zs[kRowWarps];
+  __shared__ int ns[kRowWarps];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int l = lane % LANES, g = lane / LANES;
+  for (int e = threadIdx.x; e < E; e += kRowThreads) hist[e] = 0;
+  __syncthreads();
+  float acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+  float z = 0.f;
+  int n = 0;
+  const int64_t stride = (int64_t)gridDim.x * kRowWarps * RPW;
+  for (int64_t base = ((int64_t)blockIdx.x * kRowWarps + w) * RPW; base < T; base += stride) {
+    const int64_t t = base + g;
+    const bool on = t < T && (!mask || mask[t]);
+    float x[V];
+    load_row<LANES, VEC, J>(logits + (size_t)t * E, E, l, on, x);
+    if (on && l < k) {                                        // k <= 2 <= LANES unless E is tiny
+      for (int j = l; j < k; j += LANES) {
+        const int e = topk_idx[(size_t)t * k + j];
+        if ((unsigned)e < (unsigned)E) atomicAdd(&hist[e], 1);
+      }
+    }
+    const float lse = softmax_row<LANES>(x);                  // all zero for a row that is off
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] += x[i];
+    if (on && l == 0) {
+      z += lse * lse;
+      n += 1;
+    }
+  }
+  // rows of a warp, then warps, in a fixed order
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int s = LANES; s < 32; s <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], s);
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    z += __shfl_xor_sync(0xffffffffu, z, s);
+    n += __shfl_xor_sync(0xffffffffu, n, s);
+  }
+  if (g == 0) {
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const int e = col_of<LANES, VEC>(j, l) + v;
+        if (e < E) red[w * E + e] = acc[VEC * j + v];
+      }
+  }
+  if (lane == 0) {
+    zs[w] = z;
+    ns[w] = n;
+  }
+  __syncthreads();
+  float* rec = kOne ? rec_s : records + (size_t)blockIdx.x * record_words(E);
+  for (int e = threadIdx.x; e < E; e += kRowThreads) {
+    float s = 0.f;
+    for (int q = 0; q < kRowWarps; ++q) s += red[q * E + e];
+    rec[e] = s;
+    rec[E + e] = __int_as_float(hist[e]);
+  }
+  if (threadIdx.x == 0) {
+    float zz = 0.f;
+    int nn = 0;
+    for (int q = 0; q < kRowWarps; ++q) {
+      zz += zs[q];
+      nn += ns[q];
+    }
+    rec[2 * E] = zz;
+    rec[2 * E + 1] = __int_as_float(nn);
+  }
+  if (kOne) {
+    __shared__ float sh_f[kRowThreads];
+    __shared__ int sh_i[kRowThreads];
+    __shared__ float share[kCluster];
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();                                      // every block's record is complete
+    join_records([&](int b) { return (const float*)cl.map_shared_rank(rec_s, b); }, kCluster, E, k,
+                 o, sh_f, sh_i, share);
+    // its last cluster barrier is behind every read of another block's record
+  } else {
+    pdl_trigger();
+  }
+}
+
+__global__ void __launch_bounds__(kFinalThreads) balance_join_kernel(
+    const float* __restrict__ records, int nb, int E, int k, LossOut o) {
+  __shared__ float sh_f[kFinalThreads];
+  __shared__ int sh_i[kFinalThreads];
+  __shared__ float share[kCluster];
+  pdl_wait();
+  const size_t words = record_words(E);
+  join_records([&](int b) { return records + b * words; }, nb, E, k, o, sh_f, sh_i, share);
+}
+
+// Gradient of the logits, one row per group of lanes.  Rows are taken from the last to the
+// first: right after moe_balance_loss the rows that it read last are still in L2.
+template <int LANES, int VEC, int J>
+__global__ void __launch_bounds__(256) dlogits_kernel(
+    const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
+    const float* __restrict__ dtopk_w, const float* __restrict__ dlosses,
+    const int32_t* __restrict__ counts, const int32_t* __restrict__ n_valid,
+    const uint8_t* __restrict__ mask, int T, int E, int k, float* __restrict__ dlogits) {
+  constexpr int V = VEC * J;
+  constexpr int RPW = 32 / LANES;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int l = lane % LANES, g = lane / LANES;
+  float a[V];
+  float gz = 0.f;
+  if (dlosses) {
+    const float n = (float)max(*n_valid, 1);
+    const float cb = dlosses[0] * (float)E / (n * (float)k) / n;
+    gz = 2.f * dlosses[1] / n;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const int e = col_of<LANES, VEC>(j, l) + v;
+        a[VEC * j + v] = e < E ? cb * (float)counts[e] : 0.f;
+      }
+  }
+  const int64_t stride = (int64_t)gridDim.x * 8 * RPW;
+  for (int64_t base = ((int64_t)blockIdx.x * 8 + w) * RPW; base < T; base += stride) {
+    const int64_t t = T - 1 - (base + g);
+    const bool in = t >= 0;
+    const bool on = in && (!mask || mask[t]);
+    float x[V];
+    load_row<LANES, VEC, J>(logits + (on ? t : 0) * E, E, l, on, x);
+    float top[2] = {0.f, 0.f}, dw[2] = {0.f, 0.f};
+    int idx[2] = {-1, -1};
+    if (dtopk_w && on) {
+      for (int j = 0; j < k; ++j) {
+        const int e = topk_idx[(size_t)t * k + j];
+        if ((unsigned)e < (unsigned)E) {
+          idx[j] = e;
+          top[j] = logits[(size_t)t * E + e];
+          dw[j] = dtopk_w[(size_t)t * k + j];
+        }
+      }
+    }
+    const float lse = softmax_row<LANES>(x);                 // x is p now
+    float bar = 0.f;
+    if (dlosses) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) bar += a[i] * x[i];
+    }
+    bar = group_sum<LANES>(bar);
+    // top-1: w = p[e1];  top-2: w_j = p[e_j] / (p[e1] + p[e2]), a softmax over the two logits
+    float add[2] = {0.f, 0.f}, minus = 0.f;
+    if (dtopk_w) {
+      if (k == 1) {
+        // a row of -inf only has no weight to differentiate (p = 0 there)
+        const float p1 = idx[0] < 0 || top[0] == -INFINITY ? 0.f : expf(top[0] - lse);
+        add[0] = p1 * dw[0];
+        minus = add[0];
+      } else if (idx[0] >= 0 && idx[1] >= 0 && idx[0] != idx[1] &&
+                 !(top[0] == -INFINITY && top[1] == -INFINITY)) {
+        const float hi = fmaxf(top[0], top[1]);
+        const float e0 = expf(top[0] - hi), e1 = expf(top[1] - hi);
+        const float inv = 1.f / (e0 + e1);
+        add[0] = (e0 * inv) * (e1 * inv) * (dw[0] - dw[1]);
+        add[1] = -add[0];
+      }
+    }
+    const float c0 = gz * lse - bar;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int c = col_of<LANES, VEC>(j, l);
+      if (!in || c >= E) continue;
+      float q[VEC];
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const float p = x[VEC * j + v];
+        float r = dlosses ? p * (a[VEC * j + v] + c0) : 0.f;
+        if (dtopk_w) {
+          r -= p * minus;
+          if (c + v == idx[0]) r += add[0];
+          if (c + v == idx[1]) r += add[1];
+        }
+        q[v] = r;
+      }
+      float* dst = dlogits + (size_t)t * E + c;
+      if (VEC == 4)
+        *reinterpret_cast<float4*>(dst) = make_float4(q[0], q[1 % VEC], q[2 % VEC], q[3 % VEC]);
+      else
+        dst[0] = q[0];
+    }
+  }
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return sms;
+}
+
+// Lanes per row: 16 values per lane up to 512 experts, 32 above; four-wide accesses where a
+// row's length allows them.
+template <typename F>
+cudaError_t with_shape(int E, F f) {
+  auto pick = [&](auto vec) -> cudaError_t {
+    constexpr int VEC = decltype(vec)::value;
+    constexpr int J = 16 / VEC;
+    using std::integral_constant;
+    if (E <= 16) return f(integral_constant<int, 1>(), vec, integral_constant<int, J>());
+    if (E <= 32) return f(integral_constant<int, 2>(), vec, integral_constant<int, J>());
+    if (E <= 64) return f(integral_constant<int, 4>(), vec, integral_constant<int, J>());
+    if (E <= 128) return f(integral_constant<int, 8>(), vec, integral_constant<int, J>());
+    if (E <= 256) return f(integral_constant<int, 16>(), vec, integral_constant<int, J>());
+    if (E <= 512) return f(integral_constant<int, 32>(), vec, integral_constant<int, J>());
+    return f(integral_constant<int, 32>(), vec, integral_constant<int, 2 * J>());
+  };
+  return E % 4 == 0 ? pick(std::integral_constant<int, 4>()) : pick(std::integral_constant<int, 1>());
+}
+
+int lanes_for(int E) {
+  int lanes = 1;
+  while (lanes < 32 && lanes * 16 < E) lanes <<= 1;
+  return lanes;
+}
+
+// Blocks of the row pass: two per SM, fewer for short batches.
+constexpr int kMaxRecords = 512;
+int row_blocks(int T, int E, int sms) {
+  const int rows = kRowWarps * (32 / lanes_for(E));
+  return std::max(1, std::min({(T + rows - 1) / rows, 2 * sms, kMaxRecords}));
+}
+
+// Up to this many logits one cluster does the whole call.
+constexpr long long kOneClusterElems = 256 * 1024;
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), int grid, int block, size_t smem,
+                           cudaStream_t s, bool pdl, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+  if (err == cudaSuccess) launch_counter().fetch_add(1, std::memory_order_relaxed);
+  return err;
+}
+
+}  // namespace
+
+size_t balance_records_bytes(int E) { return sizeof(float) * kMaxRecords * record_words(E); }
+
+cudaError_t launch_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* mask,
+                                int T, int E, int k, int32_t* counts, float* prob_mean,
+                                float* losses, int32_t* n_valid, float* records, cudaStream_t s) {
+  const int sms = sm_count();
+  if (sms < 1) return cudaErrorInvalidDevice;
+  const LossOut o{counts, prob_mean, losses, n_valid};
+  const bool one = (long long)T * E <= kOneClusterElems;
+  const int blocks = one ? kCluster : row_blocks(T, E, sms);
+  const size_t smem = sizeof(float) * ((size_t)(kRowWarps + 1) * E + (one ? record_words(E) : 0));
+  return with_shape(E, [&](auto lanes, auto vec, auto j) -> cudaError_t {
+    constexpr int L = decltype(lanes)::value, V = decltype(vec)::value, J = decltype(j)::value;
+    if (one) {
+      auto kern = balance_rows_kernel<L, V, J, true>;
+      MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
+      return launch_cluster(kern, blocks, kRowThreads, smem, s, false, logits, topk_idx, mask, T, E,
+                            k, records, o);
+    }
+    auto kern = balance_rows_kernel<L, V, J, false>;
+    MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
+    MOE_LAUNCH(launch_k(kern, blocks, kRowThreads, smem, s, false, logits, topk_idx, mask, T, E, k,
+                        records, o));
+    return launch_cluster(balance_join_kernel, kCluster, kFinalThreads, 0, s, true,
+                          (const float*)records, blocks, E, k, o);
+  });
+}
+
+cudaError_t launch_dlogits(const float* logits, const int32_t* topk_idx, const float* dtopk_w,
+                           const float* dlosses, const int32_t* counts, const int32_t* n_valid,
+                           const uint8_t* mask, int T, int E, int k, float* dlogits,
+                           cudaStream_t s) {
+  const int sms = sm_count();
+  if (sms < 1) return cudaErrorInvalidDevice;
+  const int rows = 8 * (32 / lanes_for(E));
+  const int grid = std::max(1, std::min((T + rows - 1) / rows, 8 * sms));
+  return with_shape(E, [&](auto lanes, auto vec, auto j) -> cudaError_t {
+    constexpr int L = decltype(lanes)::value, V = decltype(vec)::value, J = decltype(j)::value;
+    return launch_k(dlogits_kernel<L, V, J>, grid, 256, 0, s, false, logits, topk_idx, dtopk_w,
+                    dlosses, counts, n_valid, mask, T, E, k, dlogits);
+  });
+}
+
+}  // namespace moe

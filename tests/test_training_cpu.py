@@ -1,0 +1,145 @@
+"""Training and adapter calls on the CPU: workspace sizes and refusals.  Every call returns before
+any CUDA work is enqueued."""
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def m():
+    from sparse_expert_ffn_layer_gb300 import _build
+    _build.build()
+    import sparse_expert_ffn_layer_gb300 as mod
+    return mod
+
+
+P = ctypes.c_void_p(0x10000)       # never dereferenced: every call below fails its host checks
+ODD = ctypes.c_void_p(0x10002)
+S0 = ctypes.c_void_p(0)
+
+
+def test_workspace_sizes(m):
+    assert m.moe_balance_workspace_size(64, 8) % 256 == 0
+    assert m.moe_balance_workspace_size(1 << 20, 1024) >= 4 * 2 * 1024 * 2 * 148
+    # room for the status word and dh [S_max, r]
+    for r in (8, 16, 128):
+        assert m.moe_adapter_workspace_size(100, 64, 64, r, 4, 100, torch.float16) >= 256 + 400 * r
+    assert m.moe_adapter_workspace_size(0, 64, 64, 8, 4, 0, m.MOE_F32) >= 256
+    assert m.moe_gate_backward_workspace_size(64, 128, 8, torch.float16) >= 256
+    for args, code in [((-1, 8), 1), ((4, 0), 1), ((4, 1025), 2), ((1 << 22, 1024), 2)]:
+        with pytest.raises(m.MoeError) as e:
+            m.moe_balance_workspace_size(*args)
+        assert e.value.code == code
+    for args, code in [((8, 100, 64, 8, 4, 8, torch.float16), 2), ((8, 64, 100, 8, 4, 8, torch.float16), 2),
+                       ((8, 64, 64, 12, 4, 8, torch.float16), 2), ((8, 64, 64, 136, 4, 8, torch.float16), 2),
+                       ((8, 64, 64, 8, 1025, 8, torch.float16), 2), ((8, 64, 66, 8, 4, 8, torch.float32), 2),
+                       ((8, 64, 64, 0, 4, 8, torch.float16), 1), ((8, 64, 64, 8, 0, 8, torch.float16), 1),
+                       ((8, 64, 64, 8, 4, -1, torch.float16), 1), ((8, 64, 64, 8, 4, 8, 7), 1)]:
+        with pytest.raises(m.MoeError) as e:
+            m.moe_adapter_workspace_size(*args)
+        assert e.value.code == code
+    with pytest.raises(m.MoeError):
+        m.moe_gate_backward_workspace_size(8, 100, 8, torch.float16)
+    with pytest.raises(TypeError):
+        m.moe_adapter_workspace_size(8, 64, 64, 8, 4, 8, torch.bfloat16)
+
+
+def test_balance_and_gate_refusals(m):
+    f = m.lib.moe_balance_loss
+
+    def bal(logits=P, idx=P, T=8, E=4, k=1, counts=P, pm=P, losses=P, nv=P, ws=P, n=1 << 24):
+        return f(logits, idx, None, T, E, k, counts, pm, losses, nv, ws, n, S0)
+    assert bal(k=3) == bal(k=2, E=1) == bal(T=-1) == bal(E=0) == m.MOE_ERR_INVALID_ARG
+    assert bal(logits=None) == bal(idx=None) == bal(counts=None) == bal(losses=None) == \
+        bal(pm=None) == bal(nv=None) == m.MOE_ERR_INVALID_ARG
+    assert bal(E=1025) == bal(T=1 << 28, E=1000) == bal(logits=ODD) == m.MOE_ERR_UNSUPPORTED
+    assert bal(ws=None) == bal(n=100) == m.MOE_ERR_WORKSPACE
+    g = m.lib.moe_gate_topk_backward
+
+    def gate(logits=P, idx=P, dw=P, dl=P, counts=P, nv=P, mask=None, x=P, Wg=P, dt=1, T=8, d=64, E=4,
+             k=1, dlogits=P, dWg=P, din=None, dx=P, ws=P, n=1 << 24):
+        return g(logits, idx, dw, dl, counts, nv, mask, x, Wg, dt, T, d, E, k, dlogits, dWg, din, dx,
+                 ws, n, S0)
+    inv = m.MOE_ERR_INVALID_ARG
+    assert gate(dw=None, dl=None) == inv                       # nothing to differentiate
+    assert gate(counts=None) == gate(nv=None) == gate(dlogits=None) == inv
+    assert gate(x=None) == gate(Wg=None) == gate(dt=5) == gate(d=0) == inv
+    assert gate(dx=None, din=P) == inv
+    assert gate(d=68) == gate(dt=0, d=66) == gate(x=ODD) == m.MOE_ERR_UNSUPPORTED
+    assert gate(ws=None) == gate(n=8) == m.MOE_ERR_WORKSPACE
+    assert gate(T=0, dWg=None) == m.MOE_OK
+
+
+def test_combine_backward_refusals(m):
+    f = m.lib.moe_combine_backward
+
+    def comb(dout=P, y=P, slot=P, w=P, dt=1, T=8, d=64, k=1, S=8, dy=P, dw=P):
+        return f(dout, y, slot, w, dt, T, d, k, S, dy, dw, S0)
+    inv = m.MOE_ERR_INVALID_ARG
+    assert comb(dy=None, dw=None) == comb(dout=None) == comb(slot=None) == inv
+    assert comb(w=None) == comb(y=None) == comb(k=3) == comb(dt=9) == comb(S=-1) == comb(d=0) == inv
+    assert comb(dout=ODD) == comb(y=ODD) == m.MOE_ERR_UNSUPPORTED
+    assert comb(T=0) == m.MOE_OK
+
+
+def test_adapter_refusals(m):
+    f, b = m.lib.moe_adapter_forward, m.lib.moe_adapter_backward
+
+    def fwd(x=P, perm=P, off=P, A=P, B=P, sc=P, base=None, dt=1, T=8, di=64, do=64, r=8, N=4, S=8, out=P,
+            hid=None, ws=P, n=1 << 20):
+        return f(x, perm, off, A, B, sc, base, dt, T, di, do, r, N, S, out, hid, ws, n, S0)
+    inv, uns = m.MOE_ERR_INVALID_ARG, m.MOE_ERR_UNSUPPORTED
+    assert fwd(x=None) == fwd(perm=None) == fwd(off=None) == fwd(A=None) == fwd(sc=None) == inv
+    assert fwd(out=None) == fwd(T=-1) == fwd(S=-1) == fwd(r=0) == fwd(N=0) == fwd(dt=3) == inv
+    assert fwd(di=60) == fwd(do=4) == fwd(r=12) == fwd(r=136) == fwd(N=1025) == uns
+    assert fwd(x=ODD) == fwd(base=ODD) == fwd(hid=ODD) == fwd(off=ODD) == uns
+    assert fwd(ws=None) == fwd(n=256) == m.MOE_ERR_WORKSPACE
+    assert fwd(T=0) == fwd(S=0) == m.MOE_OK
+
+    def bwd(dy=P, x=P, hid=P, perm=P, off=P, A=P, B=P, sc=P, din=None, dt=1, T=8, di=64, do=64, r=8,
+            N=4, S=8, dx=P, dA=P, dB=P, ws=P, n=1 << 20):
+        return b(dy, x, hid, perm, off, A, B, sc, din, dt, T, di, do, r, N, S, dx, dA, dB, ws, n, S0)
+    assert bwd(dx=None, dA=None, dB=None) == bwd(x=None) == bwd(hid=None) == bwd(dy=None) == inv
+    assert bwd(dx=None, din=P) == bwd(A=None) == inv
+    assert bwd(dA=ODD) == bwd(di=60) == uns
+    assert bwd(n=256) == m.MOE_ERR_WORKSPACE
+    assert bwd(T=0, dA=None, dB=None) == m.MOE_OK
+
+
+def test_binding_refuses_what_the_kernels_would_misread(m):
+    T, d, r, N = 4, 16, 8, 2
+    x, out = torch.zeros(T, d, dtype=torch.float16), torch.zeros(T, d, dtype=torch.float16)
+    perm, off = torch.zeros(T, dtype=torch.int32), torch.zeros(N + 1, dtype=torch.int32)
+    A, B = torch.zeros(N, d, r, dtype=torch.float16), torch.zeros(N, r, d, dtype=torch.float16)
+    sc, ws = torch.zeros(N), torch.zeros(1 << 16, dtype=torch.uint8)
+
+    def fwd(**kw):
+        a = dict(tokens=x, perm=perm, offsets=off, A=A, B=B, scale=sc, out=out, workspace=ws)
+        a.update(kw)
+        return m.moe_adapter_forward(**a)
+    with pytest.raises(ValueError, match="CUDA device"):
+        fwd()
+    with pytest.raises(TypeError, match="perm"):
+        fwd(perm=perm.long())
+    with pytest.raises(ValueError, match="B has shape"):
+        fwd(B=torch.zeros(N, r + 1, d, dtype=torch.float16))
+    with pytest.raises(TypeError, match="A is"):
+        fwd(A=A.float())
+    with pytest.raises(ValueError, match="contiguous"):
+        fwd(tokens=torch.zeros(d, T, dtype=torch.float16).t())
+    with pytest.raises(ValueError, match="offsets has shape"):
+        fwd(offsets=off[:N].contiguous())
+    with pytest.raises(TypeError, match="unsupported dtype"):
+        fwd(tokens=x.bfloat16(), A=A.bfloat16(), B=B.bfloat16(), out=out.bfloat16())
+    logits, idx = torch.zeros(T, 4), torch.zeros(T, 1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="counts is required"):
+        m.moe_gate_topk_backward(logits, idx, logits, dlosses=torch.zeros(2))
+    with pytest.raises(ValueError, match="tokens is required"):
+        m.moe_gate_topk_backward(logits, idx, logits, dtopk_w=torch.zeros(T, 1), dWg=torch.zeros(d, 4))
+    with pytest.raises(TypeError, match="token_mask"):
+        m.moe_balance_loss(logits, idx, torch.zeros(4, dtype=torch.int32), torch.zeros(4), torch.zeros(2),
+                           torch.zeros(1, dtype=torch.int32), ws, token_mask=torch.zeros(T))
+    with pytest.raises(ValueError, match="expert_out has shape"):
+        m.moe_combine_backward(x, torch.zeros(T, d + 1, dtype=torch.float16), idx, torch.zeros(T, 1),
+                               dtopk_w=torch.zeros(T, 1))

@@ -1,0 +1,741 @@
+"""Router losses, gate / combine gradients and low-rank adapters against plain 64-bit formulas.
+
+Tolerances.  u = 2^-24 is half a step of float32, h = eps / 2 the half step of the output type.
+A sum of n float32 terms in any order is off by at most n u times the sum of their magnitudes;
+the tensor cores' additions truncate, i.e. up to 2 u each.  Each check therefore allows
+K u (sum of magnitudes) + h |value| with K counted beside it.
+"""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def m():
+    import sparse_expert_ffn_layer_gb300 as mod
+    return mod
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(g, *shape, sigma=1.0, dtype=torch.float32):
+    return (torch.randn(shape, generator=g, device="cuda") * sigma).to(dtype)
+
+
+def check(got, want, tol, what):
+    got, want, tol = got.double(), want.double(), tol.double() if torch.is_tensor(tol) else tol
+    fin = torch.isfinite(want)
+    assert torch.equal(torch.isfinite(got), fin), f"{what}: finite values differ"
+    err = torch.where(fin, (got - want).abs(), torch.zeros_like(want))
+    bad = err > tol
+    assert not bad.any(), f"{what}: {int(bad.sum())} values off, worst {float(err.max()):.3e}"
+
+
+# ---------------------------------------------------------------- router
+def ref_losses(logits, idx, mask):
+    x = logits.double()
+    T, E = x.shape
+    k = idx.shape[1]
+    on = torch.ones(T, dtype=torch.bool, device="cuda") if mask is None else mask.bool()
+    empty = torch.isneginf(x).all(1)
+    p = torch.softmax(torch.where(empty[:, None], torch.zeros_like(x), x), 1) * (~empty)[:, None]
+    lse = torch.where(empty, torch.zeros_like(x[:, 0]), torch.logsumexp(x, 1))
+    p, lse = p[on], lse[on]
+    n = int(on.sum())
+    ii = idx[on].long().flatten()
+    ii = ii[(ii >= 0) & (ii < E)]
+    counts = torch.bincount(ii, minlength=E)
+    P = p.sum(0) / max(n, 1)
+    bal = E * (counts.double() / (max(n, 1) * k) * P).sum()
+    return counts, P, torch.stack([bal, lse.square().sum() / max(n, 1)]), n
+
+
+def ref_dlogits(logits, idx, mask, counts, n, dlosses, dw):
+    """Autograd of the definition in 64 bits (rows that do not count: zero)."""
+    x = logits.double().clone()
+    T, E = x.shape
+    k = idx.shape[1]
+    on = torch.ones(T, dtype=torch.bool, device="cuda") if mask is None else mask.bool()
+    use = on & ~torch.isneginf(x).all(1)
+    out = torch.zeros_like(x)
+    if not use.any():
+        return out
+    xs = x[use].requires_grad_()
+    total = 0
+    logp = torch.log_softmax(xs, 1)
+    if dlosses is not None:
+        g = dlosses.double()
+        n = max(n, 1)
+        total = g[0] * E * (counts.double() / (n * k) * logp.exp().sum(0) / n).sum()
+        total = total + g[1] * torch.logsumexp(xs, 1).square().sum() / n
+    if dw is not None:
+        ii, w = idx[use].long(), dw[use].double()
+        ok = ((ii >= 0) & (ii < E)).all(1) if k == 2 else ((ii >= 0) & (ii < E))[:, 0]
+        if k == 2:
+            ok &= ii[:, 0] != ii[:, 1]
+        sel = logp[ok].gather(1, ii[ok])
+        ww = sel.exp() if k == 1 else torch.softmax(sel, 1)
+        total = total + (ww * w[ok]).sum()
+    (gr,) = torch.autograd.grad(total, xs)
+    out[use] = gr
+    return out
+
+
+def run_balance(m, logits, idx, mask=None):
+    T, E = logits.shape
+    counts = torch.full((E,), -7, dtype=torch.int32, device="cuda")
+    P = torch.full((E,), float("nan"), device="cuda")
+    losses = torch.full((2,), float("nan"), device="cuda")
+    nv = torch.full((1,), -7, dtype=torch.int32, device="cuda")
+    ws = torch.full((m.moe_balance_workspace_size(T, E),), 0xA5, dtype=torch.uint8, device="cuda")
+    m.moe_balance_loss(logits, idx, counts, P, losses, nv, ws, token_mask=mask)
+    return counts, P, losses, nv
+
+
+def topk(logits, k):
+    return torch.topk(logits, k, dim=1).indices.to(torch.int32).contiguous()
+
+
+SHAPES = [(1, 1), (1, 2), (2, 3), (7, 4), (64, 8), (33, 16), (100, 17), (129, 31), (65, 32), (77, 33),
+          (1000, 60), (50, 64), (201, 65), (513, 127), (3000, 128), (90, 129), (40, 255), (70, 256),
+          (31, 257), (25, 512), (19, 513), (11, 1000), (13, 1023), (300, 1024), (20000, 128),
+          (70001, 5), (9999, 36), (2500, 257)]
+
+
+@pytest.mark.parametrize("T,E", SHAPES)
+@pytest.mark.parametrize("k", [1, 2])
+@pytest.mark.parametrize("masked", [False, True])
+def test_balance_and_its_gradient(m, T, E, k, masked):
+    k = min(k, E)
+    g = gen(T * 1031 + E)
+    logits = randn(g, T, E, sigma=2.0)
+    idx = topk(logits, k)
+    mask = (torch.rand(T, generator=g, device="cuda") < 0.7) if masked else None
+    if masked:
+        logits[~mask] = float("nan")                 # what padding rows hold has no effect
+    counts, P, losses, nv = run_balance(m, logits, idx, mask)
+    rc, rP, rl, rn = ref_losses(logits, idx, mask)
+    assert int(nv) == rn and torch.equal(counts.long(), rc)
+    # p: exponent and sum within 8 u each (|x - max| <= 32 costs the subtraction nothing; expf is
+    # within 2 ulp, E <= 1024 terms summed as a tree of <= 32 + 5 steps); the mean over T rows is
+    # summed in <= T / 4000 + 40 steps
+    K = 64 + T / 4000
+    check(P, rP, K * U * rP + 1e-37, "prob_mean")
+    check(losses, rl, (K + 80) * U * rl.abs() + 1e-37, "losses")
+    dl = torch.full((T, E), float("nan"), device="cuda")
+    dloss = torch.tensor([0.7, -0.3], device="cuda")
+    dw = randn(g, T, k)
+    m.moe_gate_topk_backward(logits, idx, dl, dtopk_w=dw, dlosses=dloss, counts=counts, n_valid=nv,
+                             token_mask=mask)
+    clean = logits if mask is None else torch.where(mask[:, None], logits, torch.zeros_like(logits))
+    want = ref_dlogits(clean, idx, mask, rc, rn, dloss, dw)
+    # magnitudes: every term of a row's gradient is at most p (|a| + sum |a| p + |2 g_z lse / n| + |dw|)
+    # plus |dw| at the chosen experts
+    a = 0.7 * E * rc.double() / (max(rn, 1) ** 2 * k)
+    p = torch.softmax(clean.double(), 1)
+    lse = torch.logsumexp(clean.double(), 1, keepdim=True)
+    mag = p * (a + (a * p).sum(1, keepdim=True) + (0.6 / max(rn, 1)) * lse.abs() +
+               dw.abs().double().sum(1, keepdim=True))
+    mag.scatter_add_(1, idx.long(), dw.abs().double().sum(1, keepdim=True).expand(T, k).contiguous())
+    check(dl, want, 64 * U * mag + 1e-37, "dlogits")
+    if mask is not None:
+        assert not dl[~mask].any()
+
+
+@pytest.mark.parametrize("E", [8, 13, 128])
+def test_router_odd_values(m, E):
+    g = gen(E)
+    T = 40
+    logits = randn(g, T, E)
+    low = torch.finfo(torch.float32).min
+    logits[0] = float("-inf")                        # nothing left: adds nothing, counts as a token
+    logits[1, 1:] = float("-inf")                    # one expert left
+    logits[2] = low                                  # the type's lowest value everywhere
+    logits[3, : E // 2] = low
+    logits[4] = 80.0 * torch.arange(E, device="cuda")
+    logits[5] = -logits[4]
+    logits[6] = 0.0
+    idx = topk(logits, 2)
+    idx[7, 0] = -1                                   # outside: not counted, no gradient
+    idx[8, 1] = E
+    idx[9, 1] = idx[9, 0]                            # the same expert twice
+    counts, P, losses, nv = run_balance(m, logits, idx)
+    rc, rP, rl, rn = ref_losses(logits, idx, None)
+    assert int(nv) == rn == T and torch.equal(counts.long(), rc)
+    check(P, rP, 64 * U * rP + 1e-37, "prob_mean")
+    check(losses[:1], rl[:1], 160 * U * rl[:1].abs(), "balance")
+    assert torch.isinf(losses[1])                    # lse^2 of the lowest value overflows, as it should
+    dl = torch.empty_like(logits)
+    dw = randn(g, T, 2)
+    dloss = torch.tensor([1.0, 0.0], device="cuda")
+    m.moe_gate_topk_backward(logits, idx, dl, dtopk_w=dw, dlosses=dloss, counts=counts, n_valid=nv)
+    want = ref_dlogits(logits, idx, None, rc, rn, dloss, dw)
+    assert torch.isfinite(dl).all()
+    check(dl, want, 64 * U * (1 + dw.abs().double().sum(1, keepdim=True)), "dlogits")
+    assert not dl[0].any()
+    # NaN and +inf propagate to their own row only
+    logits2 = logits.clone()
+    logits2[10, 3], logits2[11, 2] = float("nan"), float("inf")
+    dl2 = torch.empty_like(dl)
+    m.moe_gate_topk_backward(logits2, idx, dl2, dtopk_w=dw, dlosses=dloss, counts=counts, n_valid=nv)
+    assert dl2[10].isnan().any() and dl2[11].isnan().any()
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[10:12] = False
+    assert torch.equal(dl2[keep], dl[keep])
+
+
+def test_balance_no_token_counts_and_empty_batch(m):
+    logits = torch.full((5, 6), float("nan"), device="cuda")
+    idx = torch.zeros((5, 1), dtype=torch.int32, device="cuda")
+    mask = torch.zeros(5, dtype=torch.uint8, device="cuda")
+    for T in (5, 0):
+        counts, P, losses, nv = run_balance(m, logits[:T], idx[:T], mask[:T])
+        assert not counts.any() and not P.any() and not losses.any() and int(nv) == 0
+    dl = torch.full((5, 6), 3.0, device="cuda")
+    m.moe_gate_topk_backward(logits, idx, dl, dlosses=torch.ones(2, device="cuda"), counts=counts,
+                             n_valid=nv, token_mask=mask)
+    assert not dl.any()
+
+
+def test_dlogits_against_differences(m):
+    """Central differences of the losses that the library itself returns (in 64 bits around it)."""
+    g = gen(3)
+    T, E, k = 6, 10, 2
+    logits = randn(g, T, E)
+    idx = topk(logits, k)
+    counts, P, losses, nv = run_balance(m, logits, idx)
+    dw = randn(g, T, k)
+    dloss = torch.tensor([0.5, 0.25], device="cuda")
+    dl = torch.empty_like(logits)
+    m.moe_gate_topk_backward(logits, idx, dl, dtopk_w=dw, dlosses=dloss, counts=counts, n_valid=nv)
+
+    def total(x):
+        p = torch.softmax(x, 1)
+        bal = E * (counts.double() / (T * k) * p.mean(0)).sum()
+        z = torch.logsumexp(x, 1).square().mean()
+        w = torch.softmax(x.gather(1, idx.long()), 1)
+        return 0.5 * bal + 0.25 * z + (w * dw.double()).sum()
+    x = logits.double()
+    h = 1e-5
+    for t in range(T):
+        for e in range(E):
+            d = torch.zeros_like(x)
+            d[t, e] = h
+            num = (total(x + d) - total(x - d)) / (2 * h)
+            assert abs(float(num) - float(dl[t, e])) < 1e-6      # h^2 + 64 u |terms|, terms < 4
+
+
+GATE = [("f16", 1, 128, 4, 1), ("f16", 5, 8, 1, 1), ("f16", 63, 136, 7, 2), ("f16", 64, 128, 16, 1),
+        ("f16", 65, 264, 33, 2), ("f16", 300, 1024, 128, 1), ("f16", 1000, 256, 129, 2),
+        ("f16", 2049, 128, 64, 1), ("f16", 130, 392, 1000, 2), ("f16", 4096, 1024, 128, 2),
+        ("f32", 1, 4, 2, 1), ("f32", 128, 64, 4, 1), ("f32", 77, 68, 13, 2), ("f32", 500, 252, 130, 1),
+        ("f32", 2048, 64, 8, 2)]
+
+
+def gate_inputs(g, dt, T, d, E, k):
+    x = randn(g, T, d, dtype=dt)
+    Wg = randn(g, d, E, sigma=0.1)
+    logits = (x.double() @ Wg.double()).float()
+    return x, Wg, logits, topk(logits, k), randn(g, T, k)
+
+
+@pytest.mark.parametrize("dt,T,d,E,k", GATE)
+@pytest.mark.parametrize("form", ["all", "weights", "tokens"])
+def test_gate_backward(m, dt, T, d, E, k, form):
+    dt = {"f16": torch.float16, "f32": torch.float32}[dt]
+    g = gen(T + 7 * d + E)
+    x, Wg, logits, idx, dw = gate_inputs(g, dt, T, d, E, k)
+    dw[:: 3] *= 1e-6                                 # gradients of very different sizes in one sum
+    dx_in = randn(g, T, d, dtype=dt) if form == "all" else None
+    ws = torch.empty(m.moe_gate_backward_workspace_size(T, d, E, dt), dtype=torch.uint8, device="cuda")
+    dl = torch.full((T, E), float("nan"), device="cuda")
+    dWg = torch.full((d, E), float("nan"), device="cuda") if form != "tokens" else None
+    dx = torch.full((T, d), float("nan"), device="cuda", dtype=dt) if form != "weights" else None
+    m.moe_gate_topk_backward(logits, idx, dl, dtopk_w=dw, tokens=x, Wg=Wg, dWg=dWg, dtokens=dx,
+                             dtokens_in=dx_in, workspace=ws)
+    check(dl, ref_dlogits(logits, idx, None, None, T, None, dw),
+          64 * U * (dw.abs().double().sum(1, keepdim=True) + 1e-30), "dlogits")
+    dd = dl.double()                                 # the products are checked on the dl they had
+    if dWg is not None:
+        mag = x.double().abs().t() @ dd.abs()
+        # f16: dl keeps 22 bits of its chunk's largest value (2 u of it); <= 8 truncating additions per
+        # chunk of 64 rows, then chunks and blocks: T / 64 + 16.  f32: T additions at most
+        cmax = torch.cat([c.abs().amax(0, keepdim=True).expand(1, E).amax() * c.abs().new_ones(len(c), 1)
+                          for c in dd.split(64)])
+        slack = (x.double().abs() * cmax).sum(0)[:, None]
+        tol = (64 + T / 64) * U * mag + 4 * U * slack if dt == torch.float16 else (T + 8) * U * mag
+        check(dWg, x.double().t() @ dd, tol + 1e-37, "dWg")
+    if dx is not None:
+        want = dd @ Wg.double().t()
+        mag = dd.abs() @ Wg.double().abs().t()
+        if dx_in is not None:
+            want, mag = want + dx_in.double(), mag + dx_in.double().abs()
+        # E additions, and operands of 22 bits of their row's largest value
+        slack = dd.abs().amax(1, keepdim=True) * Wg.double().abs().sum(1) + \
+            dd.abs().sum(1, keepdim=True) * Wg.double().abs().amax(1)
+        tol = (2 * E + 64) * U * mag + 4 * U * slack + torch.finfo(dt).eps / 2 * want.abs()
+        check(dx, want, tol + (2.0 ** -25 if dt == torch.float16 else 1e-37), "dtokens")
+
+
+def test_gate_backward_masked_rows_and_in_place(m):
+    g = gen(5)
+    T, d, E, k = 200, 128, 24, 2
+    x, Wg, logits, idx, dw = gate_inputs(g, torch.float16, T, d, E, k)
+    mask = torch.rand(T, generator=g, device="cuda") < 0.6
+    x[~mask] = float("nan")                          # padding rows hold anything
+    logits[~mask] = float("inf")
+    ws = torch.empty(m.moe_gate_backward_workspace_size(T, d, E, x.dtype), dtype=torch.uint8, device="cuda")
+    dl, dWg = torch.empty((T, E), device="cuda"), torch.empty((d, E), device="cuda")
+    dx = randn(g, T, d, dtype=torch.float16)
+    before = dx.clone()
+    m.moe_gate_topk_backward(logits, idx, dl, dtopk_w=dw, token_mask=mask, tokens=x, Wg=Wg, dWg=dWg,
+                             dtokens=dx, dtokens_in=dx, workspace=ws)
+    assert torch.isfinite(dWg).all() and not dl[~mask].any()
+    assert torch.equal(dx[~mask], before[~mask])
+    want = x[mask].double().t() @ dl[mask].double()
+    mag = x[mask].double().abs().t() @ dl[mask].double().abs()
+    check(dWg, want, 80 * U * (mag + x[mask].double().abs().sum(0)[:, None] * dl.abs().max().double()), "dWg")
+    dWg0 = torch.ones((d, E), device="cuda")         # an empty batch clears the sum
+    m.moe_gate_topk_backward(logits[:0], idx[:0], dl[:0], dtopk_w=dw[:0], tokens=x[:0], Wg=Wg, dWg=dWg0,
+                             workspace=ws)
+    assert not dWg0.any()
+
+
+# ---------------------------------------------------------------- combine
+@pytest.mark.parametrize("dt", [torch.float16, torch.float32])
+@pytest.mark.parametrize("T,d,k", [(1, 8, 1), (3, 7, 2), (64, 128, 2), (129, 1001, 1), (1000, 264, 2),
+                                   (5000, 72, 2), (2433, 8, 1), (40, 3584, 2)])
+@pytest.mark.parametrize("form", ["both", "dy", "dw"])
+def test_combine_backward(m, dt, T, d, k, form):
+    g = gen(T + d)
+    kept = torch.rand((T, k), generator=g, device="cuda") < 0.8
+    S = int(kept.sum())
+    slot = torch.full((T * k,), -1, dtype=torch.int32, device="cuda")
+    slot[kept.flatten()] = torch.randperm(S, generator=g, device="cuda").to(torch.int32)
+    slot = slot.view(T, k)
+    w = torch.rand((T, k), generator=g, device="cuda")
+    dout, y = randn(g, T, d, dtype=dt), randn(g, T * k + 3, d, dtype=dt)
+    y[S:] = float("nan")                             # behind the last slot: not read
+    dy = torch.full((T * k + 3, d), 7.0, dtype=dt, device="cuda") if form != "dw" else None
+    dw = torch.full((T, k), float("nan"), device="cuda") if form != "dy" else None
+    m.moe_combine_backward(dout, y if dw is not None else None, slot, w if dy is not None else None, dy, dw)
+    dd, yy = dout.double(), y.double()
+    if dw is not None:
+        ii = slot.long().clamp(min=0)
+        prod = dd[:, None, :] * yy[ii] * (slot >= 0)[:, :, None]
+        prod = torch.where((slot >= 0)[:, :, None], prod, torch.zeros_like(prod))
+        check(dw, prod.sum(2), (d / 32 + 16) * U * prod.abs().sum(2) + 1e-37, "dtopk_w")
+    if dy is not None:
+        want = torch.full_like(yy, 7.0)
+        for j in range(k):
+            on = slot[:, j] >= 0
+            want[slot[on, j].long()] = w[on, j].double()[:, None] * dd[on]
+        # rounded to 32 bits, then to the type
+        check(dy, want, want.abs() * (torch.finfo(dt).eps / 2 + U) + (2.0 ** -25 if dt == torch.float16 else 0),
+              "dexpert_out")
+        assert (dy[S:] == 7.0).all()
+
+
+def test_combine_backward_slots_outside_are_dropped(m):
+    dout = torch.ones((4, 8), device="cuda")
+    y = torch.ones((2, 8), device="cuda")
+    slot = torch.tensor([[0], [2], [1 << 30], [-5]], dtype=torch.int32, device="cuda")
+    w = torch.full((4, 1), 0.5, device="cuda")
+    dy, dw = torch.zeros_like(y), torch.full((4, 1), -1.0, device="cuda")
+    m.moe_combine_backward(dout, y, slot, w, dy, dw)
+    assert dw.flatten().tolist() == [8.0, 0.0, 0.0, 0.0]
+    assert dy[0].eq(0.5).all() and dy[1].eq(0).all()
+
+
+# ---------------------------------------------------------------- adapters
+def plan(m, ids, N):
+    """perm and offsets of adapter ids, by the library's own dispatch."""
+    T = ids.numel()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    counts, kept, off = torch.zeros(N, **i32), torch.zeros(N, **i32), torch.zeros(N + 1, **i32)
+    perm, slot = torch.zeros(T, **i32), torch.zeros((T, 1), **i32)
+    m.moe_dispatch(ids.view(T, 1), N, float("inf"), counts, kept, off, perm, slot)
+    return perm, off
+
+
+def adapter_inputs(m, g, dt, T, di, do, r, N, none=0.2, one=False):
+    ids = torch.randint(0, N, (T,), generator=g, device="cuda", dtype=torch.int32)
+    if one:
+        ids[:] = N - 1
+    ids[torch.rand(T, generator=g, device="cuda") < none] = -1
+    perm, off = plan(m, ids, N)
+    return dict(ids=ids, perm=perm, off=off, x=randn(g, T, di, dtype=dt),
+                A=randn(g, N, di, r, sigma=di ** -0.5, dtype=dt), B=randn(g, N, r, do, sigma=0.3, dtype=dt),
+                scale=randn(g, N, sigma=1.5), base=randn(g, T, do, dtype=dt))
+
+
+def adapter_ws(m, T, di, do, r, N, dt):
+    return torch.full((m.moe_adapter_workspace_size(T, di, do, r, N, T, dt),), 0x5A, dtype=torch.uint8,
+                      device="cuda")
+
+
+def tiny(dt):
+    return 2.0 ** -25 if dt == torch.float16 else 1e-37
+
+
+ADAPT = [("f16", 1, 8, 8, 8, 1), ("f16", 1, 1024, 1024, 16, 32), ("f16", 2, 64, 8, 8, 3), ("f16", 17, 72, 136, 24, 2),
+         ("f16", 64, 3584, 264, 16, 64), ("f16", 100, 520, 1000, 40, 1), ("f16", 300, 128, 2048, 64, 5),
+         ("f16", 333, 1032, 72, 128, 3), ("f16", 1000, 256, 256, 8, 1000), ("f16", 2000, 200, 328, 104, 7),
+         ("f16", 4097, 512, 512, 32, 2), ("f16", 65, 128, 128, 128, 1024), ("f32", 1, 4, 4, 8, 1),
+         ("f32", 128, 64, 256, 8, 4), ("f32", 33, 68, 100, 24, 3), ("f32", 500, 1028, 36, 64, 9),
+         ("f32", 70, 128, 260, 128, 2), ("f32", 1111, 32, 32, 16, 1)]
+
+
+@pytest.mark.parametrize("dt,T,di,do,r,N", ADAPT)
+@pytest.mark.parametrize("form", ["base", "in_place", "bare", "one"])
+def test_adapter_forward(m, dt, T, di, do, r, N, form):
+    dt = {"f16": torch.float16, "f32": torch.float32}[dt]
+    g = gen(T + di + do + r)
+    c = adapter_inputs(m, g, dt, T, di, do, r, N, none=0.0 if form == "one" else 0.2, one=form == "one")
+    ws = adapter_ws(m, T, di, do, r, N, dt)
+    out = c["base"].clone() if form == "in_place" else torch.full((T, do), 9.0, dtype=dt, device="cuda")
+    base = out if form == "in_place" else None if form == "bare" else c["base"]
+    hid = torch.full((T, r), 5.0, device="cuda")
+    before = out.clone()
+    m.moe_adapter_forward(c["x"], c["perm"], c["off"], c["A"], c["B"], c["scale"], out, ws, base=base,
+                          hidden=hid)
+    assert m.moe_status_read(ws) == m.MOE_OK
+    S = int(c["off"][-1])
+    assert (hid[S:] == 5.0).all()
+    t = c["perm"][:S].long()
+    a = c["ids"][t].long()
+    for n in a.unique().tolist():
+        s = (a == n).nonzero()[:, 0]
+        tt = t[s]
+        x, A, B, sc = c["x"][tt].double(), c["A"][n].double(), c["B"][n].double(), float(c["scale"][n])
+        h = x @ A
+        hm = x.abs() @ A.abs()
+        # a block sums at most ceil(di / 8 / 64) chunks of four products of 16, the cluster eight blocks,
+        # two units per truncating addition (f32: di / 8 + 32 + 8 additions)
+        K = 2 * (4 * (di / 512 + 1) + 16) if dt == torch.float16 else di / 8 + 48
+        check(hid[s], h, K * U * hm + 1e-37, "hidden")
+        y = sc * (h @ B)
+        ym = abs(sc) * (hm @ B.abs())
+        # h off by K, its split by 2 u of the row's largest, the second sum r / 4 + 8 additions
+        slack = abs(sc) * h.abs().amax(1, keepdim=True) * B.abs().sum(0)
+        K2 = K + (r / 2 + 24 if dt == torch.float16 else r + 8)
+        b = c["base"][tt].double() if form != "bare" else torch.zeros_like(y)
+        want = b + y
+        tol = K2 * U * (ym + b.abs()) + 2 * U * slack + torch.finfo(dt).eps / 2 * want.abs() * (1 + 2 ** -10)
+        check(out[tt], want, tol + tiny(dt), "out")
+    rest = torch.ones(T, dtype=torch.bool, device="cuda")
+    rest[t] = False
+    assert torch.equal(out[rest], before[rest])
+
+
+@pytest.mark.parametrize("dt,T,di,do,r,N", ADAPT)
+@pytest.mark.parametrize("form", ["all", "dA", "dB", "dx", "one"])
+def test_adapter_backward(m, dt, T, di, do, r, N, form):
+    dt = {"f16": torch.float16, "f32": torch.float32}[dt]
+    g = gen(T + di + do + r + 1)
+    c = adapter_inputs(m, g, dt, T, di, do, r, N, none=0.0 if form == "one" else 0.2, one=form == "one")
+    ws = adapter_ws(m, T, di, do, r, N, dt)
+    dout = randn(g, T, do, sigma=0.1, dtype=dt)
+    dout[:: 3] *= 1e-3
+    hid = randn(g, T, r)
+    din = randn(g, T, di, dtype=dt)
+    full = form in ("all", "one")
+    dx = torch.full((T, di), 9.0, dtype=dt, device="cuda") if full or form == "dx" else None
+    dA = torch.full((N, di, r), float("nan"), device="cuda") if full or form == "dA" else None
+    dB = torch.full((N, r, do), float("nan"), device="cuda") if full or form == "dB" else None
+    m.moe_adapter_backward(dout, c["x"], hid, c["perm"], c["off"], c["A"], c["B"], c["scale"], ws,
+                           dtokens=dx, dtokens_in=din if full else None, dA=dA, dB=dB)
+    assert m.moe_status_read(ws) == m.MOE_OK
+    S = int(c["off"][-1])
+    t = c["perm"][:S].long()
+    a = c["ids"][t].long()
+    half = dt == torch.float16
+    for n in range(N):
+        s = (a == n).nonzero()[:, 0]
+        if not len(s):
+            assert dA is None or not dA[n].any()
+            assert dB is None or not dB[n].any()
+            continue
+        tt = t[s]
+        x, dy, A, B = c["x"][tt].double(), dout[tt].double(), c["A"][n].double(), c["B"][n].double()
+        sc, H = float(c["scale"][n]), hid[s].double()
+        dh, dhm = dy @ B.t(), dy.abs() @ B.abs().t()
+        K = 2 * (4 * (do / 512 + 1) + 16) if half else do / 8 + 48
+        if dx is not None:
+            b = din[tt].double() if full else torch.zeros_like(x)
+            want = b + sc * (dh @ A.t())
+            mag = abs(sc) * (dhm @ A.abs().t()) + b.abs()
+            slack = abs(sc) * dh.abs().amax(1, keepdim=True) * A.abs().sum(1)
+            K2 = K + (r / 2 + 24 if half else r + 8)
+            tol = K2 * U * mag + 2 * U * slack + torch.finfo(dt).eps / 2 * want.abs() * (1 + 2 ** -10)
+            check(dx[tt], want, tol + tiny(dt), "dtokens")
+        rows = len(s)
+        # sums over rows: f16 parts keep 2 u of the largest value of the rows, 8 truncating additions
+        # per chunk, rows / 64 + 16 more; f32: one addition per row
+        KW = 64 + rows / 64 if half else rows + 16
+        if dA is not None:
+            mag = x.abs().t() @ dhm
+            slack = x.abs().sum(0)[:, None] * dh.abs().max() if half else 0
+            check(dA[n], sc * (x.t() @ dh), abs(sc) * ((KW + K) * U * mag + 2 * U * slack) + 1e-37, "dA")
+        if dB is not None:
+            # an f16 operand below 2^-14 (a subnormal q 2^-24, q < 2^10) enters the tensor core's adder
+            # with its stored exponent and leading zeros: the sum of a product keeps its 23 bits below
+            # 2^-14 |h|, not below |dy h|, so such an operand counts as 2^-14 in the bound
+            dyf = torch.where(dy == 0, dy, dy.abs().clamp(min=2.0 ** -14)) if half else dy.abs()
+            mag = H.abs().t() @ dyf
+            slack = dyf.sum(0)[None, :] * H.abs().max() if half else 0
+            check(dB[n], sc * (H.t() @ dy), abs(sc) * (KW * U * mag + 2 * U * slack) + 1e-37, "dB")
+    if dx is not None:
+        rest = torch.ones(T, dtype=torch.bool, device="cuda")
+        rest[t] = False
+        assert (dx[rest] == 9.0).all()
+
+
+def test_adapter_single_row_gradient_keeps_22_bits(m):
+    """One row: dA = scale x dh has one term, so nothing but the operands' precision shows."""
+    g = gen(11)
+    c = adapter_inputs(m, g, torch.float16, 1, 256, 256, 16, 1, none=0.0)
+    ws = adapter_ws(m, 1, 256, 256, 16, 1, torch.float16)
+    hid, dout = randn(g, 1, 16), randn(g, 1, 256, dtype=torch.float16)
+    dB = torch.empty((1, 16, 256), device="cuda")
+    m.moe_adapter_backward(dout, c["x"], hid, c["perm"], c["off"], c["A"], c["B"], c["scale"], ws, dB=dB)
+    want = float(c["scale"]) * hid.double().t() @ dout.double()
+    check(dB[0], want, 4 * U * want.abs() + 2 * U * hid.abs().max().double() * dout.double().abs() *
+          abs(float(c["scale"])), "dB")
+
+
+@pytest.mark.parametrize("T", [3, 300])
+def test_adapter_wide_range_and_infinities(m, T):
+    """h far outside f16's range, and rows with infinities or NaN that leave the others alone."""
+    g = gen(T)
+    c = adapter_inputs(m, g, torch.float16, T, 128, 128, 16, 1, none=0.0)
+    c["x"] = (c["x"].double() * 3e4).clamp(-6e4, 6e4).half()
+    c["A"] = (c["A"].double() * 1e3).half()
+    c["B"] = (c["B"].double() * 1e-3).half()
+    c["scale"][:] = 1e-4
+    ws = adapter_ws(m, T, 128, 128, 16, 1, torch.float16)
+
+    def fwd(x):
+        out = torch.empty((T, 128), dtype=torch.float16, device="cuda")
+        hid = torch.empty((T, 16), device="cuda")
+        m.moe_adapter_forward(x, c["perm"], c["off"], c["A"], c["B"], c["scale"], out, ws, base=c["base"],
+                              hidden=hid)
+        return out, hid
+    out, hid = fwd(c["x"])
+    assert hid.abs().max() > 65504
+    h = c["x"].double() @ c["A"][0].double()
+    want = c["base"].double() + 1e-4 * (h @ c["B"][0].double())
+    mag = 1e-4 * (c["x"].double().abs() @ c["A"][0].double().abs() @ c["B"][0].double().abs())
+    check(out, want, 2.0 ** -11 * want.abs() * 1.001 + 128 * U * (mag + 1) + 2.0 ** -25, "out")
+    x2 = c["x"].clone()
+    x2[1, 5], x2[2, 7] = float("inf"), float("nan")
+    out2, _ = fwd(x2)
+    assert not torch.isfinite(out2[1]).any() and out2[2].isnan().all()
+    assert torch.equal(out2[0], out[0]) and torch.equal(out2[3:], out[3:])
+
+
+def test_adapter_rows_behind_the_last_slot_and_bad_indices(m):
+    g = gen(2)
+    T, d, r, N = 70, 64, 8, 4
+    c = adapter_inputs(m, g, torch.float16, T, d, d, r, N)
+    ws = adapter_ws(m, T, d, d, r, N, torch.float16)
+
+    def fwd(perm, off):
+        out = torch.full((T, d), 3.0, dtype=torch.float16, device="cuda")
+        hid = torch.full((T, r), 3.0, device="cuda")
+        m.moe_adapter_forward(c["x"], perm, off, c["A"], c["B"], c["scale"], out, ws, base=c["base"], hidden=hid)
+        return m.moe_status_read(ws), out, hid
+    st, good, hid = fwd(c["perm"], c["off"])
+    assert st == m.MOE_OK
+    # entries that point outside are skipped and reported; the next good call reports OK again
+    S = int(c["off"][-1])
+    bad = c["perm"].clone()
+    lost = [int(bad[0]), int(bad[S - 1])]
+    bad[0], bad[S - 1] = T, -1
+    st, out, _ = fwd(bad, c["off"])
+    assert st == m.MOE_ERR_DEVICE_BOUNDS
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[lost] = False
+    assert torch.equal(out[keep], good[keep]) and (out[lost] == 3.0).all()
+    assert fwd(c["perm"], c["off"])[0] == m.MOE_OK
+    for off in ([0, 10, 5, 20, S], [0, 10, 20, 30, T + 9], [-4, 10, 20, 30, S],
+                [0, 1 << 30, 1 << 30, 1 << 30, 1 << 30], [S, S, S, S, 0]):
+        st, out, hid = fwd(c["perm"], torch.tensor(off, dtype=torch.int32, device="cuda"))
+        assert st == m.MOE_ERR_DEVICE_BOUNDS
+        dA, dB = torch.empty((N, d, r), device="cuda"), torch.empty((N, r, d), device="cuda")
+        m.moe_adapter_backward(c["x"], c["x"], hid, c["perm"], torch.tensor(off, dtype=torch.int32, device="cuda"),
+                               c["A"], c["B"], c["scale"], ws, dA=dA, dB=dB)
+        assert m.moe_status_read(ws) == m.MOE_ERR_DEVICE_BOUNDS
+    # no adapter at all
+    st, out, hid = fwd(c["perm"], torch.zeros(N + 1, dtype=torch.int32, device="cuda"))
+    assert st == m.MOE_OK and (out == 3.0).all() and (hid == 3.0).all()
+
+
+def test_empty_batches(m):
+    z = torch.zeros
+    dA, dB = torch.ones((2, 16, 8), device="cuda"), torch.ones((2, 8, 16), device="cuda")
+    x = z((0, 16), dtype=torch.float16, device="cuda")
+    perm = z((0,), dtype=torch.int32, device="cuda")
+    off = z((3,), dtype=torch.int32, device="cuda")
+    A, B = z((2, 16, 8), dtype=torch.float16, device="cuda"), z((2, 8, 16), dtype=torch.float16, device="cuda")
+    ws = adapter_ws(m, 0, 16, 16, 8, 2, torch.float16)
+    m.moe_adapter_forward(x, perm, off, A, B, z(2, device="cuda"), x.clone(), ws)
+    m.moe_adapter_backward(x, x, z((0, 8), device="cuda"), perm, off, A, B, z(2, device="cuda"), ws, dA=dA, dB=dB)
+    assert not dA.any() and not dB.any()
+    m.moe_combine_backward(x, x, z((0, 1), dtype=torch.int32, device="cuda"), z((0, 1), device="cuda"), x, None)
+
+
+# ---------------------------------------------------------------- together, streams, graphs
+def step_buffers(m, T, d, r, N, E, k):
+    f16, f32, i32 = torch.float16, torch.float32, torch.int32
+    e = lambda *s, t=f32: torch.zeros(s, dtype=t, device="cuda")
+    S = T * k
+    return dict(logits=e(T, E), idx=e(T, k, t=i32), w=e(T, k), counts=e(E, t=i32), kept=e(E, t=i32),
+                off=e(E + 1, t=i32), perm=e(S, t=i32), slot=e(T, k, t=i32), y=e(S, d, t=f16), out=e(T, d, t=f16),
+                ws=e(m.moe_workspace_size(T, d, 4 * d, E, k, float("inf"), 0, 0, m.MOE_F16), t=torch.uint8),
+                bc=e(E, t=i32), P=e(E), losses=e(2), nv=e(1, t=i32),
+                bws=e(m.moe_balance_workspace_size(T, E), t=torch.uint8),
+                hid=e(T, r), aws=e(m.moe_adapter_workspace_size(T, d, d, r, N, T, f16), t=torch.uint8),
+                acnt=e(N, t=i32), akept=e(N, t=i32), aoff=e(N + 1, t=i32), aperm=e(T, t=i32), aslot=e(T, 1, t=i32),
+                dw=e(T, k), dl=e(T, E), dWg=e(d, E), dx=e(T, d, t=f16), dA=e(N, d, r), dB=e(N, r, d),
+                gws=e(m.moe_gate_backward_workspace_size(T, d, E, f16), t=torch.uint8))
+
+
+def step(m, c, b, stream=None):
+    """A training step of the router and the adapters of a layer whose experts stay as they are."""
+    kw = dict(stream=stream)
+    E, k = c["Wg"].shape[1], b["idx"].shape[1]
+    N = c["A"].shape[0]
+    m.moe_gate_topk(c["x"], c["Wg"], k, b["idx"], b["w"], logits_out=b["logits"], **kw)
+    m.moe_dispatch(b["idx"], E, 1.0, b["counts"], b["kept"], b["off"], b["perm"], b["slot"], **kw)
+    m.moe_expert_ffn(c["x"], b["perm"], b["off"], c["W1"], c["W2"], b["y"].shape[0], b["y"], b["ws"], **kw)
+    m.moe_combine(b["y"], b["slot"], b["w"], b["out"], **kw)
+    m.moe_balance_loss(b["logits"], b["idx"], b["bc"], b["P"], b["losses"], b["nv"], b["bws"], **kw)
+    m.moe_dispatch(c["ids"], N, float("inf"), b["acnt"], b["akept"], b["aoff"], b["aperm"], b["aslot"], **kw)
+    m.moe_adapter_forward(c["x"], b["aperm"], b["aoff"], c["A"], c["B"], c["scale"], b["out"], b["aws"],
+                          base=b["out"], hidden=b["hid"], **kw)
+    m.moe_combine_backward(c["dout"], b["y"], b["slot"], b["w"], None, b["dw"], **kw)
+    m.moe_gate_topk_backward(b["logits"], b["idx"], b["dl"], dtopk_w=b["dw"], dlosses=c["dloss"],
+                             counts=b["bc"], n_valid=b["nv"], tokens=c["x"], Wg=c["Wg"], dWg=b["dWg"],
+                             dtokens=b["dx"], workspace=b["gws"], **kw)
+    m.moe_adapter_backward(c["dout"], c["x"], b["hid"], b["aperm"], b["aoff"], c["A"], c["B"], c["scale"],
+                           b["aws"], dtokens=b["dx"], dtokens_in=b["dx"], dA=b["dA"], dB=b["dB"], **kw)
+
+
+OUTS = ("out", "losses", "bc", "P", "dw", "dl", "dWg", "dx", "dA", "dB")
+
+
+def step_inputs(seed, T, d, r, N, E, k):
+    g = gen(seed)
+    f16 = torch.float16
+    ids = torch.randint(-1, N, (T, 1), generator=g, device="cuda", dtype=torch.int32)
+    return dict(x=randn(g, T, d, dtype=f16), Wg=randn(g, d, E, sigma=d ** -0.5), ids=ids,
+                W1=randn(g, E, d, 4 * d, sigma=d ** -0.5, dtype=f16),
+                W2=randn(g, E, 4 * d, d, sigma=0.5 * d ** -0.5, dtype=f16),
+                A=randn(g, N, d, r, sigma=d ** -0.5, dtype=f16), B=randn(g, N, r, d, sigma=0.1, dtype=f16),
+                scale=torch.rand(N, generator=g, device="cuda") + 0.5, dout=randn(g, T, d, sigma=0.1, dtype=f16),
+                dloss=torch.tensor([0.01, 0.001], device="cuda"))
+
+
+@pytest.mark.parametrize("T,d,r,N,E,k", [(96, 128, 16, 5, 8, 2), (700, 256, 24, 3, 12, 1)])
+def test_training_step_of_router_and_adapters(m, T, d, r, N, E, k):
+    c, b = step_inputs(1, T, d, r, N, E, k), step_buffers(m, T, d, r, N, E, k)
+    step(m, c, b)
+    torch.cuda.synchronize()
+    assert m.moe_status_read(b["ws"]) == m.MOE_OK and m.moe_status_read(b["aws"]) == m.MOE_OK
+    # the same step by autograd in 64 bits (experts' outputs as the library rounded them)
+    x = c["x"].double().requires_grad_()
+    Wg, A, B = (c[q].double().requires_grad_() for q in ("Wg", "A", "B"))
+    logits = x @ Wg
+    idx, slot = b["idx"].long(), b["slot"].long()
+    sel = torch.log_softmax(logits, 1).gather(1, idx)
+    w = sel.exp() if k == 1 else torch.softmax(sel, 1)
+    y = torch.where((slot >= 0)[..., None], b["y"].double()[slot.clamp(min=0)], torch.zeros((), device="cuda", dtype=torch.double))
+    comb = (w[..., None] * y).sum(1)
+    ids = c["ids"].flatten().long()
+    on = ids >= 0
+    delta = torch.einsum("ti,tij,tjo->to", x[on], A[ids[on]], B[ids[on]]) * c["scale"].double()[ids[on]][:, None]
+    out = comb.index_add(0, on.nonzero()[:, 0], delta)
+    p = torch.softmax(logits, 1)
+    bal = E * (b["bc"].double() / (T * k) * p.mean(0)).sum()
+    z = torch.logsumexp(logits, 1).square().mean()
+    total = (out * c["dout"].double()).sum() + 0.01 * bal + 0.001 * z
+    gx, gW, gA, gB = torch.autograd.grad(total, (x, Wg, A, B), retain_graph=True)
+    (gx_adapter,) = torch.autograd.grad((delta * c["dout"].double()[on]).sum(), x)
+    gx_gate = gx - gx_adapter
+    assert abs(float(b["losses"][0]) - float(bal)) < 1e-5 and abs(float(b["losses"][1]) - float(z)) < 1e-4
+    # out is rounded twice, after the combine and after the adapter (rows without one: once), dtokens
+    # after the gate and after the adapter; 32-bit sums of a row's terms add less than 2^-16 of its
+    # largest value.  dlogits come from logits of 32 bits (d products: 2^-24 d of their magnitudes).
+    half = 2.0 ** -11 * (1 + 2.0 ** -9)
+    row = lambda v: 2.0 ** -16 * v.abs().amax(1, keepdim=True) + 2.0 ** -24
+    check(b["out"], out, half * (comb.abs() + out.abs()) + row(out), "out")
+    check(b["dx"], gx, half * (gx_gate.abs() + gx.abs()) + row(gx), "dx")
+    for name, want in (("dWg", gW), ("dA", gA), ("dB", gB)):
+        check(b[name], want, 2.0 ** -14 * want.abs().max(), name)
+
+
+def test_training_step_streams_graph_and_repeats(m):
+    shape = (300, 128, 16, 4, 8, 2)
+    c, b = step_inputs(2, *shape), step_buffers(m, *shape)
+    step(m, c, b)
+    torch.cuda.synchronize()
+    want = {q: b[q].clone() for q in OUTS}
+    # again, and on another stream
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for stream in (None, s):
+        for q in OUTS:
+            b[q].zero_()
+        torch.cuda.synchronize()
+        step(m, c, b, stream=stream)
+        torch.cuda.synchronize()
+        for q in OUTS:
+            assert torch.equal(b[q], want[q]), (q, stream)
+    # captured and replayed with new inputs; two graphs share every workspace and run one after the other
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            step(m, c, b)
+        graphs.append(g)
+    c2 = step_inputs(3, *shape)
+    keep = {q: c[q].clone() for q in c}
+    for q in ("x", "Wg", "A", "B", "dout", "ids"):
+        c[q].copy_(c2[q])
+    for g in graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    got = {q: b[q].clone() for q in OUTS}
+    step(m, c, b)
+    torch.cuda.synchronize()
+    for q in OUTS:
+        assert torch.equal(b[q], got[q]), q
+    for q in keep:
+        c[q].copy_(keep[q])
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    for q in OUTS:
+        assert torch.equal(b[q], want[q]), q
+
+
+def test_two_adapter_calls_at_once(m):
+    """Different workspaces and outputs: calls may overlap on two streams."""
+    g = gen(9)
+    c = adapter_inputs(m, g, torch.float16, 2000, 512, 512, 32, 6)
+    outs = [torch.zeros((2000, 512), dtype=torch.float16, device="cuda") for _ in range(3)]
+    wss = [adapter_ws(m, 2000, 512, 512, 32, 6, torch.float16) for _ in range(3)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i, s in enumerate(streams):
+        for _ in range(4):
+            m.moe_adapter_forward(c["x"], c["perm"], c["off"], c["A"], c["B"], c["scale"], outs[i], wss[i],
+                                  base=c["base"], stream=s)
+    m.moe_adapter_forward(c["x"], c["perm"], c["off"], c["A"], c["B"], c["scale"], outs[2], wss[2], base=c["base"])
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[2])
