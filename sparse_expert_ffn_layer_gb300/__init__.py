@@ -223,31 +223,48 @@ def moe_expert_ffn_noalloc(tokens, perm, offsets, W1, W2, S_max, expert_out, str
 
 
 # ---------------------------------------------------------------- training and adapters
-def _given(where, dev, **tensors):
-    """Checks name=(tensor or None, dtype, shape) and returns the device all of them are on.
+# These calls take a few microseconds on the GPU at decode sizes, so their checks are kept to
+# a few attribute reads per tensor: _device_of walks (tensor, dtype, shape) triples and only
+# a call that fails builds a message.
+def _device_of(where, names, given):
+    """CUDA device index that every given tensor is on (None entries are skipped).
 
-    dtype None: any of the layer's two.  The kernels read dense row-major memory, so anything
-    else is refused here rather than read wrongly."""
-    import torch
-    for name, (t, dtype, shape) in tensors.items():
+    The kernels read dense row-major memory of the stated type and shape; anything else is
+    refused here rather than read wrongly."""
+    dev = given[0][0].get_device()
+    for t, dtype, shape in given:
+        if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != dev
+                              or not t.is_contiguous()):
+            _refuse(where, names, given, dev)
+    if dev < 0:
+        _refuse(where, names, given, dev)
+    return dev
+
+
+def _refuse(where, names, given, dev):
+    for name, (t, dtype, shape) in zip(names.split(), given):
         if t is None:
             continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{where}: {name} must be a tensor")
-        if dtype is None:
-            _dtype(t)
-        elif t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        if t.dtype is not dtype:
             raise TypeError(f"{where}: {name} is {t.dtype}, expected {dtype}")
-        if shape is not None and tuple(t.shape) != tuple(shape):
+        if t.shape != shape:
             raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{where}: {name} must be contiguous")
-        if dev is not None and t.device != dev:
-            raise ValueError(f"{where}: {name} is on {t.device}, expected {dev}")
-        dev = t.device
-    if dev is not None and dev.type != "cuda":
-        raise ValueError(f"{where}: tensors must be on a CUDA device, not {dev}")
-    return dev
+        if t.get_device() != dev:
+            raise ValueError(f"{where}: {name} is on {t.device}, expected the device of "
+                             f"{names.split()[0]}, {given[0][0].device}")
+    raise ValueError(f"{where}: tensors must be on a CUDA device")
+
+
+def _mask_type(where, token_mask):
+    """torch.bool or torch.uint8, whichever the mask is (a byte per token either way)."""
+    import torch
+    if token_mask is None:
+        return None
+    if token_mask.dtype not in (torch.bool, torch.uint8):
+        raise TypeError(f"{where}: token_mask is {token_mask.dtype}, expected torch.bool or torch.uint8")
+    return token_mask.dtype
 
 
 def _required(where, **tensors):
@@ -256,8 +273,12 @@ def _required(where, **tensors):
             raise ValueError(f"{where}: {name} is required")
 
 
-def _ws(workspace):
-    return (_ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
+def _adr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _ws_bytes(workspace):
+    return 0 if workspace is None else workspace.numel()
 
 
 def _code(dtype) -> int:
@@ -270,12 +291,21 @@ def _code(dtype) -> int:
     return MOE_F16 if dtype == torch.float16 else MOE_F32
 
 
-def _on(dev, stream):
-    """Context with `dev` current, so that the launch and the default stream are that device's."""
+def _call(where, dev, stream, *args):
+    """The library call on device `dev`: its current stream unless one is given."""
     import torch
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-    return torch.cuda.device(dev)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on cuda:{dev}")
+    fn = getattr(get_lib(), where)
+    if torch.cuda.current_device() == dev:
+        code = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, stream.cuda_stream)
+    if code != MOE_OK:
+        raise MoeError(code, where)
 
 
 def moe_balance_workspace_size(T, E) -> int:
@@ -286,20 +316,20 @@ def moe_balance_workspace_size(T, E) -> int:
 
 def moe_balance_loss(logits, topk_idx, counts, prob_mean, losses, n_valid, workspace,
                      token_mask=None, stream=None):
+    """Per-expert counts, mean probabilities and the balance and z losses of a routed batch."""
     import torch
     where = "moe_balance_loss"
     T, E = logits.shape
     k = topk_idx.shape[1]
     f32, i32 = torch.float32, torch.int32
-    dev = _given(where, None, logits=(logits, f32, (T, E)), topk_idx=(topk_idx, i32, (T, k)),
-                 counts=(counts, i32, (E,)), prob_mean=(prob_mean, f32, (E,)),
-                 losses=(losses, f32, (2,)), n_valid=(n_valid, i32, (1,)),
-                 workspace=(workspace, torch.uint8, None),
-                 token_mask=(token_mask, (torch.bool, torch.uint8), (T,)))
-    with _on(dev, stream):
-        _check(get_lib().moe_balance_loss(_ptr(logits), _ptr(topk_idx), _ptr(token_mask), T, E, k,
-                                          _ptr(counts), _ptr(prob_mean), _ptr(losses), _ptr(n_valid),
-                                          *_ws(workspace), _stream(stream)), where)
+    dev = _device_of(where, "logits topk_idx counts prob_mean losses n_valid workspace token_mask",
+                     ((logits, f32, (T, E)), (topk_idx, i32, (T, k)), (counts, i32, (E,)),
+                      (prob_mean, f32, (E,)), (losses, f32, (2,)), (n_valid, i32, (1,)),
+                      (workspace, torch.uint8, workspace.shape),
+                      (token_mask, _mask_type(where, token_mask), (T,))))
+    _call(where, dev, stream, logits.data_ptr(), topk_idx.data_ptr(), _adr(token_mask), T, E, k,
+          counts.data_ptr(), prob_mean.data_ptr(), losses.data_ptr(), n_valid.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
 
 
 def moe_gate_backward_workspace_size(T, d, E, dtype) -> int:
@@ -312,56 +342,58 @@ def moe_gate_backward_workspace_size(T, d, E, dtype) -> int:
 def moe_gate_topk_backward(logits, topk_idx, dlogits, dtopk_w=None, dlosses=None, counts=None,
                            n_valid=None, token_mask=None, tokens=None, Wg=None, dWg=None,
                            dtokens=None, dtokens_in=None, workspace=None, stream=None):
+    """Gradient of the gate weights and of the router losses: dlogits, and from it dWg and dtokens."""
     import torch
     where = "moe_gate_topk_backward"
     T, E = logits.shape
     k = topk_idx.shape[1]
     f32, i32 = torch.float32, torch.int32
-    if dWg is not None:
-        _required(where, tokens=tokens)
-        d, like = tokens.shape[1], tokens
-    elif dtokens is not None:
-        d, like = dtokens.shape[1], dtokens
-    else:
-        d, like = 8, None
-    if dtokens is not None:
-        _required(where, Wg=Wg)
+    given = [(logits, f32, (T, E)), (topk_idx, i32, (T, k)), (dlogits, f32, (T, E)),
+             (dtopk_w, f32, (T, k))]
+    names = "logits topk_idx dlogits dtopk_w"
     if dlosses is not None:
-        _required(where, counts=counts, n_valid=n_valid)
-    el = like.dtype if like is not None else None
-    dev = _given(where, None, logits=(logits, f32, (T, E)), topk_idx=(topk_idx, i32, (T, k)),
-                 dlogits=(dlogits, f32, (T, E)), dtopk_w=(dtopk_w, f32, (T, k)),
-                 dlosses=(dlosses, f32, (2,)), counts=(counts, i32, (E,)), n_valid=(n_valid, i32, (1,)),
-                 token_mask=(token_mask, (torch.bool, torch.uint8), (T,)),
-                 workspace=(workspace, torch.uint8, None))
-    if like is not None:
-        _given(where, dev, tokens=(tokens if dWg is not None else None, el, (T, d)),
-               Wg=(Wg if dtokens is not None else None, f32, (d, E)), dWg=(dWg, f32, (d, E)),
-               dtokens=(dtokens, el, (T, d)), dtokens_in=(dtokens_in, el, (T, d)))
-    with _on(dev, stream):
-        _check(get_lib().moe_gate_topk_backward(
-            _ptr(logits), _ptr(topk_idx), _ptr(dtopk_w), _ptr(dlosses), _ptr(counts), _ptr(n_valid),
-            _ptr(token_mask), _ptr(tokens), _ptr(Wg), MOE_F32 if like is None else _dtype(like), T, d,
-            E, k, _ptr(dlogits), _ptr(dWg), _ptr(dtokens_in), _ptr(dtokens), *_ws(workspace),
-            _stream(stream)), where)
+        if counts is None or n_valid is None:
+            _required(where, counts=counts, n_valid=n_valid)
+        given += [(dlosses, f32, (2,)), (counts, i32, (E,)), (n_valid, i32, (1,))]
+        names += " dlosses counts n_valid"
+    if token_mask is not None:
+        given.append((token_mask, _mask_type(where, token_mask), (T,)))
+        names += " token_mask"
+    code, d = MOE_F32, 4
+    if dWg is not None or dtokens is not None:
+        if dWg is not None:
+            _required(where, tokens=tokens)
+        if dtokens is not None:
+            _required(where, Wg=Wg)
+        like = tokens if dWg is not None else dtokens
+        d, el, code = like.shape[1], like.dtype, _dtype(like)
+        given += [(tokens if dWg is not None else None, el, (T, d)),
+                  (Wg if dtokens is not None else None, f32, (d, E)), (dWg, f32, (d, E)),
+                  (dtokens, el, (T, d)), (dtokens_in, el, (T, d)),
+                  (workspace, torch.uint8, None if workspace is None else workspace.shape)]
+        names += " tokens Wg dWg dtokens dtokens_in workspace"
+    dev = _device_of(where, names, given)
+    _call(where, dev, stream, logits.data_ptr(), topk_idx.data_ptr(), _adr(dtopk_w), _adr(dlosses),
+          _adr(counts), _adr(n_valid), _adr(token_mask), _adr(tokens), _adr(Wg), code, T, d, E, k,
+          dlogits.data_ptr(), _adr(dWg), _adr(dtokens_in), _adr(dtokens), _adr(workspace),
+          _ws_bytes(workspace))
 
 
 def moe_combine_backward(dout, expert_out, slot_of, topk_w, dexpert_out=None, dtopk_w=None,
                          stream=None):
+    """Gradient of moe_combine: dexpert_out (topk_w is read) and dtopk_w (expert_out is read)."""
     import torch
     where = "moe_combine_backward"
     T, d = dout.shape
     k = slot_of.shape[1]
-    f32, i32 = torch.float32, torch.int32
+    code, el, f32 = _dtype(dout), dout.dtype, torch.float32
     rows = expert_out if expert_out is not None else dexpert_out
     S_max = rows.shape[0] if rows is not None else 0
-    dev = _given(where, None, dout=(dout, None, (T, d)), slot_of=(slot_of, i32, (T, k)),
-                 expert_out=(expert_out, dout.dtype, (S_max, d)), topk_w=(topk_w, f32, (T, k)),
-                 dexpert_out=(dexpert_out, dout.dtype, (S_max, d)), dtopk_w=(dtopk_w, f32, (T, k)))
-    with _on(dev, stream):
-        _check(get_lib().moe_combine_backward(_ptr(dout), _ptr(expert_out), _ptr(slot_of), _ptr(topk_w),
-                                              _dtype(dout), T, d, k, S_max, _ptr(dexpert_out),
-                                              _ptr(dtopk_w), _stream(stream)), where)
+    dev = _device_of(where, "dout slot_of expert_out topk_w dexpert_out dtopk_w",
+                     ((dout, el, (T, d)), (slot_of, torch.int32, (T, k)), (expert_out, el, (S_max, d)),
+                      (topk_w, f32, (T, k)), (dexpert_out, el, (S_max, d)), (dtopk_w, f32, (T, k))))
+    _call(where, dev, stream, dout.data_ptr(), _adr(expert_out), slot_of.data_ptr(), _adr(topk_w), code,
+          T, d, k, S_max, _adr(dexpert_out), _adr(dtopk_w))
 
 
 def moe_adapter_workspace_size(T, d_in, d_out, r, N, S_max, dtype) -> int:
@@ -378,18 +410,16 @@ def moe_adapter_forward(tokens, perm, offsets, A, B, scale, out, workspace, base
     where = "moe_adapter_forward"
     T, d_in = tokens.shape
     N, _, r = A.shape
-    d_out = B.shape[2]
-    S_max = perm.shape[0]
-    el, f32, i32 = tokens.dtype, torch.float32, torch.int32
-    dev = _given(where, None, tokens=(tokens, None, (T, d_in)), perm=(perm, i32, (S_max,)),
-                 offsets=(offsets, i32, (N + 1,)), A=(A, el, (N, d_in, r)), B=(B, el, (N, r, d_out)),
-                 scale=(scale, f32, (N,)), out=(out, el, (T, d_out)), base=(base, el, (T, d_out)),
-                 hidden=(hidden, f32, (S_max, r)), workspace=(workspace, torch.uint8, None))
-    with _on(dev, stream):
-        _check(get_lib().moe_adapter_forward(_ptr(tokens), _ptr(perm), _ptr(offsets), _ptr(A), _ptr(B),
-                                             _ptr(scale), _ptr(base), _dtype(tokens), T, d_in, d_out, r,
-                                             N, S_max, _ptr(out), _ptr(hidden), *_ws(workspace),
-                                             _stream(stream)), where)
+    d_out, S_max = B.shape[2], perm.shape[0]
+    code, el, f32, i32 = _dtype(tokens), tokens.dtype, torch.float32, torch.int32
+    dev = _device_of(where, "tokens perm offsets A B scale out base hidden workspace",
+                     ((tokens, el, (T, d_in)), (perm, i32, (S_max,)), (offsets, i32, (N + 1,)),
+                      (A, el, (N, d_in, r)), (B, el, (N, r, d_out)), (scale, f32, (N,)),
+                      (out, el, (T, d_out)), (base, el, (T, d_out)), (hidden, f32, (S_max, r)),
+                      (workspace, torch.uint8, workspace.shape)))
+    _call(where, dev, stream, tokens.data_ptr(), perm.data_ptr(), offsets.data_ptr(), A.data_ptr(),
+          B.data_ptr(), scale.data_ptr(), _adr(base), code, T, d_in, d_out, r, N, S_max, out.data_ptr(),
+          _adr(hidden), workspace.data_ptr(), workspace.numel())
 
 
 def moe_adapter_backward(dout, tokens, hidden, perm, offsets, A, B, scale, workspace, dtokens=None,
@@ -400,16 +430,14 @@ def moe_adapter_backward(dout, tokens, hidden, perm, offsets, A, B, scale, works
     T, d_out = dout.shape
     N, d_in, r = A.shape
     S_max = perm.shape[0]
-    el, f32, i32 = dout.dtype, torch.float32, torch.int32
-    dev = _given(where, None, dout=(dout, None, (T, d_out)), tokens=(tokens, el, (T, d_in)),
-                 hidden=(hidden, f32, (S_max, r)), perm=(perm, i32, (S_max,)),
-                 offsets=(offsets, i32, (N + 1,)), A=(A, el, (N, d_in, r)), B=(B, el, (N, r, d_out)),
-                 scale=(scale, f32, (N,)), dtokens=(dtokens, el, (T, d_in)),
-                 dtokens_in=(dtokens_in, el, (T, d_in)), dA=(dA, f32, (N, d_in, r)),
-                 dB=(dB, f32, (N, r, d_out)), workspace=(workspace, torch.uint8, None))
-    with _on(dev, stream):
-        _check(get_lib().moe_adapter_backward(_ptr(dout), _ptr(tokens), _ptr(hidden), _ptr(perm),
-                                              _ptr(offsets), _ptr(A), _ptr(B), _ptr(scale),
-                                              _ptr(dtokens_in), _dtype(dout), T, d_in, d_out, r, N,
-                                              S_max, _ptr(dtokens), _ptr(dA), _ptr(dB), *_ws(workspace),
-                                              _stream(stream)), where)
+    code, el, f32, i32 = _dtype(dout), dout.dtype, torch.float32, torch.int32
+    dev = _device_of(where, "dout perm offsets A B scale tokens hidden dtokens dtokens_in dA dB workspace",
+                     ((dout, el, (T, d_out)), (perm, i32, (S_max,)), (offsets, i32, (N + 1,)),
+                      (A, el, (N, d_in, r)), (B, el, (N, r, d_out)), (scale, f32, (N,)),
+                      (tokens, el, (T, d_in)), (hidden, f32, (S_max, r)), (dtokens, el, (T, d_in)),
+                      (dtokens_in, el, (T, d_in)), (dA, f32, (N, d_in, r)), (dB, f32, (N, r, d_out)),
+                      (workspace, torch.uint8, workspace.shape)))
+    _call(where, dev, stream, dout.data_ptr(), _adr(tokens), _adr(hidden), perm.data_ptr(),
+          offsets.data_ptr(), A.data_ptr(), B.data_ptr(), scale.data_ptr(), _adr(dtokens_in), code, T,
+          d_in, d_out, r, N, S_max, _adr(dtokens), _adr(dA), _adr(dB), workspace.data_ptr(),
+          workspace.numel())

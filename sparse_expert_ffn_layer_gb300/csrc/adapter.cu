@@ -8,23 +8,26 @@
 // once from DRAM and then from L2; 4 r operations per token and column pair stay below the
 // tensor rate for r <= 128.
 //
-// One launch does both products.  A cluster of eight blocks takes a tile of rows of one adapter;
+// Short runs (a few rows per adapter: decode) and 32-bit inputs take one launch for both
+// products.  A cluster of eight blocks takes a tile of 16 rows of one adapter;
 // each block multiplies its eighth of the input columns (so a single token's weights are pulled
 // by eight SMs), the partial h are summed over the cluster through distributed shared memory in
 // rank order (no atomics: equal calls give equal bits), each block receives the whole h and
-// multiplies it into its eighth of the output columns.  Both products run through one ring of
-// asynchronous 128-byte-wide chunks, so the first output chunks (base and Q) load while h is
-// being exchanged.
+// multiplies it into its eighth of the output columns.  Both products of all tiles of a cluster
+// run through one ring of asynchronous 128-byte-wide chunks, so that the first output chunks
+// (base and Q) load while h is being exchanged, and the next tile's rows while this one is
+// written.  Long runs (tiles of 64 rows) take two launches, see there.
 //
 // f16: h keeps 22 bits.  It is scaled by a power of two per row and split into two f16 parts,
 // and the second product adds both (h rounded to one f16 would cost as much accuracy as the
 // rounding of y does, and could overflow).  f32: fused multiply-adds on the CUDA cores.
-//
-// Rows per tile: 64 for long runs of one adapter (weights read from L2 once per 64 rows, the
-// four warps split the rows), 16 for short ones (the warps split the columns of a chunk).
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <cstring>
+#include <map>
+#include <mutex>
+#include <tuple>
 
 #include "launch.h"
 #include "mma.cuh"
@@ -34,42 +37,16 @@ namespace cg = cooperative_groups;
 namespace moe {
 namespace {
 
-constexpr int kThreads = 128;
 constexpr int kCl = 8;                  // blocks per cluster
 constexpr int kRowB = 144;              // bytes per 128-byte chunk row in shared memory
-constexpr int kMaxGroups = 1024;
-
-template <typename T>
-struct Elt {
-  static constexpr int V = 16 / sizeof(T);        // elements per 16 bytes
-  static constexpr int C = 128 / sizeof(T);       // columns per chunk
-};
-
-// Shared-memory plan of one block.
-template <typename T, int MT, int R>
-struct Plan {
-  static constexpr int C = Elt<T>::C, V = Elt<T>::V;
-  static constexpr int kLdR = R + V;                               // rows of R elements
-  static constexpr int kLdC = kRowB / (int)sizeof(T);              // rows of C elements
-  static constexpr int kW = (C * kLdR > R * kLdC ? C * kLdR : R * kLdC) * (int)sizeof(T);
-  static constexpr int kStage = MT * kRowB + kW;
-  static constexpr int kStages = MT == 64 ? (R >= 128 ? 3 : 4) : (R >= 128 ? 4 : R >= 64 ? 6 : 8);
-  static constexpr int kPart = 4 * 16 * R * 4;                     // partial h, f32
-  static constexpr int kH = sizeof(T) == 2 ? MT * (R + 8) * 2 * 2  // h: two f16 parts
-                                           : MT * (R + 4) * 4;     // or f32
-  static constexpr int kOffPart = kStages * kStage;
-  static constexpr int kOffH = kOffPart + kPart;
-  static constexpr int kOffMult = kOffH + kH;
-  static constexpr int kOffTok = kOffMult + MT * 4;
-  static constexpr int kOffTab = kOffTok + MT * 4;                 // offsets and tile starts
-};
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
 // Group boundaries as the kernels use them, and the tile starts.  bound[n] = the largest of
 // offsets[0 .. n], clamped to [0, S_max]: runs never overlap and no slot lies outside the
 // buffers, whatever the offsets say.  start[n] = number of tiles of the groups before n.
-// All threads of the block; N <= 1024.
+// All threads of the block (at most 8 warps); N <= 1024.
+template <int kThreads>
 __device__ __forceinline__ void group_table(const int32_t* __restrict__ offsets, int N, int S_max,
                                             int MT, int* bound, int* start, int* scratch) {
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -116,17 +93,34 @@ __device__ __forceinline__ void group_table(const int32_t* __restrict__ offsets,
   __syncthreads();
 }
 
-// Checks every offset and perm entry and writes the status word (one block, beside the work).
+// The group of a tile: the last n with start[n] <= tile (a group without tiles shares its start
+// with the next one).
+__device__ __forceinline__ int group_of(int tile, const int* start, int N) {
+  int n = 0;
+#pragma unroll
+  for (int step = 512; step > 0; step >>= 1)
+    if (n + step < N && start[n + step] <= tile) n += step;
+  return n;
+}
+
+// Checks every offset and perm entry and writes the status word: one block, beside the work.
 __device__ void check_indices(const int32_t* __restrict__ perm, const int32_t* __restrict__ offsets,
                               int N, int S_max, int T, int* status) {
+  const int step = blockDim.x;
   bool bad = false;
-  for (int i = threadIdx.x; i <= N; i += kThreads) {
+  for (int i = threadIdx.x; i <= N; i += step) {
     const int v = offsets[i];
     bad |= v < 0 || v > S_max || (i > 0 && v < offsets[i - 1]);
   }
   const int S = min(max(offsets[N], 0), S_max);
-  for (int s = min(max(offsets[0], 0), S_max) + threadIdx.x; s < S; s += kThreads)
-    bad |= (unsigned)perm[s] >= (unsigned)T;
+  // eight loads in flight: this loop must not outlast the products
+  for (int64_t s = min(max(offsets[0], 0), S_max) + threadIdx.x; s < S; s += 8 * step) {
+    int v[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = s + q * step < S ? perm[s + q * step] : 0;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) bad |= (unsigned)v[q] >= (unsigned)T;
+  }
   const int any = __syncthreads_or(bad);
   if (threadIdx.x == 0) *status = any ? kErrBounds : kOk;
 }
@@ -145,14 +139,481 @@ struct AdapterArgs {
   int T, dk, dn, r, N, S_max;
 };
 
-template <typename T, int MT, int R, bool kT>
-__global__ void __launch_bounds__(kThreads) adapter_kernel(const AdapterArgs a) {
-  using PL = Plan<T, MT, R>;
-  constexpr int C = PL::C, V = PL::V, NS = PL::kStages;
-  constexpr int kRowGroups = MT / 16;             // warps along rows
-  constexpr int WK = 4 / kRowGroups;              // warps along a chunk's columns
-  constexpr bool kHalf = sizeof(T) == 2;
-  extern __shared__ __align__(128) uint8_t sm[];
+// ---------------------------------------------------------------- f16, long runs
+// Two launches of persistent blocks, h between them in 32 bits (small: r of d columns):
+//   shrink  partial h[part] = x P over a part of the input columns, per tile of 64 rows
+//   expand  h = sum of the parts in order, then y = base + scale h Q per tile and part of the
+//           output columns
+// (As one launch with h exchanged through a cluster's shared memory, each tile waited 15 us or
+// more for two cluster-wide hand-overs: 16384 rows of 3584 columns at r = 64 took 320 us.)
+//
+// Eight warps multiply, and the first of them issues the loads: rows by TMA row gathers through
+// perm, weights as boxes of three-dimensional tensors [N, rows, columns] whose edges read as
+// zeros.  (A loading warp of its own would be the ninth, the third on one of the SM's four
+// register files, which then hold one block instead of two; and with every warp issuing its
+// share of 16-byte copies, their address arithmetic was two thirds of all instructions.)
+constexpr int kTallRows = 64;
+constexpr int kTallWarps = 8, kTallThreads = 32 * kTallWarps;
+constexpr int kChunk = 64;                        // columns per chunk
+
+template <int R>
+struct PlanTall {
+  static constexpr int kStage = kTallRows * 128 + kChunk * R * 2;  // rows, weights
+  static constexpr int kStages = (96 * 1024) / kStage;             // two blocks per SM
+  static constexpr int kOffBar = kStages * kStage;
+  static constexpr int kOffTab = kOffBar + 16 * kStages;           // abort flag, group table
+  static constexpr int kBytes = kOffTab + 8 + 1024;                // with room to align
+};
+
+// Byte offset of 16-byte piece `piece` of row `row` in a swizzled tile of PITCH-byte rows
+// (PITCH 32, 64 or 128: the swizzle of that span).
+template <int PITCH>
+__device__ __forceinline__ int swz(int row, int piece) {
+  const int pat = PITCH == 128 ? row & 7 : PITCH == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
+  return row * PITCH + ((piece ^ pat) << 4);
+}
+
+struct TallArgs {
+  AdapterArgs a;
+  float* partial;            // [parts_k][S_max][r]
+  int parts_k, parts_n;      // column parts of the two products
+};
+
+// The chunks of a block's items, loaded ahead of their use.  Item i is part i % parts of tile
+// i / parts; block b takes items b, b + blocks, ...  kWide: the weights' box has r-wide rows (one
+// per column of the chunk), else chunk-wide rows (r of them).
+template <int R, bool kWide>
+struct TallRing {
+  using PL = PlanTall<R>;
+  static constexpr int NS = PL::kStages, MT = kTallRows, RB = R > 64 ? 64 : R;
+  uint8_t* sm;
+  uint64_t *full, *empty;
+  int *bound, *start;
+  volatile int* abort;
+  int* status;
+  const int32_t* perm;
+  int N, T, chunks, parts, items, blocks;         // blocks: of the grid that take items
+  bool rows_on;                                   // the chunks have rows (base may be absent)
+  const CUtensorMap *mRows, *mW;
+  // use
+  int stage = 0;
+  uint32_t phase = 0;
+  // loads (warp 0)
+  int li, lc = 0, lend = 0, ln = 0, lstage = 0, lrow[4] = {0, 0, 0, 0}, lnext[4] = {0, 0, 0, 0};
+  uint32_t lphase = 1;
+
+  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
+    const bool before = *abort != 0;
+    // a wait that gives up marks the call; the block then runs through without further waits
+    if (!mbar_wait_bounded(bar, parity, abort, nullptr, kDefaultWaitNs) && !before) *status = kErrTimeout;
+  }
+  __device__ __forceinline__ int part_begin(int p) const { return (int)((long long)chunks * p / parts); }
+  __device__ __forceinline__ void fetch_rows(int item) {   // row 0 stands in for none
+    const int lane = threadIdx.x & 31;
+    if (item >= items || lane >= MT / 4) return;
+    const int tile = item / parts, n = group_of(tile, start, N);
+    const int s0 = bound[n] + (tile - start[n]) * MT + 4 * lane;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int t = s0 + q < bound[n + 1] ? perm[s0 + q] : 0;
+      lnext[q] = (unsigned)t < (unsigned)T ? t : 0;
+    }
+  }
+  __device__ __forceinline__ void begin_item() {
+    while (li < items) {
+      const int tile = li / parts, p = li - tile * parts;
+      ln = group_of(tile, start, N);
+      lc = part_begin(p);
+      lend = part_begin(p + 1);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) lrow[q] = lnext[q];
+      fetch_rows(li + blocks);
+      if (lc < lend) return;
+      li += blocks;
+    }
+  }
+  // The next chunk, into the stage whose turn it is (whole warp 0).
+  __device__ __forceinline__ void issue() {
+    if (li >= items || *abort) return;
+    const int lane = threadIdx.x & 31, col = lc * kChunk;
+    uint8_t* st = sm + lstage * PL::kStage;
+    if (lane == 0) {
+      wait(&empty[lstage], lphase);
+      if (!*abort) mbar_expect_tx(&full[lstage], (rows_on ? MT * 128 : 0) + kChunk * R * 2);
+    }
+    __syncwarp();
+    if (*abort) return;                           // no further loads
+    if (rows_on && lane < MT / 4)
+      tma_gather4(st + lane * 512, mRows, col, lrow[0], lrow[1], lrow[2], lrow[3], &full[lstage]);
+    if (lane == 16) {
+      uint8_t* ws = st + MT * 128;
+      if (kWide) {
+#pragma unroll
+        for (int b = 0; b < R; b += RB) tma_load_3d(ws + b * kChunk * 2, mW, b, col, ln, &full[lstage]);
+      } else {
+        tma_load_3d(ws, mW, col, 0, ln, &full[lstage]);
+      }
+    }
+    if (++lstage == NS) {
+      lstage = 0;
+      lphase ^= 1u;
+    }
+    if (++lc == lend) {
+      li += blocks;
+      begin_item();
+    }
+  }
+  __device__ __forceinline__ void begin() {
+    li = blockIdx.x;
+    if (threadIdx.x < 32) {
+      fetch_rows(li);
+      begin_item();
+      for (int c = 0; c < NS - 1; ++c) issue();
+    }
+  }
+  __device__ __forceinline__ uint8_t* next() {    // the chunk that is used next
+    if (threadIdx.x < 32) issue();
+    wait(&full[stage], phase);
+    return sm + stage * PL::kStage;
+  }
+  __device__ __forceinline__ void done() {        // this warp has read (and written) it
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[stage]);
+    if (++stage == NS) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// Shared-memory set-up of both kernels; returns the number of tiles.
+template <int R, bool kWide>
+__device__ __forceinline__ int tall_setup(TallRing<R, kWide>& ring, const AdapterArgs& a, uint8_t* raw) {
+  using PL = PlanTall<R>;
+  // swizzled tiles start on 1024 bytes
+  uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  ring.sm = sm;
+  ring.full = reinterpret_cast<uint64_t*>(sm + PL::kOffBar);
+  ring.empty = ring.full + PL::kStages;
+  int* flag = reinterpret_cast<int*>(sm + PL::kOffTab);
+  ring.abort = flag;
+  ring.bound = flag + 2;
+  ring.start = ring.bound + a.N + 1;
+  ring.status = a.status;
+  ring.perm = a.perm;
+  ring.N = a.N;
+  ring.T = a.T;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < PL::kStages; ++i) {
+      mbar_init(&ring.full[i], 1);
+      mbar_init(&ring.empty[i], kTallWarps);
+    }
+    fence_mbar_init();
+    *flag = 0;
+  }
+  group_table<kTallThreads>(a.offsets, a.N, a.S_max, kTallRows, ring.bound, ring.start,
+                            ring.start + a.N + 1);
+  return ring.start[a.N];
+}
+
+template <int R, bool kT>
+__global__ void __launch_bounds__(kTallThreads, 2)
+    adapter_shrink_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mP,
+                          const TallArgs ta) {
+  const AdapterArgs& a = ta.a;
+  constexpr int MT = kTallRows, RB = R > 64 ? 64 : R;
+  constexpr int WN = R >= 32 ? 2 : 1, WK = 2 / WN;   // two warps per 16 rows: along r, or the chunk
+  constexpr int NF = R / WN / 8;                     // 8-column fragments of h per warp
+  extern __shared__ uint8_t raw[];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  pdl_trigger();
+  if (blockIdx.x == gridDim.x - 1) {              // the last block checks the indices
+    check_indices(a.perm, a.offsets, a.N, a.S_max, a.T, a.status);
+    return;
+  }
+  TallRing<R, !kT> ring;
+  const int ntiles = tall_setup(ring, a, raw);
+  ring.mRows = &mX;
+  ring.mW = &mP;
+  ring.rows_on = true;
+  ring.chunks = (a.dk + kChunk - 1) / kChunk;
+  ring.parts = ta.parts_k;
+  ring.items = ntiles * ring.parts;
+  ring.blocks = gridDim.x - 1;
+  ring.begin();
+  const int wr = (w & 3) * 16, wc = w >> 2, h0 = WN > 1 ? wc * (R / WN) : 0;
+  const int l15 = lane & 15, lh = lane >> 4, l3 = (lane >> 3) & 1, l7 = lane & 7;
+  float* pair = reinterpret_cast<float*>(ring.start + a.N + 1 + 32);   // WK > 1: [MT][R]
+  for (int item = blockIdx.x; item < ring.items; item += ring.blocks) {
+    const int tile = item / ring.parts, part = item - tile * ring.parts;
+    const int n = group_of(tile, ring.start, a.N);
+    const int s0 = ring.bound[n] + (tile - ring.start[n]) * MT, s1 = ring.bound[n + 1];
+    float acc[NF][4];
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    const int c1 = ring.part_begin(part + 1);
+    for (int c = ring.part_begin(part); c < c1; ++c) {
+      const uint8_t* xs = ring.next();
+      const uint8_t* ps = xs + MT * 128;
+      // The tensor cores' additions truncate: a chain of n of them loses up to n / 2^23 of the
+      // sum, always towards zero.  Chains end with every chunk and are added with rounding
+      // (8192 columns in chains of 64: 3e-5 of the result; this way 2e-6).
+      float run[NF][4];
+#pragma unroll
+      for (int i = 0; i < NF; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) run[i][j] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < 4 / WK; ++kk) {
+        const int k = WK > 1 ? kk * WK + wc : kk;                // k-step of 16
+        uint32_t fa[4];
+        ldsm4(fa, xs + swz<128>(wr + l15, 2 * k + lh));
+#pragma unroll
+        for (int j = 0; j < NF / 2; ++j) {
+          uint32_t fb[4];
+          if (kT) {
+            ldsm4(fb, ps + swz<128>(h0 + j * 16 + l7 + lh * 8, 2 * k + l3));
+          } else {
+            const int col = h0 + j * 16;
+            ldsm4_t(fb, ps + (col / 64) * (kChunk * 128) + swz<RB * 2>(k * 16 + l15, (col % 64) / 8 + lh));
+          }
+          mma16816(run[2 * j], fa, fb[0], fb[1]);
+          mma16816(run[2 * j + 1], fa, fb[2], fb[3]);
+        }
+      }
+      ring.done();
+#pragma unroll
+      for (int i = 0; i < NF; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] += run[i][j];
+    }
+    if (WK > 1) {                                 // the two warps of the same rows
+      float* p = pair + (wr + (lane >> 2)) * R + 2 * (lane & 3);
+      if (wc == 1) {
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+          *reinterpret_cast<float2*>(p + 8 * j) = make_float2(acc[j][0], acc[j][1]);
+          *reinterpret_cast<float2*>(p + 8 * R + 8 * j) = make_float2(acc[j][2], acc[j][3]);
+        }
+      }
+      __syncthreads();
+      if (wc == 0) {
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+          const float2 u = *reinterpret_cast<const float2*>(p + 8 * j);
+          const float2 v = *reinterpret_cast<const float2*>(p + 8 * R + 8 * j);
+          acc[j][0] += u.x; acc[j][1] += u.y; acc[j][2] += v.x; acc[j][3] += v.y;
+        }
+      }
+      __syncthreads();
+    }
+    if (WK == 1 || wc == 0) {
+      const int sa = s0 + wr + (lane >> 2), sb = sa + 8;
+      float* pa = ta.partial + ((size_t)part * a.S_max + sa) * a.r;
+      float* pb = pa + (size_t)8 * a.r;
+#pragma unroll
+      for (int j = 0; j < NF; ++j) {
+        const int col = h0 + 8 * j + 2 * (lane & 3);
+        if (col < a.r) {
+          if (sa < s1) *reinterpret_cast<float2*>(pa + col) = make_float2(acc[j][0], acc[j][1]);
+          if (sb < s1) *reinterpret_cast<float2*>(pb + col) = make_float2(acc[j][2], acc[j][3]);
+        }
+      }
+    }
+  }
+}
+
+template <int R, bool kT>
+__global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
+    adapter_expand_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mBase,
+                          const TallArgs ta) {
+  const AdapterArgs& a = ta.a;
+  constexpr int MT = kTallRows, RB = R > 64 ? 64 : R;
+  extern __shared__ uint8_t raw[];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const bool with_base = a.base != nullptr;
+  TallRing<R, kT> ring;
+  const int ntiles = tall_setup(ring, a, raw);
+  ring.mRows = &mBase;
+  ring.mW = &mQ;
+  ring.rows_on = with_base;
+  ring.chunks = (a.dn + kChunk - 1) / kChunk;
+  ring.parts = ta.parts_n;
+  ring.items = ntiles * ring.parts;
+  ring.blocks = gridDim.x;
+  ring.begin();                                   // base and Q are inputs of the call
+  pdl_wait();                                     // the partial h are complete
+  __half* Y = static_cast<__half*>(a.y);
+  const int wr = (w & 3) * 16, wc = w >> 2;
+  const int l15 = lane & 15, lh = lane >> 4, l3 = (lane >> 3) & 1, l7 = lane & 7;
+  // rows that this thread writes: two of its warp's 16, one 16-byte piece each
+  const int yrow = wr + (lane >> 2), ypc = wc * 4 + (lane & 3);
+  for (int item = blockIdx.x; item < ring.items; item += ring.blocks) {
+    const int tile = item / ring.parts, part = item - tile * ring.parts;
+    const int n = group_of(tile, ring.start, a.N);
+    const int s0 = ring.bound[n] + (tile - ring.start[n]) * MT, s1 = ring.bound[n + 1];
+    int y0 = s0 + yrow < s1 ? a.perm[s0 + yrow] : -1, y1 = s0 + yrow + 8 < s1 ? a.perm[s0 + yrow + 8] : -1;
+    if ((unsigned)y0 >= (unsigned)a.T) y0 = -1;
+    if ((unsigned)y1 >= (unsigned)a.T) y1 = -1;
+    // ---- h in the layout of the product's left operand: rows g and g + 8, columns
+    // 16 k + 2 (lane % 4) + {0, 1, 8, 9}; a row's columns are spread over four lanes
+    uint32_t fh[R / 16][4], fl[R / 16][4];
+    float m0, m1;
+    {
+      const int sa = s0 + wr + (lane >> 2), sb = sa + 8;
+      float2 v[R / 16][4];
+#pragma unroll
+      for (int k = 0; k < R / 16; ++k)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[k][q] = make_float2(0.f, 0.f);
+      for (int p = 0; p < ta.parts_k; ++p) {
+        const float* src = ta.partial + (size_t)p * a.S_max * a.r;
+#pragma unroll
+        for (int k = 0; k < R / 16; ++k)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int s = q & 1 ? sb : sa, col = 16 * k + 8 * (q >> 1) + 2 * (lane & 3);
+            if (s < s1 && col < a.r) {
+              const float2 u = *reinterpret_cast<const float2*>(src + (size_t)s * a.r + col);
+              v[k][q].x += u.x;
+              v[k][q].y += u.y;
+            }
+          }
+      }
+      float ma = 0.f, mb = 0.f;
+      bool oa = false, ob = false;
+#pragma unroll
+      for (int k = 0; k < R / 16; ++k)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float m = fmaxf(fabsf(v[k][q].x), fabsf(v[k][q].y));
+          const bool odd = !isfinite(v[k][q].x) || !isfinite(v[k][q].y);
+          if (q & 1) {
+            mb = fmaxf(mb, m);
+            ob |= odd;
+          } else {
+            ma = fmaxf(ma, m);
+            oa |= odd;
+          }
+          if (a.hidden && part == 0 && wc == 0 && ta.partial != a.hidden) {
+            const int s = q & 1 ? sb : sa, col = 16 * k + 8 * (q >> 1) + 2 * (lane & 3);
+            if (s < s1 && col < a.r)
+              *reinterpret_cast<float2*>(a.hidden + (size_t)s * a.r + col) = v[k][q];
+          }
+        }
+      if (oa) ma = INFINITY;                      // a row with infinities is not scaled
+      if (ob) mb = INFINITY;
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
+        mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+      }
+      const int ea = scale_exp(ma), eb = scale_exp(mb);
+      const float ia = exp2_int(-ea), ib = exp2_int(-eb), sc = a.scale[n];
+      m0 = sc * exp2_int(ea);
+      m1 = sc * exp2_int(eb);
+#pragma unroll
+      for (int k = 0; k < R / 16; ++k)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float i = q & 1 ? ib : ia;
+          __half2 hi, lo;
+          split_f16(v[k][q].x * i, hi.x, lo.x);
+          split_f16(v[k][q].y * i, hi.y, lo.y);
+          fh[k][q] = *reinterpret_cast<const uint32_t*>(&hi);
+          fl[k][q] = *reinterpret_cast<const uint32_t*>(&lo);
+        }
+    }
+    // ---- 32 of a chunk's 64 columns per warp
+    const int c1 = ring.part_begin(part + 1);
+    for (int c = ring.part_begin(part); c < c1; ++c) {
+      uint8_t* bs = ring.next();
+      const uint8_t* qs = bs + MT * 128;
+      float acc[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll
+      for (int k = 0; k < R / 16; ++k)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t fb[4];
+          if (kT)
+            ldsm4(fb, qs + (k / 4) * (kChunk * 128) +
+                          swz<RB * 2>(wc * 32 + j * 16 + l7 + lh * 8, 2 * (k % 4) + l3));
+          else
+            ldsm4_t(fb, qs + swz<128>(k * 16 + l15, wc * 4 + j * 2 + lh));
+          mma16816(acc[2 * j], fl[k], fb[0], fb[1]);
+          mma16816(acc[2 * j + 1], fl[k], fb[2], fb[3]);
+          mma16816(acc[2 * j], fh[k], fb[0], fb[1]);
+          mma16816(acc[2 * j + 1], fh[k], fb[2], fb[3]);
+        }
+      // base + scale * sum, rounded once, in place; then 16-byte rows out
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint8_t* at = bs + swz<128>(wr + l15, wc * 4 + j * 2 + lh);
+        uint32_t b[4] = {0u, 0u, 0u, 0u};
+        if (with_base) ldsm4(b, at);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {             // b[q]: rows + 8 (q & 1), columns + 8 (q >> 1)
+          const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&b[q]));
+          const float mm = q & 1 ? m1 : m0;
+          const __half2 o = __floats2half2_rn(fmaf(mm, acc[2 * j + (q >> 1)][2 * (q & 1)], u.x),
+                                              fmaf(mm, acc[2 * j + (q >> 1)][2 * (q & 1) + 1], u.y));
+          b[q] = *reinterpret_cast<const uint32_t*>(&o);
+        }
+        stsm4(at, b);
+      }
+      __syncwarp();
+      const int col = c * kChunk + ypc * 8;
+      if (col < a.dn) {
+        if (y0 >= 0)
+          *reinterpret_cast<uint4*>(Y + (size_t)y0 * a.dn + col) =
+              *reinterpret_cast<const uint4*>(bs + swz<128>(yrow, ypc));
+        if (y1 >= 0)
+          *reinterpret_cast<uint4*>(Y + (size_t)y1 * a.dn + col) =
+              *reinterpret_cast<const uint4*>(bs + swz<128>(yrow + 8, ypc));
+      }
+      // the stage was written here and is next written by TMA
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      ring.done();
+    }
+  }
+}
+
+// ---------------------------------------------------------------- f16, short runs
+// Tiles of 16 rows, four warps that load and multiply.
+template <int MT, int R>
+struct Plan16 {
+  static constexpr int kThreads = MT == 64 ? 256 : 128;
+  static constexpr int kWarps = kThreads / 32;
+  static constexpr int kBlocks = R >= 128 ? (MT == 64 ? 1 : 2) : MT == 64 ? 2 : 4;  // per SM
+  static constexpr int C = 64;                                     // columns per chunk
+  static constexpr int kLdC = kRowB / 2, kLdR = R + 8;             // halves per row
+  static constexpr int WR = MT / 16, WC = kWarps / WR;             // warps along rows / columns
+  static constexpr int WN = R / WC >= 16 ? WC : 1;                 // first product: along r,
+  static constexpr int WK = WC / WN;                               // or along a chunk's columns
+  static constexpr int kW = 2 * (C * kLdR > R * kLdC ? C * kLdR : R * kLdC);
+  static constexpr int kStage = MT * kRowB + kW;
+  static constexpr int kStages = MT == 64 ? (R >= 128 ? 3 : 4) : (R >= 128 ? 4 : R >= 64 ? 6 : 8);
+  static constexpr int kOffPart = kStages * kStage;                // partial h [WK][MT][R]
+  static constexpr int kOffH = kOffPart + WK * MT * R * 4;         // h: two f16 parts
+  static constexpr int kOffMult = kOffH + MT * kLdR * 4;
+  static constexpr int kOffTab = kOffMult + MT * 4;                // offsets, tile starts, scratch
+};
+
+template <int MT, int R, bool kT>
+__global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlocks)
+    adapter_f16_kernel(const AdapterArgs a) {
+  using PL = Plan16<MT, R>;
+  constexpr int NT = PL::kThreads, NS = PL::kStages, C = PL::C, WC = PL::WC, WN = PL::WN, WK = PL::WK;
+  constexpr int kLdC = PL::kLdC, kLdR = PL::kLdR;
+  constexpr int XP = MT * 8 / NT;                 // 16-byte pieces of x (or base) per thread and chunk
+  constexpr int WP = R * 8 / NT > 0 ? R * 8 / NT : 1;             // of P or Q
+  extern __shared__ __align__(16) uint8_t sm[];
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank();
   const int cid = blockIdx.x / kCl, ncl = gridDim.x / kCl - 1;
@@ -161,33 +622,355 @@ __global__ void __launch_bounds__(kThreads) adapter_kernel(const AdapterArgs a) 
     if (rank == 0) check_indices(a.perm, a.offsets, a.N, a.S_max, a.T, a.status);
     return;
   }
-  float* part = reinterpret_cast<float*>(sm + PL::kOffPart);      // [WK][MT][R]
-  __half* hhi = reinterpret_cast<__half*>(sm + PL::kOffH);        // [MT][R + 8]
-  __half* hlo = hhi + MT * (R + 8);
-  float* hf = reinterpret_cast<float*>(sm + PL::kOffH);           // f32: [MT][R + 4]
+  float* part = reinterpret_cast<float*>(sm + PL::kOffPart);
+  __half* hhi = reinterpret_cast<__half*>(sm + PL::kOffH);        // [MT][R + 8], then lo
+  __half* hlo = hhi + MT * kLdR;
   float* mult = reinterpret_cast<float*>(sm + PL::kOffMult);
-  int* tok = reinterpret_cast<int*>(sm + PL::kOffTok);
   int* bound = reinterpret_cast<int*>(sm + PL::kOffTab);
   int* start = bound + a.N + 1;
-  int* scratch = start + a.N + 1;
-  group_table(a.offsets, a.N, a.S_max, MT, bound, start, scratch);
+  group_table<NT>(a.offsets, a.N, a.S_max, MT, bound, start, start + a.N + 1);
   const int ntiles = start[a.N];
 
   const int ck = (a.dk + C - 1) / C, cn = (a.dn + C - 1) / C;
   const int k0 = (int)((long long)ck * rank / kCl), k1 = (int)((long long)ck * (rank + 1) / kCl);
   const int n0 = (int)((long long)cn * rank / kCl), n1 = (int)((long long)cn * (rank + 1) / kCl);
   const int nk = k1 - k0, total = nk + n1 - n0;
-  const T* X = static_cast<const T*>(a.x);
-  const T* base = static_cast<const T*>(a.base);
-  T* Y = static_cast<T*>(a.y);
-  const int wr = (w % kRowGroups) * 16, wk = w / kRowGroups;
+  const __half* X = static_cast<const __half*>(a.x);
+  const __half* base = static_cast<const __half*>(a.base);
+  __half* Y = static_cast<__half*>(a.y);
+
+  // Token of row `row` of a tile, -1 where there is none.
+  auto token = [&](int tile, int row) {
+    if (tile >= ntiles) return -1;
+    const int n = group_of(tile, start, a.N);
+    const int s = bound[n] + (tile - start[n]) * MT + row;
+    if (s >= bound[n + 1]) return -1;
+    const int t = a.perm[s];
+    return (unsigned)t < (unsigned)a.T ? t : -1;
+  };
+
+  // ---- loader: runs NS - 1 chunks ahead, across tiles.  Its rows' tokens are fetched a tile early.
+  const int lrow = tid >> 3, lpc = (tid & 7) * 8;
+  int ltile = cid, lc = 0, ls = 0, ltok[XP], lnext[XP];
+  const __half *lP = nullptr, *lQ = nullptr;
+  auto begin_tile = [&]() {
+#pragma unroll
+    for (int p = 0; p < XP; ++p) {
+      ltok[p] = lnext[p];
+      lnext[p] = token(ltile + ncl, lrow + p * (NT / 8));
+    }
+    if (ltile < ntiles) {
+      const int n = group_of(ltile, start, a.N);
+      lP = static_cast<const __half*>(a.P) + (size_t)n * a.dk * a.r;
+      lQ = static_cast<const __half*>(a.Q) + (size_t)n * a.dn * a.r;
+    }
+  };
+  auto issue = [&]() {
+    if (ltile < ntiles && total > 0) {
+      uint8_t* st = sm + ls * PL::kStage;
+      const bool first = lc < nk;
+      const int col0 = (first ? k0 + lc : n0 + lc - nk) * C;
+      const int d = first ? a.dk : a.dn;
+      const __half* rowsrc = first ? X : base;
+      if (rowsrc) {
+        const bool in = col0 + lpc < d;
+#pragma unroll
+        for (int p = 0; p < XP; ++p) {
+          const bool on = in && ltok[p] >= 0;
+          cp_async16(st + (lrow + p * (NT / 8)) * kRowB + lpc * 2,
+                     rowsrc + (on ? (size_t)ltok[p] * d + col0 + lpc : 0), on);
+        }
+      }
+      __half* ws = reinterpret_cast<__half*>(st + MT * kRowB);
+      const __half* W = first ? lP : lQ;
+      if (first != kT) {                          // rows of the chunk's columns, r wide
+        constexpr int RV = R / 8;
+        const int row = tid / RV, col = (tid % RV) * 8;
+        const __half* src = W + (size_t)(col0 + row) * a.r + col;
+#pragma unroll
+        for (int p = 0; p < WP; ++p) {
+          const bool on = col < a.r && col0 + row + p * (NT / RV) < d;
+          if (row + p * (NT / RV) < C)
+            cp_async16(ws + (row + p * (NT / RV)) * kLdR + col,
+                       on ? src + (size_t)p * (NT / RV) * a.r : W, on);
+        }
+      } else {                                    // r rows, the chunk's columns wide
+        const bool in = col0 + lpc < d;
+        const __half* src = W + (size_t)lrow * d + col0 + lpc;
+#pragma unroll
+        for (int p = 0; p < WP; ++p) {
+          const bool on = in && lrow + p * (NT / 8) < a.r;
+          if (lrow + p * (NT / 8) < R)
+            cp_async16(ws + (lrow + p * (NT / 8)) * kLdC + lpc,
+                       on ? src + (size_t)p * (NT / 8) * d : W, on);
+        }
+      }
+      if (++lc == total) {
+        lc = 0;
+        ltile += ncl;
+        begin_tile();
+      }
+    }
+    cp_async_commit();
+    ls = ls + 1 == NS ? 0 : ls + 1;
+  };
+#pragma unroll
+  for (int p = 0; p < XP; ++p) lnext[p] = token(ltile, lrow + p * (NT / 8));
+  begin_tile();
+  for (int c = 0; c < NS - 1; ++c) issue();
+  int cs = 0;                                     // stage of the chunk that is used next
+  auto advance = [&]() {                          // it is complete; one more load is issued
+    cp_async_wait<NS - 2>();
+    __syncthreads();
+    issue();
+    const uint8_t* st = sm + cs * PL::kStage;
+    cs = cs + 1 == NS ? 0 : cs + 1;
+    return reinterpret_cast<const __half*>(st);
+  };
+
+  const int wr = (w % PL::WR) * 16, wc = w / PL::WR;
+  // rows that this thread writes: RPT rows of its warp's 16, one 16-byte piece each
+  constexpr int LPR = 64 / WC / 8, RPT = 16 * LPR / 32;
+  const int yrow = wr + lane / LPR, ycol = wc * (64 / WC) + (lane % LPR) * 8;
+  int ynext[RPT];
+#pragma unroll
+  for (int p = 0; p < RPT; ++p) ynext[p] = token(cid, yrow + p * (32 / LPR));
 
   for (int tile = cid; tile < ntiles; tile += ncl) {
-    // the group of this tile: the last n with start[n] <= tile
-    int n = 0;
-    for (int step = 512; step > 0; step >>= 1)
-      if (n + step < a.N && start[n + step] <= tile) n += step;
-    // groups without tiles share their start with the next one: the last is the one that has it
+    const int n = group_of(tile, start, a.N);
+    const int s0 = bound[n] + (tile - start[n]) * MT;
+    const int rows = min(MT, bound[n + 1] - s0);
+    int ytok[RPT];
+#pragma unroll
+    for (int p = 0; p < RPT; ++p) {
+      ytok[p] = ynext[p];
+      ynext[p] = token(tile + ncl, yrow + p * (32 / LPR));
+    }
+
+    // ---- first product: partial h of this block's input columns.
+    // The tensor cores' additions truncate: a chain of n of them loses up to n / 2^23 of the sum,
+    // always towards zero.  Chains end after a few products and are added to 32-bit sums with
+    // rounding (8192 columns in one chain per block: 3e-5 of the result; this way below 3e-6).
+    {
+      constexpr int NF = R / WN / 8;              // 8-column fragments of h per warp
+      float acc[NF][4], run[NF][4];
+#pragma unroll
+      for (int i = 0; i < NF; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = run[i][j] = 0.f;
+      const int h0 = WN > 1 ? wc * (R / WN) : 0;
+      for (int c = 0; c < nk; ++c) {
+        const __half* xs = advance();
+        const __half* ps = xs + MT * kLdC;
+#pragma unroll
+        for (int kk = 0; kk < 4 / WK; ++kk) {
+          const int k = (WK > 1 ? kk * WK + wc : kk) * 16;
+          uint32_t fa[4];
+          frag_a(fa, xs + wr * kLdC + k, kLdC, lane);
+#pragma unroll
+          for (int j = 0; j < NF / 2; ++j) {
+            uint32_t fb[4];
+            if (kT)
+              frag_b_nk(fb, ps + (h0 + j * 16) * kLdC + k, kLdC, lane);
+            else
+              frag_b_kn(fb, ps + k * kLdR + h0 + j * 16, kLdR, lane);
+            mma16816(run[2 * j], fa, fb[0], fb[1]);
+            mma16816(run[2 * j + 1], fa, fb[2], fb[3]);
+          }
+        }
+        if (c % WK == WK - 1 || c == nk - 1) {
+#pragma unroll
+          for (int i = 0; i < NF; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              acc[i][j] += run[i][j];
+              run[i][j] = 0.f;
+            }
+        }
+      }
+      float* p = part + ((WK > 1 ? wc : 0) * MT + wr + (lane >> 2)) * R + h0 + 2 * (lane & 3);
+#pragma unroll
+      for (int j = 0; j < NF; ++j) {
+        *reinterpret_cast<float2*>(p + 8 * j) = make_float2(acc[j][0], acc[j][1]);
+        *reinterpret_cast<float2*>(p + 8 * R + 8 * j) = make_float2(acc[j][2], acc[j][3]);
+      }
+    }
+    if (WK > 1) {                                 // the warps' shares of the block
+      __syncthreads();
+      for (int i = tid; i < MT * R; i += NT) {
+        float v = part[i];
+#pragma unroll
+        for (int q = 1; q < WK; ++q) v += part[q * MT * R + i];
+        part[i] = v;
+      }
+    }
+    cl.sync();
+
+    // ---- h: this block sums rows rank * MT / 8 .. over the cluster and gives them to all
+    if (tid < MT) {                               // eight threads per row, R / 8 columns each
+      constexpr int CPT = R / 8;
+      const int row = rank * (MT / kCl) + (tid >> 3), c0 = (tid & 7) * CPT;
+      float v[CPT];
+#pragma unroll
+      for (int j = 0; j < CPT; ++j) v[j] = 0.f;
+#pragma unroll
+      for (int q = 0; q < kCl; ++q) {
+        const float* src = cl.map_shared_rank(part, q) + row * R + c0;
+#pragma unroll
+        for (int j = 0; j < CPT; j += 2) {
+          const float2 u = *reinterpret_cast<const float2*>(src + j);
+          v[j] += u.x;
+          v[j + 1] += u.y;
+        }
+      }
+      if (a.hidden && row < rows) {
+        float* dst = a.hidden + (size_t)(s0 + row) * a.r;
+#pragma unroll
+        for (int j = 0; j < CPT; ++j)
+          if (c0 + j < a.r) dst[c0 + j] = v[j];
+      }
+      float m = 0.f;
+      bool odd = false;
+#pragma unroll
+      for (int j = 0; j < CPT; ++j) {
+        m = fmaxf(m, fabsf(v[j]));
+        odd |= !isfinite(v[j]);
+      }
+      if (odd) m = INFINITY;                      // such a row is not scaled
+      const unsigned grp = 0xffu << (lane & 24);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(grp, m, o));
+      const int e = scale_exp(m);
+      const float inv = exp2_int(-e);
+      __half2 hi[CPT / 2], lo[CPT / 2];
+#pragma unroll
+      for (int j = 0; j < CPT; j += 2) {
+        split_f16(v[j] * inv, hi[j / 2].x, lo[j / 2].x);
+        split_f16(v[j + 1] * inv, hi[j / 2].y, lo[j / 2].y);
+      }
+      const float mu = a.scale[n] * exp2_int(e);
+#pragma unroll
+      for (int q = 0; q < kCl; ++q) {
+        __half* dh = cl.map_shared_rank(hhi, q) + row * kLdR + c0;
+        __half* dl = cl.map_shared_rank(hlo, q) + row * kLdR + c0;
+#pragma unroll
+        for (int j = 0; j < CPT / 2; ++j) {
+          reinterpret_cast<__half2*>(dh)[j] = hi[j];
+          reinterpret_cast<__half2*>(dl)[j] = lo[j];
+        }
+        if ((tid & 7) == 0) cl.map_shared_rank(mult, q)[row] = mu;
+      }
+    }
+    cl.sync();
+
+    // ---- second product: this block's output columns
+    constexpr int NF = 8 / WC;                    // 8-column fragments of a chunk per warp
+    const int c0 = wc * NF * 8;
+    uint32_t fh[R / 16][4], fl[R / 16][4];
+#pragma unroll
+    for (int k = 0; k < R / 16; ++k) {
+      frag_a(fh[k], hhi + wr * kLdR + k * 16, kLdR, lane);
+      frag_a(fl[k], hlo + wr * kLdR + k * 16, kLdR, lane);
+    }
+    const int g = lane >> 2, q2 = 2 * (lane & 3);
+    const float m0 = mult[wr + g], m1 = mult[wr + g + 8];
+    for (int c = n0; c < n1; ++c) {
+      __half* bs = const_cast<__half*>(advance());
+      const __half* qs = bs + MT * kLdC;
+      float acc[NF][4];
+#pragma unroll
+      for (int i = 0; i < NF; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll
+      for (int k = 0; k < R / 16; ++k)
+#pragma unroll
+        for (int j = 0; j < NF / 2; ++j) {
+          uint32_t fb[4];
+          if (kT)
+            frag_b_nk(fb, qs + (c0 + j * 16) * kLdR + k * 16, kLdR, lane);
+          else
+            frag_b_kn(fb, qs + k * 16 * kLdC + c0 + j * 16, kLdC, lane);
+          mma16816(acc[2 * j], fl[k], fb[0], fb[1]);
+          mma16816(acc[2 * j + 1], fl[k], fb[2], fb[3]);
+          mma16816(acc[2 * j], fh[k], fb[0], fb[1]);
+          mma16816(acc[2 * j + 1], fh[k], fb[2], fb[3]);
+        }
+      // base + scale * sum, rounded once, in place; then 16-byte rows out
+#pragma unroll
+      for (int j = 0; j < NF; ++j) {
+        __half2* b0 = reinterpret_cast<__half2*>(bs + (wr + g) * kLdC + c0 + 8 * j + q2);
+        __half2* b1 = reinterpret_cast<__half2*>(bs + (wr + g + 8) * kLdC + c0 + 8 * j + q2);
+        float2 u = make_float2(0.f, 0.f), v = u;
+        if (base) {
+          u = __half22float2(*b0);
+          v = __half22float2(*b1);
+        }
+        *b0 = __floats2half2_rn(fmaf(m0, acc[j][0], u.x), fmaf(m0, acc[j][1], u.y));
+        *b1 = __floats2half2_rn(fmaf(m1, acc[j][2], v.x), fmaf(m1, acc[j][3], v.y));
+      }
+      __syncwarp();
+      const int col = c * C + ycol;
+      if (col < a.dn) {
+#pragma unroll
+        for (int p = 0; p < RPT; ++p)
+          if (ytok[p] >= 0)
+            *reinterpret_cast<uint4*>(Y + (size_t)ytok[p] * a.dn + col) =
+                *reinterpret_cast<const uint4*>(bs + (yrow + p * (32 / LPR)) * kLdC + ycol);
+      }
+    }
+  }
+  cp_async_wait<0>();
+}
+
+// ---------------------------------------------------------------- f32
+template <int R>
+struct Plan32 {
+  static constexpr int MT = 16, kThreads = 128, C = 32;
+  static constexpr int kLdC = kRowB / 4, kLdR = R + 4;
+  static constexpr int kW = 4 * (C * kLdR > R * kLdC ? C * kLdR : R * kLdC);
+  static constexpr int kStage = MT * kRowB + kW;
+  static constexpr int kStages = R >= 128 ? 4 : R >= 64 ? 6 : 8;
+  static constexpr int kOffPart = kStages * kStage;
+  static constexpr int kOffH = kOffPart + MT * R * 4;
+  static constexpr int kOffMult = kOffH + MT * kLdR * 4;
+  static constexpr int kOffTok = kOffMult + MT * 4;
+  static constexpr int kOffTab = kOffTok + MT * 4;
+};
+
+template <int R, bool kT>
+__global__ void __launch_bounds__(128) adapter_f32_kernel(const AdapterArgs a) {
+  using PL = Plan32<R>;
+  constexpr int MT = PL::MT, C = PL::C, NS = PL::kStages, NT = PL::kThreads;
+  constexpr int kLdC = PL::kLdC, kLdR = PL::kLdR;
+  extern __shared__ __align__(16) uint8_t sm[];
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = (int)cl.block_rank();
+  const int cid = blockIdx.x / kCl, ncl = gridDim.x / kCl - 1;
+  const int tid = threadIdx.x;
+  if (cid == ncl) {                               // the last cluster checks the indices
+    if (rank == 0) check_indices(a.perm, a.offsets, a.N, a.S_max, a.T, a.status);
+    return;
+  }
+  float* part = reinterpret_cast<float*>(sm + PL::kOffPart);      // [MT][R]
+  float* hf = reinterpret_cast<float*>(sm + PL::kOffH);           // [MT][R + 4]
+  float* mult = reinterpret_cast<float*>(sm + PL::kOffMult);
+  int* tok = reinterpret_cast<int*>(sm + PL::kOffTok);
+  int* bound = reinterpret_cast<int*>(sm + PL::kOffTab);
+  int* start = bound + a.N + 1;
+  group_table<NT>(a.offsets, a.N, a.S_max, MT, bound, start, start + a.N + 1);
+  const int ntiles = start[a.N];
+
+  const int ck = (a.dk + C - 1) / C, cn = (a.dn + C - 1) / C;
+  const int k0 = (int)((long long)ck * rank / kCl), k1 = (int)((long long)ck * (rank + 1) / kCl);
+  const int n0 = (int)((long long)cn * rank / kCl), n1 = (int)((long long)cn * (rank + 1) / kCl);
+  const int nk = k1 - k0, total = nk + n1 - n0;
+  const float* X = static_cast<const float*>(a.x);
+  const float* base = static_cast<const float*>(a.base);
+  float* Y = static_cast<float*>(a.y);
+
+  for (int tile = cid; tile < ntiles; tile += ncl) {
+    const int n = group_of(tile, start, a.N);
     const int s0 = bound[n] + (tile - start[n]) * MT;
     const int rows = min(MT, bound[n + 1] - s0);
     if (tid < MT) {
@@ -196,8 +979,8 @@ __global__ void __launch_bounds__(kThreads) adapter_kernel(const AdapterArgs a) 
       tok[tid] = t;
     }
     __syncthreads();
-    const T* P = static_cast<const T*>(a.P) + (size_t)n * a.dk * a.r;
-    const T* Q = static_cast<const T*>(a.Q) + (size_t)n * a.dn * a.r;
+    const float* P = static_cast<const float*>(a.P) + (size_t)n * a.dk * a.r;
+    const float* Q = static_cast<const float*>(a.Q) + (size_t)n * a.dn * a.r;
 
     // chunk c of the sequence: nk input chunks (x, P), then the output chunks (base, Q)
     auto load = [&](int c) {
@@ -205,29 +988,25 @@ __global__ void __launch_bounds__(kThreads) adapter_kernel(const AdapterArgs a) 
       const bool first = c < nk;
       const int col0 = (first ? k0 + c : n0 + c - nk) * C;
       const int d = first ? a.dk : a.dn;
-      const T* rowsrc = first ? X : base;
+      const float* rowsrc = first ? X : base;
       if (rowsrc) {
-        for (int i = tid; i < MT * 8; i += kThreads) {
-          const int row = i >> 3, col = col0 + (i & 7) * V;
-          const bool on = tok[row] >= 0 && col < d;
-          cp_async16(st + row * kRowB + (i & 7) * 16, rowsrc + (on ? (size_t)tok[row] * d + col : 0), on);
-        }
+        const int row = tid >> 3, col = col0 + (tid & 7) * 4;
+        const bool on = tok[row] >= 0 && col < d;
+        cp_async16(st + row * kRowB + (tid & 7) * 16, rowsrc + (on ? (size_t)tok[row] * d + col : 0), on);
       }
-      uint8_t* ws = st + MT * kRowB;
-      const T* W = first ? P : Q;
+      float* ws = reinterpret_cast<float*>(st + MT * kRowB);
+      const float* W = first ? P : Q;
       if (first != kT) {                          // rows of the chunk's columns, r wide
-        constexpr int RV = R / V;
-        for (int i = tid; i < C * RV; i += kThreads) {
-          const int row = i / RV, col = (i % RV) * V;
+        for (int i = tid; i < C * (R / 4); i += NT) {
+          const int row = i / (R / 4), col = (i % (R / 4)) * 4;
           const bool on = col0 + row < d && col < a.r;
-          cp_async16(ws + (row * PL::kLdR + col) * sizeof(T),
-                     W + (on ? (size_t)(col0 + row) * a.r + col : 0), on);
+          cp_async16(ws + row * kLdR + col, W + (on ? (size_t)(col0 + row) * a.r + col : 0), on);
         }
       } else {                                    // r rows, the chunk's columns wide
-        for (int i = tid; i < R * 8; i += kThreads) {
-          const int row = i >> 3, col = col0 + (i & 7) * V;
-          const bool on = row < a.r && col < d;
-          cp_async16(ws + row * kRowB + (i & 7) * 16, W + (on ? (size_t)row * d + col : 0), on);
+        for (int i = tid; i < R * 8; i += NT) {
+          const int row = i >> 3, col = (i & 7) * 4;
+          const bool on = row < a.r && col0 + col < d;
+          cp_async16(ws + row * kLdC + col, W + (on ? (size_t)row * d + col0 + col : 0), on);
         }
       }
     };
@@ -240,237 +1019,96 @@ __global__ void __launch_bounds__(kThreads) adapter_kernel(const AdapterArgs a) 
       __syncthreads();
       if (c + NS - 1 < total) load(c + NS - 1);
       cp_async_commit();
+      return reinterpret_cast<const float*>(sm + (c % NS) * PL::kStage);
     };
 
-    // ---- first product: partial h of this block's input columns
-    if constexpr (kHalf) {
-      float acc[R / 8][4];
-#pragma unroll
-      for (int i = 0; i < R / 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-      for (int c = 0; c < nk; ++c) {
-        advance(c);
-        const __half* xs = reinterpret_cast<const __half*>(sm + (c % NS) * PL::kStage);
-        const __half* ps = xs + MT * PL::kLdC;
-#pragma unroll
-        for (int kk = 0; kk < 4 / WK; ++kk) {
-          const int k = (kk * WK + wk) * 16;
-          uint32_t fa[4];
-          frag_a(fa, xs + wr * PL::kLdC + k, PL::kLdC, lane);
-#pragma unroll
-          for (int j = 0; j < R / 16; ++j) {
-            uint32_t fb[4];
-            if (kT)
-              frag_b_nk(fb, ps + j * 16 * PL::kLdC + k, PL::kLdC, lane);
-            else
-              frag_b_kn(fb, ps + k * PL::kLdR + j * 16, PL::kLdR, lane);
-            mma16816(acc[2 * j], fa, fb[0], fb[1]);
-            mma16816(acc[2 * j + 1], fa, fb[2], fb[3]);
-          }
-        }
-      }
-      float* p = part + ((size_t)wk * MT + wr + (lane >> 2)) * R + 2 * (lane & 3);
-#pragma unroll
-      for (int j = 0; j < R / 8; ++j) {
-        *reinterpret_cast<float2*>(p + 8 * j) = make_float2(acc[j][0], acc[j][1]);
-        *reinterpret_cast<float2*>(p + 8 * R + 8 * j) = make_float2(acc[j][2], acc[j][3]);
-      }
-    } else {
-      // f32: thread (row, column group) of the 16 x R block; sixteen rows, eight threads each
+    // ---- first product: eight threads per row, R / 8 columns each
+    {
       constexpr int CPT = R / 8;
       const int row = tid >> 3, c0 = tid & 7;
       float acc[CPT];
 #pragma unroll
       for (int j = 0; j < CPT; ++j) acc[j] = 0.f;
       for (int c = 0; c < nk; ++c) {
-        advance(c);
-        const float* xs = reinterpret_cast<const float*>(sm + (c % NS) * PL::kStage);
-        const float* ps = xs + MT * PL::kLdC;
+        const float* xs = advance(c);
+        const float* ps = xs + MT * kLdC;
 #pragma unroll 4
         for (int k = 0; k < C; ++k) {
-          const float xv = xs[row * PL::kLdC + k];
+          const float xv = xs[row * kLdC + k];
 #pragma unroll
           for (int j = 0; j < CPT; ++j)
-            acc[j] = fmaf(xv, kT ? ps[(c0 + 8 * j) * PL::kLdC + k] : ps[k * PL::kLdR + c0 + 8 * j],
-                          acc[j]);
+            acc[j] = fmaf(xv, kT ? ps[(c0 + 8 * j) * kLdC + k] : ps[k * kLdR + c0 + 8 * j], acc[j]);
         }
       }
 #pragma unroll
       for (int j = 0; j < CPT; ++j) part[row * R + c0 + 8 * j] = acc[j];
     }
-    if (kHalf && WK > 1) {                        // the warps' shares of the block
-      __syncthreads();
-      for (int i = tid; i < MT * R; i += kThreads) {
-        float v = part[i];
+    cl.sync();
+
+    // ---- h: this block sums rows 2 rank, 2 rank + 1 over the cluster and gives them to all
+    if (tid < MT) {
+      constexpr int CPT = R / 8;
+      const int row = rank * (MT / kCl) + (tid >> 3), c0 = (tid & 7) * CPT;
+      float v[CPT];
 #pragma unroll
-        for (int q = 1; q < WK; ++q) v += part[q * MT * R + i];
-        part[i] = v;
+      for (int j = 0; j < CPT; ++j) v[j] = 0.f;
+#pragma unroll
+      for (int q = 0; q < kCl; ++q) {
+        const float* src = cl.map_shared_rank(part, q) + row * R + c0;
+#pragma unroll
+        for (int j = 0; j < CPT; j += 2) {
+          const float2 u = *reinterpret_cast<const float2*>(src + j);
+          v[j] += u.x;
+          v[j + 1] += u.y;
+        }
+      }
+      if (a.hidden && row < rows) {
+        float* dst = a.hidden + (size_t)(s0 + row) * a.r;
+#pragma unroll
+        for (int j = 0; j < CPT; ++j)
+          if (c0 + j < a.r) dst[c0 + j] = v[j];
+      }
+      const float sc = a.scale[n];
+      for (int q = 0; q < kCl; ++q) {
+        float* dh = cl.map_shared_rank(hf, q) + row * kLdR + c0;
+#pragma unroll
+        for (int j = 0; j < CPT; j += 2) *reinterpret_cast<float2*>(dh + j) = make_float2(v[j], v[j + 1]);
+        if ((tid & 7) == 0) cl.map_shared_rank(mult, q)[row] = sc;
       }
     }
     cl.sync();
 
-    // ---- h: this block sums rows rank * MT / 8 .. over the cluster and gives them to all
-    {
-      constexpr int CPT = R / 8;                  // eight threads per row, CPT columns each
-      constexpr int RO = MT / kCl;
-      const int row = rank * RO + (tid >> 3), c0 = (tid & 7) * CPT;
-      if ((tid >> 3) < RO) {
-        float v[CPT];
-#pragma unroll
-        for (int j = 0; j < CPT; ++j) v[j] = 0.f;
-#pragma unroll
-        for (int q = 0; q < kCl; ++q) {
-          const float* src = cl.map_shared_rank(part, q) + row * R + c0;
-#pragma unroll
-          for (int j = 0; j < CPT; j += 2) {
-            const float2 u = *reinterpret_cast<const float2*>(src + j);
-            v[j] += u.x;
-            v[j + 1] += u.y;
-          }
-        }
-        if (a.hidden && row < rows) {
-          float* dst = a.hidden + (size_t)(s0 + row) * a.r;
-#pragma unroll
-          for (int j = 0; j < CPT; ++j)
-            if (c0 + j < a.r) dst[c0 + j] = v[j];
-        }
-        const float sc = a.scale[n];
-        if constexpr (kHalf) {
-          float m = 0.f;
-          bool odd = false;
-#pragma unroll
-          for (int j = 0; j < CPT; ++j) {
-            m = fmaxf(m, fabsf(v[j]));
-            odd |= !isfinite(v[j]);
-          }
-          const unsigned grp = 0xffu << (lane & 24);
-#pragma unroll
-          for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(grp, m, o));
-          odd = (__ballot_sync(grp, odd) & grp) != 0;
-          const int e = odd ? 0 : scale_exp(m);
-          const float inv = exp2_int(-e);
-          __half2 hi[CPT / 2], lo[CPT / 2];
-#pragma unroll
-          for (int j = 0; j < CPT; j += 2) {
-            split_f16(v[j] * inv, hi[j / 2].x, lo[j / 2].x);
-            split_f16(v[j + 1] * inv, hi[j / 2].y, lo[j / 2].y);
-          }
-          const float mu = sc * exp2_int(e);
-          for (int q = 0; q < kCl; ++q) {
-            __half* dh = cl.map_shared_rank(hhi, q) + row * (R + 8) + c0;
-            __half* dl = cl.map_shared_rank(hlo, q) + row * (R + 8) + c0;
-#pragma unroll
-            for (int j = 0; j < CPT / 2; ++j) {
-              reinterpret_cast<__half2*>(dh)[j] = hi[j];
-              reinterpret_cast<__half2*>(dl)[j] = lo[j];
-            }
-            if ((tid & 7) == 0) cl.map_shared_rank(mult, q)[row] = mu;
-          }
-        } else {
-          for (int q = 0; q < kCl; ++q) {
-            float* dh = cl.map_shared_rank(hf, q) + row * (R + 4) + c0;
-#pragma unroll
-            for (int j = 0; j < CPT; j += 2)
-              *reinterpret_cast<float2*>(dh + j) = make_float2(v[j], v[j + 1]);
-            if ((tid & 7) == 0) cl.map_shared_rank(mult, q)[row] = sc;
-          }
-        }
-      }
-    }
-    cl.sync();
-
-    // ---- second product: this block's output columns
-    if constexpr (kHalf) {
-      constexpr int NT = 8 / WK;                  // 8-column tiles of a chunk per warp
-      const int wc = wk * NT * 8;
-      uint32_t fh[R / 16][4], fl[R / 16][4];
-#pragma unroll
-      for (int k = 0; k < R / 16; ++k) {
-        frag_a(fh[k], hhi + wr * (R + 8) + k * 16, R + 8, lane);
-        frag_a(fl[k], hlo + wr * (R + 8) + k * 16, R + 8, lane);
-      }
-      const int g = lane >> 2, q2 = 2 * (lane & 3);
-      const float m0 = mult[wr + g], m1 = mult[wr + g + 8];
-      for (int c = nk; c < total; ++c) {
-        advance(c);
-        __half* bs = reinterpret_cast<__half*>(sm + (c % NS) * PL::kStage);
-        const __half* qs = bs + MT * PL::kLdC;
-        float acc[NT][4];
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-#pragma unroll
-        for (int k = 0; k < R / 16; ++k)
-#pragma unroll
-          for (int j = 0; j < NT / 2; ++j) {
-            uint32_t fb[4];
-            if (kT)
-              frag_b_nk(fb, qs + (wc + j * 16) * PL::kLdR + k * 16, PL::kLdR, lane);
-            else
-              frag_b_kn(fb, qs + k * 16 * PL::kLdC + wc + j * 16, PL::kLdC, lane);
-            mma16816(acc[2 * j], fl[k], fb[0], fb[1]);
-            mma16816(acc[2 * j + 1], fl[k], fb[2], fb[3]);
-            mma16816(acc[2 * j], fh[k], fb[0], fb[1]);
-            mma16816(acc[2 * j + 1], fh[k], fb[2], fb[3]);
-          }
-        // base + scale * sum, rounded once, in place; then 16-byte rows out
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          __half2* b0 = reinterpret_cast<__half2*>(bs + (wr + g) * PL::kLdC + wc + 8 * j + q2);
-          __half2* b1 = reinterpret_cast<__half2*>(bs + (wr + g + 8) * PL::kLdC + wc + 8 * j + q2);
-          float2 u = make_float2(0.f, 0.f), v = u;
-          if (base) {
-            u = __half22float2(*b0);
-            v = __half22float2(*b1);
-          }
-          *b0 = __floats2half2_rn(fmaf(m0, acc[j][0], u.x), fmaf(m0, acc[j][1], u.y));
-          *b1 = __floats2half2_rn(fmaf(m1, acc[j][2], v.x), fmaf(m1, acc[j][3], v.y));
-        }
-        __syncwarp();
-        const int col0 = (n0 + c - nk) * C;
-#pragma unroll
-        for (int i = lane; i < 16 * NT; i += 32) {
-          const int row = wr + i / NT, cc = wc + (i % NT) * 8;
-          if (tok[row] >= 0 && col0 + cc < a.dn)
-            *reinterpret_cast<uint4*>(Y + (size_t)tok[row] * a.dn + col0 + cc) =
-                *reinterpret_cast<const uint4*>(bs + row * PL::kLdC + cc);
-        }
-      }
-    } else {
-      const int row = tid >> 3, c0 = (tid & 7) * 4;       // four columns of a chunk per thread
-      const float mu = mult[row];
-      const int t = tok[row];
-      for (int c = nk; c < total; ++c) {
-        advance(c);
-        const float* bs = reinterpret_cast<const float*>(sm + (c % NS) * PL::kStage);
-        const float* qs = bs + MT * PL::kLdC;
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    // ---- second product: four columns of a chunk per thread
+    const int row = tid >> 3, c0 = (tid & 7) * 4;
+    const float mu = mult[row];
+    const int t = tok[row];
+    for (int c = nk; c < total; ++c) {
+      const float* bs = advance(c);
+      const float* qs = bs + MT * kLdC;
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-        for (int k = 0; k < R; ++k) {
-          const float hv = hf[row * (R + 4) + k];
-          if (kT) {
+      for (int k = 0; k < R; ++k) {
+        const float hv = hf[row * kLdR + k];
+        if (kT) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[j] = fmaf(hv, qs[(c0 + j) * PL::kLdR + k], acc[j]);
-          } else {
-            const float4 q = load4(qs + k * PL::kLdC + c0);
-            acc[0] = fmaf(hv, q.x, acc[0]);
-            acc[1] = fmaf(hv, q.y, acc[1]);
-            acc[2] = fmaf(hv, q.z, acc[2]);
-            acc[3] = fmaf(hv, q.w, acc[3]);
-          }
+          for (int j = 0; j < 4; ++j) acc[j] = fmaf(hv, qs[(c0 + j) * kLdR + k], acc[j]);
+        } else {
+          const float4 q = load4(qs + k * kLdC + c0);
+          acc[0] = fmaf(hv, q.x, acc[0]);
+          acc[1] = fmaf(hv, q.y, acc[1]);
+          acc[2] = fmaf(hv, q.z, acc[2]);
+          acc[3] = fmaf(hv, q.w, acc[3]);
         }
-        const int col = (n0 + c - nk) * C + c0;
-        if (t >= 0 && col < a.dn) {
-          float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (base) u = load4(bs + row * PL::kLdC + c0);
-          u.x = fmaf(mu, acc[0], u.x);
-          u.y = fmaf(mu, acc[1], u.y);
-          u.z = fmaf(mu, acc[2], u.z);
-          u.w = fmaf(mu, acc[3], u.w);
-          *reinterpret_cast<float4*>(Y + (size_t)t * a.dn + col) = u;
-        }
+      }
+      const int col = (n0 + c - nk) * C + c0;
+      if (t >= 0 && col < a.dn) {
+        float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (base) u = load4(bs + row * kLdC + c0);
+        u.x = fmaf(mu, acc[0], u.x);
+        u.y = fmaf(mu, acc[1], u.y);
+        u.z = fmaf(mu, acc[2], u.z);
+        u.w = fmaf(mu, acc[3], u.w);
+        *reinterpret_cast<float4*>(Y + (size_t)t * a.dn + col) = u;
       }
     }
     cp_async_wait<0>();
@@ -478,16 +1116,40 @@ __global__ void __launch_bounds__(kThreads) adapter_kernel(const AdapterArgs a) 
   }
 }
 
-template <typename T, int MT, int R, bool kT>
-cudaError_t launch_one(const AdapterArgs& a, int sms, cudaStream_t s) {
-  auto kern = adapter_kernel<T, MT, R, kT>;
+// Bytes of the group table, in powers of two of the groups: few distinct launch plans.
+size_t table_bytes(int N) {
+  int groups = 64;
+  while (groups < N + 1) groups *= 2;
+  return sizeof(int) * (2 * (size_t)groups + 64);
+}
+
+// Clusters of a kernel that are resident on the device at once (asked once per kernel, device
+// and size of the group table; a grid of more would leave its last clusters for a second round).
+int resident_clusters(const void* kern, const cudaLaunchConfig_t& cfg) {
+  static std::mutex mu;
+  static std::map<std::tuple<const void*, int, size_t>, int> known;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lk(mu);
+  const auto key = std::make_tuple(kern, dev, cfg.dynamicSmemBytes);
+  const auto it = known.find(key);
+  if (it != known.end()) return it->second;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
+  known[key] = n;
+  return n;
+}
+
+// One cluster per tile, at most as many as are resident at once, and one more for the checks.
+template <typename Kern>
+cudaError_t launch_plan(Kern kern, const AdapterArgs& a, int MT, int threads, size_t smem,
+                        cudaStream_t s) {
   MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
+  smem += table_bytes(a.N);
   const long long most = (long long)a.S_max / MT + std::min(a.N, a.S_max);   // tiles at most
-  const int ncl = (int)std::min<long long>(most, std::max(1, sms * 4 / kCl));
-  const size_t smem = Plan<T, MT, R>::kOffTab + sizeof(int) * (2 * ((size_t)a.N + 1) + 16);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((ncl + 1) * kCl);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(kCl);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -497,35 +1159,121 @@ cudaError_t launch_one(const AdapterArgs& a, int sms, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  const int fit = resident_clusters(reinterpret_cast<const void*>(kern), cfg);
+  if (fit < 1) return cudaErrorLaunchOutOfResources;
+  cfg.gridDim = dim3(((int)std::min<long long>(most, fit) + 1) * kCl);
   const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, a);
   if (err == cudaSuccess) launch_counter().fetch_add(1, std::memory_order_relaxed);
   return err;
 }
 
-template <typename T, int MT, bool kT>
-cudaError_t launch_rank(const AdapterArgs& a, int sms, cudaStream_t s) {
-  if (a.r <= 16) return launch_one<T, MT, 16, kT>(a, sms, s);
-  if (a.r <= 32) return launch_one<T, MT, 32, kT>(a, sms, s);
-  if (a.r <= 64) return launch_one<T, MT, 64, kT>(a, sms, s);
-  return launch_one<T, MT, 128, kT>(a, sms, s);
+template <bool kT, int R>
+cudaError_t launch_short(const AdapterArgs& a, cudaStream_t s) {
+  using PL = Plan16<16, R>;
+  return launch_plan(adapter_f16_kernel<16, R, kT>, a, 16, PL::kThreads, PL::kOffTab, s);
+}
+int resident_blocks(const void* kern, int threads, size_t smem) {
+  static std::mutex mu;
+  static std::map<std::tuple<const void*, int, size_t>, int> known;
+  int dev = 0, sms = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lk(mu);
+  const auto key = std::make_tuple(kern, dev, smem);
+  const auto it = known.find(key);
+  if (it != known.end()) return it->second;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) != cudaSuccess)
+    n = 0;
+  known[key] = n * sms;
+  return n * sms;
+}
+
+template <bool kT, int R>
+cudaError_t launch_tall(const AdapterArgs& a, float* partial, cudaStream_t s) {
+  using PL = PlanTall<R>;
+  const uint64_t dk = a.dk, dn = a.dn, r = a.r, N = a.N, T = a.T;
+  const uint32_t RB = R > 64 ? 64 : R;
+  const uint32_t row_box[2] = {64, 1}, wide[3] = {RB, 64, 1}, flat[3] = {64, R, 1};
+  const size_t smem = PL::kBytes + table_bytes(a.N) + (R < 32 ? kTallRows * R * 4 : 0);
+  TallArgs ta{a, partial, adapter_parts(a.S_max, a.dk), 1};
+  const long long tiles = (long long)a.S_max / kTallRows + std::min(a.N, a.S_max);   // at most
+  {
+    auto kern = adapter_shrink_kernel<R, kT>;
+    MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
+    const int fit = resident_blocks(reinterpret_cast<const void*>(kern), kTallThreads, smem);
+    if (fit < 1) return cudaErrorLaunchOutOfResources;
+    if (ta.parts_k == 1 && a.hidden) ta.partial = a.hidden;
+    CUtensorMap mX, mP;
+    const uint64_t x_dims[2] = {dk, T}, p_fwd[3] = {r, dk, N}, p_bwd[3] = {dk, r, N};
+    if (!encode_f16_map(&mX, a.x, 2, x_dims, row_box) ||
+        !encode_f16_map(&mP, a.P, 3, kT ? p_bwd : p_fwd, kT ? flat : wide))
+      return cudaErrorInvalidValue;
+    const int grid = (int)std::min<long long>(tiles * ta.parts_k, fit - 1) + 1;   // and the checks
+    MOE_LAUNCH(launch_k(kern, grid, kTallThreads, smem, s, false, mX, mP, ta));
+  }
+  if (a.dn == 0 && ta.partial == a.hidden) return cudaSuccess;
+  auto kern = adapter_expand_kernel<R, kT>;
+  MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
+  const int fit = resident_blocks(reinterpret_cast<const void*>(kern), kTallThreads, smem);
+  if (fit < 1) return cudaErrorLaunchOutOfResources;
+  CUtensorMap mQ, mB;
+  if (a.dn) {
+    const uint64_t b_dims[2] = {dn, T}, q_fwd[3] = {dn, r, N}, q_bwd[3] = {r, dn, N};
+    if (!encode_f16_map(&mQ, a.Q, 3, kT ? q_bwd : q_fwd, kT ? wide : flat)) return cudaErrorInvalidValue;
+    if (!a.base)
+      mB = mQ;
+    else if (!encode_f16_map(&mB, a.base, 2, b_dims, row_box))
+      return cudaErrorInvalidValue;
+    ta.parts_n = std::max(1, std::min(8, (a.dn / kChunk) / 8));
+  } else {
+    memset(&mQ, 0, sizeof(mQ));
+    mB = mQ;
+  }
+  const int grid = (int)std::min<long long>(tiles * ta.parts_n, fit);
+  return launch_k(kern, grid, kTallThreads, smem, s, true, mQ, mB, ta);
+}
+template <bool kT, int R>
+cudaError_t launch_f32(const AdapterArgs& a, cudaStream_t s) {
+  using PL = Plan32<R>;
+  return launch_plan(adapter_f32_kernel<R, kT>, a, PL::MT, PL::kThreads, PL::kOffTab, s);
+}
+
+template <bool kT, int R>
+cudaError_t launch_rank(const AdapterArgs& a, bool f16, float* partial, cudaStream_t s) {
+  if (!f16) return launch_f32<kT, R>(a, s);
+  return adapter_tall(a.S_max, a.N, true) ? launch_tall<kT, R>(a, partial, s) : launch_short<kT, R>(a, s);
+}
+template <bool kT>
+cudaError_t launch_adapter_t(const AdapterArgs& a, bool f16, float* partial, cudaStream_t s) {
+  if (a.r <= 16) return launch_rank<kT, 16>(a, f16, partial, s);
+  if (a.r <= 32) return launch_rank<kT, 32>(a, f16, partial, s);
+  if (a.r <= 64) return launch_rank<kT, 64>(a, f16, partial, s);
+  return launch_rank<kT, 128>(a, f16, partial, s);
+}
+
+__global__ void __launch_bounds__(1024) adapter_check_kernel(const AdapterArgs a) {
+  check_indices(a.perm, a.offsets, a.N, a.S_max, a.T, a.status);
 }
 
 }  // namespace
 
+bool adapter_tall(int S_max, int N, bool f16) { return f16 && S_max > 32LL * std::min(N, S_max); }
+
+// Parts of the first product's columns: enough items for two blocks on each of 152 SMs, four
+// chunks each at least.
+int adapter_parts(int S_max, int dk) {
+  const int tiles = (S_max + kTallRows - 1) / kTallRows, chunks = (dk + kChunk - 1) / kChunk;
+  return std::max(1, std::min({kAdapterParts, 304 / std::max(1, tiles), chunks / 4}));
+}
+
 cudaError_t launch_adapter(const void* x, const void* P, const void* Q, const void* base, void* y,
-                           float* hidden, const float* scale, const int32_t* perm,
+                           float* hidden, float* partial, const float* scale, const int32_t* perm,
                            const int32_t* offsets, int* status, int dtype_f16, bool transposed,
                            int T, int dk, int dn, int r, int N, int S_max, cudaStream_t s) {
-  int dev = 0, sms = 0;
-  MOE_LAUNCH(cudaGetDevice(&dev));
-  MOE_LAUNCH(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   const AdapterArgs a{x, P, Q, base, y, hidden, scale, perm, offsets, status, T, dk, dn, r, N, S_max};
-  if (!dtype_f16)
-    return transposed ? launch_rank<float, 16, true>(a, sms, s) : launch_rank<float, 16, false>(a, sms, s);
-  const bool tall = S_max > 32LL * std::min(N, S_max);
-  if (tall)
-    return transposed ? launch_rank<__half, 64, true>(a, sms, s) : launch_rank<__half, 64, false>(a, sms, s);
-  return transposed ? launch_rank<__half, 16, true>(a, sms, s) : launch_rank<__half, 16, false>(a, sms, s);
+  if (dk == 0) return launch_k(adapter_check_kernel, 1, 1024, 0, s, false, a);
+  return transposed ? launch_adapter_t<true>(a, dtype_f16, partial, s)
+                    : launch_adapter_t<false>(a, dtype_f16, partial, s);
 }
 
 }  // namespace moe

@@ -191,6 +191,38 @@ bool encode_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+namespace moe {
+
+// Tensor map of an f16 tensor of two or three dimensions (dims innermost first, dense), with a
+// box of `box` and the swizzle whose span is the box's inner bytes (32, 64 or 128).
+bool encode_f16_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
+                    const uint32_t* box) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t d[3] = {1, 1, 1}, strides[2];
+  cuuint32_t b[3] = {1, 1, 1}, estr[3] = {1, 1, 1};
+  cuuint64_t bytes = 2;
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    bytes *= dims[i];
+    if (i + 1 < rank) strides[i] = bytes;
+  }
+  const uint32_t span = box[0] * 2;
+  const CUtensorMapSwizzle sw = span == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                : span == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                             : CU_TENSOR_MAP_SWIZZLE_32B;
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), d, strides,
+             b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace moe
+
+namespace {
+
 uint32_t pow2_at_least(uint32_t v) {
   uint32_t p = 32;
   while (p < v) p <<= 1;

@@ -107,6 +107,16 @@ __device__ __forceinline__ void tma_load_2d(void* smem, const CUtensorMap* m, in
       : "memory");
 }
 
+// 3-D tiled load of the box at {x, y, z}; elements outside the tensor read as zero.
+__device__ __forceinline__ void tma_load_3d(void* smem, const CUtensorMap* m, int x, int y, int z,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem)),
+      "l"(m), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // Row gather: four rows r0..r3 of a 2-D tensor, columns x .. x+box_x, one-row box.
 __device__ __forceinline__ void tma_gather4(void* smem, const CUtensorMap* m, int x, int r0, int r1,
                                             int r2, int r3, uint64_t* bar) {

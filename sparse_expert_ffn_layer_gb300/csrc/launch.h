@@ -131,6 +131,9 @@ int gemm_stages_for(int nmax, int E, int mw, int smem_limit);
 // Raises the kernel's dynamic shared-memory limit to the device maximum, once per kernel
 // and device (host side; launches of any size up to that maximum then need no further call).
 cudaError_t ensure_smem_attr(const void* kernel);
+// Tensor map of a dense f16 tensor of two or three dimensions, swizzled by its box's inner bytes.
+bool encode_f16_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
+                    const uint32_t* box);
 cudaError_t launch_grouped_gemm1(const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap& Ar,
                                  const CUtensorMap& Br, const GemmArgs& args, int grid,
                                  cudaStream_t s, bool pdl = false);
@@ -202,9 +205,14 @@ cudaError_t launch_combine_backward(const void* dout, const void* expert_out, co
                                     const float* topk_w, int dtype_f16, int T, int d, int k, int S_max,
                                     void* dexpert_out, float* dtopk_w, cudaStream_t s);
 // Low-rank adapters (adapter.cu): y[t] = base[t] + scale_n (x[t] P_n) Q_n; transposed: P, Q are
-// given as [N, r, dk] and [N, dn, r].  hidden [S_max, r] receives x P when not null.
+// given as [N, r, dk] and [N, dn, r].  hidden [S_max, r] receives x P when not null.  dk = 0: only
+// the indices are checked; dn = 0: only x P is computed.  partial: adapter_parts(S_max, dk) x
+// [S_max, r] floats where adapter_tall.
+constexpr int kAdapterParts = 8;
+bool adapter_tall(int S_max, int N, bool f16);
+int adapter_parts(int S_max, int dk);
 cudaError_t launch_adapter(const void* x, const void* P, const void* Q, const void* base, void* y,
-                           float* hidden, const float* scale, const int32_t* perm,
+                           float* hidden, float* partial, const float* scale, const int32_t* perm,
                            const int32_t* offsets, int* status, int dtype_f16, bool transposed,
                            int T, int dk, int dn, int r, int N, int S_max, cudaStream_t s);
 cudaError_t launch_selftest_wait(int* status, uint64_t timeout_ns, cudaStream_t s);

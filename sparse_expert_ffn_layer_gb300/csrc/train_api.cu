@@ -41,8 +41,14 @@ moe_status check_adapter(int T, int d_in, int d_out, int r, int N, int S_max, mo
   return MOE_OK;
 }
 
-// [status][dh]
-size_t adapter_bytes(int r, int S_max) { return kAlign + align_up((size_t)S_max * r * sizeof(float)); }
+// [status][dh][partial h]
+size_t hidden_bytes(int r, int S_max) { return align_up((size_t)S_max * r * sizeof(float)); }
+size_t adapter_bytes(int d_in, int d_out, int r, int N, int S_max, moe_dtype dtype) {
+  size_t b = kAlign + hidden_bytes(r, S_max);
+  if (adapter_tall(S_max, N, dtype == MOE_F16))
+    b += std::max(adapter_parts(S_max, d_in), adapter_parts(S_max, d_out)) * hidden_bytes(r, S_max);
+  return b;
+}
 
 }  // namespace
 
@@ -143,7 +149,7 @@ moe_status moe_adapter_workspace_size(int T, int d_in, int d_out, int r, int N, 
   if (!bytes) return MOE_ERR_INVALID_ARG;
   moe_status st = check_adapter(T, d_in, d_out, r, N, S_max, dtype);
   if (st != MOE_OK) return st;
-  *bytes = adapter_bytes(r, S_max);
+  *bytes = adapter_bytes(d_in, d_out, r, N, S_max, dtype);
   return MOE_OK;
 }
 
@@ -160,8 +166,10 @@ moe_status moe_adapter_forward(const void* tokens, const int32_t* perm, const in
       !aligned4(scale) || !aligned16(base) || !aligned16(out) || !aligned16(hidden) ||
       !aligned16(workspace))
     return MOE_ERR_UNSUPPORTED;
-  if (!workspace || ws_bytes < adapter_bytes(r, S_max)) return MOE_ERR_WORKSPACE;
-  MOE_TRY(launch_adapter(tokens, A, B, base, out, hidden, scale, perm, offsets,
+  if (!workspace || ws_bytes < adapter_bytes(d_in, d_out, r, N, S_max, dtype)) return MOE_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  float* partial = reinterpret_cast<float*>(ws + kAlign + hidden_bytes(r, S_max));
+  MOE_TRY(launch_adapter(tokens, A, B, base, out, hidden, partial, scale, perm, offsets,
                          static_cast<int*>(workspace), dtype == MOE_F16, /*transposed=*/false, T, d_in,
                          d_out, r, N, S_max, as_stream(stream)));
   return MOE_OK;
@@ -189,14 +197,15 @@ moe_status moe_adapter_backward(const void* dout, const void* tokens, const floa
       !aligned16(dtokens_in) || !aligned16(dtokens) || !aligned16(dA) || !aligned16(dB) ||
       !aligned16(workspace))
     return MOE_ERR_UNSUPPORTED;
-  if (!workspace || ws_bytes < adapter_bytes(r, S_max)) return MOE_ERR_WORKSPACE;
+  if (!workspace || ws_bytes < adapter_bytes(d_in, d_out, r, N, S_max, dtype)) return MOE_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   float* dh = reinterpret_cast<float*>(ws + kAlign);
+  float* partial = reinterpret_cast<float*>(ws + kAlign + hidden_bytes(r, S_max));
   const int f16 = dtype == MOE_F16;
   // dh, and with it the tokens' gradient.  Without dtokens only the first product runs (dn = 0),
   // and with neither dtokens nor dA the launch only checks the indices (dk = 0 too).
-  MOE_TRY(launch_adapter(dout, B, A, dtokens_in, dtokens, dA ? dh : nullptr, scale, perm, offsets,
-                         reinterpret_cast<int*>(ws), f16, /*transposed=*/true, T,
+  MOE_TRY(launch_adapter(dout, B, A, dtokens_in, dtokens, dA ? dh : nullptr, partial, scale, perm,
+                         offsets, reinterpret_cast<int*>(ws), f16, /*transposed=*/true, T,
                          dA || dtokens ? d_out : 0, dtokens ? d_in : 0, r, N, S_max, s));
   if (dA || dB)
     MOE_TRY(launch_row_sums(tokens, dh, dA, d_in, r, 0, dout, hidden, dB, d_out, r, 1, scale, perm,
