@@ -147,11 +147,10 @@ struct AdapterArgs {
 // (As one launch with h exchanged through a cluster's shared memory, each tile waited 15 us or
 // more for two cluster-wide hand-overs: 16384 rows of 3584 columns at r = 64 took 320 us.)
 //
-// Eight warps multiply, and the first of them issues the loads: rows by TMA row gathers through
-// perm, weights as boxes of three-dimensional tensors [N, rows, columns] whose edges read as
-// zeros.  (A loading warp of its own would be the ninth, the third on one of the SM's four
-// register files, which then hold one block instead of two; and with every warp issuing its
-// share of 16-byte copies, their address arithmetic was two thirds of all instructions.)
+// Eight warps multiply and copy their share of the rows (two 16-byte pieces per thread and chunk);
+// weights come as boxes of three-dimensional tensors [N, rows, columns] by TMA, whose edges read
+// as zeros.  Chunks are handed over by mbarriers that count both.  (Rows by TMA gathers of four
+// rows were bound by the gathers' rate, about 50 cycles each: shrink 66 us.)
 constexpr int kTallRows = 64;
 constexpr int kTallWarps = 8, kTallThreads = 32 * kTallWarps;
 constexpr int kChunk = 64;                        // columns per chunk
@@ -193,13 +192,14 @@ struct TallRing {
   int* status;
   const int32_t* perm;
   int N, T, chunks, parts, items, blocks;         // blocks: of the grid that take items
-  bool rows_on;                                   // the chunks have rows (base may be absent)
-  const CUtensorMap *mRows, *mW;
+  const __half* rows;                             // [T, d], or null (an absent base)
+  int d;
+  const CUtensorMap* mW;
   // use
   int stage = 0;
   uint32_t phase = 0;
-  // loads (warp 0)
-  int li, lc = 0, lend = 0, ln = 0, lstage = 0, lrow[4] = {0, 0, 0, 0}, lnext[4] = {0, 0, 0, 0};
+  // loads: thread t copies 16-byte piece t % 8 of rows t / 8 and t / 8 + 32
+  int li, lc = 0, lend = 0, ln = 0, lstage = 0, lrow[2] = {-1, -1}, lnext[2] = {-1, -1};
   uint32_t lphase = 1;
 
   __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
@@ -208,15 +208,14 @@ struct TallRing {
     if (!mbar_wait_bounded(bar, parity, abort, nullptr, kDefaultWaitNs) && !before) *status = kErrTimeout;
   }
   __device__ __forceinline__ int part_begin(int p) const { return (int)((long long)chunks * p / parts); }
-  __device__ __forceinline__ void fetch_rows(int item) {   // row 0 stands in for none
-    const int lane = threadIdx.x & 31;
-    if (item >= items || lane >= MT / 4) return;
+  __device__ __forceinline__ void fetch_rows(int item) {
+    if (item >= items) return;
     const int tile = item / parts, n = group_of(tile, start, N);
-    const int s0 = bound[n] + (tile - start[n]) * MT + 4 * lane;
+    const int s0 = bound[n] + (tile - start[n]) * MT + (threadIdx.x >> 3);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int t = s0 + q < bound[n + 1] ? perm[s0 + q] : 0;
-      lnext[q] = (unsigned)t < (unsigned)T ? t : 0;
+    for (int q = 0; q < 2; ++q) {
+      const int t = s0 + 32 * q < bound[n + 1] ? perm[s0 + 32 * q] : -1;
+      lnext[q] = (unsigned)t < (unsigned)T ? t : -1;
     }
   }
   __device__ __forceinline__ void begin_item() {
@@ -225,27 +224,21 @@ struct TallRing {
       ln = group_of(tile, start, N);
       lc = part_begin(p);
       lend = part_begin(p + 1);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) lrow[q] = lnext[q];
+      lrow[0] = lnext[0];
+      lrow[1] = lnext[1];
       fetch_rows(li + blocks);
       if (lc < lend) return;
       li += blocks;
     }
   }
-  // The next chunk, into the stage whose turn it is (whole warp 0).
+  // The next chunk, into the stage whose turn it is (all threads).
   __device__ __forceinline__ void issue() {
-    if (li >= items || *abort) return;
-    const int lane = threadIdx.x & 31, col = lc * kChunk;
+    if (li >= items) return;
+    const int col = lc * kChunk;
     uint8_t* st = sm + lstage * PL::kStage;
-    if (lane == 0) {
-      wait(&empty[lstage], lphase);
-      if (!*abort) mbar_expect_tx(&full[lstage], (rows_on ? MT * 128 : 0) + kChunk * R * 2);
-    }
-    __syncwarp();
-    if (*abort) return;                           // no further loads
-    if (rows_on && lane < MT / 4)
-      tma_gather4(st + lane * 512, mRows, col, lrow[0], lrow[1], lrow[2], lrow[3], &full[lstage]);
-    if (lane == 16) {
+    wait(&empty[lstage], lphase);
+    if (threadIdx.x == 0 && !*abort) {            // (no further loads after a wait gave up)
+      mbar_expect_tx(&full[lstage], kChunk * R * 2);
       uint8_t* ws = st + MT * 128;
       if (kWide) {
 #pragma unroll
@@ -253,6 +246,17 @@ struct TallRing {
       } else {
         tma_load_3d(ws, mW, col, 0, ln, &full[lstage]);
       }
+    }
+    if (rows) {
+      const int row = threadIdx.x >> 3, pc = threadIdx.x & 7;
+      const bool in = col + pc * 8 < d;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const bool on = in && lrow[q] >= 0;
+        cp_async16(st + (row + 32 * q) * 128 + ((pc ^ (row & 7)) << 4),
+                   rows + (on ? (size_t)lrow[q] * d + col + pc * 8 : 0), on);
+      }
+      cp_async_arrive(&full[lstage]);
     }
     if (++lstage == NS) {
       lstage = 0;
@@ -265,14 +269,12 @@ struct TallRing {
   }
   __device__ __forceinline__ void begin() {
     li = blockIdx.x;
-    if (threadIdx.x < 32) {
-      fetch_rows(li);
-      begin_item();
-      for (int c = 0; c < NS - 1; ++c) issue();
-    }
+    fetch_rows(li);
+    begin_item();
+    for (int c = 0; c < NS - 2; ++c) issue();
   }
   __device__ __forceinline__ uint8_t* next() {    // the chunk that is used next
-    if (threadIdx.x < 32) issue();
+    issue();                                      // two chunks of slack between the warps
     wait(&full[stage], phase);
     return sm + stage * PL::kStage;
   }
@@ -305,7 +307,7 @@ __device__ __forceinline__ int tall_setup(TallRing<R, kWide>& ring, const Adapte
   ring.T = a.T;
   if (threadIdx.x == 0) {
     for (int i = 0; i < PL::kStages; ++i) {
-      mbar_init(&ring.full[i], 1);
+      mbar_init(&ring.full[i], ring.rows ? 1 + kTallThreads : 1);
       mbar_init(&ring.empty[i], kTallWarps);
     }
     fence_mbar_init();
@@ -318,8 +320,7 @@ __device__ __forceinline__ int tall_setup(TallRing<R, kWide>& ring, const Adapte
 
 template <int R, bool kT>
 __global__ void __launch_bounds__(kTallThreads, 2)
-    adapter_shrink_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mP,
-                          const TallArgs ta) {
+    adapter_shrink_kernel(const __grid_constant__ CUtensorMap mP, const TallArgs ta) {
   const AdapterArgs& a = ta.a;
   constexpr int MT = kTallRows, RB = R > 64 ? 64 : R;
   constexpr int WN = R >= 32 ? 2 : 1, WK = 2 / WN;   // two warps per 16 rows: along r, or the chunk
@@ -332,10 +333,10 @@ __global__ void __launch_bounds__(kTallThreads, 2)
     return;
   }
   TallRing<R, !kT> ring;
-  const int ntiles = tall_setup(ring, a, raw);
-  ring.mRows = &mX;
+  ring.rows = static_cast<const __half*>(a.x);
+  ring.d = a.dk;
   ring.mW = &mP;
-  ring.rows_on = true;
+  const int ntiles = tall_setup(ring, a, raw);
   ring.chunks = (a.dk + kChunk - 1) / kChunk;
   ring.parts = ta.parts_k;
   ring.items = ntiles * ring.parts;
@@ -427,18 +428,17 @@ __global__ void __launch_bounds__(kTallThreads, 2)
 
 template <int R, bool kT>
 __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
-    adapter_expand_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mBase,
-                          const TallArgs ta) {
+    adapter_expand_kernel(const __grid_constant__ CUtensorMap mQ, const TallArgs ta) {
   const AdapterArgs& a = ta.a;
   constexpr int MT = kTallRows, RB = R > 64 ? 64 : R;
   extern __shared__ uint8_t raw[];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const bool with_base = a.base != nullptr;
   TallRing<R, kT> ring;
-  const int ntiles = tall_setup(ring, a, raw);
-  ring.mRows = &mBase;
+  ring.rows = static_cast<const __half*>(a.base);
+  ring.d = a.dn;
   ring.mW = &mQ;
-  ring.rows_on = with_base;
+  const int ntiles = tall_setup(ring, a, raw);
   ring.chunks = (a.dn + kChunk - 1) / kChunk;
   ring.parts = ta.parts_n;
   ring.items = ntiles * ring.parts;
@@ -577,8 +577,6 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
           *reinterpret_cast<uint4*>(Y + (size_t)y1 * a.dn + col) =
               *reinterpret_cast<const uint4*>(bs + swz<128>(yrow + 8, ypc));
       }
-      // the stage was written here and is next written by TMA
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       ring.done();
     }
   }
@@ -1191,9 +1189,9 @@ int resident_blocks(const void* kern, int threads, size_t smem) {
 template <bool kT, int R>
 cudaError_t launch_tall(const AdapterArgs& a, float* partial, cudaStream_t s) {
   using PL = PlanTall<R>;
-  const uint64_t dk = a.dk, dn = a.dn, r = a.r, N = a.N, T = a.T;
+  const uint64_t dk = a.dk, dn = a.dn, r = a.r, N = a.N;
   const uint32_t RB = R > 64 ? 64 : R;
-  const uint32_t row_box[2] = {64, 1}, wide[3] = {RB, 64, 1}, flat[3] = {64, R, 1};
+  const uint32_t wide[3] = {RB, 64, 1}, flat[3] = {64, R, 1};
   const size_t smem = PL::kBytes + table_bytes(a.N) + (R < 32 ? kTallRows * R * 4 : 0);
   TallArgs ta{a, partial, adapter_parts(a.S_max, a.dk), 1};
   const long long tiles = (long long)a.S_max / kTallRows + std::min(a.N, a.S_max);   // at most
@@ -1203,34 +1201,26 @@ cudaError_t launch_tall(const AdapterArgs& a, float* partial, cudaStream_t s) {
     const int fit = resident_blocks(reinterpret_cast<const void*>(kern), kTallThreads, smem);
     if (fit < 1) return cudaErrorLaunchOutOfResources;
     if (ta.parts_k == 1 && a.hidden) ta.partial = a.hidden;
-    CUtensorMap mX, mP;
-    const uint64_t x_dims[2] = {dk, T}, p_fwd[3] = {r, dk, N}, p_bwd[3] = {dk, r, N};
-    if (!encode_f16_map(&mX, a.x, 2, x_dims, row_box) ||
-        !encode_f16_map(&mP, a.P, 3, kT ? p_bwd : p_fwd, kT ? flat : wide))
-      return cudaErrorInvalidValue;
+    CUtensorMap mP;
+    const uint64_t p_fwd[3] = {r, dk, N}, p_bwd[3] = {dk, r, N};
+    if (!encode_f16_map(&mP, a.P, 3, kT ? p_bwd : p_fwd, kT ? flat : wide)) return cudaErrorInvalidValue;
     const int grid = (int)std::min<long long>(tiles * ta.parts_k, fit - 1) + 1;   // and the checks
-    MOE_LAUNCH(launch_k(kern, grid, kTallThreads, smem, s, false, mX, mP, ta));
+    MOE_LAUNCH(launch_k(kern, grid, kTallThreads, smem, s, false, mP, ta));
   }
   if (a.dn == 0 && ta.partial == a.hidden) return cudaSuccess;
   auto kern = adapter_expand_kernel<R, kT>;
   MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
   const int fit = resident_blocks(reinterpret_cast<const void*>(kern), kTallThreads, smem);
   if (fit < 1) return cudaErrorLaunchOutOfResources;
-  CUtensorMap mQ, mB;
+  CUtensorMap mQ;
+  memset(&mQ, 0, sizeof(mQ));                     // not used when there is no second product
   if (a.dn) {
-    const uint64_t b_dims[2] = {dn, T}, q_fwd[3] = {dn, r, N}, q_bwd[3] = {r, dn, N};
+    const uint64_t q_fwd[3] = {dn, r, N}, q_bwd[3] = {r, dn, N};
     if (!encode_f16_map(&mQ, a.Q, 3, kT ? q_bwd : q_fwd, kT ? wide : flat)) return cudaErrorInvalidValue;
-    if (!a.base)
-      mB = mQ;
-    else if (!encode_f16_map(&mB, a.base, 2, b_dims, row_box))
-      return cudaErrorInvalidValue;
     ta.parts_n = std::max(1, std::min(8, (a.dn / kChunk) / 8));
-  } else {
-    memset(&mQ, 0, sizeof(mQ));
-    mB = mQ;
   }
   const int grid = (int)std::min<long long>(tiles * ta.parts_n, fit);
-  return launch_k(kern, grid, kTallThreads, smem, s, true, mQ, mB, ta);
+  return launch_k(kern, grid, kTallThreads, smem, s, true, mQ, ta);
 }
 template <bool kT, int R>
 cudaError_t launch_f32(const AdapterArgs& a, cudaStream_t s) {
