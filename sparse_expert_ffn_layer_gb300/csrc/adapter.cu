@@ -18,9 +18,10 @@
 // (base and Q) load while h is being exchanged, and the next tile's rows while this one is
 // written.  Long runs (tiles of 64 rows) take two launches, see there.
 //
-// f16: h keeps 22 bits.  It is scaled by a power of two per row and split into two f16 parts,
-// and the second product adds both (h rounded to one f16 would cost as much accuracy as the
-// rounding of y does, and could overflow).  f32: fused multiply-adds on the CUDA cores.
+// f16: h is kept in 32 bits (and given out so) and rounded to f16 for the second product, as the
+// expert FFN rounds its hidden activations; each row is scaled by a power of two first, so that
+// no h overflows or loses bits below f16's range.  The rounding adds at most 2^-11 of the sum of
+// |h Q| to y's own 2^-11 |y|.  f32: fused multiply-adds on the CUDA cores.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -203,6 +204,7 @@ struct TallRing {
   uint32_t lphase = 1;
 
   __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return;
     const bool before = *abort != 0;
     // a wait that gives up marks the call; the block then runs through without further waits
     if (!mbar_wait_bounded(bar, parity, abort, nullptr, kDefaultWaitNs) && !before) *status = kErrTimeout;
@@ -459,7 +461,7 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
     if ((unsigned)y1 >= (unsigned)a.T) y1 = -1;
     // ---- h in the layout of the product's left operand: rows g and g + 8, columns
     // 16 k + 2 (lane % 4) + {0, 1, 8, 9}; a row's columns are spread over four lanes
-    uint32_t fh[R / 16][4], fl[R / 16][4];
+    uint32_t fh[R / 16][4];
     float m0, m1;
     {
       const int sa = s0 + wr + (lane >> 2), sb = sa + 8;
@@ -519,11 +521,8 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float i = q & 1 ? ib : ia;
-          __half2 hi, lo;
-          split_f16(v[k][q].x * i, hi.x, lo.x);
-          split_f16(v[k][q].y * i, hi.y, lo.y);
-          fh[k][q] = *reinterpret_cast<const uint32_t*>(&hi);
-          fl[k][q] = *reinterpret_cast<const uint32_t*>(&lo);
+          const __half2 h = __floats2half2_rn(v[k][q].x * i, v[k][q].y * i);
+          fh[k][q] = *reinterpret_cast<const uint32_t*>(&h);
         }
     }
     // ---- 32 of a chunk's 64 columns per warp
@@ -546,8 +545,6 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
                           swz<RB * 2>(wc * 32 + j * 16 + l7 + lh * 8, 2 * (k % 4) + l3));
           else
             ldsm4_t(fb, qs + swz<128>(k * 16 + l15, wc * 4 + j * 2 + lh));
-          mma16816(acc[2 * j], fl[k], fb[0], fb[1]);
-          mma16816(acc[2 * j + 1], fl[k], fb[2], fb[3]);
           mma16816(acc[2 * j], fh[k], fb[0], fb[1]);
           mma16816(acc[2 * j + 1], fh[k], fb[2], fb[3]);
         }
@@ -598,8 +595,8 @@ struct Plan16 {
   static constexpr int kStage = MT * kRowB + kW;
   static constexpr int kStages = MT == 64 ? (R >= 128 ? 3 : 4) : (R >= 128 ? 4 : R >= 64 ? 6 : 8);
   static constexpr int kOffPart = kStages * kStage;                // partial h [WK][MT][R]
-  static constexpr int kOffH = kOffPart + WK * MT * R * 4;         // h: two f16 parts
-  static constexpr int kOffMult = kOffH + MT * kLdR * 4;
+  static constexpr int kOffH = kOffPart + WK * MT * R * 4;         // h
+  static constexpr int kOffMult = kOffH + MT * kLdR * 2;
   static constexpr int kOffTab = kOffMult + MT * 4;                // offsets, tile starts, scratch
 };
 
@@ -621,8 +618,7 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
     return;
   }
   float* part = reinterpret_cast<float*>(sm + PL::kOffPart);
-  __half* hhi = reinterpret_cast<__half*>(sm + PL::kOffH);        // [MT][R + 8], then lo
-  __half* hlo = hhi + MT * kLdR;
+  __half* hs = reinterpret_cast<__half*>(sm + PL::kOffH);         // [MT][R + 8]
   float* mult = reinterpret_cast<float*>(sm + PL::kOffMult);
   int* bound = reinterpret_cast<int*>(sm + PL::kOffTab);
   int* start = bound + a.N + 1;
@@ -840,22 +836,15 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
       for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(grp, m, o));
       const int e = scale_exp(m);
       const float inv = exp2_int(-e);
-      __half2 hi[CPT / 2], lo[CPT / 2];
+      __half2 hv[CPT / 2];
 #pragma unroll
-      for (int j = 0; j < CPT; j += 2) {
-        split_f16(v[j] * inv, hi[j / 2].x, lo[j / 2].x);
-        split_f16(v[j + 1] * inv, hi[j / 2].y, lo[j / 2].y);
-      }
+      for (int j = 0; j < CPT; j += 2) hv[j / 2] = __floats2half2_rn(v[j] * inv, v[j + 1] * inv);
       const float mu = a.scale[n] * exp2_int(e);
 #pragma unroll
       for (int q = 0; q < kCl; ++q) {
-        __half* dh = cl.map_shared_rank(hhi, q) + row * kLdR + c0;
-        __half* dl = cl.map_shared_rank(hlo, q) + row * kLdR + c0;
+        __half* dh = cl.map_shared_rank(hs, q) + row * kLdR + c0;
 #pragma unroll
-        for (int j = 0; j < CPT / 2; ++j) {
-          reinterpret_cast<__half2*>(dh)[j] = hi[j];
-          reinterpret_cast<__half2*>(dl)[j] = lo[j];
-        }
+        for (int j = 0; j < CPT / 2; ++j) reinterpret_cast<__half2*>(dh)[j] = hv[j];
         if ((tid & 7) == 0) cl.map_shared_rank(mult, q)[row] = mu;
       }
     }
@@ -864,12 +853,9 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
     // ---- second product: this block's output columns
     constexpr int NF = 8 / WC;                    // 8-column fragments of a chunk per warp
     const int c0 = wc * NF * 8;
-    uint32_t fh[R / 16][4], fl[R / 16][4];
+    uint32_t fh[R / 16][4];
 #pragma unroll
-    for (int k = 0; k < R / 16; ++k) {
-      frag_a(fh[k], hhi + wr * kLdR + k * 16, kLdR, lane);
-      frag_a(fl[k], hlo + wr * kLdR + k * 16, kLdR, lane);
-    }
+    for (int k = 0; k < R / 16; ++k) frag_a(fh[k], hs + wr * kLdR + k * 16, kLdR, lane);
     const int g = lane >> 2, q2 = 2 * (lane & 3);
     const float m0 = mult[wr + g], m1 = mult[wr + g + 8];
     for (int c = n0; c < n1; ++c) {
@@ -889,8 +875,6 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
             frag_b_nk(fb, qs + (c0 + j * 16) * kLdR + k * 16, kLdR, lane);
           else
             frag_b_kn(fb, qs + k * 16 * kLdC + c0 + j * 16, kLdC, lane);
-          mma16816(acc[2 * j], fl[k], fb[0], fb[1]);
-          mma16816(acc[2 * j + 1], fl[k], fb[2], fb[3]);
           mma16816(acc[2 * j], fh[k], fb[0], fb[1]);
           mma16816(acc[2 * j + 1], fh[k], fb[2], fb[3]);
         }
@@ -1217,7 +1201,7 @@ cudaError_t launch_tall(const AdapterArgs& a, float* partial, cudaStream_t s) {
   if (a.dn) {
     const uint64_t q_fwd[3] = {dn, r, N}, q_bwd[3] = {r, dn, N};
     if (!encode_f16_map(&mQ, a.Q, 3, kT ? q_bwd : q_fwd, kT ? wide : flat)) return cudaErrorInvalidValue;
-    ta.parts_n = std::max(1, std::min(8, (a.dn / kChunk) / 8));
+    ta.parts_n = adapter_parts(a.S_max, a.dn);
   }
   const int grid = (int)std::min<long long>(tiles * ta.parts_n, fit);
   return launch_k(kern, grid, kTallThreads, smem, s, true, mQ, ta);
@@ -1249,11 +1233,21 @@ __global__ void __launch_bounds__(1024) adapter_check_kernel(const AdapterArgs a
 
 bool adapter_tall(int S_max, int N, bool f16) { return f16 && S_max > 32LL * std::min(N, S_max); }
 
-// Parts of the first product's columns: enough items for two blocks on each of 152 SMs, four
-// chunks each at least.
-int adapter_parts(int S_max, int dk) {
-  const int tiles = (S_max + kTallRows - 1) / kTallRows, chunks = (dk + kChunk - 1) / kChunk;
-  return std::max(1, std::min({kAdapterParts, 304 / std::max(1, tiles), chunks / 4}));
+// Parts of a product's columns over the tiles: the count with the fewest rounds of chunks (with
+// two chunks for the start of an item) on two blocks of each of 152 SMs, four chunks or more each.
+int adapter_parts(int S_max, int d) {
+  const long long tiles = std::max(1, (S_max + kTallRows - 1) / kTallRows);
+  const int chunks = (d + kChunk - 1) / kChunk;
+  int best = 1;
+  long long cost = 0;
+  for (int p = 1; p <= kAdapterParts && (p == 1 || chunks / p >= 4); ++p) {
+    const long long c = (tiles * p + 303) / 304 * ((chunks + p - 1) / p + 2);
+    if (p == 1 || c < cost) {
+      best = p;
+      cost = c;
+    }
+  }
+  return best;
 }
 
 cudaError_t launch_adapter(const void* x, const void* P, const void* Q, const void* base, void* y,
