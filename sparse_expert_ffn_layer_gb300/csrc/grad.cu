@@ -1,13 +1,12 @@
 // Gradients around the gate and the adapters: products summed over token rows (weights'
 // gradients), the tokens' gradient through the gate, and the combine's gradient.
-#include <cooperative_groups.h>
-
 #include <algorithm>
+#include <cmath>
+#include <cstring>
 
+#include "groups.cuh"
 #include "launch.h"
 #include "mma.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace moe {
 namespace {
@@ -15,21 +14,23 @@ namespace {
 // ---------------------------------------------------------------- sums over rows
 // G[n][i][j] = scale_n sum_s x[t(s)][i] h[s][j] over the rows s of group n, in 32 bits.
 //
-// Bound by DRAM: x is streamed once (per 128 columns j), G written once.  A block owns 128
-// columns i of one group and walks its rows in chunks of 64: x by asynchronous copies (a ring of
-// four chunks), h through registers.  h is a 32-bit input of any range and the rows are the
-// summed index, so per chunk it is scaled by one power of two (from the chunk's largest
-// magnitude) and split into two f16 parts, 22 bits together; the chunk's product is scaled back
-// as it is added to the 32-bit running sums (which also keeps a long sum out of the tensor
-// cores' accumulators, whose additions truncate).
+// The groups' rows are cut into segments of at most `seg` rows; a block takes one segment and 128
+// columns i (f32: 64) and walks its rows in chunks of 64 (f32: 32): x by asynchronous copies,
+// h through registers.  A group of one segment is written at once; the segments of a longer one
+// leave partial sums that a second launch adds in order (no atomics: equal calls give equal bits;
+// skewed groups are spread evenly, which a fixed number of blocks per group was not).
 //
-// Few blocks and many rows: the rows are split over a cluster of up to eight blocks, whose sums
-// are joined through distributed shared memory in rank order, so results do not depend on timing.
+// f16: h is a 32-bit input of any range and the rows are the summed index, so per chunk it is
+// scaled by one power of two (from the chunk's largest magnitude) and split into two f16 parts,
+// 22 bits together; the chunk's product is scaled back as it is added to the 32-bit running sums
+// (which also ends the tensor cores' chains of truncating additions every 64 rows).
 struct SumJob {
   const void* x;         // [rows, di]
   const float* h;        // [rows or slots, dj]
   float* G;              // [N, di, dj], or [N, dj, di] when transposed
-  int di, dj, transposed, blocks;
+  float* partial;        // [slots][di dj], laid out as G
+  int di, dj, transposed;
+  int bi, blocks;        // column blocks of di; blocks of a segment in all (bi x those of dj)
 };
 struct SumArgs {
   SumJob job[2];
@@ -37,7 +38,7 @@ struct SumArgs {
   const int32_t* perm;   // row of each slot, or null (the slot itself)
   const int32_t* offsets;   // [N + 1], or null (one group of all rows)
   const uint8_t* mask;   // rows that count, or null (perm == null only)
-  int T, S_max;
+  int T, S_max, N, seg;
 };
 
 constexpr int kSumThreads = 256;
@@ -45,15 +46,6 @@ constexpr int kIT = 128;             // columns i per block (f16)
 constexpr int kRows = 64;            // rows per chunk (f16)
 constexpr int kLdX = kIT + 8;
 constexpr int kSumStages = 4;
-
-__device__ __forceinline__ void group_rows(const SumArgs& a, int n, int* lo, int* hi) {
-  *lo = 0;
-  *hi = a.S_max;
-  if (a.offsets) {
-    *lo = min(max(a.offsets[n], 0), a.S_max);
-    *hi = max(*lo, min(max(a.offsets[n + 1], 0), a.S_max));
-  }
-}
 
 // Row of slot s, -1 where it is to be left out.
 __device__ __forceinline__ int row_of(const SumArgs& a, int s, int hi) {
@@ -65,177 +57,247 @@ __device__ __forceinline__ int row_of(const SumArgs& a, int s, int hi) {
   return a.mask && !a.mask[s] ? -1 : s;
 }
 
-// Joins the cluster's sums red[IT][ld] (this block's rows i and R columns j) and writes them.
-template <int IT, int R>
-__device__ __forceinline__ void join_and_store(const SumJob& jb, float* red, int ld, int i0, int j0,
-                                               int n, float scale) {
-  cg::cluster_group cl = cg::this_cluster();
-  const int ncl = (int)cl.num_blocks(), rank = (int)cl.block_rank();
-  cl.sync();
-  const int per = IT / ncl, r0 = rank * per;
-  const int nj = min(R, jb.dj - j0);
-  float* G = jb.G + (size_t)n * jb.di * jb.dj;
-  for (int q = threadIdx.x; q < per * R; q += kSumThreads) {
-    const int i = r0 + (jb.transposed ? q % per : q / R), j = jb.transposed ? q / per : q % R;
-    if (j >= nj || i0 + i >= jb.di) continue;
-    float v = 0.f;
-    for (int b = 0; b < ncl; ++b) v += cl.map_shared_rank(red, b)[i * ld + j];
-    v *= scale;
-    if (jb.transposed)
-      G[(size_t)(j0 + j) * jb.di + i0 + i] = v;
-    else
-      G[(size_t)(i0 + i) * jb.dj + j0 + j] = v;
+// Segments: a table over the groups in shared memory, or the one group of all rows.
+struct Segments {
+  int *bound, *start;
+  int count;
+};
+__device__ __forceinline__ Segments segment_table(const SumArgs& a, int* mem) {
+  Segments g;
+  g.bound = mem;
+  g.start = mem + a.N + 1;
+  if (a.offsets) {
+    group_table<kSumThreads>(a.offsets, a.N, a.S_max, a.seg, g.bound, g.start, g.start + a.N + 1);
+  } else {
+    if (threadIdx.x == 0) {
+      g.bound[0] = g.start[0] = 0;
+      g.bound[1] = a.S_max;
+      g.start[1] = (a.S_max + a.seg - 1) / a.seg;
+    }
+    __syncthreads();
   }
-  cl.sync();                                       // no block leaves while its sums are read
+  g.count = g.start[a.N];
+  return g;
 }
 
+// Partial sums of a segment that starts at slot s0: in a window of `seg` slots at most one
+// segment that is not its group's last one starts (it is `seg` long), and at most one last one
+// of a group with several.
+__device__ __forceinline__ int partial_slot(int s0, int seg, bool last) { return 2 * (s0 / seg) + last; }
+
+// One item of a block: rows [lo, hi) of group n, columns i0.. and j0.. of a job.
+struct SumItem {
+  int n, lo, hi, i0, j0;
+  const SumJob* jb;
+  float* dst;            // G or partial sums, at the job's [i][j] = [0][0]
+  float scale;
+};
+template <int IT, int R>
+__device__ __forceinline__ SumItem sum_item(const SumArgs& a, const Segments& g, int item) {
+  SumItem it;
+  const int per = a.job[0].blocks + a.job[1].blocks;
+  const int sgm = item / per;
+  int b = item - sgm * per;
+  it.n = a.offsets ? group_of(sgm, g.start, a.N) : 0;
+  it.lo = g.bound[it.n] + (sgm - g.start[it.n]) * a.seg;
+  it.hi = min(it.lo + a.seg, g.bound[it.n + 1]);
+  it.jb = &a.job[0];
+  if (b >= a.job[0].blocks) {
+    b -= a.job[0].blocks;
+    it.jb = &a.job[1];
+  }
+  it.i0 = (b % it.jb->bi) * IT;
+  it.j0 = (b / it.jb->bi) * R;
+  const size_t all = (size_t)it.jb->di * it.jb->dj;
+  if (g.start[it.n + 1] - g.start[it.n] == 1) {
+    it.dst = it.jb->G + it.n * all;
+    it.scale = a.scale ? a.scale[it.n] : 1.f;
+  } else {
+    it.dst = it.jb->partial + partial_slot(it.lo, a.seg, it.hi == g.bound[it.n + 1]) * all;
+    it.scale = 1.f;
+  }
+  return it;
+}
+__device__ __forceinline__ void store_sum(const SumItem& it, int i, int j, float v) {
+  if (i < it.jb->di && j < it.jb->dj)
+    it.dst[it.jb->transposed ? (size_t)j * it.jb->di + i : (size_t)i * it.jb->dj + j] = it.scale * v;
+}
+
+// Warps of a block over the 128 x R sums: 32 x R / 2 each (R = 16: 16 x 16).
 template <int R>
-__global__ void __launch_bounds__(kSumThreads) row_sum_f16_kernel(const SumArgs a) {
+struct SumWarps {
+  static constexpr int WJ = R >= 32 ? 2 : 1, WI = 8 / WJ;
+  static constexpr int MI = kIT / WI / 16, NJ = R / WJ / 8;        // 16-row and 8-column fragments
+};
+
+template <int R>
+__global__ void __launch_bounds__(kSumThreads, R >= 128 ? 1 : 2) row_sum_f16_kernel(const SumArgs a) {
   constexpr int kLdH = R + 8;
   constexpr int kHB = kRows * kLdH;                // halves of one f16 part
   constexpr int NV = kRows * R / kSumThreads;      // h values per thread and chunk
+  constexpr int MI = SumWarps<R>::MI, NJ = SumWarps<R>::NJ, WI = SumWarps<R>::WI;
   extern __shared__ __align__(128) uint8_t sm[];
   __half* xs = reinterpret_cast<__half*>(sm);                         // [stages][64][kLdX]
   __half* hs = xs + kSumStages * kRows * kLdX;                        // [2][hi, lo][64][kLdH]
-  __shared__ float wmax[2][kSumThreads / 32];
-  cg::cluster_group cl = cg::this_cluster();
-  const int ncl = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  float* wmax = reinterpret_cast<float*>(hs + 4 * kHB);               // [2][warps]
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const bool second = (int)blockIdx.x >= a.job[0].blocks;
-  const SumJob jb = second ? a.job[1] : a.job[0];
-  const int i0 = ((int)blockIdx.x - (second ? a.job[0].blocks : 0)) * kIT;
-  const int n = blockIdx.y, j0 = (blockIdx.z / ncl) * R;
-  const int dj = jb.dj;
-  const __half* X = static_cast<const __half*>(jb.x);
-  int lo, hi;
-  group_rows(a, n, &lo, &hi);
-  const int chunks = (hi - lo + kRows - 1) / kRows;
-  const int c0 = (int)((long long)chunks * rank / ncl), c1 = (int)((long long)chunks * (rank + 1) / ncl);
+  pdl_trigger();
+  pdl_wait();                                      // h may come from the launch before
+  const Segments g = segment_table(a, reinterpret_cast<int*>(wmax + 2 * kSumThreads / 32));
+  const int items = g.count * (a.job[0].blocks + a.job[1].blocks);
+  const int wi = (w % WI) * MI * 16, wj = (w / WI) * NJ * 8;
+  const int xc = (tid & 15) * 8, xr = tid >> 4;    // x: 16-byte piece, rows xr + 16 p
+  const int hr = tid * NV / R, hc = tid * NV % R;  // h: NV consecutive values of one row
 
-  // x: thread's pieces are column piece tid % 16 of rows tid / 16 + 16 p
-  const int xc = (tid & 15) * 8;
-  int rows_next[4];
-  auto fetch_rows = [&](int c) {
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const SumItem it = sum_item<kIT, R>(a, g, item);
+    const int di = it.jb->di, dj = it.jb->dj;
+    const __half* X = static_cast<const __half*>(it.jb->x) + it.i0 + xc;
+    const bool xin = it.i0 + xc < di;
+    const int chunks = (it.hi - it.lo + kRows - 1) / kRows;
+    int rows_next[4];
+    auto fetch_rows = [&](int c) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p) rows_next[p] = row_of(a, lo + c * kRows + (tid >> 4) + 16 * p, hi);
-  };
-  auto load_x = [&](int c) {                       // rows_next holds chunk c's rows
-    __half* dst = xs + (c % kSumStages) * kRows * kLdX;
+      for (int p = 0; p < 4; ++p) rows_next[p] = row_of(a, it.lo + c * kRows + xr + 16 * p, it.hi);
+    };
+    auto load_x = [&](int c) {                     // rows_next holds chunk c's rows
+      __half* dst = xs + (c % kSumStages) * kRows * kLdX + xr * kLdX + xc;
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const bool on = rows_next[p] >= 0 && i0 + xc < jb.di;
-      cp_async16(dst + ((tid >> 4) + 16 * p) * kLdX + xc,
-                 X + (on ? (size_t)rows_next[p] * jb.di + i0 + xc : 0), on);
-    }
-  };
-  // h: thread holds NV consecutive values of one row
-  const int hr = tid * NV / R, hc = tid * NV % R;
-  float hv[NV];
-  auto load_h = [&](int c) {
-    const int s = lo + c * kRows + hr;
-    const bool on = c < c1 && row_of(a, s, hi) >= 0;
-    const float* src = jb.h + (size_t)(on ? s : 0) * dj + j0 + hc;
-    if (dj % 4 == 0) {
-#pragma unroll
-      for (int q = 0; q < NV; q += 4) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (on && j0 + hc + q < dj) v = *reinterpret_cast<const float4*>(src + q);
-        hv[q] = v.x; hv[q + 1] = v.y; hv[q + 2] = v.z; hv[q + 3] = v.w;
+      for (int p = 0; p < 4; ++p) {
+        const bool on = xin && rows_next[p] >= 0;
+        cp_async16(dst + 16 * p * kLdX, on ? X + (size_t)rows_next[p] * di : X, on);
       }
-    } else {
+    };
+    float hv[NV];
+    auto load_h = [&](int c) {
+      const int s = it.lo + c * kRows + hr;
+      const bool on = row_of(a, s, it.hi) >= 0;
+      const float* src = it.jb->h + (size_t)(on ? s : 0) * dj + it.j0 + hc;
+      if (dj % 4 == 0) {
 #pragma unroll
-      for (int q = 0; q < NV; ++q) hv[q] = on && j0 + hc + q < dj ? src[q] : 0.f;
-    }
-  };
-
-  float acc[R / 8][4];
+        for (int q = 0; q < NV; q += 4) {
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (on && it.j0 + hc + q < dj) v = *reinterpret_cast<const float4*>(src + q);
+          hv[q] = v.x; hv[q + 1] = v.y; hv[q + 2] = v.z; hv[q + 3] = v.w;
+        }
+      } else {
 #pragma unroll
-  for (int i = 0; i < R / 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-
-  for (int p = 0; p < kSumStages - 1; ++p) {
-    if (c0 + p < c1) {
-      fetch_rows(c0 + p);
-      load_x(c0 + p);
-    }
-    cp_async_commit();
-  }
-  if (c0 + kSumStages - 1 < c1) fetch_rows(c0 + kSumStages - 1);
-  load_h(c0);
-  for (int c = c0; c < c1; ++c) {
-    const int b = (c - c0) & 1;
-    // this chunk's power of two
-    float m = 0.f;
-    bool odd = false;
-#pragma unroll
-    for (int q = 0; q < NV; ++q) {
-      m = fmaxf(m, fabsf(hv[q]));
-      odd |= !isfinite(hv[q]);
-    }
-    if (odd) m = INFINITY;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) wmax[b][w] = m;
-    cp_async_wait<kSumStages - 2>();
-    __syncthreads();                               // chunk c of x is in; every wmax is written
-#pragma unroll
-    for (int q = 0; q < kSumThreads / 32; ++q) m = fmaxf(m, wmax[b][q]);
-    const int e = scale_exp(m);
-    const float inv = exp2_int(-e), mul = exp2_int(e);
-    __half* hhi = hs + b * 2 * kHB;
-    __half* hlo = hhi + kHB;
-#pragma unroll
-    for (int q = 0; q < NV; q += 2) {
-      __half2 u, v;
-      split_f16(hv[q] * inv, u.x, v.x);
-      split_f16(hv[q + 1] * inv, u.y, v.y);
-      *reinterpret_cast<__half2*>(hhi + hr * kLdH + hc + q) = u;
-      *reinterpret_cast<__half2*>(hlo + hr * kLdH + hc + q) = v;
-    }
-    if (c + 1 < c1) load_h(c + 1);
-    if (c + kSumStages - 1 < c1) load_x(c + kSumStages - 1);
-    cp_async_commit();
-    if (c + kSumStages < c1) fetch_rows(c + kSumStages);
-    __syncthreads();
-    const __half* xb = xs + (c % kSumStages) * kRows * kLdX;
-    float t[R / 8][4];
-#pragma unroll
-    for (int i = 0; i < R / 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) t[i][j] = 0.f;
-#pragma unroll
-    for (int k = 0; k < kRows; k += 16) {
-      uint32_t fa[4];
-      frag_a_t(fa, xb + k * kLdX + w * 16, kLdX, lane);
-#pragma unroll
-      for (int j = 0; j < R / 16; ++j) {
-        uint32_t fh[4], fl[4];
-        frag_b_kn(fl, hlo + k * kLdH + j * 16, kLdH, lane);
-        frag_b_kn(fh, hhi + k * kLdH + j * 16, kLdH, lane);
-        mma16816(t[2 * j], fa, fl[0], fl[1]);
-        mma16816(t[2 * j + 1], fa, fl[2], fl[3]);
-        mma16816(t[2 * j], fa, fh[0], fh[1]);
-        mma16816(t[2 * j + 1], fa, fh[2], fh[3]);
+        for (int q = 0; q < NV; ++q) hv[q] = on && it.j0 + hc + q < dj ? src[q] : 0.f;
       }
+    };
+    float acc[MI][NJ][4];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[i][j][q] = 0.f;
+
+    for (int p = 0; p < kSumStages - 1; ++p) {
+      if (p < chunks) {
+        fetch_rows(p);
+        load_x(p);
+      }
+      cp_async_commit();
     }
+    if (kSumStages - 1 < chunks) fetch_rows(kSumStages - 1);
+    load_h(0);
+    for (int c = 0; c < chunks; ++c) {
+      const int b = c & 1;
+      // this chunk's power of two
+      float m = 0.f;
+      bool odd = false;
 #pragma unroll
-    for (int i = 0; i < R / 8; ++i)
+      for (int q = 0; q < NV; ++q) {
+        m = fmaxf(m, fabsf(hv[q]));
+        odd |= !(fabsf(hv[q]) < INFINITY);
+      }
+      if (odd) m = INFINITY;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(mul, t[i][j], acc[i][j]);
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (lane == 0) wmax[b * (kSumThreads / 32) + w] = m;
+      cp_async_wait<kSumStages - 2>();
+      __syncthreads();                             // chunk c of x is in; every wmax is written
+#pragma unroll
+      for (int q = 0; q < kSumThreads / 32; ++q) m = fmaxf(m, wmax[b * (kSumThreads / 32) + q]);
+      const int e = scale_exp(m);
+      const float inv = exp2_int(-e), mul = exp2_int(e);
+      __half* hhi = hs + b * 2 * kHB;
+      __half* hlo = hhi + kHB;
+      if (m < INFINITY) {
+#pragma unroll
+        for (int q = 0; q < NV; q += 2) {
+          const float u = hv[q] * inv, v = hv[q + 1] * inv;
+          const __half2 hi = __floats2half2_rn(u, v);
+          const float2 f = __half22float2(hi);
+          *reinterpret_cast<__half2*>(hhi + hr * kLdH + hc + q) = hi;
+          *reinterpret_cast<__half2*>(hlo + hr * kLdH + hc + q) = __floats2half2_rn(u - f.x, v - f.y);
+        }
+      } else {                                     // infinities or NaN: a part each, unscaled
+#pragma unroll
+        for (int q = 0; q < NV; ++q) split_f16(hv[q], hhi[hr * kLdH + hc + q], hlo[hr * kLdH + hc + q]);
+      }
+      if (c + 1 < chunks) load_h(c + 1);
+      if (c + kSumStages - 1 < chunks) load_x(c + kSumStages - 1);
+      cp_async_commit();
+      if (c + kSumStages < chunks) fetch_rows(c + kSumStages);
+      __syncthreads();
+      const __half* xb = xs + (c % kSumStages) * kRows * kLdX;
+      float t[MI][NJ][4];
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) t[i][j][q] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kRows; k += 16) {
+        uint32_t fa[MI][4];
+#pragma unroll
+        for (int i = 0; i < MI; ++i) frag_a_t(fa[i], xb + k * kLdX + wi + i * 16, kLdX, lane);
+#pragma unroll
+        for (int j = 0; j < NJ / 2 + NJ % 2; ++j) {
+          uint32_t fh[4], fl[4];
+          if (NJ == 1) {                           // eight columns: half of a 16-column load
+            frag_b_kn(fl, hlo + k * kLdH + (wj & ~15), kLdH, lane);
+            frag_b_kn(fh, hhi + k * kLdH + (wj & ~15), kLdH, lane);
+            const int o = (wj & 8) >> 2;
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+              mma16816(t[i][0], fa[i], o ? fl[2] : fl[0], o ? fl[3] : fl[1]);
+              mma16816(t[i][0], fa[i], o ? fh[2] : fh[0], o ? fh[3] : fh[1]);
+            }
+          } else {
+            frag_b_kn(fl, hlo + k * kLdH + wj + j * 16, kLdH, lane);
+            frag_b_kn(fh, hhi + k * kLdH + wj + j * 16, kLdH, lane);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+              mma16816(t[i][2 * j], fa[i], fl[0], fl[1]);
+              mma16816(t[i][2 * j + 1], fa[i], fl[2], fl[3]);
+              mma16816(t[i][2 * j], fa[i], fh[0], fh[1]);
+              mma16816(t[i][2 * j + 1], fa[i], fh[2], fh[3]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(mul, t[i][j][q], acc[i][j][q]);
+    }
+    cp_async_wait<0>();
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          store_sum(it, it.i0 + wi + 16 * i + (lane >> 2) + 8 * (q >> 1),
+                    it.j0 + wj + 8 * j + 2 * (lane & 3) + (q & 1), acc[i][j][q]);
+    __syncthreads();                               // the ring is free for the next item
   }
-  cp_async_wait<0>();
-  __syncthreads();
-  float* red = reinterpret_cast<float*>(sm);       // [128][R + 4], over the ring
-  constexpr int ld = R + 4;
-  static_assert(kIT * ld * 4 <= kSumStages * kRows * kLdX * 2, "the sums fit over the ring");
-  float* p = red + (w * 16 + (lane >> 2)) * ld + 2 * (lane & 3);
-#pragma unroll
-  for (int j = 0; j < R / 8; ++j) {
-    *reinterpret_cast<float2*>(p + 8 * j) = make_float2(acc[j][0], acc[j][1]);
-    *reinterpret_cast<float2*>(p + 8 * ld + 8 * j) = make_float2(acc[j][2], acc[j][3]);
-  }
-  join_and_store<kIT, R>(jb, red, ld, i0, j0, n, a.scale ? a.scale[n] : 1.f);
 }
 
 // 32-bit inputs: fused multiply-adds; 64 columns i per block, chunks of 32 rows.
@@ -245,99 +307,147 @@ constexpr int kRows32 = 32;
 template <int R>
 __global__ void __launch_bounds__(kSumThreads) row_sum_f32_kernel(const SumArgs a) {
   constexpr int JT = R / 16;
-  __shared__ __align__(16) float xs[kRows32][kIT32];
-  extern __shared__ __align__(16) float dyn[];     // h chunk [32][R], then the sums [64][R + 1]
-  cg::cluster_group cl = cg::this_cluster();
-  const int ncl = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  extern __shared__ __align__(16) float dyn[];     // x chunk [32][64], h chunk [32][R], table
+  float* xs = dyn;
+  float* hs = dyn + kRows32 * kIT32;
   const int tid = threadIdx.x;
-  const bool second = (int)blockIdx.x >= a.job[0].blocks;
-  const SumJob jb = second ? a.job[1] : a.job[0];
-  const int i0 = ((int)blockIdx.x - (second ? a.job[0].blocks : 0)) * kIT32;
-  const int n = blockIdx.y, j0 = (blockIdx.z / ncl) * R;
-  const float* X = static_cast<const float*>(jb.x);
-  int lo, hi;
-  group_rows(a, n, &lo, &hi);
-  const int chunks = (hi - lo + kRows32 - 1) / kRows32;
-  const int c0 = (int)((long long)chunks * rank / ncl), c1 = (int)((long long)chunks * (rank + 1) / ncl);
+  pdl_trigger();
+  pdl_wait();                                      // h may come from the launch before
+  const Segments g = segment_table(a, reinterpret_cast<int*>(hs + kRows32 * R));
+  const int items = g.count * (a.job[0].blocks + a.job[1].blocks);
   const int ti = (tid & 15) * 4, tj = tid >> 4;
-  float acc[4][JT];
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const SumItem it = sum_item<kIT32, R>(a, g, item);
+    const int di = it.jb->di, dj = it.jb->dj;
+    const float* X = static_cast<const float*>(it.jb->x);
+    const int chunks = (it.hi - it.lo + kRows32 - 1) / kRows32;
+    float acc[4][JT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < JT; ++j) acc[i][j] = 0.f;
-  for (int c = c0; c < c1; ++c) {
-    __syncthreads();
-    for (int q = tid; q < kRows32 * kIT32 / 4; q += kSumThreads) {
-      const int r = q / (kIT32 / 4), i = (q % (kIT32 / 4)) * 4;
-      const int t = row_of(a, lo + c * kRows32 + r, hi);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t >= 0 && i0 + i < jb.di) v = *reinterpret_cast<const float4*>(X + (size_t)t * jb.di + i0 + i);
-      *reinterpret_cast<float4*>(&xs[r][i]) = v;
-    }
-    for (int q = tid; q < kRows32 * R; q += kSumThreads) {
-      const int r = q / R, j = q % R, s = lo + c * kRows32 + r;
-      dyn[q] = j0 + j < jb.dj && row_of(a, s, hi) >= 0 ? jb.h[(size_t)s * jb.dj + j0 + j] : 0.f;
-    }
-    __syncthreads();
+      for (int j = 0; j < JT; ++j) acc[i][j] = 0.f;
+    for (int c = 0; c < chunks; ++c) {
+      __syncthreads();
+      for (int q = tid; q < kRows32 * kIT32 / 4; q += kSumThreads) {
+        const int r = q / (kIT32 / 4), i = (q % (kIT32 / 4)) * 4;
+        const int t = row_of(a, it.lo + c * kRows32 + r, it.hi);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t >= 0 && it.i0 + i < di) v = *reinterpret_cast<const float4*>(X + (size_t)t * di + it.i0 + i);
+        *reinterpret_cast<float4*>(xs + r * kIT32 + i) = v;
+      }
+      for (int q = tid; q < kRows32 * R; q += kSumThreads) {
+        const int r = q / R, j = q % R, s = it.lo + c * kRows32 + r;
+        hs[q] = it.j0 + j < dj && row_of(a, s, it.hi) >= 0 ? it.jb->h[(size_t)s * dj + it.j0 + j] : 0.f;
+      }
+      __syncthreads();
 #pragma unroll 4
-    for (int k = 0; k < kRows32; ++k) {
-      const float4 xv = *reinterpret_cast<const float4*>(&xs[k][ti]);
+      for (int k = 0; k < kRows32; ++k) {
+        const float4 xv = *reinterpret_cast<const float4*>(xs + k * kIT32 + ti);
 #pragma unroll
-      for (int j = 0; j < JT; ++j) {
-        const float h = dyn[k * R + tj + 16 * j];
-        acc[0][j] = fmaf(xv.x, h, acc[0][j]);
-        acc[1][j] = fmaf(xv.y, h, acc[1][j]);
-        acc[2][j] = fmaf(xv.z, h, acc[2][j]);
-        acc[3][j] = fmaf(xv.w, h, acc[3][j]);
+        for (int j = 0; j < JT; ++j) {
+          const float h = hs[k * R + tj + 16 * j];
+          acc[0][j] = fmaf(xv.x, h, acc[0][j]);
+          acc[1][j] = fmaf(xv.y, h, acc[1][j]);
+          acc[2][j] = fmaf(xv.z, h, acc[2][j]);
+          acc[3][j] = fmaf(xv.w, h, acc[3][j]);
+        }
       }
     }
+#pragma unroll
+    for (int j = 0; j < JT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) store_sum(it, it.i0 + ti + i, it.j0 + tj + 16 * j, acc[i][j]);
   }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < JT; ++j) dyn[(ti + i) * (R + 1) + tj + 16 * j] = acc[i][j];
-  join_and_store<kIT32, R>(jb, dyn, R + 1, i0, j0, n, a.scale ? a.scale[n] : 1.f);
+}
+
+// Groups of several segments: their partial sums in order; groups without rows: zero.
+__global__ void __launch_bounds__(256) row_sum_join_kernel(const SumArgs a) {
+  pdl_wait();                                      // on every path: completion stays transitive
+  const SumJob& jb = a.job[blockIdx.z];
+  const int n = blockIdx.y;
+  int lo = 0, hi = a.S_max;
+  if (a.offsets) {                                 // as group_table clamps them
+    lo = min(max(a.offsets[n], 0), a.S_max);
+    hi = max(lo, min(max(a.offsets[n + 1], 0), a.S_max));
+  }
+  const int segs = (hi - lo + a.seg - 1) / a.seg;
+  if (segs == 1 || !jb.G) return;
+  const float scale = a.scale ? a.scale[n] : 1.f;
+  const size_t all = (size_t)jb.di * jb.dj;
+  float* G = jb.G + n * all;
+  const size_t step = (size_t)gridDim.x * 256;
+  if (all % 4 == 0) {
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < all / 4; i += step) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+      for (int q = 0; q < segs; ++q) {
+        const float4 u = *reinterpret_cast<const float4*>(
+            jb.partial + partial_slot(lo + q * a.seg, a.seg, q == segs - 1) * all + 4 * i);
+        v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+      }
+      *reinterpret_cast<float4*>(G + 4 * i) = make_float4(scale * v.x, scale * v.y, scale * v.z, scale * v.w);
+    }
+  } else {
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < all; i += step) {
+      float v = 0.f;
+      for (int q = 0; q < segs; ++q)
+        v += jb.partial[partial_slot(lo + q * a.seg, a.seg, q == segs - 1) * all + i];
+      G[i] = scale * v;
+    }
+  }
+}
+
+// Rows per segment: the segments of S_max rows (and half a segment more per group) times the
+// column blocks take the fewest rounds of two blocks on each of 152 SMs, plus what a segment
+// costs in partial sums.
+int sum_segment(int S_max, int N, int blocks) {
+  int best = 64;
+  double cost = 1e300;
+  for (int p = 1; p <= kSumSegments; ++p) {
+    const int seg = std::max(256, ((S_max + p - 1) / p + 63) / 64 * 64);
+    const double items = blocks * ((double)S_max / seg + 0.5 * std::min(N, S_max));
+    const double c = ceil(items / 304) * (seg / 64 + 3) + p;
+    if (c < cost) {
+      cost = c;
+      best = seg;
+    }
+  }
+  return best;
 }
 
 template <typename Kern>
-cudaError_t launch_sum(Kern kern, size_t smem, SumArgs& a, int it, int R, int N, int rows_per_group,
-                       int chunk, int sms, cudaStream_t s) {
+cudaError_t launch_sum(Kern kern, size_t smem, SumArgs& a, int it, int R, int sms, bool pdl, cudaStream_t s) {
   MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
-  int blocks = 0, jb = 1;
+  int blocks = 0;
+  size_t widest = 0;
   for (SumJob& j : a.job) {
-    j.blocks = j.G ? (j.di + it - 1) / it : 0;
+    j.bi = (j.di + it - 1) / it;
+    j.blocks = j.G ? j.bi * ((j.dj + R - 1) / R) : 0;
     blocks += j.blocks;
-    if (j.G) jb = std::max(jb, (j.dj + R - 1) / R);
+    if (j.G) widest = std::max(widest, (size_t)j.di * j.dj);
   }
-  // rows split until the blocks fill the device twice, at two chunks per block or more
-  int cl = 1;
-  while (cl < 8 && (long long)blocks * N * jb * cl < 2LL * sms && rows_per_group >= 4 * chunk * cl) cl *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, N, jb * cl);
-  cfg.blockDim = dim3(kSumThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = cl;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, a);
-  if (err == cudaSuccess) launch_counter().fetch_add(1, std::memory_order_relaxed);
-  return err;
+  const long long most = ((long long)a.S_max / a.seg + std::min(a.N, a.S_max)) * blocks;
+  const int grid = (int)std::min<long long>(most, 2 * sms);
+  smem += sizeof(int) * (2 * ((size_t)a.N + 1) + 32);
+  MOE_LAUNCH(launch_k(kern, grid, kSumThreads, smem, s, pdl, a));
+  const int bx = (int)std::min<size_t>((widest / 4 + 255) / 256, std::max<size_t>(1, 8 * sms / a.N));
+  return launch_k(row_sum_join_kernel, dim3(std::max(1, bx), a.N, 2), 256, 0, s, true, a);
 }
 
 template <int R>
-cudaError_t launch_sum_rank(SumArgs& a, bool f16, int N, int rows, int sms, cudaStream_t s) {
+cudaError_t launch_sum_rank(SumArgs& a, bool f16, int sms, bool pdl, cudaStream_t s) {
   if (f16) {
-    const size_t smem = 2 * (size_t)(kSumStages * kRows * kLdX + 4 * kRows * (R + 8));
-    return launch_sum(row_sum_f16_kernel<R>, smem, a, kIT, R, N, rows, kRows, sms, s);
+    const size_t smem = 2 * (size_t)(kSumStages * kRows * kLdX + 4 * kRows * (R + 8)) + 64;
+    return launch_sum(row_sum_f16_kernel<R>, smem, a, kIT, R, sms, pdl, s);
   }
-  const size_t smem = sizeof(float) * std::max(kRows32 * R, kIT32 * (R + 1));
-  return launch_sum(row_sum_f32_kernel<R>, smem, a, kIT32, R, N, rows, kRows32, sms, s);
+  const size_t smem = sizeof(float) * (kRows32 * kIT32 + kRows32 * R);
+  return launch_sum(row_sum_f32_kernel<R>, smem, a, kIT32, R, sms, pdl, s);
+}
+
+// Column blocks of a job of either type, as launch_sum_rank cuts them.
+int sum_blocks(int di, int dj, int dj_max, bool f16) {
+  const int R = dj_max <= 16 ? 16 : dj_max <= 32 ? 32 : dj_max <= 64 ? 64 : 128, it = f16 ? kIT : kIT32;
+  return (di + it - 1) / it * ((dj + R - 1) / R);
 }
 
 // ---------------------------------------------------------------- tokens' gradient of the gate
@@ -476,28 +586,47 @@ cudaError_t launch_combine_backward_t(const void* dout, const void* y, const int
 
 }  // namespace
 
+size_t row_sums_bytes(int di0, int dj0, int di1, int dj1, bool f16, int S_max, int N) {
+  const int dj = std::max(dj0, dj1);
+  size_t most = 0;
+  // either job alone may be asked for: the plan of each combination fits
+  for (int q = 1; q < 4; ++q) {
+    const int b = (q & 1 ? sum_blocks(di0, dj0, q & 2 ? dj : dj0, f16) : 0) +
+                  (q & 2 ? sum_blocks(di1, dj1, q & 1 ? dj : dj1, f16) : 0);
+    const int seg = sum_segment(S_max, N, std::max(b, 1));
+    const size_t slots = 2 * (size_t)((S_max + seg - 1) / seg);
+    const size_t words = (q & 1 ? (size_t)di0 * dj0 : 0) + (q & 2 ? (size_t)di1 * dj1 : 0);
+    if (S_max > seg) most = std::max(most, slots * words * sizeof(float));
+  }
+  return most;
+}
+
 cudaError_t launch_row_sums(const void* x0, const float* h0, float* G0, int di0, int dj0, int tr0,
                             const void* x1, const float* h1, float* G1, int di1, int dj1, int tr1,
                             const float* scale, const int32_t* perm, const int32_t* offsets,
-                            const uint8_t* mask, int dtype_f16, int T, int S_max, int N,
-                            cudaStream_t s) {
+                            const uint8_t* mask, float* partial, int dtype_f16, int T, int S_max,
+                            int N, bool pdl, cudaStream_t s) {
   const int sms = sms_of_device();
   if (sms < 1) return cudaErrorInvalidDevice;
   SumArgs a;
-  a.job[0] = SumJob{x0, h0, G0, di0, dj0, tr0, 0};
-  a.job[1] = SumJob{x1, h1, G1, di1, dj1, tr1, 0};
+  memset(&a, 0, sizeof(a));
+  if (G0) a.job[0] = SumJob{x0, h0, G0, partial, di0, dj0, tr0, 0, 0};
+  if (G1) a.job[1] = SumJob{x1, h1, G1, partial, di1, dj1, tr1, 0, 0};
+  const int dj = std::max(G0 ? dj0 : 0, G1 ? dj1 : 0);
+  const int blocks = (G0 ? sum_blocks(di0, dj0, dj, dtype_f16) : 0) + (G1 ? sum_blocks(di1, dj1, dj, dtype_f16) : 0);
+  a.seg = sum_segment(S_max, N, blocks);
+  if (G0 && G1) a.job[1].partial = partial + 2 * (size_t)((S_max + a.seg - 1) / a.seg) * di0 * dj0;
   a.scale = scale;
   a.perm = perm;
   a.offsets = offsets;
   a.mask = mask;
   a.T = T;
   a.S_max = S_max;
-  const int rows = offsets ? S_max / N : S_max;
-  const int dj = std::max(G0 ? dj0 : 0, G1 ? dj1 : 0);
-  if (dj <= 16) return launch_sum_rank<16>(a, dtype_f16, N, rows, sms, s);
-  if (dj <= 32) return launch_sum_rank<32>(a, dtype_f16, N, rows, sms, s);
-  if (dj <= 64) return launch_sum_rank<64>(a, dtype_f16, N, rows, sms, s);
-  return launch_sum_rank<128>(a, dtype_f16, N, rows, sms, s);
+  a.N = N;
+  if (dj <= 16) return launch_sum_rank<16>(a, dtype_f16, sms, pdl, s);
+  if (dj <= 32) return launch_sum_rank<32>(a, dtype_f16, sms, pdl, s);
+  if (dj <= 64) return launch_sum_rank<64>(a, dtype_f16, sms, pdl, s);
+  return launch_sum_rank<128>(a, dtype_f16, sms, pdl, s);
 }
 
 cudaError_t launch_gate_dx(const float* dlogits, const float* Wg, const void* in, int dtype_f16, int T,

@@ -194,11 +194,14 @@ cudaError_t launch_dlogits(const float* logits, const int32_t* topk_idx, const f
                            cudaStream_t s);
 // Sums over token rows for up to two jobs G[n][i][j] = scale_n sum_s x[row(s)][i] h[s][j]
 // (transposed: G[n][j][i]); G0 or G1 may be null (grad.cu).
+constexpr int kSumSegments = 32;
 cudaError_t launch_row_sums(const void* x0, const float* h0, float* G0, int di0, int dj0, int tr0,
                             const void* x1, const float* h1, float* G1, int di1, int dj1, int tr1,
                             const float* scale, const int32_t* perm, const int32_t* offsets,
-                            const uint8_t* mask, int dtype_f16, int T, int S_max, int N,
-                            cudaStream_t s);
+                            const uint8_t* mask, float* partial, int dtype_f16, int T, int S_max,
+                            int N, bool pdl, cudaStream_t s);
+// Bytes of `partial` for either job alone or both.
+size_t row_sums_bytes(int di0, int dj0, int di1, int dj1, bool f16, int S_max, int N);
 cudaError_t launch_gate_dx(const float* dlogits, const float* Wg, const void* in, int dtype_f16, int T,
                            int d, int E, void* out, cudaStream_t s);
 cudaError_t launch_combine_backward(const void* dout, const void* expert_out, const int32_t* slot_of,

@@ -12,6 +12,7 @@ namespace {
 constexpr size_t kAlign = 256;
 constexpr int kMaxE = 1024;
 constexpr int kMaxRank = 128;
+constexpr int kMaxRows = 1 << 30;               // rows and columns (index arithmetic in 32 bits)
 
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -29,7 +30,7 @@ int lane_elems(moe_dtype t) { return t == MOE_F16 ? 8 : 4; }     // elements of 
 
 moe_status check_router(int T, int E, int k) {
   if (T < 0 || E < 1 || (k != 1 && k != 2) || k > E) return MOE_ERR_INVALID_ARG;
-  if (E > kMaxE || (long long)T * E > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
+  if (E > kMaxE || (long long)T * E > 0x7fffffffLL || T > kMaxRows) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -38,16 +39,21 @@ moe_status check_adapter(int T, int d_in, int d_out, int r, int N, int S_max, mo
   if (!dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
   const int v = lane_elems(dtype);
   if (N > kMaxE || r > kMaxRank || r % 8 || d_in % v || d_out % v) return MOE_ERR_UNSUPPORTED;
+  if (T > kMaxRows || S_max > kMaxRows || d_in > kMaxRows || d_out > kMaxRows) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
-// [status][dh][partial h]
+// [status][dh][partial h][partial sums of dA and dB]
 size_t hidden_bytes(int r, int S_max) { return align_up((size_t)S_max * r * sizeof(float)); }
-size_t adapter_bytes(int d_in, int d_out, int r, int N, int S_max, moe_dtype dtype) {
+size_t adapter_sums_at(int d_in, int d_out, int r, int N, int S_max, moe_dtype dtype) {
   size_t b = kAlign + hidden_bytes(r, S_max);
   if (adapter_tall(S_max, N, dtype == MOE_F16))
     b += std::max(adapter_parts(S_max, d_in), adapter_parts(S_max, d_out)) * hidden_bytes(r, S_max);
   return b;
+}
+size_t adapter_bytes(int d_in, int d_out, int r, int N, int S_max, moe_dtype dtype) {
+  return adapter_sums_at(d_in, d_out, r, N, S_max, dtype) +
+         align_up(row_sums_bytes(d_in, r, d_out, r, dtype == MOE_F16, S_max, N));
 }
 
 }  // namespace
@@ -82,8 +88,8 @@ moe_status moe_gate_backward_workspace_size(int T, int d, int E, moe_dtype dtype
   if (!bytes || d < 1 || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
   moe_status st = check_router(T, E, 1);
   if (st != MOE_OK) return st;
-  if (d % lane_elems(dtype)) return MOE_ERR_UNSUPPORTED;
-  *bytes = kAlign;
+  if (d % lane_elems(dtype) || d > kMaxRows) return MOE_ERR_UNSUPPORTED;
+  *bytes = kAlign + align_up(row_sums_bytes(d, E, 0, 0, dtype == MOE_F16, T, 1));
   return MOE_OK;
 }
 
@@ -97,7 +103,7 @@ moe_status moe_gate_topk_backward(const float* logits, const int32_t* topk_idx, 
   if (st != MOE_OK) return st;
   const bool deep = dWg || dtokens;
   if (deep && (d < 1 || !dtype_ok(dtype))) return MOE_ERR_INVALID_ARG;
-  if (deep && d % lane_elems(dtype)) return MOE_ERR_UNSUPPORTED;
+  if (deep && (d % lane_elems(dtype) || d > kMaxRows)) return MOE_ERR_UNSUPPORTED;
   cudaStream_t s = as_stream(stream);
   if (T == 0) {
     if (dWg) MOE_TRY(cudaMemsetAsync(dWg, 0, (size_t)d * E * sizeof(float), s));
@@ -122,7 +128,9 @@ moe_status moe_gate_topk_backward(const float* logits, const int32_t* topk_idx, 
   const int f16 = dtype == MOE_F16;
   if (dWg)
     MOE_TRY(launch_row_sums(tokens, dlogits, dWg, d, E, 0, nullptr, nullptr, nullptr, 0, 0, 0, nullptr,
-                            nullptr, nullptr, token_mask, f16, T, T, 1, s));
+                            nullptr, nullptr, token_mask,
+                            reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAlign), f16, T,
+                            T, 1, /*pdl=*/true, s));
   if (dtokens) MOE_TRY(launch_gate_dx(dlogits, Wg, dtokens_in, f16, T, d, E, dtokens, s));
   return MOE_OK;
 }
@@ -208,8 +216,10 @@ moe_status moe_adapter_backward(const void* dout, const void* tokens, const floa
                          offsets, reinterpret_cast<int*>(ws), f16, /*transposed=*/true, T,
                          dA || dtokens ? d_out : 0, dtokens ? d_in : 0, r, N, S_max, s));
   if (dA || dB)
-    MOE_TRY(launch_row_sums(tokens, dh, dA, d_in, r, 0, dout, hidden, dB, d_out, r, 1, scale, perm,
-                            offsets, nullptr, f16, T, S_max, N, s));
+    MOE_TRY(launch_row_sums(
+        tokens, dh, dA, d_in, r, 0, dout, hidden, dB, d_out, r, 1, scale, perm, offsets, nullptr,
+        reinterpret_cast<float*>(ws + adapter_sums_at(d_in, d_out, r, N, S_max, dtype)), f16, T, S_max,
+        N, /*pdl=*/true, s));
   return MOE_OK;
 }
 
