@@ -20,15 +20,19 @@ namespace {
 // leave partial sums that a second launch adds in order (no atomics: equal calls give equal bits;
 // skewed groups are spread evenly, which a fixed number of blocks per group was not).
 //
-// f16: h is a 32-bit input of any range and the rows are the summed index, so per chunk it is
-// scaled by one power of two (from the chunk's largest magnitude) and split into two f16 parts,
-// 22 bits together; the chunk's product is scaled back as it is added to the 32-bit running sums
-// (which also ends the tensor cores' chains of truncating additions every 64 rows).
+// f16: h is a 32-bit input of any range and the rows are the summed index, so per chunk of 64 rows
+// it is scaled by one power of two (from the chunk's largest magnitude) and split into two f16
+// parts, 22 bits together; the chunk's product is scaled back as it is added to the 32-bit running
+// sums (which also ends the tensor cores' chains of truncating additions every 64 rows).  A launch
+// of its own splits h, small beside x: with the split inside the loop, waiting for h and two
+// barriers per chunk took most of the time (8192 rows, 2048 + 8192 columns, r = 32: 115 us).
 struct SumJob {
   const void* x;         // [rows, di]
   const float* h;        // [rows or slots, dj]
   float* G;              // [N, di, dj], or [N, dj, di] when transposed
   float* partial;        // [slots][di dj], laid out as G
+  __half* split;         // f16: [S_max][2 ldh]: high parts, low parts (ldh: dj padded)
+  float* mul;            // f16: [S_max]: the power of two of the row's chunk
   int di, dj, transposed;
   int bi, blocks;        // column blocks of di; blocks of a segment in all (bi x those of dj)
 };
@@ -45,7 +49,6 @@ constexpr int kSumThreads = 256;
 constexpr int kIT = 128;             // columns i per block (f16)
 constexpr int kRows = 64;            // rows per chunk (f16)
 constexpr int kLdX = kIT + 8;
-constexpr int kSumStages = 4;
 
 // Row of slot s, -1 where it is to be left out.
 __device__ __forceinline__ int row_of(const SumArgs& a, int s, int hi) {
@@ -130,59 +133,120 @@ struct SumWarps {
   static constexpr int MI = kIT / WI / 16, NJ = R / WJ / 8;        // 16-row and 8-column fragments
 };
 
-template <int R>
-__global__ void __launch_bounds__(kSumThreads, R >= 128 ? 1 : 2) row_sum_f16_kernel(const SumArgs a) {
-  constexpr int kLdH = R + 8;
-  constexpr int kHB = kRows * kLdH;                // halves of one f16 part
-  constexpr int NV = kRows * R / kSumThreads;      // h values per thread and chunk
-  constexpr int MI = SumWarps<R>::MI, NJ = SumWarps<R>::NJ, WI = SumWarps<R>::WI;
-  extern __shared__ __align__(128) uint8_t sm[];
-  __half* xs = reinterpret_cast<__half*>(sm);                         // [stages][64][kLdX]
-  __half* hs = xs + kSumStages * kRows * kLdX;                        // [2][hi, lo][64][kLdH]
-  float* wmax = reinterpret_cast<float*>(hs + 4 * kHB);               // [2][warps]
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+// Splits h into f16 parts per chunk of 64 rows of a group; rows that are left out become zero.
+// A block takes chunks; columns beyond dj are zero up to ldh.
+__global__ void __launch_bounds__(kSumThreads) split_rows_kernel(const SumArgs a, int ldh) {
+  const SumJob& jb = a.job[blockIdx.y];
+  extern __shared__ int table[];
+  __shared__ float wmax[kSumThreads / 32];
   pdl_trigger();
   pdl_wait();                                      // h may come from the launch before
-  const Segments g = segment_table(a, reinterpret_cast<int*>(wmax + 2 * kSumThreads / 32));
+  if (!jb.G) return;
+  SumArgs b = a;
+  b.seg = kRows;                                   // the table's tiles are the chunks
+  const Segments g = segment_table(b, table);
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int dj = jb.dj, n4 = ldh / 4;              // four columns at a time
+  for (int c = blockIdx.x; c < g.count; c += gridDim.x) {
+    const int n = a.offsets ? group_of(c, g.start, a.N) : 0;
+    const int lo = g.bound[n] + (c - g.start[n]) * kRows, hi = min(lo + kRows, g.bound[n + 1]);
+    auto load = [&](int q) {
+      const int s = lo + q / n4, col = (q % n4) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row_of(a, s, hi) < 0 || col >= dj) return v;
+      const float* src = jb.h + (size_t)s * dj + col;
+      if (dj % 4 == 0) return *reinterpret_cast<const float4*>(src);
+      v.x = src[0];
+      if (col + 1 < dj) v.y = src[1];
+      if (col + 2 < dj) v.z = src[2];
+      if (col + 3 < dj) v.w = src[3];
+      return v;
+    };
+    float m = 0.f;
+    for (int q = tid; q < kRows * n4; q += kSumThreads) {
+      const float4 v = load(q);
+      const float big = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+      // NaN is not seen by fmaxf: v - v is 0 unless a value is infinite or NaN
+      m = (v.x - v.x) + (v.y - v.y) + (v.z - v.z) + (v.w - v.w) == 0.f ? fmaxf(m, big) : INFINITY;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    __syncthreads();
+    if (lane == 0) wmax[w] = m;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kSumThreads / 32; ++q) m = fmaxf(m, wmax[q]);
+    const int e = scale_exp(m);
+    const float inv = exp2_int(-e);
+    for (int q = tid; q < kRows * n4; q += kSumThreads) {
+      const int s = lo + q / n4, col = (q % n4) * 4;
+      if (s >= hi) break;
+      const float4 v = load(q);
+      __half2 h[2], l[2];
+      split_f16(v.x * inv, h[0].x, l[0].x);
+      split_f16(v.y * inv, h[0].y, l[0].y);
+      split_f16(v.z * inv, h[1].x, l[1].x);
+      split_f16(v.w * inv, h[1].y, l[1].y);
+      __half* dst = jb.split + (size_t)s * 2 * ldh + col;
+      *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(h);
+      *reinterpret_cast<uint2*>(dst + ldh) = *reinterpret_cast<const uint2*>(l);
+    }
+    if (tid < hi - lo) jb.mul[lo + tid] = exp2_int(e);
+  }
+}
+
+// Shared memory: a ring of chunks, x [64][kLdX] and the R columns of both parts of h [64][2 R + 8].
+template <int R>
+struct SumPlan {
+  static constexpr int kLdH = 2 * R + 8;
+  static constexpr int kStage = kRows * (kLdX + kLdH);             // halves
+  static constexpr int kStages = R == 64 ? 3 : 4;                  // two blocks per SM (R = 128: one)
+};
+
+template <int R>
+__global__ void __launch_bounds__(kSumThreads, R >= 128 ? 1 : 2) row_sum_f16_kernel(const SumArgs a, int ldh) {
+  constexpr int kLdH = SumPlan<R>::kLdH, NS = SumPlan<R>::kStages, kStage = SumPlan<R>::kStage;
+  constexpr int MI = SumWarps<R>::MI, NJ = SumWarps<R>::NJ, WI = SumWarps<R>::WI;
+  constexpr int HP = kRows * R * 4 / 16 / kSumThreads;             // 16-byte pieces of h per thread
+  extern __shared__ __align__(128) uint8_t sm[];
+  __half* ring = reinterpret_cast<__half*>(sm);
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  pdl_trigger();
+  pdl_wait();                                      // the split h
+  const Segments g = segment_table(a, reinterpret_cast<int*>(ring + NS * kStage));
   const int items = g.count * (a.job[0].blocks + a.job[1].blocks);
   const int wi = (w % WI) * MI * 16, wj = (w / WI) * NJ * 8;
   const int xc = (tid & 15) * 8, xr = tid >> 4;    // x: 16-byte piece, rows xr + 16 p
-  const int hr = tid * NV / R, hc = tid * NV % R;  // h: NV consecutive values of one row
 
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
     const SumItem it = sum_item<kIT, R>(a, g, item);
-    const int di = it.jb->di, dj = it.jb->dj;
+    const int di = it.jb->di;
     const __half* X = static_cast<const __half*>(it.jb->x) + it.i0 + xc;
     const bool xin = it.i0 + xc < di;
     const int chunks = (it.hi - it.lo + kRows - 1) / kRows;
+    const __half* H = it.jb->split + it.j0;
     int rows_next[4];
     auto fetch_rows = [&](int c) {
 #pragma unroll
       for (int p = 0; p < 4; ++p) rows_next[p] = row_of(a, it.lo + c * kRows + xr + 16 * p, it.hi);
     };
-    auto load_x = [&](int c) {                     // rows_next holds chunk c's rows
-      __half* dst = xs + (c % kSumStages) * kRows * kLdX + xr * kLdX + xc;
+    auto load = [&](int c) {                       // rows_next holds chunk c's rows
+      __half* st = ring + (c % NS) * kStage;
+      __half* dst = st + xr * kLdX + xc;
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         const bool on = xin && rows_next[p] >= 0;
         cp_async16(dst + 16 * p * kLdX, on ? X + (size_t)rows_next[p] * di : X, on);
       }
-    };
-    float hv[NV];
-    auto load_h = [&](int c) {
-      const int s = it.lo + c * kRows + hr;
-      const bool on = row_of(a, s, it.hi) >= 0;
-      const float* src = it.jb->h + (size_t)(on ? s : 0) * dj + it.j0 + hc;
-      if (dj % 4 == 0) {
+      __half* hst = st + kRows * kLdX;
 #pragma unroll
-        for (int q = 0; q < NV; q += 4) {
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (on && it.j0 + hc + q < dj) v = *reinterpret_cast<const float4*>(src + q);
-          hv[q] = v.x; hv[q + 1] = v.y; hv[q + 2] = v.z; hv[q + 3] = v.w;
-        }
-      } else {
-#pragma unroll
-        for (int q = 0; q < NV; ++q) hv[q] = on && it.j0 + hc + q < dj ? src[q] : 0.f;
+      for (int p = 0; p < HP; ++p) {
+        const int q = tid + p * kSumThreads;       // row, part, piece of R columns
+        const int row = q / (R / 4), part = q / (R / 8) % 2, col = (q % (R / 8)) * 8;
+        const int s = it.lo + c * kRows + row;
+        const bool on = s < it.hi && it.j0 + col < ldh;
+        cp_async16(hst + row * kLdH + part * R + col,
+                   on ? H + ((size_t)s * 2 + part) * ldh + col : H, on);
       }
     };
     float acc[MI][NJ][4];
@@ -193,56 +257,23 @@ __global__ void __launch_bounds__(kSumThreads, R >= 128 ? 1 : 2) row_sum_f16_ker
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[i][j][q] = 0.f;
 
-    for (int p = 0; p < kSumStages - 1; ++p) {
+    for (int p = 0; p < NS - 1; ++p) {
       if (p < chunks) {
         fetch_rows(p);
-        load_x(p);
+        load(p);
       }
       cp_async_commit();
     }
-    if (kSumStages - 1 < chunks) fetch_rows(kSumStages - 1);
-    load_h(0);
+    if (NS - 1 < chunks) fetch_rows(NS - 1);
     for (int c = 0; c < chunks; ++c) {
-      const int b = c & 1;
-      // this chunk's power of two
-      float m = 0.f;
-      bool odd = false;
-#pragma unroll
-      for (int q = 0; q < NV; ++q) {
-        m = fmaxf(m, fabsf(hv[q]));
-        odd |= !(fabsf(hv[q]) < INFINITY);
-      }
-      if (odd) m = INFINITY;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (lane == 0) wmax[b * (kSumThreads / 32) + w] = m;
-      cp_async_wait<kSumStages - 2>();
-      __syncthreads();                             // chunk c of x is in; every wmax is written
-#pragma unroll
-      for (int q = 0; q < kSumThreads / 32; ++q) m = fmaxf(m, wmax[b * (kSumThreads / 32) + q]);
-      const int e = scale_exp(m);
-      const float inv = exp2_int(-e), mul = exp2_int(e);
-      __half* hhi = hs + b * 2 * kHB;
-      __half* hlo = hhi + kHB;
-      if (m < INFINITY) {
-#pragma unroll
-        for (int q = 0; q < NV; q += 2) {
-          const float u = hv[q] * inv, v = hv[q + 1] * inv;
-          const __half2 hi = __floats2half2_rn(u, v);
-          const float2 f = __half22float2(hi);
-          *reinterpret_cast<__half2*>(hhi + hr * kLdH + hc + q) = hi;
-          *reinterpret_cast<__half2*>(hlo + hr * kLdH + hc + q) = __floats2half2_rn(u - f.x, v - f.y);
-        }
-      } else {                                     // infinities or NaN: a part each, unscaled
-#pragma unroll
-        for (int q = 0; q < NV; ++q) split_f16(hv[q], hhi[hr * kLdH + hc + q], hlo[hr * kLdH + hc + q]);
-      }
-      if (c + 1 < chunks) load_h(c + 1);
-      if (c + kSumStages - 1 < chunks) load_x(c + kSumStages - 1);
-      cp_async_commit();
-      if (c + kSumStages < chunks) fetch_rows(c + kSumStages);
+      const float mul = it.jb->mul[it.lo + c * kRows];
+      cp_async_wait<NS - 2>();
       __syncthreads();
-      const __half* xb = xs + (c % kSumStages) * kRows * kLdX;
+      if (c + NS - 1 < chunks) load(c + NS - 1);
+      cp_async_commit();
+      if (c + NS < chunks) fetch_rows(c + NS);
+      const __half* xb = ring + (c % NS) * kStage;
+      const __half* hb = xb + kRows * kLdX;
       float t[MI][NJ][4];
 #pragma unroll
       for (int i = 0; i < MI; ++i)
@@ -256,27 +287,16 @@ __global__ void __launch_bounds__(kSumThreads, R >= 128 ? 1 : 2) row_sum_f16_ker
 #pragma unroll
         for (int i = 0; i < MI; ++i) frag_a_t(fa[i], xb + k * kLdX + wi + i * 16, kLdX, lane);
 #pragma unroll
-        for (int j = 0; j < NJ / 2 + NJ % 2; ++j) {
+        for (int j = 0; j < NJ / 2; ++j) {
           uint32_t fh[4], fl[4];
-          if (NJ == 1) {                           // eight columns: half of a 16-column load
-            frag_b_kn(fl, hlo + k * kLdH + (wj & ~15), kLdH, lane);
-            frag_b_kn(fh, hhi + k * kLdH + (wj & ~15), kLdH, lane);
-            const int o = (wj & 8) >> 2;
+          frag_b_kn(fl, hb + k * kLdH + R + wj + j * 16, kLdH, lane);
+          frag_b_kn(fh, hb + k * kLdH + wj + j * 16, kLdH, lane);
 #pragma unroll
-            for (int i = 0; i < MI; ++i) {
-              mma16816(t[i][0], fa[i], o ? fl[2] : fl[0], o ? fl[3] : fl[1]);
-              mma16816(t[i][0], fa[i], o ? fh[2] : fh[0], o ? fh[3] : fh[1]);
-            }
-          } else {
-            frag_b_kn(fl, hlo + k * kLdH + wj + j * 16, kLdH, lane);
-            frag_b_kn(fh, hhi + k * kLdH + wj + j * 16, kLdH, lane);
-#pragma unroll
-            for (int i = 0; i < MI; ++i) {
-              mma16816(t[i][2 * j], fa[i], fl[0], fl[1]);
-              mma16816(t[i][2 * j + 1], fa[i], fl[2], fl[3]);
-              mma16816(t[i][2 * j], fa[i], fh[0], fh[1]);
-              mma16816(t[i][2 * j + 1], fa[i], fh[2], fh[3]);
-            }
+          for (int i = 0; i < MI; ++i) {
+            mma16816(t[i][2 * j], fa[i], fl[0], fl[1]);
+            mma16816(t[i][2 * j + 1], fa[i], fl[2], fl[3]);
+            mma16816(t[i][2 * j], fa[i], fh[0], fh[1]);
+            mma16816(t[i][2 * j + 1], fa[i], fh[2], fh[3]);
           }
         }
       }
@@ -415,33 +435,40 @@ int sum_segment(int S_max, int N, int blocks) {
   return best;
 }
 
-template <typename Kern>
-cudaError_t launch_sum(Kern kern, size_t smem, SumArgs& a, int it, int R, int sms, bool pdl, cudaStream_t s) {
-  MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
-  int blocks = 0;
+// Columns of h's parts: dj in whole fragments (16 columns) of the row sums.
+int split_width(int dj) { return (dj + 15) / 16 * 16; }
+
+template <int R>
+cudaError_t launch_sum_rank(SumArgs& a, bool f16, int sms, bool pdl, cudaStream_t s) {
+  const int it = f16 ? kIT : kIT32;
+  int blocks = 0, ldh = 0;
   size_t widest = 0;
   for (SumJob& j : a.job) {
     j.bi = (j.di + it - 1) / it;
     j.blocks = j.G ? j.bi * ((j.dj + R - 1) / R) : 0;
     blocks += j.blocks;
     if (j.G) widest = std::max(widest, (size_t)j.di * j.dj);
+    if (j.G) ldh = std::max(ldh, split_width(j.dj));
   }
-  const long long most = ((long long)a.S_max / a.seg + std::min(a.N, a.S_max)) * blocks;
-  const int grid = (int)std::min<long long>(most, 2 * sms);
-  smem += sizeof(int) * (2 * ((size_t)a.N + 1) + 32);
-  MOE_LAUNCH(launch_k(kern, grid, kSumThreads, smem, s, pdl, a));
+  const long long segs = (long long)a.S_max / a.seg + std::min(a.N, a.S_max);
+  const size_t table = sizeof(int) * (2 * ((size_t)a.N + 1) + 32);
+  const int grid = (int)std::min<long long>(segs * blocks, (f16 && R >= 128 ? 1 : 2) * sms);
+  if (f16) {
+    const long long chunks = (long long)a.S_max / kRows + std::min(a.N, a.S_max);
+    MOE_LAUNCH(launch_k(split_rows_kernel, dim3((int)std::min<long long>(chunks, 4 * sms), 2), kSumThreads,
+                        table, s, pdl, a, ldh));
+    auto kern = row_sum_f16_kernel<R>;
+    MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
+    const size_t smem = 2 * (size_t)SumPlan<R>::kStages * SumPlan<R>::kStage + table;
+    MOE_LAUNCH(launch_k(kern, grid, kSumThreads, smem, s, true, a, ldh));
+  } else {
+    auto kern = row_sum_f32_kernel<R>;
+    MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
+    const size_t smem = sizeof(float) * (kRows32 * kIT32 + kRows32 * R) + table;
+    MOE_LAUNCH(launch_k(kern, grid, kSumThreads, smem, s, pdl, a));
+  }
   const int bx = (int)std::min<size_t>((widest / 4 + 255) / 256, std::max<size_t>(1, 8 * sms / a.N));
   return launch_k(row_sum_join_kernel, dim3(std::max(1, bx), a.N, 2), 256, 0, s, true, a);
-}
-
-template <int R>
-cudaError_t launch_sum_rank(SumArgs& a, bool f16, int sms, bool pdl, cudaStream_t s) {
-  if (f16) {
-    const size_t smem = 2 * (size_t)(kSumStages * kRows * kLdX + 4 * kRows * (R + 8)) + 64;
-    return launch_sum(row_sum_f16_kernel<R>, smem, a, kIT, R, sms, pdl, s);
-  }
-  const size_t smem = sizeof(float) * (kRows32 * kIT32 + kRows32 * R);
-  return launch_sum(row_sum_f32_kernel<R>, smem, a, kIT32, R, sms, pdl, s);
 }
 
 // Column blocks of a job of either type, as launch_sum_rank cuts them.
@@ -586,36 +613,57 @@ cudaError_t launch_combine_backward_t(const void* dout, const void* y, const int
 
 }  // namespace
 
+namespace {
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+// f16: bytes of the split parts and their scales of one job
+size_t split_bytes(int dj, int S_max) { return up256((size_t)S_max * split_width(dj) * 4) + up256((size_t)S_max * 4); }
+}  // namespace
+
 size_t row_sums_bytes(int di0, int dj0, int di1, int dj1, bool f16, int S_max, int N) {
-  const int dj = std::max(dj0, dj1);
   size_t most = 0;
   // either job alone may be asked for: the plan of each combination fits
   for (int q = 1; q < 4; ++q) {
-    const int b = (q & 1 ? sum_blocks(di0, dj0, q & 2 ? dj : dj0, f16) : 0) +
-                  (q & 2 ? sum_blocks(di1, dj1, q & 1 ? dj : dj1, f16) : 0);
-    const int seg = sum_segment(S_max, N, std::max(b, 1));
+    const int dj = std::max(q & 1 ? dj0 : 0, q & 2 ? dj1 : 0);
+    const int b = (q & 1 ? sum_blocks(di0, dj0, dj, f16) : 0) + (q & 2 ? sum_blocks(di1, dj1, dj, f16) : 0);
+    if (b == 0) continue;
+    const int seg = sum_segment(S_max, N, b);
     const size_t slots = 2 * (size_t)((S_max + seg - 1) / seg);
     const size_t words = (q & 1 ? (size_t)di0 * dj0 : 0) + (q & 2 ? (size_t)di1 * dj1 : 0);
-    if (S_max > seg) most = std::max(most, slots * words * sizeof(float));
+    most = std::max(most, S_max > seg ? slots * words * sizeof(float) : 0);
   }
-  return most;
+  return up256(most) + (f16 ? split_bytes(dj0, S_max) + split_bytes(dj1, S_max) : 0);
 }
 
 cudaError_t launch_row_sums(const void* x0, const float* h0, float* G0, int di0, int dj0, int tr0,
                             const void* x1, const float* h1, float* G1, int di1, int dj1, int tr1,
                             const float* scale, const int32_t* perm, const int32_t* offsets,
-                            const uint8_t* mask, float* partial, int dtype_f16, int T, int S_max,
+                            const uint8_t* mask, void* workspace, int dtype_f16, int T, int S_max,
                             int N, bool pdl, cudaStream_t s) {
   const int sms = sms_of_device();
   if (sms < 1) return cudaErrorInvalidDevice;
   SumArgs a;
   memset(&a, 0, sizeof(a));
-  if (G0) a.job[0] = SumJob{x0, h0, G0, partial, di0, dj0, tr0, 0, 0};
-  if (G1) a.job[1] = SumJob{x1, h1, G1, partial, di1, dj1, tr1, 0, 0};
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  auto job = [&](SumJob& j, const void* x, const float* h, float* G, int di, int dj, int tr) {
+    j.x = x;
+    j.h = h;
+    j.G = G;
+    j.di = di;
+    j.dj = dj;
+    j.transposed = tr;
+    if (dtype_f16) {
+      j.split = reinterpret_cast<__half*>(ws);
+      j.mul = reinterpret_cast<float*>(ws + up256((size_t)S_max * split_width(dj) * 4));
+      ws += split_bytes(dj, S_max);
+    }
+  };
+  if (G0) job(a.job[0], x0, h0, G0, di0, dj0, tr0);
+  if (G1) job(a.job[1], x1, h1, G1, di1, dj1, tr1);
   const int dj = std::max(G0 ? dj0 : 0, G1 ? dj1 : 0);
   const int blocks = (G0 ? sum_blocks(di0, dj0, dj, dtype_f16) : 0) + (G1 ? sum_blocks(di1, dj1, dj, dtype_f16) : 0);
   a.seg = sum_segment(S_max, N, blocks);
-  if (G0 && G1) a.job[1].partial = partial + 2 * (size_t)((S_max + a.seg - 1) / a.seg) * di0 * dj0;
+  a.job[0].partial = a.job[1].partial = reinterpret_cast<float*>(ws);
+  if (G0) a.job[1].partial += 2 * (size_t)((S_max + a.seg - 1) / a.seg) * di0 * dj0;
   a.scale = scale;
   a.perm = perm;
   a.offsets = offsets;

@@ -198,9 +198,9 @@ constexpr int kSumSegments = 32;
 cudaError_t launch_row_sums(const void* x0, const float* h0, float* G0, int di0, int dj0, int tr0,
                             const void* x1, const float* h1, float* G1, int di1, int dj1, int tr1,
                             const float* scale, const int32_t* perm, const int32_t* offsets,
-                            const uint8_t* mask, float* partial, int dtype_f16, int T, int S_max,
+                            const uint8_t* mask, void* workspace, int dtype_f16, int T, int S_max,
                             int N, bool pdl, cudaStream_t s);
-// Bytes of `partial` for either job alone or both.
+// Bytes of its workspace, for either job alone or both (dj1 = 0: there is no second).
 size_t row_sums_bytes(int di0, int dj0, int di1, int dj1, bool f16, int S_max, int N);
 cudaError_t launch_gate_dx(const float* dlogits, const float* Wg, const void* in, int dtype_f16, int T,
                            int d, int E, void* out, cudaStream_t s);

@@ -43,7 +43,7 @@ moe_status check_adapter(int T, int d_in, int d_out, int r, int N, int S_max, mo
   return MOE_OK;
 }
 
-// [status][dh][partial h][partial sums of dA and dB]
+// [status][dh][partial h][workspace of the sums dA and dB]
 size_t hidden_bytes(int r, int S_max) { return align_up((size_t)S_max * r * sizeof(float)); }
 size_t adapter_sums_at(int d_in, int d_out, int r, int N, int S_max, moe_dtype dtype) {
   size_t b = kAlign + hidden_bytes(r, S_max);
@@ -128,9 +128,8 @@ moe_status moe_gate_topk_backward(const float* logits, const int32_t* topk_idx, 
   const int f16 = dtype == MOE_F16;
   if (dWg)
     MOE_TRY(launch_row_sums(tokens, dlogits, dWg, d, E, 0, nullptr, nullptr, nullptr, 0, 0, 0, nullptr,
-                            nullptr, nullptr, token_mask,
-                            reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAlign), f16, T,
-                            T, 1, /*pdl=*/true, s));
+                            nullptr, nullptr, token_mask, static_cast<uint8_t*>(workspace) + kAlign,
+                            f16, T, T, 1, /*pdl=*/true, s));
   if (dtokens) MOE_TRY(launch_gate_dx(dlogits, Wg, dtokens_in, f16, T, d, E, dtokens, s));
   return MOE_OK;
 }
@@ -218,8 +217,7 @@ moe_status moe_adapter_backward(const void* dout, const void* tokens, const floa
   if (dA || dB)
     MOE_TRY(launch_row_sums(
         tokens, dh, dA, d_in, r, 0, dout, hidden, dB, d_out, r, 1, scale, perm, offsets, nullptr,
-        reinterpret_cast<float*>(ws + adapter_sums_at(d_in, d_out, r, N, S_max, dtype)), f16, T, S_max,
-        N, /*pdl=*/true, s));
+        ws + adapter_sums_at(d_in, d_out, r, N, S_max, dtype), f16, T, S_max, N, /*pdl=*/true, s));
   return MOE_OK;
 }
 
