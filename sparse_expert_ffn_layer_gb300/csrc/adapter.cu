@@ -156,8 +156,7 @@ struct TallRing {
     const int s0 = bound[n] + (tile - start[n]) * MT + (threadIdx.x >> 3);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const int t = s0 + 32 * q < bound[n + 1] ? perm[s0 + 32 * q] : -1;
-      lnext[q] = (unsigned)t < (unsigned)T ? t : -1;
+      lnext[q] = s0 + 32 * q < bound[n + 1] ? perm[s0 + 32 * q] : -1;   // looked at when used
     }
   }
   __device__ __forceinline__ void begin_item() {
@@ -194,7 +193,7 @@ struct TallRing {
       const bool in = col + pc * 8 < d;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const bool on = in && lrow[q] >= 0;
+        const bool on = in && (unsigned)lrow[q] < (unsigned)T;
         cp_async16(st + (row + 32 * q) * 128 + ((pc ^ (row & 7)) << 4),
                    rows + (on ? (size_t)lrow[q] * d + col + pc * 8 : 0), on);
       }
@@ -573,14 +572,13 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
   const __half* base = static_cast<const __half*>(a.base);
   __half* Y = static_cast<__half*>(a.y);
 
-  // Token of row `row` of a tile, -1 where there is none.
+  // Perm entry of row `row` of a tile, -1 where there is none.
   auto token = [&](int tile, int row) {
     if (tile >= ntiles) return -1;
     const int n = group_of(tile, start, a.N);
     const int s = bound[n] + (tile - start[n]) * MT + row;
     if (s >= bound[n + 1]) return -1;
-    const int t = a.perm[s];
-    return (unsigned)t < (unsigned)a.T ? t : -1;
+    return a.perm[s];                             // looked at when used: no wait for the load here
   };
 
   // ---- loader: runs NS - 1 chunks ahead, across tiles.  Its rows' tokens are fetched a tile early.
@@ -610,7 +608,7 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
         const bool in = col0 + lpc < d;
 #pragma unroll
         for (int p = 0; p < XP; ++p) {
-          const bool on = in && ltok[p] >= 0;
+          const bool on = in && (unsigned)ltok[p] < (unsigned)a.T;
           cp_async16(st + (lrow + p * (NT / 8)) * kRowB + lpc * 2,
                      rowsrc + (on ? (size_t)ltok[p] * d + col0 + lpc : 0), on);
         }
@@ -836,7 +834,7 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
       if (col < a.dn) {
 #pragma unroll
         for (int p = 0; p < RPT; ++p)
-          if (ytok[p] >= 0)
+          if ((unsigned)ytok[p] < (unsigned)a.T)
             *reinterpret_cast<uint4*>(Y + (size_t)ytok[p] * a.dn + col) =
                 *reinterpret_cast<const uint4*>(bs + (yrow + p * (32 / LPR)) * kLdC + ycol);
       }

@@ -121,6 +121,27 @@ __device__ __forceinline__ SumItem sum_item(const SumArgs& a, const Segments& g,
   }
   return it;
 }
+// Writes v[i][j] of the fragments' layout: rows i, i + 8 of each 16, columns j, j + 1 of each 8.
+template <int MI, int NJ>
+__device__ __forceinline__ void store_sums(const SumItem& it, int i, int j, float (&v)[MI][NJ][4]) {
+  const int di = it.jb->di, dj = it.jb->dj;
+  const bool tr = it.jb->transposed;
+  const int64_t si = tr ? 1 : dj, sj = tr ? di : 1;
+  float* p = it.dst + i * si + j * sj;
+#pragma unroll
+  for (int a = 0; a < MI; ++a)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (i + 16 * a + 8 * q >= di) continue;
+      float* r = p + (16 * a + 8 * q) * si;
+#pragma unroll
+      for (int b = 0; b < NJ; ++b) {
+        const float x = it.scale * v[a][b][2 * q], y = it.scale * v[a][b][2 * q + 1];
+        if (j + 8 * b < dj) r[8 * b * sj] = x;
+        if (j + 8 * b + 1 < dj) r[(8 * b + 1) * sj] = y;
+      }
+    }
+}
 __device__ __forceinline__ void store_sum(const SumItem& it, int i, int j, float v) {
   if (i < it.jb->di && j < it.jb->dj)
     it.dst[it.jb->transposed ? (size_t)j * it.jb->di + i : (size_t)i * it.jb->dj + j] = it.scale * v;
@@ -216,39 +237,75 @@ __global__ void __launch_bounds__(kSumThreads, R >= 128 ? 1 : 2) row_sum_f16_ker
   const Segments g = segment_table(a, reinterpret_cast<int*>(ring + NS * kStage));
   const int items = g.count * (a.job[0].blocks + a.job[1].blocks);
   const int wi = (w % WI) * MI * 16, wj = (w / WI) * NJ * 8;
-  const int xc = (tid & 15) * 8, xr = tid >> 4;    // x: 16-byte piece, rows xr + 16 p
 
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const SumItem it = sum_item<kIT, R>(a, g, item);
-    const int di = it.jb->di;
-    const __half* X = static_cast<const __half*>(it.jb->x) + it.i0 + xc;
-    const bool xin = it.i0 + xc < di;
-    const int chunks = (it.hi - it.lo + kRows - 1) / kRows;
-    const __half* H = it.jb->split + it.j0;
-    int rows_next[4];
-    auto fetch_rows = [&](int c) {
+  // ---- loads: chunk after chunk across the block's items, each chunk's rows fetched one early
+  const int xc = (tid & 15) * 8, xr = tid >> 4;    // x: 16-byte piece, rows xr + 16 p
+  int li = blockIdx.x, lc = 0, llo = 0, lhi = 0, ldi = 0, lrow[4];
+  uint8_t lmask[4] = {};
+  const __half *lX = nullptr, *lH = nullptr;
+  bool lin = false;
+  int lw = 0;                                      // columns of h that there are
+  auto begin_item = [&]() {
+    if (li >= items) return;
+    const SumItem it = sum_item<kIT, R>(a, g, li);
+    lc = 0;
+    llo = it.lo;
+    lhi = it.hi;
+    ldi = it.jb->di;
+    lX = static_cast<const __half*>(it.jb->x) + it.i0 + xc;
+    lin = it.i0 + xc < ldi;
+    lH = it.jb->split + (size_t)it.lo * 2 * ldh + it.j0;
+    lw = min(R, ldh - it.j0);
+  };
+  // The rows are looked at when they are used, a chunk later: a comparison right here would wait
+  // for the load (a third of all stalls).
+  auto fetch_rows = [&]() {
+    if (li >= items) return;
 #pragma unroll
-      for (int p = 0; p < 4; ++p) rows_next[p] = row_of(a, it.lo + c * kRows + xr + 16 * p, it.hi);
-    };
-    auto load = [&](int c) {                       // rows_next holds chunk c's rows
-      __half* st = ring + (c % NS) * kStage;
+    for (int p = 0; p < 4; ++p) {
+      const int s = llo + lc * kRows + xr + 16 * p;
+      lrow[p] = s;
+      if (a.perm) lrow[p] = s < lhi ? a.perm[s] : -1;
+      if (a.mask) lmask[p] = s < lhi ? a.mask[s] : 0;
+    }
+  };
+  auto load = [&](int stage) {
+    if (li < items) {
+      const unsigned limit = a.perm ? a.T : lhi;
+      __half* st = ring + stage * kStage;
       __half* dst = st + xr * kLdX + xc;
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        const bool on = xin && rows_next[p] >= 0;
-        cp_async16(dst + 16 * p * kLdX, on ? X + (size_t)rows_next[p] * di : X, on);
+        const bool on = lin && (unsigned)lrow[p] < limit && (!a.mask || lmask[p]);
+        cp_async16(dst + 16 * p * kLdX, on ? lX + (size_t)lrow[p] * ldi : lX, on);
       }
       __half* hst = st + kRows * kLdX;
+      const int left = lhi - llo - lc * kRows;     // rows of this and later chunks
+      const __half* src = lH + (size_t)lc * kRows * 2 * ldh;
 #pragma unroll
       for (int p = 0; p < HP; ++p) {
         const int q = tid + p * kSumThreads;       // row, part, piece of R columns
         const int row = q / (R / 4), part = q / (R / 8) % 2, col = (q % (R / 8)) * 8;
-        const int s = it.lo + c * kRows + row;
-        const bool on = s < it.hi && it.j0 + col < ldh;
-        cp_async16(hst + row * kLdH + part * R + col,
-                   on ? H + ((size_t)s * 2 + part) * ldh + col : H, on);
+        const bool on = row < left && col < lw;
+        cp_async16(hst + row * kLdH + part * R + col, on ? src + (row * 2 + part) * ldh + col : lH, on);
       }
-    };
+      if (++lc * kRows >= lhi - llo) {
+        li += gridDim.x;
+        begin_item();
+      }
+      fetch_rows();
+    }
+    cp_async_commit();
+  };
+  begin_item();
+  fetch_rows();
+  int stage = 0;                                   // of the next load
+  for (; stage < NS - 1; ++stage) load(stage);
+
+  int use = 0;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const SumItem it = sum_item<kIT, R>(a, g, item);
+    const float* scales = it.jb->mul + it.lo;
     float acc[MI][NJ][4];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -256,24 +313,17 @@ __global__ void __launch_bounds__(kSumThreads, R >= 128 ? 1 : 2) row_sum_f16_ker
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[i][j][q] = 0.f;
-
-    for (int p = 0; p < NS - 1; ++p) {
-      if (p < chunks) {
-        fetch_rows(p);
-        load(p);
-      }
-      cp_async_commit();
-    }
-    if (NS - 1 < chunks) fetch_rows(NS - 1);
-    for (int c = 0; c < chunks; ++c) {
-      const float mul = it.jb->mul[it.lo + c * kRows];
+    float next = scales[0];
+    for (int row = 0; row < it.hi - it.lo; row += kRows) {
+      const float mul = next;
+      if (row + kRows < it.hi - it.lo) next = scales[row + kRows];
       cp_async_wait<NS - 2>();
       __syncthreads();
-      if (c + NS - 1 < chunks) load(c + NS - 1);
-      cp_async_commit();
-      if (c + NS < chunks) fetch_rows(c + NS);
-      const __half* xb = ring + (c % NS) * kStage;
+      load(stage);
+      stage = stage + 1 == NS ? 0 : stage + 1;
+      const __half* xb = ring + use * kStage;
       const __half* hb = xb + kRows * kLdX;
+      use = use + 1 == NS ? 0 : use + 1;
       float t[MI][NJ][4];
 #pragma unroll
       for (int i = 0; i < MI; ++i)
@@ -307,17 +357,9 @@ __global__ void __launch_bounds__(kSumThreads, R >= 128 ? 1 : 2) row_sum_f16_ker
 #pragma unroll
           for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(mul, t[i][j][q], acc[i][j][q]);
     }
-    cp_async_wait<0>();
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          store_sum(it, it.i0 + wi + 16 * i + (lane >> 2) + 8 * (q >> 1),
-                    it.j0 + wj + 8 * j + 2 * (lane & 3) + (q & 1), acc[i][j][q]);
-    __syncthreads();                               // the ring is free for the next item
+    store_sums(it, it.i0 + wi + (lane >> 2), it.j0 + wj + 2 * (lane & 3), acc);
   }
+  cp_async_wait<0>();
 }
 
 // 32-bit inputs: fused multiply-adds; 64 columns i per block, chunks of 32 rows.
@@ -426,7 +468,7 @@ int sum_segment(int S_max, int N, int blocks) {
   for (int p = 1; p <= kSumSegments; ++p) {
     const int seg = std::max(256, ((S_max + p - 1) / p + 63) / 64 * 64);
     const double items = blocks * ((double)S_max / seg + 0.5 * std::min(N, S_max));
-    const double c = ceil(items / 304) * (seg / 64 + 3) + p;
+    const double c = ceil(items / 304) * (seg / 64 + 1) + 0.5 * p;
     if (c < cost) {
       cost = c;
       best = seg;
@@ -467,7 +509,7 @@ cudaError_t launch_sum_rank(SumArgs& a, bool f16, int sms, bool pdl, cudaStream_
     const size_t smem = sizeof(float) * (kRows32 * kIT32 + kRows32 * R) + table;
     MOE_LAUNCH(launch_k(kern, grid, kSumThreads, smem, s, pdl, a));
   }
-  const int bx = (int)std::min<size_t>((widest / 4 + 255) / 256, std::max<size_t>(1, 8 * sms / a.N));
+  const int bx = (int)std::min<size_t>((widest / 4 + 255) / 256, std::max<size_t>(1, 32 * sms / a.N));
   return launch_k(row_sum_join_kernel, dim3(std::max(1, bx), a.N, 2), 256, 0, s, true, a);
 }
 
