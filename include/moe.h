@@ -217,8 +217,8 @@ MOE_API moe_status moe_layer_forward(const void* tokens, const float* Wg, const 
 
 /*
  * Synchronises `stream`, then returns the device-side status word of the most recent
- * moe_expert_ffn / moe_layer_forward / moe_adapter_forward / moe_adapter_backward call on this
- * workspace (MOE_OK, MOE_ERR_TIMEOUT or MOE_ERR_DEVICE_BOUNDS), or MOE_ERR_CUDA if the
+ * moe_expert_ffn / moe_layer_forward / moe_adapter_forward / moe_adapter_backward call, or
+ * moe_gate_topk_backward call with dWg or dtokens, on this workspace (MOE_OK, MOE_ERR_TIMEOUT or MOE_ERR_DEVICE_BOUNDS), or MOE_ERR_CUDA if the
  * synchronisation or the read failed.  Each of those calls sets the word anew.
  */
 MOE_API moe_status moe_status_read(const void* workspace, moe_stream_t stream);

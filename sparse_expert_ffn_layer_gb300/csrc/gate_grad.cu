@@ -1,0 +1,632 @@
+// The gate's gradient on the 5th-generation tensor cores, for f16 tokens:
+//   dWg [d, E] = X^T dL,    dX [T, d] = dX_in + dL Wg^T       (dL = dlogits, Wg: 32-bit)
+//
+// 32-bit operands on f16 tensor cores: a block of 128 rows of dL or Wg is scaled by one power of
+// two and split into v = hi + 2^-11 lo, both f16 (lo keeps its own exponent range, so v is good to
+// 2^-23 |v| + 2^-36 of the block's largest magnitude).  Products with hi and with lo go to separate
+// accumulators, joined as D1 + 2^-11 D2 in 32 bits; lo x lo is below 2^-22 and left out.  X is f16
+// and exact.  So dX takes three products and dWg two of 2 T d E operations each, which the tensor
+// cores do in less time than the operands' bytes take from DRAM.
+//
+// Both kernels: one block per SM; warp 0 loads by TMA, warp 1 issues the products, eight warps read
+// the accumulators.  Every wait is bounded (common.cuh).
+#include <algorithm>
+#include <cstring>
+
+#include "launch.h"
+#include "mma.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kBlk = 128;                 // rows per scale
+constexpr float kLoStep = 2048.f;         // 2^11
+constexpr int kThreads = 384;             // 4 warps (2 used) + 8 accumulator warps
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, int x, int y, const void* smem) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(m),
+      "r"(x), "r"(y), "r"(smem_u32(smem))
+      : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// ---------------------------------------------------------------- split
+// rows x E values -> [rows][2 Ep] f16 (hi, lo; columns beyond E are zero) and a scale per 128 rows.
+// Blocks [0, nT) take dL, the others Wg.
+struct SplitArgs {
+  const float *dl, *W;
+  __half *dl2, *W2;
+  float *sT, *sW;
+  int T, d, E, Ep, nT;
+};
+__global__ void __launch_bounds__(512) gate_split_kernel(const SplitArgs a) {
+  __shared__ float wmax[16];
+  pdl_trigger();
+  const bool w = (int)blockIdx.x >= a.nT;
+  if (!w) pdl_wait();                               // dL comes from the launch before
+  const int blk = (int)blockIdx.x - (w ? a.nT : 0);
+  const int rows = min(kBlk, (w ? a.d : a.T) - blk * kBlk);
+  const float* src = (w ? a.W : a.dl) + (size_t)blk * kBlk * a.E;
+  __half* dst = (w ? a.W2 : a.dl2) + (size_t)blk * kBlk * 2 * a.Ep;
+  const int n4 = a.Ep / 4, tid = threadIdx.x;
+  auto load = [&](int q) {
+    const int r = q / n4, c = (q % n4) * 4;
+    const float* p = src + (size_t)r * a.E + c;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c >= a.E) return v;
+    if (a.E % 4 == 0) return *reinterpret_cast<const float4*>(p);
+    v.x = p[0];
+    if (c + 1 < a.E) v.y = p[1];
+    if (c + 2 < a.E) v.z = p[2];
+    if (c + 3 < a.E) v.w = p[3];
+    return v;
+  };
+  float m = 0.f;
+#pragma unroll 4
+  for (int q = tid; q < rows * n4; q += 512) {
+    const float4 v = load(q);
+    const float big = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+    // NaN is not seen by fmaxf: v - v is 0 unless a value is infinite or NaN
+    m = (v.x - v.x) + (v.y - v.y) + (v.z - v.z) + (v.w - v.w) == 0.f ? fmaxf(m, big) : INFINITY;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((tid & 31) == 0) wmax[tid >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 16; ++q) m = fmaxf(m, wmax[q]);
+  const int e = scale_exp(m);                       // 0 for a block with infinities or NaN
+  const float inv = exp2_int(-e);
+#pragma unroll 4
+  for (int q = tid; q < rows * n4; q += 512) {
+    const int r = q / n4, c = (q % n4) * 4;
+    const float4 v = load(q);
+    const float f[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+    __half hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      hi[j] = __float2half_rn(f[j]);
+      const float h = __half2float(hi[j]);
+      lo[j] = isfinite(h) ? __float2half_rn((f[j] - h) * kLoStep) : __ushort_as_half(0);
+    }
+    __half* p = dst + (size_t)r * 2 * a.Ep + c;
+    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(hi);
+    *reinterpret_cast<uint2*>(p + a.Ep) = *reinterpret_cast<const uint2*>(lo);
+  }
+  if (tid == 0) (w ? a.sW : a.sT)[blk] = exp2_int(e);
+  if (w) pdl_wait();                                // on every path: completion stays transitive
+}
+
+// What the roles of a block share.
+struct Sync {
+  volatile int* abort;
+  int* status;
+  // Bounded; false once any wait of the block gave up.
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
+    if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait_bounded(bar, parity, abort, status, kDefaultWaitNs);
+  }
+};
+
+// ---------------------------------------------------------------- dWg
+// A block owns 256 rows i of dWg (two accumulators of 128) and 128 columns j, and a run of token
+// rows: chunks of 64 rows of X (as the transposed operand) and of the split dL.  The accumulators
+// are emptied into 32-bit registers after every 128 rows, where the scale of dL changes (and where
+// the chain of truncating additions ends); while one is emptied the other one is filled.
+struct WgArgs {
+  const float* sT;
+  float* dst;                  // [slots][d][E] (one run: dWg itself)
+  int T, d, E, Ep, run;        // run: token rows per block, a multiple of 128
+  int direct;                  // one run only
+  int* status;
+};
+constexpr int kWgStages = 3, kWgStageBytes = 65536;
+
+__global__ void __launch_bounds__(kThreads, 1)
+    gate_wgrad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mL,
+                      const WgArgs a) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kWgStages * kWgStageBytes);
+  uint64_t *full = bars, *empty = bars + kWgStages, *acc_full = bars + 2 * kWgStages, *acc_empty = acc_full + 2;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  int* flag = reinterpret_cast<int*>(holder + 1);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int s = 0; s < kWgStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&acc_full[h], 1);
+      mbar_init(&acc_empty[h], 256);
+    }
+    *flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(holder, 512);
+  pdl_trigger();
+  pdl_wait();                                       // the split dL
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *holder;
+  const Sync sy{flag, a.status};
+  const int i0 = blockIdx.x * 256, r0 = blockIdx.y * a.run, r1 = min(a.T, r0 + a.run), j0 = blockIdx.z * 128;
+  const int nb = min(2, (a.Ep - j0) / 64);          // 64-column boxes of dL's hi (and lo)
+  const int nh = i0 + 128 < a.d ? 2 : 1;            // accumulators
+  const int chunks = (r1 - r0 + 63) / 64;
+  if (warp < 4) {
+    regs_down<40>();
+    if (warp == 0) {
+      int stage = 0;
+      uint32_t phase = 1;
+      for (int c = 0; c < chunks; ++c) {
+        bool ok = true;
+        if (lane == 0) {
+          ok = sy.wait(&empty[stage], phase);
+          if (ok) {
+            uint8_t* st = sm + stage * kWgStageBytes;
+            const int y = r0 + 64 * c;
+            mbar_expect_tx(&full[stage], (2 * nh + 2 * nb) * 8192);
+            for (int b = 0; b < 2 * nh; ++b) tma_load_2d(st + b * 8192, &mX, i0 + 64 * b, y, &full[stage]);
+            for (int b = 0; b < 2 * nb; ++b)
+              tma_load_2d(st + 32768 + b * 8192, &mL, (b < nb ? 0 : a.Ep) + j0 + 64 * (b % nb), y, &full[stage]);
+          }
+        }
+        if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
+        if (++stage == kWgStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    } else if (warp == 1) {
+      const uint32_t idesc = idesc_f16(128, 128 * nb, 1, 1);
+      uint32_t seen = 0;                            // chunks known to have landed
+      for (int c = 0, blk = 0; c < chunks; c += 2, ++blk) {
+        const int n = min(2, chunks - c);
+        bool ok = true;
+        if (lane == 0) {
+          for (int h = 0; h < nh && ok; ++h) {
+            ok = sy.wait(&acc_empty[h], (blk & 1) ^ 1u);
+            if (!ok) break;
+            tc_fence_after();
+            for (int q = 0; q < n && ok; ++q) {
+              const int stage = (c + q) % kWgStages;
+              if ((int)seen <= c + q) {
+                ok = sy.wait(&full[stage], ((c + q) / kWgStages) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                seen = c + q + 1;
+              }
+              const uint32_t s0 = smem_u32(sm + stage * kWgStageBytes);
+              const uint64_t ad = smem_desc(s0 + h * 16384, 8192, 1024, 2);
+              const uint64_t bd = smem_desc(s0 + 32768, 8192, 1024, 2);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tc_mma_f16(tmem + h * 256, ad + k * 128, bd + k * 128, idesc, (q | k) ? 1u : 0u);
+              if (h == nh - 1) tc_commit(&empty[stage]);
+            }
+            if (ok) tc_commit(&acc_full[h]);
+          }
+        }
+        if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
+      }
+    }
+  } else {
+    regs_up<232>();
+    const int q = warp & 3, ch = (warp - 4) >> 2;   // TMEM lanes 32 q .., half of the columns
+    const int nc = 32 * nb;                         // columns of this warp
+    float acc[2][64];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 64; ++j) acc[h][j] = 0.f;
+    bool ok = true;
+    for (int c = 0, blk = 0; c < chunks && ok; c += 2, ++blk) {
+      const float s = a.sT[r0 / kBlk + blk], s2 = s / kLoStep;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h >= nh || !ok) break;
+        ok = sy.wait(&acc_full[h], blk & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t t0 = tmem + ((uint32_t)(32 * q) << 16) + h * 256 + ch * nc;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          if (16 * b < nc) {
+            float u[16], v[16];
+            tmem_ld16(t0 + 16 * b, u);
+            tmem_ld16(t0 + 64 * nb + 16 * b, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              acc[h][16 * b + j] = fmaf(s, u[j], fmaf(s2, v[j], acc[h][16 * b + j]));
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&acc_empty[h]);
+      }
+    }
+    // runs of partial sums are laid out as row_sum_join_kernel reads them
+    const int slot = a.direct ? 0 : 2 * (int)blockIdx.y + (r1 == a.T);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = i0 + 128 * h + 32 * q + lane;
+      if (i >= a.d) continue;
+      float* p = a.dst + ((size_t)slot * a.d + i) * a.E;
+#pragma unroll
+      for (int j = 0; j < 64; j += 4) {
+        const int col = j0 + ch * nc + j;
+        if (j >= nc || col >= a.E) continue;
+        if (a.E % 4 == 0)
+          *reinterpret_cast<float4*>(p + col) =
+              make_float4(acc[h][j], acc[h][j + 1], acc[h][j + 2], acc[h][j + 3]);
+        else
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (col + k < a.E) p[col + k] = acc[h][j + k];
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- dX
+// A block takes a tile of 128 tokens, keeps its split dL in shared memory (E <= 256) and walks a
+// part of d in tiles of 128: the split Wg comes from L2 in chunks of 64 experts, dX_in by TMA
+// into the tile that the accumulator warps add to in place and that TMA writes out.
+struct DxArgs {
+  const float *sT, *sW;
+  int T, d, E, Ep;
+  int parts;                   // column parts per token tile
+  int with_in;
+  int* status;
+};
+constexpr int kTile = 16384;                        // 128 rows x 64 columns
+constexpr int kDxB = 2;                             // stages of Wg: hi and lo of 64 experts
+template <int NKB>                                  // chunks of 64 experts
+struct DxPlan {
+  static constexpr int kIo = NKB <= 2 ? 2 : 1;      // in/out tiles of 128 x 128
+  static constexpr int kOffB = NKB * 2 * kTile, kOffIo = kOffB + kDxB * 2 * kTile;
+  static constexpr int kOffBar = kOffIo + kIo * 2 * kTile;
+  static constexpr int kBytes = kOffBar + 256 + 1024;
+};
+
+template <int NKB>
+__global__ void __launch_bounds__(kThreads, 1)
+    gate_dx_tc_kernel(const __grid_constant__ CUtensorMap mL, const __grid_constant__ CUtensorMap mW,
+                      const __grid_constant__ CUtensorMap mIn, const __grid_constant__ CUtensorMap mOut,
+                      const DxArgs a) {
+  using PL = DxPlan<NKB>;
+  constexpr int IO = PL::kIo;
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + PL::kOffBar);
+  uint64_t *a_full = bar, *a_empty = bar + 1, *b_full = bar + 2, *b_empty = bar + 4, *io_full = bar + 6,
+           *io_empty = bar + 8, *acc_full = bar + 10, *acc_empty = bar + 12;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(bar + 14);
+  int* flag = reinterpret_cast<int*>(holder + 1);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    mbar_init(a_full, 1);
+    mbar_init(a_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&b_full[s], 1);
+      mbar_init(&b_empty[s], 1);
+      mbar_init(&io_full[s], 1);
+      mbar_init(&io_empty[s], 2);
+      mbar_init(&acc_full[s], 1);
+      mbar_init(&acc_empty[s], 256);
+    }
+    *flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(holder, 512);
+  pdl_trigger();
+  pdl_wait();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *holder;
+  const Sync sy{flag, a.status};
+  const int nit = (a.d + 127) / 128, items = (a.T + 127) / 128 * a.parts;
+  auto begin_of = [&](int p) { return (int)((long long)nit * p / a.parts); };
+  if (warp == 0) {
+    int bs = 0, io = 0, round = 0;
+    uint32_t bp = 1, iop = 1;
+    bool ok = true;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x, ++round) {
+      const int t = item / a.parts, p = item - t * a.parts;
+      if (lane == 0) {
+        ok = sy.wait(a_empty, (round & 1) ^ 1u);
+        if (ok) {
+          mbar_expect_tx(a_full, NKB * 2 * kTile);
+          for (int kb = 0; kb < NKB; ++kb) {
+            tma_load_2d(sm + kb * 2 * kTile, &mL, 64 * kb, t * 128, a_full);
+            tma_load_2d(sm + (kb * 2 + 1) * kTile, &mL, a.Ep + 64 * kb, t * 128, a_full);
+          }
+        }
+        for (int i = begin_of(p); i < begin_of(p + 1) && ok; ++i) {
+          for (int kb = 0; kb < NKB && ok; ++kb) {
+            ok = sy.wait(&b_empty[bs], bp);
+            if (!ok) break;
+            uint8_t* st = sm + PL::kOffB + bs * 2 * kTile;
+            mbar_expect_tx(&b_full[bs], 2 * kTile);
+            tma_load_2d(st, &mW, 64 * kb, i * 128, &b_full[bs]);
+            tma_load_2d(st + kTile, &mW, a.Ep + 64 * kb, i * 128, &b_full[bs]);
+            if (++bs == kDxB) {
+              bs = 0;
+              bp ^= 1u;
+            }
+          }
+          if (!ok) break;
+          ok = sy.wait(&io_empty[io], iop);
+          if (!ok) break;
+          if (a.with_in) {
+            uint8_t* st = sm + PL::kOffIo + io * 2 * kTile;
+            mbar_expect_tx(&io_full[io], 2 * kTile);
+            tma_load_2d(st, &mIn, i * 128, t * 128, &io_full[io]);
+            tma_load_2d(st + kTile, &mIn, i * 128 + 64, t * 128, &io_full[io]);
+          } else {
+            mbar_arrive(&io_full[io]);
+          }
+          if (++io == IO) {
+            io = 0;
+            iop ^= 1u;
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
+    }
+  } else if (warp == 1) {
+    const uint32_t idesc = idesc_f16(128, 128, 0, 0);
+    int bs = 0, tile = 0, round = 0;
+    uint32_t bp = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x, ++round) {
+      const int p = item % a.parts;
+      if (lane == 0) {
+        ok = sy.wait(a_full, round & 1);
+        for (int i = begin_of(p); i < begin_of(p + 1) && ok; ++i, ++tile) {
+          const int buf = tile & 1;
+          ok = sy.wait(&acc_empty[buf], ((tile >> 1) & 1) ^ 1u);
+          for (int kb = 0; kb < NKB && ok; ++kb) {
+            ok = sy.wait(&b_full[bs], bp);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sa = smem_u32(sm + kb * 2 * kTile), sb = smem_u32(sm + PL::kOffB + bs * 2 * kTile);
+            const uint64_t ah = smem_desc(sa, 16, 1024, 2), al = smem_desc(sa + kTile, 16, 1024, 2);
+            const uint64_t bh = smem_desc(sb, 16, 1024, 2), bl = smem_desc(sb + kTile, 16, 1024, 2);
+            const uint32_t d1 = tmem + buf * 256, d2 = d1 + 128;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t more = (kb | k) ? 1u : 0u;
+              tc_mma_f16(d1, ah + 2 * k, bh + 2 * k, idesc, more);
+              tc_mma_f16(d2, al + 2 * k, bh + 2 * k, idesc, more);
+              tc_mma_f16(d2, ah + 2 * k, bl + 2 * k, idesc, 1u);
+            }
+            tc_commit(&b_empty[bs]);
+            if (++bs == kDxB) {
+              bs = 0;
+              bp ^= 1u;
+            }
+          }
+          if (ok) tc_commit(&acc_full[buf]);
+        }
+        if (ok) tc_commit(a_empty);
+      }
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
+    }
+  } else if (warp >= 4) {
+    const int q = warp & 3, ch = (warp - 4) >> 2;   // TMEM lanes 32 q .., 64-column half
+    const int row = 32 * q + lane;
+    int tile = 0, io = 0;
+    uint32_t iop = 0;
+    bool ok = true;
+    const bool storer = q == 0 && lane == 0;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const int t = item / a.parts, p = item - t * a.parts;
+      const float st = a.sT[t];
+      for (int i = begin_of(p); i < begin_of(p + 1) && ok; ++i, ++tile) {
+        const int buf = tile & 1;
+        ok = sy.wait(&acc_full[buf], (tile >> 1) & 1);
+        ok = ok && sy.wait(&io_full[io], iop);
+        // all warps of the half go on together: they meet at the store below
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float s = st * a.sW[i], s2 = s / kLoStep;
+        uint8_t* box = sm + PL::kOffIo + (io * 2 + ch) * kTile + row * 128;
+        const uint32_t t0 = tmem + ((uint32_t)(32 * q) << 16) + buf * 256 + ch * 64;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          float u[16], v[16];
+          tmem_ld16(t0 + 16 * b, u);
+          tmem_ld16(t0 + 128 + 16 * b, v);
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            uint4* at = reinterpret_cast<uint4*>(box + (((2 * b + w) ^ (row & 7)) << 4));
+            uint4 old = make_uint4(0u, 0u, 0u, 0u);
+            if (a.with_in) old = *at;
+            uint32_t o[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&o[j]));
+              const int k = 8 * w + 2 * j;
+              const __half2 r = __floats2half2_rn(fmaf(s, u[k], fmaf(s2, v[k], f.x)),
+                                                  fmaf(s, u[k + 1], fmaf(s2, v[k + 1], f.y)));
+              o[j] = *reinterpret_cast<const uint32_t*>(&r);
+            }
+            *at = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&acc_empty[buf]);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + ch) : "memory");
+        if (storer) {
+          const int x = i * 128 + 64 * ch;
+          if (x < a.d) tma_store_2d(&mOut, x, t * 128, sm + PL::kOffIo + (io * 2 + ch) * kTile);
+          bulk_commit();
+          if (IO == 1) {
+            bulk_wait_read<0>();
+            mbar_arrive(&io_empty[0]);
+          } else if (tile > 0) {                    // the tile before is out: its buffer is free
+            bulk_wait_read<1>();
+            mbar_arrive(&io_empty[io ^ 1]);
+          }
+        }
+        if (++io == IO) {
+          io = 0;
+          iop ^= 1u;
+        }
+      }
+    }
+    if (storer) bulk_wait_read<0>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+int pad64(int E) { return (E + 63) / 64 * 64; }
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+// Token rows per block of dWg, a multiple of 128: the fewest rounds of blocks on 152 SMs, plus what
+// the partial sums of a run cost.
+int wgrad_run(int T, int d, int E) {
+  const int blocks = (d + 255) / 256 * ((E + 127) / 128), all = (T + 127) / 128;
+  int best = all;
+  double cost = 1e300;
+  for (int p = 1; p <= std::min(all, 32); ++p) {
+    const int run = (all + p - 1) / p, runs = (all + run - 1) / run;
+    const double c = ((blocks * runs + 151) / 152) * (run + 1.0) + (runs > 1 ? 0.25 * runs + 1 : 0);
+    if (c < cost) {
+      cost = c;
+      best = run;
+    }
+  }
+  return best * 128;
+}
+
+struct GateWs {
+  size_t dl2, W2, sT, sW, partial, total;
+};
+GateWs gate_ws(int T, int d, int E) {
+  const size_t Ep = pad64(E);
+  GateWs w;
+  w.dl2 = 0;
+  w.W2 = w.dl2 + up256((size_t)T * 2 * Ep * 2);
+  w.sT = w.W2 + up256((size_t)d * 2 * Ep * 2);
+  w.sW = w.sT + up256((size_t)(T + 127) / 128 * 4);
+  w.partial = w.sW + up256((size_t)(d + 127) / 128 * 4);
+  const int run = wgrad_run(T, d, E), runs = (T + run - 1) / run;
+  w.total = w.partial + (runs > 1 ? up256((size_t)2 * runs * d * E * 4) : 0);
+  return w;
+}
+
+template <int NKB>
+cudaError_t launch_dx_tc(const CUtensorMap& mL, const CUtensorMap& mW, const CUtensorMap& mIn,
+                         const CUtensorMap& mOut, DxArgs a, int sms, cudaStream_t s) {
+  auto kern = gate_dx_tc_kernel<NKB>;
+  MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
+  const int tt = (a.T + 127) / 128, nit = (a.d + 127) / 128;
+  long long cost = 0;
+  for (int p = 1; p <= nit; ++p) {                  // fewest rounds; a part reloads dL (1 tile's time)
+    const long long c = ((long long)tt * p + sms - 1) / sms * ((nit + p - 1) / p + 1);
+    if (p == 1 || c < cost) {
+      cost = c;
+      a.parts = p;
+    }
+  }
+  const int grid = (int)std::min<long long>((long long)tt * a.parts, sms);
+  return launch_k(kern, grid, kThreads, DxPlan<NKB>::kBytes, s, true, mL, mW, mIn, mOut, a);
+}
+
+}  // namespace
+
+bool gate_tc_ok(int E) { return E <= 256; }
+size_t gate_tc_bytes(int T, int d, int E) { return T > 0 ? gate_ws(T, d, E).total : 0; }
+
+cudaError_t launch_gate_tc(const __half* tokens, const float* Wg, const float* dlogits, float* dWg,
+                           const __half* dx_in, __half* dx, uint8_t* ws, int* status, int T, int d, int E,
+                           cudaStream_t s) {
+  int dev = 0, sms = 0;
+  MOE_LAUNCH(cudaGetDevice(&dev));
+  MOE_LAUNCH(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  const GateWs w = gate_ws(T, d, E);
+  const int Ep = pad64(E);
+  SplitArgs sp;
+  sp.dl = dlogits;
+  sp.W = Wg;
+  sp.dl2 = reinterpret_cast<__half*>(ws + w.dl2);
+  sp.W2 = reinterpret_cast<__half*>(ws + w.W2);
+  sp.sT = reinterpret_cast<float*>(ws + w.sT);
+  sp.sW = reinterpret_cast<float*>(ws + w.sW);
+  sp.T = T;
+  sp.d = d;
+  sp.E = E;
+  sp.Ep = Ep;
+  sp.nT = (T + kBlk - 1) / kBlk;
+  const int blocks = sp.nT + (dx ? (d + kBlk - 1) / kBlk : 0);
+  MOE_LAUNCH(launch_k(gate_split_kernel, blocks, 512, 0, s, true, sp));
+  const uint64_t l_dims[2] = {(uint64_t)2 * Ep, (uint64_t)T}, x_dims[2] = {(uint64_t)d, (uint64_t)T};
+  const uint64_t w_dims[2] = {(uint64_t)2 * Ep, (uint64_t)d};
+  const uint32_t b64[2] = {64, 64}, b128[2] = {64, 128};
+  if (dWg) {
+    CUtensorMap mX, mL;
+    if (!encode_f16_map(&mX, tokens, 2, x_dims, b64) || !encode_f16_map(&mL, sp.dl2, 2, l_dims, b64))
+      return cudaErrorInvalidValue;
+    WgArgs a;
+    a.run = wgrad_run(T, d, E);
+    const int runs = (T + a.run - 1) / a.run;
+    a.sT = sp.sT;
+    a.direct = runs == 1;
+    float* partial = reinterpret_cast<float*>(ws + w.partial);
+    a.dst = a.direct ? dWg : partial;
+    a.T = T;
+    a.d = d;
+    a.E = E;
+    a.Ep = Ep;
+    a.status = status;
+    MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(gate_wgrad_kernel)));
+    MOE_LAUNCH(launch_k(gate_wgrad_kernel, dim3((d + 255) / 256, runs, (E + 127) / 128), kThreads,
+                        (size_t)kWgStages * kWgStageBytes + 256 + 1024, s, true, mX, mL, a));
+    if (!a.direct) MOE_LAUNCH(launch_sum_join(dWg, partial, d, E, T, a.run, sms, s));
+  }
+  if (dx) {
+    CUtensorMap mL, mW, mIn, mOut;
+    if (!encode_f16_map(&mL, sp.dl2, 2, l_dims, b128) || !encode_f16_map(&mW, sp.W2, 2, w_dims, b128) ||
+        !encode_f16_map(&mOut, dx, 2, x_dims, b128))
+      return cudaErrorInvalidValue;
+    if (!dx_in)
+      mIn = mOut;
+    else if (!encode_f16_map(&mIn, dx_in, 2, x_dims, b128))
+      return cudaErrorInvalidValue;
+    DxArgs a{sp.sT, sp.sW, T, d, E, Ep, 1, dx_in != nullptr, status};
+    const int nkb = Ep / 64;
+    if (nkb == 1) return launch_dx_tc<1>(mL, mW, mIn, mOut, a, sms, s);
+    if (nkb == 2) return launch_dx_tc<2>(mL, mW, mIn, mOut, a, sms, s);
+    if (nkb == 3) return launch_dx_tc<3>(mL, mW, mIn, mOut, a, sms, s);
+    return launch_dx_tc<4>(mL, mW, mIn, mOut, a, sms, s);
+  }
+  return cudaSuccess;
+}
+
+}  // namespace moe

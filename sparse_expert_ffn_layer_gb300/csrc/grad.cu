@@ -661,6 +661,22 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 size_t split_bytes(int dj, int S_max) { return up256((size_t)S_max * split_width(dj) * 4) + up256((size_t)S_max * 4); }
 }  // namespace
 
+// G = sum over runs of `run` of T rows, in order, of partial sums in partial_slot's layout.
+cudaError_t launch_sum_join(float* G, float* partial, int di, int dj, int T, int run, int sms, cudaStream_t s) {
+  SumArgs a;
+  memset(&a, 0, sizeof(a));
+  a.job[0].G = G;
+  a.job[0].partial = partial;
+  a.job[0].di = di;
+  a.job[0].dj = dj;
+  a.T = a.S_max = T;
+  a.N = 1;
+  a.seg = run;
+  const size_t all = (size_t)di * dj;
+  const int bx = (int)std::min<size_t>((all / 4 + 255) / 256, (size_t)32 * sms);
+  return launch_k(row_sum_join_kernel, dim3(std::max(1, bx), 1, 1), 256, 0, s, true, a);
+}
+
 size_t row_sums_bytes(int di0, int dj0, int di1, int dj1, bool f16, int S_max, int N) {
   size_t most = 0;
   // either job alone may be asked for: the plan of each combination fits

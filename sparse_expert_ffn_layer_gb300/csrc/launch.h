@@ -190,7 +190,7 @@ cudaError_t launch_balance_loss(const float* logits, const int32_t* topk_idx, co
                                 float* losses, int32_t* n_valid, float* records, cudaStream_t s);
 cudaError_t launch_dlogits(const float* logits, const int32_t* topk_idx, const float* dtopk_w,
                            const float* dlosses, const int32_t* counts, const int32_t* n_valid,
-                           const uint8_t* mask, int T, int E, int k, float* dlogits,
+                           const uint8_t* mask, int T, int E, int k, float* dlogits, int* status,
                            cudaStream_t s);
 // Sums over token rows for up to two jobs G[n][i][j] = scale_n sum_s x[row(s)][i] h[s][j]
 // (transposed: G[n][j][i]); G0 or G1 may be null (grad.cu).
@@ -202,6 +202,15 @@ cudaError_t launch_row_sums(const void* x0, const float* h0, float* G0, int di0,
                             int N, bool pdl, cudaStream_t s);
 // Bytes of its workspace, for either job alone or both (dj1 = 0: there is no second).
 size_t row_sums_bytes(int di0, int dj0, int di1, int dj1, bool f16, int S_max, int N);
+// Joins the partial sums of runs of `run` rows (slot 2 q, the last run's 2 q + 1) in order.
+cudaError_t launch_sum_join(float* G, float* partial, int di, int dj, int T, int run, int sms,
+                            cudaStream_t s);
+// The gate's gradient on the tensor cores (gate_grad.cu): f16 tokens, E <= 256, no rows left out.
+bool gate_tc_ok(int E);
+size_t gate_tc_bytes(int T, int d, int E);
+cudaError_t launch_gate_tc(const __half* tokens, const float* Wg, const float* dlogits, float* dWg,
+                           const __half* dx_in, __half* dx, uint8_t* ws, int* status, int T, int d, int E,
+                           cudaStream_t s);
 cudaError_t launch_gate_dx(const float* dlogits, const float* Wg, const void* in, int dtype_f16, int T,
                            int d, int E, void* out, cudaStream_t s);
 cudaError_t launch_combine_backward(const void* dout, const void* expert_out, const int32_t* slot_of,

@@ -296,7 +296,9 @@ __global__ void __launch_bounds__(256) dlogits_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
     const float* __restrict__ dtopk_w, const float* __restrict__ dlosses,
     const int32_t* __restrict__ counts, const int32_t* __restrict__ n_valid,
-    const uint8_t* __restrict__ mask, int T, int E, int k, float* __restrict__ dlogits) {
+    const uint8_t* __restrict__ mask, int T, int E, int k, float* __restrict__ dlogits,
+    int* __restrict__ status) {
+  if (status && blockIdx.x == 0 && threadIdx.x == 0) *status = kOk;
   constexpr int V = VEC * J;
   constexpr int RPW = 32 / LANES;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -481,7 +483,7 @@ cudaError_t launch_balance_loss(const float* logits, const int32_t* topk_idx, co
 
 cudaError_t launch_dlogits(const float* logits, const int32_t* topk_idx, const float* dtopk_w,
                            const float* dlosses, const int32_t* counts, const int32_t* n_valid,
-                           const uint8_t* mask, int T, int E, int k, float* dlogits,
+                           const uint8_t* mask, int T, int E, int k, float* dlogits, int* status,
                            cudaStream_t s) {
   const int sms = sm_count();
   if (sms < 1) return cudaErrorInvalidDevice;
@@ -490,7 +492,7 @@ cudaError_t launch_dlogits(const float* logits, const int32_t* topk_idx, const f
   return with_shape(E, [&](auto lanes, auto vec, auto j) -> cudaError_t {
     constexpr int L = decltype(lanes)::value, V = decltype(vec)::value, J = decltype(j)::value;
     return launch_k(dlogits_kernel<L, V, J>, grid, 256, 0, s, false, logits, topk_idx, dtopk_w,
-                    dlosses, counts, n_valid, mask, T, E, k, dlogits);
+                    dlosses, counts, n_valid, mask, T, E, k, dlogits, status);
   });
 }
 

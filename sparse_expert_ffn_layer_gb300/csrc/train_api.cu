@@ -89,7 +89,10 @@ moe_status moe_gate_backward_workspace_size(int T, int d, int E, moe_dtype dtype
   moe_status st = check_router(T, E, 1);
   if (st != MOE_OK) return st;
   if (d % lane_elems(dtype) || d > kMaxRows) return MOE_ERR_UNSUPPORTED;
-  *bytes = kAlign + align_up(row_sums_bytes(d, E, 0, 0, dtype == MOE_F16, T, 1));
+  // the tensor-core form, and the form that leaves masked rows out
+  size_t most = row_sums_bytes(d, E, 0, 0, dtype == MOE_F16, T, 1);
+  if (dtype == MOE_F16 && gate_tc_ok(E)) most = std::max(most, gate_tc_bytes(T, d, E));
+  *bytes = kAlign + align_up(most);
   return MOE_OK;
 }
 
@@ -124,13 +127,23 @@ moe_status moe_gate_topk_backward(const float* logits, const int32_t* topk_idx, 
     if (!workspace || ws_bytes < need) return MOE_ERR_WORKSPACE;
   }
   MOE_TRY(launch_dlogits(logits, topk_idx, dtopk_w, dlosses, counts, n_valid, token_mask, T, E, k,
-                         dlogits, s));
+                         dlogits, deep ? static_cast<int*>(workspace) : nullptr, s));
+  if (!deep) return MOE_OK;
   const int f16 = dtype == MOE_F16;
-  if (dWg)
+  uint8_t* ws = static_cast<uint8_t*>(workspace) + kAlign;
+  // Masked tokens may hold anything: their rows are left out of dWg's sums row by row, which the
+  // tensor-core form's boxes of rows cannot do.  (It needs no mask for dtokens: dlogits are zero.)
+  const bool tc = f16 && gate_tc_ok(E);
+  float* dWg_rows = dWg && (!tc || token_mask) ? dWg : nullptr;
+  if (dWg_rows)
     MOE_TRY(launch_row_sums(tokens, dlogits, dWg, d, E, 0, nullptr, nullptr, nullptr, 0, 0, 0, nullptr,
-                            nullptr, nullptr, token_mask, static_cast<uint8_t*>(workspace) + kAlign,
-                            f16, T, T, 1, /*pdl=*/true, s));
-  if (dtokens) MOE_TRY(launch_gate_dx(dlogits, Wg, dtokens_in, f16, T, d, E, dtokens, s));
+                            nullptr, nullptr, token_mask, ws, f16, T, T, 1, /*pdl=*/true, s));
+  if (tc && (dtokens || !dWg_rows))
+    MOE_TRY(launch_gate_tc(static_cast<const __half*>(tokens), Wg, dlogits, dWg_rows ? nullptr : dWg,
+                           static_cast<const __half*>(dtokens_in), static_cast<__half*>(dtokens), ws,
+                           static_cast<int*>(workspace), T, d, E, s));
+  else if (dtokens)
+    MOE_TRY(launch_gate_dx(dlogits, Wg, dtokens_in, f16, T, d, E, dtokens, s));
   return MOE_OK;
 }
 
