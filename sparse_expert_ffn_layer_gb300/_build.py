@@ -17,7 +17,7 @@ LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["api.cu", "gate.cu", "dispatch.cu", "grouped_gemm.cu", "simt_ffn.cu", "elementwise.cu",
            "noalloc.cu", "route_small.cu", "router_loss.cu", "adapter.cu", "grad.cu", "gate_grad.cu",
            "train_api.cu"]
-HEADERS = ["common.cuh", "groups.cuh", "launch.h", "mma.cuh", "topk.cuh", os.path.join("..", "..", "include", "moe.h")]
+HEADERS = ["common.cuh", "gate_split.cuh", "groups.cuh", "launch.h", "mma.cuh", "topk.cuh", os.path.join("..", "..", "include", "moe.h")]
 
 NVCC = os.environ.get("NVCC", "nvcc")
 FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",

@@ -1,26 +1,25 @@
 // The gate's gradient on the 5th-generation tensor cores, for f16 tokens:
 //   dWg [d, E] = X^T dL,    dX [T, d] = dX_in + dL Wg^T       (dL = dlogits, Wg: 32-bit)
 //
-// 32-bit operands on f16 tensor cores: a block of 128 rows of dL or Wg is scaled by one power of
-// two and split into v = hi + 2^-11 lo, both f16 (lo keeps its own exponent range, so v is good to
-// 2^-23 |v| + 2^-36 of the block's largest magnitude).  Products with hi and with lo go to separate
-// accumulators, joined as D1 + 2^-11 D2 in 32 bits; lo x lo is below 2^-22 and left out.  X is f16
-// and exact.  So dX takes three products and dWg two of 2 T d E operations each, which the tensor
-// cores do in less time than the operands' bytes take from DRAM.
+// dL stays good to 2^-23 of itself: a block of 128 rows is scaled by one power of two and split into
+// v = hi + 2^-11 lo, both f16 (lo keeps an exponent range of its own, so what is lost is 2^-23 |v| +
+// 2^-36 of the block's largest magnitude).  The products with hi and with lo go to separate
+// accumulators, joined as D1 + 2^-11 D2 in 32 bits.  X is f16 and exact, so dWg keeps the accuracy of
+// a 32-bit sum.  Wg is rounded to f16 once (scaled by 128 rows, so that none is lost below f16's
+// range): dX is f16, and the rounding adds at most 2^-11 of the sum of |dL Wg| to its own 2^-11.
+// (Wg split as well, with a third product: twice the bytes from L2 per tile, dX 73 us instead of
+// %DX% at 16384 x 3584 x 128.)  The split comes with the logits' gradient (router_loss.cu).
 //
 // Both kernels: one block per SM; warp 0 loads by TMA, warp 1 issues the products, eight warps read
 // the accumulators.  Every wait is bounded (common.cuh).
 #include <algorithm>
-#include <cstring>
 
+#include "gate_split.cuh"
 #include "launch.h"
-#include "mma.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kBlk = 128;                 // rows per scale
-constexpr float kLoStep = 2048.f;         // 2^11
 constexpr int kThreads = 384;             // 4 warps (2 used) + 8 accumulator warps
 
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, int x, int y, const void* smem) {
@@ -39,71 +38,29 @@ __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.
 template <int N>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// ---------------------------------------------------------------- split
-// rows x E values -> [rows][2 Ep] f16 (hi, lo; columns beyond E are zero) and a scale per 128 rows.
-// Blocks [0, nT) take dL, the others Wg.
-struct SplitArgs {
-  const float *dl, *W;
-  __half *dl2, *W2;
-  float *sT, *sW;
-  int T, d, E, Ep, nT;
-};
-__global__ void __launch_bounds__(512) gate_split_kernel(const SplitArgs a) {
-  __shared__ float wmax[16];
-  pdl_trigger();
-  const bool w = (int)blockIdx.x >= a.nT;
-  if (!w) pdl_wait();                               // dL comes from the launch before
-  const int blk = (int)blockIdx.x - (w ? a.nT : 0);
-  const int rows = min(kBlk, (w ? a.d : a.T) - blk * kBlk);
-  const float* src = (w ? a.W : a.dl) + (size_t)blk * kBlk * a.E;
-  __half* dst = (w ? a.W2 : a.dl2) + (size_t)blk * kBlk * 2 * a.Ep;
-  const int n4 = a.Ep / 4, tid = threadIdx.x;
-  auto load = [&](int q) {
-    const int r = q / n4, c = (q % n4) * 4;
-    const float* p = src + (size_t)r * a.E + c;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (c >= a.E) return v;
-    if (a.E % 4 == 0) return *reinterpret_cast<const float4*>(p);
-    v.x = p[0];
-    if (c + 1 < a.E) v.y = p[1];
-    if (c + 2 < a.E) v.z = p[2];
-    if (c + 3 < a.E) v.w = p[3];
-    return v;
-  };
-  float m = 0.f;
-#pragma unroll 4
-  for (int q = tid; q < rows * n4; q += 512) {
-    const float4 v = load(q);
-    const float big = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-    // NaN is not seen by fmaxf: v - v is 0 unless a value is infinite or NaN
-    m = (v.x - v.x) + (v.y - v.y) + (v.z - v.z) + (v.w - v.w) == 0.f ? fmaxf(m, big) : INFINITY;
+// 32 lanes x 32 columns of two accumulators, one wait.
+__device__ __forceinline__ void tmem_ld32x2(uint32_t t1, uint32_t t2, float (&u)[32], float (&v)[32]) {
+  uint32_t a[32], b[32];
+#define MOE_LD32(r, t)                                                                              \
+  asm volatile(                                                                                     \
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32"                                                      \
+      " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"    \
+      "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"                                                    \
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),         \
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),     \
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),  \
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),  \
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])                                          \
+      : "r"(t))
+  MOE_LD32(a, t1);
+  MOE_LD32(b, t2);
+#undef MOE_LD32
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    u[j] = __uint_as_float(a[j]);
+    v[j] = __uint_as_float(b[j]);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((tid & 31) == 0) wmax[tid >> 5] = m;
-  __syncthreads();
-#pragma unroll
-  for (int q = 0; q < 16; ++q) m = fmaxf(m, wmax[q]);
-  const int e = scale_exp(m);                       // 0 for a block with infinities or NaN
-  const float inv = exp2_int(-e);
-#pragma unroll 4
-  for (int q = tid; q < rows * n4; q += 512) {
-    const int r = q / n4, c = (q % n4) * 4;
-    const float4 v = load(q);
-    const float f[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-    __half hi[4], lo[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      hi[j] = __float2half_rn(f[j]);
-      const float h = __half2float(hi[j]);
-      lo[j] = isfinite(h) ? __float2half_rn((f[j] - h) * kLoStep) : __ushort_as_half(0);
-    }
-    __half* p = dst + (size_t)r * 2 * a.Ep + c;
-    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(hi);
-    *reinterpret_cast<uint2*>(p + a.Ep) = *reinterpret_cast<const uint2*>(lo);
-  }
-  if (tid == 0) (w ? a.sW : a.sT)[blk] = exp2_int(e);
-  if (w) pdl_wait();                                // on every path: completion stays transitive
 }
 
 // What the roles of a block share.
@@ -118,10 +75,12 @@ struct Sync {
 };
 
 // ---------------------------------------------------------------- dWg
-// A block owns 256 rows i of dWg (two accumulators of 128) and 128 columns j, and a run of token
-// rows: chunks of 64 rows of X (as the transposed operand) and of the split dL.  The accumulators
-// are emptied into 32-bit registers after every 128 rows, where the scale of dL changes (and where
-// the chain of truncating additions ends); while one is emptied the other one is filled.
+// A block owns IW x 128 rows i of dWg and 128 columns j, and a run of token rows: chunks of 64 rows
+// of X (as the transposed operand) and of the split dL.  The accumulators are emptied into 32-bit
+// registers after every 128 rows, where the scale of dL changes (and where the chain of truncating
+// additions ends).  IW = 2: the two accumulators share each chunk of dL (64 KB from L2 per 64 KB of
+// X; with one the copies from L2 bound it); while the second is emptied the first fills again.
+// IW = 1, for batches with too few blocks: two accumulators alternate.
 struct WgArgs {
   const float* sT;
   float* dst;                  // [slots][d][E] (one run: dWg itself)
@@ -129,8 +88,10 @@ struct WgArgs {
   int direct;                  // one run only
   int* status;
 };
-constexpr int kWgStages = 3, kWgStageBytes = 65536;
+constexpr int kWgStageBytes = 65536;
+constexpr int kWgStages = 3;
 
+template <int IW>
 __global__ void __launch_bounds__(kThreads, 1)
     gate_wgrad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mL,
                       const WgArgs a) {
@@ -161,9 +122,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *holder;
   const Sync sy{flag, a.status};
-  const int i0 = blockIdx.x * 256, r0 = blockIdx.y * a.run, r1 = min(a.T, r0 + a.run), j0 = blockIdx.z * 128;
+  const int i0 = blockIdx.x * 128 * IW, r0 = blockIdx.y * a.run, r1 = min(a.T, r0 + a.run);
+  const int j0 = blockIdx.z * 128;
   const int nb = min(2, (a.Ep - j0) / 64);          // 64-column boxes of dL's hi (and lo)
-  const int nh = i0 + 128 < a.d ? 2 : 1;            // accumulators
   const int chunks = (r1 - r0 + 63) / 64;
   if (warp < 4) {
     regs_down<40>();
@@ -177,8 +138,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok) {
             uint8_t* st = sm + stage * kWgStageBytes;
             const int y = r0 + 64 * c;
-            mbar_expect_tx(&full[stage], (2 * nh + 2 * nb) * 8192);
-            for (int b = 0; b < 2 * nh; ++b) tma_load_2d(st + b * 8192, &mX, i0 + 64 * b, y, &full[stage]);
+            mbar_expect_tx(&full[stage], (2 * IW + 2 * nb) * 8192);
+            for (int b = 0; b < 2 * IW; ++b) tma_load_2d(st + b * 8192, &mX, i0 + 64 * b, y, &full[stage]);
             for (int b = 0; b < 2 * nb; ++b)
               tma_load_2d(st + 32768 + b * 8192, &mL, (b < nb ? 0 : a.Ep) + j0 + 64 * (b % nb), y, &full[stage]);
           }
@@ -191,76 +152,79 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 1) {
       const uint32_t idesc = idesc_f16(128, 128 * nb, 1, 1);
-      uint32_t seen = 0;                            // chunks known to have landed
-      for (int c = 0, blk = 0; c < chunks; c += 2, ++blk) {
-        const int n = min(2, chunks - c);
-        bool ok = true;
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int c = 0; c < chunks && ok; ++c) {
+        const int blk = c >> 1;
         if (lane == 0) {
-          for (int h = 0; h < nh && ok; ++h) {
-            ok = sy.wait(&acc_empty[h], (blk & 1) ^ 1u);
-            if (!ok) break;
-            tc_fence_after();
-            for (int q = 0; q < n && ok; ++q) {
-              const int stage = (c + q) % kWgStages;
-              if ((int)seen <= c + q) {
-                ok = sy.wait(&full[stage], ((c + q) / kWgStages) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                seen = c + q + 1;
-              }
-              const uint32_t s0 = smem_u32(sm + stage * kWgStageBytes);
-              const uint64_t ad = smem_desc(s0 + h * 16384, 8192, 1024, 2);
-              const uint64_t bd = smem_desc(s0 + 32768, 8192, 1024, 2);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                tc_mma_f16(tmem + h * 256, ad + k * 128, bd + k * 128, idesc, (q | k) ? 1u : 0u);
-              if (h == nh - 1) tc_commit(&empty[stage]);
+          ok = sy.wait(&full[stage], phase);
+          tc_fence_after();
+          const uint32_t s0 = smem_u32(sm + stage * kWgStageBytes);
+          const uint64_t bd = smem_desc(s0 + 32768, 8192, 1024, 2);
+          for (int h = 0; h < IW && ok; ++h) {
+            const int buf = IW == 2 ? h : blk & 1, use = IW == 2 ? blk : blk >> 1;
+            if (!(c & 1)) {                         // a new block of 128 rows: the accumulator is empty
+              ok = sy.wait(&acc_empty[buf], (use & 1) ^ 1u);
+              if (!ok) break;
+              tc_fence_after();
             }
-            if (ok) tc_commit(&acc_full[h]);
+            const uint64_t ad = smem_desc(s0 + h * 16384, 8192, 1024, 2);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc_mma_f16(tmem + buf * 256, ad + k * 128, bd + k * 128, idesc, ((c & 1) | k) ? 1u : 0u);
+            if ((c & 1) || c == chunks - 1) tc_commit(&acc_full[buf]);
           }
+          if (ok) tc_commit(&empty[stage]);
         }
-        if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
+        if (++stage == kWgStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
     }
   } else {
     regs_up<232>();
     const int q = warp & 3, ch = (warp - 4) >> 2;   // TMEM lanes 32 q .., half of the columns
     const int nc = 32 * nb;                         // columns of this warp
-    float acc[2][64];
+    float acc[IW][64];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < IW; ++h)
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[h][j] = 0.f;
     bool ok = true;
+    float next = a.sT[r0 / kGateBlock];
     for (int c = 0, blk = 0; c < chunks && ok; c += 2, ++blk) {
-      const float s = a.sT[r0 / kBlk + blk], s2 = s / kLoStep;
+      const float s = next, s2 = s / kGateLo;
+      if (c + 2 < chunks) next = a.sT[r0 / kGateBlock + blk + 1];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (h >= nh || !ok) break;
-        ok = sy.wait(&acc_full[h], blk & 1);
+      for (int h = 0; h < IW; ++h) {
+        if (!ok) break;
+        const int buf = IW == 2 ? h : blk & 1, use = IW == 2 ? blk : blk >> 1;
+        ok = sy.wait(&acc_full[buf], use & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t t0 = tmem + ((uint32_t)(32 * q) << 16) + h * 256 + ch * nc;
+        const uint32_t t0 = tmem + ((uint32_t)(32 * q) << 16) + buf * 256 + ch * nc;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          if (16 * b < nc) {
-            float u[16], v[16];
-            tmem_ld16(t0 + 16 * b, u);
-            tmem_ld16(t0 + 64 * nb + 16 * b, v);
+        for (int b = 0; b < 2; ++b) {
+          if (b < nb) {
+            float u[32], v[32];
+            tmem_ld32x2(t0 + 32 * b, t0 + 64 * nb + 32 * b, u, v);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              acc[h][16 * b + j] = fmaf(s, u[j], fmaf(s2, v[j], acc[h][16 * b + j]));
+            for (int j = 0; j < 32; ++j)
+              acc[h][32 * b + j] = fmaf(s, u[j], fmaf(s2, v[j], acc[h][32 * b + j]));
           }
         }
         tc_fence_before();
-        mbar_arrive(&acc_empty[h]);
+        mbar_arrive(&acc_empty[buf]);
       }
     }
     // runs of partial sums are laid out as row_sum_join_kernel reads them
     const int slot = a.direct ? 0 : 2 * (int)blockIdx.y + (r1 == a.T);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < IW; ++h) {
       const int i = i0 + 128 * h + 32 * q + lane;
       if (i >= a.d) continue;
       float* p = a.dst + ((size_t)slot * a.d + i) * a.E;
@@ -296,11 +260,11 @@ struct DxArgs {
   int* status;
 };
 constexpr int kTile = 16384;                        // 128 rows x 64 columns
-constexpr int kDxB = 2;                             // stages of Wg: hi and lo of 64 experts
+constexpr int kDxB = 4;                             // stages of Wg: 64 experts each
 template <int NKB>                                  // chunks of 64 experts
 struct DxPlan {
   static constexpr int kIo = NKB <= 2 ? 2 : 1;      // in/out tiles of 128 x 128
-  static constexpr int kOffB = NKB * 2 * kTile, kOffIo = kOffB + kDxB * 2 * kTile;
+  static constexpr int kOffB = NKB * 2 * kTile, kOffIo = kOffB + kDxB * kTile;
   static constexpr int kOffBar = kOffIo + kIo * 2 * kTile;
   static constexpr int kBytes = kOffBar + 256 + 1024;
 };
@@ -315,17 +279,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + PL::kOffBar);
-  uint64_t *a_full = bar, *a_empty = bar + 1, *b_full = bar + 2, *b_empty = bar + 4, *io_full = bar + 6,
-           *io_empty = bar + 8, *acc_full = bar + 10, *acc_empty = bar + 12;
-  uint32_t* holder = reinterpret_cast<uint32_t*>(bar + 14);
+  uint64_t *a_full = bar, *a_empty = bar + 1, *io_full = bar + 2, *io_empty = bar + 4, *acc_full = bar + 6,
+           *acc_empty = bar + 8, *b_full = bar + 10, *b_empty = b_full + kDxB;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(b_empty + kDxB);
   int* flag = reinterpret_cast<int*>(holder + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     mbar_init(a_full, 1);
     mbar_init(a_empty, 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kDxB; ++s) {
       mbar_init(&b_full[s], 1);
       mbar_init(&b_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&io_full[s], 1);
       mbar_init(&io_empty[s], 2);
       mbar_init(&acc_full[s], 1);
@@ -363,10 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kb = 0; kb < NKB && ok; ++kb) {
             ok = sy.wait(&b_empty[bs], bp);
             if (!ok) break;
-            uint8_t* st = sm + PL::kOffB + bs * 2 * kTile;
-            mbar_expect_tx(&b_full[bs], 2 * kTile);
-            tma_load_2d(st, &mW, 64 * kb, i * 128, &b_full[bs]);
-            tma_load_2d(st + kTile, &mW, a.Ep + 64 * kb, i * 128, &b_full[bs]);
+            mbar_expect_tx(&b_full[bs], kTile);
+            tma_load_2d(sm + PL::kOffB + bs * kTile, &mW, 64 * kb, i * 128, &b_full[bs]);
             if (++bs == kDxB) {
               bs = 0;
               bp ^= 1u;
@@ -407,16 +371,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = sy.wait(&b_full[bs], bp);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t sa = smem_u32(sm + kb * 2 * kTile), sb = smem_u32(sm + PL::kOffB + bs * 2 * kTile);
+            const uint32_t sa = smem_u32(sm + kb * 2 * kTile), sb = smem_u32(sm + PL::kOffB + bs * kTile);
             const uint64_t ah = smem_desc(sa, 16, 1024, 2), al = smem_desc(sa + kTile, 16, 1024, 2);
-            const uint64_t bh = smem_desc(sb, 16, 1024, 2), bl = smem_desc(sb + kTile, 16, 1024, 2);
+            const uint64_t bh = smem_desc(sb, 16, 1024, 2);
             const uint32_t d1 = tmem + buf * 256, d2 = d1 + 128;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t more = (kb | k) ? 1u : 0u;
               tc_mma_f16(d1, ah + 2 * k, bh + 2 * k, idesc, more);
               tc_mma_f16(d2, al + 2 * k, bh + 2 * k, idesc, more);
-              tc_mma_f16(d2, ah + 2 * k, bl + 2 * k, idesc, 1u);
             }
             tc_commit(&b_empty[bs]);
             if (++bs == kDxB) {
@@ -450,17 +413,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        const float s = st * a.sW[i], s2 = s / kLoStep;
+        const float s = st * a.sW[i], s2 = s / kGateLo;
         uint8_t* box = sm + PL::kOffIo + (io * 2 + ch) * kTile + row * 128;
         const uint32_t t0 = tmem + ((uint32_t)(32 * q) << 16) + buf * 256 + ch * 64;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          float u[16], v[16];
-          tmem_ld16(t0 + 16 * b, u);
-          tmem_ld16(t0 + 128 + 16 * b, v);
+        for (int b = 0; b < 2; ++b) {
+          float u[32], v[32];
+          tmem_ld32x2(t0 + 32 * b, t0 + 128 + 32 * b, u, v);
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            uint4* at = reinterpret_cast<uint4*>(box + (((2 * b + w) ^ (row & 7)) << 4));
+          for (int w = 0; w < 4; ++w) {
+            uint4* at = reinterpret_cast<uint4*>(box + (((4 * b + w) ^ (row & 7)) << 4));
             uint4 old = make_uint4(0u, 0u, 0u, 0u);
             if (a.with_in) old = *at;
             uint32_t o[4] = {old.x, old.y, old.z, old.w};
@@ -508,21 +470,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 int pad64(int E) { return (E + 63) / 64 * 64; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Token rows per block of dWg, a multiple of 128: the fewest rounds of blocks on 152 SMs, plus what
-// the partial sums of a run cost.
-int wgrad_run(int T, int d, int E) {
-  const int blocks = (d + 255) / 256 * ((E + 127) / 128), all = (T + 127) / 128;
-  int best = all;
+// Token rows per block of dWg (a multiple of 128) and accumulators per block: what takes least time
+// by 1.5 us per 128 rows with two, 1 us with one, 3 us to start, and the partial sums' way through
+// L2 and the launch that joins them.
+struct WgPlan {
+  int run, iw;
+};
+WgPlan wgrad_plan(int T, int d, int E) {
+  const int all = (T + 127) / 128, jb = (E + 127) / 128;
+  WgPlan best{all * 128, 2};
   double cost = 1e300;
-  for (int p = 1; p <= std::min(all, 32); ++p) {
-    const int run = (all + p - 1) / p, runs = (all + run - 1) / run;
-    const double c = ((blocks * runs + 151) / 152) * (run + 1.0) + (runs > 1 ? 0.25 * runs + 1 : 0);
-    if (c < cost) {
-      cost = c;
-      best = run;
+  for (int iw = 1; iw <= 2; ++iw) {
+    const int blocks = (d + 128 * iw - 1) / (128 * iw) * jb;
+    for (int p = 1; p <= std::min(all, 32); ++p) {
+      const int run = (all + p - 1) / p, runs = (all + run - 1) / run;
+      const double c = ((blocks * runs + 151) / 152) * (run * (iw == 2 ? 1.5 : 1.0) + 3.0) +
+                       (runs > 1 ? 2.0 + runs * (double)d * E * 1e-6 : 0);
+      if (c < cost) {
+        cost = c;
+        best = WgPlan{run * 128, iw};
+      }
     }
   }
-  return best * 128;
+  return best;
 }
 
 struct GateWs {
@@ -533,10 +503,10 @@ GateWs gate_ws(int T, int d, int E) {
   GateWs w;
   w.dl2 = 0;
   w.W2 = w.dl2 + up256((size_t)T * 2 * Ep * 2);
-  w.sT = w.W2 + up256((size_t)d * 2 * Ep * 2);
+  w.sT = w.W2 + up256((size_t)d * Ep * 2);
   w.sW = w.sT + up256((size_t)(T + 127) / 128 * 4);
   w.partial = w.sW + up256((size_t)(d + 127) / 128 * 4);
-  const int run = wgrad_run(T, d, E), runs = (T + run - 1) / run;
+  const int run = wgrad_plan(T, d, E).run, runs = (T + run - 1) / run;
   w.total = w.partial + (runs > 1 ? up256((size_t)2 * runs * d * E * 4) : 0);
   return w;
 }
@@ -564,62 +534,47 @@ cudaError_t launch_dx_tc(const CUtensorMap& mL, const CUtensorMap& mW, const CUt
 bool gate_tc_ok(int E) { return E <= 256; }
 size_t gate_tc_bytes(int T, int d, int E) { return T > 0 ? gate_ws(T, d, E).total : 0; }
 
-cudaError_t launch_gate_tc(const __half* tokens, const float* Wg, const float* dlogits, float* dWg,
-                           const __half* dx_in, __half* dx, uint8_t* ws, int* status, int T, int d, int E,
-                           cudaStream_t s) {
+cudaError_t launch_gate_tc(const float* logits, const int32_t* topk_idx, const float* dtopk_w,
+                           const float* dlosses, const int32_t* counts, const int32_t* n_valid,
+                           const uint8_t* mask, int k, float* dlogits, const __half* tokens,
+                           const float* Wg, float* dWg, const __half* dx_in, __half* dx, uint8_t* ws,
+                           int* status, int T, int d, int E, cudaStream_t s) {
   int dev = 0, sms = 0;
   MOE_LAUNCH(cudaGetDevice(&dev));
   MOE_LAUNCH(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   const GateWs w = gate_ws(T, d, E);
   const int Ep = pad64(E);
-  SplitArgs sp;
-  sp.dl = dlogits;
-  sp.W = Wg;
-  sp.dl2 = reinterpret_cast<__half*>(ws + w.dl2);
-  sp.W2 = reinterpret_cast<__half*>(ws + w.W2);
-  sp.sT = reinterpret_cast<float*>(ws + w.sT);
-  sp.sW = reinterpret_cast<float*>(ws + w.sW);
-  sp.T = T;
-  sp.d = d;
-  sp.E = E;
-  sp.Ep = Ep;
-  sp.nT = (T + kBlk - 1) / kBlk;
-  const int blocks = sp.nT + (dx ? (d + kBlk - 1) / kBlk : 0);
-  MOE_LAUNCH(launch_k(gate_split_kernel, blocks, 512, 0, s, true, sp));
+  __half *dl2 = reinterpret_cast<__half*>(ws + w.dl2), *W2 = reinterpret_cast<__half*>(ws + w.W2);
+  float *sT = reinterpret_cast<float*>(ws + w.sT), *sW = reinterpret_cast<float*>(ws + w.sW);
+  MOE_LAUNCH(launch_dlogits_split(logits, topk_idx, dtopk_w, dlosses, counts, n_valid, mask, T, E, k,
+                                  dlogits, status, dx ? Wg : nullptr, d, Ep, dl2, sT, W2, sW, s));
   const uint64_t l_dims[2] = {(uint64_t)2 * Ep, (uint64_t)T}, x_dims[2] = {(uint64_t)d, (uint64_t)T};
-  const uint64_t w_dims[2] = {(uint64_t)2 * Ep, (uint64_t)d};
+  const uint64_t w_dims[2] = {(uint64_t)Ep, (uint64_t)d};
   const uint32_t b64[2] = {64, 64}, b128[2] = {64, 128};
   if (dWg) {
     CUtensorMap mX, mL;
-    if (!encode_f16_map(&mX, tokens, 2, x_dims, b64) || !encode_f16_map(&mL, sp.dl2, 2, l_dims, b64))
+    if (!encode_f16_map(&mX, tokens, 2, x_dims, b64) || !encode_f16_map(&mL, dl2, 2, l_dims, b64))
       return cudaErrorInvalidValue;
-    WgArgs a;
-    a.run = wgrad_run(T, d, E);
-    const int runs = (T + a.run - 1) / a.run;
-    a.sT = sp.sT;
-    a.direct = runs == 1;
+    const WgPlan pl = wgrad_plan(T, d, E);
+    const int runs = (T + pl.run - 1) / pl.run;
     float* partial = reinterpret_cast<float*>(ws + w.partial);
-    a.dst = a.direct ? dWg : partial;
-    a.T = T;
-    a.d = d;
-    a.E = E;
-    a.Ep = Ep;
-    a.status = status;
-    MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(gate_wgrad_kernel)));
-    MOE_LAUNCH(launch_k(gate_wgrad_kernel, dim3((d + 255) / 256, runs, (E + 127) / 128), kThreads,
+    const WgArgs a{sT, runs == 1 ? dWg : partial, T, d, E, Ep, pl.run, runs == 1, status};
+    auto kern = pl.iw == 2 ? gate_wgrad_kernel<2> : gate_wgrad_kernel<1>;
+    MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
+    MOE_LAUNCH(launch_k(kern, dim3((d + 128 * pl.iw - 1) / (128 * pl.iw), runs, (E + 127) / 128), kThreads,
                         (size_t)kWgStages * kWgStageBytes + 256 + 1024, s, true, mX, mL, a));
-    if (!a.direct) MOE_LAUNCH(launch_sum_join(dWg, partial, d, E, T, a.run, sms, s));
+    if (runs > 1) MOE_LAUNCH(launch_sum_join(dWg, partial, d, E, T, pl.run, sms, s));
   }
   if (dx) {
     CUtensorMap mL, mW, mIn, mOut;
-    if (!encode_f16_map(&mL, sp.dl2, 2, l_dims, b128) || !encode_f16_map(&mW, sp.W2, 2, w_dims, b128) ||
+    if (!encode_f16_map(&mL, dl2, 2, l_dims, b128) || !encode_f16_map(&mW, W2, 2, w_dims, b128) ||
         !encode_f16_map(&mOut, dx, 2, x_dims, b128))
       return cudaErrorInvalidValue;
     if (!dx_in)
       mIn = mOut;
     else if (!encode_f16_map(&mIn, dx_in, 2, x_dims, b128))
       return cudaErrorInvalidValue;
-    DxArgs a{sp.sT, sp.sW, T, d, E, Ep, 1, dx_in != nullptr, status};
+    DxArgs a{sT, sW, T, d, E, Ep, 1, dx_in != nullptr, status};
     const int nkb = Ep / 64;
     if (nkb == 1) return launch_dx_tc<1>(mL, mW, mIn, mOut, a, sms, s);
     if (nkb == 2) return launch_dx_tc<2>(mL, mW, mIn, mOut, a, sms, s);

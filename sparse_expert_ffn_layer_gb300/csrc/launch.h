@@ -205,12 +205,21 @@ size_t row_sums_bytes(int di0, int dj0, int di1, int dj1, bool f16, int S_max, i
 // Joins the partial sums of runs of `run` rows (slot 2 q, the last run's 2 q + 1) in order.
 cudaError_t launch_sum_join(float* G, float* partial, int di, int dj, int T, int run, int sms,
                             cudaStream_t s);
-// The gate's gradient on the tensor cores (gate_grad.cu): f16 tokens, E <= 256, no rows left out.
+// The gate's whole gradient on the tensor cores (gate_grad.cu): f16 tokens, E <= 256; dWg (may be
+// null) without rows left out.
 bool gate_tc_ok(int E);
 size_t gate_tc_bytes(int T, int d, int E);
-cudaError_t launch_gate_tc(const __half* tokens, const float* Wg, const float* dlogits, float* dWg,
-                           const __half* dx_in, __half* dx, uint8_t* ws, int* status, int T, int d, int E,
-                           cudaStream_t s);
+cudaError_t launch_gate_tc(const float* logits, const int32_t* topk_idx, const float* dtopk_w,
+                           const float* dlosses, const int32_t* counts, const int32_t* n_valid,
+                           const uint8_t* mask, int k, float* dlogits, const __half* tokens,
+                           const float* Wg, float* dWg, const __half* dx_in, __half* dx, uint8_t* ws,
+                           int* status, int T, int d, int E, cudaStream_t s);
+// Its first launch: the logits' gradient, also in f16 parts, and (Wg not null) Wg in f16.
+cudaError_t launch_dlogits_split(const float* logits, const int32_t* topk_idx, const float* dtopk_w,
+                                 const float* dlosses, const int32_t* counts, const int32_t* n_valid,
+                                 const uint8_t* mask, int T, int E, int k, float* dlogits, int* status,
+                                 const float* Wg, int d, int Ep, __half* dl2, float* sT, __half* W2,
+                                 float* sW, cudaStream_t s);
 cudaError_t launch_gate_dx(const float* dlogits, const float* Wg, const void* in, int dtype_f16, int T,
                            int d, int E, void* out, cudaStream_t s);
 cudaError_t launch_combine_backward(const void* dout, const void* expert_out, const int32_t* slot_of,

@@ -17,6 +17,7 @@
 
 #include <algorithm>
 
+#include "gate_split.cuh"
 #include "launch.h"
 
 namespace cg = cooperative_groups;
@@ -289,101 +290,237 @@ __global__ void __launch_bounds__(kFinalThreads) balance_join_kernel(
   join_records([&](int b) { return records + b * words; }, nb, E, k, o, sh_f, sh_i, share);
 }
 
+struct DlArgs {
+  const float* logits;
+  const int32_t* topk_idx;
+  const float *dtopk_w, *dlosses;
+  const int32_t *counts, *n_valid;
+  const uint8_t* mask;
+  int T, E, k;
+  float* dlogits;
+  int* status;                 // cleared, or null
+};
+
+// What every row needs: a_e of this lane's columns and the factor of the z loss.
+template <int LANES, int VEC, int J>
+__device__ __forceinline__ float loss_factors(const DlArgs& d, int l, float (&a)[VEC * J]) {
+  if (!d.dlosses) return 0.f;
+  const float n = (float)max(*d.n_valid, 1);
+  const float cb = d.dlosses[0] * (float)d.E / (n * (float)d.k) / n;
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      const int e = col_of<LANES, VEC>(j, l) + v;
+      a[VEC * j + v] = e < d.E ? cb * (float)d.counts[e] : 0.f;
+    }
+  return 2.f * d.dlosses[1] / n;
+}
+
+// The row's logits x become their gradient (zero for a row that is off).
+template <int LANES, int VEC, int J>
+__device__ __forceinline__ void row_gradient(const DlArgs& d, int64_t t, bool on, int l,
+                                             const float (&a)[VEC * J], float gz, float (&x)[VEC * J]) {
+  constexpr int V = VEC * J;
+  float top[2] = {0.f, 0.f}, dw[2] = {0.f, 0.f};
+  int idx[2] = {-1, -1};
+  if (d.dtopk_w && on) {
+    for (int j = 0; j < d.k; ++j) {
+      const int e = d.topk_idx[(size_t)t * d.k + j];
+      if ((unsigned)e < (unsigned)d.E) {
+        idx[j] = e;
+        top[j] = d.logits[(size_t)t * d.E + e];
+        dw[j] = d.dtopk_w[(size_t)t * d.k + j];
+      }
+    }
+  }
+  const float lse = softmax_row<LANES>(x);                   // x is p now
+  float bar = 0.f;
+  if (d.dlosses) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) bar += a[i] * x[i];
+  }
+  bar = group_sum<LANES>(bar);
+  // top-1: w = p[e1];  top-2: w_j = p[e_j] / (p[e1] + p[e2]), a softmax over the two logits
+  float add[2] = {0.f, 0.f}, minus = 0.f;
+  if (d.dtopk_w) {
+    if (d.k == 1) {
+      // a row of -inf only has no weight to differentiate (p = 0 there)
+      const float p1 = idx[0] < 0 || top[0] == -INFINITY ? 0.f : expf(top[0] - lse);
+      add[0] = p1 * dw[0];
+      minus = add[0];
+    } else if (idx[0] >= 0 && idx[1] >= 0 && idx[0] != idx[1] &&
+               !(top[0] == -INFINITY && top[1] == -INFINITY)) {
+      const float hi = fmaxf(top[0], top[1]);
+      const float e0 = expf(top[0] - hi), e1 = expf(top[1] - hi);
+      const float inv = 1.f / (e0 + e1);
+      add[0] = (e0 * inv) * (e1 * inv) * (dw[0] - dw[1]);
+      add[1] = -add[0];
+    }
+  }
+  const float c0 = gz * lse - bar;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int c = col_of<LANES, VEC>(j, l);
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      const float p = x[VEC * j + v];
+      float r = d.dlosses ? p * (a[VEC * j + v] + c0) : 0.f;
+      if (d.dtopk_w) {
+        r -= p * minus;
+        if (c + v == idx[0]) r += add[0];
+        if (c + v == idx[1]) r += add[1];
+      }
+      x[VEC * j + v] = r;
+    }
+  }
+}
+
+template <int LANES, int VEC, int J>
+__device__ __forceinline__ void store_row(const DlArgs& d, int64_t t, int l, const float (&q)[VEC * J]) {
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int c = col_of<LANES, VEC>(j, l);
+    if (c >= d.E) continue;
+    float* dst = d.dlogits + (size_t)t * d.E + c;
+    if (VEC == 4)
+      *reinterpret_cast<float4*>(dst) =
+          make_float4(q[VEC * j], q[VEC * j + 1 % VEC], q[VEC * j + 2 % VEC], q[VEC * j + 3 % VEC]);
+    else
+      dst[0] = q[j];
+  }
+}
+
 // Gradient of the logits, one row per group of lanes.  Rows are taken from the last to the
 // first: right after moe_balance_loss the rows that it read last are still in L2.
 template <int LANES, int VEC, int J>
-__global__ void __launch_bounds__(256) dlogits_kernel(
-    const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
-    const float* __restrict__ dtopk_w, const float* __restrict__ dlosses,
-    const int32_t* __restrict__ counts, const int32_t* __restrict__ n_valid,
-    const uint8_t* __restrict__ mask, int T, int E, int k, float* __restrict__ dlogits,
-    int* __restrict__ status) {
-  if (status && blockIdx.x == 0 && threadIdx.x == 0) *status = kOk;
-  constexpr int V = VEC * J;
+__global__ void __launch_bounds__(256) dlogits_kernel(const DlArgs d) {
+  if (d.status && blockIdx.x == 0 && threadIdx.x == 0) *d.status = kOk;
   constexpr int RPW = 32 / LANES;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int l = lane % LANES, g = lane / LANES;
-  float a[V];
-  float gz = 0.f;
-  if (dlosses) {
-    const float n = (float)max(*n_valid, 1);
-    const float cb = dlosses[0] * (float)E / (n * (float)k) / n;
-    gz = 2.f * dlosses[1] / n;
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const int e = col_of<LANES, VEC>(j, l) + v;
-        a[VEC * j + v] = e < E ? cb * (float)counts[e] : 0.f;
-      }
-  }
+  float a[VEC * J];
+  const float gz = loss_factors<LANES, VEC, J>(d, l, a);
   const int64_t stride = (int64_t)gridDim.x * 8 * RPW;
-  for (int64_t base = ((int64_t)blockIdx.x * 8 + w) * RPW; base < T; base += stride) {
-    const int64_t t = T - 1 - (base + g);
-    const bool in = t >= 0;
-    const bool on = in && (!mask || mask[t]);
-    float x[V];
-    load_row<LANES, VEC, J>(logits + (on ? t : 0) * E, E, l, on, x);
-    float top[2] = {0.f, 0.f}, dw[2] = {0.f, 0.f};
-    int idx[2] = {-1, -1};
-    if (dtopk_w && on) {
-      for (int j = 0; j < k; ++j) {
-        const int e = topk_idx[(size_t)t * k + j];
-        if ((unsigned)e < (unsigned)E) {
-          idx[j] = e;
-          top[j] = logits[(size_t)t * E + e];
-          dw[j] = dtopk_w[(size_t)t * k + j];
-        }
-      }
-    }
-    const float lse = softmax_row<LANES>(x);                 // x is p now
-    float bar = 0.f;
-    if (dlosses) {
+  for (int64_t base = ((int64_t)blockIdx.x * 8 + w) * RPW; base < d.T; base += stride) {
+    const int64_t t = d.T - 1 - (base + g);
+    const bool in = t >= 0, on = in && (!d.mask || d.mask[t]);
+    float x[VEC * J];
+    load_row<LANES, VEC, J>(d.logits + (on ? t : 0) * d.E, d.E, l, on, x);
+    row_gradient<LANES, VEC, J>(d, t, on, l, a, gz, x);
+    if (in) store_row<LANES, VEC, J>(d, t, l, x);
+  }
+}
+
+// The same with the f16 parts that the tensor-core form of the gate's gradient multiplies
+// (gate_grad.cu): a block takes 128 rows, keeps their gradients in registers until it knows their
+// largest magnitude, and writes them in 32 bits and as (hi, lo) with v = (hi + 2^-11 lo) 2^e.
+// Blocks beyond the rows round Wg to f16 by 128 rows and one power of two.
+struct SplitOut {
+  __half* dl2;                 // [T][2 Ep]: hi, lo; columns beyond E are zero
+  float* sT;                   // [T / 128]
+  const float* Wg;             // [d, E], or null
+  __half* W2;                  // [d][Ep]
+  float* sW;                   // [d / 128]
+  int d, Ep, nT;
+};
+constexpr int kSplitThreads = 512;
+
+// Largest magnitude in the block; infinity when any value is infinite or NaN.
+__device__ __forceinline__ float block_max(float m, float* scratch) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) bar += a[i] * x[i];
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kSplitThreads / 32; ++q) m = fmaxf(m, scratch[q]);
+  return m;
+}
+__device__ __forceinline__ float magnitude(float v) { return v - v == 0.f ? fabsf(v) : INFINITY; }
+
+template <int LANES, int VEC, int J>
+__global__ void __launch_bounds__(kSplitThreads) dlogits_split_kernel(const DlArgs d, const SplitOut o) {
+  constexpr int V = VEC * J, RPW = 32 / LANES;
+  constexpr int kPass = kSplitThreads / 32 * RPW;            // rows per pass
+  constexpr int NP = kPass >= kGateBlock ? 1 : kGateBlock / kPass;
+  __shared__ float scratch[kSplitThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  pdl_trigger();
+  if ((int)blockIdx.x >= o.nT) {
+    const int blk = blockIdx.x - o.nT, rows = min(kGateBlock, o.d - blk * kGateBlock);
+    const float* src = o.Wg + (size_t)blk * kGateBlock * d.E;
+    __half* dst = o.W2 + (size_t)blk * kGateBlock * o.Ep;
+    float m = 0.f;
+#pragma unroll 4
+    for (int q = tid; q < rows * d.E; q += kSplitThreads) m = fmaxf(m, magnitude(src[q]));
+    m = block_max(m, scratch);
+    const int e = scale_exp(m);
+    const float inv = exp2_int(-e);
+#pragma unroll 4
+    for (int q = tid; q < rows * o.Ep; q += kSplitThreads) {
+      const int r = q / o.Ep, c = q - r * o.Ep;
+      dst[q] = __float2half_rn(c < d.E ? src[(size_t)r * d.E + c] * inv : 0.f);
     }
-    bar = group_sum<LANES>(bar);
-    // top-1: w = p[e1];  top-2: w_j = p[e_j] / (p[e1] + p[e2]), a softmax over the two logits
-    float add[2] = {0.f, 0.f}, minus = 0.f;
-    if (dtopk_w) {
-      if (k == 1) {
-        // a row of -inf only has no weight to differentiate (p = 0 there)
-        const float p1 = idx[0] < 0 || top[0] == -INFINITY ? 0.f : expf(top[0] - lse);
-        add[0] = p1 * dw[0];
-        minus = add[0];
-      } else if (idx[0] >= 0 && idx[1] >= 0 && idx[0] != idx[1] &&
-                 !(top[0] == -INFINITY && top[1] == -INFINITY)) {
-        const float hi = fmaxf(top[0], top[1]);
-        const float e0 = expf(top[0] - hi), e1 = expf(top[1] - hi);
-        const float inv = 1.f / (e0 + e1);
-        add[0] = (e0 * inv) * (e1 * inv) * (dw[0] - dw[1]);
-        add[1] = -add[0];
-      }
-    }
-    const float c0 = gz * lse - bar;
+    if (tid == 0) o.sW[blk] = exp2_int(e);
+    return;
+  }
+  if (d.status && blockIdx.x == 0 && tid == 0) *d.status = kOk;
+  const int l = lane % LANES, g = lane / LANES;
+  float a[V];
+  const float gz = loss_factors<LANES, VEC, J>(d, l, a);
+  const int row0 = blockIdx.x * kGateBlock;
+  float x[NP][V];
+  float m = 0.f;
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int r = p * kPass + w * RPW + g;
+    const int64_t t = (int64_t)row0 + r;
+    const bool on = r < kGateBlock && t < d.T && (!d.mask || d.mask[t]);
+    load_row<LANES, VEC, J>(d.logits + (on ? t : 0) * d.E, d.E, l, on, x[p]);
+  }
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int r = p * kPass + w * RPW + g;
+    const int64_t t = (int64_t)row0 + r;
+    const bool in = r < kGateBlock && t < d.T, on = in && (!d.mask || d.mask[t]);
+    row_gradient<LANES, VEC, J>(d, t, on, l, a, gz, x[p]);
+    if (in) store_row<LANES, VEC, J>(d, t, l, x[p]);
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = fmaxf(m, magnitude(x[p][i]));
+  }
+  m = block_max(m, scratch);
+  const int e = scale_exp(m);                 // 0 for a block with infinities or NaN
+  const float inv = exp2_int(-e);
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int r = p * kPass + w * RPW + g;
+    const int64_t t = (int64_t)row0 + r;
+    if (r >= kGateBlock || t >= d.T) continue;
+    __half* dst = o.dl2 + t * 2 * o.Ep;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int c = col_of<LANES, VEC>(j, l);
-      if (!in || c >= E) continue;
-      float q[VEC];
+      if (c >= o.Ep) continue;
+      __half hi[VEC], lo[VEC];
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        const float p = x[VEC * j + v];
-        float r = dlosses ? p * (a[VEC * j + v] + c0) : 0.f;
-        if (dtopk_w) {
-          r -= p * minus;
-          if (c + v == idx[0]) r += add[0];
-          if (c + v == idx[1]) r += add[1];
-        }
-        q[v] = r;
+        const float f = c + v < d.E ? x[p][VEC * j + v] * inv : 0.f;
+        hi[v] = __float2half_rn(f);
+        const float h = __half2float(hi[v]);
+        lo[v] = isfinite(h) ? __float2half_rn((f - h) * kGateLo) : __ushort_as_half(0);
       }
-      float* dst = dlogits + (size_t)t * E + c;
-      if (VEC == 4)
-        *reinterpret_cast<float4*>(dst) = make_float4(q[0], q[1 % VEC], q[2 % VEC], q[3 % VEC]);
-      else
-        dst[0] = q[0];
+      if (VEC == 4) {
+        *reinterpret_cast<uint2*>(dst + c) = *reinterpret_cast<const uint2*>(hi);
+        *reinterpret_cast<uint2*>(dst + o.Ep + c) = *reinterpret_cast<const uint2*>(lo);
+      } else {
+        dst[c] = hi[0];
+        dst[o.Ep + c] = lo[0];
+      }
     }
+    // columns up to Ep that no lane's values cover
+    for (int c = LANES * V + l; c < o.Ep; c += LANES) dst[c] = dst[o.Ep + c] = __ushort_as_half(0);
   }
+  if (tid == 0) o.sT[blockIdx.x] = exp2_int(e);
 }
 
 int sm_count() {
@@ -487,12 +624,29 @@ cudaError_t launch_dlogits(const float* logits, const int32_t* topk_idx, const f
                            cudaStream_t s) {
   const int sms = sm_count();
   if (sms < 1) return cudaErrorInvalidDevice;
+  const DlArgs d{logits, topk_idx, dtopk_w, dlosses, counts, n_valid, mask, T, E, k, dlogits, status};
   const int rows = 8 * (32 / lanes_for(E));
   const int grid = std::max(1, std::min((T + rows - 1) / rows, 8 * sms));
   return with_shape(E, [&](auto lanes, auto vec, auto j) -> cudaError_t {
     constexpr int L = decltype(lanes)::value, V = decltype(vec)::value, J = decltype(j)::value;
-    return launch_k(dlogits_kernel<L, V, J>, grid, 256, 0, s, false, logits, topk_idx, dtopk_w,
-                    dlosses, counts, n_valid, mask, T, E, k, dlogits, status);
+    return launch_k(dlogits_kernel<L, V, J>, grid, 256, 0, s, false, d);
+  });
+}
+
+cudaError_t launch_dlogits_split(const float* logits, const int32_t* topk_idx, const float* dtopk_w,
+                                 const float* dlosses, const int32_t* counts, const int32_t* n_valid,
+                                 const uint8_t* mask, int T, int E, int k, float* dlogits, int* status,
+                                 const float* Wg, int d, int Ep, __half* dl2, float* sT, __half* W2,
+                                 float* sW, cudaStream_t s) {
+  const DlArgs a{logits, topk_idx, dtopk_w, dlosses, counts, n_valid, mask, T, E, k, dlogits, status};
+  const SplitOut o{dl2, sT, Wg, W2, sW, d, Ep, (T + kGateBlock - 1) / kGateBlock};
+  const int grid = o.nT + (Wg ? (d + kGateBlock - 1) / kGateBlock : 0);
+  return with_shape(E, [&](auto lanes, auto vec, auto j) -> cudaError_t {
+    constexpr int L = decltype(lanes)::value, V = decltype(vec)::value, J = decltype(j)::value;
+    if constexpr (L > 16)
+      return cudaErrorInvalidValue;               // E > 256 takes the other form
+    else
+      return launch_k(dlogits_split_kernel<L, V, J>, grid, kSplitThreads, 0, s, false, a, o);
   });
 }
 

@@ -126,24 +126,25 @@ moe_status moe_gate_topk_backward(const float* logits, const int32_t* topk_idx, 
     if (st != MOE_OK) return st;
     if (!workspace || ws_bytes < need) return MOE_ERR_WORKSPACE;
   }
-  MOE_TRY(launch_dlogits(logits, topk_idx, dtopk_w, dlosses, counts, n_valid, token_mask, T, E, k,
-                         dlogits, deep ? static_cast<int*>(workspace) : nullptr, s));
-  if (!deep) return MOE_OK;
   const int f16 = dtype == MOE_F16;
   uint8_t* ws = static_cast<uint8_t*>(workspace) + kAlign;
+  int* status = deep ? static_cast<int*>(workspace) : nullptr;
   // Masked tokens may hold anything: their rows are left out of dWg's sums row by row, which the
   // tensor-core form's boxes of rows cannot do.  (It needs no mask for dtokens: dlogits are zero.)
-  const bool tc = f16 && gate_tc_ok(E);
-  float* dWg_rows = dWg && (!tc || token_mask) ? dWg : nullptr;
-  if (dWg_rows)
-    MOE_TRY(launch_row_sums(tokens, dlogits, dWg, d, E, 0, nullptr, nullptr, nullptr, 0, 0, 0, nullptr,
-                            nullptr, nullptr, token_mask, ws, f16, T, T, 1, /*pdl=*/true, s));
-  if (tc && (dtokens || !dWg_rows))
-    MOE_TRY(launch_gate_tc(static_cast<const __half*>(tokens), Wg, dlogits, dWg_rows ? nullptr : dWg,
+  const bool tc = deep && f16 && gate_tc_ok(E) && (dtokens || !token_mask);
+  float* dWg_tc = tc && !token_mask ? dWg : nullptr;
+  if (tc)
+    MOE_TRY(launch_gate_tc(logits, topk_idx, dtopk_w, dlosses, counts, n_valid, token_mask, k, dlogits,
+                           static_cast<const __half*>(tokens), Wg, dWg_tc,
                            static_cast<const __half*>(dtokens_in), static_cast<__half*>(dtokens), ws,
-                           static_cast<int*>(workspace), T, d, E, s));
-  else if (dtokens)
-    MOE_TRY(launch_gate_dx(dlogits, Wg, dtokens_in, f16, T, d, E, dtokens, s));
+                           status, T, d, E, s));
+  else
+    MOE_TRY(launch_dlogits(logits, topk_idx, dtopk_w, dlosses, counts, n_valid, token_mask, T, E, k,
+                           dlogits, status, s));
+  if (dWg && !dWg_tc)
+    MOE_TRY(launch_row_sums(tokens, dlogits, dWg, d, E, 0, nullptr, nullptr, nullptr, 0, 0, 0, nullptr,
+                            nullptr, nullptr, token_mask, ws, f16, T, T, 1, /*pdl=*/!tc, s));
+  if (dtokens && !tc) MOE_TRY(launch_gate_dx(dlogits, Wg, dtokens_in, f16, T, d, E, dtokens, s));
   return MOE_OK;
 }
 

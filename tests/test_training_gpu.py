@@ -276,12 +276,13 @@ def test_gate_backward(m, dt, T, d, E, k, form):
         mag = dd.abs() @ Wg.double().abs().t()
         if dx_in is not None:
             want, mag = want + dx_in.double(), mag + dx_in.double().abs()
-        # E additions; f16: operands good to 2^-23 of themselves and 2^-36 of the largest value of
-        # their 128 rows, and 2^-22 of a product left out
+        # E additions; f16: dl good to 2^-23 of itself and 2^-36 of the largest value of its 128 rows,
+        # Wg rounded to f16 once (2^-11; 2^-25 of the largest of 128 rows below f16's range)
         block = lambda v: torch.cat([c.abs().amax().expand(len(c)) for c in v.split(128)])
-        slack = block(dd)[:, None] * Wg.double().abs().sum(1) + \
-            dd.abs().sum(1, keepdim=True) * block(Wg.double())
-        tol = (2 * E + 64) * U * mag + 2.0 ** -36 * slack + torch.finfo(dt).eps / 2 * want.abs()
+        slack = 2.0 ** -36 * block(dd)[:, None] * Wg.double().abs().sum(1) + \
+            2.0 ** -25 * dd.abs().sum(1, keepdim=True) * block(Wg.double())
+        K = 2 * E + 64 + (2 ** 13 if dt == torch.float16 else 0)
+        tol = K * U * mag + slack + torch.finfo(dt).eps / 2 * want.abs()
         check(dx, want, tol + (2.0 ** -25 if dt == torch.float16 else 1e-37), "dtokens")
 
 
@@ -673,7 +674,7 @@ def test_training_step_of_router_and_adapters(m, T, d, r, N, E, k):
     gx, gW, gA, gB = torch.autograd.grad(total, (x, Wg, A, B), retain_graph=True)
     (gx_adapter,) = torch.autograd.grad((delta * c["dout"].double()[on]).sum(), x)
     gx_gate = gx - gx_adapter
-    assert abs(float(b["losses"][0]) - float(bal)) < 1e-5 and abs(float(b["losses"][1]) - float(z)) < 1e-4
+    assert abs(float(b["losses"][0]) - bal.item()) < 1e-5 and abs(float(b["losses"][1]) - z.item()) < 1e-4
     # out is rounded twice, after the combine and after the adapter (rows without one: once), dtokens
     # after the gate and after the adapter; 32-bit sums of a row's terms add less than 2^-16 of its
     # largest value.  dlogits come from logits of 32 bits (d products: 2^-24 d of their magnitudes).
@@ -682,13 +683,14 @@ def test_training_step_of_router_and_adapters(m, T, d, r, N, E, k):
     hmag = torch.einsum("ti,tij->tj", c["x"].double()[on], c["A"].double()[ids_on]).abs()
     dhmag = torch.einsum("to,tjo->tj", c["dout"].double()[on], c["B"].double()[ids_on]).abs()
     sc = c["scale"].double()[ids_on][:, None]
-    # h (and dh) rounded to f16 before the second product
+    # h (and dh) rounded to f16 before the second product, Wg before the gate's
+    gate_h = b["dl"].double().abs() @ c["Wg"].double().abs().t()
     out_h, dx_h = torch.zeros_like(out), torch.zeros_like(gx)
     out_h[on] = sc * torch.einsum("tj,tjo->to", hmag, c["B"].double()[ids_on].abs())
     dx_h[on] = sc * torch.einsum("tj,tij->ti", dhmag, c["A"].double()[ids_on].abs())
     row = lambda v: 2.0 ** -16 * v.abs().amax(1, keepdim=True) + 2.0 ** -24
     check(b["out"], out, half * (comb.abs() + out.abs() + out_h) + row(out), "out")
-    check(b["dx"], gx, half * (gx_gate.abs() + gx.abs() + dx_h) + row(gx), "dx")
+    check(b["dx"], gx, half * (gx_gate.abs() + gx.abs() + dx_h + gate_h) + row(gx), "dx")
     for name, want in (("dWg", gW), ("dA", gA), ("dB", gB)):
         check(b[name], want, 2.0 ** -14 * want.abs().max(), name)
 
