@@ -291,21 +291,34 @@ def _code(dtype) -> int:
     return MOE_F16 if dtype == torch.float16 else MOE_F32
 
 
+_fns = {}
+
+
 def _call(where, dev, stream, *args):
     """The library call on device `dev`: its current stream unless one is given."""
     import torch
+    fn = _fns.get(where)
+    if fn is None:
+        fn = _fns[where] = getattr(get_lib(), where)
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        handle = _raw_stream(dev)
     elif stream.device_index != dev:
         raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on cuda:{dev}")
-    fn = getattr(get_lib(), where)
-    if torch.cuda.current_device() == dev:
-        code = fn(*args, stream.cuda_stream)
+    else:
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        code = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            code = fn(*args, stream.cuda_stream)
+            code = fn(*args, handle)
     if code != MOE_OK:
         raise MoeError(code, where)
+
+
+def _raw_stream(dev):
+    """Handle of the device's current stream, without the stream object around it."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def moe_balance_workspace_size(T, E) -> int:

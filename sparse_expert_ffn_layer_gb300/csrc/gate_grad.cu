@@ -260,10 +260,12 @@ struct DxArgs {
   int* status;
 };
 constexpr int kTile = 16384;                        // 128 rows x 64 columns
-constexpr int kDxB = 4;                             // stages of Wg: 64 experts each
 template <int NKB>                                  // chunks of 64 experts
 struct DxPlan {
-  static constexpr int kIo = NKB <= 2 ? 2 : 1;      // in/out tiles of 128 x 128
+  static constexpr int kDxB = NKB <= 2 ? 4 : 2;     // stages of Wg: 64 experts each
+  // In/out tiles of 128 x 128: one being added to, one being written, the others loading (with two
+  // in all, every tile waited for its load).
+  static constexpr int kIo = NKB == 1 ? 4 : NKB == 2 ? 3 : 2;
   static constexpr int kOffB = NKB * 2 * kTile, kOffIo = kOffB + kDxB * kTile;
   static constexpr int kOffBar = kOffIo + kIo * 2 * kTile;
   static constexpr int kBytes = kOffBar + 256 + 1024;
@@ -275,13 +277,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap mIn, const __grid_constant__ CUtensorMap mOut,
                       const DxArgs a) {
   using PL = DxPlan<NKB>;
-  constexpr int IO = PL::kIo;
+  constexpr int IO = PL::kIo, kDxB = PL::kDxB;
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + PL::kOffBar);
-  uint64_t *a_full = bar, *a_empty = bar + 1, *io_full = bar + 2, *io_empty = bar + 4, *acc_full = bar + 6,
-           *acc_empty = bar + 8, *b_full = bar + 10, *b_empty = b_full + kDxB;
-  uint32_t* holder = reinterpret_cast<uint32_t*>(b_empty + kDxB);
+  uint64_t *a_full = bar, *a_empty = bar + 1, *acc_full = bar + 2, *acc_empty = bar + 4, *b_full = bar + 6,
+           *b_empty = b_full + kDxB, *io_full = b_empty + kDxB, *io_empty = io_full + IO;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(io_empty + IO);
   int* flag = reinterpret_cast<int*>(holder + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
@@ -291,9 +293,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&b_full[s], 1);
       mbar_init(&b_empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < IO; ++s) {
       mbar_init(&io_full[s], 1);
       mbar_init(&io_empty[s], 2);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&acc_full[s], 1);
       mbar_init(&acc_empty[s], 256);
     }
@@ -445,12 +449,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int x = i * 128 + 64 * ch;
           if (x < a.d) tma_store_2d(&mOut, x, t * 128, sm + PL::kOffIo + (io * 2 + ch) * kTile);
           bulk_commit();
-          if (IO == 1) {
-            bulk_wait_read<0>();
-            mbar_arrive(&io_empty[0]);
-          } else if (tile > 0) {                    // the tile before is out: its buffer is free
+          if (tile > 0) {                           // the tile before is out: its buffer is free
             bulk_wait_read<1>();
-            mbar_arrive(&io_empty[io ^ 1]);
+            mbar_arrive(&io_empty[io == 0 ? IO - 1 : io - 1]);
           }
         }
         if (++io == IO) {

@@ -68,7 +68,9 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, i
   }
 }
 
-// Softmax in place: x becomes p; returns lse.  A row of -inf only has p = 0 and lse = 0 (it
+// Softmax in place: x becomes p; returns lse.  The exponentials are the hardware's (2 ulp and
+// 2^-23 of |x - m| relative: small where p matters); with expf the arithmetic, not DRAM, bound the
+// pass over 262144 x 128 logits (31 us instead of %ROWS%).  A row of -inf only has p = 0 and lse = 0 (it
 // adds nothing to either loss); NaN and +inf give NaN as the formula does.
 template <int LANES, int N>
 __device__ __forceinline__ float softmax_row(float (&x)[N]) {
@@ -80,7 +82,7 @@ __device__ __forceinline__ float softmax_row(float (&x)[N]) {
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    x[i] = expf(x[i] - m);
+    x[i] = __expf(x[i] - m);
     s += x[i];
   }
   s = group_sum<LANES>(s);
@@ -329,10 +331,22 @@ __device__ __forceinline__ void row_gradient(const DlArgs& d, int64_t t, bool on
       const int e = d.topk_idx[(size_t)t * d.k + j];
       if ((unsigned)e < (unsigned)d.E) {
         idx[j] = e;
-        top[j] = d.logits[(size_t)t * d.E + e];
         dw[j] = d.dtopk_w[(size_t)t * d.k + j];
       }
     }
+  }
+  // the chosen experts' logits, from the lane that holds them
+  if (d.dtopk_w) {
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const int c = col_of<LANES, VEC>(j, l) + v;
+        if (c == idx[0]) top[0] = x[VEC * j + v];
+        if (c == idx[1]) top[1] = x[VEC * j + v];
+      }
+    top[0] = group_sum<LANES>(top[0]);
+    top[1] = group_sum<LANES>(top[1]);
   }
   const float lse = softmax_row<LANES>(x);                   // x is p now
   float bar = 0.f;
@@ -450,16 +464,47 @@ __global__ void __launch_bounds__(kSplitThreads) dlogits_split_kernel(const DlAr
     const int blk = blockIdx.x - o.nT, rows = min(kGateBlock, o.d - blk * kGateBlock);
     const float* src = o.Wg + (size_t)blk * kGateBlock * d.E;
     __half* dst = o.W2 + (size_t)blk * kGateBlock * o.Ep;
+    constexpr int NQ = kGateBlock * 16 * LANES / VEC / kSplitThreads > 0
+                           ? kGateBlock * 16 * LANES / VEC / kSplitThreads : 1;
+    float v[NQ][VEC];                              // every value of the block, read once
+    const int ne = d.E / VEC;
     float m = 0.f;
-#pragma unroll 4
-    for (int q = tid; q < rows * d.E; q += kSplitThreads) m = fmaxf(m, magnitude(src[q]));
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int q = tid + i * kSplitThreads;
+#pragma unroll
+      for (int u = 0; u < VEC; ++u) v[i][u] = 0.f;
+      if (q < rows * ne) {
+        if (VEC == 4)
+          *reinterpret_cast<float4*>(v[i]) = *reinterpret_cast<const float4*>(src + 4 * q);
+        else
+          v[i][0] = src[q];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+#pragma unroll
+      for (int u = 0; u < VEC; ++u) m = fmaxf(m, magnitude(v[i][u]));
     m = block_max(m, scratch);
     const int e = scale_exp(m);
     const float inv = exp2_int(-e);
-#pragma unroll 4
-    for (int q = tid; q < rows * o.Ep; q += kSplitThreads) {
-      const int r = q / o.Ep, c = q - r * o.Ep;
-      dst[q] = __float2half_rn(c < d.E ? src[(size_t)r * d.E + c] * inv : 0.f);
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int q = tid + i * kSplitThreads;
+      if (q >= rows * ne) continue;
+      const int r = q / ne;
+      __half* p = dst + r * o.Ep + (q - r * ne) * VEC;
+      if (VEC == 4) {
+        __half2 h[2] = {__floats2half2_rn(v[i][0] * inv, v[i][1 % VEC] * inv),
+                        __floats2half2_rn(v[i][2 % VEC] * inv, v[i][3 % VEC] * inv)};
+        *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(h);
+      } else {
+        p[0] = __float2half_rn(v[i][0] * inv);
+      }
+    }
+    for (int q = tid; q < rows * (o.Ep - d.E); q += kSplitThreads) {
+      const int r = q / (o.Ep - d.E);
+      dst[r * o.Ep + d.E + q - r * (o.Ep - d.E)] = __ushort_as_half(0);
     }
     if (tid == 0) o.sW[blk] = exp2_int(e);
     return;
