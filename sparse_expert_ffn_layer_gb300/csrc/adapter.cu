@@ -98,7 +98,11 @@ constexpr int kChunk = 64;                        // columns per chunk
 
 template <int R>
 struct PlanTall {
-  static constexpr int kStage = kTallRows * 128 + kChunk * R * 2;  // rows, weights
+  // Chunks per stage of the ring: two for low ranks, where what a stage costs beside its products
+  // (waits, addresses) was most of the instructions.
+  static constexpr int kSub = R <= 32 ? 2 : 1;
+  static constexpr int kSubB = kTallRows * 128 + kChunk * R * 2;   // rows, weights
+  static constexpr int kStage = kSub * kSubB;
   static constexpr int kStages = (96 * 1024) / kStage;             // two blocks per SM
   static constexpr int kOffBar = kStages * kStage;
   static constexpr int kOffTab = kOffBar + 16 * kStages;           // abort flag, group table
@@ -175,27 +179,35 @@ struct TallRing {
   // The next chunk, into the stage whose turn it is (all threads).
   __device__ __forceinline__ void issue() {
     if (li >= items) return;
-    const int col = lc * kChunk;
+    const int col = lc * (PL::kSub * kChunk);
     uint8_t* st = sm + lstage * PL::kStage;
     wait(&empty[lstage], lphase);
     if (threadIdx.x == 0 && !*abort) {            // (no further loads after a wait gave up)
-      mbar_expect_tx(&full[lstage], kChunk * R * 2);
-      uint8_t* ws = st + MT * 128;
-      if (kWide) {
+      mbar_expect_tx(&full[lstage], PL::kSub * kChunk * R * 2);
 #pragma unroll
-        for (int b = 0; b < R; b += RB) tma_load_3d(ws + b * kChunk * 2, mW, b, col, ln, &full[lstage]);
-      } else {
-        tma_load_3d(ws, mW, col, 0, ln, &full[lstage]);
+      for (int u = 0; u < PL::kSub; ++u) {        // (behind the last column: zeros)
+        uint8_t* ws = st + u * PL::kSubB + MT * 128;
+        if (kWide) {
+#pragma unroll
+          for (int b = 0; b < R; b += RB)
+            tma_load_3d(ws + b * kChunk * 2, mW, b, col + u * kChunk, ln, &full[lstage]);
+        } else {
+          tma_load_3d(ws, mW, col + u * kChunk, 0, ln, &full[lstage]);
+        }
       }
     }
     if (rows) {
       const int row = threadIdx.x >> 3, pc = threadIdx.x & 7;
-      const bool in = col + pc * 8 < d;
+      const uint32_t dst = smem_u32(st) + row * 128 + ((pc ^ (row & 7)) << 4);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const bool on = in && (unsigned)lrow[q] < (unsigned)T;
-        cp_async16(st + (row + 32 * q) * 128 + ((pc ^ (row & 7)) << 4),
-                   rows + (on ? (size_t)lrow[q] * d + col + pc * 8 : 0), on);
+        const bool there = (unsigned)lrow[q] < (unsigned)T;
+        const __half* src = rows + (there ? (uint64_t)(uint32_t)lrow[q] * (uint32_t)d + col + pc * 8 : 0);
+#pragma unroll
+        for (int u = 0; u < PL::kSub; ++u) {
+          const bool on = there && col + u * kChunk + pc * 8 < d;
+          cp_async16_at(dst + q * 32 * 128 + u * PL::kSubB, on ? src + u * kChunk : rows, on);
+        }
       }
       cp_async_arrive(&full[lstage]);
     }
@@ -263,6 +275,7 @@ template <int R, bool kT>
 __global__ void __launch_bounds__(kTallThreads, 2)
     adapter_shrink_kernel(const __grid_constant__ CUtensorMap mP, const TallArgs ta) {
   const AdapterArgs& a = ta.a;
+  using PL = PlanTall<R>;
   constexpr int MT = kTallRows, RB = R > 64 ? 64 : R;
   constexpr int WN = R >= 32 ? 2 : 1, WK = 2 / WN;   // two warps per 16 rows: along r, or the chunk
   constexpr int NF = R / WN / 8;                     // 8-column fragments of h per warp
@@ -278,7 +291,7 @@ __global__ void __launch_bounds__(kTallThreads, 2)
   ring.d = a.dk;
   ring.mW = &mP;
   const int ntiles = tall_setup(ring, a, raw);
-  ring.chunks = (a.dk + kChunk - 1) / kChunk;
+  ring.chunks = (a.dk + PL::kSub * kChunk - 1) / (PL::kSub * kChunk);
   ring.parts = ta.parts_k;
   ring.items = ntiles * ring.parts;
   ring.blocks = gridDim.x - 1;
@@ -297,7 +310,10 @@ __global__ void __launch_bounds__(kTallThreads, 2)
       for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
     const int c1 = ring.part_begin(part + 1);
     for (int c = ring.part_begin(part); c < c1; ++c) {
-      const uint8_t* xs = ring.next();
+      const uint8_t* st = ring.next();
+#pragma unroll
+      for (int u = 0; u < PL::kSub; ++u) {
+      const uint8_t* xs = st + u * PL::kSubB;
       const uint8_t* ps = xs + MT * 128;
       // The tensor cores' additions truncate: a chain of n of them loses up to n / 2^23 of the
       // sum, always towards zero.  Chains end with every chunk and are added with rounding
@@ -325,11 +341,12 @@ __global__ void __launch_bounds__(kTallThreads, 2)
           mma16816(run[2 * j + 1], fa, fb[2], fb[3]);
         }
       }
-      ring.done();
+      if (u == PL::kSub - 1) ring.done();
 #pragma unroll
       for (int i = 0; i < NF; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] += run[i][j];
+      }
     }
     if (WK > 1) {                                 // the two warps of the same rows
       float* p = pair + (wr + (lane >> 2)) * R + 2 * (lane & 3);
@@ -371,6 +388,7 @@ template <int R, bool kT>
 __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
     adapter_expand_kernel(const __grid_constant__ CUtensorMap mQ, const TallArgs ta) {
   const AdapterArgs& a = ta.a;
+  using PL = PlanTall<R>;
   constexpr int MT = kTallRows, RB = R > 64 ? 64 : R;
   extern __shared__ uint8_t raw[];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -380,7 +398,7 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
   ring.d = a.dn;
   ring.mW = &mQ;
   const int ntiles = tall_setup(ring, a, raw);
-  ring.chunks = (a.dn + kChunk - 1) / kChunk;
+  ring.chunks = (a.dn + PL::kSub * kChunk - 1) / (PL::kSub * kChunk);
   ring.parts = ta.parts_n;
   ring.items = ntiles * ring.parts;
   ring.blocks = gridDim.x;
@@ -467,7 +485,10 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
     // ---- 32 of a chunk's 64 columns per warp
     const int c1 = ring.part_begin(part + 1);
     for (int c = ring.part_begin(part); c < c1; ++c) {
-      uint8_t* bs = ring.next();
+      uint8_t* st = ring.next();
+#pragma unroll
+      for (int u = 0; u < PL::kSub; ++u) {
+      uint8_t* bs = st + u * PL::kSubB;
       const uint8_t* qs = bs + MT * 128;
       float acc[4][4];
 #pragma unroll
@@ -495,16 +516,16 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
         if (with_base) ldsm4(b, at);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {             // b[q]: rows + 8 (q & 1), columns + 8 (q >> 1)
-          const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&b[q]));
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&b[q]));
           const float mm = q & 1 ? m1 : m0;
-          const __half2 o = __floats2half2_rn(fmaf(mm, acc[2 * j + (q >> 1)][2 * (q & 1)], u.x),
-                                              fmaf(mm, acc[2 * j + (q >> 1)][2 * (q & 1) + 1], u.y));
+          const __half2 o = __floats2half2_rn(fmaf(mm, acc[2 * j + (q >> 1)][2 * (q & 1)], f.x),
+                                              fmaf(mm, acc[2 * j + (q >> 1)][2 * (q & 1) + 1], f.y));
           b[q] = *reinterpret_cast<const uint32_t*>(&o);
         }
         stsm4(at, b);
       }
       __syncwarp();
-      const int col = c * kChunk + ypc * 8;
+      const int col = (c * PL::kSub + u) * kChunk + ypc * 8;
       if (col < a.dn) {
         if (y0 >= 0)
           *reinterpret_cast<uint4*>(Y + (size_t)y0 * a.dn + col) =
@@ -512,6 +533,7 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
         if (y1 >= 0)
           *reinterpret_cast<uint4*>(Y + (size_t)y1 * a.dn + col) =
               *reinterpret_cast<const uint4*>(bs + swz<128>(yrow + 8, ypc));
+      }
       }
       ring.done();
     }

@@ -224,7 +224,10 @@ struct SumPlan {
   static constexpr int kStages = R == 64 ? 3 : 4;                  // two blocks per SM (R = 128: one)
 };
 
-template <int R>
+// kPerm: rows through perm.  Rows behind a segment's end and entries outside [0, T) then read some
+// row that is there; their h is zero.  Otherwise the rows are the slots, and masked ones read as
+// zeros (they may hold anything).
+template <int R, bool kPerm>
 __global__ void __launch_bounds__(kSumThreads, R >= 128 ? 1 : 2) row_sum_f16_kernel(const SumArgs a, int ldh) {
   constexpr int kLdH = SumPlan<R>::kLdH, NS = SumPlan<R>::kStages, kStage = SumPlan<R>::kStage;
   constexpr int MI = SumWarps<R>::MI, NJ = SumWarps<R>::NJ, WI = SumWarps<R>::WI;
@@ -237,11 +240,14 @@ __global__ void __launch_bounds__(kSumThreads, R >= 128 ? 1 : 2) row_sum_f16_ker
   const Segments g = segment_table(a, reinterpret_cast<int*>(ring + NS * kStage));
   const int items = g.count * (a.job[0].blocks + a.job[1].blocks);
   const int wi = (w % WI) * MI * 16, wj = (w / WI) * NJ * 8;
+  const uint32_t ring_at = smem_u32(ring);
+  // this lane's row of a fragment load: x transposed (rows = summed index), h as it lies
+  const uint32_t xlane = (((lane & 7) + (lane >> 4) * 8) * kLdX + wi + ((lane >> 3) & 1) * 8) * 2;
+  const uint32_t hlane = (kRows * kLdX + (lane & 15) * kLdH + wj + (lane >> 4) * 8) * 2;
 
   // ---- loads: chunk after chunk across the block's items, each chunk's rows fetched one early
   const int xc = (tid & 15) * 8, xr = tid >> 4;    // x: 16-byte piece, rows xr + 16 p
   int li = blockIdx.x, lc = 0, llo = 0, lhi = 0, ldi = 0, lrow[4];
-  uint8_t lmask[4] = {};
   const __half *lX = nullptr, *lH = nullptr;
   bool lin = false;
   int lw = 0;                                      // columns of h that there are
@@ -252,8 +258,8 @@ __global__ void __launch_bounds__(kSumThreads, R >= 128 ? 1 : 2) row_sum_f16_ker
     llo = it.lo;
     lhi = it.hi;
     ldi = it.jb->di;
-    lX = static_cast<const __half*>(it.jb->x) + it.i0 + xc;
-    lin = it.i0 + xc < ldi;
+    lin = it.i0 + xc < ldi;                        // columns behind the last are not stored
+    lX = static_cast<const __half*>(it.jb->x) + (lin ? it.i0 + xc : 0);
     lH = it.jb->split + (size_t)it.lo * 2 * ldh + it.j0;
     lw = min(R, ldh - it.j0);
   };
@@ -261,33 +267,37 @@ __global__ void __launch_bounds__(kSumThreads, R >= 128 ? 1 : 2) row_sum_f16_ker
   // for the load (a third of all stalls).
   auto fetch_rows = [&]() {
     if (li >= items) return;
+    const int s = llo + lc * kRows + xr;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      const int s = llo + lc * kRows + xr + 16 * p;
-      lrow[p] = s;
-      if (a.perm) lrow[p] = s < lhi ? a.perm[s] : -1;
-      if (a.mask) lmask[p] = s < lhi ? a.mask[s] : 0;
+      if (kPerm)
+        lrow[p] = a.perm[min(s + 16 * p, lhi - 1)];
+      else
+        lrow[p] = s + 16 * p < lhi && (!a.mask || a.mask[s + 16 * p]) ? s + 16 * p : -1;
     }
   };
   auto load = [&](int stage) {
     if (li < items) {
-      const unsigned limit = a.perm ? a.T : lhi;
-      __half* st = ring + stage * kStage;
-      __half* dst = st + xr * kLdX + xc;
+      const uint32_t st = ring_at + stage * (kStage * 2), dst = st + (xr * kLdX + xc) * 2;
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        const bool on = lin && (unsigned)lrow[p] < limit && (!a.mask || lmask[p]);
-        cp_async16(dst + 16 * p * kLdX, on ? lX + (size_t)lrow[p] * ldi : lX, on);
+        if (kPerm) {
+          const uint32_t t = (unsigned)lrow[p] < (unsigned)a.T ? lrow[p] : 0;
+          cp_async16_at(dst + 16 * p * kLdX * 2, lX + (uint64_t)t * (uint32_t)ldi, true);
+        } else {
+          const bool on = lin && lrow[p] >= 0;
+          cp_async16_at(dst + 16 * p * kLdX * 2, on ? lX + (uint64_t)(uint32_t)lrow[p] * (uint32_t)ldi : lX, on);
+        }
       }
-      __half* hst = st + kRows * kLdX;
+      const uint32_t hst = st + kRows * kLdX * 2;
       const int left = lhi - llo - lc * kRows;     // rows of this and later chunks
-      const __half* src = lH + (size_t)lc * kRows * 2 * ldh;
+      const __half* src = lH + (uint64_t)(uint32_t)(lc * kRows * 2) * (uint32_t)ldh;
 #pragma unroll
       for (int p = 0; p < HP; ++p) {
         const int q = tid + p * kSumThreads;       // row, part, piece of R columns
         const int row = q / (R / 4), part = q / (R / 8) % 2, col = (q % (R / 8)) * 8;
         const bool on = row < left && col < lw;
-        cp_async16(hst + row * kLdH + part * R + col, on ? src + (row * 2 + part) * ldh + col : lH, on);
+        cp_async16_at(hst + (row * kLdH + part * R + col) * 2, on ? src + (row * 2 + part) * ldh + col : lH, on);
       }
       if (++lc * kRows >= lhi - llo) {
         li += gridDim.x;
@@ -321,30 +331,28 @@ __global__ void __launch_bounds__(kSumThreads, R >= 128 ? 1 : 2) row_sum_f16_ker
       __syncthreads();
       load(stage);
       stage = stage + 1 == NS ? 0 : stage + 1;
-      const __half* xb = ring + use * kStage;
-      const __half* hb = xb + kRows * kLdX;
+      const uint32_t xb = ring_at + use * (kStage * 2) + xlane, hb = ring_at + use * (kStage * 2) + hlane;
       use = use + 1 == NS ? 0 : use + 1;
       float t[MI][NJ][4];
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) t[i][j][q] = 0.f;
 #pragma unroll
       for (int k = 0; k < kRows; k += 16) {
         uint32_t fa[MI][4];
 #pragma unroll
-        for (int i = 0; i < MI; ++i) frag_a_t(fa[i], xb + k * kLdX + wi + i * 16, kLdX, lane);
+        for (int i = 0; i < MI; ++i) ldsm4_t_at(fa[i], xb + (k * kLdX + i * 16) * 2);
 #pragma unroll
         for (int j = 0; j < NJ / 2; ++j) {
           uint32_t fh[4], fl[4];
-          frag_b_kn(fl, hb + k * kLdH + R + wj + j * 16, kLdH, lane);
-          frag_b_kn(fh, hb + k * kLdH + wj + j * 16, kLdH, lane);
+          ldsm4_t_at(fl, hb + (k * kLdH + R + j * 16) * 2);
+          ldsm4_t_at(fh, hb + (k * kLdH + j * 16) * 2);
 #pragma unroll
           for (int i = 0; i < MI; ++i) {
-            mma16816(t[i][2 * j], fa[i], fl[0], fl[1]);
-            mma16816(t[i][2 * j + 1], fa[i], fl[2], fl[3]);
+            if (k == 0) {
+              mma16816_first(t[i][2 * j], fa[i], fl[0], fl[1]);
+              mma16816_first(t[i][2 * j + 1], fa[i], fl[2], fl[3]);
+            } else {
+              mma16816(t[i][2 * j], fa[i], fl[0], fl[1]);
+              mma16816(t[i][2 * j + 1], fa[i], fl[2], fl[3]);
+            }
             mma16816(t[i][2 * j], fa[i], fh[0], fh[1]);
             mma16816(t[i][2 * j + 1], fa[i], fh[2], fh[3]);
           }
@@ -437,14 +445,15 @@ __global__ void __launch_bounds__(256) row_sum_join_kernel(const SumArgs a) {
   const float scale = a.scale ? a.scale[n] : 1.f;
   const size_t all = (size_t)jb.di * jb.dj;
   float* G = jb.G + n * all;
+  const float* first = jb.partial + partial_slot(lo, a.seg, false) * all;   // and every second after it
   const size_t step = (size_t)gridDim.x * 256;
   if (all % 4 == 0) {
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < all / 4; i += step) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float* p = first + 4 * i;
 #pragma unroll 8
-      for (int q = 0; q < segs; ++q) {
-        const float4 u = *reinterpret_cast<const float4*>(
-            jb.partial + partial_slot(lo + q * a.seg, a.seg, q == segs - 1) * all + 4 * i);
+      for (int q = 0; q < segs; ++q, p += 2 * all) {
+        const float4 u = *reinterpret_cast<const float4*>(q == segs - 1 ? p + all : p);
         v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
       }
       *reinterpret_cast<float4*>(G + 4 * i) = make_float4(scale * v.x, scale * v.y, scale * v.z, scale * v.w);
@@ -452,8 +461,7 @@ __global__ void __launch_bounds__(256) row_sum_join_kernel(const SumArgs a) {
   } else {
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < all; i += step) {
       float v = 0.f;
-      for (int q = 0; q < segs; ++q)
-        v += jb.partial[partial_slot(lo + q * a.seg, a.seg, q == segs - 1) * all + i];
+      for (int q = 0; q < segs; ++q) v += first[(2 * q + (q == segs - 1)) * all + i];
       G[i] = scale * v;
     }
   }
@@ -468,7 +476,7 @@ int sum_segment(int S_max, int N, int blocks) {
   for (int p = 1; p <= kSumSegments; ++p) {
     const int seg = std::max(256, ((S_max + p - 1) / p + 63) / 64 * 64);
     const double items = blocks * ((double)S_max / seg + 0.5 * std::min(N, S_max));
-    const double c = ceil(items / 304) * (seg / 64 + 1) + 0.5 * p;
+    const double c = ceil(items / 304) * (seg / 64 + 2) + 0.7 * p;
     if (c < cost) {
       cost = c;
       best = seg;
@@ -499,7 +507,7 @@ cudaError_t launch_sum_rank(SumArgs& a, bool f16, int sms, bool pdl, cudaStream_
     const long long chunks = (long long)a.S_max / kRows + std::min(a.N, a.S_max);
     MOE_LAUNCH(launch_k(split_rows_kernel, dim3((int)std::min<long long>(chunks, 4 * sms), 2), kSumThreads,
                         table, s, pdl, a, ldh));
-    auto kern = row_sum_f16_kernel<R>;
+    auto kern = a.perm ? row_sum_f16_kernel<R, true> : row_sum_f16_kernel<R, false>;
     MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
     const size_t smem = 2 * (size_t)SumPlan<R>::kStages * SumPlan<R>::kStage + table;
     MOE_LAUNCH(launch_k(kern, grid, kSumThreads, smem, s, true, a, ldh));
