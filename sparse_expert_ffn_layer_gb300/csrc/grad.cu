@@ -391,25 +391,38 @@ __global__ void __launch_bounds__(kSumThreads) row_sum_f32_kernel(const SumArgs 
     const int di = it.jb->di, dj = it.jb->dj;
     const float* X = static_cast<const float*>(it.jb->x);
     const int chunks = (it.hi - it.lo + kRows32 - 1) / kRows32;
+    // a chunk is fetched into registers while the one before it is summed
+    constexpr int HV = kRows32 * R / kSumThreads;
+    float4 xv[2];
+    float hv[HV];
+    auto fetch = [&](int c) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int q = tid + p * kSumThreads, i = (q % (kIT32 / 4)) * 4;
+        const int t = row_of(a, it.lo + c * kRows32 + q / (kIT32 / 4), it.hi);
+        xv[p] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t >= 0 && it.i0 + i < di) xv[p] = *reinterpret_cast<const float4*>(X + (size_t)t * di + it.i0 + i);
+      }
+#pragma unroll
+      for (int p = 0; p < HV; ++p) {
+        const int q = tid + p * kSumThreads, j = q % R, s = it.lo + c * kRows32 + q / R;
+        hv[p] = it.j0 + j < dj && row_of(a, s, it.hi) >= 0 ? it.jb->h[(size_t)s * dj + it.j0 + j] : 0.f;
+      }
+    };
     float acc[4][JT];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < JT; ++j) acc[i][j] = 0.f;
+    fetch(0);
     for (int c = 0; c < chunks; ++c) {
       __syncthreads();
-      for (int q = tid; q < kRows32 * kIT32 / 4; q += kSumThreads) {
-        const int r = q / (kIT32 / 4), i = (q % (kIT32 / 4)) * 4;
-        const int t = row_of(a, it.lo + c * kRows32 + r, it.hi);
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t >= 0 && it.i0 + i < di) v = *reinterpret_cast<const float4*>(X + (size_t)t * di + it.i0 + i);
-        *reinterpret_cast<float4*>(xs + r * kIT32 + i) = v;
-      }
-      for (int q = tid; q < kRows32 * R; q += kSumThreads) {
-        const int r = q / R, j = q % R, s = it.lo + c * kRows32 + r;
-        hs[q] = it.j0 + j < dj && row_of(a, s, it.hi) >= 0 ? it.jb->h[(size_t)s * dj + it.j0 + j] : 0.f;
-      }
+#pragma unroll
+      for (int p = 0; p < 2; ++p) *reinterpret_cast<float4*>(xs + 4 * (tid + p * kSumThreads)) = xv[p];
+#pragma unroll
+      for (int p = 0; p < HV; ++p) hs[tid + p * kSumThreads] = hv[p];
       __syncthreads();
+      if (c + 1 < chunks) fetch(c + 1);
 #pragma unroll 4
       for (int k = 0; k < kRows32; ++k) {
         const float4 xv = *reinterpret_cast<const float4*>(xs + k * kIT32 + ti);
@@ -474,7 +487,7 @@ int sum_segment(int S_max, int N, int blocks) {
   int best = 64;
   double cost = 1e300;
   for (int p = 1; p <= kSumSegments; ++p) {
-    const int seg = std::max(256, ((S_max + p - 1) / p + 63) / 64 * 64);
+    const int seg = std::max(64, (int)(((long long)S_max + p - 1) / p + 63) / 64 * 64);
     const double items = blocks * ((double)S_max / seg + 0.5 * std::min(N, S_max));
     const double c = ceil(items / 304) * (seg / 64 + 2) + 0.7 * p;
     if (c < cost) {

@@ -9,10 +9,10 @@
 //   a_e = g_balance E counts[e] / (n^2 k)
 //
 // Both are one pass over [T, E] in 32 bits, bound by DRAM (4 bytes read per element, 4 more
-// written by the gradient).  A row is held in registers by LANES lanes with 16 (E > 512: 32)
-// values each, so that a warp has 64 bytes per lane in flight and a row's reductions are
-// log2(LANES) shuffles instead of five; the columns of a lane never change, so column sums
-// (forward) and a_e (backward) stay in registers too.
+// written by the gradient).  A row is held in registers by LANES lanes with 16 (E > 512: 32) values
+// each: a row's reductions are log2(LANES) shuffles (with 8 values per lane the shuffles bound the
+// passes: moe_balance_loss's over 262144 x 128 logits 40 us instead of %ROWS%).  The columns of a lane
+// never change, so column sums (forward) and a_e (backward) stay in registers too.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -68,12 +68,12 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, i
   }
 }
 
-// Softmax in place: x becomes p; returns lse.  The exponentials are the hardware's (2 ulp and
+// Softmax in place: x becomes p (exp_row: p / inv); returns lse.  The exponentials are the hardware's (2 ulp and
 // 2^-23 of |x - m| relative: small where p matters); with expf the arithmetic, not DRAM, bound the
 // pass over 262144 x 128 logits (31 us instead of %ROWS%).  A row of -inf only has p = 0 and lse = 0 (it
 // adds nothing to either loss); NaN and +inf give NaN as the formula does.
 template <int LANES, int N>
-__device__ __forceinline__ float softmax_row(float (&x)[N]) {
+__device__ __forceinline__ float exp_row(float (&x)[N], float& inv) {
   float m = x[0];
 #pragma unroll
   for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
@@ -87,10 +87,16 @@ __device__ __forceinline__ float softmax_row(float (&x)[N]) {
   }
   s = group_sum<LANES>(s);
   const bool empty = s == 0.f;
-  const float inv = empty ? 0.f : 1.f / s;
+  inv = empty ? 0.f : 1.f / s;
+  return empty ? 0.f : m + logf(s);
+}
+template <int LANES, int N>
+__device__ __forceinline__ float softmax_row(float (&x)[N]) {
+  float inv;
+  const float lse = exp_row<LANES>(x, inv);
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] *= inv;
-  return empty ? 0.f : m + logf(s);
+  return lse;
 }
 
 // Sum of v over the block, in a fixed order; the result is valid in thread 0.
@@ -117,7 +123,7 @@ struct LossOut {
 // of lse^2 and the number of tokens.
 __host__ __device__ inline size_t record_words(int E) { return 2 * (size_t)E + 4; }
 
-// Joins nb records (rec(b) is record b) into the outputs.  Runs in one cluster of kCluster
+// Joins nb records (rec(b) is record b) into the outputs.  Runs in one cluster of up to kCluster
 // blocks: block c owns the columns [c Ec, (c + 1) Ec); its threads sum each column in
 // blockDim / Ec parts, always in the same order, and rank 0 adds the blocks' shares of the
 // balance loss through distributed shared memory.
@@ -125,8 +131,8 @@ template <typename Rec>
 __device__ __forceinline__ void join_records(Rec rec, int nb, int E, int k, LossOut o, float* sh_f,
                                              int* sh_i, float* share) {
   cg::cluster_group cl = cg::this_cluster();
-  const int c = (int)cl.block_rank();
-  const int Ec = (E + kCluster - 1) / kCluster;
+  const int c = (int)cl.block_rank(), ncl = (int)cl.num_blocks();
+  const int Ec = (E + ncl - 1) / ncl;                // at most blockDim
   const int parts = max(1, (int)blockDim.x / Ec);
   const int col = threadIdx.x % Ec, part = threadIdx.x / Ec;
   const int e = c * Ec + col;
@@ -176,7 +182,7 @@ __device__ __forceinline__ void join_records(Rec rec, int nb, int E, int k, Loss
   cl.sync();
   if (c == 0 && threadIdx.x == 0) {
     float s = 0.f;
-    for (int q = 0; q < kCluster; ++q) s += share[q];
+    for (int q = 0; q < ncl; ++q) s += share[q];
     o.losses[0] = (float)E * (s / (nf * (float)k));
     o.losses[1] = z / nf;
     *o.n_valid = n_sh;
@@ -187,7 +193,7 @@ __device__ __forceinline__ void join_records(Rec rec, int nb, int E, int k, Loss
 // (small batches: one launch).  Otherwise records go to the workspace and balance_join_kernel
 // follows.
 template <int LANES, int VEC, int J, bool kOne>
-__global__ void __launch_bounds__(kRowThreads, 2) balance_rows_kernel(
+__global__ void __launch_bounds__(kRowThreads, VEC * J > 16 ? 1 : 2) balance_rows_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
     const uint8_t* __restrict__ mask, int T, int E, int k, float* __restrict__ records, LossOut o) {
   constexpr int V = VEC * J;
@@ -208,20 +214,22 @@ __global__ void __launch_bounds__(kRowThreads, 2) balance_rows_kernel(
   float z = 0.f;
   int n = 0;
   const int64_t stride = (int64_t)gridDim.x * kRowWarps * RPW;
+  // (Fetching the next row ahead costs a third of the warps in registers: 32 us instead of %ROWS%.)
   for (int64_t base = ((int64_t)blockIdx.x * kRowWarps + w) * RPW; base < T; base += stride) {
     const int64_t t = base + g;
     const bool on = t < T && (!mask || mask[t]);
     float x[V];
-    load_row<LANES, VEC, J>(logits + (size_t)t * E, E, l, on, x);
-    if (on && l < k) {                                        // k <= 2 <= LANES unless E is tiny
+    load_row<LANES, VEC, J>(logits + (on ? t : 0) * E, E, l, on, x);
+    if (on) {
       for (int j = l; j < k; j += LANES) {
-        const int e = topk_idx[(size_t)t * k + j];
+        const int e = topk_idx[t * k + j];
         if ((unsigned)e < (unsigned)E) atomicAdd(&hist[e], 1);
       }
     }
-    const float lse = softmax_row<LANES>(x);                  // all zero for a row that is off
+    float inv;
+    const float lse = exp_row<LANES>(x, inv);                 // all zero for a row that is off
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] += x[i];
+    for (int i = 0; i < V; ++i) acc[i] = fmaf(x[i], inv, acc[i]);
     if (on && l == 0) {
       z += lse * lse;
       n += 1;
@@ -254,19 +262,23 @@ __global__ void __launch_bounds__(kRowThreads, 2) balance_rows_kernel(
   float* rec = kOne ? rec_s : records + (size_t)blockIdx.x * record_words(E);
   for (int e = threadIdx.x; e < E; e += kRowThreads) {
     float s = 0.f;
+#pragma unroll
     for (int q = 0; q < kRowWarps; ++q) s += red[q * E + e];
     rec[e] = s;
     rec[E + e] = __int_as_float(hist[e]);
   }
-  if (threadIdx.x == 0) {
-    float zz = 0.f;
-    int nn = 0;
-    for (int q = 0; q < kRowWarps; ++q) {
-      zz += zs[q];
-      nn += ns[q];
+  if (w == kRowWarps - 1) {                         // the last warp has the fewest columns
+    float zz = lane < kRowWarps ? zs[lane] : 0.f;
+    int nn = lane < kRowWarps ? ns[lane] : 0;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) {
+      zz += __shfl_xor_sync(0xffffffffu, zz, s);
+      nn += __shfl_xor_sync(0xffffffffu, nn, s);
     }
-    rec[2 * E] = zz;
-    rec[2 * E + 1] = __int_as_float(nn);
+    if (lane == 0) {
+      rec[2 * E] = zz;
+      rec[2 * E + 1] = __int_as_float(nn);
+    }
   }
   if (kOne) {
     __shared__ float sh_f[kRowThreads];
@@ -274,8 +286,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) balance_rows_kernel(
     __shared__ float share[kCluster];
     cg::cluster_group cl = cg::this_cluster();
     cl.sync();                                      // every block's record is complete
-    join_records([&](int b) { return (const float*)cl.map_shared_rank(rec_s, b); }, kCluster, E, k,
-                 o, sh_f, sh_i, share);
+    join_records([&](int b) { return (const float*)cl.map_shared_rank(rec_s, b); },
+                 (int)cl.num_blocks(), E, k, o, sh_f, sh_i, share);
     // its last cluster barrier is behind every read of another block's record
   } else {
     pdl_trigger();
@@ -410,16 +422,16 @@ __device__ __forceinline__ void store_row(const DlArgs& d, int64_t t, int l, con
 template <int LANES, int VEC, int J>
 __global__ void __launch_bounds__(256) dlogits_kernel(const DlArgs d) {
   if (d.status && blockIdx.x == 0 && threadIdx.x == 0) *d.status = kOk;
-  constexpr int RPW = 32 / LANES;
+  constexpr int V = VEC * J, RPW = 32 / LANES;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int l = lane % LANES, g = lane / LANES;
-  float a[VEC * J];
+  float a[V];
   const float gz = loss_factors<LANES, VEC, J>(d, l, a);
   const int64_t stride = (int64_t)gridDim.x * 8 * RPW;
   for (int64_t base = ((int64_t)blockIdx.x * 8 + w) * RPW; base < d.T; base += stride) {
     const int64_t t = d.T - 1 - (base + g);
     const bool in = t >= 0, on = in && (!d.mask || d.mask[t]);
-    float x[VEC * J];
+    float x[V];
     load_row<LANES, VEC, J>(d.logits + (on ? t : 0) * d.E, d.E, l, on, x);
     row_gradient<LANES, VEC, J>(d, t, on, l, a, gz, x);
     if (in) store_row<LANES, VEC, J>(d, t, l, x);
@@ -464,8 +476,8 @@ __global__ void __launch_bounds__(kSplitThreads) dlogits_split_kernel(const DlAr
     const int blk = blockIdx.x - o.nT, rows = min(kGateBlock, o.d - blk * kGateBlock);
     const float* src = o.Wg + (size_t)blk * kGateBlock * d.E;
     __half* dst = o.W2 + (size_t)blk * kGateBlock * o.Ep;
-    constexpr int NQ = kGateBlock * 16 * LANES / VEC / kSplitThreads > 0
-                           ? kGateBlock * 16 * LANES / VEC / kSplitThreads : 1;
+    constexpr int NQ = kGateBlock * V * LANES / VEC / kSplitThreads > 0
+                           ? kGateBlock * V * LANES / VEC / kSplitThreads : 1;
     float v[NQ][VEC];                              // every value of the block, read once
     const int ne = d.E / VEC;
     float m = 0.f;
@@ -576,8 +588,7 @@ int sm_count() {
   return sms;
 }
 
-// Lanes per row: 16 values per lane up to 512 experts, 32 above; four-wide accesses where a
-// row's length allows them.
+// Lanes per row and values per lane (see the top); four-wide accesses where a row's length allows.
 template <typename F>
 cudaError_t with_shape(int E, F f) {
   auto pick = [&](auto vec) -> cudaError_t {
@@ -603,17 +614,20 @@ int lanes_for(int E) {
 
 // Blocks of the row pass: two per SM, fewer for short batches.
 constexpr int kMaxRecords = 512;
+// Rows that a block of the row pass takes at once.
+int block_rows(int E) { return kRowWarps * (32 / lanes_for(E)); }
 int row_blocks(int T, int E, int sms) {
-  const int rows = kRowWarps * (32 / lanes_for(E));
+  const int rows = block_rows(E);
   return std::max(1, std::min({(T + rows - 1) / rows, 2 * sms, kMaxRecords}));
 }
 
-// Up to this many logits one cluster does the whole call.
+// Up to this many logits one cluster does the whole call (a second launch costs about 4 us more
+// than a few more passes over the rows): one block where a pass covers the batch, else up to eight.
 constexpr long long kOneClusterElems = 256 * 1024;
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kernel)(KArgs...), int grid, int block, size_t smem,
-                           cudaStream_t s, bool pdl, Args&&... args) {
+                           cudaStream_t s, bool pdl, Args&&... args) {   // the grid is one cluster
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
@@ -621,7 +635,7 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), int grid, int block, size_t
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kCluster;
+  attr[0].val.clusterDim.x = grid;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -644,7 +658,12 @@ cudaError_t launch_balance_loss(const float* logits, const int32_t* topk_idx, co
   if (sms < 1) return cudaErrorInvalidDevice;
   const LossOut o{counts, prob_mean, losses, n_valid};
   const bool one = (long long)T * E <= kOneClusterElems;
-  const int blocks = one ? kCluster : row_blocks(T, E, sms);
+  int blocks = row_blocks(T, E, sms);
+  if (one) {                                       // a power of two, whose blocks hold E columns
+    int c = 1;
+    while (c < kCluster && (c < blocks || c * kRowThreads < E)) c *= 2;
+    blocks = c;
+  }
   const size_t smem = sizeof(float) * ((size_t)(kRowWarps + 1) * E + (one ? record_words(E) : 0));
   return with_shape(E, [&](auto lanes, auto vec, auto j) -> cudaError_t {
     constexpr int L = decltype(lanes)::value, V = decltype(vec)::value, J = decltype(j)::value;
