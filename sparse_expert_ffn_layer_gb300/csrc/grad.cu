@@ -590,6 +590,15 @@ __global__ void __launch_bounds__(256) gate_dx_kernel(const float* __restrict__ 
 // dy_s = w_tj dout_t,  dw_tj = <dout_t, y_s>,  s = slot_of[t,j].  Bound by DRAM: dout, y read
 // once, dy written once.  WPR warps per token row (8 where there are too few rows to fill the
 // device with a warp each).
+// Written once and not read here: first to leave L2.
+template <typename Vec>
+__device__ __forceinline__ void store_stream(void* p, const Vec& v) {
+  if constexpr (sizeof(Vec) == 16)
+    __stcs(static_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&v));
+  else
+    *static_cast<Vec*>(p) = v;
+}
+
 template <typename T, int V, int WPR>
 __global__ void __launch_bounds__(256) combine_backward_kernel(
     const T* __restrict__ dout, const T* __restrict__ y, const int32_t* __restrict__ slot_of,
@@ -625,7 +634,7 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(
               Vec o;
 #pragma unroll
               for (int i = 0; i < V; ++i) o.v[i] = (T)(g[j] * (float)u.v[i]);
-              *reinterpret_cast<Vec*>(dy + (int64_t)s[j] * d + c) = o;
+              store_stream(dy + (int64_t)s[j] * d + c, o);
             }
           }
         }
