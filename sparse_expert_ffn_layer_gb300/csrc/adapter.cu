@@ -427,19 +427,33 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
       for (int k = 0; k < R / 16; ++k)
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[k][q] = make_float2(0.f, 0.f);
+      // Unconditional loads, in batches: each waited for on its own under a condition, they took
+      // most of the time (3575 rows, 1808 columns, r = 96: 80 us).  A row behind the run's end reads
+      // the last one and is not stored; columns behind r read the first and count as zero.
+      const uint32_t ra = (uint32_t)min(sa, s1 - 1), rb = (uint32_t)min(sb, s1 - 1);
       for (int p = 0; p < ta.parts_k; ++p) {
-        const float* src = ta.partial + (size_t)p * a.S_max * a.r;
+        const float* src = ta.partial + (size_t)p * a.S_max * a.r + 2 * (lane & 3);
+        const float *pa = src + (uint64_t)ra * (uint32_t)a.r, *pb = src + (uint64_t)rb * (uint32_t)a.r;
+        constexpr int KB = R / 16 < 4 ? R / 16 : 4;
 #pragma unroll
-        for (int k = 0; k < R / 16; ++k)
+        for (int k0 = 0; k0 < R / 16; k0 += KB) {
+          float2 u[KB][4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int s = q & 1 ? sb : sa, col = 16 * k + 8 * (q >> 1) + 2 * (lane & 3);
-            if (s < s1 && col < a.r) {
-              const float2 u = *reinterpret_cast<const float2*>(src + (size_t)s * a.r + col);
-              v[k][q].x += u.x;
-              v[k][q].y += u.y;
+          for (int k = 0; k < KB; ++k)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int col = 16 * (k0 + k) + 8 * (q >> 1);
+              u[k][q] = *reinterpret_cast<const float2*>((q & 1 ? pb : pa) + (col < a.r ? col : 0));
             }
-          }
+#pragma unroll
+          for (int k = 0; k < KB; ++k)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (16 * (k0 + k) + 8 * (q >> 1) < a.r) {
+                v[k0 + k][q].x += u[k][q].x;
+                v[k0 + k][q].y += u[k][q].y;
+              }
+        }
       }
       float ma = 0.f, mb = 0.f;
       bool oa = false, ob = false;

@@ -439,8 +439,9 @@ __global__ void __launch_bounds__(256) dlogits_kernel(const DlArgs d) {
 }
 
 // The same with the f16 parts that the tensor-core form of the gate's gradient multiplies
-// (gate_grad.cu): a block takes 128 rows, keeps their gradients in registers until it knows their
-// largest magnitude, and writes them in 32 bits and as (hi, lo) with v = (hi + 2^-11 lo) 2^e.
+// (gate_grad.cu): a block takes 128 rows, writes their gradients in 32 bits, and when it knows their
+// largest magnitude also as (hi, lo) with v = (hi + 2^-11 lo) 2^e (from L2; kept in registers, the
+// unrolled passes were fetched as instructions for longer than they ran).
 // Blocks beyond the rows round Wg to f16 by 128 rows and one power of two.
 struct SplitOut {
   __half* dl2;                 // [T][2 Ep]: hi, lo; columns beyond E are zero
@@ -464,120 +465,90 @@ __device__ __forceinline__ float block_max(float m, float* scratch) {
 }
 __device__ __forceinline__ float magnitude(float v) { return v - v == 0.f ? fabsf(v) : INFINITY; }
 
+// Rounds rows x E values (m: their largest magnitude) to f16 parts of `ld` columns, lo null: one
+// part only; returns the power of two.
+template <int VEC>
+__device__ __forceinline__ float split_block(const float* src, int rows, int E, int Ep, float m, __half* hi,
+                                             __half* lo, int ld) {
+  const int e = scale_exp(m);                      // 0 for a block with infinities or NaN
+  const float inv = exp2_int(-e);
+  const int n = Ep / VEC;
+#pragma unroll 4
+  for (int q = threadIdx.x; q < rows * n; q += kSplitThreads) {
+    const int r = q / n, c = (q - r * n) * VEC;
+    float f[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) f[v] = 0.f;
+    if (c < E) {
+      if (VEC == 4)
+        *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(src + r * E + c);
+      else
+        f[0] = src[r * E + c];
+    }
+    __half h[VEC], l[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      h[v] = __float2half_rn(f[v] * inv);
+      const float b = __half2float(h[v]);
+      l[v] = isfinite(b) ? __float2half_rn((f[v] * inv - b) * kGateLo) : __ushort_as_half(0);
+    }
+    if (VEC == 4) {
+      *reinterpret_cast<uint2*>(hi + (size_t)r * ld + c) = *reinterpret_cast<const uint2*>(h);
+      if (lo) *reinterpret_cast<uint2*>(lo + (size_t)r * ld + c) = *reinterpret_cast<const uint2*>(l);
+    } else {
+      hi[(size_t)r * ld + c] = h[0];
+      if (lo) lo[(size_t)r * ld + c] = l[0];
+    }
+  }
+  return exp2_int(e);
+}
+
 template <int LANES, int VEC, int J>
 __global__ void __launch_bounds__(kSplitThreads) dlogits_split_kernel(const DlArgs d, const SplitOut o) {
   constexpr int V = VEC * J, RPW = 32 / LANES;
-  constexpr int kPass = kSplitThreads / 32 * RPW;            // rows per pass
-  constexpr int NP = kPass >= kGateBlock ? 1 : kGateBlock / kPass;
   __shared__ float scratch[kSplitThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   pdl_trigger();
   if ((int)blockIdx.x >= o.nT) {
     const int blk = blockIdx.x - o.nT, rows = min(kGateBlock, o.d - blk * kGateBlock);
     const float* src = o.Wg + (size_t)blk * kGateBlock * d.E;
-    __half* dst = o.W2 + (size_t)blk * kGateBlock * o.Ep;
-    constexpr int NQ = kGateBlock * V * LANES / VEC / kSplitThreads > 0
-                           ? kGateBlock * V * LANES / VEC / kSplitThreads : 1;
-    float v[NQ][VEC];                              // every value of the block, read once
-    const int ne = d.E / VEC;
     float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      const int q = tid + i * kSplitThreads;
-#pragma unroll
-      for (int u = 0; u < VEC; ++u) v[i][u] = 0.f;
-      if (q < rows * ne) {
-        if (VEC == 4)
-          *reinterpret_cast<float4*>(v[i]) = *reinterpret_cast<const float4*>(src + 4 * q);
-        else
-          v[i][0] = src[q];
+    if (VEC == 4) {
+#pragma unroll 8
+      for (int q = tid; q < rows * d.E / 4; q += kSplitThreads) {
+        const float4 v = reinterpret_cast<const float4*>(src)[q];
+        m = fmaxf(fmaxf(m, fmaxf(magnitude(v.x), magnitude(v.y))), fmaxf(magnitude(v.z), magnitude(v.w)));
       }
+    } else {
+#pragma unroll 8
+      for (int q = tid; q < rows * d.E; q += kSplitThreads) m = fmaxf(m, magnitude(src[q]));
     }
-#pragma unroll
-    for (int i = 0; i < NQ; ++i)
-#pragma unroll
-      for (int u = 0; u < VEC; ++u) m = fmaxf(m, magnitude(v[i][u]));
     m = block_max(m, scratch);
-    const int e = scale_exp(m);
-    const float inv = exp2_int(-e);
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      const int q = tid + i * kSplitThreads;
-      if (q >= rows * ne) continue;
-      const int r = q / ne;
-      __half* p = dst + r * o.Ep + (q - r * ne) * VEC;
-      if (VEC == 4) {
-        __half2 h[2] = {__floats2half2_rn(v[i][0] * inv, v[i][1 % VEC] * inv),
-                        __floats2half2_rn(v[i][2 % VEC] * inv, v[i][3 % VEC] * inv)};
-        *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(h);
-      } else {
-        p[0] = __float2half_rn(v[i][0] * inv);
-      }
-    }
-    for (int q = tid; q < rows * (o.Ep - d.E); q += kSplitThreads) {
-      const int r = q / (o.Ep - d.E);
-      dst[r * o.Ep + d.E + q - r * (o.Ep - d.E)] = __ushort_as_half(0);
-    }
-    if (tid == 0) o.sW[blk] = exp2_int(e);
+    const float s = split_block<VEC>(src, rows, d.E, o.Ep, m, o.W2 + (size_t)blk * kGateBlock * o.Ep, nullptr, o.Ep);
+    if (tid == 0) o.sW[blk] = s;
     return;
   }
   if (d.status && blockIdx.x == 0 && tid == 0) *d.status = kOk;
   const int l = lane % LANES, g = lane / LANES;
   float a[V];
   const float gz = loss_factors<LANES, VEC, J>(d, l, a);
-  const int row0 = blockIdx.x * kGateBlock;
-  float x[NP][V];
+  const int row0 = blockIdx.x * kGateBlock, rows = min(kGateBlock, d.T - row0);
   float m = 0.f;
-#pragma unroll
-  for (int p = 0; p < NP; ++p) {
-    const int r = p * kPass + w * RPW + g;
+  for (int r0 = w * RPW; r0 < rows; r0 += kSplitThreads / 32 * RPW) {
+    const int r = r0 + g;
     const int64_t t = (int64_t)row0 + r;
-    const bool on = r < kGateBlock && t < d.T && (!d.mask || d.mask[t]);
-    load_row<LANES, VEC, J>(d.logits + (on ? t : 0) * d.E, d.E, l, on, x[p]);
+    const bool in = r < rows, on = in && (!d.mask || d.mask[t]);
+    float x[V];
+    load_row<LANES, VEC, J>(d.logits + (on ? t : 0) * d.E, d.E, l, on, x);
+    row_gradient<LANES, VEC, J>(d, t, on, l, a, gz, x);
+    if (in) store_row<LANES, VEC, J>(d, t, l, x);
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = fmaxf(m, magnitude(x[i]));
   }
-#pragma unroll
-  for (int p = 0; p < NP; ++p) {
-    const int r = p * kPass + w * RPW + g;
-    const int64_t t = (int64_t)row0 + r;
-    const bool in = r < kGateBlock && t < d.T, on = in && (!d.mask || d.mask[t]);
-    row_gradient<LANES, VEC, J>(d, t, on, l, a, gz, x[p]);
-    if (in) store_row<LANES, VEC, J>(d, t, l, x[p]);
-#pragma unroll
-    for (int i = 0; i < V; ++i) m = fmaxf(m, magnitude(x[p][i]));
-  }
-  m = block_max(m, scratch);
-  const int e = scale_exp(m);                 // 0 for a block with infinities or NaN
-  const float inv = exp2_int(-e);
-#pragma unroll
-  for (int p = 0; p < NP; ++p) {
-    const int r = p * kPass + w * RPW + g;
-    const int64_t t = (int64_t)row0 + r;
-    if (r >= kGateBlock || t >= d.T) continue;
-    __half* dst = o.dl2 + t * 2 * o.Ep;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int c = col_of<LANES, VEC>(j, l);
-      if (c >= o.Ep) continue;
-      __half hi[VEC], lo[VEC];
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const float f = c + v < d.E ? x[p][VEC * j + v] * inv : 0.f;
-        hi[v] = __float2half_rn(f);
-        const float h = __half2float(hi[v]);
-        lo[v] = isfinite(h) ? __float2half_rn((f - h) * kGateLo) : __ushort_as_half(0);
-      }
-      if (VEC == 4) {
-        *reinterpret_cast<uint2*>(dst + c) = *reinterpret_cast<const uint2*>(hi);
-        *reinterpret_cast<uint2*>(dst + o.Ep + c) = *reinterpret_cast<const uint2*>(lo);
-      } else {
-        dst[c] = hi[0];
-        dst[o.Ep + c] = lo[0];
-      }
-    }
-    // columns up to Ep that no lane's values cover
-    for (int c = LANES * V + l; c < o.Ep; c += LANES) dst[c] = dst[o.Ep + c] = __ushort_as_half(0);
-  }
-  if (tid == 0) o.sT[blockIdx.x] = exp2_int(e);
+  m = block_max(m, scratch);                       // behind its barrier the block's rows are written
+  __half* dst = o.dl2 + (size_t)row0 * 2 * o.Ep;
+  const float s = split_block<VEC>(d.dlogits + (size_t)row0 * d.E, rows, d.E, o.Ep, m, dst, dst + o.Ep, 2 * o.Ep);
+  if (tid == 0) o.sT[blockIdx.x] = s;
 }
 
 int sm_count() {
