@@ -119,9 +119,28 @@ __device__ __forceinline__ int swz(int row, int piece) {
 
 struct TallArgs {
   AdapterArgs a;
-  float* partial;            // [parts_k][S_max][r]
-  int parts_k, parts_n;      // column parts of the two products
+  float* partial;            // [parts of the first product][rows of all groups][r]
+  int slots_k, slots_n;      // resident blocks of the two launches
 };
+
+// Parts of a product's columns over the tiles that there are (the caller only knows a bound): the
+// count that takes the fewest chunk times on `slots` resident blocks, with `start` chunk times for
+// the start of an item.  Four chunks or more each, and no more than kPartItems items (which bounds
+// the partial h).  Every warp computes it, a count per lane.
+__device__ __forceinline__ int column_parts(int tiles, int chunks, int slots, int start) {
+  const int p = (threadIdx.x & 31) + 1;
+  int cost = 0x7fffffff;
+  if (p == 1 || (p <= kAdapterParts && chunks >= 4 * p && (long long)tiles * p <= kPartItems))
+    cost = min((tiles * p + slots - 1) / slots, 1 << 12) * ((chunks + p - 1) / p + start);
+  const int best = __reduce_min_sync(0xffffffffu, cost);
+  return __ffs(__ballot_sync(0xffffffffu, cost == best));
+}
+// Chunks of a product and the start of its items, in both launches' terms.
+template <int R>
+__device__ __forceinline__ int parts_of_k(const TallArgs& ta, int tiles) {
+  const int w = PlanTall<R>::kSub * kChunk;
+  return column_parts(tiles, (ta.a.dk + w - 1) / w, ta.slots_k, 2);
+}
 
 // The chunks of a block's items, loaded ahead of their use.  Item i is part i % parts of tile
 // i / parts; block b takes items b, b + blocks, ...  kWide: the weights' box has r-wide rows (one
@@ -292,9 +311,11 @@ __global__ void __launch_bounds__(kTallThreads, 2)
   ring.mW = &mP;
   const int ntiles = tall_setup(ring, a, raw);
   ring.chunks = (a.dk + PL::kSub * kChunk - 1) / (PL::kSub * kChunk);
-  ring.parts = ta.parts_k;
+  ring.parts = parts_of_k<R>(ta, ntiles);
   ring.items = ntiles * ring.parts;
   ring.blocks = gridDim.x - 1;
+  const int S = ring.bound[a.N];
+  float* partial = ring.parts == 1 && a.hidden ? a.hidden : ta.partial;
   ring.begin();
   const int wr = (w & 3) * 16, wc = w >> 2, h0 = WN > 1 ? wc * (R / WN) : 0;
   const int l15 = lane & 15, lh = lane >> 4, l3 = (lane >> 3) & 1, l7 = lane & 7;
@@ -370,7 +391,7 @@ __global__ void __launch_bounds__(kTallThreads, 2)
     }
     if (WK == 1 || wc == 0) {
       const int sa = s0 + wr + (lane >> 2), sb = sa + 8;
-      float* pa = ta.partial + ((size_t)part * a.S_max + sa) * a.r;
+      float* pa = partial + ((size_t)part * S + sa) * a.r;
       float* pb = pa + (size_t)8 * a.r;
 #pragma unroll
       for (int j = 0; j < NF; ++j) {
@@ -399,7 +420,10 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
   ring.mW = &mQ;
   const int ntiles = tall_setup(ring, a, raw);
   ring.chunks = (a.dn + PL::kSub * kChunk - 1) / (PL::kSub * kChunk);
-  ring.parts = ta.parts_n;
+  const int parts_k = parts_of_k<R>(ta, ntiles), S = ring.bound[a.N];
+  const float* partial = parts_k == 1 && a.hidden ? a.hidden : ta.partial;
+  // an item reads and converts its tile's h first, all its parts
+  ring.parts = column_parts(ntiles, ring.chunks, ta.slots_n, 2 + (R >= 64 ? 2 : 1) * parts_k);
   ring.items = ntiles * ring.parts;
   ring.blocks = gridDim.x;
   ring.begin();                                   // base and Q are inputs of the call
@@ -431,8 +455,8 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
       // most of the time (3575 rows, 1808 columns, r = 96: 80 us).  A row behind the run's end reads
       // the last one and is not stored; columns behind r read the first and count as zero.
       const uint32_t ra = (uint32_t)min(sa, s1 - 1), rb = (uint32_t)min(sb, s1 - 1);
-      for (int p = 0; p < ta.parts_k; ++p) {
-        const float* src = ta.partial + (size_t)p * a.S_max * a.r + 2 * (lane & 3);
+      for (int p = 0; p < parts_k; ++p) {
+        const float* src = partial + (size_t)p * S * a.r + 2 * (lane & 3);
         const float *pa = src + (uint64_t)ra * (uint32_t)a.r, *pb = src + (uint64_t)rb * (uint32_t)a.r;
         constexpr int KB = R / 16 < 4 ? R / 16 : 4;
 #pragma unroll
@@ -470,7 +494,7 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
             ma = fmaxf(ma, m);
             oa |= odd;
           }
-          if (a.hidden && part == 0 && wc == 0 && ta.partial != a.hidden) {
+          if (a.hidden && part == 0 && wc == 0 && partial != a.hidden) {
             const int s = q & 1 ? sb : sa, col = 16 * k + 8 * (q >> 1) + 2 * (lane & 3);
             if (s < s1 && col < a.r)
               *reinterpret_cast<float2*>(a.hidden + (size_t)s * a.r + col) = v[k][q];
@@ -1128,6 +1152,7 @@ cudaError_t launch_short(const AdapterArgs& a, cudaStream_t s) {
   using PL = Plan16<16, R>;
   return launch_plan(adapter_f16_kernel<16, R, kT>, a, 16, PL::kThreads, PL::kOffTab, s);
 }
+// Blocks of a kernel that are resident on the device at once, asked once as resident_clusters.
 int resident_blocks(const void* kern, int threads, size_t smem) {
   static std::mutex mu;
   static std::map<std::tuple<const void*, int, size_t>, int> known;
@@ -1151,34 +1176,23 @@ cudaError_t launch_tall(const AdapterArgs& a, float* partial, cudaStream_t s) {
   const uint32_t RB = R > 64 ? 64 : R;
   const uint32_t wide[3] = {RB, 64, 1}, flat[3] = {64, R, 1};
   const size_t smem = PL::kBytes + table_bytes(a.N) + (R < 32 ? kTallRows * R * 4 : 0);
-  TallArgs ta{a, partial, adapter_parts(a.S_max, a.dk), 1};
-  const long long tiles = (long long)a.S_max / kTallRows + std::min(a.N, a.S_max);   // at most
-  {
-    auto kern = adapter_shrink_kernel<R, kT>;
-    MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
-    const int fit = resident_blocks(reinterpret_cast<const void*>(kern), kTallThreads, smem);
-    if (fit < 1) return cudaErrorLaunchOutOfResources;
-    if (ta.parts_k == 1 && a.hidden) ta.partial = a.hidden;
-    CUtensorMap mP;
-    const uint64_t p_fwd[3] = {r, dk, N}, p_bwd[3] = {dk, r, N};
-    if (!encode_f16_map(&mP, a.P, 3, kT ? p_bwd : p_fwd, kT ? flat : wide)) return cudaErrorInvalidValue;
-    const int grid = (int)std::min<long long>(tiles * ta.parts_k, fit - 1) + 1;   // and the checks
-    MOE_LAUNCH(launch_k(kern, grid, kTallThreads, smem, s, false, mP, ta));
-  }
-  if (a.dn == 0 && ta.partial == a.hidden) return cudaSuccess;
-  auto kern = adapter_expand_kernel<R, kT>;
-  MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
-  const int fit = resident_blocks(reinterpret_cast<const void*>(kern), kTallThreads, smem);
-  if (fit < 1) return cudaErrorLaunchOutOfResources;
-  CUtensorMap mQ;
+  const long long items = ((long long)a.S_max / kTallRows + std::min(a.N, a.S_max)) * kAdapterParts;
+  auto shrink = adapter_shrink_kernel<R, kT>;
+  auto expand = adapter_expand_kernel<R, kT>;
+  MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(shrink)));
+  MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(expand)));
+  const TallArgs ta{a, partial, resident_blocks(reinterpret_cast<const void*>(shrink), kTallThreads, smem),
+                    resident_blocks(reinterpret_cast<const void*>(expand), kTallThreads, smem)};
+  if (ta.slots_k < 2 || ta.slots_n < 1) return cudaErrorLaunchOutOfResources;
+  CUtensorMap mP, mQ;
+  const uint64_t p_fwd[3] = {r, dk, N}, p_bwd[3] = {dk, r, N}, q_fwd[3] = {dn, r, N}, q_bwd[3] = {r, dn, N};
+  if (!encode_f16_map(&mP, a.P, 3, kT ? p_bwd : p_fwd, kT ? flat : wide)) return cudaErrorInvalidValue;
   memset(&mQ, 0, sizeof(mQ));                     // not used when there is no second product
-  if (a.dn) {
-    const uint64_t q_fwd[3] = {dn, r, N}, q_bwd[3] = {r, dn, N};
-    if (!encode_f16_map(&mQ, a.Q, 3, kT ? q_bwd : q_fwd, kT ? wide : flat)) return cudaErrorInvalidValue;
-    ta.parts_n = adapter_parts(a.S_max, a.dn);
-  }
-  const int grid = (int)std::min<long long>(tiles * ta.parts_n, fit);
-  return launch_k(kern, grid, kTallThreads, smem, s, true, mQ, ta);
+  if (a.dn && !encode_f16_map(&mQ, a.Q, 3, kT ? q_bwd : q_fwd, kT ? wide : flat)) return cudaErrorInvalidValue;
+  const int grid_k = (int)std::min<long long>(items, ta.slots_k - 1) + 1;      // and the checks
+  MOE_LAUNCH(launch_k(shrink, grid_k, kTallThreads, smem, s, false, mP, ta));
+  const int grid_n = (int)std::min<long long>(items, ta.slots_n);
+  return launch_k(expand, grid_n, kTallThreads, smem, s, true, mQ, ta);
 }
 template <bool kT, int R>
 cudaError_t launch_f32(const AdapterArgs& a, cudaStream_t s) {
@@ -1207,21 +1221,8 @@ __global__ void __launch_bounds__(1024) adapter_check_kernel(const AdapterArgs a
 
 bool adapter_tall(int S_max, int N, bool f16) { return f16 && S_max > 32LL * std::min(N, S_max); }
 
-// Parts of a product's columns over the tiles: the count with the fewest rounds of chunks (with
-// two chunks for the start of an item) on two blocks of each of 152 SMs, four chunks or more each.
-int adapter_parts(int S_max, int d) {
-  const long long tiles = std::max(1, (S_max + kTallRows - 1) / kTallRows);
-  const int chunks = (d + kChunk - 1) / kChunk;
-  int best = 1;
-  long long cost = 0;
-  for (int p = 1; p <= kAdapterParts && (p == 1 || chunks / p >= 4); ++p) {
-    const long long c = (tiles * p + 303) / 304 * ((chunks + p - 1) / p + 2);
-    if (p == 1 || c < cost) {
-      best = p;
-      cost = c;
-    }
-  }
-  return best;
+size_t adapter_partial_rows(int S_max) {
+  return std::max<size_t>(S_max, std::min<size_t>((size_t)kAdapterParts * S_max, (size_t)kPartItems * kTallRows));
 }
 
 cudaError_t launch_adapter(const void* x, const void* P, const void* Q, const void* base, void* y,

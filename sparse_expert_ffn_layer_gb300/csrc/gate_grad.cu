@@ -532,7 +532,8 @@ cudaError_t launch_dx_tc(const CUtensorMap& mL, const CUtensorMap& mW, const CUt
 
 }  // namespace
 
-bool gate_tc_ok(int E) { return E <= 256; }
+// (Short batches: the chain of launches takes 23 to 31 us, the multiply-add kernels half of it.)
+bool gate_tc_ok(int T, int E) { return E <= 256 && T > kSumShort; }
 size_t gate_tc_bytes(int T, int d, int E) { return T > 0 ? gate_ws(T, d, E).total : 0; }
 
 cudaError_t launch_gate_tc(const float* logits, const int32_t* topk_idx, const float* dtopk_w,

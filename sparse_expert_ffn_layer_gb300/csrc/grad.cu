@@ -65,12 +65,13 @@ struct Segments {
   int *bound, *start;
   int count;
 };
+template <int NT = kSumThreads>
 __device__ __forceinline__ Segments segment_table(const SumArgs& a, int* mem) {
   Segments g;
   g.bound = mem;
   g.start = mem + a.N + 1;
   if (a.offsets) {
-    group_table<kSumThreads>(a.offsets, a.N, a.S_max, a.seg, g.bound, g.start, g.start + a.N + 1);
+    group_table<NT>(a.offsets, a.N, a.S_max, a.seg, g.bound, g.start, g.start + a.N + 1);
   } else {
     if (threadIdx.x == 0) {
       g.bound[0] = g.start[0] = 0;
@@ -147,10 +148,31 @@ __device__ __forceinline__ void store_sum(const SumItem& it, int i, int j, float
     it.dst[it.jb->transposed ? (size_t)j * it.jb->di + i : (size_t)i * it.jb->dj + j] = it.scale * v;
 }
 
-// Warps of a block over the 128 x R sums: 32 x R / 2 each (R = 16: 16 x 16).
+// Groups without rows have zero sums; the grid shares them out.
+__device__ __forceinline__ void clear_empty(const SumArgs& a, const Segments& g) {
+  if (g.count > 0 && a.N == 1) return;
+  for (int q = 0; q < 2; ++q) {
+    const SumJob& jb = a.job[q];
+    if (!jb.G) continue;
+    const size_t all = (size_t)jb.di * jb.dj, step = (size_t)gridDim.x * blockDim.x;
+    for (int n = 0; n < a.N; ++n) {
+      if (g.start[n + 1] > g.start[n]) continue;
+      float* G = jb.G + n * all;
+      const size_t i0 = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
+      if (all % 4 == 0)
+        for (size_t i = i0; i < all / 4; i += step) reinterpret_cast<float4*>(G)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      else
+        for (size_t i = i0; i < all; i += step) G[i] = 0.f;
+    }
+  }
+}
+
+// Warps of a block over the 128 x R sums: 32 x R / 2 each (R = 16: 16 x 16; R = 128, where only one
+// block fits an SM: sixteen warps of 32 x 32).
 template <int R>
 struct SumWarps {
-  static constexpr int WJ = R >= 32 ? 2 : 1, WI = 8 / WJ;
+  static constexpr int kThreads = R >= 128 ? 512 : 256;
+  static constexpr int WJ = R >= 128 ? 4 : R >= 32 ? 2 : 1, WI = kThreads / 32 / WJ;
   static constexpr int MI = kIT / WI / 16, NJ = R / WJ / 8;        // 16-row and 8-column fragments
 };
 
@@ -228,16 +250,17 @@ struct SumPlan {
 // row that is there; their h is zero.  Otherwise the rows are the slots, and masked ones read as
 // zeros (they may hold anything).
 template <int R, bool kPerm>
-__global__ void __launch_bounds__(kSumThreads, R >= 128 ? 1 : 2) row_sum_f16_kernel(const SumArgs a, int ldh) {
+__global__ void __launch_bounds__(SumWarps<R>::kThreads, R >= 128 ? 1 : 2) row_sum_f16_kernel(const SumArgs a, int ldh) {
+  constexpr int NT = SumWarps<R>::kThreads, XP = kRows * 16 / NT;   // 16-byte pieces of x per thread
   constexpr int kLdH = SumPlan<R>::kLdH, NS = SumPlan<R>::kStages, kStage = SumPlan<R>::kStage;
   constexpr int MI = SumWarps<R>::MI, NJ = SumWarps<R>::NJ, WI = SumWarps<R>::WI;
-  constexpr int HP = kRows * R * 4 / 16 / kSumThreads;             // 16-byte pieces of h per thread
+  constexpr int HP = kRows * R * 4 / 16 / NT;                      // and of h
   extern __shared__ __align__(128) uint8_t sm[];
   __half* ring = reinterpret_cast<__half*>(sm);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   pdl_trigger();
   pdl_wait();                                      // the split h
-  const Segments g = segment_table(a, reinterpret_cast<int*>(ring + NS * kStage));
+  const Segments g = segment_table<NT>(a, reinterpret_cast<int*>(ring + NS * kStage));
   const int items = g.count * (a.job[0].blocks + a.job[1].blocks);
   const int wi = (w % WI) * MI * 16, wj = (w / WI) * NJ * 8;
   const uint32_t ring_at = smem_u32(ring);
@@ -246,8 +269,8 @@ __global__ void __launch_bounds__(kSumThreads, R >= 128 ? 1 : 2) row_sum_f16_ker
   const uint32_t hlane = (kRows * kLdX + (lane & 15) * kLdH + wj + (lane >> 4) * 8) * 2;
 
   // ---- loads: chunk after chunk across the block's items, each chunk's rows fetched one early
-  const int xc = (tid & 15) * 8, xr = tid >> 4;    // x: 16-byte piece, rows xr + 16 p
-  int li = blockIdx.x, lc = 0, llo = 0, lhi = 0, ldi = 0, lrow[4];
+  const int xc = (tid & 15) * 8, xr = tid >> 4;    // x: 16-byte piece, rows xr + NT / 16 p
+  int li = blockIdx.x, lc = 0, llo = 0, lhi = 0, ldi = 0, lrow[XP];
   const __half *lX = nullptr, *lH = nullptr;
   bool lin = false;
   int lw = 0;                                      // columns of h that there are
@@ -269,24 +292,25 @@ __global__ void __launch_bounds__(kSumThreads, R >= 128 ? 1 : 2) row_sum_f16_ker
     if (li >= items) return;
     const int s = llo + lc * kRows + xr;
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
+    for (int p = 0; p < XP; ++p) {
+      const int r = s + NT / 16 * p;
       if (kPerm)
-        lrow[p] = a.perm[min(s + 16 * p, lhi - 1)];
+        lrow[p] = a.perm[min(r, lhi - 1)];
       else
-        lrow[p] = s + 16 * p < lhi && (!a.mask || a.mask[s + 16 * p]) ? s + 16 * p : -1;
+        lrow[p] = r < lhi && (!a.mask || a.mask[r]) ? r : -1;
     }
   };
   auto load = [&](int stage) {
     if (li < items) {
       const uint32_t st = ring_at + stage * (kStage * 2), dst = st + (xr * kLdX + xc) * 2;
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
+      for (int p = 0; p < XP; ++p) {
         if (kPerm) {
           const uint32_t t = (unsigned)lrow[p] < (unsigned)a.T ? lrow[p] : 0;
-          cp_async16_at(dst + 16 * p * kLdX * 2, lX + (uint64_t)t * (uint32_t)ldi, true);
+          cp_async16_at(dst + NT / 16 * p * kLdX * 2, lX + (uint64_t)t * (uint32_t)ldi, true);
         } else {
           const bool on = lin && lrow[p] >= 0;
-          cp_async16_at(dst + 16 * p * kLdX * 2, on ? lX + (uint64_t)(uint32_t)lrow[p] * (uint32_t)ldi : lX, on);
+          cp_async16_at(dst + NT / 16 * p * kLdX * 2, on ? lX + (uint64_t)(uint32_t)lrow[p] * (uint32_t)ldi : lX, on);
         }
       }
       const uint32_t hst = st + kRows * kLdX * 2;
@@ -294,7 +318,7 @@ __global__ void __launch_bounds__(kSumThreads, R >= 128 ? 1 : 2) row_sum_f16_ker
       const __half* src = lH + (uint64_t)(uint32_t)(lc * kRows * 2) * (uint32_t)ldh;
 #pragma unroll
       for (int p = 0; p < HP; ++p) {
-        const int q = tid + p * kSumThreads;       // row, part, piece of R columns
+        const int q = tid + p * NT;                // row, part, piece of R columns
         const int row = q / (R / 4), part = q / (R / 8) % 2, col = (q % (R / 8)) * 8;
         const bool on = row < left && col < lw;
         cp_async16_at(hst + (row * kLdH + part * R + col) * 2, on ? src + (row * 2 + part) * ldh + col : lH, on);
@@ -368,14 +392,24 @@ __global__ void __launch_bounds__(kSumThreads, R >= 128 ? 1 : 2) row_sum_f16_ker
     store_sums(it, it.i0 + wi + (lane >> 2), it.j0 + wj + 2 * (lane & 3), acc);
   }
   cp_async_wait<0>();
+  clear_empty(a, g);
 }
 
-// 32-bit inputs: fused multiply-adds; 64 columns i per block, chunks of 32 rows.
+// 32-bit inputs, and f16 ones in short batches (one launch, no split): fused multiply-adds; 64
+// columns i per block, chunks of 32 rows.
 constexpr int kIT32 = 64;
 constexpr int kRows32 = 32;
 
-template <int R>
-__global__ void __launch_bounds__(kSumThreads) row_sum_f32_kernel(const SumArgs a) {
+__device__ __forceinline__ float4 load_four(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load_four(const __half* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+template <typename T, int R>
+__global__ void __launch_bounds__(kSumThreads) row_sum_fma_kernel(const SumArgs a) {
   constexpr int JT = R / 16;
   extern __shared__ __align__(16) float dyn[];     // x chunk [32][64], h chunk [32][R], table
   float* xs = dyn;
@@ -386,43 +420,51 @@ __global__ void __launch_bounds__(kSumThreads) row_sum_f32_kernel(const SumArgs 
   const Segments g = segment_table(a, reinterpret_cast<int*>(hs + kRows32 * R));
   const int items = g.count * (a.job[0].blocks + a.job[1].blocks);
   const int ti = (tid & 15) * 4, tj = tid >> 4;
+  // a chunk is fetched into registers while the one before it is summed, across the block's items
+  constexpr int HV = kRows32 * R / kSumThreads;
+  float4 xv[2];
+  float hv[HV];
+  int li = blockIdx.x, lc = 0;
+  SumItem nx;
+  if (li < items) nx = sum_item<kIT32, R>(a, g, li);
+  auto fetch = [&]() {
+    if (li >= items) return;
+    const T* X = static_cast<const T*>(nx.jb->x);
+    const int di = nx.jb->di, dj = nx.jb->dj, s0 = nx.lo + lc * kRows32;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int q = tid + p * kSumThreads, i = (q % (kIT32 / 4)) * 4;
+      const int t = row_of(a, s0 + q / (kIT32 / 4), nx.hi);
+      xv[p] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t >= 0 && nx.i0 + i < di) xv[p] = load_four(X + (size_t)t * di + nx.i0 + i);
+    }
+#pragma unroll
+    for (int p = 0; p < HV; ++p) {
+      const int q = tid + p * kSumThreads, j = q % R, s = s0 + q / R;
+      hv[p] = nx.j0 + j < dj && row_of(a, s, nx.hi) >= 0 ? nx.jb->h[(size_t)s * dj + nx.j0 + j] : 0.f;
+    }
+    if (++lc * kRows32 >= nx.hi - nx.lo) {
+      lc = 0;
+      li += gridDim.x;
+      if (li < items) nx = sum_item<kIT32, R>(a, g, li);
+    }
+  };
+  fetch();
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
     const SumItem it = sum_item<kIT32, R>(a, g, item);
-    const int di = it.jb->di, dj = it.jb->dj;
-    const float* X = static_cast<const float*>(it.jb->x);
-    const int chunks = (it.hi - it.lo + kRows32 - 1) / kRows32;
-    // a chunk is fetched into registers while the one before it is summed
-    constexpr int HV = kRows32 * R / kSumThreads;
-    float4 xv[2];
-    float hv[HV];
-    auto fetch = [&](int c) {
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int q = tid + p * kSumThreads, i = (q % (kIT32 / 4)) * 4;
-        const int t = row_of(a, it.lo + c * kRows32 + q / (kIT32 / 4), it.hi);
-        xv[p] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t >= 0 && it.i0 + i < di) xv[p] = *reinterpret_cast<const float4*>(X + (size_t)t * di + it.i0 + i);
-      }
-#pragma unroll
-      for (int p = 0; p < HV; ++p) {
-        const int q = tid + p * kSumThreads, j = q % R, s = it.lo + c * kRows32 + q / R;
-        hv[p] = it.j0 + j < dj && row_of(a, s, it.hi) >= 0 ? it.jb->h[(size_t)s * dj + it.j0 + j] : 0.f;
-      }
-    };
     float acc[4][JT];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < JT; ++j) acc[i][j] = 0.f;
-    fetch(0);
-    for (int c = 0; c < chunks; ++c) {
+    for (int row = it.lo; row < it.hi; row += kRows32) {
       __syncthreads();
 #pragma unroll
       for (int p = 0; p < 2; ++p) *reinterpret_cast<float4*>(xs + 4 * (tid + p * kSumThreads)) = xv[p];
 #pragma unroll
       for (int p = 0; p < HV; ++p) hs[tid + p * kSumThreads] = hv[p];
       __syncthreads();
-      if (c + 1 < chunks) fetch(c + 1);
+      fetch();
 #pragma unroll 4
       for (int k = 0; k < kRows32; ++k) {
         const float4 xv = *reinterpret_cast<const float4*>(xs + k * kIT32 + ti);
@@ -441,9 +483,10 @@ __global__ void __launch_bounds__(kSumThreads) row_sum_f32_kernel(const SumArgs 
 #pragma unroll
       for (int i = 0; i < 4; ++i) store_sum(it, it.i0 + ti + i, it.j0 + tj + 16 * j, acc[i][j]);
   }
+  clear_empty(a, g);
 }
 
-// Groups of several segments: their partial sums in order; groups without rows: zero.
+// Groups of several segments: their partial sums in order.
 __global__ void __launch_bounds__(256) row_sum_join_kernel(const SumArgs a) {
   pdl_wait();                                      // on every path: completion stays transitive
   const SumJob& jb = a.job[blockIdx.z];
@@ -454,7 +497,7 @@ __global__ void __launch_bounds__(256) row_sum_join_kernel(const SumArgs a) {
     hi = max(lo, min(max(a.offsets[n + 1], 0), a.S_max));
   }
   const int segs = (hi - lo + a.seg - 1) / a.seg;
-  if (segs == 1 || !jb.G) return;
+  if (segs < 2 || !jb.G) return;
   const float scale = a.scale ? a.scale[n] : 1.f;
   const size_t all = (size_t)jb.di * jb.dj;
   float* G = jb.G + n * all;
@@ -480,16 +523,22 @@ __global__ void __launch_bounds__(256) row_sum_join_kernel(const SumArgs a) {
   }
 }
 
+// Short batches of f16 rows take the multiply-add form (see row_sum_fma_kernel) where its items are
+// two rounds of blocks at most: a single chunk each, they are bound by their loads' latency.
+bool sum_tc(bool f16, int S_max, int N, int columns) {
+  return f16 && (S_max > kSumShort || (long long)std::min(N, S_max) * (columns / kIT32 + 2) > 608);
+}
+
 // Rows per segment: the segments of S_max rows (and half a segment more per group) times the
 // column blocks take the fewest rounds of two blocks on each of 152 SMs, plus what a segment
-// costs in partial sums.
+// costs in partial sums and the launch that joins them.
 int sum_segment(int S_max, int N, int blocks) {
   int best = 64;
   double cost = 1e300;
   for (int p = 1; p <= kSumSegments; ++p) {
     const int seg = std::max(64, (int)(((long long)S_max + p - 1) / p + 63) / 64 * 64);
     const double items = blocks * ((double)S_max / seg + 0.5 * std::min(N, S_max));
-    const double c = ceil(items / 304) * (seg / 64 + 2) + 0.7 * p;
+    const double c = ceil(items / 304) * (seg / 64 + 2) + 0.7 * p + (seg < S_max ? 6 : 0);
     if (c < cost) {
       cost = c;
       best = seg;
@@ -502,8 +551,8 @@ int sum_segment(int S_max, int N, int blocks) {
 int split_width(int dj) { return (dj + 15) / 16 * 16; }
 
 template <int R>
-cudaError_t launch_sum_rank(SumArgs& a, bool f16, int sms, bool pdl, cudaStream_t s) {
-  const int it = f16 ? kIT : kIT32;
+cudaError_t launch_sum_rank(SumArgs& a, bool f16, bool tc, int sms, bool pdl, cudaStream_t s) {
+  const int it = tc ? kIT : kIT32;
   int blocks = 0, ldh = 0;
   size_t widest = 0;
   for (SumJob& j : a.job) {
@@ -514,74 +563,90 @@ cudaError_t launch_sum_rank(SumArgs& a, bool f16, int sms, bool pdl, cudaStream_
     if (j.G) ldh = std::max(ldh, split_width(j.dj));
   }
   const long long segs = (long long)a.S_max / a.seg + std::min(a.N, a.S_max);
-  const size_t table = sizeof(int) * (2 * ((size_t)a.N + 1) + 32);
-  const int grid = (int)std::min<long long>(segs * blocks, (f16 && R >= 128 ? 1 : 2) * sms);
-  if (f16) {
+  const size_t table = sizeof(int) * (2 * ((size_t)a.N + 1) + 64);
+  // empty groups are cleared by the whole grid: at least a block per 32 KB of the sums
+  const long long clear = (long long)std::min(a.N, 64) * (long long)widest / 8192;
+  const int grid = (int)std::min<long long>(std::max(segs * blocks, clear), (tc && R >= 128 ? 1 : 2) * sms);
+  if (tc) {
     const long long chunks = (long long)a.S_max / kRows + std::min(a.N, a.S_max);
     MOE_LAUNCH(launch_k(split_rows_kernel, dim3((int)std::min<long long>(chunks, 4 * sms), 2), kSumThreads,
                         table, s, pdl, a, ldh));
     auto kern = a.perm ? row_sum_f16_kernel<R, true> : row_sum_f16_kernel<R, false>;
     MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
     const size_t smem = 2 * (size_t)SumPlan<R>::kStages * SumPlan<R>::kStage + table;
-    MOE_LAUNCH(launch_k(kern, grid, kSumThreads, smem, s, true, a, ldh));
+    MOE_LAUNCH(launch_k(kern, grid, SumWarps<R>::kThreads, smem, s, true, a, ldh));
   } else {
-    auto kern = row_sum_f32_kernel<R>;
+    auto kern = f16 ? row_sum_fma_kernel<__half, R> : row_sum_fma_kernel<float, R>;
     MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
     const size_t smem = sizeof(float) * (kRows32 * kIT32 + kRows32 * R) + table;
     MOE_LAUNCH(launch_k(kern, grid, kSumThreads, smem, s, pdl, a));
   }
+  if (a.S_max <= a.seg) return cudaSuccess;        // no group has a second segment
   const int bx = (int)std::min<size_t>((widest / 4 + 255) / 256, std::max<size_t>(1, 32 * sms / a.N));
   return launch_k(row_sum_join_kernel, dim3(std::max(1, bx), a.N, 2), 256, 0, s, true, a);
 }
 
 // Column blocks of a job of either type, as launch_sum_rank cuts them.
-int sum_blocks(int di, int dj, int dj_max, bool f16) {
-  const int R = dj_max <= 16 ? 16 : dj_max <= 32 ? 32 : dj_max <= 64 ? 64 : 128, it = f16 ? kIT : kIT32;
+int sum_blocks(int di, int dj, int dj_max, bool tc) {
+  const int R = dj_max <= 16 ? 16 : dj_max <= 32 ? 32 : dj_max <= 64 ? 64 : 128, it = tc ? kIT : kIT32;
   return (di + it - 1) / it * ((dj + R - 1) / R);
 }
 
 // ---------------------------------------------------------------- tokens' gradient of the gate
-// out[t,i] = in[t,i] + sum_e dl[t,e] W[i,e], fused multiply-adds on 64 x 64 tiles.
+// out[t,i] = in[t,i] + sum_e dl[t,e] W[i,e], fused multiply-adds on tiles of 32 tokens x 64 columns,
+// chunks of 32 experts whose loads are issued together and one chunk ahead: 32-bit tokens, short
+// batches, and E > 256 (the other form is in gate_grad.cu).
+constexpr int kDxT = 32, kDxI = 64, kDxE = 32;
+
 template <typename T>
 __global__ void __launch_bounds__(256) gate_dx_kernel(const float* __restrict__ dl,
                                                       const float* __restrict__ W,
-                                                      const T* __restrict__ in, int rows, int d,
-                                                      int E, T* __restrict__ out) {
-  __shared__ float as[16][68], bs[16][68];
+                                                      const T* in, int rows, int d, int E, T* out) {
+  __shared__ float as[kDxE][kDxT + 4], bs[kDxE][kDxI + 4];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int i0 = blockIdx.y * 64, t0 = blockIdx.x * 64;
-  float acc[4][4] = {};
-  for (int e0 = 0; e0 < E; e0 += 16) {
-    __syncthreads();
-    for (int q = tid; q < 64 * 16; q += 256) {
-      const int r = q >> 4, e = q & 15;
-      as[e][r] = t0 + r < rows && e0 + e < E ? dl[(size_t)(t0 + r) * E + e0 + e] : 0.f;
-      bs[e][r] = i0 + r < d && e0 + e < E ? W[(size_t)(i0 + r) * E + e0 + e] : 0.f;
-    }
+  const int64_t t0 = (int64_t)blockIdx.x * kDxT;
+  const int i0 = blockIdx.y * kDxI, le = tid & 31, lr = tid >> 5;
+  float av[4], bv[8];
+  auto fetch = [&](int e0) {
+    const bool on = e0 + le < E;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) av[q] = on && t0 + lr + 8 * q < rows ? dl[(t0 + lr + 8 * q) * E + e0 + le] : 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) bv[q] = on && i0 + lr + 8 * q < d ? W[(size_t)(i0 + lr + 8 * q) * E + e0 + le] : 0.f;
+  };
+  float acc[2][4] = {};
+  pdl_wait();                                       // dl comes from a launch before
+  fetch(0);
+  for (int e0 = 0; e0 < E; e0 += kDxE) {
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float4 u = *reinterpret_cast<const float4*>(&as[e][ty * 4]);
+    for (int q = 0; q < 4; ++q) as[le][lr + 8 * q] = av[q];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) bs[le][lr + 8 * q] = bv[q];
+    __syncthreads();
+    if (e0 + kDxE < E) fetch(e0 + kDxE);
+#pragma unroll
+    for (int e = 0; e < kDxE; ++e) {
+      const float2 u = *reinterpret_cast<const float2*>(&as[e][ty * 2]);
       const float4 v = *reinterpret_cast<const float4*>(&bs[e][tx * 4]);
-      const float av[4] = {u.x, u.y, u.z, u.w}, bv[4] = {v.x, v.y, v.z, v.w};
+      const float a2[2] = {u.x, u.y}, b4[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a2[i], b4[j], acc[i][j]);
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = t0 + ty * 4 + i;
+  for (int i = 0; i < 2; ++i) {
+    const int64_t t = t0 + ty * 2 + i;
     if (t >= rows) continue;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int c = i0 + tx * 4 + j;
       if (c >= d) continue;
-      const size_t at = (size_t)t * d + c;
       float v = acc[i][j];
-      if (in) v += (float)in[at];
-      out[at] = (T)v;
+      if (in) v += (float)in[t * d + c];
+      out[t * d + c] = (T)v;
     }
   }
 }
@@ -712,7 +777,8 @@ size_t row_sums_bytes(int di0, int dj0, int di1, int dj1, bool f16, int S_max, i
   // either job alone may be asked for: the plan of each combination fits
   for (int q = 1; q < 4; ++q) {
     const int dj = std::max(q & 1 ? dj0 : 0, q & 2 ? dj1 : 0);
-    const int b = (q & 1 ? sum_blocks(di0, dj0, dj, f16) : 0) + (q & 2 ? sum_blocks(di1, dj1, dj, f16) : 0);
+    const bool tc = sum_tc(f16, S_max, N, (q & 1 ? di0 : 0) + (q & 2 ? di1 : 0));
+    const int b = (q & 1 ? sum_blocks(di0, dj0, dj, tc) : 0) + (q & 2 ? sum_blocks(di1, dj1, dj, tc) : 0);
     if (b == 0) continue;
     const int seg = sum_segment(S_max, N, b);
     const size_t slots = 2 * (size_t)((S_max + seg - 1) / seg);
@@ -729,6 +795,7 @@ cudaError_t launch_row_sums(const void* x0, const float* h0, float* G0, int di0,
                             int N, bool pdl, cudaStream_t s) {
   const int sms = sms_of_device();
   if (sms < 1) return cudaErrorInvalidDevice;
+  const bool tc = sum_tc(dtype_f16, S_max, N, (G0 ? di0 : 0) + (G1 ? di1 : 0));
   SumArgs a;
   memset(&a, 0, sizeof(a));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -739,7 +806,7 @@ cudaError_t launch_row_sums(const void* x0, const float* h0, float* G0, int di0,
     j.di = di;
     j.dj = dj;
     j.transposed = tr;
-    if (dtype_f16) {
+    if (tc) {
       j.split = reinterpret_cast<__half*>(ws);
       j.mul = reinterpret_cast<float*>(ws + up256((size_t)S_max * split_width(dj) * 4));
       ws += split_bytes(dj, S_max);
@@ -748,7 +815,7 @@ cudaError_t launch_row_sums(const void* x0, const float* h0, float* G0, int di0,
   if (G0) job(a.job[0], x0, h0, G0, di0, dj0, tr0);
   if (G1) job(a.job[1], x1, h1, G1, di1, dj1, tr1);
   const int dj = std::max(G0 ? dj0 : 0, G1 ? dj1 : 0);
-  const int blocks = (G0 ? sum_blocks(di0, dj0, dj, dtype_f16) : 0) + (G1 ? sum_blocks(di1, dj1, dj, dtype_f16) : 0);
+  const int blocks = (G0 ? sum_blocks(di0, dj0, dj, tc) : 0) + (G1 ? sum_blocks(di1, dj1, dj, tc) : 0);
   a.seg = sum_segment(S_max, N, blocks);
   a.job[0].partial = a.job[1].partial = reinterpret_cast<float*>(ws);
   if (G0) a.job[1].partial += 2 * (size_t)((S_max + a.seg - 1) / a.seg) * di0 * dj0;
@@ -759,19 +826,19 @@ cudaError_t launch_row_sums(const void* x0, const float* h0, float* G0, int di0,
   a.T = T;
   a.S_max = S_max;
   a.N = N;
-  if (dj <= 16) return launch_sum_rank<16>(a, dtype_f16, sms, pdl, s);
-  if (dj <= 32) return launch_sum_rank<32>(a, dtype_f16, sms, pdl, s);
-  if (dj <= 64) return launch_sum_rank<64>(a, dtype_f16, sms, pdl, s);
-  return launch_sum_rank<128>(a, dtype_f16, sms, pdl, s);
+  if (dj <= 16) return launch_sum_rank<16>(a, dtype_f16, tc, sms, pdl, s);
+  if (dj <= 32) return launch_sum_rank<32>(a, dtype_f16, tc, sms, pdl, s);
+  if (dj <= 64) return launch_sum_rank<64>(a, dtype_f16, tc, sms, pdl, s);
+  return launch_sum_rank<128>(a, dtype_f16, tc, sms, pdl, s);
 }
 
 cudaError_t launch_gate_dx(const float* dlogits, const float* Wg, const void* in, int dtype_f16, int T,
                            int d, int E, void* out, cudaStream_t s) {
-  const dim3 grid((T + 63) / 64, (d + 63) / 64);
+  const dim3 grid((T + kDxT - 1) / kDxT, (d + kDxI - 1) / kDxI);
   if (dtype_f16)
-    return launch_k(gate_dx_kernel<__half>, grid, 256, 0, s, false, dlogits, Wg,
+    return launch_k(gate_dx_kernel<__half>, grid, 256, 0, s, true, dlogits, Wg,
                     static_cast<const __half*>(in), T, d, E, static_cast<__half*>(out));
-  return launch_k(gate_dx_kernel<float>, grid, 256, 0, s, false, dlogits, Wg,
+  return launch_k(gate_dx_kernel<float>, grid, 256, 0, s, true, dlogits, Wg,
                   static_cast<const float*>(in), T, d, E, static_cast<float*>(out));
 }
 

@@ -195,6 +195,7 @@ cudaError_t launch_dlogits(const float* logits, const int32_t* topk_idx, const f
 // Sums over token rows for up to two jobs G[n][i][j] = scale_n sum_s x[row(s)][i] h[s][j]
 // (transposed: G[n][j][i]); G0 or G1 may be null (grad.cu).
 constexpr int kSumSegments = 32;
+constexpr int kSumShort = 128;       // f16 batches of up to this many rows take the multiply-add form
 cudaError_t launch_row_sums(const void* x0, const float* h0, float* G0, int di0, int dj0, int tr0,
                             const void* x1, const float* h1, float* G1, int di1, int dj1, int tr1,
                             const float* scale, const int32_t* perm, const int32_t* offsets,
@@ -205,9 +206,9 @@ size_t row_sums_bytes(int di0, int dj0, int di1, int dj1, bool f16, int S_max, i
 // Joins the partial sums of runs of `run` rows (slot 2 q, the last run's 2 q + 1) in order.
 cudaError_t launch_sum_join(float* G, float* partial, int di, int dj, int T, int run, int sms,
                             cudaStream_t s);
-// The gate's whole gradient on the tensor cores (gate_grad.cu): f16 tokens, E <= 256; dWg (may be
-// null) without rows left out.
-bool gate_tc_ok(int E);
+// The gate's whole gradient on the tensor cores (gate_grad.cu): f16 tokens, E <= 256, more
+// than kSumShort rows; dWg (may be null) without rows left out.
+bool gate_tc_ok(int T, int E);
 size_t gate_tc_bytes(int T, int d, int E);
 cudaError_t launch_gate_tc(const float* logits, const int32_t* topk_idx, const float* dtopk_w,
                            const float* dlosses, const int32_t* counts, const int32_t* n_valid,
@@ -227,11 +228,11 @@ cudaError_t launch_combine_backward(const void* dout, const void* expert_out, co
                                     void* dexpert_out, float* dtopk_w, cudaStream_t s);
 // Low-rank adapters (adapter.cu): y[t] = base[t] + scale_n (x[t] P_n) Q_n; transposed: P, Q are
 // given as [N, r, dk] and [N, dn, r].  hidden [S_max, r] receives x P when not null.  dk = 0: only
-// the indices are checked; dn = 0: only x P is computed.  partial: adapter_parts(S_max, dk) x
-// [S_max, r] floats where adapter_tall.
-constexpr int kAdapterParts = 8;
+// the indices are checked; dn = 0: only x P is computed.  partial: adapter_partial_rows(S_max) rows
+// of r floats where adapter_tall.
+constexpr int kAdapterParts = 8, kPartItems = 1216;
 bool adapter_tall(int S_max, int N, bool f16);
-int adapter_parts(int S_max, int dk);
+size_t adapter_partial_rows(int S_max);
 cudaError_t launch_adapter(const void* x, const void* P, const void* Q, const void* base, void* y,
                            float* hidden, float* partial, const float* scale, const int32_t* perm,
                            const int32_t* offsets, int* status, int dtype_f16, bool transposed,

@@ -467,37 +467,55 @@ __device__ __forceinline__ float magnitude(float v) { return v - v == 0.f ? fabs
 
 // Rounds rows x E values (m: their largest magnitude) to f16 parts of `ld` columns, lo null: one
 // part only; returns the power of two.
+// A warp takes rows; eight loads are issued before the first result is stored (the compiler cannot
+// move loads over stores that might alias them).
 template <int VEC>
 __device__ __forceinline__ float split_block(const float* src, int rows, int E, int Ep, float m, __half* hi,
                                              __half* lo, int ld) {
   const int e = scale_exp(m);                      // 0 for a block with infinities or NaN
   const float inv = exp2_int(-e);
-  const int n = Ep / VEC;
-#pragma unroll 4
-  for (int q = threadIdx.x; q < rows * n; q += kSplitThreads) {
-    const int r = q / n, c = (q - r * n) * VEC;
-    float f[VEC];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  constexpr int kW = kSplitThreads / 32, UR = VEC == 4 ? 4 : 2, UC = VEC == 4 ? 1 : 4;
+  for (int r0 = w; r0 < rows; r0 += kW * UR) {
+    for (int c0 = lane * VEC; c0 < Ep; c0 += 32 * VEC * UC) {
+      float f[UR][UC][VEC];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) f[v] = 0.f;
-    if (c < E) {
-      if (VEC == 4)
-        *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(src + r * E + c);
-      else
-        f[0] = src[r * E + c];
-    }
-    __half h[VEC], l[VEC];
+      for (int i = 0; i < UR; ++i)
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      h[v] = __float2half_rn(f[v] * inv);
-      const float b = __half2float(h[v]);
-      l[v] = isfinite(b) ? __float2half_rn((f[v] * inv - b) * kGateLo) : __ushort_as_half(0);
-    }
-    if (VEC == 4) {
-      *reinterpret_cast<uint2*>(hi + (size_t)r * ld + c) = *reinterpret_cast<const uint2*>(h);
-      if (lo) *reinterpret_cast<uint2*>(lo + (size_t)r * ld + c) = *reinterpret_cast<const uint2*>(l);
-    } else {
-      hi[(size_t)r * ld + c] = h[0];
-      if (lo) lo[(size_t)r * ld + c] = l[0];
+        for (int j = 0; j < UC; ++j) {
+          const int r = r0 + i * kW, c = c0 + j * 32 * VEC;
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) f[i][j][v] = 0.f;
+          if (r < rows && c < E) {
+            if (VEC == 4)
+              *reinterpret_cast<float4*>(f[i][j]) = *reinterpret_cast<const float4*>(src + r * E + c);
+            else
+              f[i][j][0] = src[r * E + c];
+          }
+        }
+#pragma unroll
+      for (int i = 0; i < UR; ++i)
+#pragma unroll
+        for (int j = 0; j < UC; ++j) {
+          const int r = r0 + i * kW, c = c0 + j * 32 * VEC;
+          if (r >= rows || c >= Ep) continue;
+          __half h[VEC], l[VEC];
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) {
+            const float x = f[i][j][v] * inv;
+            h[v] = __float2half_rn(x);
+            const float b = __half2float(h[v]);
+            l[v] = isfinite(b) ? __float2half_rn((x - b) * kGateLo) : __ushort_as_half(0);
+          }
+          __half* p = hi + (size_t)r * ld + c;
+          if (VEC == 4) {
+            *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(h);
+            if (lo) *reinterpret_cast<uint2*>(p + (lo - hi)) = *reinterpret_cast<const uint2*>(l);
+          } else {
+            p[0] = h[0];
+            if (lo) p[lo - hi] = l[0];
+          }
+        }
     }
   }
   return exp2_int(e);

@@ -12,7 +12,8 @@ namespace {
 constexpr size_t kAlign = 256;
 constexpr int kMaxE = 1024;
 constexpr int kMaxRank = 128;
-constexpr int kMaxRows = 1 << 30;               // rows and columns (index arithmetic in 32 bits)
+constexpr int kMaxRows = 1 << 30;               // index arithmetic in 32 bits
+constexpr int kMaxCols = 1 << 20;               // blocks along a grid's second dimension
 
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -39,16 +40,15 @@ moe_status check_adapter(int T, int d_in, int d_out, int r, int N, int S_max, mo
   if (!dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
   const int v = lane_elems(dtype);
   if (N > kMaxE || r > kMaxRank || r % 8 || d_in % v || d_out % v) return MOE_ERR_UNSUPPORTED;
-  if (T > kMaxRows || S_max > kMaxRows || d_in > kMaxRows || d_out > kMaxRows) return MOE_ERR_UNSUPPORTED;
+  if (T > kMaxRows || S_max > kMaxRows || d_in > kMaxCols || d_out > kMaxCols) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
 // [status][dh][partial h][workspace of the sums dA and dB]
-size_t hidden_bytes(int r, int S_max) { return align_up((size_t)S_max * r * sizeof(float)); }
+size_t hidden_bytes(int r, size_t rows) { return align_up(rows * r * sizeof(float)); }
 size_t adapter_sums_at(int d_in, int d_out, int r, int N, int S_max, moe_dtype dtype) {
   size_t b = kAlign + hidden_bytes(r, S_max);
-  if (adapter_tall(S_max, N, dtype == MOE_F16))
-    b += std::max(adapter_parts(S_max, d_in), adapter_parts(S_max, d_out)) * hidden_bytes(r, S_max);
+  if (adapter_tall(S_max, N, dtype == MOE_F16)) b += hidden_bytes(r, adapter_partial_rows(S_max));
   return b;
 }
 size_t adapter_bytes(int d_in, int d_out, int r, int N, int S_max, moe_dtype dtype) {
@@ -88,10 +88,10 @@ moe_status moe_gate_backward_workspace_size(int T, int d, int E, moe_dtype dtype
   if (!bytes || d < 1 || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
   moe_status st = check_router(T, E, 1);
   if (st != MOE_OK) return st;
-  if (d % lane_elems(dtype) || d > kMaxRows) return MOE_ERR_UNSUPPORTED;
+  if (d % lane_elems(dtype) || d > kMaxCols) return MOE_ERR_UNSUPPORTED;
   // the tensor-core form, and the form that leaves masked rows out
   size_t most = row_sums_bytes(d, E, 0, 0, dtype == MOE_F16, T, 1);
-  if (dtype == MOE_F16 && gate_tc_ok(E)) most = std::max(most, gate_tc_bytes(T, d, E));
+  if (dtype == MOE_F16 && gate_tc_ok(T, E)) most = std::max(most, gate_tc_bytes(T, d, E));
   *bytes = kAlign + align_up(most);
   return MOE_OK;
 }
@@ -106,7 +106,7 @@ moe_status moe_gate_topk_backward(const float* logits, const int32_t* topk_idx, 
   if (st != MOE_OK) return st;
   const bool deep = dWg || dtokens;
   if (deep && (d < 1 || !dtype_ok(dtype))) return MOE_ERR_INVALID_ARG;
-  if (deep && (d % lane_elems(dtype) || d > kMaxRows)) return MOE_ERR_UNSUPPORTED;
+  if (deep && (d % lane_elems(dtype) || d > kMaxCols)) return MOE_ERR_UNSUPPORTED;
   cudaStream_t s = as_stream(stream);
   if (T == 0) {
     if (dWg) MOE_TRY(cudaMemsetAsync(dWg, 0, (size_t)d * E * sizeof(float), s));
@@ -131,7 +131,7 @@ moe_status moe_gate_topk_backward(const float* logits, const int32_t* topk_idx, 
   int* status = deep ? static_cast<int*>(workspace) : nullptr;
   // Masked tokens may hold anything: their rows are left out of dWg's sums row by row, which the
   // tensor-core form's boxes of rows cannot do.  (It needs no mask for dtokens: dlogits are zero.)
-  const bool tc = deep && f16 && gate_tc_ok(E) && (dtokens || !token_mask);
+  const bool tc = deep && f16 && gate_tc_ok(T, E) && (dtokens || !token_mask);
   float* dWg_tc = tc && !token_mask ? dWg : nullptr;
   if (tc)
     MOE_TRY(launch_gate_tc(logits, topk_idx, dtopk_w, dlosses, counts, n_valid, token_mask, k, dlogits,
