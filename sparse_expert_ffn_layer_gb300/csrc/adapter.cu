@@ -579,34 +579,34 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
 }
 
 // ---------------------------------------------------------------- f16, short runs
-// Tiles of 16 rows, four warps that load and multiply.
-template <int MT, int R>
+// Tiles of 16 rows, four warps that load and multiply (64 requests with an adapter each, 3584
+// columns, r = 16: 11 us, of which the weights' bytes are 2; the rest is the chain of table, loads,
+// two exchanges and stores, so chunks are wide and few at low ranks).
+template <int R>
 struct Plan16 {
-  static constexpr int kThreads = MT == 64 ? 256 : 128;
-  static constexpr int kWarps = kThreads / 32;
-  static constexpr int kBlocks = R >= 128 ? (MT == 64 ? 1 : 2) : MT == 64 ? 2 : 4;  // per SM
-  static constexpr int C = 64;                                     // columns per chunk
-  static constexpr int kLdC = kRowB / 2, kLdR = R + 8;             // halves per row
-  static constexpr int WR = MT / 16, WC = kWarps / WR;             // warps along rows / columns
-  static constexpr int WN = R / WC >= 16 ? WC : 1;                 // first product: along r,
-  static constexpr int WK = WC / WN;                               // or along a chunk's columns
-  static constexpr int kW = 2 * (C * kLdR > R * kLdC ? C * kLdR : R * kLdC);
-  static constexpr int kStage = MT * kRowB + kW;
-  static constexpr int kStages = MT == 64 ? (R >= 128 ? 3 : 4) : (R >= 128 ? 4 : R >= 64 ? 6 : 8);
+  static constexpr int MT = 16, kThreads = 128, kWarps = 4;
+  static constexpr int kBlocks = R >= 128 ? 2 : 4;                 // per SM
+  static constexpr int C = R <= 32 ? 128 : 64;                     // columns per chunk
+  static constexpr int kLdC = C + 8, kLdR = R + 8;                 // halves per row
+  static constexpr int WN = R / kWarps >= 16 ? kWarps : 1;         // first product: warps along r,
+  static constexpr int WK = kWarps / WN;                           // or along a chunk's columns
+  static constexpr int kW = C * kLdR > R * kLdC ? C * kLdR : R * kLdC;
+  static constexpr int kStage = 2 * (MT * kLdC + kW);
+  static constexpr int kStages = R >= 64 && R < 128 ? 6 : 4;
   static constexpr int kOffPart = kStages * kStage;                // partial h [WK][MT][R]
   static constexpr int kOffH = kOffPart + WK * MT * R * 4;         // h
   static constexpr int kOffMult = kOffH + MT * kLdR * 2;
   static constexpr int kOffTab = kOffMult + MT * 4;                // offsets, tile starts, scratch
 };
 
-template <int MT, int R, bool kT>
-__global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlocks)
-    adapter_f16_kernel(const AdapterArgs a) {
-  using PL = Plan16<MT, R>;
-  constexpr int NT = PL::kThreads, NS = PL::kStages, C = PL::C, WC = PL::WC, WN = PL::WN, WK = PL::WK;
+template <int R, bool kT>
+__global__ void __launch_bounds__(128, Plan16<R>::kBlocks) adapter_f16_kernel(const AdapterArgs a) {
+  using PL = Plan16<R>;
+  constexpr int MT = PL::MT, NT = PL::kThreads, NS = PL::kStages, C = PL::C, WN = PL::WN, WK = PL::WK;
   constexpr int kLdC = PL::kLdC, kLdR = PL::kLdR;
-  constexpr int XP = MT * 8 / NT;                 // 16-byte pieces of x (or base) per thread and chunk
-  constexpr int WP = R * 8 / NT > 0 ? R * 8 / NT : 1;             // of P or Q
+  constexpr int CV = C / 8, RV = R / 8;           // 16-byte pieces of a chunk's row, of r
+  constexpr int XP = MT * CV / NT;                // of x (or base) per thread and chunk
+  constexpr int WP = R * CV / NT;                 // of P or Q
   extern __shared__ __align__(16) uint8_t sm[];
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank();
@@ -642,14 +642,14 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
   };
 
   // ---- loader: runs NS - 1 chunks ahead, across tiles.  Its rows' tokens are fetched a tile early.
-  const int lrow = tid >> 3, lpc = (tid & 7) * 8;
+  const int lrow = tid / CV, lpc = (tid % CV) * 8;                // pieces: rows lrow + NT / CV p
   int ltile = cid, lc = 0, ls = 0, ltok[XP], lnext[XP];
   const __half *lP = nullptr, *lQ = nullptr;
   auto begin_tile = [&]() {
 #pragma unroll
     for (int p = 0; p < XP; ++p) {
       ltok[p] = lnext[p];
-      lnext[p] = token(ltile + ncl, lrow + p * (NT / 8));
+      lnext[p] = token(ltile + ncl, lrow + p * (NT / CV));
     }
     if (ltile < ntiles) {
       const int n = group_of(ltile, start, a.N);
@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
   };
   auto issue = [&]() {
     if (ltile < ntiles && total > 0) {
-      uint8_t* st = sm + ls * PL::kStage;
+      __half* st = reinterpret_cast<__half*>(sm + ls * PL::kStage);
       const bool first = lc < nk;
       const int col0 = (first ? k0 + lc : n0 + lc - nk) * C;
       const int d = first ? a.dk : a.dn;
@@ -669,32 +669,29 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
 #pragma unroll
         for (int p = 0; p < XP; ++p) {
           const bool on = in && (unsigned)ltok[p] < (unsigned)a.T;
-          cp_async16(st + (lrow + p * (NT / 8)) * kRowB + lpc * 2,
+          cp_async16(st + (lrow + p * (NT / CV)) * kLdC + lpc,
                      rowsrc + (on ? (size_t)ltok[p] * d + col0 + lpc : 0), on);
         }
       }
-      __half* ws = reinterpret_cast<__half*>(st + MT * kRowB);
+      __half* ws = st + MT * kLdC;
       const __half* W = first ? lP : lQ;
       if (first != kT) {                          // rows of the chunk's columns, r wide
-        constexpr int RV = R / 8;
         const int row = tid / RV, col = (tid % RV) * 8;
         const __half* src = W + (size_t)(col0 + row) * a.r + col;
 #pragma unroll
         for (int p = 0; p < WP; ++p) {
           const bool on = col < a.r && col0 + row + p * (NT / RV) < d;
-          if (row + p * (NT / RV) < C)
-            cp_async16(ws + (row + p * (NT / RV)) * kLdR + col,
-                       on ? src + (size_t)p * (NT / RV) * a.r : W, on);
+          cp_async16(ws + (row + p * (NT / RV)) * kLdR + col,
+                     on ? src + (size_t)p * (NT / RV) * a.r : W, on);
         }
       } else {                                    // r rows, the chunk's columns wide
         const bool in = col0 + lpc < d;
         const __half* src = W + (size_t)lrow * d + col0 + lpc;
 #pragma unroll
         for (int p = 0; p < WP; ++p) {
-          const bool on = in && lrow + p * (NT / 8) < a.r;
-          if (lrow + p * (NT / 8) < R)
-            cp_async16(ws + (lrow + p * (NT / 8)) * kLdC + lpc,
-                       on ? src + (size_t)p * (NT / 8) * d : W, on);
+          const bool on = in && lrow + p * (NT / CV) < a.r;
+          cp_async16(ws + (lrow + p * (NT / CV)) * kLdC + lpc,
+                     on ? src + (size_t)p * (NT / CV) * d : W, on);
         }
       }
       if (++lc == total) {
@@ -707,7 +704,7 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
     ls = ls + 1 == NS ? 0 : ls + 1;
   };
 #pragma unroll
-  for (int p = 0; p < XP; ++p) lnext[p] = token(ltile, lrow + p * (NT / 8));
+  for (int p = 0; p < XP; ++p) lnext[p] = token(ltile, lrow + p * (NT / CV));
   begin_tile();
   for (int c = 0; c < NS - 1; ++c) issue();
   int cs = 0;                                     // stage of the chunk that is used next
@@ -720,10 +717,9 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
     return reinterpret_cast<const __half*>(st);
   };
 
-  const int wr = (w % PL::WR) * 16, wc = w / PL::WR;
-  // rows that this thread writes: RPT rows of its warp's 16, one 16-byte piece each
-  constexpr int LPR = 64 / WC / 8, RPT = 16 * LPR / 32;
-  const int yrow = wr + lane / LPR, ycol = wc * (64 / WC) + (lane % LPR) * 8;
+  // rows that this thread writes, one 16-byte piece of its warp's columns each
+  constexpr int WCOL = C / PL::kWarps, LPR = WCOL / 8, RPT = MT * LPR / 32;
+  const int yrow = lane / LPR, ycol = w * WCOL + (lane % LPR) * 8;
   int ynext[RPT];
 #pragma unroll
   for (int p = 0; p < RPT; ++p) ynext[p] = token(cid, yrow + p * (32 / LPR));
@@ -732,6 +728,7 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
     const int n = group_of(tile, start, a.N);
     const int s0 = bound[n] + (tile - start[n]) * MT;
     const int rows = min(MT, bound[n + 1] - s0);
+    const float scale = a.scale[n];
     int ytok[RPT];
 #pragma unroll
     for (int p = 0; p < RPT; ++p) {
@@ -739,26 +736,25 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
       ynext[p] = token(tile + ncl, yrow + p * (32 / LPR));
     }
 
-    // ---- first product: partial h of this block's input columns.
-    // The tensor cores' additions truncate: a chain of n of them loses up to n / 2^23 of the sum,
-    // always towards zero.  Chains end after a few products and are added to 32-bit sums with
-    // rounding (8192 columns in one chain per block: 3e-5 of the result; this way below 3e-6).
+    // ---- first product: partial h of this block's input columns (chains of truncating additions
+    // end after four products, see adapter_shrink_kernel)
     {
       constexpr int NF = R / WN / 8;              // 8-column fragments of h per warp
+      constexpr int KS = C / 16 / WK;             // k-steps per warp and chunk
       float acc[NF][4], run[NF][4];
 #pragma unroll
       for (int i = 0; i < NF; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = run[i][j] = 0.f;
-      const int h0 = WN > 1 ? wc * (R / WN) : 0;
+      const int h0 = WN > 1 ? w * (R / WN) : 0;
       for (int c = 0; c < nk; ++c) {
         const __half* xs = advance();
         const __half* ps = xs + MT * kLdC;
 #pragma unroll
-        for (int kk = 0; kk < 4 / WK; ++kk) {
-          const int k = (WK > 1 ? kk * WK + wc : kk) * 16;
+        for (int kk = 0; kk < KS; ++kk) {
+          const int k = (WK > 1 ? kk * WK + w : kk) * 16;
           uint32_t fa[4];
-          frag_a(fa, xs + wr * kLdC + k, kLdC, lane);
+          frag_a(fa, xs + k, kLdC, lane);
 #pragma unroll
           for (int j = 0; j < NF / 2; ++j) {
             uint32_t fb[4];
@@ -770,7 +766,7 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
             mma16816(run[2 * j + 1], fa, fb[2], fb[3]);
           }
         }
-        if (c % WK == WK - 1 || c == nk - 1) {
+        if (c % (4 / KS) == 4 / KS - 1 || c == nk - 1) {
 #pragma unroll
           for (int i = 0; i < NF; ++i)
 #pragma unroll
@@ -780,7 +776,7 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
             }
         }
       }
-      float* p = part + ((WK > 1 ? wc : 0) * MT + wr + (lane >> 2)) * R + h0 + 2 * (lane & 3);
+      float* p = part + ((WK > 1 ? w : 0) * MT + (lane >> 2)) * R + h0 + 2 * (lane & 3);
 #pragma unroll
       for (int j = 0; j < NF; ++j) {
         *reinterpret_cast<float2*>(p + 8 * j) = make_float2(acc[j][0], acc[j][1]);
@@ -798,7 +794,7 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
     }
     cl.sync();
 
-    // ---- h: this block sums rows rank * MT / 8 .. over the cluster and gives them to all
+    // ---- h: this block sums rows 2 rank, 2 rank + 1 over the cluster and gives them to all
     if (tid < MT) {                               // eight threads per row, R / 8 columns each
       constexpr int CPT = R / 8;
       const int row = rank * (MT / kCl) + (tid >> 3), c0 = (tid & 7) * CPT;
@@ -814,12 +810,6 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
           v[j] += u.x;
           v[j + 1] += u.y;
         }
-      }
-      if (a.hidden && row < rows) {
-        float* dst = a.hidden + (size_t)(s0 + row) * a.r;
-#pragma unroll
-        for (int j = 0; j < CPT; ++j)
-          if (c0 + j < a.r) dst[c0 + j] = v[j];
       }
       float m = 0.f;
       bool odd = false;
@@ -837,7 +827,7 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
       __half2 hv[CPT / 2];
 #pragma unroll
       for (int j = 0; j < CPT; j += 2) hv[j / 2] = __floats2half2_rn(v[j] * inv, v[j + 1] * inv);
-      const float mu = a.scale[n] * exp2_int(e);
+      const float mu = scale * exp2_int(e);
 #pragma unroll
       for (int q = 0; q < kCl; ++q) {
         __half* dh = cl.map_shared_rank(hs, q) + row * kLdR + c0;
@@ -845,17 +835,23 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
         for (int j = 0; j < CPT / 2; ++j) reinterpret_cast<__half2*>(dh)[j] = hv[j];
         if ((tid & 7) == 0) cl.map_shared_rank(mult, q)[row] = mu;
       }
+      if (a.hidden && row < rows) {
+        float* dst = a.hidden + (size_t)(s0 + row) * a.r;
+#pragma unroll
+        for (int j = 0; j < CPT; ++j)
+          if (c0 + j < a.r) dst[c0 + j] = v[j];
+      }
     }
     cl.sync();
 
     // ---- second product: this block's output columns
-    constexpr int NF = 8 / WC;                    // 8-column fragments of a chunk per warp
-    const int c0 = wc * NF * 8;
+    constexpr int NF = WCOL / 8;                  // 8-column fragments of a chunk per warp
+    const int c0 = w * WCOL;
     uint32_t fh[R / 16][4];
 #pragma unroll
-    for (int k = 0; k < R / 16; ++k) frag_a(fh[k], hs + wr * kLdR + k * 16, kLdR, lane);
+    for (int k = 0; k < R / 16; ++k) frag_a(fh[k], hs + k * 16, kLdR, lane);
     const int g = lane >> 2, q2 = 2 * (lane & 3);
-    const float m0 = mult[wr + g], m1 = mult[wr + g + 8];
+    const float m0 = mult[g], m1 = mult[g + 8];
     for (int c = n0; c < n1; ++c) {
       __half* bs = const_cast<__half*>(advance());
       const __half* qs = bs + MT * kLdC;
@@ -879,8 +875,8 @@ __global__ void __launch_bounds__(Plan16<MT, R>::kThreads, Plan16<MT, R>::kBlock
       // base + scale * sum, rounded once, in place; then 16-byte rows out
 #pragma unroll
       for (int j = 0; j < NF; ++j) {
-        __half2* b0 = reinterpret_cast<__half2*>(bs + (wr + g) * kLdC + c0 + 8 * j + q2);
-        __half2* b1 = reinterpret_cast<__half2*>(bs + (wr + g + 8) * kLdC + c0 + 8 * j + q2);
+        __half2* b0 = reinterpret_cast<__half2*>(bs + g * kLdC + c0 + 8 * j + q2);
+        __half2* b1 = reinterpret_cast<__half2*>(bs + (g + 8) * kLdC + c0 + 8 * j + q2);
         float2 u = make_float2(0.f, 0.f), v = u;
         if (base) {
           u = __half22float2(*b0);
@@ -1149,8 +1145,8 @@ cudaError_t launch_plan(Kern kern, const AdapterArgs& a, int MT, int threads, si
 
 template <bool kT, int R>
 cudaError_t launch_short(const AdapterArgs& a, cudaStream_t s) {
-  using PL = Plan16<16, R>;
-  return launch_plan(adapter_f16_kernel<16, R, kT>, a, 16, PL::kThreads, PL::kOffTab, s);
+  using PL = Plan16<R>;
+  return launch_plan(adapter_f16_kernel<R, kT>, a, PL::MT, PL::kThreads, PL::kOffTab, s);
 }
 // Blocks of a kernel that are resident on the device at once, asked once as resident_clusters.
 int resident_blocks(const void* kern, int threads, size_t smem) {

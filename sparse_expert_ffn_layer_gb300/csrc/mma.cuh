@@ -49,12 +49,6 @@ __device__ __forceinline__ void stsm4(void* p, const uint32_t (&r)[4]) {
 
 // The same from shared-memory addresses (bytes): loops that step through a ring keep one base and
 // constant offsets instead of a generic pointer per load.
-__device__ __forceinline__ void ldsm4_at(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
 __device__ __forceinline__ void ldsm4_t_at(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -90,10 +84,6 @@ __device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a
 // `a` operand with rows = m, columns = k.
 __device__ __forceinline__ void frag_a(uint32_t (&r)[4], const __half* s, int ld, int lane) {
   ldsm4(r, s + (lane & 15) * ld + (lane >> 4) * 8);
-}
-// `a` operand stored transposed: rows = k, columns = m.
-__device__ __forceinline__ void frag_a_t(uint32_t (&r)[4], const __half* s, int ld, int lane) {
-  ldsm4_t(r, s + ((lane & 7) + (lane >> 4) * 8) * ld + ((lane >> 3) & 1) * 8);
 }
 // Two adjacent `b` operands (16 columns): r[0..1] the first eight, r[2..3] the next.
 // Stored with rows = k, columns = n:
