@@ -390,7 +390,8 @@ def tiny(dt):
 ADAPT = [("f16", 1, 8, 8, 8, 1), ("f16", 1, 1024, 1024, 16, 32), ("f16", 2, 64, 8, 8, 3), ("f16", 17, 72, 136, 24, 2),
          ("f16", 64, 3584, 264, 16, 64), ("f16", 100, 520, 1000, 40, 1), ("f16", 300, 128, 2048, 64, 5),
          ("f16", 333, 1032, 72, 128, 3), ("f16", 1000, 256, 256, 8, 1000), ("f16", 2000, 200, 328, 104, 7),
-         ("f16", 4097, 512, 512, 32, 2), ("f16", 65, 128, 128, 128, 1024), ("f32", 1, 4, 4, 8, 1),
+         ("f16", 4097, 512, 512, 32, 2), ("f16", 500, 136, 200, 8, 2), ("f16", 3000, 2048, 64, 16, 4),
+         ("f16", 700, 64, 1032, 48, 20), ("f16", 65, 128, 128, 128, 1024), ("f32", 1, 4, 4, 8, 1),
          ("f32", 128, 64, 256, 8, 4), ("f32", 33, 68, 100, 24, 3), ("f32", 500, 1028, 36, 64, 9),
          ("f32", 70, 128, 260, 128, 2), ("f32", 1111, 32, 32, 16, 1)]
 
@@ -580,6 +581,92 @@ def test_adapter_rows_behind_the_last_slot_and_bad_indices(m):
     # no adapter at all
     st, out, hid = fwd(c["perm"], torch.zeros(N + 1, dtype=torch.int32, device="cuda"))
     assert st == m.MOE_OK and (out == 3.0).all() and (hid == 3.0).all()
+
+
+def test_adapter_few_tokens_of_many(m):
+    """Most tokens without an adapter: the plans go by the caller's bound, the work by the offsets."""
+    g = gen(21)
+    T, di, do, r, N = 6000, 520, 1048, 24, 3
+    dt = torch.float16
+    c = adapter_inputs(m, g, dt, T, di, do, r, N, none=0.97)
+    ws = adapter_ws(m, T, di, do, r, N, dt)
+    out, hid = c["base"].clone(), torch.full((T, r), 4.0, device="cuda")
+    m.moe_adapter_forward(c["x"], c["perm"], c["off"], c["A"], c["B"], c["scale"], out, ws, base=out, hidden=hid)
+    dA, dB = torch.empty((N, di, r), device="cuda"), torch.empty((N, r, do), device="cuda")
+    m.moe_adapter_backward(c["base"], c["x"], hid, c["perm"], c["off"], c["A"], c["B"], c["scale"], ws, dA=dA, dB=dB)
+    S = int(c["off"][-1])
+    assert 50 < S < 400 and (hid[S:] == 4.0).all()
+    # the same tokens as a batch of their own give the same bits of what belongs to a row
+    t = c["perm"][:S].long()
+    x2, b2 = c["x"][t].contiguous(), c["base"][t].contiguous()
+    perm2 = torch.arange(S, device="cuda", dtype=torch.int32)
+    ws2 = adapter_ws(m, S, di, do, r, N, dt)
+    out2, hid2 = b2.clone(), torch.empty((S, r), device="cuda")
+    m.moe_adapter_forward(x2, perm2, c["off"], c["A"], c["B"], c["scale"], out2, ws2, base=out2, hidden=hid2)
+    K = 2 * (4 * (di / 512 + 1) + 16)
+    a = c["ids"][t].long()
+    hm = torch.einsum("ti,tij->tj", x2.double().abs(), c["A"].double().abs()[a])
+    check(hid[:S], hid2.double(), 2 * K * U * hm, "hidden")
+    check(out[t], out2.double(), 2.0 ** -10 * out2.double().abs() + 2.0 ** -24 +
+          2.0 ** -10 * c["scale"].double().abs()[a][:, None] *
+          torch.einsum("tj,tjo->to", hid2.double().abs(), c["B"].double().abs()[a]), "out")
+    for n in range(N):
+        s = (a == n).nonzero()[:, 0]
+        dy, x = c["base"][t[s]].double(), x2[s].double()
+        dhm = dy.abs() @ c["B"][n].double().abs().t()
+        want = float(c["scale"][n]) * x.t() @ (dy @ c["B"][n].double().t())
+        Kd = 2 * (4 * (do / 512 + 1) + 16) + 64 + len(s) / 64
+        check(dA[n], want, abs(float(c["scale"][n])) * (Kd * U * (x.abs().t() @ dhm) +
+              2 * U * x.abs().sum(0)[:, None] * dhm.max()) + 1e-37, "dA")
+
+
+def test_offsets_past_32_bits(m):
+    """Rows whose elements lie behind 2^31: 4.4 GB per matrix."""
+    T, d, r, N, E = 620_000, 3584, 8, 2, 4
+    dt = torch.float16
+    x = torch.empty((T, d), dtype=dt, device="cuda").normal_()
+    rows = torch.cat([torch.arange(3), torch.arange(599_180, 599_190), torch.arange(T - 200, T)]).cuda()
+    g = gen(31)
+    ids = (torch.arange(T, device="cuda", dtype=torch.int32) % 3) - 1
+    perm, off = plan(m, ids, N)
+    A, B = randn(g, N, d, r, sigma=d ** -0.5, dtype=dt), randn(g, N, r, d, sigma=0.3, dtype=dt)
+    scale = torch.tensor([0.5, -1.5], device="cuda")
+    ws = adapter_ws(m, T, d, d, r, N, dt)
+    out = x.clone()
+    m.moe_adapter_forward(x, perm, off, A, B, scale, out, ws, base=out)
+    xs, a = x[rows].double(), ids[rows].long()
+    delta = torch.einsum("ti,tij,tjo->to", xs, A.double()[a.clamp(min=0)], B.double()[a.clamp(min=0)])
+    want = xs + delta * (scale.double()[a.clamp(min=0)] * (a >= 0))[:, None]
+    mag = torch.einsum("ti,tij,tjo->to", xs.abs(), A.double().abs()[a.clamp(min=0)], B.double().abs()[a.clamp(min=0)])
+    check(out[rows], want, 2.0 ** -11 * (1 + 2 ** -9) * want.abs() + 2.0 ** -25 + 1.5 * mag * (256 * U) +
+          1.5 * 2.0 ** -11 * torch.einsum("tj,tjo->to", torch.einsum("ti,tij->tj", xs, A.double()[a.clamp(min=0)]).abs(),
+                                          B.double().abs()[a.clamp(min=0)]), "out")
+    # gate: dtokens row by row, dWg over all rows
+    Wg = randn(g, d, E, sigma=0.1)
+    logits = randn(g, T, E)
+    idx, dw = topk(logits, 1), randn(g, T, 1)
+    dl, dWg, dx = torch.empty((T, E), device="cuda"), torch.empty((d, E), device="cuda"), out
+    gws = torch.empty(m.moe_gate_backward_workspace_size(T, d, E, dt), dtype=torch.uint8, device="cuda")
+    m.moe_gate_topk_backward(logits, idx, dl, dtopk_w=dw, tokens=x, Wg=Wg, dWg=dWg, dtokens=dx, workspace=gws)
+    assert m.moe_status_read(gws) == m.MOE_OK
+    want = dl[rows].double() @ Wg.double().t()
+    mag = dl[rows].double().abs() @ Wg.double().abs().t()
+    check(dx[rows], want, 2.0 ** -11 * 1.01 * (want.abs() + mag) + 2.0 ** -24, "dtokens")
+    want, mag = torch.zeros((d, E), dtype=torch.double, device="cuda"), torch.zeros((d, E), dtype=torch.double, device="cuda")
+    for c in range(0, T, 20_000):
+        xd, dd = x[c:c + 20_000].double(), dl[c:c + 20_000].double()
+        want += xd.t() @ dd
+        mag += xd.abs().t() @ dd.abs()
+    check(dWg, want, (80 + T / 128 / 8) * U * mag, "dWg")
+    # combine: slots in reverse order, so that high slots meet low tokens
+    slot = torch.arange(T - 1, -1, -1, device="cuda", dtype=torch.int32).view(T, 1)
+    w = torch.rand((T, 1), generator=g, device="cuda")
+    dy, dwo = torch.empty_like(x), torch.empty((T, 1), device="cuda")
+    m.moe_combine_backward(x, out, slot, w, dy, dwo)
+    s = slot[rows, 0].long()
+    check(dy[s], w[rows].double() * xs, 2.0 ** -11 * 1.01 * (w[rows].double() * xs).abs() + 2.0 ** -25, "dexpert_out")
+    prod = xs * out[s].double()
+    check(dwo[rows, 0], prod.sum(1), 128 * U * prod.abs().sum(1), "dtopk_w")
 
 
 def test_empty_batches(m):
