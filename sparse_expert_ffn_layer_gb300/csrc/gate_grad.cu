@@ -6,9 +6,9 @@
 // 2^-36 of the block's largest magnitude).  The products with hi and with lo go to separate
 // accumulators, joined as D1 + 2^-11 D2 in 32 bits.  X is f16 and exact, so dWg keeps the accuracy of
 // a 32-bit sum.  Wg is rounded to f16 once (scaled by 128 rows, so that none is lost below f16's
-// range): dX is f16, and the rounding adds at most 2^-11 of the sum of |dL Wg| to its own 2^-11.
-// (Wg split as well, with a third product: twice the bytes from L2 per tile, dX 73 us instead of
-// %DX% at 16384 x 3584 x 128.)  The split comes with the logits' gradient (router_loss.cu).
+// range): dX is f16, and the rounding adds at most 2^-11 of the sum of |dL Wg| to its own 2^-11.  (With
+// Wg split as well, a third product, each tile took twice the bytes from L2.)  The split comes with
+// the logits' gradient (router_loss.cu).
 //
 // Both kernels: one block per SM; warp 0 loads by TMA, warp 1 issues the products, eight warps read
 // the accumulators.  Every wait is bounded (common.cuh).

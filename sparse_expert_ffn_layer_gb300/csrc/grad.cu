@@ -208,9 +208,9 @@ __global__ void __launch_bounds__(kSumThreads) split_rows_kernel(const SumArgs a
     float m = 0.f;
     for (int q = tid; q < kRows * n4; q += kSumThreads) {
       const float4 v = load(q);
-      const float big = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-      // NaN is not seen by fmaxf: v - v is 0 unless a value is infinite or NaN
-      m = (v.x - v.x) + (v.y - v.y) + (v.z - v.z) + (v.w - v.w) == 0.f ? fmaxf(m, big) : INFINITY;
+      // of the finite values: infinities and NaN need no scale, and must not take the others' away
+      auto mag = [](float f) { return f - f == 0.f ? fabsf(f) : 0.f; };
+      m = fmaxf(m, fmaxf(fmaxf(mag(v.x), mag(v.y)), fmaxf(mag(v.z), mag(v.w))));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));

@@ -9,7 +9,7 @@ namespace moe {
 // Group boundaries as the kernels use them, and the tile starts.  bound[n] = the largest of
 // offsets[0 .. n], clamped to [0, S_max]: runs never overlap and no slot lies outside the
 // buffers, whatever the offsets say.  start[n] = number of tiles of the groups before n.
-// All threads of the block (at most 8 warps); N <= 1024; scratch: 16 words.
+// All threads of the block (at most 16 warps); N <= 1024; scratch: 24 words.
 template <int kThreads>
 __device__ __forceinline__ void group_table(const int32_t* __restrict__ offsets, int N, int S_max,
                                             int MT, int* bound, int* start, int* scratch) {

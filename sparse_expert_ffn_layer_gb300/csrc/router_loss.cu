@@ -11,7 +11,7 @@
 // Both are one pass over [T, E] in 32 bits, bound by DRAM (4 bytes read per element, 4 more
 // written by the gradient).  A row is held in registers by LANES lanes with 16 (E > 512: 32) values
 // each: a row's reductions are log2(LANES) shuffles (with 8 values per lane the shuffles bound the
-// passes: moe_balance_loss's over 262144 x 128 logits 40 us instead of %ROWS%).  The columns of a lane
+// passes: moe_balance_loss's over 262144 x 128 logits 40 us instead of 28).  The columns of a lane
 // never change, so column sums (forward) and a_e (backward) stay in registers too.
 #include <cooperative_groups.h>
 
@@ -70,7 +70,7 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, i
 
 // Softmax in place: x becomes p (exp_row: p / inv); returns lse.  The exponentials are the hardware's (2 ulp and
 // 2^-23 of |x - m| relative: small where p matters); with expf the arithmetic, not DRAM, bound the
-// pass over 262144 x 128 logits (31 us instead of %ROWS%).  A row of -inf only has p = 0 and lse = 0 (it
+// pass over 262144 x 128 logits (31 us instead of 28).  A row of -inf only has p = 0 and lse = 0 (it
 // adds nothing to either loss); NaN and +inf give NaN as the formula does.
 template <int LANES, int N>
 __device__ __forceinline__ float exp_row(float (&x)[N], float& inv) {
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kRowThreads, VEC * J > 16 ? 1 : 2) balance_row
   float z = 0.f;
   int n = 0;
   const int64_t stride = (int64_t)gridDim.x * kRowWarps * RPW;
-  // (Fetching the next row ahead costs a third of the warps in registers: 32 us instead of %ROWS%.)
+  // (Fetching the next row ahead costs a third of the warps in registers: 32 us instead of 28.)
   for (int64_t base = ((int64_t)blockIdx.x * kRowWarps + w) * RPW; base < T; base += stride) {
     const int64_t t = base + g;
     const bool on = t < T && (!mask || mask[t]);
@@ -453,7 +453,8 @@ struct SplitOut {
 };
 constexpr int kSplitThreads = 512;
 
-// Largest magnitude in the block; infinity when any value is infinite or NaN.
+// Largest magnitude in the block (of its finite values: infinities and NaN need no scale, and must
+// not take the others' away).
 __device__ __forceinline__ float block_max(float m, float* scratch) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -463,7 +464,7 @@ __device__ __forceinline__ float block_max(float m, float* scratch) {
   for (int q = 0; q < kSplitThreads / 32; ++q) m = fmaxf(m, scratch[q]);
   return m;
 }
-__device__ __forceinline__ float magnitude(float v) { return v - v == 0.f ? fabsf(v) : INFINITY; }
+__device__ __forceinline__ float magnitude(float v) { return v - v == 0.f ? fabsf(v) : 0.f; }
 
 // Rounds rows x E values (m: their largest magnitude) to f16 parts of `ld` columns, lo null: one
 // part only; returns the power of two.
@@ -472,7 +473,7 @@ __device__ __forceinline__ float magnitude(float v) { return v - v == 0.f ? fabs
 template <int VEC>
 __device__ __forceinline__ float split_block(const float* src, int rows, int E, int Ep, float m, __half* hi,
                                              __half* lo, int ld) {
-  const int e = scale_exp(m);                      // 0 for a block with infinities or NaN
+  const int e = scale_exp(m);
   const float inv = exp2_int(-e);
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   constexpr int kW = kSplitThreads / 32, UR = VEC == 4 ? 4 : 2, UC = VEC == 4 ? 1 : 4;

@@ -310,6 +310,35 @@ def test_gate_backward_masked_rows_and_in_place(m):
     assert not dWg0.any()
 
 
+@pytest.mark.parametrize("T", [40, 300])
+def test_gate_backward_infinities_stay_where_they_are(m, T):
+    """A token whose gradient is NaN spoils its own row of dtokens and nothing of the others'."""
+    g = gen(T)
+    d, E = 136, 20
+    x, Wg, logits, idx, dw = gate_inputs(g, torch.float16, T, d, E, 2)
+    dw *= 1e-7                                       # small beside what a NaN might leave unscaled
+    ws = torch.empty(m.moe_gate_backward_workspace_size(T, d, E, x.dtype), dtype=torch.uint8, device="cuda")
+    out = []
+    for bad in (False, True):
+        if bad:
+            logits = logits.clone()
+            logits[5, 3] = float("nan")
+        dl, dWg = torch.empty((T, E), device="cuda"), torch.empty((d, E), device="cuda")
+        dx = torch.empty((T, d), dtype=torch.float16, device="cuda")
+        m.moe_gate_topk_backward(logits, idx, dl, dtopk_w=dw * 1e3, tokens=x, Wg=Wg, dWg=dWg, dtokens=dx, workspace=ws)
+        out.append((dl, dWg, dx))
+    keep = torch.arange(T, device="cuda") != 5
+    assert out[1][2][5].isnan().any() and torch.equal(out[1][2][keep], out[0][2][keep])
+    assert torch.equal(out[1][0][keep], out[0][0][keep])
+    # columns of dWg that no NaN reaches are those of the batch without that token
+    clean = ~out[1][0][5].isnan()
+    dd = out[1][0][keep].double()
+    want, mag = x[keep].double().t() @ dd, x[keep].double().abs().t() @ dd.abs()
+    add = x[5].double()[:, None] * out[1][0][5].double().nan_to_num()[None]
+    tol = 80 * U * (mag + add.abs() + x.double().abs().sum(0)[:, None] * dd.abs().max())
+    check(out[1][1][:, clean], (want + add)[:, clean], tol[:, clean], "dWg")
+
+
 # ---------------------------------------------------------------- combine
 @pytest.mark.parametrize("dt", [torch.float16, torch.float32])
 @pytest.mark.parametrize("T,d,k", [(1, 8, 1), (3, 7, 2), (64, 128, 2), (129, 1001, 1), (1000, 264, 2),
@@ -544,6 +573,21 @@ def test_adapter_wide_range_and_infinities(m, T):
     out2, _ = fwd(x2)
     assert not torch.isfinite(out2[1]).any() and out2[2].isnan().all()
     assert torch.equal(out2[0], out[0]) and torch.equal(out2[3:], out[3:])
+    # a NaN in one column of hidden reaches that column of dB only, whatever its rows' scale
+    hid2 = torch.randn(hid.shape, generator=g, device="cuda") * 1e-6
+    dy = randn(g, T, 128, dtype=torch.float16)
+    dB = [torch.empty((1, 16, 128), device="cuda") for _ in range(2)]
+    for q in range(2):
+        if q:
+            hid2[2, 7] = float("nan")
+        m.moe_adapter_backward(dy, c["x"], hid2, c["perm"], c["off"], c["A"], c["B"], c["scale"], ws, dB=dB[q])
+    keep = torch.arange(16, device="cuda") != 7
+    assert dB[1][0, 7].isnan().all()
+    t = c["perm"].long()
+    want = 1e-4 * hid2.double().t() @ dy[t].double()
+    mag = 1e-4 * hid2.double().nan_to_num().abs().t() @ dy[t].double().abs().clamp(min=2.0 ** -14)
+    slack = 1e-4 * dy[t].double().abs().clamp(min=2.0 ** -14).sum(0) * hid2.nan_to_num().abs().max()
+    check(dB[1][0][keep], want[keep], 80 * U * mag[keep] + 2 * U * slack + 1e-37, "dB")
 
 
 def test_adapter_rows_behind_the_last_slot_and_bad_indices(m):
