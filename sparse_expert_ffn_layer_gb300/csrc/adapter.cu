@@ -98,9 +98,9 @@ constexpr int kChunk = 64;                        // columns per chunk
 
 template <int R>
 struct PlanTall {
-  // Chunks per stage of the ring: two for low ranks, where what a stage costs beside its products
+  // Chunks per stage of the ring: two up to rank 64, where what a stage costs beside its products
   // (waits, addresses) was most of the instructions.
-  static constexpr int kSub = R <= 32 ? 2 : 1;
+  static constexpr int kSub = R <= 64 ? 2 : 1;
   static constexpr int kSubB = kTallRows * 128 + kChunk * R * 2;   // rows, weights
   static constexpr int kStage = kSub * kSubB;
   static constexpr int kStages = (96 * 1024) / kStage;             // two blocks per SM
