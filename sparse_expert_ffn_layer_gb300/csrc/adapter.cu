@@ -431,13 +431,15 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
   __half* Y = static_cast<__half*>(a.y);
   const int wr = (w & 3) * 16, wc = w >> 2;
   const int l15 = lane & 15, lh = lane >> 4, l3 = (lane >> 3) & 1, l7 = lane & 7;
-  // rows that this thread writes: two of its warp's 16, one 16-byte piece each
-  const int yrow = wr + (lane >> 2), ypc = wc * 4 + (lane & 3);
+  // Rows that this thread writes: two of the 16 that its warp and the one beside it computed, one
+  // 16-byte piece each, so that eight lanes write a whole 128-byte line (four lanes on 64 bytes:
+  // 58 us for 16384 x 3584 at r = 64; eight rows at once: 73).
+  const int yrow = wr + wc * 8 + (lane >> 3), ypc = l7;
   for (int item = blockIdx.x; item < ring.items; item += ring.blocks) {
     const int tile = item / ring.parts, part = item - tile * ring.parts;
     const int n = group_of(tile, ring.start, a.N);
     const int s0 = ring.bound[n] + (tile - ring.start[n]) * MT, s1 = ring.bound[n + 1];
-    int y0 = s0 + yrow < s1 ? a.perm[s0 + yrow] : -1, y1 = s0 + yrow + 8 < s1 ? a.perm[s0 + yrow + 8] : -1;
+    int y0 = s0 + yrow < s1 ? a.perm[s0 + yrow] : -1, y1 = s0 + yrow + 4 < s1 ? a.perm[s0 + yrow + 4] : -1;
     if ((unsigned)y0 >= (unsigned)a.T) y0 = -1;
     if ((unsigned)y1 >= (unsigned)a.T) y1 = -1;
     // ---- h in the layout of the product's left operand: rows g and g + 8, columns
@@ -562,7 +564,7 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
         }
         stsm4(at, b);
       }
-      __syncwarp();
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + (w & 3)) : "memory");   // the two warps of these rows
       const int col = (c * PL::kSub + u) * kChunk + ypc * 8;
       if (col < a.dn) {
         if (y0 >= 0)
@@ -570,7 +572,7 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
               *reinterpret_cast<const uint4*>(bs + swz<128>(yrow, ypc));
         if (y1 >= 0)
           *reinterpret_cast<uint4*>(Y + (size_t)y1 * a.dn + col) =
-              *reinterpret_cast<const uint4*>(bs + swz<128>(yrow + 8, ypc));
+              *reinterpret_cast<const uint4*>(bs + swz<128>(yrow + 4, ypc));
       }
       }
       ring.done();
