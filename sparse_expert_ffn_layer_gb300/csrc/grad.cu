@@ -126,7 +126,7 @@ __device__ __forceinline__ SumItem sum_item(const SumArgs& a, const Segments& g,
 template <int MI, int NJ>
 __device__ __forceinline__ void store_sums(const SumItem& it, int i, int j, float (&v)[MI][NJ][4]) {
   const int di = it.jb->di, dj = it.jb->dj;
-  const bool tr = it.jb->transposed;
+  const bool tr = it.jb->transposed, pairs = !tr && dj % 2 == 0;   // j is even
   const int64_t si = tr ? 1 : dj, sj = tr ? di : 1;
   float* p = it.dst + i * si + j * sj;
 #pragma unroll
@@ -138,6 +138,10 @@ __device__ __forceinline__ void store_sums(const SumItem& it, int i, int j, floa
 #pragma unroll
       for (int b = 0; b < NJ; ++b) {
         const float x = it.scale * v[a][b][2 * q], y = it.scale * v[a][b][2 * q + 1];
+        if (pairs) {
+          if (j + 8 * b < dj) *reinterpret_cast<float2*>(r + 8 * b) = make_float2(x, y);
+          continue;
+        }
         if (j + 8 * b < dj) r[8 * b * sj] = x;
         if (j + 8 * b + 1 < dj) r[(8 * b + 1) * sj] = y;
       }
