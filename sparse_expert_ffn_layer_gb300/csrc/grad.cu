@@ -496,9 +496,17 @@ __global__ void __launch_bounds__(256) row_sum_join_kernel(const SumArgs a) {
   const SumJob& jb = a.job[blockIdx.z];
   const int n = blockIdx.y;
   int lo = 0, hi = a.S_max;
-  if (a.offsets) {                                 // as group_table clamps them
-    lo = min(max(a.offsets[n], 0), a.S_max);
-    hi = max(lo, min(max(a.offsets[n + 1], 0), a.S_max));
+  if (a.offsets) {                                 // as group_table: clamped, a running maximum
+    __shared__ int top[8];
+    auto bound = [&](int i) { return min(max(a.offsets[i], 0), a.S_max); };
+    hi = bound(n + 1);
+    for (int i = threadIdx.x; i <= n; i += 256) lo = max(lo, bound(i));
+    lo = __reduce_max_sync(0xffffffffu, lo);
+    if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = lo;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 8; ++q) lo = max(lo, top[q]);
+    hi = max(lo, hi);
   }
   const int segs = (hi - lo + a.seg - 1) / a.seg;
   if (segs < 2 || !jb.G) return;

@@ -627,6 +627,39 @@ def test_adapter_rows_behind_the_last_slot_and_bad_indices(m):
     assert st == m.MOE_OK and (out == 3.0).all() and (hid == 3.0).all()
 
 
+@pytest.mark.parametrize("dt", [torch.float16, torch.float32])
+def test_adapter_gradients_under_decreasing_offsets(m, dt):
+    """Offsets that decrease are reported, and the sums are those of the runs that the other products
+    take: a boundary is the largest offset up to it.  (Long runs: their partial sums are joined.)"""
+    g = gen(31)
+    T, d, r, N = 1900, 64, 16, 5
+    c = adapter_inputs(m, g, dt, T, d, d, r, N, none=0.0)
+    ws = adapter_ws(m, T, d, d, r, N, dt)
+    off = torch.tensor([0, 1100, 100, 1500, 1200, T], dtype=torch.int32, device="cuda")
+    bound = [0, 1100, 1100, 1500, 1500, T]
+    dy, hid = randn(g, T, d, dtype=dt), randn(g, T, r)
+    dA, dB = torch.full((N, d, r), 7.0, device="cuda"), torch.full((N, r, d), 7.0, device="cuda")
+    m.moe_adapter_backward(dy, c["x"], hid, c["perm"], off, c["A"], c["B"], c["scale"], ws, dA=dA, dB=dB)
+    assert m.moe_status_read(ws) == m.MOE_ERR_DEVICE_BOUNDS
+    for n in range(N):
+        s = slice(bound[n], bound[n + 1])
+        t, sc = c["perm"][s].long(), float(c["scale"][n])
+        x, y, h, B = c["x"][t].double(), dy[t].double(), hid[s].double(), c["B"][n].double()
+        dh, dhm = y @ B.t(), y.abs() @ B.abs().t()
+        if not len(t):
+            assert not dA[n].any() and not dB[n].any()
+            continue
+        # as in test_adapter_backward
+        half = dt == torch.float16
+        K = 2 * (4 * (d / 512 + 1) + 16) if half else d / 8 + 48
+        KW = 64 + len(t) / 64 if half else len(t) + 16
+        yf = torch.where(y == 0, y, y.abs().clamp(min=2.0 ** -14)) if half else y.abs()
+        sa = x.abs().sum(0)[:, None] * dh.abs().max() if half else 0
+        sb = yf.sum(0)[None, :] * h.abs().max() if half else 0
+        check(dA[n], sc * (x.t() @ dh), abs(sc) * ((KW + K) * U * (x.abs().t() @ dhm) + 2 * U * sa) + 1e-37, "dA")
+        check(dB[n], sc * (h.t() @ y), abs(sc) * (KW * U * (h.abs().t() @ yf) + 2 * U * sb) + 1e-37, "dB")
+
+
 def test_adapter_few_tokens_of_many(m):
     """Most tokens without an adapter: the plans go by the caller's bound, the work by the offsets."""
     g = gen(21)
