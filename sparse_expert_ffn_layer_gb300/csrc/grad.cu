@@ -250,9 +250,9 @@ struct SumPlan {
   static constexpr int kStages = R == 64 ? 3 : 4;                  // two blocks per SM (R = 128: one)
 };
 
-// kPerm: rows through perm.  Rows behind a segment's end and entries outside [0, T) then read some
-// row that is there; their h is zero.  Otherwise the rows are the slots, and masked ones read as
-// zeros (they may hold anything).
+// kPerm: rows through perm.  Rows behind a segment's end then read its last one again (their h is
+// zero), and entries outside [0, T) read as zeros.  Otherwise the rows are the slots, and masked ones
+// read as zeros (they may hold anything).
 template <int R, bool kPerm>
 __global__ void __launch_bounds__(SumWarps<R>::kThreads, R >= 128 ? 1 : 2) row_sum_f16_kernel(const SumArgs a, int ldh) {
   constexpr int NT = SumWarps<R>::kThreads, XP = kRows * 16 / NT;   // 16-byte pieces of x per thread
@@ -310,8 +310,9 @@ __global__ void __launch_bounds__(SumWarps<R>::kThreads, R >= 128 ? 1 : 2) row_s
 #pragma unroll
       for (int p = 0; p < XP; ++p) {
         if (kPerm) {
-          const uint32_t t = (unsigned)lrow[p] < (unsigned)a.T ? lrow[p] : 0;
-          cp_async16_at(dst + NT / 16 * p * kLdX * 2, lX + (uint64_t)t * (uint32_t)ldi, true);
+          const bool on = (unsigned)lrow[p] < (unsigned)a.T;
+          const uint32_t t = on ? lrow[p] : 0;
+          cp_async16_at(dst + NT / 16 * p * kLdX * 2, lX + (uint64_t)t * (uint32_t)ldi, on);
         } else {
           const bool on = lin && lrow[p] >= 0;
           cp_async16_at(dst + NT / 16 * p * kLdX * 2, on ? lX + (uint64_t)(uint32_t)lrow[p] * (uint32_t)ldi : lX, on);

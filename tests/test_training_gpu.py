@@ -660,6 +660,57 @@ def test_adapter_gradients_under_decreasing_offsets(m, dt):
         check(dB[n], sc * (h.t() @ y), abs(sc) * (KW * U * (h.abs().t() @ yf) + 2 * U * sb) + 1e-37, "dB")
 
 
+@pytest.mark.parametrize("dt", [torch.float16, torch.float32])
+@pytest.mark.parametrize("T", [40, 700])
+def test_adapter_bad_entries_take_nothing_into_the_gradients(m, dt, T):
+    """Entries outside [0, T) are left out of every sum, whatever a token without an adapter holds."""
+    g = gen(37 + T)
+    d, r, N = 64, 16, 2
+    c = adapter_inputs(m, g, dt, T, d, d, r, N, none=0.0)
+    ws = adapter_ws(m, T, d, d, r, N, dt)
+    ids = c["ids"].clone()
+    ids[0] = -1
+    perm, off = plan(m, ids, N)
+    S = T - 1
+    assert int(off[-1]) == S
+    bad = perm.clone()
+    lost = torch.tensor([0, 3, 5, S - 1], device="cuda")
+    bad[lost] = torch.tensor([-1, T, 1 << 30, -(1 << 30)], dtype=torch.int32, device="cuda")
+    x, dy, hid = c["x"].clone(), randn(g, T, d, dtype=dt), randn(g, T, r)
+    x[0], dy[0] = float("nan"), float("inf")
+    dx = torch.full((T, d), 9.0, dtype=dt, device="cuda")
+    got = []
+    for h in (hid, hid.clone().index_fill_(0, lost, 0.0)):
+        # the second call names row 1 in the slots that the first skips, with nothing to add
+        dA, dB = torch.empty((N, d, r), device="cuda"), torch.empty((N, r, d), device="cuda")
+        p = bad if h is hid else bad.clone().index_fill_(0, lost, 1)
+        m.moe_adapter_backward(dy, x, h, p, off, c["A"], c["B"], c["scale"], ws, dtokens=dx if h is hid else None,
+                               dA=dA, dB=dB)
+        assert m.moe_status_read(ws) == (m.MOE_ERR_DEVICE_BOUNDS if h is hid else m.MOE_OK)
+        got.append((dA, dB))
+    for n in range(N):
+        s = torch.arange(int(off[n]), int(off[n + 1]), device="cuda")
+        s = s[~torch.isin(s, lost)]
+        t, sc = perm[s].long(), float(c["scale"][n])
+        xx, y, B = x[t].double(), dy[t].double(), c["B"][n].double()
+        dh, dhm = y @ B.t(), y.abs() @ B.abs().t()
+        half = dt == torch.float16
+        K = (2 * (4 * (d / 512 + 1) + 16) if half else d / 8 + 48) + (64 + len(t) / 64 if half else len(t) + 16)
+        slack = xx.abs().sum(0)[:, None] * dh.abs().max() if half else 0
+        check(got[0][0][n], sc * (xx.t() @ dh), abs(sc) * (K * U * (xx.abs().t() @ dhm) + 2 * U * slack) + 1e-37, "dA")
+        assert torch.isfinite(got[0][1][n]).all()
+        h = hid[s].double()
+        want = sc * (h.t() @ y)
+        yf = torch.where(y == 0, y, y.abs().clamp(min=2.0 ** -14)) if half else y.abs()
+        tol = abs(sc) * (K * U * (h.abs().t() @ yf) + (2 * U * yf.sum(0)[None, :] * h.abs().max() if half else 0)) + 1e-37
+        check(got[0][1][n], want, tol, "dB")
+        check(got[1][1][n], want, tol, "dB with zero rows")
+    rest = torch.ones(T, dtype=torch.bool, device="cuda")
+    rest[perm[:S].long()] = False
+    rest[perm[lost].long()] = True
+    assert (dx[rest] == 9.0).all()
+
+
 def test_adapter_few_tokens_of_many(m):
     """Most tokens without an adapter: the plans go by the caller's bound, the work by the offsets."""
     g = gen(21)
