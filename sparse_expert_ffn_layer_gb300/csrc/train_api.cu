@@ -168,6 +168,7 @@ moe_status moe_combine_backward(const void* dout, const void* expert_out, const 
   return guarded([&]() -> moe_status {
     if (T < 0 || d < 1 || S_max < 0 || (k != 1 && k != 2)) return MOE_ERR_INVALID_ARG;
     if (!dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+    if (T > kMaxRows || d > kMaxCols) return MOE_ERR_UNSUPPORTED;
     if (T == 0) return MOE_OK;
     if (!dexpert_out && !dtopk_w) return MOE_ERR_INVALID_ARG;
     if (!dout || !slot_of || (dexpert_out && !topk_w) || (dtopk_w && !expert_out && S_max > 0))

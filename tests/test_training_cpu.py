@@ -83,6 +83,12 @@ def test_combine_backward_refusals(m):
     assert comb(T=0) == m.MOE_OK
 
 
+def test_combine_backward_refuses_lengths_beyond_its_indices(m):
+    f = m.lib.moe_combine_backward
+    for T, d in [((1 << 31) - 1, 8), ((1 << 30) + 1, 8), (8, (1 << 31) - 8), (8, (1 << 20) + 8)]:
+        assert f(P, P, P, P, 1, T, d, 1, 8, P, P, S0) == m.MOE_ERR_UNSUPPORTED
+
+
 def test_adapter_refusals(m):
     f, b = m.lib.moe_adapter_forward, m.lib.moe_adapter_backward
 
