@@ -309,7 +309,11 @@ MOE_API moe_status moe_gate_backward_workspace_size(int T, int d, int E, moe_dty
  *   dWg nullable (then tokens is not read), dtokens nullable (then Wg is not read), dtokens_in
  *   nullable (zero; may be dtokens itself).
  *   workspace: moe_gate_backward_workspace_size bytes; may be NULL when dWg and dtokens are.
- * Shapes: those of moe_gate_topk, and for dWg / dtokens d a multiple of 8 (MOE_F16) or 4.
+ *   token_mask also leaves the masked tokens' rows out of dWg: what they hold has no effect.
+ *   MOE_F16, T > 128 and E <= 256: Wg is rounded to f16 (scaled by powers of two) for dtokens, as
+ *   the expert FFN's weights are; dWg keeps 32-bit accuracy.
+ * Shapes: those of moe_gate_topk, T <= 2^30, and for dWg / dtokens d a multiple of 8 (MOE_F16) or
+ * 4, at most 2^20.
  */
 MOE_API moe_status moe_gate_topk_backward(const float* logits, const int32_t* topk_idx,
                                           const float* dtopk_w, const float* dlosses,
@@ -327,6 +331,8 @@ MOE_API moe_status moe_gate_topk_backward(const float* logits, const int32_t* to
  *   dout [T, d], expert_out and dexpert_out [S_max, d] in `dtype`.  Slots that no assignment
  *   names are left as they were.  dexpert_out nullable (then topk_w is not read), dtopk_w
  *   nullable (then expert_out is not read); not both.  residual_in's gradient is dout itself.
+ *   A slot that two assignments name (moe_dispatch names none twice) gets one of their rows.
+ * Shapes: T <= 2^30, d <= 2^20.
  */
 MOE_API moe_status moe_combine_backward(const void* dout, const void* expert_out,
                                         const int32_t* slot_of, const float* topk_w, moe_dtype dtype,
@@ -354,8 +360,10 @@ MOE_API moe_status moe_adapter_workspace_size(int T, int d_in, int d_out, int r,
  *   decreasing and perm entries outside [0, T) are skipped and recorded as
  *   MOE_ERR_DEVICE_BOUNDS in the workspace's status word.
  *   workspace: moe_adapter_workspace_size bytes; contents need no initialisation.
+ * MOE_F16: hidden is given out in float32 and rounded to f16, each row scaled by a power of two,
+ * for the second product (as the expert FFN rounds its hidden activations).
  * Shapes: N <= 1024; r a multiple of 8, at most 128 (adapters of different ranks are padded with
- * zeros); d_in, d_out multiples of 8 (MOE_F16) or 4 (MOE_F32).
+ * zeros); d_in, d_out multiples of 8 (MOE_F16) or 4 (MOE_F32), at most 2^20; T, S_max <= 2^30.
  */
 MOE_API moe_status moe_adapter_forward(const void* tokens, const int32_t* perm,
                                        const int32_t* offsets, const void* A, const void* B,
@@ -372,7 +380,8 @@ MOE_API moe_status moe_adapter_forward(const void* tokens, const int32_t* perm,
  *   hidden: as moe_adapter_forward wrote it.  dtokens nullable; dtokens_in nullable (zero) and
  *   may be dtokens itself; dA nullable (then tokens is not read), dB nullable (then hidden is
  *   not read); not all three.  base's gradient is dout itself.
- *   Everything else as moe_adapter_forward.
+ *   Everything else as moe_adapter_forward (dh is the row that is rounded to f16, for dtokens
+ *   only).  MOE_F16, long runs: an infinite token or dout row makes its sums infinite or NaN.
  */
 MOE_API moe_status moe_adapter_backward(const void* dout, const void* tokens, const float* hidden,
                                         const int32_t* perm, const int32_t* offsets, const void* A,

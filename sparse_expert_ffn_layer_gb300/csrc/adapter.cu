@@ -81,7 +81,9 @@ struct AdapterArgs {
 };
 
 // ---------------------------------------------------------------- f16, long runs
-// Two launches of persistent blocks, h between them in 32 bits (small: r of d columns):
+// Two launches of persistent blocks, h between them in 32 bits (small: r of d columns); 16384 rows of
+// 3584 columns, r = 64, 8 adapters: 36 + 51 us (DRAM floor 53), bound by the shared-memory pipe's
+// fragment loads and by latency at 16 warps per SM:
 //   shrink  partial h[part] = x P over a part of the input columns, per tile of 64 rows
 //   expand  h = sum of the parts in order, then y = base + scale h Q per tile and part of the
 //           output columns
@@ -582,7 +584,7 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
 
 // ---------------------------------------------------------------- f16, short runs
 // Tiles of 16 rows, four warps that load and multiply (64 requests with an adapter each, 3584
-// columns, r = 16: 11 us, of which the weights' bytes are 2; the rest is the chain of table, loads,
+// columns, r = 16: 10 us, of which the weights' bytes are 2; the rest is the chain of table, loads,
 // two exchanges and stores, so chunks are wide and few at low ranks).
 template <int R>
 struct Plan16 {
@@ -902,6 +904,8 @@ __global__ void __launch_bounds__(128, Plan16<R>::kBlocks) adapter_f16_kernel(co
 }
 
 // ---------------------------------------------------------------- f32
+// As the short f16 form, with fused multiply-adds; every run goes in tiles of 16 rows (1 row of 64 to
+// 256 columns: 6 us of latency; long runs are bound by the multiply-adds' operands from shared memory).
 template <int R>
 struct Plan32 {
   static constexpr int MT = 16, kThreads = 128, C = 32;
@@ -1217,6 +1221,8 @@ __global__ void __launch_bounds__(1024) adapter_check_kernel(const AdapterArgs a
 
 }  // namespace
 
+// More than 32 rows per adapter on average: tiles of 64 rows in two launches.  Below, a tile of 64
+// is mostly empty rows and the second launch costs more than the weights' reuse saves.
 bool adapter_tall(int S_max, int N, bool f16) { return f16 && S_max > 32LL * std::min(N, S_max); }
 
 size_t adapter_partial_rows(int S_max) {

@@ -78,7 +78,8 @@ struct Sync {
 // A block owns IW x 128 rows i of dWg and 128 columns j, and a run of token rows: chunks of 64 rows
 // of X (as the transposed operand) and of the split dL.  The accumulators are emptied into 32-bit
 // registers after every 128 rows, where the scale of dL changes (and where the chain of truncating
-// additions ends).  IW = 2: the two accumulators share each chunk of dL (64 KB from L2 per 64 KB of
+// additions ends).  16384 x 3584 tokens, 128 experts: 32 us, X read once at 3.7 TB/s; the hand-over of
+// an accumulator every 128 rows, not a pipe, bounds it.  IW = 2: the two accumulators share each chunk of dL (64 KB from L2 per 64 KB of
 // X; with one the copies from L2 bound it); while the second is emptied the first fills again.
 // IW = 1, for batches with too few blocks: two accumulators alternate.
 struct WgArgs {
@@ -251,7 +252,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------- dX
 // A block takes a tile of 128 tokens, keeps its split dL in shared memory (E <= 256) and walks a
 // part of d in tiles of 128: the split Wg comes from L2 in chunks of 64 experts, dX_in by TMA
-// into the tile that the accumulator warps add to in place and that TMA writes out.
+// into the tile that the accumulator warps add to in place and that TMA writes out.  16384 x 3584
+// tokens, 128 experts: 44 us, 5.3 TB/s of dX_in and dX; the tiles' loads and stores bound it.
 struct DxArgs {
   const float *sT, *sW;
   int T, d, E, Ep;
@@ -532,7 +534,8 @@ cudaError_t launch_dx_tc(const CUtensorMap& mL, const CUtensorMap& mW, const CUt
 
 }  // namespace
 
-// (Short batches: the chain of launches takes 23 to 31 us, the multiply-add kernels half of it.)
+// Short batches go to the multiply-add kernels (grad.cu): at T = 128 these three launches take 23 to
+// 31 us, those 12 to 20; from there on theirs grow with T E d (dX alone 494 us at 16384 x 3584 x 128).
 bool gate_tc_ok(int T, int E) { return E <= 256 && T > kSumShort; }
 size_t gate_tc_bytes(int T, int d, int E) { return T > 0 ? gate_ws(T, d, E).total : 0; }
 
