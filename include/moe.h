@@ -288,7 +288,10 @@ MOE_API moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx
                                     float* prob_mean, float* losses, int32_t* n_valid,
                                     void* workspace, size_t ws_bytes, moe_stream_t stream);
 
-/* Bytes of workspace of moe_gate_topk_backward when it takes the gradient to Wg or the tokens. */
+/*
+ * Bytes of workspace of moe_gate_topk_backward when it takes the gradient to Wg or the tokens.  The
+ * bytes of a batch are enough for every smaller T.
+ */
 MOE_API moe_status moe_gate_backward_workspace_size(int T, int d, int E, moe_dtype dtype,
                                                     size_t* bytes);
 
@@ -339,7 +342,10 @@ MOE_API moe_status moe_combine_backward(const void* dout, const void* expert_out
                                         int T, int d, int k, int S_max, void* dexpert_out,
                                         float* dtopk_w, moe_stream_t stream);
 
-/* Bytes of workspace that moe_adapter_forward and moe_adapter_backward need for this shape. */
+/*
+ * Bytes of workspace that moe_adapter_forward and moe_adapter_backward need for this shape.  The
+ * bytes of an S_max are enough for every smaller one (and any T).
+ */
 MOE_API moe_status moe_adapter_workspace_size(int T, int d_in, int d_out, int r, int N, int S_max,
                                               moe_dtype dtype, size_t* bytes);
 

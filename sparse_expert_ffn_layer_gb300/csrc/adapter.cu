@@ -1205,7 +1205,7 @@ cudaError_t launch_f32(const AdapterArgs& a, cudaStream_t s) {
 template <bool kT, int R>
 cudaError_t launch_rank(const AdapterArgs& a, bool f16, float* partial, cudaStream_t s) {
   if (!f16) return launch_f32<kT, R>(a, s);
-  return adapter_tall(a.S_max, a.N, true) ? launch_tall<kT, R>(a, partial, s) : launch_short<kT, R>(a, s);
+  return adapter_tall(a.S_max, a.N, a.r, true) ? launch_tall<kT, R>(a, partial, s) : launch_short<kT, R>(a, s);
 }
 template <bool kT>
 cudaError_t launch_adapter_t(const AdapterArgs& a, bool f16, float* partial, cudaStream_t s) {
@@ -1221,9 +1221,15 @@ __global__ void __launch_bounds__(1024) adapter_check_kernel(const AdapterArgs a
 
 }  // namespace
 
-// More than 32 rows per adapter on average: tiles of 64 rows in two launches.  Below, a tile of 64
-// is mostly empty rows and the second launch costs more than the weights' reuse saves.
-bool adapter_tall(int S_max, int N, bool f16) { return f16 && S_max > 32LL * std::min(N, S_max); }
+// Two launches with tiles of 64 rows, where tiles of 16 would take the resident clusters more than
+// one round (estimated, with half a tile per adapter lost) and an adapter has more than 16 rows on
+// average: fewer leave a tile of 64 mostly empty.  One adapter, 3584 columns, us short / long: r = 64,
+// 48 tiles of 16 rows 17 / 20, 52 tiles 24 / 20; r = 16, 72 tiles 13.1 / 12.8, 80 tiles 17 / 13; r = 128,
+// 36 tiles 22 / 32, 80 tiles 50 / 36.  64 adapters with r = 64: 16 rows each 24 / 30, 24 each 45 / 31.
+bool adapter_tall(int S_max, int N, int r, bool f16) {
+  const int n = std::min(N, S_max), round = r <= 16 ? 72 : r <= 64 ? 48 : 36;
+  return f16 && S_max > 16LL * n && S_max / 16 + n / 2 > round;
+}
 
 size_t adapter_partial_rows(int S_max) {
   return std::max<size_t>(S_max, std::min<size_t>((size_t)kAdapterParts * S_max, (size_t)kPartItems * kTallRows));

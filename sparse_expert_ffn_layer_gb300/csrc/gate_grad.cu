@@ -485,7 +485,7 @@ WgPlan wgrad_plan(int T, int d, int E) {
   double cost = 1e300;
   for (int iw = 1; iw <= 2; ++iw) {
     const int blocks = (d + 128 * iw - 1) / (128 * iw) * jb;
-    for (int p = 1; p <= std::min(all, 32); ++p) {
+    for (int p = 1; p <= std::min(all, sum_parts((size_t)d * E)); ++p) {
       const int run = (all + p - 1) / p, runs = (all + run - 1) / run;
       const double c = ((blocks * runs + 151) / 152) * (run * (iw == 2 ? 1.5 : 1.0) + 3.0) +
                        (runs > 1 ? 2.0 + runs * (double)d * E * 1e-6 : 0);
@@ -509,8 +509,7 @@ GateWs gate_ws(int T, int d, int E) {
   w.sT = w.W2 + up256((size_t)d * Ep * 2);
   w.sW = w.sT + up256((size_t)(T + 127) / 128 * 4);
   w.partial = w.sW + up256((size_t)(d + 127) / 128 * 4);
-  const int run = wgrad_plan(T, d, E).run, runs = (T + run - 1) / run;
-  w.total = w.partial + (runs > 1 ? up256((size_t)2 * runs * d * E * 4) : 0);
+  w.total = w.partial + up256(sum_partial_bytes((size_t)d * E, T, 128));
   return w;
 }
 
@@ -534,9 +533,11 @@ cudaError_t launch_dx_tc(const CUtensorMap& mL, const CUtensorMap& mW, const CUt
 
 }  // namespace
 
-// Short batches go to the multiply-add kernels (grad.cu): at T = 128 these three launches take 23 to
-// 31 us, those 12 to 20; from there on theirs grow with T E d (dX alone 494 us at 16384 x 3584 x 128).
-bool gate_tc_ok(int T, int E) { return E <= 256 && T > kSumShort; }
+// Few logits go to the multiply-add kernels (grad.cu), few of odd rows (whose split is scalar) longer.
+// us for dlogits, dWg and dX of 1024 columns, multiply-adds / here: E = 64: T = 32 11.1 / 10.6, 128
+// 17.8 / 12.4; E = 8: T = 256 11.0 / 12.1, 1024 13.6 / 12; E = 13: T = 256 12.9 / 14.1; E = 127: T = 128
+// 25 / 26, T = 256 28.6 / 28.2.  At 16384 x 3584 x 128 the multiply-adds' dX alone takes 494 us.
+bool gate_tc_ok(int T, int E) { return E <= 256 && (long long)T * E >= (E % 4 ? 32768 : 4096); }
 size_t gate_tc_bytes(int T, int d, int E) { return T > 0 ? gate_ws(T, d, E).total : 0; }
 
 cudaError_t launch_gate_tc(const float* logits, const int32_t* topk_idx, const float* dtopk_w,

@@ -538,19 +538,23 @@ __global__ void __launch_bounds__(256) row_sum_join_kernel(const SumArgs a) {
   }
 }
 
-// Short batches of f16 rows take the multiply-add form (see row_sum_fma_kernel) where its items are
-// two rounds of blocks at most: a single chunk each, they are bound by their loads' latency.
+// Short f16 groups take the multiply-add form (one launch less), where its items are two rounds of
+// blocks at most.  us, both gradients, multiply-adds / tensor cores: one group, 1024 columns each,
+// r = 16: 64 rows 15.4 / 16.1, 128 rows 19.0 / 16.8, 512 rows 40 / 21; eight groups of 32 rows 13.8 / 15.2,
+// of 64 rows 18.9 / 18.3 (skewed groups make it 40 / 21); 16 groups of 3584 columns, 32 rows in all:
+// 31 / 23.
 bool sum_tc(bool f16, int S_max, int N, int columns) {
-  return f16 && (S_max > kSumShort || (long long)std::min(N, S_max) * (columns / kIT32 + 2) > 608);
+  const long long n = std::min(N, S_max);
+  return f16 && (S_max > std::max(64LL, 32 * n) || n * (columns / kIT32 + 2) > 608);
 }
 
 // Rows per segment: the segments of S_max rows (and half a segment more per group) times the
 // column blocks take the fewest rounds of two blocks on each of 152 SMs, plus what a segment
 // costs in partial sums and the launch that joins them.
-int sum_segment(int S_max, int N, int blocks) {
+int sum_segment(int S_max, int N, int blocks, size_t words) {
   int best = 64;
   double cost = 1e300;
-  for (int p = 1; p <= kSumSegments; ++p) {
+  for (int p = 1; p <= sum_parts(words); ++p) {
     const int seg = std::max(64, (int)(((long long)S_max + p - 1) / p + 63) / 64 * 64);
     const double items = blocks * ((double)S_max / seg + 0.5 * std::min(N, S_max));
     const double c = ceil(items / 304) * (seg / 64 + 2) + 0.7 * p + (seg < S_max ? 6 : 0);
@@ -757,7 +761,10 @@ cudaError_t launch_combine_backward_t(const void* dout, const void* y, const int
                                       float* dw, int sms, cudaStream_t s) {
   const T* du = static_cast<const T*>(dout);
   const T* yy = static_cast<const T*>(y);
-  if (T_ < 16 * sms)
+  // Eight warps per row while a warp each leaves the device's loads waiting for one another: f16, us
+  // one / eight: 3584 columns 1024 rows 6.3 / 4.8, 2432 rows 7.3 / 8.1; 1024 columns 256 rows 3.1 / 2.4,
+  // 1024 rows 3.2 / 3.6; 64 columns the same or less for one.
+  if (T_ < 128LL * ((d + 32 * V - 1) / (32 * V)))
     return launch_k(combine_backward_kernel<T, V, 8>, std::min(T_, 8 * sms), 256, 0, s, false, du, yy,
                     slot_of, topk_w, T_, d, k, S_max, static_cast<T*>(dy), dw);
   return launch_k(combine_backward_kernel<T, V, 1>, std::min((T_ + 7) / 8, 8 * sms), 256, 0, s, false,
@@ -788,18 +795,12 @@ cudaError_t launch_sum_join(float* G, float* partial, int di, int dj, int T, int
   return launch_k(row_sum_join_kernel, dim3(std::max(1, bx), 1, 1), 256, 0, s, true, a);
 }
 
-size_t row_sums_bytes(int di0, int dj0, int di1, int dj1, bool f16, int S_max, int N) {
+size_t row_sums_bytes(int di0, int dj0, int di1, int dj1, bool f16, int S_max) {
   size_t most = 0;
   // either job alone may be asked for: the plan of each combination fits
   for (int q = 1; q < 4; ++q) {
-    const int dj = std::max(q & 1 ? dj0 : 0, q & 2 ? dj1 : 0);
-    const bool tc = sum_tc(f16, S_max, N, (q & 1 ? di0 : 0) + (q & 2 ? di1 : 0));
-    const int b = (q & 1 ? sum_blocks(di0, dj0, dj, tc) : 0) + (q & 2 ? sum_blocks(di1, dj1, dj, tc) : 0);
-    if (b == 0) continue;
-    const int seg = sum_segment(S_max, N, b);
-    const size_t slots = 2 * (size_t)((S_max + seg - 1) / seg);
     const size_t words = (q & 1 ? (size_t)di0 * dj0 : 0) + (q & 2 ? (size_t)di1 * dj1 : 0);
-    most = std::max(most, S_max > seg ? slots * words * sizeof(float) : 0);
+    if (words > 0) most = std::max(most, sum_partial_bytes(words, S_max, 64));
   }
   return up256(most) + (f16 ? split_bytes(dj0, S_max) + split_bytes(dj1, S_max) : 0);
 }
@@ -832,7 +833,7 @@ cudaError_t launch_row_sums(const void* x0, const float* h0, float* G0, int di0,
   if (G1) job(a.job[1], x1, h1, G1, di1, dj1, tr1);
   const int dj = std::max(G0 ? dj0 : 0, G1 ? dj1 : 0);
   const int blocks = (G0 ? sum_blocks(di0, dj0, dj, tc) : 0) + (G1 ? sum_blocks(di1, dj1, dj, tc) : 0);
-  a.seg = sum_segment(S_max, N, blocks);
+  a.seg = sum_segment(S_max, N, blocks, (G0 ? (size_t)di0 * dj0 : 0) + (G1 ? (size_t)di1 * dj1 : 0));
   a.job[0].partial = a.job[1].partial = reinterpret_cast<float*>(ws);
   if (G0) a.job[1].partial += 2 * (size_t)((S_max + a.seg - 1) / a.seg) * di0 * dj0;
   a.scale = scale;

@@ -1,6 +1,7 @@
 // Internal interface between the C-ABI front end (api.cu) and the kernels.
 #pragma once
 
+#include <algorithm>
 #include <atomic>
 #include <utility>
 
@@ -194,20 +195,31 @@ cudaError_t launch_dlogits(const float* logits, const int32_t* topk_idx, const f
                            cudaStream_t s);
 // Sums over token rows for up to two jobs G[n][i][j] = scale_n sum_s x[row(s)][i] h[s][j]
 // (transposed: G[n][j][i]); G0 or G1 may be null (grad.cu).
+// Segments that the rows are cut into at most, for sums of `words` values in all: two partial sums
+// each, which stay within half of L2.
 constexpr int kSumSegments = 32;
-constexpr int kSumShort = 128;       // f16 batches of up to this many rows take the multiply-add form
+constexpr size_t kSumBudget = (size_t)64 << 20;
+inline int sum_parts(size_t words) {
+  return (int)std::max<size_t>(1, std::min<size_t>(kSumSegments, kSumBudget / (2 * words * sizeof(float))));
+}
+// Bytes of those partial sums; no less for more rows, so that one workspace serves every batch up to
+// the largest.
+inline size_t sum_partial_bytes(size_t words, int rows, int least) {   // least: rows of a segment
+  const size_t parts = std::min<size_t>(sum_parts(words), ((size_t)rows + least - 1) / least);
+  return parts > 1 ? 2 * parts * words * sizeof(float) : 0;
+}
 cudaError_t launch_row_sums(const void* x0, const float* h0, float* G0, int di0, int dj0, int tr0,
                             const void* x1, const float* h1, float* G1, int di1, int dj1, int tr1,
                             const float* scale, const int32_t* perm, const int32_t* offsets,
                             const uint8_t* mask, void* workspace, int dtype_f16, int T, int S_max,
                             int N, bool pdl, cudaStream_t s);
 // Bytes of its workspace, for either job alone or both (dj1 = 0: there is no second).
-size_t row_sums_bytes(int di0, int dj0, int di1, int dj1, bool f16, int S_max, int N);
+size_t row_sums_bytes(int di0, int dj0, int di1, int dj1, bool f16, int S_max);
 // Joins the partial sums of runs of `run` rows (slot 2 q, the last run's 2 q + 1) in order.
 cudaError_t launch_sum_join(float* G, float* partial, int di, int dj, int T, int run, int sms,
                             cudaStream_t s);
-// The gate's whole gradient on the tensor cores (gate_grad.cu): f16 tokens, E <= 256, more
-// than kSumShort rows; dWg (may be null) without rows left out.
+// The gate's whole gradient on the tensor cores (gate_grad.cu): f16 tokens, where gate_tc_ok; dWg
+// (may be null) without rows left out.
 bool gate_tc_ok(int T, int E);
 size_t gate_tc_bytes(int T, int d, int E);
 cudaError_t launch_gate_tc(const float* logits, const int32_t* topk_idx, const float* dtopk_w,
@@ -231,7 +243,7 @@ cudaError_t launch_combine_backward(const void* dout, const void* expert_out, co
 // the indices are checked; dn = 0: only x P is computed.  partial: adapter_partial_rows(S_max) rows
 // of r floats where adapter_tall.
 constexpr int kAdapterParts = 8, kPartItems = 1216;
-bool adapter_tall(int S_max, int N, bool f16);
+bool adapter_tall(int S_max, int N, int r, bool f16);
 size_t adapter_partial_rows(int S_max);
 cudaError_t launch_adapter(const void* x, const void* P, const void* Q, const void* base, void* y,
                            float* hidden, float* partial, const float* scale, const int32_t* perm,

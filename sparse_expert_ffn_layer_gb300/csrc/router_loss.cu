@@ -29,6 +29,8 @@ constexpr int kRowThreads = 512;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kCluster = 8;
 constexpr int kFinalThreads = 1024;
+// Parts of a column's sum over the records (one thread adds them up: 1024 of them took 10 us).
+constexpr int kJoinParts = 64;
 
 template <int LANES>
 __device__ __forceinline__ float group_max(float v) {
@@ -125,7 +127,7 @@ __host__ __device__ inline size_t record_words(int E) { return 2 * (size_t)E + 4
 
 // Joins nb records (rec(b) is record b) into the outputs.  Runs in one cluster of up to kCluster
 // blocks: block c owns the columns [c Ec, (c + 1) Ec); its threads sum each column in
-// blockDim / Ec parts, always in the same order, and rank 0 adds the blocks' shares of the
+// up to kJoinParts parts, always in the same order, and rank 0 adds the blocks' shares of the
 // balance loss through distributed shared memory.
 template <typename Rec>
 __device__ __forceinline__ void join_records(Rec rec, int nb, int E, int k, LossOut o, float* sh_f,
@@ -133,7 +135,7 @@ __device__ __forceinline__ void join_records(Rec rec, int nb, int E, int k, Loss
   cg::cluster_group cl = cg::this_cluster();
   const int c = (int)cl.block_rank(), ncl = (int)cl.num_blocks();
   const int Ec = (E + ncl - 1) / ncl;                // at most blockDim
-  const int parts = max(1, (int)blockDim.x / Ec);
+  const int parts = max(1, min((int)blockDim.x / Ec, min(nb, kJoinParts)));
   const int col = threadIdx.x % Ec, part = threadIdx.x / Ec;
   const int e = c * Ec + col;
   float ps = 0.f;
@@ -596,8 +598,15 @@ __global__ void __launch_bounds__(kSplitThreads) dlogits_split_kernel(const DlAr
         for (int v = 0; v < 4; ++v) f[v] = c < d.E ? x[p][4 * j + v] : 0.f;
         split_four(f, inv, hi + c, hi + o.Ep + c);
       }
-      // columns up to Ep that no lane's values cover
-      for (int c = LANES * V + l; c < o.Ep; c += LANES) hi[c] = hi[o.Ep + c] = __ushort_as_half(0);
+    }
+    // columns up to Ep that no lane's values cover
+    const int rest = (o.Ep - LANES * V) / 8;
+    if (rest > 0) {
+      for (int q = tid; q < rows * 2 * rest; q += kSplitThreads) {
+        const int r = q / (2 * rest), c = q - r * (2 * rest);
+        __half* at = dst + (size_t)r * 2 * o.Ep + (c < rest ? LANES * V + c * 8 : o.Ep + LANES * V + (c - rest) * 8);
+        *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
+      }
     }
     if (tid == 0) o.sT[blockIdx.x] = exp2_int(e);
   } else {
@@ -662,9 +671,11 @@ int row_blocks(int T, int E, int sms) {
   return std::max(1, std::min({(T + rows - 1) / rows, 2 * sms, kMaxRecords}));
 }
 
-// Up to this many logits one cluster does the whole call (a second launch costs about 4 us more
-// than a few more passes over the rows): one block where a pass covers the batch, else up to eight.
-constexpr long long kOneClusterElems = 256 * 1024;
+// Up to this many passes of eight blocks over the rows one cluster does the whole call: one block
+// where a pass covers the batch, else up to eight.  us, two launches / one: E = 64, 1024 rows (one pass)
+// 6.1 / 5.4, two passes 6.2 / 6.5 (and a launch less on the host), four 6.5 / 8.5; E = 8, 4096 rows
+// 6.0 / 5.4, 8192 rows 6.4 / 6.4.
+constexpr int kOnePasses = 2;
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kernel)(KArgs...), int grid, int block, size_t smem,
@@ -698,7 +709,7 @@ cudaError_t launch_balance_loss(const float* logits, const int32_t* topk_idx, co
   const int sms = sm_count();
   if (sms < 1) return cudaErrorInvalidDevice;
   const LossOut o{counts, prob_mean, losses, n_valid};
-  const bool one = (long long)T * E <= kOneClusterElems;
+  const bool one = T <= kOnePasses * kCluster * block_rows(E);
   int blocks = row_blocks(T, E, sms);
   if (one) {                                       // a power of two, whose blocks hold E columns
     int c = 1;

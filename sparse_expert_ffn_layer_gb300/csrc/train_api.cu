@@ -58,12 +58,12 @@ moe_status check_adapter(int T, int d_in, int d_out, int r, int N, int S_max, mo
 size_t hidden_bytes(int r, size_t rows) { return align_up(rows * r * sizeof(float)); }
 size_t adapter_sums_at(int d_in, int d_out, int r, int N, int S_max, moe_dtype dtype) {
   size_t b = kAlign + hidden_bytes(r, S_max);
-  if (adapter_tall(S_max, N, dtype == MOE_F16)) b += hidden_bytes(r, adapter_partial_rows(S_max));
+  if (adapter_tall(S_max, N, r, dtype == MOE_F16)) b += hidden_bytes(r, adapter_partial_rows(S_max));
   return b;
 }
 size_t adapter_bytes(int d_in, int d_out, int r, int N, int S_max, moe_dtype dtype) {
   return adapter_sums_at(d_in, d_out, r, N, S_max, dtype) +
-         align_up(row_sums_bytes(d_in, r, d_out, r, dtype == MOE_F16, S_max, N));
+         align_up(row_sums_bytes(d_in, r, d_out, r, dtype == MOE_F16, S_max));
 }
 
 }  // namespace
@@ -102,7 +102,7 @@ moe_status moe_gate_backward_workspace_size(int T, int d, int E, moe_dtype dtype
   if (st != MOE_OK) return st;
   if (d % lane_elems(dtype) || d > kMaxCols) return MOE_ERR_UNSUPPORTED;
   // the tensor-core form, and the form that leaves masked rows out
-  size_t most = row_sums_bytes(d, E, 0, 0, dtype == MOE_F16, T, 1);
+  size_t most = row_sums_bytes(d, E, 0, 0, dtype == MOE_F16, T);
   if (dtype == MOE_F16 && gate_tc_ok(T, E)) most = std::max(most, gate_tc_bytes(T, d, E));
   *bytes = kAlign + align_up(most);
   return MOE_OK;

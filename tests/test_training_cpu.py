@@ -45,6 +45,20 @@ def test_workspace_sizes(m):
         m.moe_adapter_workspace_size(8, 64, 64, 8, 4, 8, torch.bfloat16)
 
 
+def test_one_workspace_serves_every_smaller_batch(m):
+    rows = [*range(0, 1400, 9), *range(1400, 20000, 311)]
+    for dt in (torch.float16, torch.float32):
+        for d, E in [(1024, 64), (256, 8), (3584, 128), (1024, 13), (512, 1000)]:
+            size = [m.moe_gate_backward_workspace_size(T, d, E, dt) for T in rows]
+            assert size == sorted(size)
+        for di, do, r, N in [(1024, 1024, 16, 8), (2048, 8192, 32, 4), (3584, 3584, 64, 64), (64, 256, 128, 1)]:
+            size = [m.moe_adapter_workspace_size(T, di, do, r, N, T, dt) for T in rows]
+            assert size == sorted(size)
+    for E in (8, 1000):
+        size = [m.moe_balance_workspace_size(T, E) for T in rows]
+        assert size == sorted(size)
+
+
 def test_balance_and_gate_refusals(m):
     f = m.lib.moe_balance_loss
 

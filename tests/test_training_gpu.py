@@ -237,6 +237,12 @@ GATE = [("f16", 1, 128, 4, 1), ("f16", 5, 8, 1, 1), ("f16", 63, 136, 7, 2), ("f1
         ("f32", 2048, 64, 8, 2)]
 
 
+# where the two forms change over, on both sides, and small ones of the tensor-core form
+GATE += [("f16", 16, 136, 256, 2), ("f16", 15, 136, 256, 2), ("f16", 40, 264, 128, 1), ("f16", 64, 8, 64, 2),
+         ("f16", 512, 72, 8, 2), ("f16", 511, 72, 8, 2), ("f16", 2048, 264, 2, 1), ("f16", 2521, 136, 13, 2),
+         ("f16", 129, 72, 255, 2), ("f16", 128, 72, 255, 2), ("f16", 4097, 64, 4, 1), ("f16", 100, 128, 60, 2)]
+
+
 def gate_inputs(g, dt, T, d, E, k):
     x = randn(g, T, d, dtype=dt)
     Wg = randn(g, d, E, sigma=0.1)
@@ -425,6 +431,12 @@ ADAPT = [("f16", 1, 8, 8, 8, 1), ("f16", 1, 1024, 1024, 16, 32), ("f16", 2, 64, 
          ("f32", 70, 128, 260, 128, 2), ("f32", 1111, 32, 32, 16, 1)]
 
 
+# long runs of every rank's form, and where short ones change over
+ADAPT += [("f16", 1300, 136, 1000, 16, 1), ("f16", 1184, 72, 64, 8, 1), ("f16", 1500, 264, 136, 128, 3),
+          ("f16", 1400, 328, 200, 64, 2), ("f16", 900, 1032, 72, 24, 2), ("f16", 784, 128, 264, 64, 1),
+          ("f16", 768, 128, 264, 64, 1), ("f16", 600, 64, 72, 112, 1), ("f16", 128, 200, 72, 16, 2)]
+
+
 @pytest.mark.parametrize("dt,T,di,do,r,N", ADAPT)
 @pytest.mark.parametrize("form", ["base", "in_place", "bare", "one"])
 def test_adapter_forward(m, dt, T, di, do, r, N, form):
@@ -544,7 +556,7 @@ def test_adapter_single_row_gradient_keeps_22_bits(m):
           abs(float(c["scale"])), "dB")
 
 
-@pytest.mark.parametrize("T", [3, 300])
+@pytest.mark.parametrize("T", [3, 300, 1300])
 def test_adapter_wide_range_and_infinities(m, T):
     """h far outside f16's range, and rows with infinities or NaN that leave the others alone."""
     g = gen(T)
@@ -661,7 +673,7 @@ def test_adapter_gradients_under_decreasing_offsets(m, dt):
 
 
 @pytest.mark.parametrize("dt", [torch.float16, torch.float32])
-@pytest.mark.parametrize("T", [40, 700])
+@pytest.mark.parametrize("T", [40, 700, 1500])
 def test_adapter_bad_entries_take_nothing_into_the_gradients(m, dt, T):
     """Entries outside [0, T) are left out of every sum, whatever a token without an adapter holds."""
     g = gen(37 + T)
@@ -863,7 +875,7 @@ def step_inputs(seed, T, d, r, N, E, k):
                 dloss=torch.tensor([0.01, 0.001], device="cuda"))
 
 
-@pytest.mark.parametrize("T,d,r,N,E,k", [(96, 128, 16, 5, 8, 2), (700, 256, 24, 3, 12, 1)])
+@pytest.mark.parametrize("T,d,r,N,E,k", [(96, 128, 16, 5, 8, 2), (700, 256, 24, 3, 12, 1), (1700, 128, 40, 2, 16, 2)])
 def test_training_step_of_router_and_adapters(m, T, d, r, N, E, k):
     c, b = step_inputs(1, T, d, r, N, E, k), step_buffers(m, T, d, r, N, E, k)
     step(m, c, b)
