@@ -550,14 +550,16 @@ bool sum_tc(bool f16, int S_max, int N, int columns) {
 
 // Rows per segment: the segments of S_max rows (and half a segment more per group) times the
 // column blocks take the fewest rounds of two blocks on each of 152 SMs, plus what a segment
-// costs in partial sums and the launch that joins them.
-int sum_segment(int S_max, int N, int blocks, size_t words) {
+// costs in partial sums and the launch that joins them.  chunk: us of 64 rows (fused multiply-adds:
+// up to six times the tensor cores'; counted as theirs, 651 x 848 rows by 67 columns took 60 us in one
+// segment).
+int sum_segment(int S_max, int N, int blocks, size_t words, double chunk) {
   int best = 64;
   double cost = 1e300;
   for (int p = 1; p <= sum_parts(words); ++p) {
     const int seg = std::max(64, (int)(((long long)S_max + p - 1) / p + 63) / 64 * 64);
     const double items = blocks * ((double)S_max / seg + 0.5 * std::min(N, S_max));
-    const double c = ceil(items / 304) * (seg / 64 + 2) + 0.7 * p + (seg < S_max ? 6 : 0);
+    const double c = ceil(items / 304) * (seg / 64 * chunk + 2) + 0.7 * p + (seg < S_max ? 6 : 0);
     if (c < cost) {
       cost = c;
       best = seg;
@@ -833,7 +835,8 @@ cudaError_t launch_row_sums(const void* x0, const float* h0, float* G0, int di0,
   if (G1) job(a.job[1], x1, h1, G1, di1, dj1, tr1);
   const int dj = std::max(G0 ? dj0 : 0, G1 ? dj1 : 0);
   const int blocks = (G0 ? sum_blocks(di0, dj0, dj, tc) : 0) + (G1 ? sum_blocks(di1, dj1, dj, tc) : 0);
-  a.seg = sum_segment(S_max, N, blocks, (G0 ? (size_t)di0 * dj0 : 0) + (G1 ? (size_t)di1 * dj1 : 0));
+  a.seg = sum_segment(S_max, N, blocks, (G0 ? (size_t)di0 * dj0 : 0) + (G1 ? (size_t)di1 * dj1 : 0),
+                      tc ? 1.0 : std::max(1.0, std::min(dj, 128) * (6.0 / 128)));
   a.job[0].partial = a.job[1].partial = reinterpret_cast<float*>(ws);
   if (G0) a.job[1].partial += 2 * (size_t)((S_max + a.seg - 1) / a.seg) * di0 * dj0;
   a.scale = scale;

@@ -671,11 +671,12 @@ int row_blocks(int T, int E, int sms) {
   return std::max(1, std::min({(T + rows - 1) / rows, 2 * sms, kMaxRecords}));
 }
 
-// Up to this many passes of eight blocks over the rows one cluster does the whole call: one block
-// where a pass covers the batch, else up to eight.  us, two launches / one: E = 64, 1024 rows (one pass)
-// 6.1 / 5.4, two passes 6.2 / 6.5 (and a launch less on the host), four 6.5 / 8.5; E = 8, 4096 rows
-// 6.0 / 5.4, 8192 rows 6.4 / 6.4.
-constexpr int kOnePasses = 2;
+// Up to this many passes of eight blocks over the rows one cluster does the whole call (one block where
+// a pass covers the batch, else up to eight): a pass takes it about 1 us, the second launch of the other
+// form 4 us of the host's time.  us on the GPU, two launches / one: E = 64, 1024 rows (one pass) 6.1 / 5.4,
+// two passes 6.2 / 6.5, four 6.5 / 8.5, eight 6.9 / 12.4; wall clock with the gradient's call after it,
+// E = 60, 4099 rows (five passes): 20.3 / 18.0.
+constexpr int kOnePasses = 5;
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kernel)(KArgs...), int grid, int block, size_t smem,
