@@ -313,7 +313,7 @@ MOE_API moe_status moe_gate_backward_workspace_size(int T, int d, int E, moe_dty
  *   nullable (zero; may be dtokens itself).
  *   workspace: moe_gate_backward_workspace_size bytes; may be NULL when dWg and dtokens are.
  *   token_mask also leaves the masked tokens' rows out of dWg: what they hold has no effect.
- *   MOE_F16, T > 128 and E <= 256: Wg is rounded to f16 (scaled by powers of two) for dtokens, as
+ *   MOE_F16, E <= 256: Wg may be rounded to f16 (scaled by powers of two) for dtokens, as
  *   the expert FFN's weights are; dWg keeps 32-bit accuracy.
  * Shapes: those of moe_gate_topk, T <= 2^30, and for dWg / dtokens d a multiple of 8 (MOE_F16) or
  * 4, at most 2^20.

@@ -10,9 +10,14 @@
 // Wg split as well, a third product, each tile took twice the bytes from L2.)  The split comes with
 // the logits' gradient (router_loss.cu).
 //
-// Both kernels: one block per SM; warp 0 loads by TMA, warp 1 issues the products, eight warps read
-// the accumulators.  Every wait is bounded (common.cuh).
+// One launch computes both, a part of its blocks dWg and the rest dX, one block per SM; warp 0 loads by
+// TMA, warp 1 issues the products, eight warps read the accumulators.  Every wait is bounded (common.cuh).
+// 16384 x 3584 tokens, 128 experts: 62 us after the split's 12 and before the join's 6 (as two launches
+// 32 + 44, each with SMs idle at its end: dWg waits at the hand-over of its accumulators and leaves DRAM
+// half free, dX streams dX_in and dX); 4096 x 1024: 25.9 us in all, 30 with two.
 #include <algorithm>
+#include <cstring>
+#include <type_traits>
 
 #include "gate_split.cuh"
 #include "launch.h"
@@ -78,8 +83,7 @@ struct Sync {
 // A block owns IW x 128 rows i of dWg and 128 columns j, and a run of token rows: chunks of 64 rows
 // of X (as the transposed operand) and of the split dL.  The accumulators are emptied into 32-bit
 // registers after every 128 rows, where the scale of dL changes (and where the chain of truncating
-// additions ends).  16384 x 3584 tokens, 128 experts: 32 us, X read once at 3.7 TB/s; the hand-over of
-// an accumulator every 128 rows, not a pipe, bounds it.  IW = 2: the two accumulators share each chunk of dL (64 KB from L2 per 64 KB of
+// additions ends).  The hand-over of an accumulator every 128 rows, not a pipe, bounds it.  IW = 2: the two accumulators share each chunk of dL (64 KB from L2 per 64 KB of
 // X; with one the copies from L2 bound it); while the second is emptied the first fills again.
 // IW = 1, for batches with too few blocks: two accumulators alternate.
 struct WgArgs {
@@ -93,11 +97,8 @@ constexpr int kWgStageBytes = 65536;
 constexpr int kWgStages = 3;
 
 template <int IW>
-__global__ void __launch_bounds__(kThreads, 1)
-    gate_wgrad_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mL,
-                      const WgArgs a) {
-  extern __shared__ uint8_t raw[];
-  uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+__device__ __forceinline__ void wgrad_block(uint8_t* sm, const CUtensorMap& mX, const CUtensorMap& mL,
+                                            const WgArgs& a, int block) {
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kWgStages * kWgStageBytes);
   uint64_t *full = bars, *empty = bars + kWgStages, *acc_full = bars + 2 * kWgStages, *acc_empty = acc_full + 2;
   uint32_t* holder = reinterpret_cast<uint32_t*>(acc_empty + 2);
@@ -123,8 +124,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *holder;
   const Sync sy{flag, a.status};
-  const int i0 = blockIdx.x * 128 * IW, r0 = blockIdx.y * a.run, r1 = min(a.T, r0 + a.run);
-  const int j0 = blockIdx.z * 128;
+  const int bi = (a.d + 128 * IW - 1) / (128 * IW), runs = (a.T + a.run - 1) / a.run;
+  const int r_at = block / bi % runs;
+  const int i0 = block % bi * 128 * IW, r0 = r_at * a.run, r1 = min(a.T, r0 + a.run);
+  const int j0 = block / bi / runs * 128;
   const int nb = min(2, (a.Ep - j0) / 64);          // 64-column boxes of dL's hi (and lo)
   const int chunks = (r1 - r0 + 63) / 64;
   if (warp < 4) {
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // runs of partial sums are laid out as row_sum_join_kernel reads them
-    const int slot = a.direct ? 0 : 2 * (int)blockIdx.y + (r1 == a.T);
+    const int slot = a.direct ? 0 : 2 * r_at + (r1 == a.T);
 #pragma unroll
     for (int h = 0; h < IW; ++h) {
       const int i = i0 + 128 * h + 32 * q + lane;
@@ -252,8 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------- dX
 // A block takes a tile of 128 tokens, keeps its split dL in shared memory (E <= 256) and walks a
 // part of d in tiles of 128: the split Wg comes from L2 in chunks of 64 experts, dX_in by TMA
-// into the tile that the accumulator warps add to in place and that TMA writes out.  16384 x 3584
-// tokens, 128 experts: 44 us, 5.3 TB/s of dX_in and dX; the tiles' loads and stores bound it.
+// into the tile that the accumulator warps add to in place and that TMA writes out.  Bound by the
+// tiles' loads and stores (dX_in and dX at 5.3 TB/s where dX has the device alone).
 struct DxArgs {
   const float *sT, *sW;
   int T, d, E, Ep;
@@ -274,14 +277,11 @@ struct DxPlan {
 };
 
 template <int NKB>
-__global__ void __launch_bounds__(kThreads, 1)
-    gate_dx_tc_kernel(const __grid_constant__ CUtensorMap mL, const __grid_constant__ CUtensorMap mW,
-                      const __grid_constant__ CUtensorMap mIn, const __grid_constant__ CUtensorMap mOut,
-                      const DxArgs a) {
+__device__ __forceinline__ void dx_block(uint8_t* sm, const CUtensorMap& mL, const CUtensorMap& mW,
+                                         const CUtensorMap& mIn, const CUtensorMap& mOut, const DxArgs& a,
+                                         int block, int blocks) {
   using PL = DxPlan<NKB>;
   constexpr int IO = PL::kIo, kDxB = PL::kDxB;
-  extern __shared__ uint8_t raw[];
-  uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + PL::kOffBar);
   uint64_t *a_full = bar, *a_empty = bar + 1, *acc_full = bar + 2, *acc_empty = bar + 4, *b_full = bar + 6,
            *b_empty = b_full + kDxB, *io_full = b_empty + kDxB, *io_empty = io_full + IO;
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int bs = 0, io = 0, round = 0;
     uint32_t bp = 1, iop = 1;
     bool ok = true;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x, ++round) {
+    for (int item = block; item < items && ok; item += blocks, ++round) {
       const int t = item / a.parts, p = item - t * a.parts;
       if (lane == 0) {
         ok = sy.wait(a_empty, (round & 1) ^ 1u);
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int bs = 0, tile = 0, round = 0;
     uint32_t bp = 0;
     bool ok = true;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x, ++round) {
+    for (int item = block; item < items && ok; item += blocks, ++round) {
       const int p = item % a.parts;
       if (lane == 0) {
         ok = sy.wait(a_full, round & 1);
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t iop = 0;
     bool ok = true;
     const bool storer = q == 0 && lane == 0;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+    for (int item = block; item < items && ok; item += blocks) {
       const int t = item / a.parts, p = item - t * a.parts;
       const float st = a.sT[t];
       for (int i = begin_of(p); i < begin_of(p + 1) && ok; ++i, ++tile) {
@@ -470,31 +470,89 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+// ---------------------------------------------------------------- both in one launch
+// The first w_blocks blocks sum dWg, the others write dX as they find an SM free.
+struct BothMaps {
+  CUtensorMap X, L64, L, W, in, out;
+};
+template <int IW, int NKB>
+__global__ void __launch_bounds__(kThreads, 1)
+    gate_grad_kernel(const __grid_constant__ BothMaps m, const WgArgs wa, const DxArgs xa, int w_blocks) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  if ((int)blockIdx.x < w_blocks)
+    wgrad_block<IW>(sm, m.X, m.L64, wa, blockIdx.x);
+  else
+    dx_block<NKB>(sm, m.L, m.W, m.in, m.out, xa, (int)blockIdx.x - w_blocks, (int)gridDim.x - w_blocks);
+}
+
 int pad64(int E) { return (E + 63) / 64 * 64; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Token rows per block of dWg (a multiple of 128) and accumulators per block: what takes least time
-// by 1.5 us per 128 rows with two, 1 us with one, 3 us to start, and the partial sums' way through
-// L2 and the launch that joins them.
-struct WgPlan {
-  int run, iw;
+// How a call is cut: token rows per block of dWg (a multiple of 128) and accumulators per block, and
+// column parts per token tile of dX.  What takes least time by 2.2 us per 128 rows of dWg with two
+// accumulators, 1.4 with one, 1 us and 0.3 per 64 experts for a 128 x 128 tile of dX, 3 us to start
+// either, and the partial sums' way through L2 and the launch that joins them; the blocks of dX take
+// the SMs that dWg leaves and each of the others when its block ends.
+struct GatePlan {
+  int run, iw, parts;
 };
-WgPlan wgrad_plan(int T, int d, int E) {
-  const int all = (T + 127) / 128, jb = (E + 127) / 128;
-  WgPlan best{all * 128, 2};
+GatePlan gate_plan(int T, int d, int E, bool wgrad, bool dx, int sms) {
+  struct Last {
+    int T, d, E, what, sms;
+    GatePlan plan;
+  };
+  thread_local Last last{-1, 0, 0, 0, 0, {}};       // a layer's calls are alike
+  const int what = wgrad + 2 * dx;
+  if (last.T == T && last.d == d && last.E == E && last.what == what && last.sms == sms) return last.plan;
+  const int tt = (T + 127) / 128, nit = (d + 127) / 128, jb = (E + 127) / 128, nkb = (E + 63) / 64;
+  const int most = wgrad ? std::min(tt, sum_parts((size_t)d * E)) : 1;
+  GatePlan best{tt * 128, 1, 1};
   double cost = 1e300;
-  for (int iw = 1; iw <= 2; ++iw) {
-    const int blocks = (d + 128 * iw - 1) / (128 * iw) * jb;
-    for (int p = 1; p <= std::min(all, sum_parts((size_t)d * E)); ++p) {
-      const int run = (all + p - 1) / p, runs = (all + run - 1) / run;
-      const double c = ((blocks * runs + 151) / 152) * (run * (iw == 2 ? 1.5 : 1.0) + 3.0) +
-                       (runs > 1 ? 2.0 + runs * (double)d * E * 1e-6 : 0);
-      if (c < cost) {
-        cost = c;
-        best = WgPlan{run * 128, iw};
+  for (int iw = 1; iw <= (wgrad ? 2 : 1); ++iw) {
+    const int cols = (d + 128 * iw - 1) / (128 * iw) * jb;
+    for (int q = 1; q <= most; ++q) {
+      const int run = (tt + q - 1) / q, runs = (tt + run - 1) / run;
+      const long long W = wgrad ? (long long)cols * runs : 0;
+      const double w = run * (iw == 2 ? 2.2 : 1.4) + 3.0;
+      const double join = runs > 1 ? 2.0 + runs * (double)d * E * 1e-6 : 0.0;
+      const double early = (double)(W / sms) * w;    // SMs without a last block of dWg are free then
+      const long long late = W % sms;
+      if (!dx) {
+        const double c = early + (late ? w : 0.0) + join;
+        if (c < cost) {
+          cost = c;
+          best = GatePlan{run * 128, iw, 1};
+        }
+        continue;
+      }
+      for (int p = 1; p <= std::min(nit, 16); p += p < 4 ? 1 : p < 8 ? 2 : 4) {
+        const double us = (nit + p - 1) / p * (1.0 + 0.3 * nkb) + 3.0;
+        const long long X = (long long)tt * p;
+        // n rounds of the free SMs, and what the late ones add in that time
+        long long n = std::max<long long>(1, (long long)((X * us - late * us) / (sms * us)));
+        double end = 0.0;
+        for (int step = 0; step < 8; ++step, ++n) {
+          const double t = n * us;                   // after `early`
+          const long long m = t > w ? (long long)((t - w) / us) : 0;
+          if ((sms - late) * n + late * m >= X) {
+            end = early + std::max(t, late ? w : 0.0);
+            break;
+          }
+          if ((sms - late) * n + late * (m + 1) >= X) {   // the late ones' next blocks end it
+            end = early + std::max(w + (m + 1) * us, t);
+            break;
+          }
+        }
+        if (end == 0.0) end = early + w + n * us;
+        if (end + join < cost) {
+          cost = end + join;
+          best = GatePlan{run * 128, iw, p};
+        }
       }
     }
   }
+  last = Last{T, d, E, what, sms, best};
   return best;
 }
 
@@ -513,31 +571,30 @@ GateWs gate_ws(int T, int d, int E) {
   return w;
 }
 
-template <int NKB>
-cudaError_t launch_dx_tc(const CUtensorMap& mL, const CUtensorMap& mW, const CUtensorMap& mIn,
-                         const CUtensorMap& mOut, DxArgs a, int sms, cudaStream_t s) {
-  auto kern = gate_dx_tc_kernel<NKB>;
+template <int IW, int NKB>
+cudaError_t launch_both(const BothMaps& m, const WgArgs& wa, const DxArgs& xa, int w_blocks, int x_blocks,
+                        cudaStream_t s) {
+  auto kern = gate_grad_kernel<IW, NKB>;
   MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
-  const int tt = (a.T + 127) / 128, nit = (a.d + 127) / 128;
-  long long cost = 0;
-  for (int p = 1; p <= nit; ++p) {                  // fewest rounds; a part reloads dL (1 tile's time)
-    const long long c = ((long long)tt * p + sms - 1) / sms * ((nit + p - 1) / p + 1);
-    if (p == 1 || c < cost) {
-      cost = c;
-      a.parts = p;
-    }
-  }
-  const int grid = (int)std::min<long long>((long long)tt * a.parts, sms);
-  return launch_k(kern, grid, kThreads, DxPlan<NKB>::kBytes, s, true, mL, mW, mIn, mOut, a);
+  const size_t w_smem = (size_t)kWgStages * kWgStageBytes + 256 + 1024, x_smem = DxPlan<NKB>::kBytes;
+  const size_t smem = !x_blocks ? w_smem : !w_blocks ? x_smem : std::max(w_smem, x_smem);
+  return launch_k(kern, w_blocks + x_blocks, kThreads, smem, s, true, m, wa, xa, w_blocks);
 }
 
 }  // namespace
 
-// Few logits go to the multiply-add kernels (grad.cu), few of odd rows (whose split is scalar) longer.
-// us for dlogits, dWg and dX of 1024 columns, multiply-adds / here: E = 64: T = 32 11.1 / 10.6, 128
-// 17.8 / 12.4; E = 8: T = 256 11.0 / 12.1, 1024 13.6 / 12; E = 13: T = 256 12.9 / 14.1; E = 127: T = 128
-// 25 / 26, T = 256 28.6 / 28.2.  At 16384 x 3584 x 128 the multiply-adds' dX alone takes 494 us.
-bool gate_tc_ok(int T, int E) { return E <= 256 && (long long)T * E >= (E % 4 ? 32768 : 4096); }
+// The multiply-add kernels (grad.cu) need no split and start faster.  us there / here: both gradients,
+// 1024 columns, E = 8: T = 16 7.5 / 7.3, E = 128: T = 1 15.0 / 10.9, 256 24.5 / 15.1; odd rows, whose split
+// is scalar: E = 127: T = 16 15.2 / 15.9, 64 19.4 / 17.1.  dWg alone: E = 128: T = 16 10.0 / 10.2, 64
+// 13.7 / 11.3; E = 256: T = 64 14.3 / 17.9, 256 24.2 / 21.5; E = 127: T = 256 22.4 / 24.1.  dX alone: 256 x 1024
+// x 128 8.9 / 11.7, 256 x 3584 x 128 16.0 / 12.8 (16384 x 3584 x 128: 494 / 44).
+bool gate_tc_ok(int T, int d, int E, bool wgrad, bool dx) {
+  if (E > 256) return false;
+  const bool odd = E % 4 != 0;
+  if (wgrad && dx) return !odd || (long long)T * E >= 2048;
+  if (wgrad) return T >= (odd ? 512 : 128);
+  return dx && (double)T * d * E >= 64e6;
+}
 size_t gate_tc_bytes(int T, int d, int E) { return T > 0 ? gate_ws(T, d, E).total : 0; }
 
 cudaError_t launch_gate_tc(const float* logits, const int32_t* topk_idx, const float* dtopk_w,
@@ -557,36 +614,39 @@ cudaError_t launch_gate_tc(const float* logits, const int32_t* topk_idx, const f
   const uint64_t l_dims[2] = {(uint64_t)2 * Ep, (uint64_t)T}, x_dims[2] = {(uint64_t)d, (uint64_t)T};
   const uint64_t w_dims[2] = {(uint64_t)Ep, (uint64_t)d};
   const uint32_t b64[2] = {64, 64}, b128[2] = {64, 128};
+  BothMaps m;
+  memset(&m, 0, sizeof(m));
+  const GatePlan pl = gate_plan(T, d, E, dWg != nullptr, dx != nullptr, sms);
+  WgArgs wa{};
+  DxArgs xa{};
+  int w_blocks = 0, x_blocks = 0, runs = 0;
+  float* partial = reinterpret_cast<float*>(ws + w.partial);
   if (dWg) {
-    CUtensorMap mX, mL;
-    if (!encode_f16_map(&mX, tokens, 2, x_dims, b64) || !encode_f16_map(&mL, dl2, 2, l_dims, b64))
+    if (!encode_f16_map(&m.X, tokens, 2, x_dims, b64) || !encode_f16_map(&m.L64, dl2, 2, l_dims, b64))
       return cudaErrorInvalidValue;
-    const WgPlan pl = wgrad_plan(T, d, E);
-    const int runs = (T + pl.run - 1) / pl.run;
-    float* partial = reinterpret_cast<float*>(ws + w.partial);
-    const WgArgs a{sT, runs == 1 ? dWg : partial, T, d, E, Ep, pl.run, runs == 1, status};
-    auto kern = pl.iw == 2 ? gate_wgrad_kernel<2> : gate_wgrad_kernel<1>;
-    MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
-    MOE_LAUNCH(launch_k(kern, dim3((d + 128 * pl.iw - 1) / (128 * pl.iw), runs, (E + 127) / 128), kThreads,
-                        (size_t)kWgStages * kWgStageBytes + 256 + 1024, s, true, mX, mL, a));
-    if (runs > 1) MOE_LAUNCH(launch_sum_join(dWg, partial, d, E, T, pl.run, sms, s));
+    runs = (T + pl.run - 1) / pl.run;
+    wa = WgArgs{sT, runs == 1 ? dWg : partial, T, d, E, Ep, pl.run, runs == 1, status};
+    w_blocks = (d + 128 * pl.iw - 1) / (128 * pl.iw) * runs * ((E + 127) / 128);
   }
   if (dx) {
-    CUtensorMap mL, mW, mIn, mOut;
-    if (!encode_f16_map(&mL, dl2, 2, l_dims, b128) || !encode_f16_map(&mW, W2, 2, w_dims, b128) ||
-        !encode_f16_map(&mOut, dx, 2, x_dims, b128))
+    if (!encode_f16_map(&m.L, dl2, 2, l_dims, b128) || !encode_f16_map(&m.W, W2, 2, w_dims, b128) ||
+        !encode_f16_map(&m.out, dx, 2, x_dims, b128) || (dx_in && !encode_f16_map(&m.in, dx_in, 2, x_dims, b128)))
       return cudaErrorInvalidValue;
-    if (!dx_in)
-      mIn = mOut;
-    else if (!encode_f16_map(&mIn, dx_in, 2, x_dims, b128))
-      return cudaErrorInvalidValue;
-    DxArgs a{sT, sW, T, d, E, Ep, 1, dx_in != nullptr, status};
-    const int nkb = Ep / 64;
-    if (nkb == 1) return launch_dx_tc<1>(mL, mW, mIn, mOut, a, sms, s);
-    if (nkb == 2) return launch_dx_tc<2>(mL, mW, mIn, mOut, a, sms, s);
-    if (nkb == 3) return launch_dx_tc<3>(mL, mW, mIn, mOut, a, sms, s);
-    return launch_dx_tc<4>(mL, mW, mIn, mOut, a, sms, s);
+    xa = DxArgs{sT, sW, T, d, E, Ep, pl.parts, dx_in != nullptr, status};
+    x_blocks = (T + 127) / 128 * pl.parts;
   }
+  auto with_iw = [&](auto nkb) {
+    constexpr int K = decltype(nkb)::value;
+    return pl.iw == 2 ? launch_both<2, K>(m, wa, xa, w_blocks, x_blocks, s)
+                      : launch_both<1, K>(m, wa, xa, w_blocks, x_blocks, s);
+  };
+  using std::integral_constant;
+  const int nkb = Ep / 64;
+  MOE_LAUNCH(nkb == 1   ? with_iw(integral_constant<int, 1>())
+             : nkb == 2 ? with_iw(integral_constant<int, 2>())
+             : nkb == 3 ? with_iw(integral_constant<int, 3>())
+                        : with_iw(integral_constant<int, 4>()));
+  if (runs > 1) MOE_LAUNCH(launch_sum_join(dWg, partial, d, E, T, pl.run, sms, s));
   return cudaSuccess;
 }
 

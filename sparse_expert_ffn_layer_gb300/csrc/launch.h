@@ -218,9 +218,9 @@ size_t row_sums_bytes(int di0, int dj0, int di1, int dj1, bool f16, int S_max);
 // Joins the partial sums of runs of `run` rows (slot 2 q, the last run's 2 q + 1) in order.
 cudaError_t launch_sum_join(float* G, float* partial, int di, int dj, int T, int run, int sms,
                             cudaStream_t s);
-// The gate's whole gradient on the tensor cores (gate_grad.cu): f16 tokens, where gate_tc_ok; dWg
-// (may be null) without rows left out.
-bool gate_tc_ok(int T, int E);
+// The gate's gradients on the tensor cores (gate_grad.cu): f16 tokens, E <= 256, where gate_tc_ok says
+// that they are faster; dWg without rows left out.
+bool gate_tc_ok(int T, int d, int E, bool wgrad, bool dx);
 size_t gate_tc_bytes(int T, int d, int E);
 cudaError_t launch_gate_tc(const float* logits, const int32_t* topk_idx, const float* dtopk_w,
                            const float* dlosses, const int32_t* counts, const int32_t* n_valid,

@@ -103,7 +103,7 @@ moe_status moe_gate_backward_workspace_size(int T, int d, int E, moe_dtype dtype
   if (d % lane_elems(dtype) || d > kMaxCols) return MOE_ERR_UNSUPPORTED;
   // the tensor-core form, and the form that leaves masked rows out
   size_t most = row_sums_bytes(d, E, 0, 0, dtype == MOE_F16, T);
-  if (dtype == MOE_F16 && gate_tc_ok(T, E)) most = std::max(most, gate_tc_bytes(T, d, E));
+  if (dtype == MOE_F16 && E <= 256) most = std::max(most, gate_tc_bytes(T, d, E));
   *bytes = kAlign + align_up(most);
   return MOE_OK;
 }
@@ -144,8 +144,9 @@ moe_status moe_gate_topk_backward(const float* logits, const int32_t* topk_idx, 
     int* status = deep ? static_cast<int*>(workspace) : nullptr;
     // Masked tokens may hold anything: their rows are left out of dWg's sums row by row, which the
     // tensor-core form's boxes of rows cannot do.  (It needs no mask for dtokens: dlogits are zero.)
-    const bool tc = deep && f16 && gate_tc_ok(T, E) && (dtokens || !token_mask);
-    float* dWg_tc = tc && !token_mask ? dWg : nullptr;
+    float* dWg_tc = f16 && !token_mask ? dWg : nullptr;
+    const bool tc = f16 && gate_tc_ok(T, d, E, dWg_tc, dtokens);
+    if (!tc) dWg_tc = nullptr;
     if (tc)
       MOE_TRY(launch_gate_tc(logits, topk_idx, dtopk_w, dlosses, counts, n_valid, token_mask, k, dlogits,
                              static_cast<const __half*>(tokens), Wg, dWg_tc,

@@ -240,7 +240,8 @@ GATE = [("f16", 1, 128, 4, 1), ("f16", 5, 8, 1, 1), ("f16", 63, 136, 7, 2), ("f1
 # where the two forms change over, on both sides, and small ones of the tensor-core form
 GATE += [("f16", 16, 136, 256, 2), ("f16", 15, 136, 256, 2), ("f16", 40, 264, 128, 1), ("f16", 64, 8, 64, 2),
          ("f16", 512, 72, 8, 2), ("f16", 511, 72, 8, 2), ("f16", 2048, 264, 2, 1), ("f16", 2521, 136, 13, 2),
-         ("f16", 129, 72, 255, 2), ("f16", 128, 72, 255, 2), ("f16", 4097, 64, 4, 1), ("f16", 100, 128, 60, 2)]
+         ("f16", 129, 72, 255, 2), ("f16", 128, 72, 255, 2), ("f16", 4097, 64, 4, 1), ("f16", 100, 128, 60, 2), ("f16", 1, 1024, 128, 2),
+         ("f16", 3, 264, 256, 2), ("f16", 17, 136, 127, 1), ("f16", 256, 2048, 128, 2), ("f16", 513, 72, 127, 2)]
 
 
 def gate_inputs(g, dt, T, d, E, k):
