@@ -309,8 +309,11 @@ __global__ void __launch_bounds__(SumWarps<R>::kThreads, R >= 128 ? 1 : 2) row_s
   auto load = [&](int stage) {
     if (li < items) {
       const uint32_t st = ring_at + stage * (kStage * 2), dst = st + (xr * kLdX + xc) * 2;
+      const int left = lhi - llo - lc * kRows;     // rows of this and later chunks
+      const int need = (left + 15) & ~15;          // rows that the products read
 #pragma unroll
       for (int p = 0; p < XP; ++p) {
+        if (xr + NT / 16 * p >= need) break;
         if (kPerm) {
           const bool on = (unsigned)lrow[p] < (unsigned)a.T;
           const uint32_t t = on ? lrow[p] : 0;
@@ -321,12 +324,12 @@ __global__ void __launch_bounds__(SumWarps<R>::kThreads, R >= 128 ? 1 : 2) row_s
         }
       }
       const uint32_t hst = st + kRows * kLdX * 2;
-      const int left = lhi - llo - lc * kRows;     // rows of this and later chunks
       const __half* src = lH + (uint64_t)(uint32_t)(lc * kRows * 2) * (uint32_t)ldh;
 #pragma unroll
       for (int p = 0; p < HP; ++p) {
         const int q = tid + p * NT;                // row, part, piece of R columns
         const int row = q / (R / 4), part = q / (R / 8) % 2, col = (q % (R / 8)) * 8;
+        if (row >= need) break;
         const bool on = row < left && col < lw;
         cp_async16_at(hst + (row * kLdH + part * R + col) * 2, on ? src + (row * 2 + part) * ldh + col : lH, on);
       }
@@ -367,6 +370,7 @@ __global__ void __launch_bounds__(SumWarps<R>::kThreads, R >= 128 ? 1 : 2) row_s
       float t[MI][NJ][4];
 #pragma unroll
       for (int k = 0; k < kRows; k += 16) {
+        if (k > 0 && k >= it.hi - it.lo - row) break;   // short groups: no products of empty rows
         uint32_t fa[MI][4];
 #pragma unroll
         for (int i = 0; i < MI; ++i) ldsm4_t_at(fa[i], xb + (k * kLdX + i * 16) * 2);
@@ -493,33 +497,41 @@ __global__ void __launch_bounds__(kSumThreads) row_sum_fma_kernel(const SumArgs 
   clear_empty(a, g);
 }
 
-// Groups of several segments: their partial sums in order.
-__global__ void __launch_bounds__(256) row_sum_join_kernel(const SumArgs a) {
-  pdl_wait();                                      // on every path: completion stays transitive
-  const SumJob& jb = a.job[blockIdx.z];
-  const int n = blockIdx.y;
-  int lo = 0, hi = a.S_max;
-  if (a.offsets) {                                 // as group_table: clamped, a running maximum
-    __shared__ int top[8];
-    auto bound = [&](int i) { return min(max(a.offsets[i], 0), a.S_max); };
-    hi = bound(n + 1);
-    for (int i = threadIdx.x; i <= n; i += 256) lo = max(lo, bound(i));
-    lo = __reduce_max_sync(0xffffffffu, lo);
-    if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = lo;
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < 8; ++q) lo = max(lo, top[q]);
-    hi = max(lo, hi);
-  }
-  const int segs = (hi - lo + a.seg - 1) / a.seg;
-  if (segs < 2 || !jb.G) return;
-  const float scale = a.scale ? a.scale[n] : 1.f;
-  const size_t all = (size_t)jb.di * jb.dj;
-  float* G = jb.G + n * all;
-  const float* first = jb.partial + partial_slot(lo, a.seg, false) * all;   // and every second after it
-  const size_t step = (size_t)gridDim.x * 256;
-  if (all % 4 == 0) {
-    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < all / 4; i += step) {
+// Groups of several segments: their partial sums in order.  A block finds those groups (while the
+// sums still run) and takes pieces of 1024 values of theirs; a grid over all groups, most of which may
+// have one segment, took 10 us to start and end its blocks.
+constexpr int kJoinThreads = 256;
+__host__ __device__ inline int join_pieces(int di, int dj) {
+  const size_t all = (size_t)di * dj, per = all % 4 ? kJoinThreads : 4 * kJoinThreads;
+  return (int)((all + per - 1) / per);
+}
+__global__ void __launch_bounds__(kJoinThreads) row_sum_join_kernel(const SumArgs a) {
+  extern __shared__ int table[];
+  __shared__ int several;
+  const int tid = threadIdx.x;
+  if (tid == 0) several = 0;
+  const Segments g = segment_table<kJoinThreads>(a, table);
+  int* list = table + 2 * (a.N + 1) + 64;
+  for (int n = tid; n < a.N; n += kJoinThreads)
+    if (g.start[n + 1] - g.start[n] > 1) list[atomicAdd(&several, 1)] = n;   // each sums for itself
+  __syncthreads();
+  pdl_wait();                                       // on every path: completion stays transitive
+  const int p0 = a.job[0].G ? join_pieces(a.job[0].di, a.job[0].dj) : 0;
+  const int p1 = a.job[1].G ? join_pieces(a.job[1].di, a.job[1].dj) : 0;
+  const long long items = (long long)several * (p0 + p1);
+  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+    const int n = list[it / (p0 + p1)];
+    int piece = (int)(it % (p0 + p1));
+    const bool second = piece >= p0;
+    if (second) piece -= p0;
+    const SumJob& jb = a.job[second];
+    const int segs = g.start[n + 1] - g.start[n];
+    const float scale = a.scale ? a.scale[n] : 1.f;
+    const size_t all = (size_t)jb.di * jb.dj, i = (size_t)piece * kJoinThreads + tid;
+    float* G = jb.G + n * all;
+    const float* first = jb.partial + partial_slot(g.bound[n], a.seg, false) * all;   // and every second after it
+    if (all % 4 == 0) {
+      if (i >= all / 4) continue;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       const float* p = first + 4 * i;
 #pragma unroll 8
@@ -528,14 +540,20 @@ __global__ void __launch_bounds__(256) row_sum_join_kernel(const SumArgs a) {
         v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
       }
       *reinterpret_cast<float4*>(G + 4 * i) = make_float4(scale * v.x, scale * v.y, scale * v.z, scale * v.w);
-    }
-  } else {
-    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < all; i += step) {
+    } else if (i < all) {
       float v = 0.f;
       for (int q = 0; q < segs; ++q) v += first[(2 * q + (q == segs - 1)) * all + i];
       G[i] = scale * v;
     }
   }
+}
+cudaError_t launch_join(const SumArgs& a, int sms, cudaStream_t s) {
+  long long pieces = 0;
+  for (const SumJob& j : a.job)
+    if (j.G) pieces += join_pieces(j.di, j.dj);
+  const long long groups = std::min<long long>(a.N, a.S_max / (a.seg + 1));   // longer than a segment
+  const int grid = (int)std::max<long long>(1, std::min<long long>(groups * pieces, 8 * sms));
+  return launch_k(row_sum_join_kernel, grid, kJoinThreads, sizeof(int) * (3 * ((size_t)a.N + 1) + 64), s, true, a);
 }
 
 // Short f16 groups take the multiply-add form (one launch less), where its items are two rounds of
@@ -603,8 +621,7 @@ cudaError_t launch_sum_rank(SumArgs& a, bool f16, bool tc, int sms, bool pdl, cu
     MOE_LAUNCH(launch_k(kern, grid, kSumThreads, smem, s, pdl, a));
   }
   if (a.S_max <= a.seg) return cudaSuccess;        // no group has a second segment
-  const int bx = (int)std::min<size_t>((widest / 4 + 255) / 256, std::max<size_t>(1, 32 * sms / a.N));
-  return launch_k(row_sum_join_kernel, dim3(std::max(1, bx), a.N, 2), 256, 0, s, true, a);
+  return launch_join(a, sms, s);
 }
 
 // Column blocks of a job of either type, as launch_sum_rank cuts them.
@@ -792,9 +809,7 @@ cudaError_t launch_sum_join(float* G, float* partial, int di, int dj, int T, int
   a.T = a.S_max = T;
   a.N = 1;
   a.seg = run;
-  const size_t all = (size_t)di * dj;
-  const int bx = (int)std::min<size_t>((all / 4 + 255) / 256, (size_t)32 * sms);
-  return launch_k(row_sum_join_kernel, dim3(std::max(1, bx), 1, 1), 256, 0, s, true, a);
+  return launch_join(a, sms, s);
 }
 
 size_t row_sums_bytes(int di0, int dj0, int di1, int dj1, bool f16, int S_max) {
