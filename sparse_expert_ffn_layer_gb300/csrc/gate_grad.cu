@@ -12,7 +12,7 @@
 //
 // One launch computes both, a part of its blocks dWg and the rest dX, one block per SM; warp 0 loads by
 // TMA, warp 1 issues the products, eight warps read the accumulators.  Every wait is bounded (common.cuh).
-// 16384 x 3584 tokens, 128 experts: 62 us after the split's 12 and before the join's 6 (as two launches
+// 16384 x 3584 tokens, 128 experts: 64 us after the split's 12 and before the join's 5 (as two launches
 // 32 + 44, each with SMs idle at its end: dWg waits at the hand-over of its accumulators and leaves DRAM
 // half free, dX streams dX_in and dX); 4096 x 1024: 25.9 us in all, 30 with two.
 #include <algorithm>
