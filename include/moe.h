@@ -312,6 +312,7 @@ MOE_API moe_status moe_gate_backward_workspace_size(int T, int d, int E, moe_dty
  *   dWg nullable (then tokens is not read), dtokens nullable (then Wg is not read), dtokens_in
  *   nullable (zero; may be dtokens itself).
  *   workspace: moe_gate_backward_workspace_size bytes; may be NULL when dWg and dtokens are.
+ *   Otherwise no output overlaps an input (dtokens and tokens the same: MOE_ERR_INVALID_ARG).
  *   token_mask also leaves the masked tokens' rows out of dWg: what they hold has no effect.
  *   MOE_F16, E <= 256: Wg may be rounded to f16 (scaled by powers of two) for dtokens, as
  *   the expert FFN's weights are; dWg keeps 32-bit accuracy.
@@ -334,6 +335,7 @@ MOE_API moe_status moe_gate_topk_backward(const float* logits, const int32_t* to
  *   dout [T, d], expert_out and dexpert_out [S_max, d] in `dtype`.  Slots that no assignment
  *   names are left as they were.  dexpert_out nullable (then topk_w is not read), dtopk_w
  *   nullable (then expert_out is not read); not both.  residual_in's gradient is dout itself.
+ *   dexpert_out does not overlap dout, nor expert_out.
  *   A slot that two assignments name (moe_dispatch names none twice) gets one of their rows.
  * Shapes: T <= 2^30, d <= 2^20.
  */
@@ -360,7 +362,8 @@ MOE_API moe_status moe_adapter_workspace_size(int T, int d_in, int d_out, int r,
  *   tokens [T, d_in], A [N, d_in, r], B [N, r, d_out], base (nullable: zero) and out [T, d_out]
  *   in `dtype`; scale [N] float32.  base may be out itself (the shared projection's result, in
  *   place).  Rows of out whose token has no adapter are left as they were.  Otherwise out
- *   overlaps no input.  A token named by more than one slot gets one of their results.
+ *   overlaps no input (out and tokens the same: MOE_ERR_INVALID_ARG).  A token named by more
+ *   than one slot gets one of their results.
  *   hidden nullable [S_max, r] float32, for the backward pass; rows >= offsets[N] are not written.
  *   Bounds: as moe_expert_ffn's: no slot >= S_max is used, and offsets outside [0, S_max] or
  *   decreasing and perm entries outside [0, T) are skipped and recorded as
@@ -386,6 +389,7 @@ MOE_API moe_status moe_adapter_forward(const void* tokens, const int32_t* perm,
  *   hidden: as moe_adapter_forward wrote it.  dtokens nullable; dtokens_in nullable (zero) and
  *   may be dtokens itself; dA nullable (then tokens is not read), dB nullable (then hidden is
  *   not read); not all three.  base's gradient is dout itself.
+ *   dtokens overlaps neither dout nor tokens (the same: MOE_ERR_INVALID_ARG).
  *   Everything else as moe_adapter_forward (dh is the row that is rounded to f16, for dtokens
  *   only).  MOE_F16, long runs: an infinite token or dout row makes its sums infinite or NaN.
  */

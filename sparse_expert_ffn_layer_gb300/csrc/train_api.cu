@@ -139,6 +139,7 @@ moe_status moe_gate_topk_backward(const float* logits, const int32_t* topk_idx, 
       if (st != MOE_OK) return st;
       if (!workspace || ws_bytes < need) return MOE_ERR_WORKSPACE;
     }
+    if (dtokens && dWg && dtokens == tokens) return MOE_ERR_INVALID_ARG;   // written while read
     const int f16 = dtype == MOE_F16;
     uint8_t* ws = static_cast<uint8_t*>(workspace) + kAlign;
     int* status = deep ? static_cast<int*>(workspace) : nullptr;
@@ -177,6 +178,7 @@ moe_status moe_combine_backward(const void* dout, const void* expert_out, const 
     if (!aligned16(dout) || !aligned16(expert_out) || !aligned16(slot_of) || !aligned16(topk_w) ||
         !aligned16(dexpert_out) || !aligned16(dtopk_w))
       return MOE_ERR_UNSUPPORTED;
+    if (dexpert_out && dexpert_out == dout) return MOE_ERR_INVALID_ARG;   // written while read
     MOE_TRY(launch_combine_backward(dout, expert_out, slot_of, topk_w, dtype == MOE_F16, T, d, k, S_max,
                                     dexpert_out, dtopk_w, as_stream(stream)));
     return MOE_OK;
@@ -207,6 +209,7 @@ moe_status moe_adapter_forward(const void* tokens, const int32_t* perm, const in
         !aligned16(workspace))
       return MOE_ERR_UNSUPPORTED;
     if (!workspace || ws_bytes < adapter_bytes(d_in, d_out, r, N, S_max, dtype)) return MOE_ERR_WORKSPACE;
+    if (out == tokens) return MOE_ERR_INVALID_ARG;   // written while read
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     float* partial = reinterpret_cast<float*>(ws + kAlign + hidden_bytes(r, S_max));
     MOE_TRY(launch_adapter(tokens, A, B, base, out, hidden, partial, scale, perm, offsets,
@@ -240,6 +243,7 @@ moe_status moe_adapter_backward(const void* dout, const void* tokens, const floa
         !aligned16(workspace))
       return MOE_ERR_UNSUPPORTED;
     if (!workspace || ws_bytes < adapter_bytes(d_in, d_out, r, N, S_max, dtype)) return MOE_ERR_WORKSPACE;
+    if (dtokens && (dtokens == dout || (dA && dtokens == tokens))) return MOE_ERR_INVALID_ARG;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     float* dh = reinterpret_cast<float*>(ws + kAlign);
     float* partial = reinterpret_cast<float*>(ws + kAlign + hidden_bytes(r, S_max));

@@ -127,6 +127,19 @@ def test_adapter_refusals(m):
     assert bwd(T=0, dA=None, dB=None) == m.MOE_OK
 
 
+def test_outputs_that_would_overwrite_what_is_read(m):
+    """The same buffer as an input that other blocks still read is refused."""
+    Q, inv = ctypes.c_void_p(0x20000), m.MOE_ERR_INVALID_ARG
+    n = 1 << 24
+    assert m.lib.moe_adapter_forward(P, Q, Q, Q, Q, Q, P, 1, 8, 64, 64, 8, 4, 8, P, None, Q, n, S0) == inv
+    b = m.lib.moe_adapter_backward
+    assert b(P, Q, Q, Q, Q, Q, Q, Q, None, 1, 8, 64, 64, 8, 4, 8, P, None, None, Q, n, S0) == inv
+    assert b(Q, P, Q, Q, Q, Q, Q, Q, None, 1, 8, 64, 64, 8, 4, 8, P, Q, None, Q, n, S0) == inv
+    assert m.lib.moe_combine_backward(P, Q, Q, Q, 1, 8, 64, 1, 8, P, Q, S0) == inv
+    assert m.lib.moe_gate_topk_backward(Q, Q, Q, None, None, None, None, P, Q, 1, 8, 64, 4, 1, Q, Q, None, P,
+                                        Q, n, S0) == inv
+
+
 def test_binding_refuses_what_the_kernels_would_misread(m):
     T, d, r, N = 4, 16, 8, 2
     x, out = torch.zeros(T, d, dtype=torch.float16), torch.zeros(T, d, dtype=torch.float16)
