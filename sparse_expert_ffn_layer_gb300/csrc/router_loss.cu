@@ -662,13 +662,13 @@ int lanes_for(int E) {
   return lanes;
 }
 
-// Blocks of the row pass: two per SM, fewer for short batches.
+// Blocks of the row pass: as many as an SM holds (see its launch bounds), fewer for short batches.
 constexpr int kMaxRecords = 512;
 // Rows that a block of the row pass takes at once.
 int block_rows(int E) { return kRowWarps * (32 / lanes_for(E)); }
 int row_blocks(int T, int E, int sms) {
   const int rows = block_rows(E);
-  return std::max(1, std::min({(T + rows - 1) / rows, 2 * sms, kMaxRecords}));
+  return std::max(1, std::min({(T + rows - 1) / rows, (E > 512 ? 1 : 2) * sms, kMaxRecords}));
 }
 
 // Up to this many passes of eight blocks over the rows one cluster does the whole call (one block where

@@ -923,8 +923,8 @@ def test_training_step_of_router_and_adapters(m, T, d, r, N, E, k):
         check(b[name], want, 2.0 ** -14 * want.abs().max(), name)
 
 
-def test_training_step_streams_graph_and_repeats(m):
-    shape = (300, 128, 16, 4, 8, 2)
+@pytest.mark.parametrize("shape", [(300, 128, 16, 4, 8, 2), (1300, 256, 40, 2, 64, 2)])
+def test_training_step_streams_graph_and_repeats(m, shape):
     c, b = step_inputs(2, *shape), step_buffers(m, *shape)
     step(m, c, b)
     torch.cuda.synchronize()
@@ -965,6 +965,33 @@ def test_training_step_streams_graph_and_repeats(m):
     torch.cuda.synchronize()
     for q in OUTS:
         assert torch.equal(b[q], want[q]), q
+
+
+def test_two_router_calls_at_once(m):
+    """Losses and gate gradients of two batches on two streams, each with its own workspace."""
+    g = gen(10)
+    T, d, E, k = 3000, 512, 64, 2
+    x, Wg, logits, idx, dw = gate_inputs(g, torch.float16, T, d, E, k)
+    dloss = torch.tensor([0.01, 0.001], device="cuda")
+    e = lambda *s, t=torch.float32: torch.zeros(s, dtype=t, device="cuda")
+    out = [dict(c=e(E, t=torch.int32), p=e(E), l=e(2), n=e(1, t=torch.int32), dl=e(T, E), dWg=e(d, E),
+                dx=e(T, d, t=torch.float16), bws=e(m.moe_balance_workspace_size(T, E), t=torch.uint8),
+                gws=e(m.moe_gate_backward_workspace_size(T, d, E, x.dtype), t=torch.uint8)) for _ in range(3)]
+
+    def run(o, stream=None):
+        m.moe_balance_loss(logits, idx, o["c"], o["p"], o["l"], o["n"], o["bws"], stream=stream)
+        m.moe_gate_topk_backward(logits, idx, o["dl"], dtopk_w=dw, dlosses=dloss, counts=o["c"], n_valid=o["n"],
+                                 tokens=x, Wg=Wg, dWg=o["dWg"], dtokens=o["dx"], workspace=o["gws"], stream=stream)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for o, s in zip(out, streams):
+            run(o, s)
+    run(out[2])
+    torch.cuda.synchronize()
+    for q in ("c", "p", "l", "n", "dl", "dWg", "dx"):
+        assert torch.equal(out[0][q], out[2][q]) and torch.equal(out[1][q], out[2][q]), q
+    assert all(m.moe_status_read(o["gws"]) == m.MOE_OK for o in out)
 
 
 def test_two_adapter_calls_at_once(m):
