@@ -219,7 +219,7 @@ size_t row_sums_bytes(int di0, int dj0, int di1, int dj1, bool f16, int S_max);
 cudaError_t launch_sum_join(float* G, float* partial, int di, int dj, int T, int run, int sms,
                             cudaStream_t s);
 // The gate's gradients on the tensor cores (gate_grad.cu): f16 tokens, E <= 256, where gate_tc_ok says
-// that they are faster; dWg without rows left out.
+// that they are faster.
 bool gate_tc_ok(int T, int d, int E, bool wgrad, bool dx);
 size_t gate_tc_bytes(int T, int d, int E);
 cudaError_t launch_gate_tc(const float* logits, const int32_t* topk_idx, const float* dtopk_w,

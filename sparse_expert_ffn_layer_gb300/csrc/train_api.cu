@@ -101,7 +101,7 @@ moe_status moe_gate_backward_workspace_size(int T, int d, int E, moe_dtype dtype
   moe_status st = check_router(T, E, 1);
   if (st != MOE_OK) return st;
   if (d % lane_elems(dtype) || d > kMaxCols) return MOE_ERR_UNSUPPORTED;
-  // the tensor-core form, and the form that leaves masked rows out
+  // either form
   size_t most = row_sums_bytes(d, E, 0, 0, dtype == MOE_F16, T);
   if (dtype == MOE_F16 && E <= 256) most = std::max(most, gate_tc_bytes(T, d, E));
   *bytes = kAlign + align_up(most);
@@ -143,22 +143,20 @@ moe_status moe_gate_topk_backward(const float* logits, const int32_t* topk_idx, 
     const int f16 = dtype == MOE_F16;
     uint8_t* ws = static_cast<uint8_t*>(workspace) + kAlign;
     int* status = deep ? static_cast<int*>(workspace) : nullptr;
-    // Masked tokens may hold anything: their rows are left out of dWg's sums row by row, which the
-    // tensor-core form's boxes of rows cannot do.  (It needs no mask for dtokens: dlogits are zero.)
-    float* dWg_tc = f16 && !token_mask ? dWg : nullptr;
-    const bool tc = f16 && gate_tc_ok(T, d, E, dWg_tc, dtokens);
-    if (!tc) dWg_tc = nullptr;
+    // Masked tokens may hold anything: their rows are left out of dWg's sums (dtokens need no mask:
+    // dlogits are zero).
+    const bool tc = f16 && gate_tc_ok(T, d, E, dWg, dtokens);
     if (tc)
       MOE_TRY(launch_gate_tc(logits, topk_idx, dtopk_w, dlosses, counts, n_valid, token_mask, k, dlogits,
-                             static_cast<const __half*>(tokens), Wg, dWg_tc,
+                             static_cast<const __half*>(tokens), Wg, dWg,
                              static_cast<const __half*>(dtokens_in), static_cast<__half*>(dtokens), ws,
                              status, T, d, E, s));
     else
       MOE_TRY(launch_dlogits(logits, topk_idx, dtopk_w, dlosses, counts, n_valid, token_mask, T, E, k,
                              dlogits, status, s));
-    if (dWg && !dWg_tc)
+    if (dWg && !tc)
       MOE_TRY(launch_row_sums(tokens, dlogits, dWg, d, E, 0, nullptr, nullptr, nullptr, 0, 0, 0, nullptr,
-                              nullptr, nullptr, token_mask, ws, f16, T, T, 1, /*pdl=*/!tc, s));
+                              nullptr, nullptr, token_mask, ws, f16, T, T, 1, /*pdl=*/true, s));
     if (dtokens && !tc) MOE_TRY(launch_gate_dx(dlogits, Wg, dtokens_in, f16, T, d, E, dtokens, s));
     return MOE_OK;
   });

@@ -317,6 +317,38 @@ def test_gate_backward_masked_rows_and_in_place(m):
     assert not dWg0.any()
 
 
+@pytest.mark.parametrize("T,d,E", [(1, 8, 4), (70, 136, 64), (130, 264, 128), (1000, 520, 128), (4100, 1024, 64),
+                                   (2050, 776, 255), (700, 392, 300), (900, 3584, 256)])
+@pytest.mark.parametrize("kind", ["some", "blocks", "tail", "one", "none"])
+@pytest.mark.parametrize("form", ["all", "weights"])
+def test_gate_backward_masks(m, T, d, E, kind, form):
+    """Masked tokens hold NaN and infinities: they add nothing to dWg, and their dlogits are zero."""
+    g = gen(T + d + E)
+    x, Wg, logits, idx, dw = gate_inputs(g, torch.float16, T, d, E, 2)
+    t = torch.arange(T, device="cuda")
+    mask = {"some": torch.rand(T, generator=g, device="cuda") < 0.7, "blocks": (t // 64) % 3 != 1,
+            "tail": t < (T * 5) // 8, "one": t == T // 2, "none": t < 0}[kind]
+    x[~mask] = torch.where(t[~mask] % 2 == 0, float("nan"), float("inf"))[:, None].half()
+    logits[~mask] = float("nan")
+    ws = torch.empty(m.moe_gate_backward_workspace_size(T, d, E, x.dtype), dtype=torch.uint8, device="cuda")
+    dl, dWg = torch.full((T, E), 5.0, device="cuda"), torch.full((d, E), 5.0, device="cuda")
+    dx = randn(g, T, d, dtype=torch.float16) if form == "all" else None
+    before = dx.clone() if form == "all" else None
+    m.moe_gate_topk_backward(logits, idx, dl, dtopk_w=dw, token_mask=mask, tokens=x, Wg=Wg, dWg=dWg,
+                             dtokens=dx, dtokens_in=dx, workspace=ws)
+    assert m.moe_status_read(ws) == m.MOE_OK
+    assert not dl[~mask].any() and torch.isfinite(dl).all()
+    xd, dd = x[mask].double(), dl[mask].double()
+    mag = xd.abs().t() @ dd.abs()
+    top = dd.abs().max() if len(dd) else 0           # as in test_gate_backward, by the largest of all rows
+    check(dWg, xd.t() @ dd, (64 + T / 64) * U * mag + 4 * U * xd.abs().sum(0)[:, None] * top, "dWg")
+    if form == "all":
+        assert torch.equal(dx[~mask], before[~mask])
+        want = before[mask].double() + dd @ Wg.double().t()
+        mag = before[mask].double().abs() + dd.abs() @ Wg.double().abs().t()
+        check(dx[mask], want, 2.0 ** -11 * 1.02 * (want.abs() + mag) + 2.0 ** -24 + 2.0 ** -36 * top * d, "dtokens")
+
+
 @pytest.mark.parametrize("T", [40, 300])
 def test_gate_backward_infinities_stay_where_they_are(m, T):
     """A token whose gradient is NaN spoils its own row of dtokens and nothing of the others'."""
