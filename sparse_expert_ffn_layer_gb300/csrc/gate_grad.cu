@@ -623,17 +623,17 @@ cudaError_t launch_both(const BothMaps& m, const WgArgs& wa, const DxArgs& xa, i
 
 }  // namespace
 
-// The multiply-add kernels (grad.cu) need no split and start faster.  us there / here: both gradients,
-// 1024 columns, E = 8: T = 16 7.5 / 7.3, E = 128: T = 1 15.0 / 10.9, 256 24.5 / 15.1; odd rows, whose split
-// is scalar: E = 127: T = 16 15.2 / 15.9, 64 19.4 / 17.1.  dWg alone: E = 128: T = 16 10.0 / 10.2, 64
-// 13.7 / 11.3; E = 256: T = 64 14.3 / 17.9, 256 24.2 / 21.5; E = 127: T = 256 22.4 / 24.1.  dX alone: 256 x 1024
-// x 128 8.9 / 11.7, 256 x 3584 x 128 16.0 / 12.8 (16384 x 3584 x 128: 494 / 44).
+// The multiply-add kernels (grad.cu) need no split but take a launch per gradient.  us there / here: both
+// gradients, 1024 columns, T = 1: E = 8 7.6 / 7.2, E = 127 14.6 / 9.3; T = 256: E = 8 11.2 / 9.2, E = 127
+// 28 / 17.  dWg alone: E = 8: T = 256 8.7 / 9.2, 512 11.0 / 10.4; E = 128: T = 16 10.0 / 9.4, 128 14.8 / 12.4;
+// 3584 columns, E = 256: T = 64 14.2 / 17.1, 128 19.4 / 20.4, 256 24.4 / 21.0.  dX alone: 512 x 1024 x 128
+// 11.6 / 12.0, 256 x 3584 x 256 27.4 / 22.4; odd rows, whose split is scalar: 512 x 1024 x 127 12.0 / 15.3,
+// 256 x 3584 x 255 27.7 / 27.0 (16384 x 3584 x 128: 494 / 44).
 bool gate_tc_ok(int T, int d, int E, bool wgrad, bool dx) {
   if (E > 256) return false;
-  const bool odd = E % 4 != 0;
-  if (wgrad && dx) return !odd || (long long)T * E >= 2048;
-  if (wgrad) return T >= (odd ? 512 : 128);
-  return dx && (double)T * d * E >= 64e6;
+  if (wgrad && dx) return true;
+  if (wgrad) return T >= 128 && (long long)T * E >= 4096;
+  return dx && (double)T * d * E >= (E % 4 ? 230e6 : 100e6);
 }
 size_t gate_tc_bytes(int T, int d, int E) { return T > 0 ? gate_ws(T, d, E).total : 0; }
 
