@@ -121,7 +121,7 @@ __device__ __forceinline__ int swz(int row, int piece) {
 
 struct TallArgs {
   AdapterArgs a;
-  float* partial;            // [parts of the first product][rows of all groups][r]
+  float* partial;            // [parts of the first product][slots from the first group's first on][r]
   int slots_k, slots_n;      // resident blocks of the two launches
 };
 
@@ -142,6 +142,19 @@ template <int R>
 __device__ __forceinline__ int parts_of_k(const TallArgs& ta, int tiles) {
   const int w = PlanTall<R>::kSub * kChunk;
   return column_parts(tiles, (ta.a.dk + w - 1) / w, ta.slots_k, 2);
+}
+
+// Where partial h lie: a whole one (a single part) is given out at once, by its slot.  Others are counted
+// from the first group's first slot: their rows are bounded by the tiles (kPartItems), which only cover
+// the slots that groups own, not those before offsets[0].
+struct PartialRows {
+  float* at;
+  int first, count;          // slot of row 0; rows of a part
+};
+__device__ __forceinline__ PartialRows partial_rows(const TallArgs& ta, const int* bound, int parts) {
+  const int first = bound[0], count = bound[ta.a.N] - first;
+  if (parts == 1 && ta.a.hidden) return {ta.a.hidden, 0, count};
+  return {ta.partial, first, count};
 }
 
 // The chunks of a block's items, loaded ahead of their use.  Item i is part i % parts of tile
@@ -316,8 +329,7 @@ __global__ void __launch_bounds__(kTallThreads, 2)
   ring.parts = parts_of_k<R>(ta, ntiles);
   ring.items = ntiles * ring.parts;
   ring.blocks = gridDim.x - 1;
-  const int S = ring.bound[a.N];
-  float* partial = ring.parts == 1 && a.hidden ? a.hidden : ta.partial;
+  const PartialRows pr = partial_rows(ta, ring.bound, ring.parts);
   ring.begin();
   const int wr = (w & 3) * 16, wc = w >> 2, h0 = WN > 1 ? wc * (R / WN) : 0;
   const int l15 = lane & 15, lh = lane >> 4, l3 = (lane >> 3) & 1, l7 = lane & 7;
@@ -393,7 +405,7 @@ __global__ void __launch_bounds__(kTallThreads, 2)
     }
     if (WK == 1 || wc == 0) {
       const int sa = s0 + wr + (lane >> 2), sb = sa + 8;
-      float* pa = partial + ((size_t)part * S + sa) * a.r;
+      float* pa = pr.at + ((size_t)part * pr.count + (sa - pr.first)) * a.r;
       float* pb = pa + (size_t)8 * a.r;
 #pragma unroll
       for (int j = 0; j < NF; ++j) {
@@ -422,8 +434,8 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
   ring.mW = &mQ;
   const int ntiles = tall_setup(ring, a, raw);
   ring.chunks = (a.dn + PL::kSub * kChunk - 1) / (PL::kSub * kChunk);
-  const int parts_k = parts_of_k<R>(ta, ntiles), S = ring.bound[a.N];
-  const float* partial = parts_k == 1 && a.hidden ? a.hidden : ta.partial;
+  const int parts_k = parts_of_k<R>(ta, ntiles);
+  const PartialRows pr = partial_rows(ta, ring.bound, parts_k);
   // an item reads and converts its tile's h first, all its parts
   ring.parts = column_parts(ntiles, ring.chunks, ta.slots_n, 2 + (R >= 64 ? 2 : 1) * parts_k);
   ring.items = ntiles * ring.parts;
@@ -458,9 +470,9 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
       // Unconditional loads, in batches: each waited for on its own under a condition, they took
       // most of the time (3575 rows, 1808 columns, r = 96: 80 us).  A row behind the run's end reads
       // the last one and is not stored; columns behind r read the first and count as zero.
-      const uint32_t ra = (uint32_t)min(sa, s1 - 1), rb = (uint32_t)min(sb, s1 - 1);
+      const uint32_t ra = (uint32_t)(min(sa, s1 - 1) - pr.first), rb = (uint32_t)(min(sb, s1 - 1) - pr.first);
       for (int p = 0; p < parts_k; ++p) {
-        const float* src = partial + (size_t)p * S * a.r + 2 * (lane & 3);
+        const float* src = pr.at + (size_t)p * pr.count * a.r + 2 * (lane & 3);
         const float *pa = src + (uint64_t)ra * (uint32_t)a.r, *pb = src + (uint64_t)rb * (uint32_t)a.r;
         constexpr int KB = R / 16 < 4 ? R / 16 : 4;
 #pragma unroll
@@ -498,7 +510,7 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
             ma = fmaxf(ma, m);
             oa |= odd;
           }
-          if (a.hidden && part == 0 && wc == 0 && partial != a.hidden) {
+          if (a.hidden && part == 0 && wc == 0 && pr.at != a.hidden) {
             const int s = q & 1 ? sb : sa, col = 16 * k + 8 * (q >> 1) + 2 * (lane & 3);
             if (s < s1 && col < a.r)
               *reinterpret_cast<float2*>(a.hidden + (size_t)s * a.r + col) = v[k][q];

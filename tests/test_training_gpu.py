@@ -756,6 +756,68 @@ def test_adapter_bad_entries_take_nothing_into_the_gradients(m, dt, T):
     assert (dx[rest] == 9.0).all()
 
 
+def behind(m, size, extra=16 << 20):
+    """A workspace of exactly `size` bytes with a guard behind it."""
+    buf = torch.full((size + extra,), 0x5A, dtype=torch.uint8, device="cuda")
+    return buf[:size], buf[size:]
+
+
+@pytest.mark.parametrize("r", [8, 24, 64, 128])
+@pytest.mark.parametrize("off", [[19000, 20000], [18200, 18900, 18900, 20000], [19500, 19700, 100, 20000],
+                                 [12000, 12500, 13000]])
+def test_adapter_long_plan_that_starts_late(m, off, r):
+    """Slots before offsets[0] belong to no adapter (a slice of a larger plan): nothing is read from or
+    written for them, nor behind the workspace, and the rows are those of the plan without the gap."""
+    g = gen(41 + r)
+    S, T, di, do, N = 20000, 1900, 2048, 1032, len(off) - 1
+    dt, i32 = torch.float16, dict(dtype=torch.int32, device="cuda")
+    bound = [max(off[:n + 1]) for n in range(N + 1)]
+    rows = bound[N] - bound[0]
+    tok = torch.randperm(T, generator=g, device="cuda")[:rows].to(torch.int32)
+    perm = torch.full((S,), -1, **i32)               # entries that no adapter owns are not looked at
+    perm[bound[0]:bound[N]] = tok
+    perm0 = torch.full((S,), -1, **i32)
+    perm0[:rows] = tok
+    x, base = randn(g, T, di, dtype=dt), randn(g, T, do, dtype=dt)
+    A, B = randn(g, N, di, r, sigma=di ** -0.5, dtype=dt), randn(g, N, r, do, sigma=0.3, dtype=dt)
+    scale = randn(g, N)
+    got = []
+    for p, o in ((perm, off), (perm0, [b - bound[0] for b in bound])):
+        o = torch.tensor(o, **i32)
+        size = m.moe_adapter_workspace_size(T, di, do, r, N, S, dt)
+        e = lambda *s, t=torch.float32: torch.full(s, 3.0, dtype=t, device="cuda")
+        out, hid, dx, dA, dB = e(T, do, t=dt), e(S, r), e(T, di, t=dt), e(N, di, r), e(N, r, do)
+        want_status = m.MOE_ERR_DEVICE_BOUNDS if p is perm and off != bound else m.MOE_OK
+        ws, guard = behind(m, size)
+        m.moe_adapter_forward(x, p, o, A, B, scale, out, ws, base=base, hidden=hid)
+        assert m.moe_status_read(ws) == want_status
+        assert (guard == 0x5A).all()
+        ws, guard = behind(m, size)
+        m.moe_adapter_backward(base, x, hid, p, o, A, B, scale, ws, dtokens=dx, dtokens_in=x, dA=dA, dB=dB)
+        assert m.moe_status_read(ws) == want_status
+        assert (guard == 0x5A).all()
+        first = bound[0] if p is perm else 0
+        assert (hid[:first] == 3.0).all() and (hid[first + rows:] == 3.0).all()
+        got.append((out, hid[first:first + rows], dx, dA, dB))
+    for a, b in zip(got[0][:3], got[1][:3]):
+        assert torch.equal(a, b)
+    for n in range(N):
+        s = slice(bound[n] - bound[0], bound[n + 1] - bound[0])
+        t, sc = tok[s].long(), scale[n].double()
+        xx, y, h = x[t].double(), base[t].double(), got[0][1][s].double()
+        # a chain of K truncating additions per hidden value, then one of rows / 64 + 64 for the sums
+        K = 2 * (4 * (di / 512 + 1) + 16)
+        check(h, xx @ A[n].double(), K * U * (xx.abs() @ A[n].double().abs()) + 1e-37, "hidden")
+        yf = torch.where(y == 0, y, y.abs().clamp(min=2.0 ** -14))
+        dh, dhm = y @ B[n].double().t(), y.abs() @ B[n].double().abs().t()
+        KW, top = 64 + len(t) / 64, lambda v: v.abs().max() if len(t) else 0
+        for q in got:
+            check(q[3][n], sc * (xx.t() @ dh), sc.abs() * ((KW + K) * U * (xx.abs().t() @ dhm) +
+                  2 * U * xx.abs().sum(0)[:, None] * top(dh)) + 1e-37, "dA")
+            check(q[4][n], sc * (h.t() @ y), sc.abs() * (KW * U * (h.abs().t() @ yf) +
+                  2 * U * yf.sum(0)[None, :] * top(h)) + 1e-37, "dB")
+
+
 def test_adapter_few_tokens_of_many(m):
     """Most tokens without an adapter: the plans go by the caller's bound, the work by the offsets."""
     g = gen(21)
