@@ -446,48 +446,47 @@ __device__ __forceinline__ void dx_block(uint8_t* sm, const CUtensorMap& mL, con
     uint32_t iop = 0;
     bool ok = true;
     const bool storer = q == 0 && lane == 0;
-    for (int item = block; item < items && ok; item += blocks) {
+    for (int item = block; item < items; item += blocks) {
       const int t = item / a.parts, p = item - t * a.parts;
       const float st = a.sT[t];
-      for (int i = begin_of(p); i < begin_of(p + 1) && ok; ++i, ++tile) {
+      for (int i = begin_of(p); i < begin_of(p + 1); ++i, ++tile) {
         const int buf = tile & 1;
-        ok = sy.wait(&acc_full[buf], (tile >> 1) & 1);
-        ok = ok && sy.wait(&io_full[io], iop);
-        // all warps of the half go on together: they meet at the store below
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const float s = st * a.sW[i], s2 = s / kGateLo;
-        uint8_t* box = sm + PL::kOffIo + (io * 2 + ch) * kTile + row * 128;
-        const uint32_t t0 = tmem + ((uint32_t)(32 * q) << 16) + buf * 256 + ch * 64;
+        if (ok) ok = sy.wait(&acc_full[buf], (tile >> 1) & 1) && sy.wait(&io_full[io], iop);
+        ok = __all_sync(0xffffffffu, ok);
+        // The four warps of a half meet at the barrier below, and each learns by itself that a wait gave
+        // up: it then goes on to the barrier of every tile that is left, without waits, sums or stores.
+        if (ok) {
+          tc_fence_after();
+          const float s = st * a.sW[i], s2 = s / kGateLo;
+          uint8_t* box = sm + PL::kOffIo + (io * 2 + ch) * kTile + row * 128;
+          const uint32_t t0 = tmem + ((uint32_t)(32 * q) << 16) + buf * 256 + ch * 64;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          float u[32], v[32];
-          tmem_ld32x2(t0 + 32 * b, t0 + 128 + 32 * b, u, v);
+          for (int b = 0; b < 2; ++b) {
+            float u[32], v[32];
+            tmem_ld32x2(t0 + 32 * b, t0 + 128 + 32 * b, u, v);
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint4* at = reinterpret_cast<uint4*>(box + (((4 * b + w) ^ (row & 7)) << 4));
-            uint4 old = make_uint4(0u, 0u, 0u, 0u);
-            if (a.with_in) old = *at;
-            uint32_t o[4] = {old.x, old.y, old.z, old.w};
+            for (int w = 0; w < 4; ++w) {
+              uint4* at = reinterpret_cast<uint4*>(box + (((4 * b + w) ^ (row & 7)) << 4));
+              uint4 old = make_uint4(0u, 0u, 0u, 0u);
+              if (a.with_in) old = *at;
+              uint32_t o[4] = {old.x, old.y, old.z, old.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&o[j]));
-              const int k = 8 * w + 2 * j;
-              const __half2 r = __floats2half2_rn(fmaf(s, u[k], fmaf(s2, v[k], f.x)),
-                                                  fmaf(s, u[k + 1], fmaf(s2, v[k + 1], f.y)));
-              o[j] = *reinterpret_cast<const uint32_t*>(&r);
+              for (int j = 0; j < 4; ++j) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&o[j]));
+                const int k = 8 * w + 2 * j;
+                const __half2 r = __floats2half2_rn(fmaf(s, u[k], fmaf(s2, v[k], f.x)),
+                                                    fmaf(s, u[k + 1], fmaf(s2, v[k + 1], f.y)));
+                o[j] = *reinterpret_cast<const uint32_t*>(&r);
+              }
+              *at = make_uint4(o[0], o[1], o[2], o[3]);
             }
-            *at = make_uint4(o[0], o[1], o[2], o[3]);
           }
+          tc_fence_before();
+          mbar_arrive(&acc_empty[buf]);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        tc_fence_before();
-        mbar_arrive(&acc_empty[buf]);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         asm volatile("bar.sync %0, 128;" ::"r"(1 + ch) : "memory");
-        if (storer) {
+        if (storer && ok) {
           const int x = i * 128 + 64 * ch;
           if (x < a.d) tma_store_2d(&mOut, x, t * 128, sm + PL::kOffIo + (io * 2 + ch) * kTile);
           bulk_commit();

@@ -1,6 +1,8 @@
 """Training and adapter calls on the CPU: workspace sizes and refusals.  Every call returns before
 any CUDA work is enqueued."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -176,3 +178,40 @@ def test_binding_refuses_what_the_kernels_would_misread(m):
     with pytest.raises(ValueError, match="expert_out has shape"):
         m.moe_combine_backward(x, torch.zeros(T, d + 1, dtype=torch.float16), idx, torch.zeros(T, 1),
                                dtopk_w=torch.zeros(T, 1))
+
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "sparse_expert_ffn_layer_gb300", "csrc")
+
+
+def source(name):
+    """A source file without its comments."""
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def block_behind(text, at):
+    """The braces' content that opens at or behind `at`."""
+    i = text.index("{", at)
+    depth = 0
+    for j in range(i, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[j], 0)
+        if depth == 0:
+            return text[i + 1:j]
+    raise AssertionError("unbalanced")
+
+
+def test_no_warp_leaves_a_loop_whose_barrier_others_wait_at():
+    """A bounded wait may give up in one warp and not in the next.  In a loop that meets at a barrier of
+    several warps, each warp therefore goes round as often as the others, whatever its waits say."""
+    text = source("gate_grad.cu")
+    seen = 0
+    for mt in re.finditer(r"\bfor \(", text):
+        head = text[mt.start():text.index("{", mt.start())]
+        body = block_behind(text, mt.start())
+        if "bar.sync" not in body:
+            continue
+        seen += 1
+        assert not re.search(r"\b(break|return|continue|goto)\b", body.split("bar.sync")[0]), head
+        assert not re.search(r"\bok\b", head), head
+    assert seen >= 1
