@@ -273,6 +273,16 @@ struct TallRing {
       phase ^= 1u;
     }
   }
+  // The end of a block (all threads): after a wait gave up, what is in flight lands before the shared
+  // memory is released.  A stage's last load is of this round of the ring or of the one before it
+  // (none yet: a phase that counts as complete).
+  __device__ __forceinline__ void finish() {
+    __syncthreads();
+    if (!*abort) return;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (threadIdx.x == 0)
+      for (int s = 0; s < NS; ++s) mbar_drain(&full[s], s < lstage ? lphase ^ 1u : lphase);
+  }
 };
 
 // Shared-memory set-up of both kernels; returns the number of tiles.
@@ -417,6 +427,7 @@ __global__ void __launch_bounds__(kTallThreads, 2)
       }
     }
   }
+  ring.finish();
 }
 
 template <int R, bool kT>
@@ -592,6 +603,7 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
       ring.done();
     }
   }
+  ring.finish();
 }
 
 // ---------------------------------------------------------------- f16, short runs

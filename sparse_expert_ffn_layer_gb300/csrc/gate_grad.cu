@@ -79,6 +79,37 @@ struct Sync {
   }
 };
 
+// What warp 0 has in flight: the last load into each of the barriers whose bits are set, with the parity
+// of its phase.
+struct InFlight {
+  uint32_t issued = 0, parity = 0;
+  __device__ __forceinline__ void note(int bar, uint32_t p) {
+    issued |= 1u << bar;
+    parity = (parity & ~(1u << bar)) | p << bar;
+  }
+};
+// The end of a block, all threads.  After a wait gave up, the loads and products that are still in
+// flight land before their memory is released (bounded: 100 ms each).  bars: the barriers that loads
+// count on, from InFlight's bit 0 on; spare: one of which nothing has used yet.
+__device__ __forceinline__ void end_block(const Sync& sy, const InFlight& fl, uint64_t* bars, uint64_t* spare,
+                                          uint32_t tmem) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (*sy.abort && lane == 0) {
+    if (warp == 0)
+      for (int b = 0; b < 32; ++b)
+        if (fl.issued >> b & 1u) mbar_drain(&bars[b], fl.parity >> b & 1u);
+    if (warp == 1) {
+      tc_commit(spare);
+      mbar_drain(spare, 0);
+    }
+  }
+  __syncwarp();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
 // ---------------------------------------------------------------- dWg
 // A block owns IW x 128 rows i of dWg and 128 columns j, and a run of token rows: chunks of 64 rows
 // of X (as the transposed operand) and of the split dL.  The accumulators are emptied into 32-bit
@@ -105,8 +136,8 @@ __device__ __forceinline__ void wgrad_block(uint8_t* sm, const CUtensorMap& mX, 
                                             const WgArgs& a, int block) {
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kWgStages * kWgStageBytes);
   uint64_t *full = bars, *empty = bars + kWgStages, *clean = bars + 2 * kWgStages, *acc_full = clean + kWgStages,
-           *acc_empty = acc_full + 2;
-  uint32_t* holder = reinterpret_cast<uint32_t*>(acc_empty + 2);
+           *acc_empty = acc_full + 2, *spare = acc_empty + 2;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(spare + 1);
   int* flag = reinterpret_cast<int*>(holder + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
@@ -119,6 +150,7 @@ __device__ __forceinline__ void wgrad_block(uint8_t* sm, const CUtensorMap& mX, 
       mbar_init(&acc_full[h], 1);
       mbar_init(&acc_empty[h], 256);
     }
+    mbar_init(spare, 1);
     *flag = 0;
     fence_mbar_init();
   }
@@ -136,6 +168,7 @@ __device__ __forceinline__ void wgrad_block(uint8_t* sm, const CUtensorMap& mX, 
   const int j0 = block / bi / runs * 128;
   const int nb = min(2, (a.Ep - j0) / 64);          // 64-column boxes of dL's hi (and lo)
   const int chunks = (r1 - r0 + 63) / 64;
+  InFlight fl;
   if (warp < 4) {
     regs_down<40>();
     if (warp == 0) {
@@ -149,6 +182,7 @@ __device__ __forceinline__ void wgrad_block(uint8_t* sm, const CUtensorMap& mX, 
             uint8_t* st = sm + stage * kWgStageBytes;
             const int y = r0 + 64 * c;
             mbar_expect_tx(&full[stage], (2 * IW + 2 * nb) * 8192);
+            fl.note(stage, phase ^ 1u);
             for (int b = 0; b < 2 * IW; ++b) tma_load_2d(st + b * 8192, &mX, i0 + 64 * b, y, &full[stage]);
             for (int b = 0; b < 2 * nb; ++b)
               tma_load_2d(st + 32768 + b * 8192, &mL, (b < nb ? 0 : a.Ep) + j0 + 64 * (b % nb), y, &full[stage]);
@@ -286,10 +320,7 @@ __device__ __forceinline__ void wgrad_block(uint8_t* sm, const CUtensorMap& mX, 
       }
     }
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  end_block(sy, fl, full, spare, tmem);
 }
 
 // ---------------------------------------------------------------- dX
@@ -324,8 +355,8 @@ __device__ __forceinline__ void dx_block(uint8_t* sm, const CUtensorMap& mL, con
   constexpr int IO = PL::kIo, kDxB = PL::kDxB;
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + PL::kOffBar);
   uint64_t *a_full = bar, *a_empty = bar + 1, *acc_full = bar + 2, *acc_empty = bar + 4, *b_full = bar + 6,
-           *b_empty = b_full + kDxB, *io_full = b_empty + kDxB, *io_empty = io_full + IO;
-  uint32_t* holder = reinterpret_cast<uint32_t*>(io_empty + IO);
+           *b_empty = b_full + kDxB, *io_full = b_empty + kDxB, *io_empty = io_full + IO, *spare = io_empty + IO;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(spare + 1);
   int* flag = reinterpret_cast<int*>(holder + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
@@ -343,6 +374,7 @@ __device__ __forceinline__ void dx_block(uint8_t* sm, const CUtensorMap& mL, con
       mbar_init(&acc_full[s], 1);
       mbar_init(&acc_empty[s], 256);
     }
+    mbar_init(spare, 1);
     *flag = 0;
     fence_mbar_init();
   }
@@ -355,6 +387,7 @@ __device__ __forceinline__ void dx_block(uint8_t* sm, const CUtensorMap& mL, con
   const uint32_t tmem = *holder;
   const Sync sy{flag, a.status};
   const int nit = (a.d + 127) / 128, items = (a.T + 127) / 128 * a.parts;
+  InFlight fl;
   auto begin_of = [&](int p) { return (int)((long long)nit * p / a.parts); };
   if (warp == 0) {
     int bs = 0, io = 0, round = 0;
@@ -366,6 +399,7 @@ __device__ __forceinline__ void dx_block(uint8_t* sm, const CUtensorMap& mL, con
         ok = sy.wait(a_empty, (round & 1) ^ 1u);
         if (ok) {
           mbar_expect_tx(a_full, NKB * 2 * kTile);
+          fl.note((int)(a_full - bar), round & 1);
           for (int kb = 0; kb < NKB; ++kb) {
             tma_load_2d(sm + kb * 2 * kTile, &mL, 64 * kb, t * 128, a_full);
             tma_load_2d(sm + (kb * 2 + 1) * kTile, &mL, a.Ep + 64 * kb, t * 128, a_full);
@@ -376,6 +410,7 @@ __device__ __forceinline__ void dx_block(uint8_t* sm, const CUtensorMap& mL, con
             ok = sy.wait(&b_empty[bs], bp);
             if (!ok) break;
             mbar_expect_tx(&b_full[bs], kTile);
+            fl.note((int)(b_full - bar) + bs, bp ^ 1u);
             tma_load_2d(sm + PL::kOffB + bs * kTile, &mW, 64 * kb, i * 128, &b_full[bs]);
             if (++bs == kDxB) {
               bs = 0;
@@ -388,6 +423,7 @@ __device__ __forceinline__ void dx_block(uint8_t* sm, const CUtensorMap& mL, con
           if (a.with_in) {
             uint8_t* st = sm + PL::kOffIo + io * 2 * kTile;
             mbar_expect_tx(&io_full[io], 2 * kTile);
+            fl.note((int)(io_full - bar) + io, iop ^ 1u);
             tma_load_2d(st, &mIn, i * 128, t * 128, &io_full[io]);
             tma_load_2d(st + kTile, &mIn, i * 128 + 64, t * 128, &io_full[io]);
           } else {
@@ -503,10 +539,7 @@ __device__ __forceinline__ void dx_block(uint8_t* sm, const CUtensorMap& mL, con
     }
     if (storer) bulk_wait_read<0>();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  end_block(sy, fl, bar, spare, tmem);
 }
 
 // ---------------------------------------------------------------- both in one launch

@@ -215,3 +215,16 @@ def test_no_warp_leaves_a_loop_whose_barrier_others_wait_at():
         assert not re.search(r"\b(break|return|continue|goto)\b", body.split("bar.sync")[0]), head
         assert not re.search(r"\bok\b", head), head
     assert seen >= 1
+
+
+def test_blocks_that_give_up_wait_for_their_copies():
+    """Each kernel with bounded waits on bulk copies waits for those in flight at its end: its block's
+    shared memory may be another's a moment later."""
+    for name, body, end in [("gate_grad.cu", "void wgrad_block(", "end_block"), ("gate_grad.cu", "void dx_block(", "end_block"),
+                            ("adapter.cu", "adapter_shrink_kernel(", "ring.finish"),
+                            ("adapter.cu", "adapter_expand_kernel(", "ring.finish")]:
+        text = source(name)
+        last = block_behind(text, text.index(body)).strip().splitlines()[-1]
+        assert last.strip().startswith(end), (name, body, last)
+    assert "mbar_drain" in block_behind(source("gate_grad.cu"), source("gate_grad.cu").index("void end_block("))
+    assert "mbar_drain" in block_behind(source("adapter.cu"), source("adapter.cu").index("void finish("))
