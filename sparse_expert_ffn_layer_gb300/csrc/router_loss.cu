@@ -114,6 +114,10 @@ __device__ __forceinline__ float block_sum(float v, float* scratch) {
   return r;
 }
 
+// The two halves of a cluster's barrier, with work between them (every thread of every block).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 struct LossOut {
   int32_t* counts;
   float* prob_mean;
@@ -133,6 +137,7 @@ template <typename Rec>
 __device__ __forceinline__ void join_records(Rec rec, int nb, int E, int k, LossOut o, float* sh_f,
                                              int* sh_i, float* share) {
   cg::cluster_group cl = cg::this_cluster();
+  cluster_arrive();                                 // waited for below, behind the records' loads
   const int c = (int)cl.block_rank(), ncl = (int)cl.num_blocks();
   const int Ec = (E + ncl - 1) / ncl;                // at most blockDim
   const int parts = max(1, min((int)blockDim.x / Ec, min(nb, kJoinParts)));
@@ -180,6 +185,7 @@ __device__ __forceinline__ void join_records(Rec rec, int nb, int E, int k, Loss
     mine = (float)cnt * p;
   }
   mine = block_sum(mine, scratch);
+  cluster_wait();                                   // rank 0 has started: its shared memory is there
   if (threadIdx.x == 0) cl.map_shared_rank(share, 0)[c] = mine;
   cl.sync();
   if (c == 0 && threadIdx.x == 0) {

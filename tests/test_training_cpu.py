@@ -228,3 +228,14 @@ def test_blocks_that_give_up_wait_for_their_copies():
         assert last.strip().startswith(end), (name, body, last)
     assert "mbar_drain" in block_behind(source("gate_grad.cu"), source("gate_grad.cu").index("void end_block("))
     assert "mbar_drain" in block_behind(source("adapter.cu"), source("adapter.cu").index("void finish("))
+
+
+def test_no_block_writes_to_another_before_the_cluster_has_met():
+    """Another block's shared memory may be touched only once that block has started, which a cluster
+    barrier says.  (Reads through map_shared_rank in the kernels are of complete data, behind cl.sync.)"""
+    for name, body in [("router_loss.cu", "void join_records("), ("adapter.cu", "adapter_f16_kernel("),
+                       ("adapter.cu", "adapter_f32_kernel(")]:
+        text = source(name)
+        kernel = block_behind(text, text.index(body))
+        first = kernel.index("map_shared_rank")
+        assert "cl.sync()" in kernel[:first] or "cluster_wait()" in kernel[:first], (name, body)
