@@ -369,8 +369,8 @@ MOE_API moe_status moe_adapter_workspace_size(int T, int d_in, int d_out, int r,
  *   decreasing and perm entries outside [0, T) are skipped and recorded as
  *   MOE_ERR_DEVICE_BOUNDS in the workspace's status word.
  *   workspace: moe_adapter_workspace_size bytes; contents need no initialisation.
- * MOE_F16: hidden is given out in float32 and rounded to f16, each row scaled by a power of two,
- * for the second product (as the expert FFN rounds its hidden activations).
+ * MOE_F16: hidden is given out in float32, and the second product takes it with 22 bits (2^-25 of the
+ * row's largest value below that), so that out is what float32 sums give, rounded once.
  * Shapes: N <= 1024; r a multiple of 8, at most 128 (adapters of different ranks are padded with
  * zeros); d_in, d_out multiples of 8 (MOE_F16) or 4 (MOE_F32), at most 2^20; T, S_max <= 2^30.
  */
@@ -390,8 +390,7 @@ MOE_API moe_status moe_adapter_forward(const void* tokens, const int32_t* perm,
  *   may be dtokens itself; dA nullable (then tokens is not read), dB nullable (then hidden is
  *   not read); not all three.  base's gradient is dout itself.
  *   dtokens overlaps neither dout nor tokens (the same: MOE_ERR_INVALID_ARG).
- *   Everything else as moe_adapter_forward (dh is the row that is rounded to f16, for dtokens
- *   only).  MOE_F16, long runs: an infinite token or dout row makes its sums infinite or NaN.
+ *   Everything else as moe_adapter_forward (dh in hidden's place).  MOE_F16, long runs: an infinite token or dout row makes its sums infinite or NaN.
  */
 MOE_API moe_status moe_adapter_backward(const void* dout, const void* tokens, const float* hidden,
                                         const int32_t* perm, const int32_t* offsets, const void* A,

@@ -18,10 +18,11 @@
 // (base and Q) load while h is being exchanged, and the next tile's rows while this one is
 // written.  Long runs (tiles of 64 rows) take two launches, see there.
 //
-// f16: h is kept in 32 bits (and given out so) and rounded to f16 for the second product, as the
-// expert FFN rounds its hidden activations; each row is scaled by a power of two first, so that
-// no h overflows or loses bits below f16's range.  The rounding adds at most 2^-11 of the sum of
-// |h Q| to y's own 2^-11 |y|.  f32: fused multiply-adds on the CUDA cores.
+// f16: h is kept in 32 bits (and given out so).  For the second product each row is scaled by a power
+// of two, so that no h overflows or is lost below f16's range, and split into two f16 parts: together
+// h to 2^-22 of itself, 2^-25 of the row's largest, so that y differs from the 32-bit form's by 32-bit
+// rounding before its own 2^-11 |y|.  (One part only: the error of 8192 rows of dtokens, r = 32, was
+// 1.37 times that of 32-bit sums.)  f32: fused multiply-adds on the CUDA cores.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
     if ((unsigned)y1 >= (unsigned)a.T) y1 = -1;
     // ---- h in the layout of the product's left operand: rows g and g + 8, columns
     // 16 k + 2 (lane % 4) + {0, 1, 8, 9}; a row's columns are spread over four lanes
-    uint32_t fh[R / 16][4];
+    uint32_t fh[R / 16][4], fl[R / 16][4];          // high and low parts
     float m0, m1;
     {
       const int sa = s0 + wr + (lane >> 2), sb = sa + 8;
@@ -543,8 +544,11 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float i = q & 1 ? ib : ia;
-          const __half2 h = __floats2half2_rn(v[k][q].x * i, v[k][q].y * i);
+          __half2 h, l;
+          split_f16(v[k][q].x * i, h.x, l.x);
+          split_f16(v[k][q].y * i, h.y, l.y);
           fh[k][q] = *reinterpret_cast<const uint32_t*>(&h);
+          fl[k][q] = *reinterpret_cast<const uint32_t*>(&l);
         }
     }
     // ---- 32 of a chunk's 64 columns per warp
@@ -561,18 +565,21 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
 #pragma unroll
-      for (int k = 0; k < R / 16; ++k)
+      for (int k = 0; k < R / 16; ++k) {
+        uint32_t fb[2][4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          uint32_t fb[4];
           if (kT)
-            ldsm4(fb, qs + (k / 4) * (kChunk * 128) +
-                          swz<RB * 2>(wc * 32 + j * 16 + l7 + lh * 8, 2 * (k % 4) + l3));
+            ldsm4(fb[j], qs + (k / 4) * (kChunk * 128) +
+                             swz<RB * 2>(wc * 32 + j * 16 + l7 + lh * 8, 2 * (k % 4) + l3));
           else
-            ldsm4_t(fb, qs + swz<128>(k * 16 + l15, wc * 4 + j * 2 + lh));
-          mma16816(acc[2 * j], fh[k], fb[0], fb[1]);
-          mma16816(acc[2 * j + 1], fh[k], fb[2], fb[3]);
+            ldsm4_t(fb[j], qs + swz<128>(k * 16 + l15, wc * 4 + j * 2 + lh));
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma16816(acc[j], fl[k], fb[j / 2][j % 2 * 2], fb[j / 2][j % 2 * 2 + 1]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma16816(acc[j], fh[k], fb[j / 2][j % 2 * 2], fb[j / 2][j % 2 * 2 + 1]);
+      }
       // base + scale * sum, rounded once, in place; then 16-byte rows out
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -620,10 +627,10 @@ struct Plan16 {
   static constexpr int WK = kWarps / WN;                           // or along a chunk's columns
   static constexpr int kW = C * kLdR > R * kLdC ? C * kLdR : R * kLdC;
   static constexpr int kStage = 2 * (MT * kLdC + kW);
-  static constexpr int kStages = R >= 64 && R < 128 ? 6 : 4;
+  static constexpr int kStages = R >= 64 && R < 128 ? 5 : 4;       // (three blocks per SM at R = 64)
   static constexpr int kOffPart = kStages * kStage;                // partial h [WK][MT][R]
   static constexpr int kOffH = kOffPart + WK * MT * R * 4;         // h
-  static constexpr int kOffMult = kOffH + MT * kLdR * 2;
+  static constexpr int kOffMult = kOffH + 2 * MT * kLdR * 2;       // (h in two parts)
   static constexpr int kOffTab = kOffMult + MT * 4;                // offsets, tile starts, scratch
 };
 
@@ -645,7 +652,7 @@ __global__ void __launch_bounds__(128, Plan16<R>::kBlocks) adapter_f16_kernel(co
     return;
   }
   float* part = reinterpret_cast<float*>(sm + PL::kOffPart);
-  __half* hs = reinterpret_cast<__half*>(sm + PL::kOffH);         // [MT][R + 8]
+  __half* hs = reinterpret_cast<__half*>(sm + PL::kOffH);         // [MT][R + 8] high parts, then low
   float* mult = reinterpret_cast<float*>(sm + PL::kOffMult);
   int* bound = reinterpret_cast<int*>(sm + PL::kOffTab);
   int* start = bound + a.N + 1;
@@ -852,15 +859,15 @@ __global__ void __launch_bounds__(128, Plan16<R>::kBlocks) adapter_f16_kernel(co
       for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(grp, m, o));
       const int e = scale_exp(m);
       const float inv = exp2_int(-e);
-      __half2 hv[CPT / 2];
+      struct alignas(CPT >= 8 ? 16 : 2 * CPT) Halves { __half v[CPT]; } hv, lv;
 #pragma unroll
-      for (int j = 0; j < CPT; j += 2) hv[j / 2] = __floats2half2_rn(v[j] * inv, v[j + 1] * inv);
+      for (int j = 0; j < CPT; ++j) split_f16(v[j] * inv, hv.v[j], lv.v[j]);
       const float mu = scale * exp2_int(e);
 #pragma unroll
       for (int q = 0; q < kCl; ++q) {
         __half* dh = cl.map_shared_rank(hs, q) + row * kLdR + c0;
-#pragma unroll
-        for (int j = 0; j < CPT / 2; ++j) reinterpret_cast<__half2*>(dh)[j] = hv[j];
+        *reinterpret_cast<Halves*>(dh) = hv;
+        *reinterpret_cast<Halves*>(dh + MT * kLdR) = lv;
         if ((tid & 7) == 0) cl.map_shared_rank(mult, q)[row] = mu;
       }
       if (a.hidden && row < rows) {
@@ -875,9 +882,12 @@ __global__ void __launch_bounds__(128, Plan16<R>::kBlocks) adapter_f16_kernel(co
     // ---- second product: this block's output columns
     constexpr int NF = WCOL / 8;                  // 8-column fragments of a chunk per warp
     const int c0 = w * WCOL;
-    uint32_t fh[R / 16][4];
+    uint32_t fh[R / 16][4], fl[R / 16][4];
 #pragma unroll
-    for (int k = 0; k < R / 16; ++k) frag_a(fh[k], hs + k * 16, kLdR, lane);
+    for (int k = 0; k < R / 16; ++k) {
+      frag_a(fh[k], hs + k * 16, kLdR, lane);
+      frag_a(fl[k], hs + MT * kLdR + k * 16, kLdR, lane);
+    }
     const int g = lane >> 2, q2 = 2 * (lane & 3);
     const float m0 = mult[g], m1 = mult[g + 8];
     for (int c = n0; c < n1; ++c) {
@@ -897,6 +907,8 @@ __global__ void __launch_bounds__(128, Plan16<R>::kBlocks) adapter_f16_kernel(co
             frag_b_nk(fb, qs + (c0 + j * 16) * kLdR + k * 16, kLdR, lane);
           else
             frag_b_kn(fb, qs + k * 16 * kLdC + c0 + j * 16, kLdC, lane);
+          mma16816(acc[2 * j], fl[k], fb[0], fb[1]);
+          mma16816(acc[2 * j + 1], fl[k], fb[2], fb[3]);
           mma16816(acc[2 * j], fh[k], fb[0], fb[1]);
           mma16816(acc[2 * j + 1], fh[k], fb[2], fb[3]);
         }

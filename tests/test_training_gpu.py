@@ -576,6 +576,37 @@ def test_adapter_backward(m, dt, T, di, do, r, N, form):
         assert (dx[rest] == 9.0).all()
 
 
+@pytest.mark.parametrize("dt,T,di,do,r,N", [c for c in ADAPT if c[0] == "f16"])
+@pytest.mark.parametrize("back", [False, True])
+def test_adapter_hidden_rows_keep_32_bit_accuracy(m, dt, T, di, do, r, N, back):
+    """The second product takes h (dh) with more than f16's 11 bits: beside the output's own rounding
+    only what 32-bit sums lose is left."""
+    g = gen(T + di + do + r + 2)
+    dt = torch.float16
+    c = adapter_inputs(m, g, dt, T, di, do, r, N)
+    ws = adapter_ws(m, T, di, do, r, N, dt)
+    e, dk = (di, do) if back else (do, di)
+    src, out = randn(g, T, dk, dtype=dt), torch.full((T, e), 9.0, dtype=dt, device="cuda")
+    if back:
+        m.moe_adapter_backward(src, None, None, c["perm"], c["off"], c["A"], c["B"], c["scale"], ws, dtokens=out)
+    else:
+        m.moe_adapter_forward(src, c["perm"], c["off"], c["A"], c["B"], c["scale"], out, ws)
+    t = c["perm"][:int(c["off"][-1])].long()
+    a = c["ids"][t].long()
+    for n in a.unique().tolist():
+        tt = t[(a == n).nonzero()[:, 0]]
+        P, Q = (c["B"][n].double().t(), c["A"][n].double().t()) if back else (c["A"][n].double(), c["B"][n].double())
+        x, sc = src[tt].double(), float(c["scale"][n])
+        h, hm = x @ P, x.abs() @ P.abs()
+        y, ym = sc * (h @ Q), abs(sc) * (hm @ Q.abs())
+        # h: as in test_adapter_forward.  Its parts leave 2 u of it and 2^-25 of the row's largest; the
+        # second chain has r / 8 products of two units each, and the scale and the addition 4 more
+        K = 2 * (4 * (dk / 512 + 1) + 16) + r / 2 + 24
+        slack = abs(sc) * h.abs().amax(1, keepdim=True) * Q.abs().sum(0)
+        tol = K * U * ym + 2 * U * slack + 2.0 ** -11 * y.abs() * (1 + 2 ** -10) + 2.0 ** -25
+        check(out[tt], y, tol, "dtokens" if back else "out")
+
+
 def test_adapter_single_row_gradient_keeps_22_bits(m):
     """One row: dA = scale x dh has one term, so nothing but the operands' precision shows."""
     g = gen(11)
