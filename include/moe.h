@@ -315,7 +315,8 @@ MOE_API moe_status moe_gate_backward_workspace_size(int T, int d, int E, moe_dty
  *   Otherwise no output overlaps an input (dtokens and tokens the same: MOE_ERR_INVALID_ARG).
  *   token_mask also leaves the masked tokens' rows out of dWg: what they hold has no effect.
  *   MOE_F16, E <= 256: Wg may be rounded to f16 (scaled by powers of two) for dtokens, as
- *   the expert FFN's weights are; dWg keeps 32-bit accuracy.
+ *   the expert FFN's weights are.  MOE_F16, dWg: dlogits enter the products to 2^-23 of each value
+ *   and 2^-36 of the largest of 128 rows; a token's values below 2^-14 lose bits as if they were 2^-14.
  * Shapes: those of moe_gate_topk, T <= 2^30, and for dWg / dtokens d a multiple of 8 (MOE_F16) or
  * 4, at most 2^20.
  */
@@ -369,8 +370,8 @@ MOE_API moe_status moe_adapter_workspace_size(int T, int d_in, int d_out, int r,
  *   decreasing and perm entries outside [0, T) are skipped and recorded as
  *   MOE_ERR_DEVICE_BOUNDS in the workspace's status word.
  *   workspace: moe_adapter_workspace_size bytes; contents need no initialisation.
- * MOE_F16: hidden is given out in float32, and the second product takes it with 22 bits (2^-25 of the
- * row's largest value below that), so that out is what float32 sums give, rounded once.
+ * MOE_F16: hidden is given out in float32, and the second product takes it to 2^-23 (and 2^-39
+ * of the row's largest value), so that out is what float32 sums give, rounded once.
  * Shapes: N <= 1024; r a multiple of 8, at most 128 (adapters of different ranks are padded with
  * zeros); d_in, d_out multiples of 8 (MOE_F16) or 4 (MOE_F32), at most 2^20; T, S_max <= 2^30.
  */
@@ -390,6 +391,8 @@ MOE_API moe_status moe_adapter_forward(const void* tokens, const int32_t* perm,
  *   may be dtokens itself; dA nullable (then tokens is not read), dB nullable (then hidden is
  *   not read); not all three.  base's gradient is dout itself.
  *   dtokens overlaps neither dout nor tokens (the same: MOE_ERR_INVALID_ARG).
+ *   MOE_F16: dA and dB take dh and hidden to 2^-23 of each value and 2^-39 of the largest of 64 rows;
+ *   values of tokens and dout below 2^-14 lose bits as if they were 2^-14.
  *   Everything else as moe_adapter_forward (dh in hidden's place).  MOE_F16, long runs: an infinite token or dout row makes its sums infinite or NaN.
  */
 MOE_API moe_status moe_adapter_backward(const void* dout, const void* tokens, const float* hidden,

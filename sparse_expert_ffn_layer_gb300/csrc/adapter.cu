@@ -20,7 +20,7 @@
 //
 // f16: h is kept in 32 bits (and given out so).  For the second product each row is scaled by a power
 // of two, so that no h overflows or is lost below f16's range, and split into two f16 parts: together
-// h to 2^-22 of itself, 2^-25 of the row's largest, so that y differs from the 32-bit form's by 32-bit
+// h to 2^-23 of itself, 2^-39 of the row's largest, so that y differs from the 32-bit form's by 32-bit
 // rounding before its own 2^-11 |y|.  (One part only: the error of 8192 rows of dtokens, r = 32, was
 // 1.37 times that of 32-bit sums.)  f32: fused multiply-adds on the CUDA cores.
 #include <cooperative_groups.h>
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
         ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
         mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
       }
-      const int ea = scale_exp(ma), eb = scale_exp(mb);
+      const int ea = split_exp(ma), eb = split_exp(mb);
       const float ia = exp2_int(-ea), ib = exp2_int(-eb), sc = a.scale[n];
       m0 = sc * exp2_int(ea);
       m1 = sc * exp2_int(eb);
@@ -857,7 +857,7 @@ __global__ void __launch_bounds__(128, Plan16<R>::kBlocks) adapter_f16_kernel(co
       const unsigned grp = 0xffu << (lane & 24);
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(grp, m, o));
-      const int e = scale_exp(m);
+      const int e = split_exp(m);
       const float inv = exp2_int(-e);
       struct alignas(CPT >= 8 ? 16 : 2 * CPT) Halves { __half v[CPT]; } hv, lv;
 #pragma unroll

@@ -22,7 +22,7 @@ namespace {
 //
 // f16: h is a 32-bit input of any range and the rows are the summed index, so per chunk of 64 rows
 // it is scaled by one power of two (from the chunk's largest magnitude) and split into two f16
-// parts, 22 bits together; the chunk's product is scaled back as it is added to the 32-bit running
+// parts, 2^-23 of each value and 2^-39 of the largest; the chunk's product is scaled back as it is added to the 32-bit running
 // sums (which also ends the tensor cores' chains of truncating additions every 64 rows).  A launch
 // of its own splits h, small beside x: with the split inside the loop, waiting for h and two
 // barriers per chunk took most of the time (8192 rows, 2048 + 8192 columns, r = 32: 115 us; now 6 to
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kSumThreads) split_rows_kernel(const SumArgs a
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < kSumThreads / 32; ++q) m = fmaxf(m, wmax[q]);
-    const int e = scale_exp(m);
+    const int e = split_exp(m);
     const float inv = exp2_int(-e);
     for (int q = tid; q < kRows * n4; q += kSumThreads) {
       const int s = lo + q / n4, col = (q % n4) * 4;

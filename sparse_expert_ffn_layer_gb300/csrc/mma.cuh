@@ -103,8 +103,16 @@ __device__ __forceinline__ int scale_exp(float m) {
 }
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// v = hi + lo up to 2^-25 of the set's largest magnitude (v was scaled by that set's 2^-e, so
-// |v| < 2; hi has 11 bits, lo the next 11, and lo's smallest step is 2^-24).
+// The same for values that are split into two f16 parts: 2^-e brings the largest into [2^14, 2^15), the
+// top of f16's range, so that the low part of a value far below it still has its bits (scaled to
+// [1, 2) instead, a value 2^-17 of the largest kept eight).
+__device__ __forceinline__ int split_exp(float m) {
+  const int e = (int)((__float_as_uint(m) >> 23) & 255u) - 127;
+  return m == 0.f || e == 128 ? 0 : max(-126, e - 14);
+}
+
+// v = hi + lo up to 2^-23 |v| and 2^-25 (|v| < 2^15 by split_exp's scale: 2^-39 of the set's largest; hi
+// has 11 bits, lo the next 11, and the smallest step of either is 2^-24).
 // A value whose hi is not finite keeps it and has no lo.
 __device__ __forceinline__ void split_f16(float v, __half& hi, __half& lo) {
   hi = __float2half_rn(v);

@@ -607,6 +607,59 @@ def test_adapter_hidden_rows_keep_32_bit_accuracy(m, dt, T, di, do, r, N, back):
         check(out[tt], y, tol, "dtokens" if back else "out")
 
 
+@pytest.mark.parametrize("T,N", [(300, 1), (1500, 3), (70, 1)])
+@pytest.mark.parametrize("r", [16, 40, 128])
+def test_adapter_gradients_of_small_columns(m, T, N, r):
+    """Columns of h far smaller than others (and one row far larger) keep their own bits in dA and dB."""
+    g = gen(T + r)
+    dt, di, do = torch.float16, 264, 136
+    c = adapter_inputs(m, g, dt, T, di, do, r, N, none=0.0)
+    # f16 weights and upstream rows in their normal range: dh spans 2^15, hidden 2^30
+    j = torch.arange(r, device="cuda") % 16
+    c["B"] = (c["B"].float() * 2.0 ** (8 - j.float())[None, :, None]).to(dt)
+    dout = randn(g, T, do, dtype=dt)
+    hid = randn(g, T, r) * 2.0 ** (-2.0 * j.float())
+    hid[T // 2] *= 2.0 ** 8
+    ws = adapter_ws(m, T, di, do, r, N, dt)
+    dA, dB = torch.empty((N, di, r), device="cuda"), torch.empty((N, r, do), device="cuda")
+    m.moe_adapter_backward(dout, c["x"], hid, c["perm"], c["off"], c["A"], c["B"], c["scale"], ws, dA=dA, dB=dB)
+    for n in range(N):
+        s = slice(int(c["off"][n]), int(c["off"][n + 1]))
+        t, sc = c["perm"][s].long(), float(c["scale"][n])
+        x, y, h, B = c["x"][t].double(), dout[t].double(), hid[s].double(), c["B"][n].double()
+        dh, dhm = y @ B.t(), y.abs() @ B.abs().t()
+        rows, K = len(t), 2 * (4 * (do / 512 + 1) + 16)
+        # h to 2 u, 8 truncating products per 64 rows (one more for the low part), rows / 64 + 16 additions;
+        # 2^-39 of the chunk's largest h; f16 operands below 2^-14 count as that (see test_adapter_backward)
+        KW = 66 + rows / 64
+        up = lambda v: torch.where(v == 0, v, v.abs().clamp(min=2.0 ** -14))
+        check(dA[n], sc * (x.t() @ dh), abs(sc) * ((KW + K) * U * (up(x).t() @ dhm) +
+              2.0 ** -39 * up(x).sum(0)[:, None] * dh.abs().max()) + 1e-37, "dA")
+        check(dB[n], sc * (h.t() @ y), abs(sc) * (KW * U * (h.abs().t() @ up(y)) +
+              2.0 ** -39 * up(y).sum(0)[None, :] * h.abs().max()) + 1e-37, "dB")
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.float32])
+@pytest.mark.parametrize("T,E", [(300, 300), (1100, 1000), (70, 300), (300, 64), (2100, 200), (40, 13)])
+def test_gate_gradient_of_small_columns(m, dt, T, E):
+    """Experts whose probabilities are far below the others' keep their bits in dWg, at every E."""
+    g = gen(T + E)
+    d = 264
+    x = randn(g, T, d, dtype=dt)
+    logits = randn(g, T, E) - torch.arange(E, device="cuda") % 24    # p down to 2^-33 of the largest
+    idx, dw = topk(logits, 1), randn(g, T, 1)
+    dw[T // 2] *= 2.0 ** 8
+    ws = torch.empty(m.moe_gate_backward_workspace_size(T, d, E, dt), dtype=torch.uint8, device="cuda")
+    dl, dWg = torch.empty((T, E), device="cuda"), torch.empty((d, E), device="cuda")
+    m.moe_gate_topk_backward(logits, idx, dl, dtopk_w=dw, tokens=x, dWg=dWg, workspace=ws)
+    dd, xd = dl.double(), x.double()
+    # as above; the tensor-core form of up to 256 experts: 2^-36 of the largest of 128 rows, separate sums of
+    # both parts
+    K, low = (70 + T / 64, 2.0 ** -36) if dt == torch.float16 else (T + 8, 0)
+    up = xd.abs().clamp(min=2.0 ** -14)
+    check(dWg, xd.t() @ dd, K * U * (up.t() @ dd.abs()) + low * up.sum(0)[:, None] * dd.abs().max() + 1e-37, "dWg")
+
+
 def test_adapter_single_row_gradient_keeps_22_bits(m):
     """One row: dA = scale x dh has one term, so nothing but the operands' precision shows."""
     g = gen(11)
