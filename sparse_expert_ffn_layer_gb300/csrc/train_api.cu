@@ -226,7 +226,8 @@ moe_status moe_adapter_backward(const void* dout, const void* tokens, const floa
   return guarded([&]() -> moe_status {
     moe_status st = check_adapter(T, d_in, d_out, r, N, S_max, dtype);
     if (st != MOE_OK) return st;
-    if (!dtokens && !dA && !dB) return MOE_ERR_INVALID_ARG;
+    // (the tokens' gradient of an empty batch may be a null pointer: it has no rows)
+    if (T > 0 && !dtokens && !dA && !dB) return MOE_ERR_INVALID_ARG;
     cudaStream_t s = as_stream(stream);
     if (T == 0 || S_max == 0) {
       if (dA) MOE_TRY(cudaMemsetAsync(dA, 0, (size_t)N * d_in * r * sizeof(float), s));

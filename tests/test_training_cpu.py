@@ -129,6 +129,15 @@ def test_adapter_refusals(m):
     assert bwd(T=0, dA=None, dB=None) == m.MOE_OK
 
 
+def test_empty_batch_whose_only_output_has_no_rows(m):
+    """The tokens' gradient of an empty batch is an empty tensor, whose pointer is null."""
+    assert m.lib.moe_adapter_backward(None, None, None, P, P, P, P, P, None, 1, 0, 64, 64, 8, 4, 8, None, None, None,
+                                      None, 0, S0) == m.MOE_OK
+    assert m.lib.moe_adapter_backward(P, P, P, P, P, P, P, P, None, 1, 8, 64, 64, 8, 4, 8, None, None, None,
+                                      P, 1 << 20, S0) == m.MOE_ERR_INVALID_ARG
+    assert m.lib.moe_combine_backward(None, None, None, None, 1, 0, 64, 1, 8, None, None, S0) == m.MOE_OK
+
+
 def test_outputs_that_would_overwrite_what_is_read(m):
     """The same buffer as an input that other blocks still read is refused."""
     Q, inv = ctypes.c_void_p(0x20000), m.MOE_ERR_INVALID_ARG
