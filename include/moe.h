@@ -35,7 +35,7 @@
  *   - No call throws across this boundary; all are safe to call from any host thread as
  *     long as concurrent calls use different workspaces and outputs.
  *   - T = 0 (an empty batch) is valid: the call enqueues nothing and returns MOE_OK (the
- *     training calls clear what is summed over the batch).
+ *     training calls clear what is summed over the batch, and their status word).
  *
  * Supported shapes: E <= 1024, k in {1, 2}, k <= E.  MOE_F16 (tensor-core path): d, f and
  * f_res multiples of 128.  MOE_F32 (SIMT path): d and f multiples of 4.  Every pointer
@@ -218,8 +218,9 @@ MOE_API moe_status moe_layer_forward(const void* tokens, const float* Wg, const 
 /*
  * Synchronises `stream`, then returns the device-side status word of the most recent
  * moe_expert_ffn / moe_layer_forward / moe_adapter_forward / moe_adapter_backward call, or
- * moe_gate_topk_backward call with dWg or dtokens, on this workspace (MOE_OK, MOE_ERR_TIMEOUT or MOE_ERR_DEVICE_BOUNDS), or MOE_ERR_CUDA if the
- * synchronisation or the read failed.  Each of those calls sets the word anew.
+ * moe_gate_topk_backward call with dWg or dtokens, on this workspace (MOE_OK, MOE_ERR_TIMEOUT
+ * or MOE_ERR_DEVICE_BOUNDS), or MOE_ERR_CUDA if the synchronisation or the read failed.  Each of
+ * those calls sets the word anew (of the empty ones the training calls; the others enqueue nothing).
  */
 MOE_API moe_status moe_status_read(const void* workspace, moe_stream_t stream);
 

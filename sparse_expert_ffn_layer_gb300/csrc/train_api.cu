@@ -54,6 +54,20 @@ moe_status check_adapter(int T, int d_in, int d_out, int r, int N, int S_max, mo
   return MOE_OK;
 }
 
+// An empty call launches nothing that would write the status word: it is cleared here, in a workspace
+// that is device memory (an empty call needs none).
+moe_status clear_status(void* workspace, size_t ws_bytes, cudaStream_t s) {
+  if (!workspace || ws_bytes < sizeof(int)) return MOE_OK;
+  cudaPointerAttributes at = {};
+  if (cudaPointerGetAttributes(&at, workspace) != cudaSuccess) {
+    cudaGetLastError();                           // no device, or not a pointer of this process
+    return MOE_OK;
+  }
+  if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged) return MOE_OK;
+  MOE_TRY(cudaMemsetAsync(workspace, 0, sizeof(int), s));
+  return MOE_OK;
+}
+
 // [status][dh][partial h][workspace of the sums dA and dB]
 size_t hidden_bytes(int r, size_t rows) { return align_up(rows * r * sizeof(float)); }
 size_t adapter_sums_at(int d_in, int d_out, int r, int N, int S_max, moe_dtype dtype) {
@@ -123,7 +137,7 @@ moe_status moe_gate_topk_backward(const float* logits, const int32_t* topk_idx, 
     cudaStream_t s = as_stream(stream);
     if (T == 0) {
       if (dWg) MOE_TRY(cudaMemsetAsync(dWg, 0, (size_t)d * E * sizeof(float), s));
-      return MOE_OK;
+      return deep ? clear_status(workspace, ws_bytes, s) : MOE_OK;
     }
     if (!logits || !topk_idx || !dlogits || (!dtopk_w && !dlosses)) return MOE_ERR_INVALID_ARG;
     if (dlosses && (!counts || !n_valid)) return MOE_ERR_INVALID_ARG;
@@ -200,7 +214,7 @@ moe_status moe_adapter_forward(const void* tokens, const int32_t* perm, const in
   return guarded([&]() -> moe_status {
     moe_status st = check_adapter(T, d_in, d_out, r, N, S_max, dtype);
     if (st != MOE_OK) return st;
-    if (T == 0 || S_max == 0) return MOE_OK;
+    if (T == 0 || S_max == 0) return clear_status(workspace, ws_bytes, as_stream(stream));
     if (!tokens || !perm || !offsets || !A || !B || !scale || !out) return MOE_ERR_INVALID_ARG;
     if (!aligned16(tokens) || !aligned4(perm) || !aligned4(offsets) || !aligned16(A) || !aligned16(B) ||
         !aligned4(scale) || !aligned16(base) || !aligned16(out) || !aligned16(hidden) ||
@@ -232,7 +246,7 @@ moe_status moe_adapter_backward(const void* dout, const void* tokens, const floa
     if (T == 0 || S_max == 0) {
       if (dA) MOE_TRY(cudaMemsetAsync(dA, 0, (size_t)N * d_in * r * sizeof(float), s));
       if (dB) MOE_TRY(cudaMemsetAsync(dB, 0, (size_t)N * r * d_out * sizeof(float), s));
-      return MOE_OK;
+      return clear_status(workspace, ws_bytes, s);
     }
     if (!dout || !perm || !offsets || !A || !B || !scale) return MOE_ERR_INVALID_ARG;
     if ((dA && !tokens) || (dB && !hidden) || (dtokens_in && !dtokens)) return MOE_ERR_INVALID_ARG;

@@ -1002,6 +1002,43 @@ def test_empty_batches(m):
     m.moe_combine_backward(x, x, z((0, 1), dtype=torch.int32, device="cuda"), z((0, 1), device="cuda"), x, None)
 
 
+def test_empty_calls_set_the_status_word(m):
+    """An empty call after one that found a bad index, or on a workspace that holds anything, reads OK."""
+    z = lambda *s, t=torch.float16: torch.zeros(s, dtype=t, device="cuda")
+    i32 = torch.int32
+    d, r, N, E = 16, 8, 2, 4
+    off = z(N + 1, t=i32)
+    A, B, sc = z(N, d, r), z(N, r, d), z(N, t=torch.float32)
+    for S in (0, 3):                                 # no token, or no slot
+        T = 3 - S
+        perm, x = z(S if T == 0 else 0, t=i32), z(T, d)
+        for fill in (0x5A, 6):
+            ws = torch.full((m.moe_adapter_workspace_size(8, d, d, r, N, 8, x.dtype),), fill, dtype=torch.uint8, device="cuda")
+            m.moe_adapter_forward(x, perm, off, A, B, sc, x.clone(), ws)
+            assert m.moe_status_read(ws) == m.MOE_OK
+            ws.fill_(fill)
+            m.moe_adapter_backward(x, x, z(perm.numel(), r, t=torch.float32), perm, off, A, B, sc, ws, dtokens=x.clone())
+            assert m.moe_status_read(ws) == m.MOE_OK
+    gws = torch.full((m.moe_gate_backward_workspace_size(8, d, E, torch.float16),), 0x5A, dtype=torch.uint8, device="cuda")
+    f = lambda *s: z(*s, t=torch.float32)
+    m.moe_gate_topk_backward(f(0, E), z(0, 1, t=i32), f(0, E), dtopk_w=f(0, 1), tokens=z(0, d), dWg=f(d, E), workspace=gws)
+    assert m.moe_status_read(gws) == m.MOE_OK
+    # a bad plan, then an empty one
+    ws.zero_()
+    m.moe_adapter_forward(z(4, d), z(4, t=i32) + 9, torch.tensor([0, 2, 4], dtype=i32, device="cuda"), A, B, sc, z(4, d), ws)
+    assert m.moe_status_read(ws) == m.MOE_ERR_DEVICE_BOUNDS
+    m.moe_adapter_forward(z(0, d), z(0, t=i32), off, A, B, sc, z(0, d), ws)
+    assert m.moe_status_read(ws) == m.MOE_OK
+    # captured as well
+    x0, p0 = z(0, d), z(0, t=i32)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        m.moe_adapter_forward(x0, p0, off, A, B, sc, x0, ws)
+    ws.fill_(6)
+    g.replay()
+    assert m.moe_status_read(ws) == m.MOE_OK
+
+
 # ---------------------------------------------------------------- together, streams, graphs
 def step_buffers(m, T, d, r, N, E, k):
     f16, f32, i32 = torch.float16, torch.float32, torch.int32
