@@ -400,6 +400,8 @@ def moe_combine_backward(dout, expert_out, slot_of, topk_w, dexpert_out=None, dt
     T, d = dout.shape
     k = slot_of.shape[1]
     code, el, f32 = _dtype(dout), dout.dtype, torch.float32
+    if dtopk_w is not None:
+        _required(where, expert_out=expert_out)
     rows = expert_out if expert_out is not None else dexpert_out
     S_max = rows.shape[0] if rows is not None else 0
     dev = _device_of(where, "dout slot_of expert_out topk_w dexpert_out dtopk_w",

@@ -226,6 +226,14 @@ def test_no_warp_leaves_a_loop_whose_barrier_others_wait_at():
     assert seen >= 1
 
 
+def test_combine_backward_needs_the_experts_output_for_the_gate_weights(m):
+    """Without it (and without a dexpert_out that says how many slots there are) the gradient was zero."""
+    x, idx = torch.zeros(4, 16, dtype=torch.float16), torch.zeros(4, 1, dtype=torch.int32)
+    for dy in (None, torch.zeros(4, 16, dtype=torch.float16)):
+        with pytest.raises(ValueError, match="expert_out is required"):
+            m.moe_combine_backward(x, None, idx, torch.zeros(4, 1), dy, torch.zeros(4, 1))
+
+
 def test_blocks_that_give_up_wait_for_their_copies():
     """Each kernel with bounded waits on bulk copies waits for those in flight at its end: its block's
     shared memory may be another's a moment later."""
