@@ -365,7 +365,8 @@ MOE_API moe_status moe_adapter_workspace_size(int T, int d_in, int d_out, int r,
  *   in `dtype`; scale [N] float32.  base may be out itself (the shared projection's result, in
  *   place).  Rows of out whose token has no adapter are left as they were.  Otherwise out
  *   overlaps no input (out and tokens the same: MOE_ERR_INVALID_ARG).  A token named by more
- *   than one slot gets one of their results.
+ *   than one slot (moe_dispatch names none twice) gets one of their results in each element; with
+ *   base = out no token may be (a result that is written may be read as the other's base).
  *   hidden nullable [S_max, r] float32, for the backward pass; rows >= offsets[N] are not written.
  *   Bounds: as moe_expert_ffn's: no slot >= S_max is used, and offsets outside [0, S_max] or
  *   decreasing and perm entries outside [0, T) are skipped and recorded as
@@ -392,6 +393,7 @@ MOE_API moe_status moe_adapter_forward(const void* tokens, const int32_t* perm,
  *   may be dtokens itself; dA nullable (then tokens is not read), dB nullable (then hidden is
  *   not read); not all three.  base's gradient is dout itself.
  *   dtokens overlaps neither dout nor tokens (the same: MOE_ERR_INVALID_ARG).
+ *   With dtokens_in = dtokens no token is named by more than one slot.
  *   MOE_F16: dA and dB take dh and hidden to 2^-23 of each value and 2^-39 of the largest of 64 rows;
  *   values of tokens and dout below 2^-14 lose bits as if they were 2^-14.
  *   Everything else as moe_adapter_forward (dh in hidden's place).  MOE_F16, long runs: an infinite token or dout row makes its sums infinite or NaN.
