@@ -324,7 +324,7 @@ __device__ __forceinline__ void wgrad_block(uint8_t* sm, const CUtensorMap& mX, 
 }
 
 // ---------------------------------------------------------------- dX
-// A block takes a tile of 128 tokens, keeps its split dL in shared memory (E <= 256) and walks a
+// A block takes one tile of 128 tokens, keeps its split dL in shared memory (E <= 256) and walks a
 // part of d in tiles of 128: the split Wg comes from L2 in chunks of 64 experts, dX_in by TMA
 // into the tile that the accumulator warps add to in place and that TMA writes out.  Bound by the
 // tiles' loads and stores (dX_in and dX at 5.3 TB/s where dX has the device alone).
@@ -350,18 +350,17 @@ struct DxPlan {
 template <int NKB>
 __device__ __forceinline__ void dx_block(uint8_t* sm, const CUtensorMap& mL, const CUtensorMap& mW,
                                          const CUtensorMap& mIn, const CUtensorMap& mOut, const DxArgs& a,
-                                         int block, int blocks) {
+                                         int block) {
   using PL = DxPlan<NKB>;
   constexpr int IO = PL::kIo, kDxB = PL::kDxB;
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + PL::kOffBar);
-  uint64_t *a_full = bar, *a_empty = bar + 1, *acc_full = bar + 2, *acc_empty = bar + 4, *b_full = bar + 6,
+  uint64_t *a_full = bar, *acc_full = bar + 1, *acc_empty = bar + 3, *b_full = bar + 5,
            *b_empty = b_full + kDxB, *io_full = b_empty + kDxB, *io_empty = io_full + IO, *spare = io_empty + IO;
   uint32_t* holder = reinterpret_cast<uint32_t*>(spare + 1);
   int* flag = reinterpret_cast<int*>(holder + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     mbar_init(a_full, 1);
-    mbar_init(a_empty, 1);
     for (int s = 0; s < kDxB; ++s) {
       mbar_init(&b_full[s], 1);
       mbar_init(&b_empty[s], 1);
@@ -386,155 +385,141 @@ __device__ __forceinline__ void dx_block(uint8_t* sm, const CUtensorMap& mL, con
   tc_fence_after();
   const uint32_t tmem = *holder;
   const Sync sy{flag, a.status};
-  const int nit = (a.d + 127) / 128, items = (a.T + 127) / 128 * a.parts;
+  const int nit = (a.d + 127) / 128, t = block / a.parts, p = block - t * a.parts;
+  const int i0 = (int)((long long)nit * p / a.parts), i1 = (int)((long long)nit * (p + 1) / a.parts);
   InFlight fl;
-  auto begin_of = [&](int p) { return (int)((long long)nit * p / a.parts); };
   if (warp == 0) {
-    int bs = 0, io = 0, round = 0;
-    uint32_t bp = 1, iop = 1;
-    bool ok = true;
-    for (int item = block; item < items && ok; item += blocks, ++round) {
-      const int t = item / a.parts, p = item - t * a.parts;
-      if (lane == 0) {
-        ok = sy.wait(a_empty, (round & 1) ^ 1u);
-        if (ok) {
-          mbar_expect_tx(a_full, NKB * 2 * kTile);
-          fl.note((int)(a_full - bar), round & 1);
-          for (int kb = 0; kb < NKB; ++kb) {
-            tma_load_2d(sm + kb * 2 * kTile, &mL, 64 * kb, t * 128, a_full);
-            tma_load_2d(sm + (kb * 2 + 1) * kTile, &mL, a.Ep + 64 * kb, t * 128, a_full);
-          }
-        }
-        for (int i = begin_of(p); i < begin_of(p + 1) && ok; ++i) {
-          for (int kb = 0; kb < NKB && ok; ++kb) {
-            ok = sy.wait(&b_empty[bs], bp);
-            if (!ok) break;
-            mbar_expect_tx(&b_full[bs], kTile);
-            fl.note((int)(b_full - bar) + bs, bp ^ 1u);
-            tma_load_2d(sm + PL::kOffB + bs * kTile, &mW, 64 * kb, i * 128, &b_full[bs]);
-            if (++bs == kDxB) {
-              bs = 0;
-              bp ^= 1u;
-            }
-          }
-          if (!ok) break;
-          ok = sy.wait(&io_empty[io], iop);
-          if (!ok) break;
-          if (a.with_in) {
-            uint8_t* st = sm + PL::kOffIo + io * 2 * kTile;
-            mbar_expect_tx(&io_full[io], 2 * kTile);
-            fl.note((int)(io_full - bar) + io, iop ^ 1u);
-            tma_load_2d(st, &mIn, i * 128, t * 128, &io_full[io]);
-            tma_load_2d(st + kTile, &mIn, i * 128 + 64, t * 128, &io_full[io]);
-          } else {
-            mbar_arrive(&io_full[io]);
-          }
-          if (++io == IO) {
-            io = 0;
-            iop ^= 1u;
-          }
-        }
+    if (lane == 0) {
+      mbar_expect_tx(a_full, NKB * 2 * kTile);
+      fl.note((int)(a_full - bar), 0);
+      for (int kb = 0; kb < NKB; ++kb) {
+        tma_load_2d(sm + kb * 2 * kTile, &mL, 64 * kb, t * 128, a_full);
+        tma_load_2d(sm + (kb * 2 + 1) * kTile, &mL, a.Ep + 64 * kb, t * 128, a_full);
       }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
-    }
-  } else if (warp == 1) {
-    const uint32_t idesc = idesc_f16(128, 128, 0, 0);
-    int bs = 0, tile = 0, round = 0;
-    uint32_t bp = 0;
-    bool ok = true;
-    for (int item = block; item < items && ok; item += blocks, ++round) {
-      const int p = item % a.parts;
-      if (lane == 0) {
-        ok = sy.wait(a_full, round & 1);
-        for (int i = begin_of(p); i < begin_of(p + 1) && ok; ++i, ++tile) {
-          const int buf = tile & 1;
-          ok = sy.wait(&acc_empty[buf], ((tile >> 1) & 1) ^ 1u);
-          for (int kb = 0; kb < NKB && ok; ++kb) {
-            ok = sy.wait(&b_full[bs], bp);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t sa = smem_u32(sm + kb * 2 * kTile), sb = smem_u32(sm + PL::kOffB + bs * kTile);
-            const uint64_t ah = smem_desc(sa, 16, 1024, 2), al = smem_desc(sa + kTile, 16, 1024, 2);
-            const uint64_t bh = smem_desc(sb, 16, 1024, 2);
-            const uint32_t d1 = tmem + buf * 256, d2 = d1 + 128;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t more = (kb | k) ? 1u : 0u;
-              tc_mma_f16(d1, ah + 2 * k, bh + 2 * k, idesc, more);
-              tc_mma_f16(d2, al + 2 * k, bh + 2 * k, idesc, more);
-            }
-            tc_commit(&b_empty[bs]);
-            if (++bs == kDxB) {
-              bs = 0;
-              bp ^= 1u;
-            }
+      int bs = 0, io = 0;
+      uint32_t bp = 1, iop = 1;
+      bool ok = true;
+      for (int i = i0; i < i1 && ok; ++i) {
+        for (int kb = 0; kb < NKB && ok; ++kb) {
+          ok = sy.wait(&b_empty[bs], bp);
+          if (!ok) break;
+          mbar_expect_tx(&b_full[bs], kTile);
+          fl.note((int)(b_full - bar) + bs, bp ^ 1u);
+          tma_load_2d(sm + PL::kOffB + bs * kTile, &mW, 64 * kb, i * 128, &b_full[bs]);
+          if (++bs == kDxB) {
+            bs = 0;
+            bp ^= 1u;
           }
-          if (ok) tc_commit(&acc_full[buf]);
         }
-        if (ok) tc_commit(a_empty);
-      }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
-    }
-  } else if (warp >= 4) {
-    const int q = warp & 3, ch = (warp - 4) >> 2;   // TMEM lanes 32 q .., 64-column half
-    const int row = 32 * q + lane;
-    int tile = 0, io = 0;
-    uint32_t iop = 0;
-    bool ok = true;
-    const bool storer = q == 0 && lane == 0;
-    for (int item = block; item < items; item += blocks) {
-      const int t = item / a.parts, p = item - t * a.parts;
-      const float st = a.sT[t];
-      for (int i = begin_of(p); i < begin_of(p + 1); ++i, ++tile) {
-        const int buf = tile & 1;
-        if (ok) ok = sy.wait(&acc_full[buf], (tile >> 1) & 1) && sy.wait(&io_full[io], iop);
-        ok = __all_sync(0xffffffffu, ok);
-        // The four warps of a half meet at the barrier below, and each learns by itself that a wait gave
-        // up: it then goes on to the barrier of every tile that is left, without waits, sums or stores.
-        if (ok) {
-          tc_fence_after();
-          const float s = st * a.sW[i], s2 = s / kGateLo;
-          uint8_t* box = sm + PL::kOffIo + (io * 2 + ch) * kTile + row * 128;
-          const uint32_t t0 = tmem + ((uint32_t)(32 * q) << 16) + buf * 256 + ch * 64;
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            float u[32], v[32];
-            tmem_ld32x2(t0 + 32 * b, t0 + 128 + 32 * b, u, v);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              uint4* at = reinterpret_cast<uint4*>(box + (((4 * b + w) ^ (row & 7)) << 4));
-              uint4 old = make_uint4(0u, 0u, 0u, 0u);
-              if (a.with_in) old = *at;
-              uint32_t o[4] = {old.x, old.y, old.z, old.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&o[j]));
-                const int k = 8 * w + 2 * j;
-                const __half2 r = __floats2half2_rn(fmaf(s, u[k], fmaf(s2, v[k], f.x)),
-                                                    fmaf(s, u[k + 1], fmaf(s2, v[k + 1], f.y)));
-                o[j] = *reinterpret_cast<const uint32_t*>(&r);
-              }
-              *at = make_uint4(o[0], o[1], o[2], o[3]);
-            }
-          }
-          tc_fence_before();
-          mbar_arrive(&acc_empty[buf]);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + ch) : "memory");
-        if (storer && ok) {
-          const int x = i * 128 + 64 * ch;
-          if (x < a.d) tma_store_2d(&mOut, x, t * 128, sm + PL::kOffIo + (io * 2 + ch) * kTile);
-          bulk_commit();
-          if (tile > 0) {                           // the tile before is out: its buffer is free
-            bulk_wait_read<1>();
-            mbar_arrive(&io_empty[io == 0 ? IO - 1 : io - 1]);
-          }
+        if (!ok) break;
+        ok = sy.wait(&io_empty[io], iop);
+        if (!ok) break;
+        if (a.with_in) {
+          uint8_t* st = sm + PL::kOffIo + io * 2 * kTile;
+          mbar_expect_tx(&io_full[io], 2 * kTile);
+          fl.note((int)(io_full - bar) + io, iop ^ 1u);
+          tma_load_2d(st, &mIn, i * 128, t * 128, &io_full[io]);
+          tma_load_2d(st + kTile, &mIn, i * 128 + 64, t * 128, &io_full[io]);
+        } else {
+          mbar_arrive(&io_full[io]);
         }
         if (++io == IO) {
           io = 0;
           iop ^= 1u;
         }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    const uint32_t idesc = idesc_f16(128, 128, 0, 0);
+    if (lane == 0) {
+      int bs = 0;
+      uint32_t bp = 0;
+      bool ok = sy.wait(a_full, 0);
+      for (int i = i0; i < i1 && ok; ++i) {
+        const int tile = i - i0, buf = tile & 1;
+        ok = sy.wait(&acc_empty[buf], ((tile >> 1) & 1) ^ 1u);
+        for (int kb = 0; kb < NKB && ok; ++kb) {
+          ok = sy.wait(&b_full[bs], bp);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sa = smem_u32(sm + kb * 2 * kTile), sb = smem_u32(sm + PL::kOffB + bs * kTile);
+          const uint64_t ah = smem_desc(sa, 16, 1024, 2), al = smem_desc(sa + kTile, 16, 1024, 2);
+          const uint64_t bh = smem_desc(sb, 16, 1024, 2);
+          const uint32_t d1 = tmem + buf * 256, d2 = d1 + 128;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t more = (kb | k) ? 1u : 0u;
+            tc_mma_f16(d1, ah + 2 * k, bh + 2 * k, idesc, more);
+            tc_mma_f16(d2, al + 2 * k, bh + 2 * k, idesc, more);
+          }
+          tc_commit(&b_empty[bs]);
+          if (++bs == kDxB) {
+            bs = 0;
+            bp ^= 1u;
+          }
+        }
+        if (ok) tc_commit(&acc_full[buf]);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    const int q = warp & 3, ch = (warp - 4) >> 2;   // TMEM lanes 32 q .., 64-column half
+    const int row = 32 * q + lane;
+    int io = 0;
+    uint32_t iop = 0;
+    bool ok = true;
+    const bool storer = q == 0 && lane == 0;
+    const float st = a.sT[t];
+    for (int i = i0; i < i1; ++i) {
+      const int tile = i - i0, buf = tile & 1;
+      if (ok) ok = sy.wait(&acc_full[buf], (tile >> 1) & 1) && sy.wait(&io_full[io], iop);
+      ok = __all_sync(0xffffffffu, ok);
+      // The four warps of a half meet at the barrier below, and each learns by itself that a wait gave
+      // up: it then goes on to the barrier of every tile that is left, without waits, sums or stores.
+      if (ok) {
+        tc_fence_after();
+        const float s = st * a.sW[i], s2 = s / kGateLo;
+        uint8_t* box = sm + PL::kOffIo + (io * 2 + ch) * kTile + row * 128;
+        const uint32_t t0 = tmem + ((uint32_t)(32 * q) << 16) + buf * 256 + ch * 64;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          float u[32], v[32];
+          tmem_ld32x2(t0 + 32 * b, t0 + 128 + 32 * b, u, v);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint4* at = reinterpret_cast<uint4*>(box + (((4 * b + w) ^ (row & 7)) << 4));
+            uint4 old = make_uint4(0u, 0u, 0u, 0u);
+            if (a.with_in) old = *at;
+            uint32_t o[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&o[j]));
+              const int k = 8 * w + 2 * j;
+              const __half2 r = __floats2half2_rn(fmaf(s, u[k], fmaf(s2, v[k], f.x)),
+                                                  fmaf(s, u[k + 1], fmaf(s2, v[k + 1], f.y)));
+              o[j] = *reinterpret_cast<const uint32_t*>(&r);
+            }
+            *at = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&acc_empty[buf]);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + ch) : "memory");
+      if (storer && ok) {
+        const int x = i * 128 + 64 * ch;
+        if (x < a.d) tma_store_2d(&mOut, x, t * 128, sm + PL::kOffIo + (io * 2 + ch) * kTile);
+        bulk_commit();
+        if (tile > 0) {                           // the tile before is out: its buffer is free
+          bulk_wait_read<1>();
+          mbar_arrive(&io_empty[io == 0 ? IO - 1 : io - 1]);
+        }
+      }
+      if (++io == IO) {
+        io = 0;
+        iop ^= 1u;
       }
     }
     if (storer) bulk_wait_read<0>();
@@ -555,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if ((int)blockIdx.x < w_blocks)
     wgrad_block<IW>(sm, m.X, m.L64, wa, blockIdx.x);
   else
-    dx_block<NKB>(sm, m.L, m.W, m.in, m.out, xa, (int)blockIdx.x - w_blocks, (int)gridDim.x - w_blocks);
+    dx_block<NKB>(sm, m.L, m.W, m.in, m.out, xa, (int)blockIdx.x - w_blocks);
 }
 
 int pad64(int E) { return (E + 63) / 64 * 64; }
