@@ -315,9 +315,8 @@ MOE_API moe_status moe_gate_backward_workspace_size(int T, int d, int E, moe_dty
  *   workspace: moe_gate_backward_workspace_size bytes; may be NULL when dWg and dtokens are.
  *   Otherwise no output overlaps an input (dtokens and tokens the same: MOE_ERR_INVALID_ARG).
  *   token_mask also leaves the masked tokens' rows out of dWg: what they hold has no effect.
- *   MOE_F16, E <= 256: Wg may be rounded to f16 (scaled by powers of two) for dtokens, as
- *   the expert FFN's weights are.  MOE_F16, dWg: dlogits enter the products to 2^-23 of each value
- *   and 2^-36 of the largest of 128 rows; a token's values below 2^-14 lose bits as if they were 2^-14.
+ *   MOE_F16: dlogits and Wg may enter the products to 2^-23 of each value and 2^-36 of the largest of
+ *   128 rows; in dWg a token's values below 2^-14 lose bits as if they were 2^-14.
  * Shapes: those of moe_gate_topk, T <= 2^30, and for dWg / dtokens d a multiple of 8 (MOE_F16) or
  * 4, at most 2^20.
  */

@@ -5,9 +5,8 @@
 // v = hi + 2^-11 lo, both f16 (lo keeps an exponent range of its own, so what is lost is 2^-23 |v| +
 // 2^-36 of the block's largest magnitude).  The products with hi and with lo go to separate
 // accumulators, joined as D1 + 2^-11 D2 in 32 bits.  X is f16 and exact, so dWg keeps the accuracy of
-// a 32-bit sum.  Wg is rounded to f16 once (scaled by 128 rows, so that none is lost below f16's
-// range): dX is f16, and the rounding adds at most 2^-11 of the sum of |dL Wg| to its own 2^-11.  (With
-// Wg split as well, a third product, each tile took twice the bytes from L2.)  The split comes with
+// a 32-bit sum.  Wg is split in the same way, by 128 of its rows, and D2 takes hi lo and lo hi, so that
+// dX is what 32-bit sums give, rounded once (lo lo is below 2^-22 of a product).  The splits come with
 // the logits' gradient (router_loss.cu).
 //
 // One launch computes both, a part of its blocks dWg and the rest dX, one block per SM; warp 0 loads by
@@ -400,12 +399,12 @@ __device__ __forceinline__ void dx_block(uint8_t* sm, const CUtensorMap& mL, con
       uint32_t bp = 1, iop = 1;
       bool ok = true;
       for (int i = i0; i < i1 && ok; ++i) {
-        for (int kb = 0; kb < NKB && ok; ++kb) {
+        for (int c = 0; c < 2 * NKB && ok; ++c) {   // 64 experts' high parts, then their low parts
           ok = sy.wait(&b_empty[bs], bp);
           if (!ok) break;
           mbar_expect_tx(&b_full[bs], kTile);
           fl.note((int)(b_full - bar) + bs, bp ^ 1u);
-          tma_load_2d(sm + PL::kOffB + bs * kTile, &mW, 64 * kb, i * 128, &b_full[bs]);
+          tma_load_2d(sm + PL::kOffB + bs * kTile, &mW, (c & 1 ? a.Ep : 0) + 64 * (c >> 1), i * 128, &b_full[bs]);
           if (++bs == kDxB) {
             bs = 0;
             bp ^= 1u;
@@ -439,19 +438,23 @@ __device__ __forceinline__ void dx_block(uint8_t* sm, const CUtensorMap& mL, con
       for (int i = i0; i < i1 && ok; ++i) {
         const int tile = i - i0, buf = tile & 1;
         ok = sy.wait(&acc_empty[buf], ((tile >> 1) & 1) ^ 1u);
-        for (int kb = 0; kb < NKB && ok; ++kb) {
+        for (int c = 0; c < 2 * NKB && ok; ++c) {
           ok = sy.wait(&b_full[bs], bp);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = smem_u32(sm + kb * 2 * kTile), sb = smem_u32(sm + PL::kOffB + bs * kTile);
+          const uint32_t sa = smem_u32(sm + (c >> 1) * 2 * kTile), sb = smem_u32(sm + PL::kOffB + bs * kTile);
           const uint64_t ah = smem_desc(sa, 16, 1024, 2), al = smem_desc(sa + kTile, 16, 1024, 2);
-          const uint64_t bh = smem_desc(sb, 16, 1024, 2);
+          const uint64_t bd = smem_desc(sb, 16, 1024, 2);
           const uint32_t d1 = tmem + buf * 256, d2 = d1 + 128;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint32_t more = (kb | k) ? 1u : 0u;
-            tc_mma_f16(d1, ah + 2 * k, bh + 2 * k, idesc, more);
-            tc_mma_f16(d2, al + 2 * k, bh + 2 * k, idesc, more);
+            const uint32_t more = (c | k) ? 1u : 0u;
+            if (c & 1) {
+              tc_mma_f16(d2, ah + 2 * k, bd + 2 * k, idesc, 1u);
+            } else {
+              tc_mma_f16(d1, ah + 2 * k, bd + 2 * k, idesc, more);
+              tc_mma_f16(d2, al + 2 * k, bd + 2 * k, idesc, more);
+            }
           }
           tc_commit(&b_empty[bs]);
           if (++bs == kDxB) {
@@ -548,7 +551,7 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // How a call is cut: token rows per block of dWg (a multiple of 128) and accumulators per block, and
 // column parts per token tile of dX.  What takes least time by 2.2 us per 128 rows of dWg with two
-// accumulators, 1.4 with one, 1 us and 0.3 per 64 experts for a 128 x 128 tile of dX, 3 us to start
+// accumulators, 1.4 with one, 1 us and 0.3 per 64 experts (above 128: 0.8) for a 128 x 128 tile of dX, 3 us to start
 // either, and the partial sums' way through L2 and the launch that joins them; the blocks of dX take
 // the SMs that dWg leaves and each of the others when its block ends.
 struct GatePlan {
@@ -584,7 +587,7 @@ GatePlan gate_plan(int T, int d, int E, bool wgrad, bool dx, int sms) {
         continue;
       }
       for (int p = 1; p <= std::min(nit, 16); p += p < 4 ? 1 : p < 8 ? 2 : 4) {
-        const double us = (nit + p - 1) / p * (1.0 + 0.3 * nkb) + 3.0;
+        const double us = (nit + p - 1) / p * (1.0 + (nkb <= 2 ? 0.3 : 0.8) * nkb) + 3.0;
         const long long X = (long long)tt * p;
         // n rounds of the free SMs, and what the late ones add in that time
         long long n = std::max<long long>(1, (long long)((X * us - late * us) / (sms * us)));
@@ -621,7 +624,7 @@ GateWs gate_ws(int T, int d, int E) {
   GateWs w;
   w.dl2 = 0;
   w.W2 = w.dl2 + up256((size_t)T * 2 * Ep * 2);
-  w.sT = w.W2 + up256((size_t)d * Ep * 2);
+  w.sT = w.W2 + up256((size_t)d * 2 * Ep * 2);
   w.sW = w.sT + up256((size_t)(T + 127) / 128 * 4);
   w.partial = w.sW + up256((size_t)(d + 127) / 128 * 4);
   w.total = w.partial + up256(sum_partial_bytes((size_t)d * E, T, 128));
@@ -641,16 +644,17 @@ cudaError_t launch_both(const BothMaps& m, const WgArgs& wa, const DxArgs& xa, i
 }  // namespace
 
 // The multiply-add kernels (grad.cu) need no split but take a launch per gradient.  us there / here: both
-// gradients, 1024 columns, T = 1: E = 8 7.6 / 7.2, E = 127 14.6 / 9.3; T = 256: E = 8 11.2 / 9.2, E = 127
-// 28 / 17.  dWg alone: E = 8: T = 256 8.7 / 9.2, 512 11.0 / 10.4; E = 128: T = 16 10.0 / 9.4, 128 14.8 / 12.4;
-// 3584 columns, E = 256: T = 64 14.2 / 17.1, 128 19.4 / 20.4, 256 24.4 / 21.0.  dX alone: 512 x 1024 x 128
-// 11.6 / 12.0, 256 x 3584 x 256 27.4 / 22.4; odd rows, whose split is scalar: 512 x 1024 x 127 12.0 / 15.3,
-// 256 x 3584 x 255 27.7 / 27.0 (16384 x 3584 x 128: 494 / 44).
+// gradients, 1024 columns, T = 1: E = 8 7.9 / 7.7, E = 127 15.3 / 10.6; T = 256: E = 8 12.0 / 9.4, E = 127
+// 29 / 17.  dWg alone: E = 8: T = 256 9.3 / 9.6, 512 11.5 / 10.8; E = 128: T = 16 10.5 / 9.9, 128 15.3 / 12.9;
+// 3584 columns, E = 256: T = 64 14.5 / 17.1, 128 20.4 / 20.3, 256 24.5 / 20.9.  dX alone: 512 x 1024 x 128
+// 11.9 / 12.5, 1024 x 1024 x 128 19.8 / 12.4; above 128 experts, whose ring of Wg is short: 128 x 3584 x 256
+// 19.7 / 27.1, 256 x 3584 x 256 27.6 / 26.8; odd rows, whose split is scalar: 512 x 1024 x 127 12.2 / 15.6,
+// 256 x 3584 x 255 27.8 / 31.4 (16384 x 3584 x 128: 705 / 54).
 bool gate_tc_ok(int T, int d, int E, bool wgrad, bool dx) {
   if (E > 256) return false;
   if (wgrad && dx) return true;
   if (wgrad) return T >= 128 && (long long)T * E >= 4096;
-  return dx && (double)T * d * E >= (E % 4 ? 230e6 : 100e6);
+  return dx && (double)T * d * E >= (E % 4 || E > 128 ? 240e6 : 100e6);
 }
 size_t gate_tc_bytes(int T, int d, int E) { return T > 0 ? gate_ws(T, d, E).total : 0; }
 
@@ -669,7 +673,7 @@ cudaError_t launch_gate_tc(const float* logits, const int32_t* topk_idx, const f
   MOE_LAUNCH(launch_dlogits_split(logits, topk_idx, dtopk_w, dlosses, counts, n_valid, mask, T, E, k,
                                   dlogits, status, dx ? Wg : nullptr, d, Ep, dl2, sT, W2, sW, s));
   const uint64_t l_dims[2] = {(uint64_t)2 * Ep, (uint64_t)T}, x_dims[2] = {(uint64_t)d, (uint64_t)T};
-  const uint64_t w_dims[2] = {(uint64_t)Ep, (uint64_t)d};
+  const uint64_t w_dims[2] = {(uint64_t)2 * Ep, (uint64_t)d};
   const uint32_t b64[2] = {64, 64}, b128[2] = {64, 128};
   BothMaps m;
   memset(&m, 0, sizeof(m));

@@ -227,7 +227,7 @@ cudaError_t launch_gate_tc(const float* logits, const int32_t* topk_idx, const f
                            const uint8_t* mask, int k, float* dlogits, const __half* tokens,
                            const float* Wg, float* dWg, const __half* dx_in, __half* dx, uint8_t* ws,
                            int* status, int T, int d, int E, cudaStream_t s);
-// Its first launch: the logits' gradient, also in f16 parts, and (Wg not null) Wg in f16.
+// Its first launch: the logits' gradient, also in f16 parts, and (Wg not null) Wg in f16 parts.
 cudaError_t launch_dlogits_split(const float* logits, const int32_t* topk_idx, const float* dtopk_w,
                                  const float* dlosses, const int32_t* counts, const int32_t* n_valid,
                                  const uint8_t* mask, int T, int E, int k, float* dlogits, int* status,

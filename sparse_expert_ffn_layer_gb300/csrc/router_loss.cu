@@ -452,12 +452,12 @@ __global__ void __launch_bounds__(256) dlogits_kernel(const DlArgs d) {
 // (gate_grad.cu): a block takes 128 rows, writes their gradients in 32 bits, and when it knows their
 // largest magnitude also as (hi, lo) with v = (hi + 2^-11 lo) 2^e.  16384 x 128 with a Wg of 3584 rows:
 // 12 us, 156 blocks on 152 SMs; a block's chain of loads, two block-wide steps and stores bounds it.
-// Blocks beyond the rows round Wg to f16 by 128 rows and one power of two.
+// Blocks beyond the rows split Wg in the same way.
 struct SplitOut {
   __half* dl2;                 // [T][2 Ep]: hi, lo; columns beyond E are zero
   float* sT;                   // [T / 128]
   const float* Wg;             // [d, E], or null
-  __half* W2;                  // [d][Ep]
+  __half* W2;                  // [d][2 Ep], as dl2
   float* sW;                   // [d / 128]
   int d, Ep, nT;
 };
@@ -486,11 +486,11 @@ __device__ __forceinline__ void split_four(const float (&f)[4], float inv, __hal
 #pragma unroll
   for (int v = 0; v < 4; ++v) split_one(f[v] * inv, h[v], l[v]);
   *reinterpret_cast<uint2*>(hi) = *reinterpret_cast<const uint2*>(h);
-  if (lo) *reinterpret_cast<uint2*>(lo) = *reinterpret_cast<const uint2*>(l);
+  *reinterpret_cast<uint2*>(lo) = *reinterpret_cast<const uint2*>(l);
 }
 
-// Rounds rows x E values (m: their largest magnitude) to f16 parts of `ld` columns, lo null: one
-// part only; returns the power of two.
+// Splits rows x E values (m: their largest magnitude) into f16 parts of `ld` columns; returns the power
+// of two.
 // A warp takes rows; eight loads are issued before the first result is stored (the compiler cannot
 // move loads over stores that might alias them).
 template <int VEC>
@@ -525,12 +525,12 @@ __device__ __forceinline__ float split_block(const float* src, int rows, int E, 
           if (r >= rows || c >= Ep) continue;
           __half* p = hi + (size_t)r * ld + c;
           if constexpr (VEC == 4) {
-            split_four(f[i][j], inv, p, lo ? p + (lo - hi) : nullptr);
+            split_four(f[i][j], inv, p, p + (lo - hi));
           } else {
             __half h, l;
             split_one(f[i][j][0] * inv, h, l);
             p[0] = h;
-            if (lo) p[lo - hi] = l;
+            p[lo - hi] = l;
           }
         }
     }
@@ -547,6 +547,7 @@ __global__ void __launch_bounds__(kSplitThreads) dlogits_split_kernel(const DlAr
   if ((int)blockIdx.x >= o.nT) {
     const int blk = blockIdx.x - o.nT, rows = min(kGateBlock, o.d - blk * kGateBlock);
     const float* src = o.Wg + (size_t)blk * kGateBlock * d.E;
+    __half* dst = o.W2 + (size_t)blk * kGateBlock * 2 * o.Ep;
     float m = 0.f;
     if (VEC == 4) {
 #pragma unroll 8
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(kSplitThreads) dlogits_split_kernel(const DlAr
       for (int q = tid; q < rows * d.E; q += kSplitThreads) m = fmaxf(m, magnitude(src[q]));
     }
     m = block_max(m, scratch);
-    const float s = split_block<VEC>(src, rows, d.E, o.Ep, m, o.W2 + (size_t)blk * kGateBlock * o.Ep, nullptr, o.Ep);
+    const float s = split_block<VEC>(src, rows, d.E, o.Ep, m, dst, dst + o.Ep, 2 * o.Ep);
     if (tid == 0) o.sW[blk] = s;
     return;
   }

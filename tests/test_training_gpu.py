@@ -293,6 +293,27 @@ def test_gate_backward(m, dt, T, d, E, k, form):
         check(dx, want, tol + (2.0 ** -25 if dt == torch.float16 else 1e-37), "dtokens")
 
 
+@pytest.mark.parametrize("dt,T,d,E,k", [c for c in GATE if c[0] == "f16"] + [("f16", 700, 1408, 256, 2), ("f16", 700, 1408, 255, 1)])
+@pytest.mark.parametrize("with_dWg", [False, True])
+def test_gate_dtokens_keep_32_bit_accuracy(m, dt, T, d, E, k, with_dWg):
+    """Beside the output's own rounding only what 32-bit sums lose is left, whether dWg is asked for or not."""
+    g = gen(T + 7 * d + E + 3)
+    dt = torch.float16
+    x, Wg, logits, idx, dw = gate_inputs(g, dt, T, d, E, k)
+    ws = torch.empty(m.moe_gate_backward_workspace_size(T, d, E, dt), dtype=torch.uint8, device="cuda")
+    dl, dx = torch.empty((T, E), device="cuda"), torch.empty((T, d), dtype=dt, device="cuda")
+    dWg = torch.empty((d, E), device="cuda") if with_dWg else None
+    m.moe_gate_topk_backward(logits, idx, dl, dtopk_w=dw, tokens=x, Wg=Wg, dWg=dWg, dtokens=dx, workspace=ws)
+    dd, W = dl.double(), Wg.double()
+    want, mag = dd @ W.t(), dd.abs() @ W.abs().t()
+    # two parts each: 2 u of either operand and of their low parts' product, 2^-36 of the largest of 128
+    # rows; E additions at two units each at most (f16 products: chains of 3 E / 16 and one join)
+    block = lambda v: torch.cat([c.abs().amax().expand(len(c)) for c in v.split(128)])
+    slack = 2.0 ** -36 * (block(dd)[:, None] * W.abs().sum(1) + dd.abs().sum(1, keepdim=True) * block(W))
+    tol = (2 * E + 64) * U * mag + slack + 2.0 ** -11 * want.abs() * (1 + 2 ** -10) + 2.0 ** -25
+    check(dx, want, tol, "dtokens")
+
+
 def test_gate_backward_masked_rows_and_in_place(m):
     g = gen(5)
     T, d, E, k = 200, 128, 24, 2
