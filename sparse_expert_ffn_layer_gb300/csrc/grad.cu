@@ -561,23 +561,23 @@ cudaError_t launch_join(const SumArgs& a, int sms, cudaStream_t s) {
 // r = 16: 64 rows 15.4 / 16.1, 128 rows 19.0 / 16.8, 512 rows 40 / 21; eight groups of 32 rows 13.8 / 15.2,
 // of 64 rows 18.9 / 18.3 (skewed groups make it 40 / 21); 16 groups of 3584 columns, 32 rows in all:
 // 31 / 23.
-bool sum_tc(bool f16, int S_max, int N, int columns) {
+bool sum_tc(bool f16, int S_max, int N, int columns, int sms) {
   const long long n = std::min(N, S_max);
-  return f16 && (S_max > std::max(64LL, 32 * n) || n * (columns / kIT32 + 2) > 608);
+  return f16 && (S_max > std::max(64LL, 32 * n) || n * (columns / kIT32 + 2) > 4 * sms);
 }
 
 // Rows per segment: the segments of S_max rows (and half a segment more per group) times the
-// column blocks take the fewest rounds of two blocks on each of 152 SMs, plus what a segment
+// column blocks take the fewest rounds of two blocks on each SM, plus what a segment
 // costs in partial sums and the launch that joins them.  chunk: us of 64 rows (fused multiply-adds:
 // up to six times the tensor cores'; counted as theirs, 651 x 848 rows by 67 columns took 60 us in one
 // segment).
-int sum_segment(int S_max, int N, int blocks, size_t words, double chunk) {
+int sum_segment(int S_max, int N, int blocks, size_t words, double chunk, int sms) {
   int best = 64;
   double cost = 1e300;
   for (int p = 1; p <= sum_parts(words); ++p) {
     const int seg = std::max(64, (int)(((long long)S_max + p - 1) / p + 63) / 64 * 64);
     const double items = blocks * ((double)S_max / seg + 0.5 * std::min(N, S_max));
-    const double c = ceil(items / 304) * (seg / 64 * chunk + 2) + 0.7 * p + (seg < S_max ? 6 : 0);
+    const double c = ceil(items / (2 * sms)) * (seg / 64 * chunk + 2) + 0.7 * p + (seg < S_max ? 6 : 0);
     if (c < cost) {
       cost = c;
       best = seg;
@@ -829,7 +829,7 @@ cudaError_t launch_row_sums(const void* x0, const float* h0, float* G0, int di0,
                             int N, bool pdl, cudaStream_t s) {
   const int sms = sms_of_device();
   if (sms < 1) return cudaErrorInvalidDevice;
-  const bool tc = sum_tc(dtype_f16, S_max, N, (G0 ? di0 : 0) + (G1 ? di1 : 0));
+  const bool tc = sum_tc(dtype_f16, S_max, N, (G0 ? di0 : 0) + (G1 ? di1 : 0), sms);
   SumArgs a;
   memset(&a, 0, sizeof(a));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -851,7 +851,7 @@ cudaError_t launch_row_sums(const void* x0, const float* h0, float* G0, int di0,
   const int dj = std::max(G0 ? dj0 : 0, G1 ? dj1 : 0);
   const int blocks = (G0 ? sum_blocks(di0, dj0, dj, tc) : 0) + (G1 ? sum_blocks(di1, dj1, dj, tc) : 0);
   a.seg = sum_segment(S_max, N, blocks, (G0 ? (size_t)di0 * dj0 : 0) + (G1 ? (size_t)di1 * dj1 : 0),
-                      tc ? 1.0 : std::max(1.0, std::min(dj, 128) * (6.0 / 128)));
+                      tc ? 1.0 : std::max(1.0, std::min(dj, 128) * (6.0 / 128)), sms);
   a.job[0].partial = a.job[1].partial = reinterpret_cast<float*>(ws);
   if (G0) a.job[1].partial += 2 * (size_t)((S_max + a.seg - 1) / a.seg) * di0 * dj0;
   a.scale = scale;
