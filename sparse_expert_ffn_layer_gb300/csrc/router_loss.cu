@@ -679,11 +679,12 @@ int row_blocks(int T, int E, int sms) {
 }
 
 // Up to this many passes of eight blocks over the rows one cluster does the whole call (one block where
-// a pass covers the batch, else up to eight): a pass takes it about 1 us, the second launch of the other
-// form 4 us of the host's time.  us on the GPU, two launches / one: E = 64, 1024 rows (one pass) 6.1 / 5.4,
-// two passes 6.2 / 6.5, four 6.5 / 8.5, eight 6.9 / 12.4; wall clock with the gradient's call after it,
-// E = 60, 4099 rows (five passes): 20.3 / 18.0.
-constexpr int kOnePasses = 5;
+// a pass covers the batch, else up to eight).  us on the GPU with the gradient's call after it, two launches /
+// one: E = 128, 900 rows (two passes) 10.0 / 10.4, E = 16, 8000 rows (two) 10.9 / 11.5, E = 64, 2000 rows
+// (two) 10.1 / 10.1, 3000 rows (three) 10.2 / 11.2, E = 60, 4099 rows (five) 10.7 / 13.8.  The second launch is
+// 2.3 us of the host's time, which a captured step or a stream with work ahead does not see: so one cluster
+// where the GPU takes as long either way.
+constexpr int kOnePasses = 2;
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kernel)(KArgs...), int grid, int block, size_t smem,
