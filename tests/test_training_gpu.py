@@ -399,6 +399,54 @@ def test_gate_backward_infinities_stay_where_they_are(m, T):
     check(out[1][1][:, clean], (want + add)[:, clean], tol[:, clean], "dWg")
 
 
+@pytest.mark.parametrize("T,cut,d,E,k", [(500, 130, 136, 24, 2), (3000, 2999, 264, 128, 1), (900, 450, 64, 300, 2)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_one_batch_over_two_callers(m, T, cut, d, E, k, masked):
+    """Each caller has a part of the batch's tokens: with counts and n_valid summed over both first, the
+    gradients of their rows are the whole batch's, and their dWg add up to its."""
+    g = gen(T + E)
+    x, Wg, logits, idx, dw = gate_inputs(g, torch.float16, T, d, E, k)
+    mask = (torch.rand(T, generator=g, device="cuda") < 0.7) if masked else None
+    dloss = torch.tensor([0.7, -0.3], device="cuda")
+    parts = [slice(0, cut), slice(cut, T)]
+    cutm = lambda s: None if mask is None else mask[s].clone()
+    # (a slice need not start on 16 bytes: a caller has tensors of its own)
+    own = [run_balance(m, logits[s].clone(), idx[s].clone(), cutm(s)) for s in parts]
+    counts, nv = own[0][0] + own[1][0], own[0][3] + own[1][3]
+    whole = run_balance(m, logits, idx, mask)
+    assert torch.equal(counts, whole[0]) and torch.equal(nv, whole[3])
+    # the losses from the parts' means: prob_mean and z weighted by their tokens
+    w = [o[3].double() / max(int(nv), 1) for o in own]
+    P = w[0] * own[0][1] + w[1] * own[1][1]
+    check(P, whole[1].double(), 128 * U * P + 1e-37, "prob_mean")
+    bal = E * (counts.double() / (max(int(nv), 1) * k) * P).sum()
+    check(whole[2], torch.stack([bal, (w[0] * own[0][2][1] + w[1] * own[1][2][1])[0]]), 256 * U * whole[2].double().abs(), "losses")
+
+    def back(s, mk):
+        n = logits[s].shape[0]
+        ws = torch.empty(m.moe_gate_backward_workspace_size(n, d, E, x.dtype), dtype=torch.uint8, device="cuda")
+        dl, dWg = torch.full((n, E), 5.0, device="cuda"), torch.full((d, E), 5.0, device="cuda")
+        m.moe_gate_topk_backward(logits[s].clone(), idx[s].clone(), dl, dtopk_w=dw[s].clone(), dlosses=dloss, counts=counts,
+                                 n_valid=nv, token_mask=mk, tokens=x[s].clone(), dWg=dWg, workspace=ws)
+        return dl, dWg
+    a, b = (back(s, cutm(s)) for s in parts)
+    dl, dWg = back(slice(0, T), mask)
+    clean = logits if mask is None else torch.where(mask[:, None], logits, torch.zeros_like(logits))
+    want = ref_dlogits(clean, idx, mask, counts, int(nv), dloss, dw)
+    got = torch.cat([a[0], b[0]])
+    # as in test_balance_and_its_gradient
+    c = 0.7 * E * counts.double() / (max(int(nv), 1) ** 2 * k)
+    p = torch.softmax(clean.double(), 1)
+    lse = torch.logsumexp(clean.double(), 1, keepdim=True)
+    mag = p * (c + (c * p).sum(1, keepdim=True) + 0.6 / max(int(nv), 1) * lse.abs() + dw.abs().double().sum(1, keepdim=True))
+    mag.scatter_add_(1, idx.long(), dw.abs().double().sum(1, keepdim=True).expand(T, k).contiguous())
+    check(got, want, 64 * U * mag + 1e-37, "dlogits of the parts")
+    check(dl, want, 64 * U * mag + 1e-37, "dlogits of the batch")
+    xd, dd = x.double(), got.double()
+    both = (64 + T / 64 + 2) * U * (xd.abs().clamp(min=2.0 ** -14).t() @ dd.abs()) + 2.0 ** -36 * xd.abs().sum(0)[:, None] * dd.abs().max()
+    check(a[1].double() + b[1].double(), xd.t() @ dd, both + 1e-37, "dWg of the parts")
+
+
 # ---------------------------------------------------------------- combine
 @pytest.mark.parametrize("dt", [torch.float16, torch.float32])
 @pytest.mark.parametrize("T,d,k", [(1, 8, 1), (3, 7, 2), (64, 128, 2), (129, 1001, 1), (1000, 264, 2),
