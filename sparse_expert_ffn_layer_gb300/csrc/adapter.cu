@@ -1258,12 +1258,14 @@ __global__ void __launch_bounds__(1024) adapter_check_kernel(const AdapterArgs a
 }  // namespace
 
 // Two launches with tiles of 64 rows, where tiles of 16 would take the resident clusters more than
-// one round (estimated, with half a tile per adapter lost) and an adapter has more than 16 rows on
-// average: fewer leave a tile of 64 mostly empty.  One adapter, 3584 columns, us short / long: r = 64,
-// 48 tiles of 16 rows 17 / 20, 52 tiles 24 / 20; r = 16, 72 tiles 13.1 / 12.8, 80 tiles 17 / 13; r = 128,
-// 36 tiles 22 / 32, 80 tiles 50 / 36.  64 adapters with r = 64: 16 rows each 24 / 30, 24 each 45 / 31.
+// one round (estimated, with half a tile per adapter lost; above rank 64, where long runs have one block per
+// SM, two) and an adapter has more than 16 rows on average: fewer leave a tile of 64 mostly empty.  One
+// adapter, 3584 columns, us short / long: r = 16, 72 tiles of 16 rows 13.4 / 13.8, 80 tiles 17.7 / 14.6;
+// r = 32, 48 tiles 13.2 / 15.5, 52 tiles 18.2 / 15.6; r = 64, 48 tiles 17.2 / 19.5, 52 tiles 24.3 / 19.4;
+// r = 128, 36 tiles 20 / 34, 72 tiles 37 / 38, 80 tiles 48 / 40.  64 adapters with r = 64: 16 rows each
+// 30 / 34, 24 each 41 / 35.
 bool adapter_tall(int S_max, int N, int r, bool f16) {
-  const int n = std::min(N, S_max), round = r <= 16 ? 72 : r <= 64 ? 48 : 36;
+  const int n = std::min(N, S_max), round = r > 16 && r <= 64 ? 48 : 72;
   return f16 && S_max > 16LL * n && S_max / 16 + n / 2 > round;
 }
 
