@@ -264,7 +264,12 @@ MOE_API unsigned long long moe_kernel_launches(void);
  * low-rank adapters of many requests beside the layer (or any projection of its tokens).
  * An empty batch (T = 0) is valid for each: outputs with a row per token or slot have none, and
  * what is summed over the batch (counts, losses, dWg, dA, dB) is written as zeros.
- * Deterministic: equal calls give equal bits.  All sums are in float32 or wider.
+ * Deterministic: equal calls give equal bits.  All sums are in float32 or wider; the softmax takes the
+ * hardware's exponential, good to 2 + 1.2 |x - max| units of the last place.
+ * They go with the staged calls (moe_gate_topk, moe_dispatch, moe_expert_ffn, moe_combine), whose
+ * logits, gate weights and expert outputs they read; moe_layer_forward hands none of these out.  The
+ * gradient of the expert FFN (dexpert_out to its tokens) and of the residual MLP is the caller's: what
+ * these calls write to dtokens are the gate's and the adapters' addends of the tokens' gradient.
  */
 
 /* Bytes of workspace of moe_balance_loss.  Host only; writes *bytes. */
@@ -319,6 +324,8 @@ MOE_API moe_status moe_gate_backward_workspace_size(int T, int d, int E, moe_dty
  *   128 rows; in dWg a token's values below 2^-14 lose bits as if they were 2^-14.
  * Shapes: those of moe_gate_topk, T <= 2^30, and for dWg / dtokens d a multiple of 8 (MOE_F16) or
  * 4, at most 2^20.
+ * Speed: MOE_F16 with E <= 256 runs on the 5th-generation tensor cores; MOE_F32, and dtokens of more
+ * experts, take multiply-adds (T = 4096, d = 1024, both gradients: E = 256 40 us, E = 257 186 us).
  */
 MOE_API moe_status moe_gate_topk_backward(const float* logits, const int32_t* topk_idx,
                                           const float* dtopk_w, const float* dlosses,
@@ -375,6 +382,8 @@ MOE_API moe_status moe_adapter_workspace_size(int T, int d_in, int d_out, int r,
  * of the row's largest value), so that out is what float32 sums give, rounded once.
  * Shapes: N <= 1024; r a multiple of 8, at most 128 (adapters of different ranks are padded with
  * zeros); d_in, d_out multiples of 8 (MOE_F16) or 4 (MOE_F32), at most 2^20; T, S_max <= 2^30.
+ * Speed: long runs cost the same from r = 72 to 128, and 1.8 times r = 64 (16384 rows of 3584 columns:
+ * 170 us and 96 us); MOE_F32 takes multiply-adds in tiles of 16 rows.
  */
 MOE_API moe_status moe_adapter_forward(const void* tokens, const int32_t* perm,
                                        const int32_t* offsets, const void* A, const void* B,
@@ -395,7 +404,8 @@ MOE_API moe_status moe_adapter_forward(const void* tokens, const int32_t* perm,
  *   With dtokens_in = dtokens no token is named by more than one slot.
  *   MOE_F16: dA and dB take dh and hidden to 2^-23 of each value and 2^-39 of the largest of 64 rows;
  *   values of tokens and dout below 2^-14 lose bits as if they were 2^-14.
- *   Everything else as moe_adapter_forward (dh in hidden's place).  MOE_F16, long runs: an infinite token or dout row makes its sums infinite or NaN.
+ *   Everything else as moe_adapter_forward (dh in hidden's place).  MOE_F16, long runs: an infinite
+ *   token or dout row makes its sums infinite or NaN.
  */
 MOE_API moe_status moe_adapter_backward(const void* dout, const void* tokens, const float* hidden,
                                         const int32_t* perm, const int32_t* offsets, const void* A,

@@ -4,9 +4,10 @@
 //   h_s = x_t P_n           [r]      (forward: P = A, Q = B;  gradient: P = B^T, Q = A^T)
 //   y_t = base_t + scale_n h_s Q_n   (base may be absent)
 //
-// Bound by DRAM: x and base are read and y written once, the weights of the adapters in use come
-// once from DRAM and then from L2; 4 r operations per token and column pair stay below the
-// tensor rate for r <= 128.
+// x and base are read and y written once, the weights of the adapters in use come once from DRAM
+// and then from L2; 4 r operations per token and column pair stay below the tensor rate for
+// r <= 128.  Those bytes are the floor; short runs are bound by their chain of latencies and long
+// runs by fragment loads and products (see either).
 //
 // Short runs (a few rows per adapter: decode) and 32-bit inputs take one launch for both
 // products.  A cluster of eight blocks takes a tile of 16 rows of one adapter;
@@ -83,8 +84,9 @@ struct AdapterArgs {
 
 // ---------------------------------------------------------------- f16, long runs
 // Two launches of persistent blocks, h between them in 32 bits (small: r of d columns); 16384 rows of
-// 3584 columns, r = 64, 8 adapters: 36 + 51 us (DRAM floor 53), bound by the shared-memory pipe's
-// fragment loads and by latency at 16 warps per SM:
+// 3584 columns, r = 64, 8 adapters: 36 + 60 us (DRAM floor 53; 36 + 51 with h in one f16 part), bound by
+// fragment loads, by the products' latency at 16 warps per SM and, in the second launch, by the tensor pipe
+// where the warps' products coincide (DRAM 40%, shared-memory pipe 50 to 56%, tensor 40 to 47%):
 //   shrink  partial h[part] = x P over a part of the input columns, per tile of 64 rows
 //   expand  h = sum of the parts in order, then y = base + scale h Q per tile and part of the
 //           output columns
@@ -459,7 +461,7 @@ __global__ void __launch_bounds__(kTallThreads, R >= 128 ? 1 : 2)
   const int l15 = lane & 15, lh = lane >> 4, l3 = (lane >> 3) & 1, l7 = lane & 7;
   // Rows that this thread writes: two of the 16 that its warp and the one beside it computed, one
   // 16-byte piece each, so that eight lanes write a whole 128-byte line (four lanes on 64 bytes:
-  // 58 us for 16384 x 3584 at r = 64; eight rows at once: 73).
+  // 58 us for 16384 x 3584 at r = 64 where this took 51; eight rows at once: 73).
   const int yrow = wr + wc * 8 + (lane >> 3), ypc = l7;
   for (int item = blockIdx.x; item < ring.items; item += ring.blocks) {
     const int tile = item / ring.parts, part = item - tile * ring.parts;

@@ -11,9 +11,9 @@
 //
 // One launch computes both, a part of its blocks dWg and the rest dX, one block per SM; warp 0 loads by
 // TMA, warp 1 issues the products, eight warps read the accumulators.  Every wait is bounded (common.cuh).
-// 16384 x 3584 tokens, 128 experts: 64 us after the split's 12 and before the join's 5 (as two launches
-// 32 + 44, each with SMs idle at its end: dWg waits at the hand-over of its accumulators and leaves DRAM
-// half free, dX streams dX_in and dX); 4096 x 1024: 25.9 us in all, 30 with two.
+// 16384 x 3584 tokens, 128 experts: 71 us after the split's 12 and before the join's 5.  (Before Wg had a low
+// part 64, and as two launches 32 + 44, each with SMs idle at its end: dWg waits at the hand-over of its
+// accumulators and leaves DRAM half free, dX streams dX_in and dX.)  4096 x 1024: 24.2 us in all.
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
@@ -117,8 +117,8 @@ __device__ __forceinline__ void end_block(const Sync& sy, const InFlight& fl, ui
 // X; with one the copies from L2 bound it); while the second is emptied the first fills again.
 // IW = 1, for batches with too few blocks: two accumulators alternate.
 // Rows of masked tokens may hold anything (0 x NaN is NaN): warps 2 and 3 clear them in each chunk of X
-// before the products read it (16384 x 3584 x 128, 30% masked: both gradients 85 us, 84 without a mask;
-// by the row sums of grad.cu, which copy row by row, 187).
+// before the products read it (16384 x 3584 x 128, 30% masked, before Wg had a low part: both gradients 85 us,
+// 84 without a mask; by the row sums of grad.cu, which copy row by row, 187).
 struct WgArgs {
   const float* sT;
   const uint8_t* mask;         // rows that count, or null (all)
@@ -324,7 +324,7 @@ __device__ __forceinline__ void wgrad_block(uint8_t* sm, const CUtensorMap& mX, 
 
 // ---------------------------------------------------------------- dX
 // A block takes one tile of 128 tokens, keeps its split dL in shared memory (E <= 256) and walks a
-// part of d in tiles of 128: the split Wg comes from L2 in chunks of 64 experts, dX_in by TMA
+// part of d in tiles of 128: the split Wg comes from L2 in chunks of 64 experts, high parts and low, dX_in by TMA
 // into the tile that the accumulator warps add to in place and that TMA writes out.  Bound by the
 // tiles' loads and stores (dX_in and dX at 5.3 TB/s where dX has the device alone).
 struct DxArgs {

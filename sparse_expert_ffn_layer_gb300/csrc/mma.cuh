@@ -2,9 +2,10 @@
 // 16 x 8 x 16 f16 product, and the split of a 32-bit value into two f16 parts.
 //
 // The low-rank products have 2 r operations per element that they stream (r <= 128), far below
-// what the tensor cores can do per byte of DRAM: they are bound by their loads, and a product
-// issued by the warp that loaded the operands needs no tensor memory and no hand-over to an
-// issuing thread.
+// what the tensor cores can do per byte of DRAM.  A product issued by the warp that loaded the operands
+// needs no tensor memory and no hand-over to an issuing thread, which short runs, chains of
+// latencies, gain by.  Long runs pay for it: their operands pass through registers, and the fragment loads
+// (half of the shared-memory pipe) and the products' latencies hold them rather than DRAM (adapter.cu).
 #pragma once
 
 #include "common.cuh"

@@ -451,7 +451,8 @@ __global__ void __launch_bounds__(256) dlogits_kernel(const DlArgs d) {
 // The same with the f16 parts that the tensor-core form of the gate's gradient multiplies
 // (gate_grad.cu): a block takes 128 rows, writes their gradients in 32 bits, and when it knows their
 // largest magnitude also as (hi, lo) with v = (hi + 2^-11 lo) 2^e.  16384 x 128 with a Wg of 3584 rows:
-// 12 us, 156 blocks on 152 SMs; a block's chain of loads, two block-wide steps and stores bounds it.
+// 12 us: a block's chain of loads, two block-wide steps and stores, and one block per SM (512 threads of 73
+// registers), so that the last four of the 156 blocks run behind the others.
 // Blocks beyond the rows split Wg in the same way.
 struct SplitOut {
   __half* dl2;                 // [T][2 Ep]: hi, lo; columns beyond E are zero
