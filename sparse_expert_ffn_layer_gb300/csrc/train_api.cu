@@ -137,7 +137,7 @@ moe_status moe_gate_topk_backward(const float* logits, const int32_t* topk_idx, 
     cudaStream_t s = as_stream(stream);
     if (T == 0) {
       if (dWg) MOE_TRY(cudaMemsetAsync(dWg, 0, (size_t)d * E * sizeof(float), s));
-      return deep ? clear_status(workspace, ws_bytes, s) : MOE_OK;
+      return clear_status(workspace, ws_bytes, s);   // (dtokens without rows may be a null pointer)
     }
     if (!logits || !topk_idx || !dlogits || (!dtopk_w && !dlosses)) return MOE_ERR_INVALID_ARG;
     if (dlosses && (!counts || !n_valid)) return MOE_ERR_INVALID_ARG;

@@ -1108,6 +1108,14 @@ def test_empty_calls_set_the_status_word(m):
     assert m.moe_status_read(ws) == m.MOE_OK
 
 
+def test_empty_gate_call_for_the_tokens_alone_sets_the_status_word(m):
+    f = lambda *s, t=torch.float32: torch.zeros(s, dtype=t, device="cuda")
+    x = f(0, 16, t=torch.float16)
+    ws = torch.full((m.moe_gate_backward_workspace_size(8, 16, 4, x.dtype),), 6, dtype=torch.uint8, device="cuda")
+    m.moe_gate_topk_backward(f(0, 4), f(0, 1, t=torch.int32), f(0, 4), dtopk_w=f(0, 1), Wg=f(16, 4), dtokens=x, workspace=ws)
+    assert m.moe_status_read(ws) == m.MOE_OK
+
+
 # ---------------------------------------------------------------- together, streams, graphs
 def step_buffers(m, T, d, r, N, E, k):
     f16, f32, i32 = torch.float16, torch.float32, torch.int32
