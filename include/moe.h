@@ -379,7 +379,8 @@ MOE_API moe_status moe_adapter_workspace_size(int T, int d_in, int d_out, int r,
  *   MOE_ERR_DEVICE_BOUNDS in the workspace's status word.
  *   workspace: moe_adapter_workspace_size bytes; contents need no initialisation.
  * MOE_F16: hidden is given out in float32, and the second product takes it to 2^-23 (and 2^-39
- * of the row's largest value), so that out is what float32 sums give, rounded once.
+ * of the row's largest value), so that out is what float32 sums give, rounded once.  (An infinite
+ * weight makes what it enters infinite or NaN.)
  * Shapes: N <= 1024; r a multiple of 8, at most 128 (adapters of different ranks are padded with
  * zeros); d_in, d_out multiples of 8 (MOE_F16) or 4 (MOE_F32), at most 2^20; T, S_max <= 2^30.
  * Speed: long runs cost the same from r = 72 to 128, and 1.8 times r = 64 (16384 rows of 3584 columns:
