@@ -918,11 +918,12 @@ def behind(m, size, extra=16 << 20):
 @pytest.mark.parametrize("r", [8, 24, 64, 128])
 @pytest.mark.parametrize("off", [[19000, 20000], [18200, 18900, 18900, 20000], [19500, 19700, 100, 20000],
                                  [12000, 12500, 13000]])
-def test_adapter_long_plan_that_starts_late(m, off, r):
+@pytest.mark.parametrize("di,do", [(2048, 1032), (72, 136)])     # several column parts, one
+def test_adapter_long_plan_that_starts_late(m, off, di, do, r):
     """Slots before offsets[0] belong to no adapter (a slice of a larger plan): nothing is read from or
     written for them, nor behind the workspace, and the rows are those of the plan without the gap."""
     g = gen(41 + r)
-    S, T, di, do, N = 20000, 1900, 2048, 1032, len(off) - 1
+    S, T, N = 20000, 1900, len(off) - 1
     dt, i32 = torch.float16, dict(dtype=torch.int32, device="cuda")
     bound = [max(off[:n + 1]) for n in range(N + 1)]
     rows = bound[N] - bound[0]
@@ -949,6 +950,13 @@ def test_adapter_long_plan_that_starts_late(m, off, r):
         m.moe_adapter_backward(base, x, hid, p, o, A, B, scale, ws, dtokens=dx, dtokens_in=x, dA=dA, dB=dB)
         assert m.moe_status_read(ws) == want_status
         assert (guard == 0x5A).all()
+        # without hidden rows, and without their gradient
+        bare, ws = e(T, do, t=dt), behind(m, size)[0]
+        m.moe_adapter_forward(x, p, o, A, B, scale, bare, ws, base=base)
+        assert torch.equal(bare, out)
+        dx2 = e(T, di, t=dt)
+        m.moe_adapter_backward(base, None, None, p, o, A, B, scale, ws, dtokens=dx2, dtokens_in=x)
+        assert torch.equal(dx2, dx)
         first = bound[0] if p is perm else 0
         assert (hid[:first] == 3.0).all() and (hid[first + rows:] == 3.0).all()
         got.append((out, hid[first:first + rows], dx, dA, dB))
