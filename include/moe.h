@@ -37,7 +37,8 @@
  *   - T = 0 (an empty batch) is valid: the call enqueues nothing and returns MOE_OK (the
  *     training calls clear what is summed over the batch, and their status word).
  *
- * Supported shapes: E <= 1024, k in {1, 2}, k <= E.  MOE_F16 (tensor-core path): d, f and
+ * Supported shapes: E <= 1024, k in {1, 2} (moe_dispatch, moe_dispatch_sharded, moe_route and
+ * moe_block_norm: up to 16), k <= E.  MOE_F16 (tensor-core path): d, f and
  * f_res multiples of 128.  MOE_F32 (SIMT path): d and f multiples of 4.  Every pointer
  * 16-byte aligned.  Otherwise MOE_ERR_UNSUPPORTED.
  */
@@ -120,7 +121,7 @@ MOE_API moe_status moe_gate_topk(const void* tokens, moe_dtype dtype, const floa
 
 /*
  * Capacity-limited dispatch (reading: token-major order, capacity ceil(cf T / E)).
- *   topk_idx   [T, k] int32 experts; an index outside [0, E) is not counted and its
+ *   topk_idx   [T, k] int32 experts, k <= 16; an index outside [0, E) is not counted and its
  *              assignment is dropped (slot_of = -1).
  *   counts_raw [E]    assignments per expert before the capacity cut.
  *   kept       [E]    min(counts_raw, C).
@@ -217,8 +218,8 @@ MOE_API moe_status moe_layer_forward(const void* tokens, const float* Wg, const 
 
 /*
  * Synchronises `stream`, then returns the device-side status word of the most recent
- * moe_expert_ffn / moe_layer_forward / moe_adapter_forward / moe_adapter_backward call, or
- * moe_gate_topk_backward call with dWg or dtokens, on this workspace (MOE_OK, MOE_ERR_TIMEOUT
+ * moe_expert_ffn / moe_expert_ffn_fp8 / moe_layer_forward / moe_adapter_forward / moe_adapter_backward call, or
+ * moe_gate_topk_backward / moe_route_backward call with dWg or dtokens, on this workspace (MOE_OK, MOE_ERR_TIMEOUT
  * or MOE_ERR_DEVICE_BOUNDS), or MOE_ERR_CUDA if the synchronisation or the read failed.  Each of
  * those calls sets the word anew (of the empty ones the training calls; the others enqueue nothing).
  */
@@ -414,6 +415,148 @@ MOE_API moe_status moe_adapter_backward(const void* dout, const void* tokens, co
                                         moe_dtype dtype, int T, int d_in, int d_out, int r, int N,
                                         int S_max, void* dtokens, float* dA, float* dB,
                                         void* workspace, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * ---- A block of routed experts: routing by scores, experts in 8 bits, the norms around the block ----
+ *
+ * The pages have no counterpart of the calls from here to moe_block_norm_backward.  In the order of a layer:
+ *   moe_block_norm (the norm before the block), moe_route, moe_dispatch (k <= 16), moe_expert_ffn_fp8 or
+ *   moe_expert_ffn, moe_block_norm (the sum over a token's experts, the block's end and the next norm),
+ * and moe_block_norm_backward and moe_route_backward for training the router, norms and gates.  An empty batch
+ * (T = 0) is valid for each: outputs with a row per token have none, sums over the batch are written as zeros.
+ * Deterministic: equal calls give equal bits.  All sums are in float32 or wider.
+ */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+/*
+ * Routing by scores.  For every token t:
+ *   s[e] = softmax(logits[t, :])[e]  or  1 / (1 + exp(-logits[t, e])),      c[e] = s[e] + bias[e],
+ *   the experts form n_groups groups of E / n_groups neighbours; the top_groups groups with the largest sum of
+ *   their group_top (1 or 2) largest c remain (n_groups = 1: all experts),
+ *   topk_idx[t, :] = the k experts of largest c among them, in descending order,
+ *   topk_w[t, j]   = scale s[e_j], divided by sum_j s[e_j] when renormalize is not 0.
+ * Ties go to the lower index.  Order and ties are those of the scores as 64-bit numbers, not of their
+ * rounded 32-bit values (without a bias they are ordered by their logits).
+ *   tokens, Wg, logits_in, logits_out, dtype, d: as moe_gate_topk's.
+ *   bias       nullable [E] float32, added for the choice only (raised for experts that get too few tokens).
+ *   token_mask nullable [T] bytes: a token with 0 gets topk_idx = -1, which moe_dispatch drops, and zero
+ *              weights; what its row holds has no effect.
+ *   scores_out nullable [T, E] float32: s (rows of masked tokens: 0).
+ * Scores of logits of -infinity are zero; chosen experts whose scores sum to zero get zero weights.  Logits of
+ * NaN or +infinity give unspecified experts (in [0, E)) and weights.
+ * Shapes: k <= 16, k <= top_groups E / n_groups, n_groups <= 32 and a divisor of E; otherwise as moe_gate_topk.
+ */
+MOE_API moe_status moe_route(const void* tokens, moe_dtype dtype, const float* Wg, const float* logits_in,
+                             const float* bias, const uint8_t* token_mask, int T, int d, int E, int k,
+                             moe_score score, int n_groups, int top_groups, int group_top, int renormalize,
+                             float scale, float* logits_out, float* scores_out, int32_t* topk_idx,
+                             float* topk_w, moe_stream_t stream);
+
+/*
+ * Gradient of moe_route's weights and scores (topk_idx held constant; the bias has none):
+ *   dlogits [T, E] = d/dlogits ( sum dtopk_w . topk_w + sum dscores . scores ),
+ *   dWg [d, E]     = tokens^T dlogits                               (float32),
+ *   dtokens [T, d] = dtokens_in + dlogits Wg^T                      (`dtype`, rounded once).
+ *   logits, topk_idx as given to / written by moe_route, score, renormalize and scale as there; indices
+ *   outside [0, E) carry no gradient and leave the sum that renormalises the others.
+ *   dtopk_w nullable [T, k], dscores nullable [T, E] (of a loss of the caller's over scores_out): not both NULL.
+ *   token_mask nullable [T]: rows of tokens with 0 are zero (dtokens: dtokens_in).
+ *   Everything else, the workspace (moe_gate_backward_workspace_size) among it, as moe_gate_topk_backward.
+ */
+MOE_API moe_status moe_route_backward(const float* logits, const int32_t* topk_idx, const float* dtopk_w,
+                                      const float* dscores, const uint8_t* token_mask, const void* tokens,
+                                      const float* Wg, moe_dtype dtype, int T, int d, int E, int k,
+                                      moe_score score, int renormalize, float scale, float* dlogits,
+                                      float* dWg, const void* dtokens_in, void* dtokens, void* workspace,
+                                      size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Weights in 8-bit floating point (e4m3: 4 exponent bits, 3 mantissa bits, largest value 448, no infinities),
+ * once when a layer is loaded:
+ *   scales[e, n, k] = the smallest power of two with  max |W[e, 128 k .. +127, 128 n .. +127]| <= 448 scale,
+ *   Wq[e, j, i]     = W[e, i, j] / scales[e, j / 128, i / 128], rounded to the nearest e4m3 value (ties to even).
+ *   W [E, K, N] in `dtype` (the layout of W1 and W2); Wq [E, N, K], one byte a value: each output's K weights
+ *   side by side; scales [E, N / 128, K / 128] float32 (a block of zeros: 1).
+ *   A block that holds an infinity or a NaN gets scale NaN and Wq NaN.
+ * Shapes: K, N multiples of 128, E K N < 2^43.  T plays no part here; E = 0 is an error.
+ */
+MOE_API moe_status moe_fp8_quantize(const void* W, moe_dtype dtype, int E, int K, int N, uint8_t* Wq,
+                                    float* scales, moe_stream_t stream);
+
+/* Bytes of workspace of moe_expert_ffn_fp8.  The bytes of an S_max are enough for every smaller one.
+ * Host only; writes *bytes. */
+MOE_API moe_status moe_expert_fp8_workspace_size(int T, int d, int f, int E, int S_max, moe_dtype dtype,
+                                                 size_t* bytes);
+
+/*
+ * moe_expert_ffn with weights and products in 8 bits, sums in float32:
+ *   x8, sx = q(tokens[perm[s], :]),   u[s, j] = sum_b sx[s, b] W1s[e, j / 128, b] sum_{i in b} x8[s, i] W1q[e, j, i],
+ *   h8, sh = q(GeLU_tanh(u[s, :])),   expert_out[s, j] = the same sum over h8, sh, W2q [E, d, f], W2s,
+ * where b runs over blocks of 128 inputs and q brings each block of 128 of a row to e4m3 as moe_fp8_quantize
+ * does a weight block (a scale that is a power of two, one rounding of each value).
+ *   W1q [E, f, d], W1s [E, f / 128, d / 128], W2q [E, d, f], W2s [E, d / 128, f / 128]: as moe_fp8_quantize
+ *   writes them, or with any finite float32 scales.
+ *   Everything else as moe_expert_ffn; workspace: moe_expert_fp8_workspace_size bytes, contents need no
+ *   initialisation; the device-side status word is in it (moe_status_read).
+ *   A token block that holds an infinity or a NaN makes its outputs NaN.
+ * Shapes: MOE_F16 (tokens and expert_out), d and f multiples of 128.  MOE_F32: MOE_ERR_UNSUPPORTED.
+ */
+MOE_API moe_status moe_expert_ffn_fp8(const void* tokens, const int32_t* perm, const int32_t* offsets,
+                                      const uint8_t* W1q, const float* W1s, const uint8_t* W2q,
+                                      const float* W2s, moe_dtype dtype, int T, int d, int f, int E, int S_max,
+                                      void* expert_out, void* workspace, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * The end of a block and the start of the next one, in one pass.  For every token t:
+ *   y = sum_j [0 <= slot_of[t,j] < S_max] topk_w[t,j] expert_out[slot_of[t,j], :]  (+ shared[t, :]),
+ *   z = gate . post_w . y / sqrt(mean(y^2) + eps)     (gate NULL: without; post_w NULL: z = gate . y, no norm),
+ *   hidden_out[t, :] = residual[t, :] + alpha z,
+ *   normed_out[t, :] = next_w . h / sqrt(mean(h^2) + eps),   h = hidden_out's row before its rounding,
+ * everything in float32, each output rounded once to `dtype`.
+ *   expert_out [S_max, d] with slot_of [T, k] and topk_w [T, k] float32 as moe_combine's, or all NULL with k = 0;
+ *   shared nullable [T, d] (a dense MLP's output, or any block's: the norms of one without experts).  With
+ *   neither, hidden_out is residual: hidden_out may be NULL then (the norm before the first block).
+ *   residual [T, d]; hidden_out may be residual itself.  post_w, gate, next_w nullable [d] float32; normed_out
+ *   nullable (with next_w: a norm whose weights are NULL does not exist), not NULL together with hidden_out.
+ *   rstd_post, rstd_next nullable [T] float32: 1 / sqrt(mean + eps) of the two norms, for the backward pass.
+ *   No output overlaps an input otherwise.
+ * Shapes: k <= 16, d a multiple of 8 (MOE_F16) or 4 (MOE_F32), at most 16384; T <= 2^30.
+ */
+MOE_API moe_status moe_block_norm(const void* residual, const void* expert_out, const int32_t* slot_of,
+                                  const float* topk_w, const void* shared, const float* post_w,
+                                  const float* gate, float alpha, const float* next_w, float eps,
+                                  moe_dtype dtype, int T, int d, int k, int S_max, void* hidden_out,
+                                  void* normed_out, float* rstd_post, float* rstd_next, moe_stream_t stream);
+
+/* Bytes of workspace of moe_block_norm_backward.  The bytes of a T are enough for every smaller one. */
+MOE_API moe_status moe_block_norm_workspace_size(int T, int d, int k, moe_dtype dtype, size_t* bytes);
+
+/*
+ * Gradient of moe_block_norm, from dhidden (of hidden_out) and dnormed (of normed_out), both nullable [T, d], not
+ * both NULL.  With rn = rstd_next, rp = rstd_post, h = hidden (as moe_block_norm wrote it) and y as there:
+ *   dh = dhidden + rn (next_w . dnormed - h rn^2 mean(h . next_w . dnormed)),      dresidual = dh,
+ *   dz = alpha gate . dh,    dy = rp (post_w . dz - y rp^2 mean(y . post_w . dz))    (post_w NULL: dy = dz),
+ *   dshared = dy,   dexpert_out[s, :] = topk_w[t,j] dy,   dtopk_w[t,j] = sum_i dy_i expert_out[s, i],
+ *   dnext_w = sum_t rn dnormed . h,   dgate = sum_t alpha dh . z0 (z0: z before its gate),   dpost_w = sum_t rp dz . y,
+ * for every assignment with s = slot_of[t, j] in [0, S_max) (dtopk_w of the others: 0; slots that no assignment
+ * names are left as they were; a slot that two name gets one of their rows).
+ *   hidden, rstd_next and next_w are read with dnormed only; rstd_post with post_w only.
+ *   dresidual, dexpert_out, dshared [like their values, `dtype`], dtopk_w [T, k], dpost_w, dgate, dnext_w [d]
+ *   (float32): each nullable, not all.  dgate needs gate, dpost_w post_w, dnext_w dnormed, dtopk_w and dexpert_out
+ *   expert_out.  dresidual may be dhidden itself; no output overlaps an input otherwise.
+ *   workspace: moe_block_norm_workspace_size bytes (NULL without dpost_w, dgate and dnext_w).
+ * With k = 1, post_w and no shared, dtopk_w is what rounding leaves of a sum that is zero but for eps: the norm
+ * does not change with the weight.
+ * Shapes: as moe_block_norm.
+ */
+MOE_API moe_status moe_block_norm_backward(const void* dhidden, const void* dnormed, const void* hidden,
+                                           const float* rstd_next, const float* next_w, const void* expert_out,
+                                           const int32_t* slot_of, const float* topk_w, const void* shared,
+                                           const float* post_w, const float* rstd_post, const float* gate,
+                                           float alpha, moe_dtype dtype, int T, int d, int k, int S_max,
+                                           void* dresidual, void* dexpert_out, float* dtopk_w, void* dshared,
+                                           float* dpost_w, float* dgate, float* dnext_w, void* workspace,
+                                           size_t ws_bytes, moe_stream_t stream);
 
 /*
  * Allocation-free variant of moe_expert_ffn (the pages have no counterpart).

@@ -18,6 +18,7 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE = 0, 1, 2, 3
 MOE_ERR_CUDA, MOE_ERR_TIMEOUT, MOE_ERR_DEVICE_BOUNDS = 4, 5, 6
 MOE_F32, MOE_F16 = 0, 1
 MOE_MLP_STANDARD, MOE_MLP_RESIDUAL = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 
 EXPORTED = ("moe_capacity", "moe_workspace_size", "moe_gate_topk", "moe_dispatch",
             "moe_expert_ffn", "moe_combine", "moe_layer_forward", "moe_status_read",
@@ -25,7 +26,9 @@ EXPORTED = ("moe_capacity", "moe_workspace_size", "moe_gate_topk", "moe_dispatch
             "moe_expert_ffn_noalloc", "moe_dispatch_sharded", "moe_kernel_launches",
             "moe_balance_workspace_size", "moe_balance_loss", "moe_gate_backward_workspace_size",
             "moe_gate_topk_backward", "moe_combine_backward", "moe_adapter_workspace_size",
-            "moe_adapter_forward", "moe_adapter_backward")
+            "moe_adapter_forward", "moe_adapter_backward", "moe_route", "moe_route_backward",
+            "moe_fp8_quantize", "moe_expert_fp8_workspace_size", "moe_expert_ffn_fp8", "moe_block_norm",
+            "moe_block_norm_workspace_size", "moe_block_norm_backward")
 
 _lib = None
 MOE_STAGE_EVENTS = 7
@@ -66,6 +69,14 @@ def get_lib():
         "moe_adapter_workspace_size": ([I, I, I, I, I, I, I, ctypes.POINTER(S)], I),
         "moe_adapter_forward": ([P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, P, P, S, P], I),
         "moe_adapter_backward": ([P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, P, P, P, S, P], I),
+        "moe_route": ([P, I, P, P, P, P, I, I, I, I, I, I, I, I, I, F, P, P, P, P, P], I),
+        "moe_route_backward": ([P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, P, P, P, P, P, S, P], I),
+        "moe_fp8_quantize": ([P, I, I, I, I, P, P, P], I),
+        "moe_expert_fp8_workspace_size": ([I, I, I, I, I, I, ctypes.POINTER(S)], I),
+        "moe_expert_ffn_fp8": ([P, P, P, P, P, P, P, I, I, I, I, I, I, P, P, S, P], I),
+        "moe_block_norm": ([P, P, P, P, P, P, P, F, P, F, I, I, I, I, I, P, P, P, P, P], I),
+        "moe_block_norm_workspace_size": ([I, I, I, I, ctypes.POINTER(S)], I),
+        "moe_block_norm_backward": ([P] * 12 + [F] + [I] * 5 + [P] * 8 + [S, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -456,3 +467,173 @@ def moe_adapter_backward(dout, tokens, hidden, perm, offsets, A, B, scale, works
           offsets.data_ptr(), A.data_ptr(), B.data_ptr(), scale.data_ptr(), _adr(dtokens_in), code, T,
           d_in, d_out, r, N, S_max, _adr(dtokens), _adr(dA), _adr(dB), workspace.data_ptr(),
           workspace.numel())
+
+
+# ---------------------------------------------------------------- a block of routed experts
+def moe_route(tokens, Wg, k, topk_idx, topk_w, logits_out=None, logits_in=None, scores_out=None, bias=None,
+              token_mask=None, score=MOE_SCORE_SOFTMAX, n_groups=1, top_groups=1, group_top=1,
+              renormalize=True, scale=1.0, stream=None):
+    """Routing by softmax or sigmoid scores: balance bias, groups of experts, top-k, weights."""
+    import torch
+    where = "moe_route"
+    f32, i32 = torch.float32, torch.int32
+    if logits_in is not None:
+        T, E = logits_in.shape
+        d, code = 1, MOE_F32
+        given = [(logits_in, f32, (T, E))]
+        names = "logits_in"
+    else:
+        _required(where, tokens=tokens, Wg=Wg, logits_out=logits_out)
+        T, d = tokens.shape
+        E, code = Wg.shape[1], _dtype(tokens)
+        given = [(tokens, tokens.dtype, (T, d)), (Wg, f32, (d, E))]
+        names = "tokens Wg"
+    given += [(topk_idx, i32, (T, k)), (topk_w, f32, (T, k)), (logits_out, f32, (T, E)),
+              (scores_out, f32, (T, E)), (bias, f32, (E,)), (token_mask, _mask_type(where, token_mask), (T,))]
+    dev = _device_of(where, names + " topk_idx topk_w logits_out scores_out bias token_mask", given)
+    x = None if logits_in is not None else tokens.data_ptr()
+    _call(where, dev, stream, x, code, None if x is None else Wg.data_ptr(), _adr(logits_in), _adr(bias),
+          _adr(token_mask), T, d, E, k, score, n_groups, top_groups, group_top, int(renormalize), scale,
+          _adr(logits_out), _adr(scores_out), topk_idx.data_ptr(), topk_w.data_ptr())
+
+
+def moe_route_backward(logits, topk_idx, dlogits, dtopk_w=None, dscores=None, token_mask=None,
+                       score=MOE_SCORE_SOFTMAX, renormalize=True, scale=1.0, tokens=None, Wg=None, dWg=None,
+                       dtokens=None, dtokens_in=None, workspace=None, stream=None):
+    """Gradient of moe_route's weights and scores: dlogits, and from it dWg and dtokens.
+
+    The workspace is moe_gate_backward_workspace_size's."""
+    import torch
+    where = "moe_route_backward"
+    T, E = logits.shape
+    k = topk_idx.shape[1]
+    f32 = torch.float32
+    given = [(logits, f32, (T, E)), (topk_idx, torch.int32, (T, k)), (dlogits, f32, (T, E)),
+             (dtopk_w, f32, (T, k)), (dscores, f32, (T, E)), (token_mask, _mask_type(where, token_mask), (T,))]
+    names = "logits topk_idx dlogits dtopk_w dscores token_mask"
+    code, d = MOE_F32, 4
+    if dWg is not None or dtokens is not None:
+        if dWg is not None:
+            _required(where, tokens=tokens)
+        if dtokens is not None:
+            _required(where, Wg=Wg)
+        like = tokens if dWg is not None else dtokens
+        d, el, code = like.shape[1], like.dtype, _dtype(like)
+        given += [(tokens if dWg is not None else None, el, (T, d)),
+                  (Wg if dtokens is not None else None, f32, (d, E)), (dWg, f32, (d, E)),
+                  (dtokens, el, (T, d)), (dtokens_in, el, (T, d)),
+                  (workspace, torch.uint8, None if workspace is None else workspace.shape)]
+        names += " tokens Wg dWg dtokens dtokens_in workspace"
+    dev = _device_of(where, names, given)
+    _call(where, dev, stream, logits.data_ptr(), topk_idx.data_ptr(), _adr(dtopk_w), _adr(dscores),
+          _adr(token_mask), _adr(tokens), _adr(Wg), code, T, d, E, k, score, int(renormalize), scale,
+          dlogits.data_ptr(), _adr(dWg), _adr(dtokens_in), _adr(dtokens), _adr(workspace), _ws_bytes(workspace))
+
+
+def _fp8_type(where, name, t):
+    """torch.float8_e4m3fn, or torch.uint8 for the same bytes."""
+    import torch
+    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise TypeError(f"{where}: {name} is {t.dtype}, expected torch.float8_e4m3fn or torch.uint8")
+    return t.dtype
+
+
+def moe_fp8_quantize(W, Wq, scales, stream=None):
+    """Expert weights W [E, K, N] to e4m3: Wq [E, N, K] and the scale of each 128 x 128 block."""
+    import torch
+    where = "moe_fp8_quantize"
+    E, K, N = W.shape
+    code = _dtype(W)
+    dev = _device_of(where, "W Wq scales",
+                     ((W, W.dtype, (E, K, N)), (Wq, _fp8_type(where, "Wq", Wq), (E, N, K)),
+                      (scales, torch.float32, (E, N // 128, K // 128))))
+    _call(where, dev, stream, W.data_ptr(), code, E, K, N, Wq.data_ptr(), scales.data_ptr())
+
+
+def moe_expert_fp8_workspace_size(T, d, f, E, S_max, dtype) -> int:
+    n = ctypes.c_size_t(0)
+    _check(get_lib().moe_expert_fp8_workspace_size(T, d, f, E, S_max, _code(dtype), ctypes.byref(n)),
+           "moe_expert_fp8_workspace_size")
+    return n.value
+
+
+def moe_expert_ffn_fp8(tokens, perm, offsets, W1q, W1s, W2q, W2s, S_max, expert_out, workspace, stream=None):
+    """moe_expert_ffn with weights, tokens and hidden rows in e4m3, a scale for each 128."""
+    import torch
+    where = "moe_expert_ffn_fp8"
+    T, d = tokens.shape
+    E, f, _ = W1q.shape
+    el, f32, i32 = tokens.dtype, torch.float32, torch.int32
+    if perm.numel() < S_max or expert_out.shape[0] < S_max:
+        raise ValueError(f"{where}: perm and expert_out need S_max = {S_max} rows")
+    dev = _device_of(where, "tokens perm offsets W1q W1s W2q W2s expert_out workspace",
+                     ((tokens, el, (T, d)), (perm, i32, (perm.numel(),)), (offsets, i32, (E + 1,)),
+                      (W1q, _fp8_type(where, "W1q", W1q), (E, f, d)), (W1s, f32, (E, f // 128, d // 128)),
+                      (W2q, _fp8_type(where, "W2q", W2q), (E, d, f)), (W2s, f32, (E, d // 128, f // 128)),
+                      (expert_out, el, (expert_out.shape[0], d)), (workspace, torch.uint8, workspace.shape)))
+    _call(where, dev, stream, tokens.data_ptr(), perm.data_ptr(), offsets.data_ptr(), W1q.data_ptr(),
+          W1s.data_ptr(), W2q.data_ptr(), W2s.data_ptr(), _dtype(tokens), T, d, f, E, S_max,
+          expert_out.data_ptr(), workspace.data_ptr(), workspace.numel())
+
+
+def _experts_of(expert_out, slot_of, topk_w, el, T, d):
+    """k, S_max and the checks of a block's expert rows (all None: a block without experts)."""
+    import torch
+    k = 0 if slot_of is None else slot_of.shape[1]
+    S_max = 0 if expert_out is None else expert_out.shape[0]
+    return k, S_max, [(expert_out, el, (S_max, d)), (slot_of, torch.int32, (T, k)),
+                      (topk_w, torch.float32, (T, k))]
+
+
+def moe_block_norm(residual, hidden_out=None, expert_out=None, slot_of=None, topk_w=None, shared=None, post_w=None,
+                   gate=None, alpha=1.0, next_w=None, normed_out=None, eps=1e-6, rstd_post=None, rstd_next=None,
+                   stream=None):
+    """hidden = residual + alpha gate norm(sum of expert rows + shared) post_w;  normed = norm(hidden) next_w."""
+    import torch
+    where = "moe_block_norm"
+    T, d = residual.shape
+    code, el, f32 = _dtype(residual), residual.dtype, torch.float32
+    k, S_max, experts = _experts_of(expert_out, slot_of, topk_w, el, T, d)
+    dev = _device_of(where, "residual expert_out slot_of topk_w hidden_out shared post_w gate next_w normed_out "
+                            "rstd_post rstd_next",
+                     [(residual, el, (T, d))] + experts +
+                     [(hidden_out, el, (T, d)), (shared, el, (T, d)), (post_w, f32, (d,)), (gate, f32, (d,)),
+                      (next_w, f32, (d,)), (normed_out, el, (T, d)), (rstd_post, f32, (T,)), (rstd_next, f32, (T,))])
+    _call(where, dev, stream, residual.data_ptr(), _adr(expert_out), _adr(slot_of), _adr(topk_w), _adr(shared),
+          _adr(post_w), _adr(gate), alpha, _adr(next_w), eps, code, T, d, k, S_max, _adr(hidden_out),
+          _adr(normed_out), _adr(rstd_post), _adr(rstd_next))
+
+
+def moe_block_norm_workspace_size(T, d, k, dtype) -> int:
+    n = ctypes.c_size_t(0)
+    _check(get_lib().moe_block_norm_workspace_size(T, d, k, _code(dtype), ctypes.byref(n)),
+           "moe_block_norm_workspace_size")
+    return n.value
+
+
+def moe_block_norm_backward(dhidden=None, dnormed=None, hidden=None, rstd_next=None, next_w=None, expert_out=None,
+                            slot_of=None, topk_w=None, shared=None, post_w=None, rstd_post=None, gate=None,
+                            alpha=1.0, dresidual=None, dexpert_out=None, dtopk_w=None, dshared=None, dpost_w=None,
+                            dgate=None, dnext_w=None, workspace=None, stream=None):
+    """Gradients of moe_block_norm from those of hidden_out and normed_out."""
+    import torch
+    where = "moe_block_norm_backward"
+    like = dhidden if dhidden is not None else dnormed
+    if like is None:
+        raise ValueError(f"{where}: dhidden or dnormed is required")
+    T, d = like.shape
+    code, el, f32 = _dtype(like), like.dtype, torch.float32
+    k, S_max, experts = _experts_of(expert_out, slot_of, topk_w, el, T, d)
+    dev = _device_of(where, ("dhidden" if dhidden is not None else "dnormed") + " dnormed hidden rstd_next next_w "
+                            "expert_out slot_of topk_w shared post_w rstd_post gate dresidual dexpert_out dtopk_w "
+                            "dshared dpost_w dgate dnext_w workspace",
+                     [(like, el, (T, d)), (dnormed, el, (T, d)), (hidden, el, (T, d)), (rstd_next, f32, (T,)),
+                      (next_w, f32, (d,))] + experts +
+                     [(shared, el, (T, d)), (post_w, f32, (d,)), (rstd_post, f32, (T,)), (gate, f32, (d,)),
+                      (dresidual, el, (T, d)), (dexpert_out, el, (S_max, d)), (dtopk_w, f32, (T, k)),
+                      (dshared, el, (T, d)), (dpost_w, f32, (d,)), (dgate, f32, (d,)), (dnext_w, f32, (d,)),
+                      (workspace, torch.uint8, None if workspace is None else workspace.shape)])
+    _call(where, dev, stream, _adr(dhidden), _adr(dnormed), _adr(hidden), _adr(rstd_next), _adr(next_w),
+          _adr(expert_out), _adr(slot_of), _adr(topk_w), _adr(shared), _adr(post_w), _adr(rstd_post), _adr(gate),
+          alpha, code, T, d, k, S_max, _adr(dresidual), _adr(dexpert_out), _adr(dtopk_w), _adr(dshared),
+          _adr(dpost_w), _adr(dgate), _adr(dnext_w), _adr(workspace), _ws_bytes(workspace))

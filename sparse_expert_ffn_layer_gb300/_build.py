@@ -16,7 +16,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["api.cu", "gate.cu", "dispatch.cu", "grouped_gemm.cu", "simt_ffn.cu", "elementwise.cu",
            "noalloc.cu", "route_small.cu", "router_loss.cu", "adapter.cu", "grad.cu", "gate_grad.cu",
-           "train_api.cu"]
+           "train_api.cu", "route.cu", "fp8.cu", "block_norm.cu", "block_api.cu"]
 HEADERS = ["common.cuh", "gate_split.cuh", "groups.cuh", "launch.h", "mma.cuh", "topk.cuh", os.path.join("..", "..", "include", "moe.h")]
 
 NVCC = os.environ.get("NVCC", "nvcc")

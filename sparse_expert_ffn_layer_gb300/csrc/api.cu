@@ -219,6 +219,19 @@ bool encode_f16_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* d
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_u8_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_inner,
+                   uint32_t box_outer) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {inner};
+  cuuint32_t box[2] = {box_inner, box_outer};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace moe
 
 namespace {
@@ -663,7 +676,7 @@ moe_status moe_gate_topk(const void* tokens, moe_dtype dtype, const float* Wg,
 moe_status moe_dispatch(const int32_t* topk_idx, int T, int E, int k, float capacity_factor,
                         int32_t* counts_raw, int32_t* kept, int32_t* offsets, int32_t* perm,
                         int32_t* slot_of, moe_stream_t stream) {
-  if (T < 0 || E < 1 || (k != 1 && k != 2) || k > E) return MOE_ERR_INVALID_ARG;
+  if (T < 0 || E < 1 || k < 1 || k > kRouteMaxK || k > E) return MOE_ERR_INVALID_ARG;
   const int C = capacity_of(T, E, capacity_factor);
   if (C < 0) return MOE_ERR_INVALID_ARG;
   if (E > kMaxE || (long long)T * k > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
@@ -679,7 +692,7 @@ moe_status moe_dispatch_sharded(const int32_t* topk_idx, int T, int E, int k,
                                 int n_ranks, int rank, int32_t* counts_raw, int32_t* kept,
                                 int32_t* offsets, int32_t* perm, int32_t* slot_of,
                                 moe_stream_t stream) {
-  if (T < 0 || T_global < T || E < 1 || (k != 1 && k != 2) || k > E) return MOE_ERR_INVALID_ARG;
+  if (T < 0 || T_global < T || E < 1 || k < 1 || k > kRouteMaxK || k > E) return MOE_ERR_INVALID_ARG;
   if (n_ranks < 1 || rank < 0 || rank >= n_ranks) return MOE_ERR_INVALID_ARG;
   const int C = capacity_of(T_global, E, capacity_factor);
   if (C < 0) return MOE_ERR_INVALID_ARG;

@@ -667,7 +667,7 @@ cudaError_t launch_gate_tc(const float* logits, const int32_t* topk_idx, const f
                            const float* dlosses, const int32_t* counts, const int32_t* n_valid,
                            const uint8_t* mask, int k, float* dlogits, const __half* tokens,
                            const float* Wg, float* dWg, const __half* dx_in, __half* dx, uint8_t* ws,
-                           int* status, int T, int d, int E, cudaStream_t s) {
+                           int* status, int T, int d, int E, cudaStream_t s, const RouteScore* how) {
   int dev = 0, sms = 0;
   MOE_LAUNCH(cudaGetDevice(&dev));
   MOE_LAUNCH(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
@@ -676,7 +676,7 @@ cudaError_t launch_gate_tc(const float* logits, const int32_t* topk_idx, const f
   __half *dl2 = reinterpret_cast<__half*>(ws + w.dl2), *W2 = reinterpret_cast<__half*>(ws + w.W2);
   float *sT = reinterpret_cast<float*>(ws + w.sT), *sW = reinterpret_cast<float*>(ws + w.sW);
   MOE_LAUNCH(launch_dlogits_split(logits, topk_idx, dtopk_w, dlosses, counts, n_valid, mask, T, E, k,
-                                  dlogits, status, dx ? Wg : nullptr, d, Ep, dl2, sT, W2, sW, s));
+                                  dlogits, status, dx ? Wg : nullptr, d, Ep, dl2, sT, W2, sW, s, how));
   const uint64_t l_dims[2] = {(uint64_t)2 * Ep, (uint64_t)T}, x_dims[2] = {(uint64_t)d, (uint64_t)T};
   const uint64_t w_dims[2] = {(uint64_t)2 * Ep, (uint64_t)d};
   const uint32_t b64[2] = {64, 64}, b128[2] = {64, 128};

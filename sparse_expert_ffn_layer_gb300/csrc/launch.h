@@ -135,6 +135,9 @@ cudaError_t ensure_smem_attr(const void* kernel);
 // Tensor map of a dense f16 tensor of two or three dimensions, swizzled by its box's inner bytes.
 bool encode_f16_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
                     const uint32_t* box);
+// Tensor map of a dense matrix of bytes [outer, inner]; a box of box_outer rows and 128 bytes, swizzled.
+bool encode_u8_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_inner,
+                   uint32_t box_outer);
 cudaError_t launch_grouped_gemm1(const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap& Ar,
                                  const CUtensorMap& Br, const GemmArgs& args, int grid,
                                  cudaStream_t s, bool pdl = false);
@@ -184,6 +187,59 @@ cudaError_t launch_finalize(const float* acc32, const float* r32, int T, int d, 
 cudaError_t launch_combine(const void* expert_out, const int32_t* slot_of, const float* topk_w,
                            const void* residual_in, int dtype_f16, int T, int d, int k, void* out,
                            cudaStream_t s);
+// Routing by scores (route.cu).
+constexpr int kRouteMaxK = 16, kRouteMaxGroups = 32;
+struct ScoreArgs {
+  const float *logits, *bias;
+  const uint8_t* mask;
+  int T, E, k, sigmoid, n_groups, top_groups, group_top, renorm;
+  float scale;
+  float *logits_copy, *scores;       // null: not written
+  int32_t* topk_idx;
+  float* topk_w;
+};
+cudaError_t launch_route(const ScoreArgs& a, cudaStream_t s, bool pdl);
+// How moe_route made its weights, for their gradient: given in place of moe_gate_topk's softmax top-1 /
+// top-2 (dlosses null then).
+struct RouteScore {
+  const float* dscores;              // [T, E], or null
+  int sigmoid, renorm;
+  float scale;
+};
+// Experts in 8 bits (fp8.cu).
+size_t fp8_ffn_bytes(int d, int f, int S_max);
+cudaError_t launch_fp8_weights(const void* W, bool f16, int E, int K, int N, uint8_t* Wq, float* scales,
+                               cudaStream_t s);
+cudaError_t launch_fp8_ffn(const void* tokens, const int32_t* perm, const int32_t* offsets, const uint8_t* W1q,
+                           const float* W1s, const uint8_t* W2q, const float* W2s, int T, int d, int f, int E,
+                           int S_max, void* out, uint8_t* ws, cudaStream_t s);
+// A block's end and the next one's start (block_norm.cu; include/moe.h has the meanings).
+struct NormArgs {
+  const void *residual, *expert_out;
+  const int32_t* slot_of;
+  const float* topk_w;
+  const void* shared;
+  const float *post_w, *gate, *next_w;
+  float alpha, eps;
+  int T, d, k, S_max;
+  int with_block;                    // 0: neither experts nor shared: h = residual
+  void *hidden_out, *normed_out;
+  float *rstd_post, *rstd_next;
+};
+struct NormGrads {
+  const void *dhidden, *dnormed, *hidden;
+  const float *rstd_next, *rstd_post;
+  void *dresidual, *dexpert_out;
+  float* dtopk_w;
+  void* dshared;
+  float *dpost_w, *dgate, *dnext_w;
+  float* partial;                    // [norm_teams][3][d], null without a sum over tokens
+  int through;                       // 1: something behind dresidual is wanted
+  int need_y;                        // 1: y is
+};
+int norm_teams(int T, int d, bool f16);
+cudaError_t launch_block_norm(const NormArgs& a, bool f16, cudaStream_t s);
+cudaError_t launch_block_norm_backward(const NormArgs& a, const NormGrads& b, bool f16, cudaStream_t s);
 // Router losses and the logits' gradient (router_loss.cu).
 size_t balance_records_bytes(int E);
 cudaError_t launch_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* mask,
@@ -192,7 +248,7 @@ cudaError_t launch_balance_loss(const float* logits, const int32_t* topk_idx, co
 cudaError_t launch_dlogits(const float* logits, const int32_t* topk_idx, const float* dtopk_w,
                            const float* dlosses, const int32_t* counts, const int32_t* n_valid,
                            const uint8_t* mask, int T, int E, int k, float* dlogits, int* status,
-                           cudaStream_t s);
+                           cudaStream_t s, const RouteScore* how = nullptr);
 // Sums over token rows for up to two jobs G[n][i][j] = scale_n sum_s x[row(s)][i] h[s][j]
 // (transposed: G[n][j][i]); G0 or G1 may be null (grad.cu).
 // Segments that the rows are cut into at most, for sums of `words` values in all: two partial sums
@@ -226,13 +282,14 @@ cudaError_t launch_gate_tc(const float* logits, const int32_t* topk_idx, const f
                            const float* dlosses, const int32_t* counts, const int32_t* n_valid,
                            const uint8_t* mask, int k, float* dlogits, const __half* tokens,
                            const float* Wg, float* dWg, const __half* dx_in, __half* dx, uint8_t* ws,
-                           int* status, int T, int d, int E, cudaStream_t s);
+                           int* status, int T, int d, int E, cudaStream_t s,
+                           const RouteScore* how = nullptr);
 // Its first launch: the logits' gradient, also in f16 parts, and (Wg not null) Wg in f16 parts.
 cudaError_t launch_dlogits_split(const float* logits, const int32_t* topk_idx, const float* dtopk_w,
                                  const float* dlosses, const int32_t* counts, const int32_t* n_valid,
                                  const uint8_t* mask, int T, int E, int k, float* dlogits, int* status,
                                  const float* Wg, int d, int Ep, __half* dl2, float* sT, __half* W2,
-                                 float* sW, cudaStream_t s);
+                                 float* sW, cudaStream_t s, const RouteScore* how = nullptr);
 cudaError_t launch_gate_dx(const float* dlogits, const float* Wg, const void* in, int dtype_f16, int T,
                            int d, int E, void* out, cudaStream_t s);
 cudaError_t launch_combine_backward(const void* dout, const void* expert_out, const int32_t* slot_of,

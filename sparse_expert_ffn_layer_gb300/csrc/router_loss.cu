@@ -324,6 +324,17 @@ struct DlArgs {
   int* status;                 // cleared, or null
 };
 
+// The gradient of moe_route's weights and scores, by the same passes.
+struct RouteDlArgs : DlArgs {
+  RouteScore how;
+};
+
+// One row's logits.
+template <int LANES, int VEC, int J>
+__device__ __forceinline__ void take_row(const DlArgs& d, int64_t t, bool on, int l, float (&x)[VEC * J]) {
+  load_row<LANES, VEC, J>(d.logits + (on ? t : 0) * d.E, d.E, l, on, x);
+}
+
 // What every row needs: a_e of this lane's columns and the factor of the z loss.
 template <int LANES, int VEC, int J>
 __device__ __forceinline__ float loss_factors(const DlArgs& d, int l, float (&a)[VEC * J]) {
@@ -411,6 +422,126 @@ __device__ __forceinline__ void row_gradient(const DlArgs& d, int64_t t, bool on
   }
 }
 
+// moe_route: s = softmax(x) or sigmoid(x), w_j = c s_j (c = scale, or scale / sum of the chosen s).  With
+// g = dtopk_w and u_j proportional to s_j:
+//   c constant:    d/ds_j = scale g_j;     renormalised: w_j's share (g_j - sum g u / sum u) / s_j,
+//   sigmoid:  dx_e = s_e (1 - s_e) ds_e;   softmax: dx_e = s_e (ds_e - sum ds s).
+// Of the renormalised weights nothing is divided by s_j: dx_j = w_j (g_j - mean) (times 1 - s_j for the
+// sigmoid; the softmax's sum ds s is zero), so that scores near zero lose nothing.  Unless dscores or the
+// softmax's own sum is wanted only the chosen columns are not zero, and the row itself is not read.
+__device__ __forceinline__ bool route_row_read(const RouteDlArgs& d) {
+  return d.how.dscores || (!d.how.sigmoid && !d.how.renorm && d.dtopk_w);
+}
+template <int LANES, int VEC, int J>
+__device__ __forceinline__ void take_row(const RouteDlArgs& d, int64_t t, bool on, int l, float (&x)[VEC * J]) {
+  load_row<LANES, VEC, J>(d.logits + (on ? t : 0) * d.E, d.E, l, on && route_row_read(d), x);
+}
+template <int LANES, int VEC, int J>
+__device__ __forceinline__ float loss_factors(const RouteDlArgs&, int, float (&)[VEC * J]) {
+  return 0.f;
+}
+template <int LANES, int VEC, int J>
+__device__ __forceinline__ void row_gradient(const RouteDlArgs& d, int64_t t, bool on, int l,
+                                             const float (&)[VEC * J], float, float (&x)[VEC * J]) {
+  constexpr int V = VEC * J;
+  constexpr int KL = LANES >= kRouteMaxK ? 1 : kRouteMaxK / LANES;   // chosen experts per lane of the row
+  const bool whole = route_row_read(d);
+  float lse = 0.f;
+  if (whole && !d.how.sigmoid) lse = softmax_row<LANES>(x);           // x is s now
+  // this lane's share of the chosen experts
+  int idx[KL];
+  float xs[KL], g[KL], u[KL];
+  float top = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < KL; ++q) {
+    const int j = q * LANES + l;
+    idx[q] = -1;
+    xs[q] = -INFINITY;
+    g[q] = 0.f;
+    if (d.dtopk_w && on && j < d.k) {
+      const int e = d.topk_idx[(size_t)t * d.k + j];
+      if ((unsigned)e < (unsigned)d.E) {
+        idx[q] = e;
+        xs[q] = d.logits[(size_t)t * d.E + e];
+        g[q] = d.dtopk_w[(size_t)t * d.k + j] * d.how.scale;
+      }
+    }
+    top = fmaxf(top, d.how.sigmoid ? fminf(xs[q], 0.f) : xs[q]);
+  }
+  float su = 0.f, sg = 0.f;                                          // sums of u and g u
+  if (d.how.renorm) top = group_max<LANES>(top);
+#pragma unroll
+  for (int q = 0; q < KL; ++q) {
+    float v;
+    if (d.how.sigmoid) {
+      const float low = fminf(xs[q], 0.f) - (d.how.renorm ? top : 0.f);
+      v = xs[q] == -INFINITY ? 0.f : expf(low) / (1.f + expf(-fabsf(xs[q])));
+    } else {
+      v = xs[q] == -INFINITY ? 0.f : expf(xs[q] - (d.how.renorm ? top : lse));
+    }
+    u[q] = v;
+    su += v;
+    sg += g[q] * v;
+  }
+  su = group_sum<LANES>(su);
+  sg = group_sum<LANES>(sg);
+  const float inv = su > 0.f ? 1.f / su : 0.f, mean = sg * inv;
+  float add[KL];
+#pragma unroll
+  for (int q = 0; q < KL; ++q) {
+    add[q] = d.how.renorm ? u[q] * inv * (g[q] - mean) : u[q] * g[q];
+    if (d.how.sigmoid && u[q] > 0.f) add[q] *= 1.f / (1.f + expf(xs[q]));   // 1 - s
+  }
+  // every column: the scores' own gradient, and what the softmax takes off for its sum
+  if (whole) {
+    float bar = 0.f;
+    float ds[V];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const int c = col_of<LANES, VEC>(j, l) + v;
+        ds[VEC * j + v] = d.how.dscores && on && c < d.E ? d.how.dscores[(size_t)t * d.E + c] : 0.f;
+        if (!d.how.sigmoid) bar += ds[VEC * j + v] * x[VEC * j + v];
+      }
+    if (!d.how.sigmoid) bar = group_sum<LANES>(bar) + (d.how.renorm ? 0.f : sg);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (d.how.sigmoid) {
+        const float e = expf(-fabsf(x[i])), r = 1.f / (1.f + e);      // s (1 - s) = e / (1 + e)^2
+        x[i] = x[i] == -INFINITY ? 0.f : e * r * r * ds[i];
+      } else {
+        x[i] *= ds[i] - bar;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = 0.f;
+  }
+  if (!on)
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = 0.f;
+  if (d.dtopk_w) {
+    for (int j = 0; j < d.k; ++j) {
+      int e = -1;
+      float a = 0.f;
+#pragma unroll
+      for (int q = 0; q < KL; ++q)
+        if (j / LANES == q) {
+          e = idx[q];
+          a = add[q];
+        }
+      e = __shfl_sync(0xffffffffu, e, j % LANES, LANES);
+      a = __shfl_sync(0xffffffffu, a, j % LANES, LANES);
+#pragma unroll
+      for (int jj = 0; jj < J; ++jj)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+          if (col_of<LANES, VEC>(jj, l) + v == e) x[VEC * jj + v] += a;
+    }
+  }
+}
+
 template <int LANES, int VEC, int J>
 __device__ __forceinline__ void store_row(const DlArgs& d, int64_t t, int l, const float (&q)[VEC * J]) {
 #pragma unroll
@@ -429,8 +560,8 @@ __device__ __forceinline__ void store_row(const DlArgs& d, int64_t t, int l, con
 // Gradient of the logits, one row per group of lanes.  Rows are taken from the last to the
 // first: right after moe_balance_loss the rows that it read last are still in L2.  262144 x 128
 // logits: 43 us, 6.2 TB/s read and written (DRAM; streaming stores changed nothing).
-template <int LANES, int VEC, int J>
-__global__ void __launch_bounds__(256) dlogits_kernel(const DlArgs d) {
+template <int LANES, int VEC, int J, typename D>
+__global__ void __launch_bounds__(256) dlogits_kernel(const D d) {
   if (d.status && blockIdx.x == 0 && threadIdx.x == 0) *d.status = kOk;
   constexpr int V = VEC * J, RPW = 32 / LANES;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -442,7 +573,7 @@ __global__ void __launch_bounds__(256) dlogits_kernel(const DlArgs d) {
     const int64_t t = d.T - 1 - (base + g);
     const bool in = t >= 0, on = in && (!d.mask || d.mask[t]);
     float x[V];
-    load_row<LANES, VEC, J>(d.logits + (on ? t : 0) * d.E, d.E, l, on, x);
+    take_row<LANES, VEC, J>(d, t, on, l, x);
     row_gradient<LANES, VEC, J>(d, t, on, l, a, gz, x);
     if (in) store_row<LANES, VEC, J>(d, t, l, x);
   }
@@ -539,8 +670,8 @@ __device__ __forceinline__ float split_block(const float* src, int rows, int E, 
   return exp2_int(e);
 }
 
-template <int LANES, int VEC, int J>
-__global__ void __launch_bounds__(kSplitThreads) dlogits_split_kernel(const DlArgs d, const SplitOut o) {
+template <int LANES, int VEC, int J, typename D>
+__global__ void __launch_bounds__(kSplitThreads) dlogits_split_kernel(const D d, const SplitOut o) {
   constexpr int V = VEC * J, RPW = 32 / LANES;
   __shared__ float scratch[kSplitThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -583,7 +714,7 @@ __global__ void __launch_bounds__(kSplitThreads) dlogits_split_kernel(const DlAr
       const int r = p * kPass + w * RPW + g;
       const int64_t t = (int64_t)row0 + r;
       const bool in = r < rows, on = in && (!d.mask || d.mask[t]);
-      load_row<LANES, VEC, J>(d.logits + (on ? t : 0) * d.E, d.E, l, on, x[p]);
+      take_row<LANES, VEC, J>(d, t, on, l, x[p]);
       row_gradient<LANES, VEC, J>(d, t, on, l, a, gz, x[p]);
       if (in) store_row<LANES, VEC, J>(d, t, l, x[p]);
 #pragma unroll
@@ -626,7 +757,7 @@ __global__ void __launch_bounds__(kSplitThreads) dlogits_split_kernel(const DlAr
       const int64_t t = (int64_t)row0 + r;
       const bool in = r < rows, on = in && (!d.mask || d.mask[t]);
       float x[V];
-      load_row<LANES, VEC, J>(d.logits + (on ? t : 0) * d.E, d.E, l, on, x);
+      take_row<LANES, VEC, J>(d, t, on, l, x);
       row_gradient<LANES, VEC, J>(d, t, on, l, a, gz, x);
       if (in) store_row<LANES, VEC, J>(d, t, l, x);
 #pragma unroll
@@ -747,7 +878,7 @@ cudaError_t launch_balance_loss(const float* logits, const int32_t* topk_idx, co
 cudaError_t launch_dlogits(const float* logits, const int32_t* topk_idx, const float* dtopk_w,
                            const float* dlosses, const int32_t* counts, const int32_t* n_valid,
                            const uint8_t* mask, int T, int E, int k, float* dlogits, int* status,
-                           cudaStream_t s) {
+                           cudaStream_t s, const RouteScore* how) {
   const int sms = sm_count();
   if (sms < 1) return cudaErrorInvalidDevice;
   const DlArgs d{logits, topk_idx, dtopk_w, dlosses, counts, n_valid, mask, T, E, k, dlogits, status};
@@ -755,7 +886,8 @@ cudaError_t launch_dlogits(const float* logits, const int32_t* topk_idx, const f
   const int grid = std::max(1, std::min((T + rows - 1) / rows, 8 * sms));
   return with_shape(E, [&](auto lanes, auto vec, auto j) -> cudaError_t {
     constexpr int L = decltype(lanes)::value, V = decltype(vec)::value, J = decltype(j)::value;
-    return launch_k(dlogits_kernel<L, V, J>, grid, 256, 0, s, false, d);
+    if (how) return launch_k(dlogits_kernel<L, V, J, RouteDlArgs>, grid, 256, 0, s, false, RouteDlArgs{d, *how});
+    return launch_k(dlogits_kernel<L, V, J, DlArgs>, grid, 256, 0, s, false, d);
   });
 }
 
@@ -763,7 +895,7 @@ cudaError_t launch_dlogits_split(const float* logits, const int32_t* topk_idx, c
                                  const float* dlosses, const int32_t* counts, const int32_t* n_valid,
                                  const uint8_t* mask, int T, int E, int k, float* dlogits, int* status,
                                  const float* Wg, int d, int Ep, __half* dl2, float* sT, __half* W2,
-                                 float* sW, cudaStream_t s) {
+                                 float* sW, cudaStream_t s, const RouteScore* how) {
   const DlArgs a{logits, topk_idx, dtopk_w, dlosses, counts, n_valid, mask, T, E, k, dlogits, status};
   const SplitOut o{dl2, sT, Wg, W2, sW, d, Ep, (T + kGateBlock - 1) / kGateBlock};
   const int grid = o.nT + (Wg ? (d + kGateBlock - 1) / kGateBlock : 0);
@@ -771,8 +903,11 @@ cudaError_t launch_dlogits_split(const float* logits, const int32_t* topk_idx, c
     constexpr int L = decltype(lanes)::value, V = decltype(vec)::value, J = decltype(j)::value;
     if constexpr (L > 16)
       return cudaErrorInvalidValue;               // E > 256 takes the other form
+    else if (how)
+      return launch_k(dlogits_split_kernel<L, V, J, RouteDlArgs>, grid, kSplitThreads, 0, s, false,
+                      RouteDlArgs{a, *how}, o);
     else
-      return launch_k(dlogits_split_kernel<L, V, J>, grid, kSplitThreads, 0, s, false, a, o);
+      return launch_k(dlogits_split_kernel<L, V, J, DlArgs>, grid, kSplitThreads, 0, s, false, a, o);
   });
 }
 
