@@ -185,7 +185,7 @@ moe_status moe_expert_fp8_workspace_size(int T, int d, int f, int E, int S_max, 
   if (!bytes) return MOE_ERR_INVALID_ARG;
   moe_status st = check_fp8(T, d, f, E, S_max, dtype);
   if (st != MOE_OK) return st;
-  *bytes = fp8_ffn_bytes(d, f, S_max);
+  *bytes = fp8_ffn_bytes(d, f, E, S_max);
   return MOE_OK;
 }
 
@@ -201,7 +201,7 @@ moe_status moe_expert_ffn_fp8(const void* tokens, const int32_t* perm, const int
     if (!aligned16(tokens) || !aligned4(perm) || !aligned4(offsets) || !aligned16(W1q) || !aligned4(W1s) ||
         !aligned16(W2q) || !aligned4(W2s) || !aligned16(expert_out) || !aligned16(workspace))
       return MOE_ERR_UNSUPPORTED;
-    if (!workspace || ws_bytes < fp8_ffn_bytes(d, f, S_max)) return MOE_ERR_WORKSPACE;
+    if (!workspace || ws_bytes < fp8_ffn_bytes(d, f, E, S_max)) return MOE_ERR_WORKSPACE;
     MOE_TRY(launch_fp8_ffn(tokens, perm, offsets, W1q, W1s, W2q, W2s, T, d, f, E, S_max, expert_out,
                            static_cast<uint8_t*>(workspace), as_stream(stream)));
     return MOE_OK;

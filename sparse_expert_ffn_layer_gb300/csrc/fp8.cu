@@ -11,7 +11,10 @@
 // four MMAs whose sum goes to a TMEM slot, from where 16 warps add it, times its scale, to the running sums in
 // their registers (column n of a tile has one scale, a weight tile has one for all its rows).  So the sums over
 // blocks are in 32 bits with every scale applied before them, and a slot is free again as soon as it was read.
+// One more warp multiplies the two scales, so that the 16 do one multiply-add a value and no product (which
+// their multiply-add pipes would pay for in each of the four quarters: they bound the kernel then).
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 
 #include "launch.h"
@@ -120,69 +123,127 @@ __global__ void __launch_bounds__(256) fp8_weights_kernel(const T* __restrict__ 
   if (tid == 0) scales[(e * nn + nb) * nk + kb] = scale;
 }
 
+// ---------------------------------------------------------------- slots
+// Boundaries of the experts' slots as every kernel here uses them, by one warp: the largest offset so far, clamped
+// to [0, S_max], so that runs never overlap or leave the buffers.  prefix[e] (not null): tiles of at most `nmax`
+// rows of the experts before e.  True where an offset was changed.
+__device__ __forceinline__ bool slot_table(const int32_t* offsets, int E, int S_max, int nmax, int32_t* offs,
+                                           int32_t* prefix) {
+  const int lane = threadIdx.x & 31;
+  bool bad = false;
+  int run = 0, tiles = 0;
+  for (int e0 = 0; e0 <= E; e0 += 32) {
+    const int e = e0 + lane;
+    const int o = e <= E ? __ldcg(offsets + e) : 0;
+    int v = min(max(o, 0), S_max);
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int q = __shfl_up_sync(0xffffffffu, v, k);
+      if (lane >= k) v = max(v, q);
+    }
+    v = max(v, run);
+    bad |= e <= E && v != o;
+    if (e <= E) offs[e] = v;
+    int before = __shfl_up_sync(0xffffffffu, v, 1);
+    if (lane == 0) before = run;
+    run = __shfl_sync(0xffffffffu, v, 31);
+    if (!prefix) continue;
+    int c = e >= 1 && e <= E ? (v - before + nmax - 1) / nmax : 0;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int q = __shfl_up_sync(0xffffffffu, c, k);
+      if (lane >= k) c += q;
+    }
+    if (e <= E) prefix[e] = tiles + c;
+    tiles += __shfl_sync(0xffffffffu, c, 31);
+  }
+  return bad;
+}
+// Where the scales of expert e's slots begin in a row of scales: a multiple of four, and no run reaches the next
+// (rounded up to four, a run is at least three shorter than its slots; four are added for each expert).
+__device__ __forceinline__ int scale_base(int first_slot, int e) { return ((first_slot + 3) & ~3) + 4 * e; }
+int scale_row(int S_max, int E) { return (S_max + 3) / 4 * 4 + 4 * (E + 1); }
+
 // ---------------------------------------------------------------- rows
-// Slot s of an expert: its token's row in 8 bits, by 16 lanes a block of 128 columns.  sx is [d / 128][Sp].
+// Slot s of an expert: its token's row in 8 bits.  A warp takes a row, 16 lanes a block of 128 columns.  sx is
+// [d / 128][Sp], a slot's place in it by scale_base.
 __global__ void __launch_bounds__(256) fp8_rows_kernel(const __half* __restrict__ tokens, const int32_t* __restrict__ perm,
                                                        const int32_t* __restrict__ offsets, int E, int S_max, int T, int d,
                                                        int Sp, uint8_t* __restrict__ Xq, float* __restrict__ sx,
                                                        int* status) {
+  extern __shared__ int32_t offs[];
   pdl_wait();
   pdl_trigger();
-  const int S = min(max(offsets[E], 0), S_max);
-  const int nb = d / 128, l = threadIdx.x & 15;
-  const long long total = (long long)S * nb, step = (long long)gridDim.x * 16;
+  if (threadIdx.x < 32 && slot_table(offsets, E, S_max, 1, offs, nullptr)) record_status(status, kErrBounds);
+  __syncthreads();
+  const int lane = threadIdx.x & 31, l = lane & 15, nb = d / 128, S = offs[E];
   bool bad = false;
-  for (long long u = (long long)blockIdx.x * 16 + (threadIdx.x >> 4); __any_sync(0xffffffffu, u < total); u += step) {
-    const bool on = u < total;
-    const int s = on ? (int)(u / nb) : 0, b = on ? (int)(u - (long long)s * nb) : 0;
-    const int t = on ? perm[s] : 0;
+  for (int s = blockIdx.x * 8 + (threadIdx.x >> 5); s < S; s += gridDim.x * 8) {
+    const int t = perm[s];
     const bool in = (unsigned)t < (unsigned)T;
     bad |= !in;
-    float f[8];
+    int lo = 0, hi = E;                         // the last e with offs[e] <= s
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (offs[mid] <= s) lo = mid; else hi = mid;
+    }
+    float* scale_at = sx + scale_base(offs[lo], lo) + (s - offs[lo]);
+    const __half* src = tokens + (long long)(in ? t : 0) * d + l * 8;
+    uint8_t* dst = Xq + (long long)s * d + l * 8;
+#pragma unroll 4
+    for (int b0 = 0; b0 < nb; b0 += 2) {
+      const int b = b0 + (lane >> 4);
+      float f[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = 0.f;
-    if (on && in) load8(tokens + (long long)t * d + b * 128 + l * 8, f);
-    uint32_t m = 0;
+      for (int j = 0; j < 8; ++j) f[j] = 0.f;
+      if (b < nb && in) load8(src + b * 128, f);
+      uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, magnitude_bits(f[j]));
+      for (int j = 0; j < 8; ++j) m = max(m, magnitude_bits(f[j]));
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float scale, inv;
-    fp8_scale(m, scale, inv);
-    if (on) {
-      const uint2 r = make_uint2(fp8_four(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-                                 fp8_four(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
-      *reinterpret_cast<uint2*>(Xq + (long long)s * d + b * 128 + l * 8) = r;
-      if (l == 0) sx[(long long)b * Sp + s] = scale;
+      for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      float scale, inv;
+      fp8_scale(m, scale, inv);
+      if (b < nb) {
+        *reinterpret_cast<uint2*>(dst + b * 128) =
+            make_uint2(fp8_four(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
+                       fp8_four(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
+        if (l == 0) scale_at[(long long)b * Sp] = scale;
+      }
     }
   }
   if (bad) record_status(status, kErrBounds);
 }
 
 // ---------------------------------------------------------------- products
+// Warps 0 to 3 load the weight tiles, issue the products, multiply the scales and load the rows; 16 more add.
+// (One warp for both loads took 600 cycles a block of its own time, and bound the kernel.)
 constexpr int kEpiWarps = 16;                 // four column groups of the four TMEM lane quarters
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kABytes = 128 * 128;            // a weight tile: 128 outputs, 128 inputs
-constexpr int kScaleSlots = 8;
+constexpr int kScaleSlots = 16;               // blocks whose scales are on their way
 constexpr int kMaxSlots = 16;
 constexpr int kMaxStages = 16;
 constexpr size_t kMinSmem = 116 * 1024;       // one block per SM: each takes all of TMEM
 
 struct Fp8Smem {
-  uint32_t stage_bytes, b_off, scale_off, scale_bytes, amax_off, bars_off, misc_off, total;
+  uint32_t stage_bytes, b_off, raw_off, raw_bytes, scale_off, scale_bytes, amax_off, bars_off, misc_off, total;
 };
 __host__ __device__ inline Fp8Smem fp8_smem(int nmax, int mw, int stages, int E) {
   Fp8Smem L;
   L.b_off = (uint32_t)mw * kABytes;
   L.stage_bytes = L.b_off + (uint32_t)nmax * 128u;
   uint32_t off = (uint32_t)stages * L.stage_bytes;
-  L.scale_off = off;
-  L.scale_bytes = (uint32_t)(nmax + 4) * 4u;
-  off += kScaleSlots * L.scale_bytes;
+  L.raw_off = off;                            // the rows' scales of a block, and the weight tiles'
+  L.raw_bytes = (uint32_t)nmax * 4u + 16u;
+  off += kScaleSlots * L.raw_bytes;
+  L.scale_off = off;                          // their products, for each sum's slot
+  L.scale_bytes = (uint32_t)nmax * 4u;
+  off += kMaxSlots * L.scale_bytes;
   L.amax_off = off;
   off += 2u * (uint32_t)(mw * nmax) * 16u;    // two items' [column][lane quarter]
   L.bars_off = off;
-  off += (2u * kMaxStages + 2u * kMaxSlots + 2u * kScaleSlots + 1u) * 8u;
+  off += (2u * kMaxStages + 2u * kMaxSlots + 1u) * 8u + 8u;
   L.misc_off = off;
   off += 16u + 8u * (uint32_t)(E + 1);
   L.total = off + 1024u;                      // slack for the alignment of the stages
@@ -221,16 +282,58 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[B][8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) asm volatile("" : "+r"(r[b][i]));   // no use of them moves above the wait
 }
-// Untiled copy to shared memory: addresses and size are multiples of 16 bytes.
-__device__ __forceinline__ void bulk_load(void* smem, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(smem)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
+// 4 and 16 bytes global -> shared, by the thread itself.
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// As mbar_wait_bounded; the clock is read only by a wait that is long already.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+    if ((it & 63u) == 0) {
+      if (*abort) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kDefaultWaitNs) {
+        record_status(status, kErrTimeout);
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
+// Two 32-bit operations at a time.
+__device__ __forceinline__ unsigned long long bits2(float2 v) {
+  return (unsigned long long)__float_as_uint(v.y) << 32 | __float_as_uint(v.x);
+}
+__device__ __forceinline__ float2 float2_of(unsigned long long r) {
+  return make_float2(__uint_as_float((uint32_t)r), __uint_as_float((uint32_t)(r >> 32)));
+}
+__device__ __forceinline__ float2 pair(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
+__device__ __forceinline__ void fma2(float2& d, float2 a, float2 b) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(d)));
+  d = float2_of(r);
 }
 
 struct Tile8 {
   int e, row0, n, mt;
+  int sc0;                                    // its first slot's place in a row of scales
 };
 // Item i: an expert, MW neighbouring weight tiles and a run of its rows; the runs of one weight tile are next to
 // each other, on different SMs at the same time, and share it in L2.
@@ -248,6 +351,7 @@ __device__ __forceinline__ Tile8 tile_at(int i, const int32_t* prefix, const int
   t.mt = local / chunks;
   const int c = local - t.mt * chunks;
   t.row0 = offs[lo] + c * per;
+  t.sc0 = scale_base(offs[lo], lo) + c * per;
   t.n = min(per, rows - c * per);
   return t;
 }
@@ -256,14 +360,15 @@ __device__ __forceinline__ Tile8 tile_at(int i, const int32_t* prefix, const int
 // with one load of the rows.  kGelu: first product.
 template <int C8, int MW, bool kGelu>
 __global__ void __launch_bounds__(kThreads, 1)
-    fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Fp8Args a) {
-  constexpr int NMAX = 32 * C8, COLS = 8 * C8;
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmB16, const Fp8Args a) {
+  constexpr int NMAX = 32 * C8;
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const Fp8Smem L = fp8_smem(NMAX, MW, a.stages, a.E);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L.bars_off);
   uint64_t *empty = full + kMaxStages, *acc_full = empty + kMaxStages, *acc_empty = acc_full + kMaxSlots,
-           *sc_full = acc_empty + kMaxSlots, *sc_empty = sc_full + kScaleSlots, *spare = sc_empty + kScaleSlots;
+           *spare = acc_empty + kMaxSlots;
   uint32_t* holder = reinterpret_cast<uint32_t*>(sm + L.misc_off);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L.misc_off + 4);
   int32_t* prefix = reinterpret_cast<int32_t*>(sm + L.misc_off + 16);
@@ -271,16 +376,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);                   // weights and rows
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < a.nslots; ++s) {
-      mbar_init(&acc_full[s], 1);
+      mbar_init(&acc_full[s], 2);               // the sum and its scales
       mbar_init(&acc_empty[s], kEpiWarps);
-    }
-    for (int s = 0; s < kScaleSlots; ++s) {
-      mbar_init(&sc_full[s], 1);
-      mbar_init(&sc_empty[s], kEpiWarps);
     }
     mbar_init(spare, 1);
     *abort_flag = 0;
@@ -289,199 +390,220 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
+    prefetch_tmap(&tmB16);
   }
   if (warp == 1) tmem_alloc(holder, 512);
   pdl_wait();
   pdl_trigger();
-  if (warp == 2) {
-    // boundaries: the largest so far, clamped to [0, S_max], so that runs never overlap or leave the buffers
-    bool bad = false;
-    int run = 0, tiles = 0;
-    for (int e0 = 0; e0 <= a.E; e0 += 32) {
-      const int e = e0 + lane;
-      const int o = e <= a.E ? __ldcg(a.offsets + e) : 0;
-      int v = min(max(o, 0), a.S_max);
-#pragma unroll
-      for (int k = 1; k < 32; k <<= 1) {
-        const int q = __shfl_up_sync(0xffffffffu, v, k);
-        if (lane >= k) v = max(v, q);
-      }
-      v = max(v, run);
-      bad |= e <= a.E && v != o;
-      if (e <= a.E) offs[e] = v;
-      int before = __shfl_up_sync(0xffffffffu, v, 1);
-      if (lane == 0) before = run;
-      run = __shfl_sync(0xffffffffu, v, 31);
-      // tiles of the experts before e
-      int c = e >= 1 && e <= a.E ? (v - before + NMAX - 1) / NMAX : 0;
-#pragma unroll
-      for (int k = 1; k < 32; k <<= 1) {
-        const int q = __shfl_up_sync(0xffffffffu, c, k);
-        if (lane >= k) c += q;
-      }
-      if (e <= a.E) prefix[e] = tiles + c;
-      tiles += __shfl_sync(0xffffffffu, c, 31);
-    }
-    if (bad) record_status(a.status, kErrBounds);
-  }
+  if (warp == 2 && slot_table(a.offsets, a.E, a.S_max, NMAX, offs, prefix)) record_status(a.status, kErrBounds);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *holder;
   const int mt = a.M / (128 * MW), nkb = a.K / 128;
   const int total = prefix[a.E] * mt;
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return mbar_try_wait(bar, parity) || mbar_wait_bounded(bar, parity, abort_flag, a.status, kDefaultWaitNs);
-  };
-  uint32_t issued = 0, issued_par = 0, sc_issued = 0, sc_par = 0;   // loads in flight, for the end
-  if (warp == 0) {
-    // ------------------------------------------------------------ loads
-    int st = 0, ss = 0;
-    uint32_t sp = 1, scp = 1;
-    bool ok = true;
-    for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
-      const Tile8 t = tile_at(i, prefix, offs, a.E, mt, NMAX);
-      const int npad = max(16, (t.n + 15) & ~15);
-      const int arow = t.e * a.M + t.mt * MW * 128;
-      const int r0 = t.row0 & ~3;
-      const uint32_t sc_bytes = (uint32_t)((t.row0 + t.n - r0 + 3) & ~3) * 4u;
-      for (int kb = 0; kb < nkb; ++kb) {
-        if (lane == 0) ok = wait(&empty[st], sp) && wait(&sc_empty[ss], scp);
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        if (!ok) break;
-        uint8_t* stage = sm + (size_t)st * L.stage_bytes;
-        if (lane == 0) {
-          mbar_expect_tx(&full[st], MW * kABytes + (uint32_t)npad * 128u);
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_for(bar, parity, abort_flag, a.status); };
+  uint32_t issued = 0, issued_par = 0;           // stages with a load in flight, for the end
+  if (warp < 4) {
+    regs_down<56>();
+    if (warp == 0 || warp == 3) {
+      // ---------------------------------------------------------- loads
+      if (lane == 0) {
+        int st = 0;
+        uint32_t sp = 1;
+        bool ok = true;
+        for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+          const Tile8 t = tile_at(i, prefix, offs, a.E, mt, NMAX);
+          const int npad = max(16, (t.n + 15) & ~15);
+          const int arow = t.e * a.M + t.mt * MW * 128;
+          for (int kb = 0; kb < nkb; ++kb) {
+            ok = wait(&empty[st], sp);
+            if (!ok) break;
+            uint8_t* stage = sm + (size_t)st * L.stage_bytes;
+            issued |= 1u << st;
+            issued_par = (issued_par & ~(1u << st)) | (sp ^ 1u) << st;
+            if (warp == 0) {
+              mbar_expect_tx(&full[st], MW * kABytes);
 #pragma unroll
-          for (int h = 0; h < MW; ++h)
-            tma_load_2d(stage + h * kABytes, &tmA, kb * 128, arow + h * 128, &full[st]);
-          mbar_expect_tx(&sc_full[ss], sc_bytes);
-          bulk_load(sm + L.scale_off + ss * L.scale_bytes, a.xscale + (size_t)kb * a.Sp + r0, sc_bytes, &sc_full[ss]);
-        }
-        __syncwarp();
-        for (int b = lane; b < npad / 16; b += 32)
-          tma_load_2d(stage + L.b_off + b * 2048, &tmB, kb * 128, t.row0 + 16 * b, &full[st]);
-        issued |= 1u << st;
-        issued_par = (issued_par & ~(1u << st)) | (sp ^ 1u) << st;
-        sc_issued |= 1u << ss;
-        sc_par = (sc_par & ~(1u << ss)) | (scp ^ 1u) << ss;
-        if (++st == a.stages) {
-          st = 0;
-          sp ^= 1u;
-        }
-        if (++ss == kScaleSlots) {
-          ss = 0;
-          scp ^= 1u;
+              for (int h = 0; h < MW; ++h)
+                tma_load_2d(stage + h * kABytes, &tmA, kb * 128, arow + h * 128, &full[st]);
+            } else {
+              // boxes of 64 rows, and of 16 for the rest
+              mbar_expect_tx(&full[st], (uint32_t)npad * 128u);
+              int r = 0;
+              for (; r + 64 <= npad; r += 64)
+                tma_load_2d(stage + L.b_off + r * 128, &tmB, kb * 128, t.row0 + r, &full[st]);
+              for (; r < npad; r += 16)
+                tma_load_2d(stage + L.b_off + r * 128, &tmB16, kb * 128, t.row0 + r, &full[st]);
+            }
+            if (++st == a.stages) {
+              st = 0;
+              sp ^= 1u;
+            }
+          }
         }
       }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ products
-    if (lane == 0) {
-      int st = 0, slot = 0;
-      uint32_t sp = 0, ap = 1;
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- products
+      if (lane == 0) {
+        int st = 0, slot = 0;
+        uint32_t sp = 0, ap = 1;
+        bool ok = true;
+        // descriptors differ only in the start address (16-byte units, bits 0..13)
+        const uint64_t d0 = smem_desc(smem_u32(sm), 16, 1024, 2);
+        const uint32_t stage16 = L.stage_bytes >> 4, b16 = L.b_off >> 4;
+        for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+          const Tile8 t = tile_at(i, prefix, offs, a.E, mt, NMAX);
+          const uint32_t idesc = idesc_f16(128, max(16, (t.n + 15) & ~15), 0, 0);   // (e4m3 has f16's code 0)
+          for (int kb = 0; kb < nkb && ok; ++kb) {
+            ok = wait(&full[st], sp);
+            const uint64_t ad = d0 + (uint64_t)(st * stage16), bd = ad + b16;
+#pragma unroll
+            for (int h = 0; h < MW; ++h) {
+              if (ok) ok = wait(&acc_empty[slot], ap);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_f8(tmem + slot * NMAX, ad + h * (kABytes >> 4) + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
+              tc_commit(&acc_full[slot]);
+              if (++slot == a.nslots) {
+                slot = 0;
+                ap ^= 1u;
+              }
+            }
+            if (!ok) break;
+            tc_commit(&empty[st]);
+            if (++st == a.stages) {
+              st = 0;
+              sp ^= 1u;
+            }
+          }
+        }
+      }
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------- scales
+      // Copies run kScaleSlots - 1 blocks ahead of their use, over the ends of items; each lane reads what it copied
+      // itself, but for the weight tiles' scales.
+      int li = blockIdx.x, lkb = 0, ls = 0;
+      Tile8 lt = {};
+      if (li < total) lt = tile_at(li, prefix, offs, a.E, mt, NMAX);
+      auto next_copy = [&]() {
+        if (li < total) {
+          const uint32_t dst = smem_u32(sm + L.raw_off) + ls * L.raw_bytes;
+          const float* src = a.xscale + (size_t)lkb * a.Sp + lt.sc0;
+#pragma unroll
+          for (int j = lane; j < NMAX / 4; j += 32)
+            if (4 * j < lt.n) copy16(dst + 16 * j, src + 4 * j);
+          if (lane < MW)
+            copy4(dst + NMAX * 4 + 4 * lane,
+                  a.wscale + ((size_t)lt.e * (a.M / 128) + lt.mt * MW + lane) * nkb + lkb);
+          if (++ls == kScaleSlots) ls = 0;
+          if (++lkb == nkb) {
+            lkb = 0;
+            li += gridDim.x;
+            if (li < total) lt = tile_at(li, prefix, offs, a.E, mt, NMAX);
+          }
+        }
+        copies_commit();
+      };
+      for (int k = 0; k < kScaleSlots - 1; ++k) next_copy();
+      int slot = 0, us = 0;
+      uint32_t ap = 1;
       bool ok = true;
       for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
-        const Tile8 t = tile_at(i, prefix, offs, a.E, mt, NMAX);
-        const uint32_t idesc = idesc_f16(128, max(16, (t.n + 15) & ~15), 0, 0);   // (e4m3 has f16's code 0)
-        for (int kb = 0; kb < nkb && ok; ++kb) {
-          ok = wait(&full[st], sp);
-          const uint32_t s0 = smem_u32(sm + (size_t)st * L.stage_bytes);
-          const uint64_t bd = smem_desc(s0 + L.b_off, 16, 1024, 2);
+        const int n = tile_at(i, prefix, offs, a.E, mt, NMAX).n;
+        for (int kb = 0; kb < nkb; ++kb) {
+          copies_wait<kScaleSlots - 2>();
+          __syncwarp();
+          const uint8_t* raw = sm + L.raw_off + us * L.raw_bytes;
+          if (++us == kScaleSlots) us = 0;
 #pragma unroll
           for (int h = 0; h < MW; ++h) {
-            if (ok) ok = wait(&acc_empty[slot], ap);
+            if (ok) ok = __all_sync(0xffffffffu, wait(&acc_empty[slot], ap));
             if (!ok) break;
-            tc_fence_after();
-            const uint64_t ad = smem_desc(s0 + h * kABytes, 16, 1024, 2);
+            const float w = reinterpret_cast<const float*>(raw)[NMAX + h];
+            float4* to = reinterpret_cast<float4*>(sm + L.scale_off + slot * L.scale_bytes);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f8(tmem + slot * NMAX, ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
-            tc_commit(&acc_full[slot]);
+            for (int j = lane; j < NMAX / 4; j += 32) {
+              const float4 x = reinterpret_cast<const float4*>(raw)[j];
+              if (4 * j < n) to[j] = make_float4(x.x * w, x.y * w, x.z * w, x.w * w);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_full[slot]);
             if (++slot == a.nslots) {
               slot = 0;
               ap ^= 1u;
             }
           }
           if (!ok) break;
-          tc_commit(&empty[st]);
-          if (++st == a.stages) {
-            st = 0;
-            sp ^= 1u;
-          }
+          next_copy();                           // into the ring's place before this one: read, behind __syncwarp
         }
       }
+      copies_wait<0>();
     }
-    __syncwarp();
   } else {
+    regs_up<104>();
     // ------------------------------------------------------------ sums
-    const int q = warp & 3, g = (warp - 2) >> 2;
+    const int q = warp & 3, g = (warp - 4) >> 2;
     const int m = 32 * q + lane;                 // row of the weight tile
-    const uint32_t t0 = tmem + ((uint32_t)(32 * q) << 16) + g * COLS;
-    int slot = 0, ss = 0;
-    uint32_t ap = 0, scp = 0;
+    const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
+    int slot = 0;
+    uint32_t ap = 0;
     bool ok = true;
     int turn = 0;
     // a warp whose wait gives up still meets the others at every item's barrier
     for (int i = blockIdx.x; i < total; i += gridDim.x, turn ^= 1) {
       const Tile8 t = tile_at(i, prefix, offs, a.E, mt, NMAX);
-      const int shift = t.row0 & 3;
-      float acc[MW][C8][8];
+      const int cw = (t.n + 31) >> 5;            // groups of eight columns of each warp of this tile
+      const int col0 = g * cw * 8;
+      float2 acc[MW][C8][4];
 #pragma unroll
       for (int h = 0; h < MW; ++h)
 #pragma unroll
         for (int c = 0; c < C8; ++c)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc[h][c][j] = 0.f;
-      const float* ws = a.wscale + ((size_t)t.e * (a.M / 128) + t.mt * MW) * nkb;
-      float wnext[MW];
-#pragma unroll
-      for (int h = 0; h < MW; ++h) wnext[h] = __ldg(ws + (size_t)h * nkb);
+          for (int j = 0; j < 4; ++j) acc[h][c][j] = make_float2(0.f, 0.f);
       for (int kb = 0; kb < nkb && ok; ++kb) {
-        float w[MW];
-#pragma unroll
-        for (int h = 0; h < MW; ++h) {
-          w[h] = wnext[h];
-          if (kb + 1 < nkb) wnext[h] = __ldg(ws + (size_t)h * nkb + kb + 1);
-        }
-        ok = __all_sync(0xffffffffu, wait(&sc_full[ss], scp));
-        if (!ok) break;
-        const float* sc = reinterpret_cast<const float*>(sm + L.scale_off + ss * L.scale_bytes) + shift + g * COLS;
 #pragma unroll
         for (int h = 0; h < MW; ++h) {
           if (ok) ok = __all_sync(0xffffffffu, wait(&acc_full[slot], ap));
           if (!ok) break;
           tc_fence_after();
-          constexpr int B = C8 % 2 ? 1 : 2;      // loads in flight
+          const float4* sc = reinterpret_cast<const float4*>(sm + L.scale_off + slot * L.scale_bytes) + col0 / 4;
+          constexpr int B = C8 <= 5 ? C8 : C8 == 6 ? 3 : 2;   // loads in flight
 #pragma unroll
           for (int c = 0; c < C8; c += B) {
-            uint32_t v[B][8];
+            if (c < cw) {
+              uint32_t v[B][8];
 #pragma unroll
-            for (int b = 0; b < B; ++b) tmem_ld8(t0 + slot * NMAX + (c + b) * 8, v[b]);
-            tmem_wait<B>(v);
-            if (c + B >= C8) {                   // read: the slot may take the next sum
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&acc_empty[slot]);
+              for (int b = 0; b < B; ++b)
+                if (c + b < C8 && c + b < cw) tmem_ld8(tq + slot * NMAX + col0 + (c + b) * 8, v[b]);
+              tmem_wait<B>(v);
+#pragma unroll
+              for (int b = 0; b < B; ++b)
+                if (c + b < C8 && c + b < cw) {
+#pragma unroll
+                  for (int j = 0; j < 4; j += 2) {
+                    const float4 x = sc[(c + b) * 2 + j / 2];
+                    fma2(acc[h][c + b][j], pair(v[b][2 * j], v[b][2 * j + 1]), make_float2(x.x, x.y));
+                    fma2(acc[h][c + b][j + 1], pair(v[b][2 * j + 2], v[b][2 * j + 3]), make_float2(x.z, x.w));
+                  }
+                }
             }
-#pragma unroll
-            for (int b = 0; b < B; ++b)
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                acc[h][c + b][j] = fmaf(__uint_as_float(v[b][j]), w[h] * sc[(c + b) * 8 + j], acc[h][c + b][j]);
           }
+          tc_fence_before();                     // read: the slot may take the next sum
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[slot]);
           if (++slot == a.nslots) {
             slot = 0;
             ap ^= 1u;
           }
         }
-        __syncwarp();
-        if (lane == 0 && ok) mbar_arrive(&sc_empty[ss]);
-        if (++ss == kScaleSlots) {
-          ss = 0;
-          scp ^= 1u;
-        }
       }
-      const int col0 = g * COLS;
+      auto value = [&](int h, int c, int j) -> float& { return j & 1 ? acc[h][c][j >> 1].y : acc[h][c][j >> 1].x; };
       if constexpr (kGelu) {
         // GeLU, the largest magnitude of each slot's 128 columns (four warps), and 8 bits
         uint32_t* am = reinterpret_cast<uint32_t*>(sm + L.amax_off) + turn * (MW * NMAX * 4);
@@ -489,11 +611,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < MW; ++h)
 #pragma unroll
           for (int c = 0; c < C8; ++c) {
+            if (c >= cw) continue;
             uint32_t keep = 0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              acc[h][c][j] = gelu_tanh(acc[h][c][j]);
-              const uint32_t r = __reduce_max_sync(0xffffffffu, magnitude_bits(acc[h][c][j]));
+              value(h, c, j) = gelu_tanh(value(h, c, j));
+              const uint32_t r = __reduce_max_sync(0xffffffffu, magnitude_bits(value(h, c, j)));
               if (lane == j) keep = r;
             }
             if (lane < 8) am[(h * NMAX + col0 + c * 8 + lane) * 4 + q] = keep;
@@ -505,6 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int mb = t.mt * MW + h;
 #pragma unroll
           for (int c = 0; c < C8; ++c) {
+            if (c >= cw) continue;
 #pragma unroll
             for (int j = 0; j < 8; j += 4) {
               uint32_t u = 0;                    // this lane's values of four slots
@@ -516,9 +640,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const int col = col0 + c * 8 + j + k + p;
                   const uint4 r = *reinterpret_cast<const uint4*>(am + (h * NMAX + col) * 4);
                   fp8_scale(max(max(r.x, r.y), max(r.z, r.w)), scale[p], inv[p]);
-                  if (m == 0 && col < t.n) a.hscale[(size_t)mb * a.Sp + t.row0 + col] = scale[p];
+                  if (m == 0 && col < t.n) a.hscale[(size_t)mb * a.Sp + t.sc0 + col] = scale[p];
                 }
-                u |= fp8_pair(acc[h][c][j + k] * inv[0], acc[h][c][j + k + 1] * inv[1]) << (8 * k);
+                u |= fp8_pair(value(h, c, j + k) * inv[0], value(h, c, j + k + 1) * inv[1]) << (8 * k);
               }
               // four lanes trade bytes: lane 4 i + r gets slot r's values of columns 4 i .. 4 i + 3
               uint32_t o = __shfl_xor_sync(0xffffffffu, u, 1);
@@ -539,16 +663,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int h = 0; h < MW; ++h)
 #pragma unroll
-          for (int c = 0; c < C8; ++c)
+          for (int c = 0; c < C8; ++c) {
+            if (c >= cw) continue;
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
-              const float v0 = acc[h][c][j], v1 = acc[h][c][j + 1];
+              const float v0 = value(h, c, j), v1 = value(h, c, j + 1);
               const float recv = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
               const int col = col0 + c * 8 + j + (odd ? 1 : 0);
               if (col < t.n)
                 *reinterpret_cast<__half2*>(a.out + (size_t)(t.row0 + col) * a.M + ((t.mt * MW + h) * 128 + (m & ~1))) =
                     odd ? __floats2half2_rn(recv, v1) : __floats2half2_rn(v0, recv);
             }
+          }
       }
     }
   }
@@ -558,12 +684,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   if (*abort_flag && lane == 0) {
     // what is still in flight lands before its memory is released (bounded)
-    if (warp == 0) {
+    if (warp == 0 || warp == 3)
       for (int s = 0; s < a.stages; ++s)
         if (issued >> s & 1u) mbar_drain(&full[s], issued_par >> s & 1u);
-      for (int s = 0; s < kScaleSlots; ++s)
-        if (sc_issued >> s & 1u) mbar_drain(&sc_full[s], sc_par >> s & 1u);
-    }
     if (warp == 1) {
       tc_commit(spare);
       mbar_drain(spare, 0);
@@ -580,18 +703,18 @@ int fp8_stages(int nmax, int mw, int E, int smem) {
 }
 
 template <int C8, int MW, bool G>
-cudaError_t launch_one(const CUtensorMap& A, const CUtensorMap& B, Fp8Args a, int sms, int smem, cudaStream_t s) {
+cudaError_t launch_one(const CUtensorMap& A, const CUtensorMap (&B)[2], Fp8Args a, int sms, int smem, cudaStream_t s) {
   auto kern = fp8_gemm_kernel<C8, MW, G>;
   MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
   a.stages = fp8_stages(32 * C8, MW, a.E, smem);
   if (a.stages < 2) return cudaErrorInvalidValue;
   a.nslots = std::min(kMaxSlots, 512 / (32 * C8));
   const size_t bytes = std::max<size_t>(fp8_smem(32 * C8, MW, a.stages, a.E).total, kMinSmem);
-  return launch_k(kern, sms, kThreads, bytes, s, true, A, B, a);
+  return launch_k(kern, sms, kThreads, bytes, s, true, A, B[0], B[1], a);
 }
 
 template <bool G>
-cudaError_t launch_gemm(int c8, const CUtensorMap& A, const CUtensorMap& B, const Fp8Args& a, int sms, int smem,
+cudaError_t launch_gemm(int c8, const CUtensorMap& A, const CUtensorMap (&B)[2], const Fp8Args& a, int sms, int smem,
                         cudaStream_t s) {
   switch (c8) {
     case 1: return launch_one<1, 1, G>(A, B, a, sms, smem, s);
@@ -610,10 +733,10 @@ struct Fp8Ws {
   size_t x, sx, h, sh, total;
   int Sp;
 };
-Fp8Ws fp8_ws(int d, int f, int S_max) {
+Fp8Ws fp8_ws(int d, int f, int E, int S_max) {
   Fp8Ws w;
   const size_t S = std::max(S_max, 1);
-  w.Sp = (int)((S + 3) / 4 * 4);
+  w.Sp = scale_row((int)S, E);
   w.x = 256;                                    // the status word
   w.sx = w.x + up256(S * d);
   w.h = w.sx + up256((size_t)w.Sp * (d / 128) * 4);
@@ -624,7 +747,7 @@ Fp8Ws fp8_ws(int d, int f, int S_max) {
 
 }  // namespace
 
-size_t fp8_ffn_bytes(int d, int f, int S_max) { return fp8_ws(d, f, S_max).total; }
+size_t fp8_ffn_bytes(int d, int f, int E, int S_max) { return fp8_ws(d, f, E, S_max).total; }
 
 cudaError_t launch_fp8_weights(const void* W, bool f16, int E, int K, int N, uint8_t* Wq, float* scales,
                                cudaStream_t s) {
@@ -641,20 +764,21 @@ cudaError_t launch_fp8_ffn(const void* tokens, const int32_t* perm, const int32_
   MOE_LAUNCH(cudaGetDevice(&dev));
   MOE_LAUNCH(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   MOE_LAUNCH(cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev));
-  const Fp8Ws w = fp8_ws(d, f, S_max);
+  const Fp8Ws w = fp8_ws(d, f, E, S_max);
   int* status = reinterpret_cast<int*>(ws);
   MOE_LAUNCH(cudaMemsetAsync(status, 0, sizeof(int), s));
   uint8_t *x = ws + w.x, *h = ws + w.h;
   float *sx = reinterpret_cast<float*>(ws + w.sx), *sh = reinterpret_cast<float*>(ws + w.sh);
-  const long long units = (long long)S_max * (d / 128);
-  MOE_LAUNCH(launch_k(fp8_rows_kernel, (unsigned)std::min<long long>((units + 15) / 16, 8LL * sms), 256, 0, s, false,
-                      static_cast<const __half*>(tokens), perm, offsets, E, S_max, T, d, w.Sp, x, sx, status));
-  // rows per tile: those of an expert that is somewhat fuller than the average one
-  const int rows = (int)std::min<long long>(S_max, (long long)S_max * 5 / (4LL * E) + 8);
+  MOE_LAUNCH(launch_k(fp8_rows_kernel, (unsigned)std::min((S_max + 7) / 8, 8 * sms), 256, (E + 1) * sizeof(int32_t), s,
+                      false, static_cast<const __half*>(tokens), perm, offsets, E, S_max, T, d, w.Sp, x, sx, status));
+  // rows per tile: those of an expert that is two standard deviations fuller than the average one
+  const double mean = (double)S_max / E;
+  const int rows = (int)std::min<double>(S_max, mean + 2.0 * std::sqrt(mean) + 1.0);
   const int c8 = rows <= 32 ? 1 : rows <= 64 ? 2 : rows <= 128 ? 4 : rows <= 160 ? 5 : rows <= 192 ? 6 : 8;
-  CUtensorMap A1, A2, B1, B2;
+  CUtensorMap A1, A2, B1[2], B2[2];
   if (!encode_u8_map(&A1, W1q, d, (uint64_t)E * f, 128, 128) || !encode_u8_map(&A2, W2q, f, (uint64_t)E * d, 128, 128) ||
-      !encode_u8_map(&B1, x, d, S_max, 128, 16) || !encode_u8_map(&B2, h, f, S_max, 128, 16))
+      !encode_u8_map(&B1[0], x, d, S_max, 128, 64) || !encode_u8_map(&B1[1], x, d, S_max, 128, 16) ||
+      !encode_u8_map(&B2[0], h, f, S_max, 128, 64) || !encode_u8_map(&B2[1], h, f, S_max, 128, 16))
     return cudaErrorInvalidValue;
   Fp8Args g;
   memset(&g, 0, sizeof(g));

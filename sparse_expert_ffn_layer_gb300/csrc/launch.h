@@ -207,7 +207,7 @@ struct RouteScore {
   float scale;
 };
 // Experts in 8 bits (fp8.cu).
-size_t fp8_ffn_bytes(int d, int f, int S_max);
+size_t fp8_ffn_bytes(int d, int f, int E, int S_max);
 cudaError_t launch_fp8_weights(const void* W, bool f16, int E, int K, int N, uint8_t* Wq, float* scales,
                                cudaStream_t s);
 cudaError_t launch_fp8_ffn(const void* tokens, const int32_t* perm, const int32_t* offsets, const uint8_t* W1q,
