@@ -232,6 +232,20 @@ bool encode_u8_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t out
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [outer, inner] bytes as {inner, 8, 4, outer / 32}: row 32 g + 4 r + j at {., r, j, g}.  Boxes of 128 rows and 128
+// bytes, swizzled.
+bool encode_weight_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {inner, 8, 4, outer / 32};
+  cuuint64_t strides[3] = {4 * inner, inner, 32 * inner};
+  cuuint32_t box[4] = {128, 8, 4, 4};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace moe
 
 namespace {

@@ -11,8 +11,10 @@
 // four MMAs whose sum goes to a TMEM slot, from where 16 warps add it, times its scale, to the running sums in
 // their registers (column n of a tile has one scale, a weight tile has one for all its rows).  So the sums over
 // blocks are in 32 bits with every scale applied before them, and a slot is free again as soon as it was read.
-// One more warp multiplies the two scales, so that the 16 do one multiply-add a value and no product (which
-// their multiply-add pipes would pay for in each of the four quarters: they bound the kernel then).
+// One more warp multiplies the two scales, so that the 16 do one multiply-add a value.  They read TMEM in the shape
+// in which a lane has two of each eight columns and four rows: with a row of every column a lane, each of the four
+// lane quarters took 128 N bytes of scales from shared memory a block, which with what the MMAs read and the copies
+// write there bound the kernel (N = 160: 1120 cycles a block).
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -23,22 +25,14 @@ namespace moe {
 namespace {
 
 // ---------------------------------------------------------------- values
-// Exponent p of the smallest power of two with amax <= 448 2^p: 448 = 1.75 x 2^8.
-__device__ __forceinline__ int fp8_exp(uint32_t amax_bits) {
-  const int e = (int)(amax_bits >> 23) - 127;
-  return max(-126, e - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0));
-}
-// The scale and its inverse; zero: 1; infinity or NaN: NaN.
+// The smallest power of two 2^p with amax <= 448 2^p, and its inverse (448 = 1.75 x 2^8); zero: 1; infinity or NaN: NaN.
 __device__ __forceinline__ void fp8_scale(uint32_t amax_bits, float& scale, float& inv) {
-  if (amax_bits >= 0x7f800000u) {
-    scale = inv = __uint_as_float(0x7fc00000u);
-  } else if (amax_bits == 0u) {
-    scale = inv = 1.f;
-  } else {
-    const int p = fp8_exp(amax_bits);
-    scale = __uint_as_float((uint32_t)(127 + p) << 23);
-    inv = __uint_as_float((uint32_t)(127 - p) << 23);
-  }
+  // the exponent field of amax, one more above 1.75 (a carry out of the mantissa), less 8
+  const int e = max(1, (int)((amax_bits + 0x1fffffu) >> 23) - 8);
+  scale = __uint_as_float((uint32_t)e << 23);
+  inv = __uint_as_float((uint32_t)(254 - e) << 23);
+  if (amax_bits == 0u) scale = inv = 1.f;
+  if (amax_bits >= 0x7f800000u) scale = inv = __uint_as_float(0x7fc00000u);
 }
 __device__ __forceinline__ uint32_t magnitude_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 // Two values to e4m3, nearest (ties to even): a in the low byte.
@@ -52,8 +46,7 @@ __device__ __forceinline__ uint32_t fp8_four(float a, float b, float c, float d)
 }
 
 // ---------------------------------------------------------------- weights
-__device__ __forceinline__ void load8(const __half* p, float (&f)[8]) {
-  const uint4 r = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack8(const uint4& r, float (&f)[8]) {
   const uint32_t u[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -62,6 +55,7 @@ __device__ __forceinline__ void load8(const __half* p, float (&f)[8]) {
     f[2 * i + 1] = v.y;
   }
 }
+__device__ __forceinline__ void load8(const __half* p, float (&f)[8]) { unpack8(*reinterpret_cast<const uint4*>(p), f); }
 __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
   f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
@@ -165,8 +159,9 @@ __device__ __forceinline__ int scale_base(int first_slot, int e) { return ((firs
 int scale_row(int S_max, int E) { return (S_max + 3) / 4 * 4 + 4 * (E + 1); }
 
 // ---------------------------------------------------------------- rows
-// Slot s of an expert: its token's row in 8 bits.  A warp takes a row, 16 lanes a block of 128 columns.  sx is
-// [d / 128][Sp], a slot's place in it by scale_base.
+// Slot s of an expert: its token's row in 8 bits.  A warp takes eight blocks of 128 columns of a row, 16 lanes each.
+// sx is [d / 128][Sp], a slot's place in it by scale_base.
+constexpr int kRowPart = 8;
 __global__ void __launch_bounds__(256) fp8_rows_kernel(const __half* __restrict__ tokens, const int32_t* __restrict__ perm,
                                                        const int32_t* __restrict__ offsets, int E, int S_max, int T, int d,
                                                        int Sp, uint8_t* __restrict__ Xq, float* __restrict__ sx,
@@ -177,26 +172,31 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const __half* __restrict_
   if (threadIdx.x < 32 && slot_table(offsets, E, S_max, 1, offs, nullptr)) record_status(status, kErrBounds);
   __syncthreads();
   const int lane = threadIdx.x & 31, l = lane & 15, nb = d / 128, S = offs[E];
+  const int parts = (nb + kRowPart - 1) / kRowPart;
+  const long long units = (long long)S * parts;
   bool bad = false;
-  for (int s = blockIdx.x * 8 + (threadIdx.x >> 5); s < S; s += gridDim.x * 8) {
+  for (long long u = blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += (long long)gridDim.x * 8) {
+    const int s = (int)(u / parts), b0 = (int)(u - (long long)s * parts) * kRowPart + (lane >> 4);
     const int t = perm[s];
     const bool in = (unsigned)t < (unsigned)T;
     bad |= !in;
+    const __half* src = tokens + (long long)(in ? t : 0) * d + l * 8;
+    uint4 r[kRowPart / 2];
+#pragma unroll
+    for (int i = 0; i < kRowPart / 2; ++i)
+      r[i] = b0 + 2 * i < nb && in ? *reinterpret_cast<const uint4*>(src + (b0 + 2 * i) * 128) : make_uint4(0u, 0u, 0u, 0u);
     int lo = 0, hi = E;                         // the last e with offs[e] <= s
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (offs[mid] <= s) lo = mid; else hi = mid;
     }
     float* scale_at = sx + scale_base(offs[lo], lo) + (s - offs[lo]);
-    const __half* src = tokens + (long long)(in ? t : 0) * d + l * 8;
     uint8_t* dst = Xq + (long long)s * d + l * 8;
-#pragma unroll 4
-    for (int b0 = 0; b0 < nb; b0 += 2) {
-      const int b = b0 + (lane >> 4);
-      float f[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = 0.f;
-      if (b < nb && in) load8(src + b * 128, f);
+    for (int i = 0; i < kRowPart / 2; ++i) {
+      const int b = b0 + 2 * i;
+      float f[8];
+      unpack8(r[i], f);
       uint32_t m = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) m = max(m, magnitude_bits(f[j]));
@@ -216,37 +216,40 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const __half* __restrict_
 }
 
 // ---------------------------------------------------------------- products
-// Warps 0 to 3 load the weight tiles, issue the products, multiply the scales and load the rows; 16 more add.
-// (One warp for both loads took 600 cycles a block of its own time, and bound the kernel.)
-constexpr int kEpiWarps = 16;                 // four column groups of the four TMEM lane quarters
+// Warps 0 to 3 load the weight tiles, issue the products, multiply the scales and load the rows; eight more add.
+// (One warp for both loads took 600 cycles a block of its own time, and bound the kernel; 16 warps for the sums had
+// too few registers each for two weight tiles.)
+constexpr int kEpiWarps = 8;                  // two column groups of the four TMEM lane quarters
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kABytes = 128 * 128;            // a weight tile: 128 outputs, 128 inputs
-constexpr int kScaleSlots = 16;               // blocks whose scales are on their way
-constexpr int kMaxSlots = 16;
-constexpr int kMaxStages = 16;
+constexpr int kScaleSlots = 8;                // blocks whose scales are on their way
+constexpr int kMaxSlots = 16;                 // sums in TMEM
+constexpr int kMaxStages = 12;                // of either ring
 constexpr size_t kMinSmem = 116 * 1024;       // one block per SM: each takes all of TMEM
-
+// Weight tiles and rows have rings of their own: na tiles of 16 KB, nb runs of nmax rows.
 struct Fp8Smem {
-  uint32_t stage_bytes, b_off, raw_off, raw_bytes, scale_off, scale_bytes, amax_off, bars_off, misc_off, total;
+  uint32_t b_off, b_bytes, raw_off, raw_bytes, scale_off, scale_bytes, amax_off, bars_off, misc_off, total;
 };
-__host__ __device__ inline Fp8Smem fp8_smem(int nmax, int mw, int stages, int E) {
+__host__ __device__ inline Fp8Smem fp8_smem(int nmax, int na, int nb, int E) {
   Fp8Smem L;
-  L.b_off = (uint32_t)mw * kABytes;
-  L.stage_bytes = L.b_off + (uint32_t)nmax * 128u;
-  uint32_t off = (uint32_t)stages * L.stage_bytes;
+  uint32_t off = (uint32_t)(na * kABytes);
+  L.b_off = off;
+  L.b_bytes = (uint32_t)nmax * 128u;
+  off += (uint32_t)nb * L.b_bytes;
   L.raw_off = off;                            // the rows' scales of a block, and the weight tiles'
   L.raw_bytes = (uint32_t)nmax * 4u + 16u;
   off += kScaleSlots * L.raw_bytes;
   L.scale_off = off;                          // their products, for each sum's slot
   L.scale_bytes = (uint32_t)nmax * 4u;
-  off += kMaxSlots * L.scale_bytes;
+  const uint32_t slots = 512u / (uint32_t)nmax;
+  off += (slots < kMaxSlots ? slots : kMaxSlots) * L.scale_bytes;
   L.amax_off = off;
-  off += 2u * (uint32_t)(mw * nmax) * 16u;    // two items' [column][lane quarter]
+  off += 2u * (uint32_t)nmax * 16u;    // two items' [column][lane quarter]
   L.bars_off = off;
-  off += (2u * kMaxStages + 2u * kMaxSlots + 1u) * 8u + 8u;
+  off += (4u * kMaxStages + 2u * kMaxSlots + 1u) * 8u + 8u;
   L.misc_off = off;
   off += 16u + 8u * (uint32_t)(E + 1);
-  L.total = off + 1024u;                      // slack for the alignment of the stages
+  L.total = off + 1024u;                      // slack for the alignment of the rings
   return L;
 }
 
@@ -254,7 +257,7 @@ struct Fp8Args {
   const int32_t* offsets;
   const float* wscale;         // [E][M / 128][K / 128]
   const float* xscale;         // [K / 128][Sp]
-  int E, S_max, Sp, K, M, stages, nslots;
+  int E, S_max, Sp, K, M, na, nb, nslots;
   uint8_t* h;                  // first product: [S_max][M], with hscale [M / 128][Sp]
   float* hscale;
   __half* out;                 // second: [S_max][M]
@@ -268,19 +271,59 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// 32 lanes x 8 columns; the values are valid after tmem_wait.
-__device__ __forceinline__ void tmem_ld8(uint32_t t, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(t));
+// 16 lanes x 8 X columns: of each eight columns lane l gets columns 2 (l % 4) and the next of rows l / 4 (r[0], r[1])
+// and l / 4 + 8.  Valid after tmem_wait.
+template <int X>
+__device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t* r) {
+  if constexpr (X == 4)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(t));
+  else if constexpr (X == 2)
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(t));
+  else
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(t));
+}
+// All 32 lanes of a quarter, B groups of eight columns: v[half][4 b ..].
+template <int B>
+__device__ __forceinline__ void tmem_ld32(uint32_t t, uint32_t (&v)[2][4 * B]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t at = t + ((uint32_t)(16 * h) << 16);
+#pragma unroll
+    for (int b = 0; b + 4 <= B; b += 4) tmem_ld16<4>(at + 8 * b, v[h] + 4 * b);
+    if constexpr (B % 4 >= 2) tmem_ld16<2>(at + 8 * (B / 4 * 4), v[h] + 16 * (B / 4));
+    if constexpr (B % 2) tmem_ld16<1>(at + 8 * (B - 1), v[h] + 4 * (B - 1));
+  }
 }
 template <int B>
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[B][8]) {
+__device__ __forceinline__ void tmem_wait(uint32_t (&v)[2][4 * B]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int b = 0; b < B; ++b)
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) asm volatile("" : "+r"(r[b][i]));   // no use of them moves above the wait
+    for (int i = 0; i < 4 * B; ++i) asm volatile("" : "+r"(v[h][i]));   // no use of them moves above the wait
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+// The 128 rows of a weight tile, in each 32 of them rows 4 r + j at place 8 j + r: a lane's four TMEM rows of a
+// column (r + 8 j) then are four neighbouring outputs, and leave as one store.
+__device__ __forceinline__ void load_weight_tile(void* smem, const CUtensorMap* m, int x, int group, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(smem)),
+      "l"(m), "r"(x), "r"(0), "r"(0), "r"(group), "r"(smem_u32(bar))
+      : "memory");
 }
 // 4 and 16 bytes global -> shared, by the thread itself.
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
@@ -331,12 +374,17 @@ __device__ __forceinline__ void fma2(float2& d, float2 a, float2 b) {
   d = float2_of(r);
 }
 
+// The rows by boxes of 128, 64 and 32 of them.
+struct RowMaps {
+  CUtensorMap box[3];
+};
+
 struct Tile8 {
   int e, row0, n, mt;
   int sc0;                                    // its first slot's place in a row of scales
 };
-// Item i: an expert, MW neighbouring weight tiles and a run of its rows; the runs of one weight tile are next to
-// each other, on different SMs at the same time, and share it in L2.
+// Item i: an expert, a weight tile and a run of its rows; the runs of one weight tile are next to each other, on
+// different SMs at the same time, and share it in L2.
 __device__ __forceinline__ Tile8 tile_at(int i, const int32_t* prefix, const int32_t* offs, int E, int mt, int nmax) {
   int lo = 0, hi = E;                         // largest e with prefix[e] mt <= i
   while (hi - lo > 1) {
@@ -356,28 +404,31 @@ __device__ __forceinline__ Tile8 tile_at(int i, const int32_t* prefix, const int
   return t;
 }
 
-// C8: groups of eight columns per warp (a tile has up to 32 C8 rows); MW: weight tiles per item, all multiplied
-// with one load of the rows.  kGelu: first product.
-template <int C8, int MW, bool kGelu>
+// C8: groups of eight columns per warp (a tile has up to 16 C8 rows).  kGelu: first product.
+template <int C8, bool kGelu>
 __global__ void __launch_bounds__(kThreads, 1)
-    fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                    const __grid_constant__ CUtensorMap tmB16, const Fp8Args a) {
-  constexpr int NMAX = 32 * C8;
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ RowMaps tmB, const Fp8Args a) {
+  constexpr int NMAX = 16 * C8, B = C8 > 12 ? 8 : C8;   // groups in flight: as many as registers are left for
+  static_assert(C8 % B == 0);
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  const Fp8Smem L = fp8_smem(NMAX, MW, a.stages, a.E);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + L.bars_off);
-  uint64_t *empty = full + kMaxStages, *acc_full = empty + kMaxStages, *acc_empty = acc_full + kMaxSlots,
-           *spare = acc_empty + kMaxSlots;
+  const Fp8Smem L = fp8_smem(NMAX, a.na, a.nb, a.E);
+  uint64_t* a_full = reinterpret_cast<uint64_t*>(sm + L.bars_off);
+  uint64_t *a_empty = a_full + kMaxStages, *b_full = a_empty + kMaxStages, *b_empty = b_full + kMaxStages,
+           *acc_full = b_empty + kMaxStages, *acc_empty = acc_full + kMaxSlots, *spare = acc_empty + kMaxSlots;
   uint32_t* holder = reinterpret_cast<uint32_t*>(sm + L.misc_off);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L.misc_off + 4);
   int32_t* prefix = reinterpret_cast<int32_t*>(sm + L.misc_off + 16);
   int32_t* offs = prefix + a.E + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < a.stages; ++s) {
-      mbar_init(&full[s], 2);                   // weights and rows
-      mbar_init(&empty[s], 1);
+    for (int s = 0; s < a.na; ++s) {
+      mbar_init(&a_full[s], 1);
+      mbar_init(&a_empty[s], 1);
+    }
+    for (int s = 0; s < a.nb; ++s) {
+      mbar_init(&b_full[s], 1);
+      mbar_init(&b_empty[s], 1);
     }
     for (int s = 0; s < a.nslots; ++s) {
       mbar_init(&acc_full[s], 2);               // the sum and its scales
@@ -387,11 +438,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 0 && lane == 0) {
-    prefetch_tmap(&tmA);
-    prefetch_tmap(&tmB);
-    prefetch_tmap(&tmB16);
-  }
+  if (warp == 0 && lane == 0) prefetch_tmap(&tmA);
+  if (warp == 3 && lane < 3) prefetch_tmap(&tmB.box[lane]);
   if (warp == 1) tmem_alloc(holder, 512);
   pdl_wait();
   pdl_trigger();
@@ -400,89 +448,110 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *holder;
-  const int mt = a.M / (128 * MW), nkb = a.K / 128;
+  const int mt = a.M / 128, nkb = a.K / 128;
   const int total = prefix[a.E] * mt;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_for(bar, parity, abort_flag, a.status); };
-  uint32_t issued = 0, issued_par = 0;           // stages with a load in flight, for the end
+  uint32_t issued = 0, issued_par = 0;           // ring places with a load in flight, for the end
+  auto note = [&](int at, uint32_t par) {
+    issued |= 1u << at;
+    issued_par = (issued_par & ~(1u << at)) | par << at;
+  };
   if (warp < 4) {
     regs_down<56>();
-    if (warp == 0 || warp == 3) {
-      // ---------------------------------------------------------- loads
-      if (lane == 0) {
-        int st = 0;
-        uint32_t sp = 1;
-        bool ok = true;
-        for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
-          const Tile8 t = tile_at(i, prefix, offs, a.E, mt, NMAX);
-          const int npad = max(16, (t.n + 15) & ~15);
-          const int arow = t.e * a.M + t.mt * MW * 128;
-          for (int kb = 0; kb < nkb; ++kb) {
-            ok = wait(&empty[st], sp);
-            if (!ok) break;
-            uint8_t* stage = sm + (size_t)st * L.stage_bytes;
-            issued |= 1u << st;
-            issued_par = (issued_par & ~(1u << st)) | (sp ^ 1u) << st;
-            if (warp == 0) {
-              mbar_expect_tx(&full[st], MW * kABytes);
-#pragma unroll
-              for (int h = 0; h < MW; ++h)
-                tma_load_2d(stage + h * kABytes, &tmA, kb * 128, arow + h * 128, &full[st]);
-            } else {
-              // boxes of 64 rows, and of 16 for the rest
-              mbar_expect_tx(&full[st], (uint32_t)npad * 128u);
-              int r = 0;
-              for (; r + 64 <= npad; r += 64)
-                tma_load_2d(stage + L.b_off + r * 128, &tmB, kb * 128, t.row0 + r, &full[st]);
-              for (; r < npad; r += 16)
-                tma_load_2d(stage + L.b_off + r * 128, &tmB16, kb * 128, t.row0 + r, &full[st]);
-            }
-            if (++st == a.stages) {
-              st = 0;
-              sp ^= 1u;
-            }
+    if (warp == 0) {
+      // ---------------------------------------------------------- weight tiles
+      // (These three loops are run by whole warps, and one lane issues: their values stay uniform, and a block takes
+      // half the time that it takes a lane alone.)
+      int st = 0;
+      uint32_t sp = 1;
+      bool ok = true;
+      for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+        const Tile8 t = tile_at(i, prefix, offs, a.E, mt, NMAX);
+        const int agroup = t.e * (a.M / 32) + t.mt * 4;
+        for (int kb = 0; kb < nkb; ++kb) {
+          ok = __all_sync(0xffffffffu, wait(&a_empty[st], sp));
+          if (!ok) break;
+          note(st, sp ^ 1u);
+          if (elect_one()) {
+            mbar_expect_tx(&a_full[st], kABytes);
+            load_weight_tile(sm + st * kABytes, &tmA, kb * 128, agroup, &a_full[st]);
+          }
+          if (++st == a.na) {
+            st = 0;
+            sp ^= 1u;
           }
         }
       }
-      __syncwarp();
+    } else if (warp == 3) {
+      // ---------------------------------------------------------- rows
+      int st = 0;
+      uint32_t sp = 1;
+      bool ok = true;
+      for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+        const Tile8 t = tile_at(i, prefix, offs, a.E, mt, NMAX);
+        const int rows = (t.n + 31) & ~31;
+        for (int kb = 0; kb < nkb; ++kb) {
+          ok = __all_sync(0xffffffffu, wait(&b_empty[st], sp));
+          if (!ok) break;
+          note(st, sp ^ 1u);
+          uint8_t* to = sm + L.b_off + st * L.b_bytes;
+          if (elect_one()) {
+            mbar_expect_tx(&b_full[st], (uint32_t)rows * 128u);
+            int r = 0;
+            if constexpr (NMAX >= 128)
+              for (; r + 128 <= rows; r += 128) tma_load_2d(to + r * 128, &tmB.box[0], kb * 128, t.row0 + r, &b_full[st]);
+            if constexpr (NMAX >= 64)
+              if (rows - r >= 64) {
+                tma_load_2d(to + r * 128, &tmB.box[1], kb * 128, t.row0 + r, &b_full[st]);
+                r += 64;
+              }
+            if (r < rows) tma_load_2d(to + r * 128, &tmB.box[2], kb * 128, t.row0 + r, &b_full[st]);
+          }
+          if (++st == a.nb) {
+            st = 0;
+            sp ^= 1u;
+          }
+        }
+      }
     } else if (warp == 1) {
       // ---------------------------------------------------------- products
-      if (lane == 0) {
-        int st = 0, slot = 0;
-        uint32_t sp = 0, ap = 1;
-        bool ok = true;
-        // descriptors differ only in the start address (16-byte units, bits 0..13)
-        const uint64_t d0 = smem_desc(smem_u32(sm), 16, 1024, 2);
-        const uint32_t stage16 = L.stage_bytes >> 4, b16 = L.b_off >> 4;
-        for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
-          const Tile8 t = tile_at(i, prefix, offs, a.E, mt, NMAX);
-          const uint32_t idesc = idesc_f16(128, max(16, (t.n + 15) & ~15), 0, 0);   // (e4m3 has f16's code 0)
-          for (int kb = 0; kb < nkb && ok; ++kb) {
-            ok = wait(&full[st], sp);
-            const uint64_t ad = d0 + (uint64_t)(st * stage16), bd = ad + b16;
+      int as = 0, bs = 0, slot = 0;
+      uint32_t asp = 0, bsp = 0, ap = 1;
+      bool ok = true;
+      // descriptors differ only in the start address (16-byte units, bits 0..13)
+      const uint64_t d0 = smem_desc(smem_u32(sm), 16, 1024, 2);
+      const uint32_t b0 = L.b_off >> 4, b16 = L.b_bytes >> 4;
+      for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+        const Tile8 t = tile_at(i, prefix, offs, a.E, mt, NMAX);
+        const uint32_t idesc = idesc_f16(128, (t.n + 15) & ~15, 0, 0);   // (e4m3 has f16's code 0)
+        for (int kb = 0; kb < nkb; ++kb) {
+          // rows, weight tile and a free slot: a lane waits for each
+          uint64_t* bar = lane == 0 ? &b_full[bs] : lane == 1 ? &a_full[as] : &acc_empty[slot];
+          ok = __all_sync(0xffffffffu, wait(bar, lane == 0 ? bsp : lane == 1 ? asp : ap));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t ad = d0 + (uint64_t)(as * (kABytes >> 4)), bd = d0 + (uint64_t)(b0 + bs * b16);
+          if (elect_one()) {
 #pragma unroll
-            for (int h = 0; h < MW; ++h) {
-              if (ok) ok = wait(&acc_empty[slot], ap);
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_f8(tmem + slot * NMAX, ad + h * (kABytes >> 4) + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
-              tc_commit(&acc_full[slot]);
-              if (++slot == a.nslots) {
-                slot = 0;
-                ap ^= 1u;
-              }
-            }
-            if (!ok) break;
-            tc_commit(&empty[st]);
-            if (++st == a.stages) {
-              st = 0;
-              sp ^= 1u;
-            }
+            for (int k = 0; k < 4; ++k) mma_f8(tmem + slot * NMAX, ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
+            tc_commit(&acc_full[slot]);
+            tc_commit(&a_empty[as]);
+            tc_commit(&b_empty[bs]);
+          }
+          if (++slot == a.nslots) {
+            slot = 0;
+            ap ^= 1u;
+          }
+          if (++as == a.na) {
+            as = 0;
+            asp ^= 1u;
+          }
+          if (++bs == a.nb) {
+            bs = 0;
+            bsp ^= 1u;
           }
         }
       }
-      __syncwarp();
     } else {
       // ---------------------------------------------------------- scales
       // Copies run kScaleSlots - 1 blocks ahead of their use, over the ends of items; each lane reads what it copied
@@ -497,9 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = lane; j < NMAX / 4; j += 32)
             if (4 * j < lt.n) copy16(dst + 16 * j, src + 4 * j);
-          if (lane < MW)
-            copy4(dst + NMAX * 4 + 4 * lane,
-                  a.wscale + ((size_t)lt.e * (a.M / 128) + lt.mt * MW + lane) * nkb + lkb);
+          if (lane == 0) copy4(dst + NMAX * 4, a.wscale + ((size_t)lt.e * mt + lt.mt) * nkb + lkb);
           if (++ls == kScaleSlots) ls = 0;
           if (++lkb == nkb) {
             lkb = 0;
@@ -520,35 +587,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           const uint8_t* raw = sm + L.raw_off + us * L.raw_bytes;
           if (++us == kScaleSlots) us = 0;
-#pragma unroll
-          for (int h = 0; h < MW; ++h) {
-            if (ok) ok = __all_sync(0xffffffffu, wait(&acc_empty[slot], ap));
-            if (!ok) break;
-            const float w = reinterpret_cast<const float*>(raw)[NMAX + h];
-            float4* to = reinterpret_cast<float4*>(sm + L.scale_off + slot * L.scale_bytes);
-#pragma unroll
-            for (int j = lane; j < NMAX / 4; j += 32) {
-              const float4 x = reinterpret_cast<const float4*>(raw)[j];
-              if (4 * j < n) to[j] = make_float4(x.x * w, x.y * w, x.z * w, x.w * w);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_full[slot]);
-            if (++slot == a.nslots) {
-              slot = 0;
-              ap ^= 1u;
-            }
-          }
+          ok = __all_sync(0xffffffffu, wait(&acc_empty[slot], ap));
           if (!ok) break;
+          const float w = reinterpret_cast<const float*>(raw)[NMAX];
+          float4* to = reinterpret_cast<float4*>(sm + L.scale_off + slot * L.scale_bytes);
+#pragma unroll
+          for (int j = lane; j < NMAX / 4; j += 32) {
+            const float4 x = reinterpret_cast<const float4*>(raw)[j];
+            if (4 * j < n) to[j] = make_float4(x.x * w, x.y * w, x.z * w, x.w * w);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_full[slot]);
+          if (++slot == a.nslots) {
+            slot = 0;
+            ap ^= 1u;
+          }
           next_copy();                           // into the ring's place before this one: read, behind __syncwarp
         }
       }
       copies_wait<0>();
     }
   } else {
-    regs_up<104>();
+    regs_up<224>();
     // ------------------------------------------------------------ sums
     const int q = warp & 3, g = (warp - 4) >> 2;
-    const int m = 32 * q + lane;                 // row of the weight tile
+    const int lr = lane >> 2, lc = 2 * (lane & 3);   // TMEM rows lr + 8 j of the quarter's 32, columns lc, lc + 1 of eight
     const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
     int slot = 0;
     uint32_t ap = 0;
@@ -557,124 +620,106 @@ __global__ void __launch_bounds__(kThreads, 1)
     // a warp whose wait gives up still meets the others at every item's barrier
     for (int i = blockIdx.x; i < total; i += gridDim.x, turn ^= 1) {
       const Tile8 t = tile_at(i, prefix, offs, a.E, mt, NMAX);
-      const int cw = (t.n + 31) >> 5;            // groups of eight columns of each warp of this tile
+      const int cw = (t.n + 15) >> 4;            // groups of eight columns of each warp of this tile
       const int col0 = g * cw * 8;
-      float2 acc[MW][C8][4];
+      float2 acc[C8][4];
 #pragma unroll
-      for (int h = 0; h < MW; ++h)
+      for (int c = 0; c < C8; ++c)
 #pragma unroll
-        for (int c = 0; c < C8; ++c)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[h][c][j] = make_float2(0.f, 0.f);
+        for (int j = 0; j < 4; ++j) acc[c][j] = make_float2(0.f, 0.f);
       for (int kb = 0; kb < nkb && ok; ++kb) {
+        ok = __all_sync(0xffffffffu, wait(&acc_full[slot], ap));
+        if (!ok) break;
+        tc_fence_after();
+        const float* sc = reinterpret_cast<const float*>(sm + L.scale_off + slot * L.scale_bytes) + col0 + lc;
+        const uint32_t ts = tq + slot * NMAX + col0;
+        // (what is loaded beyond the tile's columns stays within the slot, and is not used)
 #pragma unroll
-        for (int h = 0; h < MW; ++h) {
-          if (ok) ok = __all_sync(0xffffffffu, wait(&acc_full[slot], ap));
-          if (!ok) break;
-          tc_fence_after();
-          const float4* sc = reinterpret_cast<const float4*>(sm + L.scale_off + slot * L.scale_bytes) + col0 / 4;
-          constexpr int B = C8 <= 5 ? C8 : C8 == 6 ? 3 : 2;   // loads in flight
+        for (int c = 0; c < C8; c += B) {
+          if (c < cw) {
+            uint32_t v[2][4 * B];
+            float2 x[B];
+            tmem_ld32<B>(ts + c * 8, v);
 #pragma unroll
-          for (int c = 0; c < C8; c += B) {
-            if (c < cw) {
-              uint32_t v[B][8];
+            for (int b = 0; b < B; ++b) x[b] = *reinterpret_cast<const float2*>(sc + (c + b) * 8);
+            tmem_wait<B>(v);
 #pragma unroll
-              for (int b = 0; b < B; ++b)
-                if (c + b < C8 && c + b < cw) tmem_ld8(tq + slot * NMAX + col0 + (c + b) * 8, v[b]);
-              tmem_wait<B>(v);
+            for (int b = 0; b < B; ++b)
 #pragma unroll
-              for (int b = 0; b < B; ++b)
-                if (c + b < C8 && c + b < cw) {
-#pragma unroll
-                  for (int j = 0; j < 4; j += 2) {
-                    const float4 x = sc[(c + b) * 2 + j / 2];
-                    fma2(acc[h][c + b][j], pair(v[b][2 * j], v[b][2 * j + 1]), make_float2(x.x, x.y));
-                    fma2(acc[h][c + b][j + 1], pair(v[b][2 * j + 2], v[b][2 * j + 3]), make_float2(x.z, x.w));
-                  }
-                }
-            }
-          }
-          tc_fence_before();                     // read: the slot may take the next sum
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[slot]);
-          if (++slot == a.nslots) {
-            slot = 0;
-            ap ^= 1u;
+              for (int j = 0; j < 4; ++j)
+                fma2(acc[c + b][j], pair(v[j >> 1][4 * b + 2 * (j & 1)], v[j >> 1][4 * b + 2 * (j & 1) + 1]), x[b]);
           }
         }
+        tc_fence_before();                       // read: the slot may take the next sum
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[slot]);
+        if (++slot == a.nslots) {
+          slot = 0;
+          ap ^= 1u;
+        }
       }
-      auto value = [&](int h, int c, int j) -> float& { return j & 1 ? acc[h][c][j >> 1].y : acc[h][c][j >> 1].x; };
+      const size_t tile0 = (size_t)t.row0 * a.M + t.mt * 128 + 32 * q + 4 * lr;   // this lane's four outputs of a slot
       if constexpr (kGelu) {
         // GeLU, the largest magnitude of each slot's 128 columns (four warps), and 8 bits
-        uint32_t* am = reinterpret_cast<uint32_t*>(sm + L.amax_off) + turn * (MW * NMAX * 4);
+        uint32_t* am = reinterpret_cast<uint32_t*>(sm + L.amax_off) + turn * (NMAX * 4);
 #pragma unroll
-        for (int h = 0; h < MW; ++h)
+        for (int c = 0; c < C8; ++c) {
+          if (c >= cw) continue;
+          uint32_t m0 = 0, m1 = 0;
 #pragma unroll
-          for (int c = 0; c < C8; ++c) {
-            if (c >= cw) continue;
-            uint32_t keep = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              value(h, c, j) = gelu_tanh(value(h, c, j));
-              const uint32_t r = __reduce_max_sync(0xffffffffu, magnitude_bits(value(h, c, j)));
-              if (lane == j) keep = r;
-            }
-            if (lane < 8) am[(h * NMAX + col0 + c * 8 + lane) * 4 + q] = keep;
+          for (int j = 0; j < 4; ++j) {
+            float2& v = acc[c][j];
+            v = make_float2(gelu_tanh(v.x), gelu_tanh(v.y));
+            m0 = max(m0, magnitude_bits(v.x));
+            m1 = max(m1, magnitude_bits(v.y));
           }
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+            m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+          }
+          if (lr == 0) {
+            am[(col0 + c * 8 + lc) * 4 + q] = m0;
+            am[(col0 + c * 8 + lc + 1) * 4 + q] = m1;
+          }
+        }
         asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
         if (!ok) continue;
 #pragma unroll
-        for (int h = 0; h < MW; ++h) {
-          const int mb = t.mt * MW + h;
+        for (int c = 0; c < C8; ++c) {
+          if (c >= cw) continue;
 #pragma unroll
-          for (int c = 0; c < C8; ++c) {
-            if (c >= cw) continue;
-#pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-              uint32_t u = 0;                    // this lane's values of four slots
-#pragma unroll
-              for (int k = 0; k < 4; k += 2) {
-                float inv[2], scale[2];
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                  const int col = col0 + c * 8 + j + k + p;
-                  const uint4 r = *reinterpret_cast<const uint4*>(am + (h * NMAX + col) * 4);
-                  fp8_scale(max(max(r.x, r.y), max(r.z, r.w)), scale[p], inv[p]);
-                  if (m == 0 && col < t.n) a.hscale[(size_t)mb * a.Sp + t.sc0 + col] = scale[p];
-                }
-                u |= fp8_pair(value(h, c, j + k) * inv[0], value(h, c, j + k + 1) * inv[1]) << (8 * k);
-              }
-              // four lanes trade bytes: lane 4 i + r gets slot r's values of columns 4 i .. 4 i + 3
-              uint32_t o = __shfl_xor_sync(0xffffffffu, u, 1);
-              u = (lane & 1) ? __byte_perm(u, o, 0x3715) : __byte_perm(u, o, 0x6240);
-              o = __shfl_xor_sync(0xffffffffu, u, 2);
-              u = (lane & 2) ? __byte_perm(u, o, 0x3276) : __byte_perm(u, o, 0x5410);
-              const int col = col0 + c * 8 + j + (lane & 3);
-              if (col < t.n)
-                *reinterpret_cast<uint32_t*>(a.h + (size_t)(t.row0 + col) * a.M + mb * 128 + (m & ~3)) = u;
+          for (int p = 0; p < 2; ++p) {
+            const int col = col0 + c * 8 + lc + p;
+            const uint4 r = *reinterpret_cast<const uint4*>(am + col * 4);
+            float scale, inv;
+            fp8_scale(max(max(r.x, r.y), max(r.z, r.w)), scale, inv);
+            if (col < t.n) {
+              if (q == 0 && lr == 0) a.hscale[(size_t)t.mt * a.Sp + t.sc0 + col] = scale;
+              const float2 (&v)[4] = acc[c];
+              *reinterpret_cast<uint32_t*>(a.h + tile0 + (size_t)col * a.M) =
+                  p ? fp8_four(v[0].y * inv, v[1].y * inv, v[2].y * inv, v[3].y * inv)
+                    : fp8_four(v[0].x * inv, v[1].x * inv, v[2].x * inv, v[3].x * inv);
             }
           }
         }
       } else {
         if (!ok) continue;
-        // two columns per 4-byte store: lanes 2 i and 2 i + 1 hold columns m and m + 1; for a pair of slots
-        // the even lane stores the first, the odd lane the second
-        const bool odd = lane & 1;
 #pragma unroll
-        for (int h = 0; h < MW; ++h)
+        for (int c = 0; c < C8; ++c) {
+          if (c >= cw) continue;
 #pragma unroll
-          for (int c = 0; c < C8; ++c) {
-            if (c >= cw) continue;
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              const float v0 = value(h, c, j), v1 = value(h, c, j + 1);
-              const float recv = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-              const int col = col0 + c * 8 + j + (odd ? 1 : 0);
-              if (col < t.n)
-                *reinterpret_cast<__half2*>(a.out + (size_t)(t.row0 + col) * a.M + ((t.mt * MW + h) * 128 + (m & ~1))) =
-                    odd ? __floats2half2_rn(recv, v1) : __floats2half2_rn(v0, recv);
+          for (int p = 0; p < 2; ++p) {
+            const int col = col0 + c * 8 + lc + p;
+            if (col < t.n) {
+              const float2 (&v)[4] = acc[c];
+              const __half2 lo = p ? __floats2half2_rn(v[0].y, v[1].y) : __floats2half2_rn(v[0].x, v[1].x);
+              const __half2 hi = p ? __floats2half2_rn(v[2].y, v[3].y) : __floats2half2_rn(v[2].x, v[3].x);
+              *reinterpret_cast<uint2*>(a.out + tile0 + (size_t)col * a.M) =
+                  make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
             }
           }
+        }
       }
     }
   }
@@ -682,47 +727,51 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (*abort_flag && lane == 0) {
+  if (*abort_flag) {
     // what is still in flight lands before its memory is released (bounded)
-    if (warp == 0 || warp == 3)
-      for (int s = 0; s < a.stages; ++s)
-        if (issued >> s & 1u) mbar_drain(&full[s], issued_par >> s & 1u);
+    if ((warp == 0 || warp == 3) && lane == 0) {
+      uint64_t* bars = warp == 0 ? a_full : b_full;
+      for (int s = 0; s < kMaxStages; ++s)
+        if (issued >> s & 1u) mbar_drain(&bars[s], issued_par >> s & 1u);
+    }
     if (warp == 1) {
-      tc_commit(spare);
-      mbar_drain(spare, 0);
+      if (elect_one()) tc_commit(spare);         // (the lane that issued the products)
+      __syncwarp();
+      if (lane == 0) mbar_drain(spare, 0);
     }
   }
   __syncwarp();
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-int fp8_stages(int nmax, int mw, int E, int smem) {
-  for (int st = kMaxStages; st >= 2; --st)
-    if ((int)fp8_smem(nmax, mw, st, E).total <= smem) return st;
-  return 0;
+// Ring lengths: as many runs of rows as fit beside as many weight tiles (at most kMaxStages), the rest for weight tiles.
+bool fp8_rings(int nmax, int E, int smem, int* na, int* nb) {
+  const int fixed = (int)fp8_smem(nmax, 0, 0, E).total, row_bytes = nmax * 128;
+  *nb = std::min(kMaxStages, (smem - fixed) / (kABytes + row_bytes));
+  *na = std::min(kMaxStages, (smem - fixed - *nb * row_bytes) / kABytes);
+  return *nb >= 2;
 }
 
-template <int C8, int MW, bool G>
-cudaError_t launch_one(const CUtensorMap& A, const CUtensorMap (&B)[2], Fp8Args a, int sms, int smem, cudaStream_t s) {
-  auto kern = fp8_gemm_kernel<C8, MW, G>;
+template <int C8, bool G>
+cudaError_t launch_one(const CUtensorMap& A, const RowMaps& B, Fp8Args a, int sms, int smem, cudaStream_t s) {
+  auto kern = fp8_gemm_kernel<C8, G>;
   MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
-  a.stages = fp8_stages(32 * C8, MW, a.E, smem);
-  if (a.stages < 2) return cudaErrorInvalidValue;
-  a.nslots = std::min(kMaxSlots, 512 / (32 * C8));
-  const size_t bytes = std::max<size_t>(fp8_smem(32 * C8, MW, a.stages, a.E).total, kMinSmem);
-  return launch_k(kern, sms, kThreads, bytes, s, true, A, B[0], B[1], a);
+  if (!fp8_rings(16 * C8, a.E, smem, &a.na, &a.nb)) return cudaErrorInvalidValue;
+  a.nslots = std::min(kMaxSlots, 512 / (16 * C8));
+  const size_t bytes = std::max<size_t>(fp8_smem(16 * C8, a.na, a.nb, a.E).total, kMinSmem);
+  return launch_k(kern, sms, kThreads, bytes, s, true, A, B, a);
 }
 
 template <bool G>
-cudaError_t launch_gemm(int c8, const CUtensorMap& A, const CUtensorMap (&B)[2], const Fp8Args& a, int sms, int smem,
+cudaError_t launch_gemm(int c8, const CUtensorMap& A, const RowMaps& B, const Fp8Args& a, int sms, int smem,
                         cudaStream_t s) {
   switch (c8) {
-    case 1: return launch_one<1, 1, G>(A, B, a, sms, smem, s);
-    case 2: return launch_one<2, 1, G>(A, B, a, sms, smem, s);
-    case 4: return launch_one<4, 1, G>(A, B, a, sms, smem, s);
-    case 5: return launch_one<5, 1, G>(A, B, a, sms, smem, s);
-    case 6: return launch_one<6, 1, G>(A, B, a, sms, smem, s);
-    case 8: return launch_one<8, 1, G>(A, B, a, sms, smem, s);
+    case 2: return launch_one<2, G>(A, B, a, sms, smem, s);
+    case 4: return launch_one<4, G>(A, B, a, sms, smem, s);
+    case 8: return launch_one<8, G>(A, B, a, sms, smem, s);
+    case 10: return launch_one<10, G>(A, B, a, sms, smem, s);
+    case 12: return launch_one<12, G>(A, B, a, sms, smem, s);
+    case 16: return launch_one<16, G>(A, B, a, sms, smem, s);
   }
   return cudaErrorInvalidValue;
 }
@@ -769,16 +818,21 @@ cudaError_t launch_fp8_ffn(const void* tokens, const int32_t* perm, const int32_
   MOE_LAUNCH(cudaMemsetAsync(status, 0, sizeof(int), s));
   uint8_t *x = ws + w.x, *h = ws + w.h;
   float *sx = reinterpret_cast<float*>(ws + w.sx), *sh = reinterpret_cast<float*>(ws + w.sh);
-  MOE_LAUNCH(launch_k(fp8_rows_kernel, (unsigned)std::min((S_max + 7) / 8, 8 * sms), 256, (E + 1) * sizeof(int32_t), s,
+  MOE_LAUNCH(launch_k(fp8_rows_kernel, (unsigned)std::min<long long>(((long long)S_max * ((d / 128 + kRowPart - 1) / kRowPart) + 7) / 8, 8 * sms), 256,
+                      (E + 1) * sizeof(int32_t), s,
                       false, static_cast<const __half*>(tokens), perm, offsets, E, S_max, T, d, w.Sp, x, sx, status));
-  // rows per tile: those of an expert that is two standard deviations fuller than the average one
+  // Rows per tile.  Slots that are no multiple of the tokens come from a capacity, S_max / E for each expert; otherwise
+  // those of an expert that is two standard deviations fuller than the average one (2.4B top-2 layer, 160 slots each:
+  // tiles of 192 rows, two sums in TMEM, 2810 us, of 160, three sums, 2514).
   const double mean = (double)S_max / E;
-  const int rows = (int)std::min<double>(S_max, mean + 2.0 * std::sqrt(mean) + 1.0);
-  const int c8 = rows <= 32 ? 1 : rows <= 64 ? 2 : rows <= 128 ? 4 : rows <= 160 ? 5 : rows <= 192 ? 6 : 8;
-  CUtensorMap A1, A2, B1[2], B2[2];
-  if (!encode_u8_map(&A1, W1q, d, (uint64_t)E * f, 128, 128) || !encode_u8_map(&A2, W2q, f, (uint64_t)E * d, 128, 128) ||
-      !encode_u8_map(&B1[0], x, d, S_max, 128, 64) || !encode_u8_map(&B1[1], x, d, S_max, 128, 16) ||
-      !encode_u8_map(&B2[0], h, f, S_max, 128, 64) || !encode_u8_map(&B2[1], h, f, S_max, 128, 16))
+  const int rows = (int)std::min<double>(S_max, S_max % T && S_max % E == 0 ? mean : mean + 2.0 * std::sqrt(mean) + 1.0);
+  const int c8 = rows <= 32 ? 2 : rows <= 64 ? 4 : rows <= 128 ? 8 : rows <= 160 ? 10 : rows <= 192 ? 12 : 16;
+  CUtensorMap A1, A2;
+  RowMaps B1, B2;
+  bool maps = encode_weight_map(&A1, W1q, d, (uint64_t)E * f) && encode_weight_map(&A2, W2q, f, (uint64_t)E * d);
+  for (int i = 0; i < 3; ++i)
+    maps = maps && encode_u8_map(&B1.box[i], x, d, S_max, 128, 128 >> i) && encode_u8_map(&B2.box[i], h, f, S_max, 128, 128 >> i);
+  if (!maps)
     return cudaErrorInvalidValue;
   Fp8Args g;
   memset(&g, 0, sizeof(g));

@@ -138,6 +138,9 @@ bool encode_f16_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* d
 // Tensor map of a dense matrix of bytes [outer, inner]; a box of box_outer rows and 128 bytes, swizzled.
 bool encode_u8_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_inner,
                    uint32_t box_outer);
+// The same matrix as weight tiles of the 8-bit products: a box is 128 rows, in each 32 of them rows 4 r + j at place
+// 8 j + r.
+bool encode_weight_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer);
 cudaError_t launch_grouped_gemm1(const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap& Ar,
                                  const CUtensorMap& Br, const GemmArgs& args, int grid,
                                  cudaStream_t s, bool pdl = false);
