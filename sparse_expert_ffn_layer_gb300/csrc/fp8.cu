@@ -408,8 +408,7 @@ __device__ __forceinline__ Tile8 tile_at(int i, const int32_t* prefix, const int
 template <int C8, bool kGelu>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ RowMaps tmB, const Fp8Args a) {
-  constexpr int NMAX = 16 * C8, B = C8 > 12 ? 8 : C8;   // groups in flight: as many as registers are left for
-  static_assert(C8 % B == 0);
+  constexpr int NMAX = 16 * C8;
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const Fp8Smem L = fp8_smem(NMAX, a.na, a.nb, a.E);
@@ -634,22 +633,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* sc = reinterpret_cast<const float*>(sm + L.scale_off + slot * L.scale_bytes) + col0 + lc;
         const uint32_t ts = tq + slot * NMAX + col0;
         // (what is loaded beyond the tile's columns stays within the slot, and is not used)
+        uint32_t v[2][4 * C8];
+        float2 x[C8];
+        tmem_ld32<C8>(ts, v);
 #pragma unroll
-        for (int c = 0; c < C8; c += B) {
-          if (c < cw) {
-            uint32_t v[2][4 * B];
-            float2 x[B];
-            tmem_ld32<B>(ts + c * 8, v);
+        for (int c = 0; c < C8; ++c) x[c] = *reinterpret_cast<const float2*>(sc + c * 8);
+        tmem_wait<C8>(v);
 #pragma unroll
-            for (int b = 0; b < B; ++b) x[b] = *reinterpret_cast<const float2*>(sc + (c + b) * 8);
-            tmem_wait<B>(v);
+        for (int c = 0; c < C8; ++c)
 #pragma unroll
-            for (int b = 0; b < B; ++b)
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                fma2(acc[c + b][j], pair(v[j >> 1][4 * b + 2 * (j & 1)], v[j >> 1][4 * b + 2 * (j & 1) + 1]), x[b]);
-          }
-        }
+          for (int j = 0; j < 4; ++j)
+            fma2(acc[c][j], pair(v[j >> 1][4 * c + 2 * (j & 1)], v[j >> 1][4 * c + 2 * (j & 1) + 1]), x[c]);
         tc_fence_before();                       // read: the slot may take the next sum
         __syncwarp();
         if (lane == 0) mbar_arrive(&acc_empty[slot]);
@@ -771,7 +765,6 @@ cudaError_t launch_gemm(int c8, const CUtensorMap& A, const RowMaps& B, const Fp
     case 8: return launch_one<8, G>(A, B, a, sms, smem, s);
     case 10: return launch_one<10, G>(A, B, a, sms, smem, s);
     case 12: return launch_one<12, G>(A, B, a, sms, smem, s);
-    case 16: return launch_one<16, G>(A, B, a, sms, smem, s);
   }
   return cudaErrorInvalidValue;
 }
@@ -822,11 +815,14 @@ cudaError_t launch_fp8_ffn(const void* tokens, const int32_t* perm, const int32_
                       (E + 1) * sizeof(int32_t), s,
                       false, static_cast<const __half*>(tokens), perm, offsets, E, S_max, T, d, w.Sp, x, sx, status));
   // Rows per tile.  Slots that are no multiple of the tokens come from a capacity, S_max / E for each expert; otherwise
-  // those of an expert that is two standard deviations fuller than the average one (2.4B top-2 layer, 160 slots each:
-  // tiles of 192 rows, two sums in TMEM, 2810 us, of 160, three sums, 2514).
+  // those of an expert that is two standard deviations fuller than the average one.  us of both products: 160 slots
+  // each, 128 experts of the 2.4B layer: tiles of 160 rows (three sums in TMEM) 2514, of 192 (two sums) 2810; 160 on
+  // average, 64 experts of half that width: 911 and 772, since half of the experts take two tiles of 160; 256 on
+  // average: 683, 723, of 256 rows 737; 512: 492, 504, 523; 1024: 247, 247, 268.  20 on average: tiles of 32 rows
+  // 534, 64 517, 128 552; 40: 884, 529, 576.
   const double mean = (double)S_max / E;
   const int rows = (int)std::min<double>(S_max, S_max % T && S_max % E == 0 ? mean : mean + 2.0 * std::sqrt(mean) + 1.0);
-  const int c8 = rows <= 32 ? 2 : rows <= 64 ? 4 : rows <= 128 ? 8 : rows <= 160 ? 10 : rows <= 192 ? 12 : 16;
+  const int c8 = rows <= 32 ? 2 : rows <= 64 ? 4 : rows <= 128 ? 8 : rows <= 160 || rows > 192 ? 10 : 12;
   CUtensorMap A1, A2;
   RowMaps B1, B2;
   bool maps = encode_weight_map(&A1, W1q, d, (uint64_t)E * f) && encode_weight_map(&A2, W2q, f, (uint64_t)E * d);
