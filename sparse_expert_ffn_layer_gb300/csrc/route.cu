@@ -7,9 +7,12 @@
 // values whose order matters are nearer than its rounding errors allow is decided again in 64 bits:
 // the experts of a token do not depend on how exp or a sum was rounded.
 //
-// A warp takes a row: its values stay in registers (column lane + 32 v), a round of the selection is two
-// warp-wide reductions over order-preserving integer keys and a pass over the lane's own values.
-// Bound by these rounds' latencies and instructions, not by the 4 E bytes of a row.
+// A warp takes a row: its values stay in registers, a round of the selection is two warp-wide reductions over
+// order-preserving integer keys and a pass over the lane's own values.  A lane has V neighbouring columns where a row
+// is 32 V of them (their loads are wide, and groups of whole lanes need no shared memory), else every 32nd.
+// Bound by the rounds' instructions and latencies, not by the 4 E bytes of a row.
+#include <type_traits>
+
 #include "launch.h"
 
 namespace moe {
@@ -59,21 +62,37 @@ template <>
 struct KeyOf<double> {
   using type = uint64_t;
 };
+template <typename K>
+struct ShflOf {
+  using type = K;
+};
+template <>
+struct ShflOf<uint64_t> {
+  using type = unsigned long long;
+};
+
+// Column of value v of a lane.
+template <int V, bool kWide>
+__device__ __forceinline__ int col_at(int v, int lane) { return kWide ? lane * V + v : lane + 32 * v; }
 
 // Two choices further apart than slack (unit + |c|), unit the largest score a row can have, keep their order
-// in 32 bits.  With u = 2^-24: exp is good to 2 ulp = 4 u, and the sigmoid's sum and quotient to u each:
-// 6 u s; the softmax's sum of E terms adds V + 5 u, x - max at most 0.4 u and the product u: (12 + V) u s.
-// The bias's addition is off by u |c|.  Twice that for the two values.
+// in 32 bits.  With u = 2^-24: the hardware's exponential is good to 2 ulp = 4 u and |x| u, its sum and quotient to u
+// and 2 u, which for the sigmoid is s (|x| + 7) u where exp(-x) matters, at most 4 u; the softmax's sum of E terms adds
+// V + 5 u, x - max at most 0.4 u and the product u: (12 + V) u s.  The bias's addition is off by u |c|.  Twice that for
+// the two values.
 __device__ __forceinline__ float slack(int sigmoid, int V) {
-  return 2.f * (sigmoid ? 8.f : 14.f + V) * 5.9604645e-08f;
+  return 2.f * (sigmoid ? 5.f : 14.f + V) * 5.9604645e-08f;
 }
+
+__device__ __forceinline__ float sigmoid_of(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+__device__ __forceinline__ double sigmoid_of(double x) { return 1.0 / (1.0 + exp(-x)); }
 
 // Scores of a row in place (logits -> s); columns beyond E, and rows of -inf only, have s = 0.
 template <int V, typename F>
 __device__ __forceinline__ void scores(F (&x)[V], int sigmoid, F& m, F& sum) {
   if (sigmoid) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) x[v] = F(1) / (F(1) + exp_of(-x[v]));
+    for (int v = 0; v < V; ++v) x[v] = sigmoid_of(x[v]);
     return;
   }
   m = x[0];
@@ -97,72 +116,80 @@ __device__ __forceinline__ void scores(F (&x)[V], int sigmoid, F& m, F& sum) {
   for (int v = 0; v < V; ++v) x[v] *= inv;
 }
 
-// The k experts of largest choice; lane j < k gets expert j.  Returns whether the order is certain: of the
-// values whose order matters no two are within tol (unit + |c|) of each other (tol = 0: not looked at).
-template <int V, typename F>
-__device__ __forceinline__ bool select(F (&c)[V], const ScoreArgs& a, F* sh, int lane, F tol, F unit, int& mine) {
+// The k experts of largest choice; lane j < k gets expert j, lane k the first that is left out.  Says where the order is
+// not certain, because two values whose order matters are within tol (unit + |c|) of each other (tol = 0: not looked
+// at): bit 0 of the experts, bit 1 of the groups.  key: the choices that are left.  taken, floor: how many experts were taken (fewer than k + 1 where
+// no more are in the groups) and the least of their choices.
+template <int V, bool kWide, typename F>
+__device__ __forceinline__ int select(F (&c)[V], const ScoreArgs& a, F* sh, int lane, F tol, F unit, int& mine,
+                                      typename KeyOf<F>::type (&key)[V], F& floor, int& taken) {
   using K = typename KeyOf<F>::type;
-  bool sure = true;
-  K key[V];
+  int unsure = 0;
 #pragma unroll
-  for (int v = 0; v < V; ++v) key[v] = lane + 32 * v < a.E ? key_of(c[v]) : K(0);
+  for (int v = 0; v < V; ++v) key[v] = kWide || lane + 32 * v < a.E ? key_of(c[v]) : K(0);
   if (a.n_groups > 1 && a.top_groups < a.n_groups) {
     const int M = a.E / a.n_groups;
-    __syncwarp();
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (lane + 32 * v < a.E) sh[lane + 32 * v] = c[v];
-    __syncwarp();
-    // a power of two of lanes per group
+    // lanes per group, a power of two: all of a group's own, or as many as there are
+    const int own = kWide && M % V == 0 && ((M / V) & (M / V - 1)) == 0 ? M / V : 0;
     int per = 1;
-    while (per * 2 * a.n_groups <= 32) per *= 2;
-    const int g = lane / per, l = lane % per;
     F b1 = -INFINITY, b2 = -INFINITY;
-    if (g < a.n_groups)
-      for (int i = l; i < M; i += per) {
-        const F q = sh[g * M + i];
-        if (q > b1) {
-          b2 = b1;
-          b1 = q;
-        } else if (q > b2) {
-          b2 = q;
-        }
-      }
+    auto take = [&](F q) {
+      const F lo = q < b1 ? q : b1;
+      b1 = q > b1 ? q : b1;
+      b2 = lo > b2 ? lo : b2;
+    };
+    if (own) {
+      per = own;
+#pragma unroll
+      for (int v = 0; v < V; ++v) take(c[v]);
+    } else {
+      while (per * 2 * a.n_groups <= 32) per *= 2;
+      __syncwarp();
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (col_at<V, kWide>(v, lane) < a.E) sh[col_at<V, kWide>(v, lane)] = c[v];
+      __syncwarp();
+      if (lane / per < a.n_groups)
+        for (int i = lane % per; i < M; i += per) take(sh[lane / per * M + i]);
+    }
+    const int g = lane / per, l = lane % per;
     for (int o = per / 2; o > 0; o >>= 1) {
       const F q1 = __shfl_xor_sync(0xffffffffu, b1, o), q2 = __shfl_xor_sync(0xffffffffu, b2, o);
-      const F lo = q1 < b1 ? q1 : b1;
-      b1 = q1 > b1 ? q1 : b1;
-      b2 = b2 > q2 ? b2 : q2;
-      b2 = lo > b2 ? lo : b2;
+      take(q1);
+      b2 = q2 > b2 ? q2 : b2;
     }
     const F value = (a.group_top == 2 && M > 1) ? b1 + b2 : b1;
-    // rank of this lane's group; near: another group's value is not surely on its side
     const K kv = key_of(value);
     int rank = 0;
-    bool near = false;
     for (int q = 0; q < a.n_groups; ++q) {
-      const F w = __shfl_sync(0xffffffffu, value, q * per);
-      const K kw = key_of(w);
+      const K kw = __shfl_sync(0xffffffffu, (typename ShflOf<K>::type)kv, q * per);
       rank += (kw > kv || (kw == kv && q < g)) ? 1 : 0;
-      const F gap = w > value ? w - value : value - w;
-      // (sums of two: twice the error)
-      near |= q != g && gap <= F(2) * tol * (unit + (value < F(0) ? -value : value));
     }
-    const bool in = g < a.n_groups && rank < a.top_groups;
-    // only the border between the last group inside and the first outside matters
-    const bool edge = g < a.n_groups && near && (rank == a.top_groups - 1 || rank == a.top_groups);
-    if (tol > F(0) && __any_sync(0xffffffffu, edge)) sure = false;
-    const unsigned inside = __ballot_sync(0xffffffffu, in && l == 0);
+    if (tol > F(0)) {
+      // only the border between the last group inside and the first outside matters (sums of two: twice the error)
+      const unsigned last = __ballot_sync(0xffffffffu, g < a.n_groups && rank == a.top_groups - 1);
+      const unsigned next = __ballot_sync(0xffffffffu, g < a.n_groups && rank == a.top_groups);
+      const F in = __shfl_sync(0xffffffffu, value, __ffs(last) - 1), out = __shfl_sync(0xffffffffu, value, __ffs(next) - 1);
+      if (in - out <= F(2) * tol * (unit + (in < F(0) ? -in : in))) unsure |= 2;
+    }
+    if (own) {
+      if (rank >= a.top_groups)
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = lane + 32 * v;
-      if (e < a.E && !((inside >> (e / M * per)) & 1u)) key[v] = K(0);
+        for (int v = 0; v < V; ++v) key[v] = K(0);
+    } else {
+      const unsigned inside = __ballot_sync(0xffffffffu, g < a.n_groups && rank < a.top_groups && l == 0);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int e = col_at<V, kWide>(v, lane);
+        if (e < a.E && !((inside >> (e / M * per)) & 1u)) key[v] = K(0);
+      }
     }
   }
   // k rounds, and one more for the first expert that is left out
   mine = 0;
   const int rounds = (a.k < a.E && tol > F(0)) ? a.k + 1 : a.k;
   F last = F(0);
+  taken = 0;
   for (int j = 0; j < rounds; ++j) {
     K best = key[0];
 #pragma unroll
@@ -170,61 +197,122 @@ __device__ __forceinline__ bool select(F (&c)[V], const ScoreArgs& a, F* sh, int
     const K top = warp_max(best);
     int at = 0x7fffffff;
 #pragma unroll
-    for (int v = V - 1; v >= 0; --v) at = key[v] == top ? lane + 32 * v : at;
-    at = (int)__reduce_min_sync(0xffffffffu, (unsigned)at);
-    if (j < a.k && lane == j) mine = min(at, a.E - 1);
+    for (int v = V - 1; v >= 0; --v) at = key[v] == top ? col_at<V, kWide>(v, lane) : at;
+    const int all = (int)__reduce_min_sync(0xffffffffu, (unsigned)at);
+    if (lane == j) mine = min(all, a.E - 1);
     if (tol > F(0)) {
       F val;
       if constexpr (sizeof(F) == 4) val = value_of(top);
       else val = F(0);
-      if (top == K(0)) val = -INFINITY;
-      if (j > 0 && last - val <= tol * (unit + (val < F(0) ? -val : val))) sure = false;
+      if (top == K(0)) break;
+      ++taken;
+      if (j > 0 && last - val <= tol * (unit + (val < F(0) ? -val : val))) unsure |= 1;
       last = val;
     }
+    if (at == all) {                             // (one lane)
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (lane + 32 * v == at) key[v] = K(0);
+      for (int v = 0; v < V; ++v)
+        if (col_at<V, kWide>(v, lane) == all) key[v] = K(0);
+    }
   }
-  return sure;
+  floor = last;
+  return unsure;
 }
 
-template <int V>
+template <int V, bool kWide>
 __device__ __forceinline__ void load(float (&x)[V], const float* row, int E, int lane) {
+  if constexpr (kWide && V % 4 == 0) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) x[v] = lane + 32 * v < E ? row[lane + 32 * v] : -INFINITY;
+    for (int v = 0; v < V; v += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(row + lane * V + v);
+      x[v] = q.x; x[v + 1] = q.y; x[v + 2] = q.z; x[v + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = kWide || lane + 32 * v < E ? row[col_at<V, kWide>(v, lane)] : -INFINITY;
+  }
 }
 
 // 64 bits, from the logits: rare rows only, so it is kept out of the row loop's registers.
-template <int V>
+template <int V, bool kWide>
 __device__ __noinline__ int route_wide(const float* row, const ScoreArgs& a, double* sh, int lane) {
   double c[V], m, sum;
 #pragma unroll
-  for (int v = 0; v < V; ++v) c[v] = lane + 32 * v < a.E ? (double)row[lane + 32 * v] : -INFINITY;
+  for (int v = 0; v < V; ++v) {
+    const int e = col_at<V, kWide>(v, lane);
+    c[v] = e < a.E ? (double)row[e] : -INFINITY;
+  }
   scores<V, double>(c, a.sigmoid, m, sum);
 #pragma unroll
-  for (int v = 0; v < V; ++v)
-    if (a.bias && lane + 32 * v < a.E) c[v] += (double)a.bias[lane + 32 * v];
+  for (int v = 0; v < V; ++v) {
+    const int e = col_at<V, kWide>(v, lane);
+    if (a.bias && e < a.E) c[v] += (double)a.bias[e];
+  }
   int mine;
-  select<V, double>(c, a, sh, lane, 0.0, 0.0, mine);
+  uint64_t key[V];
+  double floor;
+  int taken;
+  select<V, kWide, double>(c, a, sh, lane, 0.0, 0.0, mine, key, floor, taken);
   return mine;
 }
 
-template <int V>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const ScoreArgs a, int direct) {
+// The same for sigmoid scores where only the order of the experts near the last one taken is not certain: a lane decides
+// for each expert that was taken, or is within `margin` of the least of these (so that no other can be among the k).
+// False if these are more than 32.  (All columns in 64 bits take a row 3 us, of which a batch waits for the last.)
+template <int V, bool kWide>
+__device__ __forceinline__ bool route_near(const float* row, const ScoreArgs& a, const uint32_t (&key)[V], int taken,
+                                           float floor, float margin, int* sh, int lane, int& mine) {
+  const uint32_t least = key_of(floor - margin);
+  int n = taken;
+  __syncwarp();
+  if (lane < n) sh[lane] = mine;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const bool near = key[v] != 0u && key[v] >= least;
+    const unsigned m = __ballot_sync(0xffffffffu, near);
+    const int at = n + __popc(m & ((1u << lane) - 1u));
+    if (near && at < 32) sh[at] = col_at<V, kWide>(v, lane);
+    n += __popc(m);
+  }
+  if (n > 32) return false;
+  __syncwarp();
+  const int e = lane < n ? sh[lane] : 0;
+  const uint64_t mykey = lane < n ? key_of(sigmoid_of((double)row[e]) + (a.bias ? (double)a.bias[e] : 0.0)) : 0u;
+  int rank = 0;
+  for (int q = 0; q < n; ++q) {
+    const uint64_t k = __shfl_sync(0xffffffffu, (unsigned long long)mykey, q);
+    const int i = __shfl_sync(0xffffffffu, e, q);
+    rank += (k > mykey || (k == mykey && i < e)) ? 1 : 0;
+  }
+  __syncwarp();
+  if (lane < n) sh[rank] = e;
+  __syncwarp();
+  mine = sh[min(lane, n - 1)];
+  return true;
+}
+
+template <int V, bool kWide>
+__global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 8 : V <= 16 ? 4 : 2) route_kernel(const ScoreArgs a, int direct) {
   extern __shared__ double shared[];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  float bias[V];                                 // (complete: nothing but the gate kernel may still run)
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = col_at<V, kWide>(v, lane);
+    bias[v] = a.bias && e < a.E ? a.bias[e] : 0.f;
+  }
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  double* sh = shared + (size_t)w * a.E;
+  double* sh = shared + (size_t)w * max(a.E, 16);
   for (int t = blockIdx.x * kWarps + w; t < a.T; t += gridDim.x * kWarps) {
     const float* row = a.logits + (size_t)t * a.E;
     const bool on = !a.mask || a.mask[t];
     float x[V];
-    load<V>(x, row, a.E, lane);
+    load<V, kWide>(x, row, a.E, lane);
     if (a.logits_copy)
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (lane + 32 * v < a.E) a.logits_copy[(size_t)t * a.E + lane + 32 * v] = x[v];
+        if (col_at<V, kWide>(v, lane) < a.E) a.logits_copy[(size_t)t * a.E + col_at<V, kWide>(v, lane)] = x[v];
     float m = 0.f, sum = 0.f;
     int mine = 0;
     // the scores of all columns: where they are wanted or order the row, or their sum is
@@ -236,7 +324,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const ScoreArgs a, i
     if (a.scores)
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (lane + 32 * v < a.E) a.scores[(size_t)t * a.E + lane + 32 * v] = on ? s[v] : 0.f;
+        if (col_at<V, kWide>(v, lane) < a.E) a.scores[(size_t)t * a.E + col_at<V, kWide>(v, lane)] = on ? s[v] : 0.f;
     if (!on) {
       if (lane < a.k) {
         a.topk_idx[(size_t)t * a.k + lane] = -1;
@@ -245,14 +333,23 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const ScoreArgs a, i
       continue;
     }
     if (direct) {
-      select<V, float>(x, a, reinterpret_cast<float*>(sh), lane, 0.f, 0.f, mine);
+      uint32_t key[V];
+      float floor;
+      int taken;
+      select<V, kWide, float>(x, a, reinterpret_cast<float*>(sh), lane, 0.f, 0.f, mine, key, floor, taken);
     } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (a.bias && lane + 32 * v < a.E) s[v] += a.bias[lane + 32 * v];
+      for (int v = 0; v < V; ++v) s[v] += bias[v];
       const float unit = a.sigmoid ? 1.f : (sum > 0.f ? 1.f / sum : 0.f);
-      if (!select<V, float>(s, a, reinterpret_cast<float*>(sh), lane, slack(a.sigmoid, V), unit, mine))
-        mine = route_wide<V>(row, a, sh, lane);
+      uint32_t key[V];
+      float floor;
+      int taken;
+      const float tol = slack(a.sigmoid, V);
+      const int unsure = select<V, kWide, float>(s, a, reinterpret_cast<float*>(sh), lane, tol, unit, mine, key, floor, taken);
+      if (unsure && (unsure != 1 || !a.sigmoid || taken < a.k ||
+                     !route_near<V, kWide>(row, a, key, taken, floor, 2.f * tol * (unit + fabsf(floor)), reinterpret_cast<int*>(sh),
+                                           lane, mine)))
+        mine = route_wide<V, kWide>(row, a, sh, lane);
     }
     // weights of lanes 0 .. k-1 (scores of -inf: zero)
     const bool have = lane < a.k;
@@ -288,15 +385,20 @@ cudaError_t launch_route(const ScoreArgs& a, cudaStream_t s, bool pdl) {
   MOE_LAUNCH(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   const bool limited = a.n_groups > 1 && a.top_groups < a.n_groups;
   const int direct = !a.bias && !(limited && a.group_top == 2 && a.E > a.n_groups);
-  const size_t smem = limited || !direct ? sizeof(double) * kWarps * a.E : 0;
+  const size_t smem = limited || !direct ? sizeof(double) * kWarps * std::max(a.E, 16) : 0;   // (at least 32 indices)
   const int grid = std::min((a.T + kWarps - 1) / kWarps, 16 * sms);
-  auto go = [&](auto kern) { return launch_k(kern, grid, kWarps * 32, smem, s, pdl, a, direct); };
-  if (a.E <= 32) return go(route_kernel<1>);
-  if (a.E <= 64) return go(route_kernel<2>);
-  if (a.E <= 128) return go(route_kernel<4>);
-  if (a.E <= 256) return go(route_kernel<8>);
-  if (a.E <= 512) return go(route_kernel<16>);
-  return go(route_kernel<32>);
+  auto go = [&](auto v) {
+    constexpr int V = decltype(v)::value;
+    return a.E == 32 * V ? launch_k(route_kernel<V, true>, grid, kWarps * 32, smem, s, pdl, a, direct)
+                         : launch_k(route_kernel<V, false>, grid, kWarps * 32, smem, s, pdl, a, direct);
+  };
+  using std::integral_constant;
+  if (a.E <= 32) return go(integral_constant<int, 1>());
+  if (a.E <= 64) return go(integral_constant<int, 2>());
+  if (a.E <= 128) return go(integral_constant<int, 4>());
+  if (a.E <= 256) return go(integral_constant<int, 8>());
+  if (a.E <= 512) return go(integral_constant<int, 16>());
+  return go(integral_constant<int, 32>());
 }
 
 }  // namespace moe
