@@ -50,7 +50,10 @@ struct Piece<float> {
 };
 
 template <int WPR>
-constexpr int kBlockWarps = WPR > 8 ? WPR : 8;
+constexpr int kBlockWarps = WPR > 4 ? WPR : 4;
+// Rows of experts that a thread has in flight.
+template <int NV>
+constexpr int kFlight = NV > 1 ? 2 : 4;
 
 // Sums over a team's threads.  red: two buffers of WPR words; one barrier per sum (a buffer is written again
 // two sums later, behind the barrier of the sum between).
@@ -86,7 +89,7 @@ __device__ __forceinline__ void weights_at(const float* w, int p, float (&f)[N])
   }
 }
 
-// y: the weighted sum of the token's kept rows, four of them in flight, and the shared row.
+// y: the weighted sum of the token's kept rows, a few of them in flight, and the shared row.
 template <typename T, int WPR, int NV>
 __device__ __forceinline__ void block_sum(const NormArgs& a, size_t t, int tl, float (&y)[NV][Piece<T>::N]) {
   constexpr int N = Piece<T>::N;
@@ -95,11 +98,12 @@ __device__ __forceinline__ void block_sum(const NormArgs& a, size_t t, int tl, f
   for (int n = 0; n < NV; ++n)
 #pragma unroll
     for (int i = 0; i < N; ++i) y[n][i] = 0.f;
-  for (int j0 = 0; j0 < a.k; j0 += 4) {
-    uint4 raw[4][NV];
-    float w[4];
+  constexpr int U = kFlight<NV>;
+  for (int j0 = 0; j0 < a.k; j0 += U) {
+    uint4 raw[U][NV];
+    float w[U];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < U; ++j) {
       const int s = j0 + j < a.k ? a.slot_of[t * a.k + j0 + j] : -1;
       const bool on = (unsigned)s < (unsigned)a.S_max;
       w[j] = on ? a.topk_w[t * a.k + j0 + j] : 0.f;
@@ -111,7 +115,7 @@ __device__ __forceinline__ void block_sum(const NormArgs& a, size_t t, int tl, f
       }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < U; ++j)
 #pragma unroll
       for (int n = 0; n < NV; ++n) {
         float f[N];
@@ -136,7 +140,8 @@ __device__ __forceinline__ void block_sum(const NormArgs& a, size_t t, int tl, f
 }
 
 template <typename T, int WPR, int NV>
-__global__ void __launch_bounds__(32 * kBlockWarps<WPR>) block_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(32 * kBlockWarps<WPR>, (NV * Piece<T>::N <= 16 ? 32 : 16) / kBlockWarps<WPR>)
+    block_norm_kernel(const NormArgs a) {
   constexpr int N = Piece<T>::N, TPB = kBlockWarps<WPR> / WPR;
   __shared__ float red[TPB][2 * WPR];
   pdl_wait();
@@ -209,19 +214,20 @@ __global__ void __launch_bounds__(32 * kBlockWarps<WPR>) block_norm_kernel(const
 }
 
 // A team walks the rows team, team + teams, ...: its threads' columns never change, so the sums over tokens stay
-// with them (in registers up to 16 columns, beyond that in shared memory), and leave once, as one partial row per
-// team and sum; norm_join_kernel adds these in order.
+// with them, in shared memory (each thread's own words: with 16 columns and more of three sums in registers an SM
+// had eight warps, 2048 columns, k = 4: 192 us), and leave once, as one partial row per team and sum;
+// norm_join_kernel adds these in order.  Up to eight columns are kept in registers.
 template <typename T, int NV>
-constexpr bool kSumsInSmem = NV * Piece<T>::N > 16;
+constexpr bool kSumsInSmem = NV * Piece<T>::N > 8;
 
 template <typename T, int WPR, int NV>
-__global__ void __launch_bounds__(32 * kBlockWarps<WPR>) block_norm_backward_kernel(const NormArgs a, const NormGrads b,
-                                                                                   int teams) {
+__global__ void __launch_bounds__(32 * kBlockWarps<WPR>, (NV * Piece<T>::N <= 16 ? 20 : 16) / kBlockWarps<WPR>)
+    block_norm_backward_kernel(const NormArgs a, const NormGrads b, int teams) {
   constexpr int N = Piece<T>::N, TPB = kBlockWarps<WPR> / WPR;
   constexpr bool kSmem = kSumsInSmem<T, NV>;
   __shared__ float red[TPB][2 * WPR];
   __shared__ float dots[TPB][kRouteMaxK][WPR];
-  extern __shared__ float4 dyn[];
+  extern __shared__ float4 dyn[];              // the teams' sums
   pdl_wait();
   pdl_trigger();
   const int team = threadIdx.x / (32 * WPR), tl = threadIdx.x % (32 * WPR), lane = tl & 31, wt = tl >> 5;
@@ -231,24 +237,32 @@ __global__ void __launch_bounds__(32 * kBlockWarps<WPR>) block_norm_backward_ker
   const int pieces = a.d / N;
   const float inv_d = 1.f / (float)a.d;
   // sums[0]: dpost_w, [1]: dgate, [2]: dnext_w
-  float sums[3][kSmem ? 1 : NV][kSmem ? 1 : N];
-  float* mine = reinterpret_cast<float*>(dyn);   // [3][pieces][N], used by one team per block (WPR = 16)
+  float4 sums[3][kSmem ? 1 : NV][kSmem ? 1 : N / 4];
+  float4* mine = dyn + (size_t)team * 3 * (N / 4) * pieces;   // [3][N / 4][pieces]: a warp's words are neighbours
   if constexpr (kSmem) {
-    for (int q = 0; q < 3; ++q)
-      for (int p = tl; p < pieces; p += 32 * WPR)
-#pragma unroll
-        for (int i = 0; i < N; ++i) mine[((size_t)q * pieces + p) * N + i] = 0.f;
+    for (int q = tl; q < 3 * (N / 4) * pieces; q += 32 * WPR) mine[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    // (a thread's words may have been cleared by another)
+    if (WPR > 1) asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(32 * WPR) : "memory");
+    else __syncwarp();
   } else {
 #pragma unroll
     for (int q = 0; q < 3; ++q)
 #pragma unroll
       for (int n = 0; n < NV; ++n)
 #pragma unroll
-        for (int i = 0; i < N; ++i) sums[q][n][i] = 0.f;
+        for (int i = 0; i < N / 4; ++i) sums[q][n][i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  auto add = [&](int q, int n, int p, int i, float v) {
-    if constexpr (kSmem) mine[((size_t)q * pieces + p) * N + i] += v;
-    else sums[q][n][i] += v;
+  auto add = [&](int q, int n, int p, const float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      float4* at = kSmem ? mine + (q * (N / 4) + i) * pieces + p : &sums[q][kSmem ? 0 : n][kSmem ? 0 : i];
+      float4 s = *at;
+      s.x += v[4 * i];
+      s.y += v[4 * i + 1];
+      s.z += v[4 * i + 2];
+      s.w += v[4 * i + 3];
+      *at = s;
+    }
   };
   for (size_t t = at; t < (size_t)a.T; t += teams) {
     float dh[NV][N], y[NV][N];
@@ -274,9 +288,14 @@ __global__ void __launch_bounds__(32 * kBlockWarps<WPR>) block_norm_backward_ker
           Piece<T>::unpack(reinterpret_cast<const uint4*>(static_cast<const T*>(b.hidden) + t * a.d)[p], h[n]);
           Piece<T>::unpack(reinterpret_cast<const uint4*>(static_cast<const T*>(b.dnormed) + t * a.d)[p], dn);
           weights_at<N>(a.next_w, p, w);
+          if (b.dnext_w) {
+            float s[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[i] = dn[i] * h[n][i] * rn;
+            add(2, n, p, s);
+          }
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            if (b.dnext_w) add(2, n, p, i, dn[i] * h[n][i] * rn);
             const float v = dn[i] * w[i];
             c = fmaf(v, h[n][i], c);
             dh[n][i] = fmaf(rn, v, dh[n][i]);
@@ -310,16 +329,24 @@ __global__ void __launch_bounds__(32 * kBlockWarps<WPR>) block_norm_backward_ker
         if (a.post_w) weights_at<N>(a.post_w, p, pw);
         if (a.gate) {
           weights_at<N>(a.gate, p, g);
+          if (b.dgate) {
+            float s[N];
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            if (b.dgate) add(1, n, p, i, dh[n][i] * (a.post_w ? y[n][i] * rp * pw[i] : y[n][i]));
-            dh[n][i] *= g[i];
+            for (int i = 0; i < N; ++i) s[i] = dh[n][i] * (a.post_w ? y[n][i] * rp * pw[i] : y[n][i]);
+            add(1, n, p, s);
           }
+#pragma unroll
+          for (int i = 0; i < N; ++i) dh[n][i] *= g[i];
         }
         if (a.post_w) {
+          if (b.dpost_w) {
+            float s[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[i] = dh[n][i] * y[n][i] * rp;
+            add(0, n, p, s);
+          }
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            if (b.dpost_w) add(0, n, p, i, dh[n][i] * y[n][i] * rp);
             dh[n][i] *= pw[i];
             c = fmaf(dh[n][i], y[n][i], c);
           }
@@ -394,15 +421,9 @@ __global__ void __launch_bounds__(32 * kBlockWarps<WPR>) block_norm_backward_ker
       const int p = n * 32 * WPR + tl;
       if (p < pieces)
 #pragma unroll
-        for (int i = 0; i < N; i += 4) {
-          float4 v;
-          if constexpr (kSmem) {
-            v = *reinterpret_cast<const float4*>(mine + ((size_t)q * pieces + p) * N + i);
-          } else {
-            v = make_float4(sums[q][n][i], sums[q][n][i + 1], sums[q][n][i + 2], sums[q][n][i + 3]);
-          }
-          *reinterpret_cast<float4*>(dst + p * N + i) = v;
-        }
+        for (int i = 0; i < N / 4; ++i)
+          reinterpret_cast<float4*>(dst + p * N)[i] =
+              kSmem ? mine[(q * (N / 4) + i) * pieces + p] : sums[q][kSmem ? 0 : n][kSmem ? 0 : i];
     }
   }
 }
@@ -456,10 +477,10 @@ cudaError_t with_team(int d, F f) {
 
 }  // namespace
 
-// Teams of the backward pass: two blocks' worth per SM of the largest device this is built for.
+// Teams of the backward pass: 20 warps for each of 152 SMs, fewer where the sums of more would not fit shared memory.
 int norm_teams(int T, int d, bool f16) {
-  const int w = warps_for(d, f16);
-  return std::min(T, w >= 8 ? 304 : 304 * 8 / w);
+  const int w = warps_for(d, f16), per_sm = std::max(1, std::min(20 / w, 200 * 1024 / (12 * d)));
+  return std::min(T, 152 * per_sm);
 }
 
 cudaError_t launch_block_norm(const NormArgs& a, bool f16, cudaStream_t s) {
@@ -480,7 +501,7 @@ cudaError_t launch_block_norm_backward(const NormArgs& a, const NormGrads& b, bo
     return with_team<T>(a.d, [&](auto wpr, auto nv) -> cudaError_t {
       constexpr int W = decltype(wpr)::value, V = decltype(nv)::value, TPB = kBlockWarps<W> / W;
       auto kern = block_norm_backward_kernel<T, W, V>;
-      const size_t smem = kSumsInSmem<T, V> ? (size_t)3 * a.d * sizeof(float) : 0;
+      const size_t smem = kSumsInSmem<T, V> ? (size_t)TPB * 3 * a.d * sizeof(float) : 0;
       if (smem) MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
       return launch_k(kern, (teams + TPB - 1) / TPB, 32 * kBlockWarps<W>, smem, s, false, a, b, teams);
     });
