@@ -82,7 +82,7 @@ moe_status clear_status(void* workspace, size_t ws_bytes, cudaStream_t s) {
 }
 
 size_t norm_bytes(int T, int d, bool f16) {
-  return align_up((size_t)std::max(norm_teams(std::max(T, 1), d, f16), 1) * 3 * d * sizeof(float));
+  return align_up((size_t)std::max(norm_teams(std::max(T, 1), d, f16), 1) * 2 * d * sizeof(float));
 }
 
 }  // namespace

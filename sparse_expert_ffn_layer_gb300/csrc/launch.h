@@ -236,7 +236,7 @@ struct NormGrads {
   float* dtopk_w;
   void* dshared;
   float *dpost_w, *dgate, *dnext_w;
-  float* partial;                    // [norm_teams][3][d], null without a sum over tokens
+  float* partial;                    // [norm_teams][2][d], null without a sum over tokens
   int through;                       // 1: something behind dresidual is wanted
   int need_y;                        // 1: y is
 };

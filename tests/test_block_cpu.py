@@ -33,7 +33,7 @@ def test_workspace_sizes(m):
         assert size == sorted(size) and size[-1] >= rows[-1] * (d + f) and all(s % 256 == 0 for s in size)
     for dt, d in [(torch.float16, 8), (torch.float16, 3584), (torch.float32, 1024), (torch.float16, 16384)]:
         size = [m.moe_block_norm_workspace_size(T, d, 2, dt) for T in rows]
-        assert size == sorted(size) and size[0] >= 12 * d
+        assert size == sorted(size) and size[0] >= 8 * d
     for args, code in [((4, 100, 128, 2, 4, torch.float16), 2), ((4, 128, 200, 2, 4, torch.float16), 2),
                        ((4, 128, 128, 1025, 4, torch.float16), 2), ((4, 128, 128, 2, 4, torch.float32), 2),
                        ((4, 128, 128, 0, 4, torch.float16), 1), ((4, 128, 128, 2, -1, torch.float16), 1),
