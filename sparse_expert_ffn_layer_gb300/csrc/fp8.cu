@@ -120,36 +120,44 @@ __global__ void __launch_bounds__(256) fp8_weights_kernel(const T* __restrict__ 
 // ---------------------------------------------------------------- slots
 // Boundaries of the experts' slots as every kernel here uses them, by one warp: the largest offset so far, clamped
 // to [0, S_max], so that runs never overlap or leave the buffers.  prefix[e] (not null): tiles of at most `nmax`
-// rows of the experts before e.  True where an offset was changed.
+// rows of the experts before e.  True where an offset was changed.  kAhead x 32 boundaries are loaded together (one
+// after another, each load takes the latency of L2, which short batches notice).
+template <int kAhead>
 __device__ __forceinline__ bool slot_table(const int32_t* offsets, int E, int S_max, int nmax, int32_t* offs,
                                            int32_t* prefix) {
   const int lane = threadIdx.x & 31;
   bool bad = false;
   int run = 0, tiles = 0;
-  for (int e0 = 0; e0 <= E; e0 += 32) {
-    const int e = e0 + lane;
-    const int o = e <= E ? __ldcg(offsets + e) : 0;
-    int v = min(max(o, 0), S_max);
+  for (int base = 0; base <= E; base += 32 * kAhead) {
+    int o[kAhead];
 #pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-      const int q = __shfl_up_sync(0xffffffffu, v, k);
-      if (lane >= k) v = max(v, q);
-    }
-    v = max(v, run);
-    bad |= e <= E && v != o;
-    if (e <= E) offs[e] = v;
-    int before = __shfl_up_sync(0xffffffffu, v, 1);
-    if (lane == 0) before = run;
-    run = __shfl_sync(0xffffffffu, v, 31);
-    if (!prefix) continue;
-    int c = e >= 1 && e <= E ? (v - before + nmax - 1) / nmax : 0;
+    for (int i = 0; i < kAhead; ++i) o[i] = base + 32 * i + lane <= E ? __ldcg(offsets + base + 32 * i + lane) : 0;
 #pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-      const int q = __shfl_up_sync(0xffffffffu, c, k);
-      if (lane >= k) c += q;
+    for (int i = 0; i < kAhead; ++i) {
+      const int e = base + 32 * i + lane;
+      if (e - lane > E) break;
+      int v = min(max(o[i], 0), S_max);
+#pragma unroll
+      for (int k = 1; k < 32; k <<= 1) {
+        const int q = __shfl_up_sync(0xffffffffu, v, k);
+        if (lane >= k) v = max(v, q);
+      }
+      v = max(v, run);
+      bad |= e <= E && v != o[i];
+      if (e <= E) offs[e] = v;
+      int before = __shfl_up_sync(0xffffffffu, v, 1);
+      if (lane == 0) before = run;
+      run = __shfl_sync(0xffffffffu, v, 31);
+      if (!prefix) continue;
+      int c = e >= 1 && e <= E ? (v - before + nmax - 1) / nmax : 0;
+#pragma unroll
+      for (int k = 1; k < 32; k <<= 1) {
+        const int q = __shfl_up_sync(0xffffffffu, c, k);
+        if (lane >= k) c += q;
+      }
+      if (e <= E) prefix[e] = tiles + c;
+      tiles += __shfl_sync(0xffffffffu, c, 31);
     }
-    if (e <= E) prefix[e] = tiles + c;
-    tiles += __shfl_sync(0xffffffffu, c, 31);
   }
   return bad;
 }
@@ -169,7 +177,7 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const __half* __restrict_
   extern __shared__ int32_t offs[];
   pdl_wait();
   pdl_trigger();
-  if (threadIdx.x < 32 && slot_table(offsets, E, S_max, 1, offs, nullptr)) record_status(status, kErrBounds);
+  if (threadIdx.x < 32 && slot_table<8>(offsets, E, S_max, 1, offs, nullptr)) record_status(status, kErrBounds);
   __syncthreads();
   const int lane = threadIdx.x & 31, l = lane & 15, nb = d / 128, S = offs[E];
   const int parts = (nb + kRowPart - 1) / kRowPart;
@@ -228,9 +236,9 @@ constexpr int kMaxStages = 12;                // of either ring
 constexpr size_t kMinSmem = 116 * 1024;       // one block per SM: each takes all of TMEM
 // Weight tiles and rows have rings of their own: na tiles of 16 KB, nb runs of nmax rows.
 struct Fp8Smem {
-  uint32_t b_off, b_bytes, raw_off, raw_bytes, scale_off, scale_bytes, amax_off, bars_off, misc_off, total;
+  uint32_t b_off, b_bytes, raw_off, raw_bytes, scale_off, scale_bytes, amax_off, join_off, bars_off, misc_off, total;
 };
-__host__ __device__ inline Fp8Smem fp8_smem(int nmax, int na, int nb, int E) {
+__host__ __device__ inline Fp8Smem fp8_smem(int nmax, int na, int nb, int E, int split) {
   Fp8Smem L;
   uint32_t off = (uint32_t)(na * kABytes);
   L.b_off = off;
@@ -244,9 +252,11 @@ __host__ __device__ inline Fp8Smem fp8_smem(int nmax, int na, int nb, int E) {
   const uint32_t slots = 512u / (uint32_t)nmax;
   off += (slots < kMaxSlots ? slots : kMaxSlots) * L.scale_bytes;
   L.amax_off = off;
-  off += 2u * (uint32_t)nmax * 16u;    // two items' [column][lane quarter]
+  off += 2u * (uint32_t)nmax * 16u;           // two items' [column][lane quarter]
+  L.join_off = off;
+  off += (uint32_t)(split - 1) * (uint32_t)nmax * 512u;   // the other blocks' sums
   L.bars_off = off;
-  off += (4u * kMaxStages + 2u * kMaxSlots + 1u) * 8u + 8u;
+  off += (4u * kMaxStages + 2u * kMaxSlots + 2u) * 8u;
   L.misc_off = off;
   off += 16u + 8u * (uint32_t)(E + 1);
   L.total = off + 1024u;                      // slack for the alignment of the rings
@@ -258,6 +268,7 @@ struct Fp8Args {
   const float* wscale;         // [E][M / 128][K / 128]
   const float* xscale;         // [K / 128][Sp]
   int E, S_max, Sp, K, M, na, nb, nslots;
+  int split;                   // blocks of a cluster that share an item
   uint8_t* h;                  // first product: [S_max][M], with hscale [M / 128][Sp]
   float* hscale;
   __half* out;                 // second: [S_max][M]
@@ -342,10 +353,38 @@ __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.
 template <int N>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
+// Clusters: all threads meet; the first block's address of a shared-memory address; stores and arrivals there.
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t first_block(uint32_t addr) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void store_remote(uint32_t addr, float2 v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
+}
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // As mbar_wait_bounded; the clock is read only by a wait that is long already.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
   uint64_t t0 = 0;
-  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+  for (uint32_t it = 1; !(kCluster ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)); ++it) {
     if ((it & 63u) == 0) {
       if (*abort) return false;
       const uint64_t now = globaltimer_ns();
@@ -404,37 +443,42 @@ __device__ __forceinline__ Tile8 tile_at(int i, const int32_t* prefix, const int
   return t;
 }
 
-// C8: groups of eight columns per warp (a tile has up to 16 C8 rows).  kGelu: first product.
-template <int C8, bool kGelu>
+// C8: groups of eight columns per warp (a tile has up to 16 C8 rows).  kGelu: first product.  kSplit: a cluster of
+// a.split blocks takes an item, each a part of its inputs; the blocks' sums go to the first block's shared memory, which
+// adds them in order.  One item for each cluster at most.
+template <int C8, bool kGelu, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ RowMaps tmB, const Fp8Args a) {
   constexpr int NMAX = 16 * C8;
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  const Fp8Smem L = fp8_smem(NMAX, a.na, a.nb, a.E);
+  const Fp8Smem L = fp8_smem(NMAX, a.na, a.nb, a.E, kSplit ? a.split : 1);
   uint64_t* a_full = reinterpret_cast<uint64_t*>(sm + L.bars_off);
   uint64_t *a_empty = a_full + kMaxStages, *b_full = a_empty + kMaxStages, *b_empty = b_full + kMaxStages,
-           *acc_full = b_empty + kMaxStages, *acc_empty = acc_full + kMaxSlots, *spare = acc_empty + kMaxSlots;
+           *acc_full = b_empty + kMaxStages, *acc_empty = acc_full + kMaxSlots, *spare = acc_empty + kMaxSlots, *joined = spare + 1;
   uint32_t* holder = reinterpret_cast<uint32_t*>(sm + L.misc_off);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L.misc_off + 4);
   int32_t* prefix = reinterpret_cast<int32_t*>(sm + L.misc_off + 16);
   int32_t* offs = prefix + a.E + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < a.na; ++s) {
-      mbar_init(&a_full[s], 1);
-      mbar_init(&a_empty[s], 1);
+  if (warp == 0) {
+    if (lane < a.na) {
+      mbar_init(&a_full[lane], 1);
+      mbar_init(&a_empty[lane], 1);
     }
-    for (int s = 0; s < a.nb; ++s) {
-      mbar_init(&b_full[s], 1);
-      mbar_init(&b_empty[s], 1);
+    if (lane < a.nb) {
+      mbar_init(&b_full[lane], 1);
+      mbar_init(&b_empty[lane], 1);
     }
-    for (int s = 0; s < a.nslots; ++s) {
-      mbar_init(&acc_full[s], 2);               // the sum and its scales
-      mbar_init(&acc_empty[s], kEpiWarps);
+    if (lane < a.nslots) {
+      mbar_init(&acc_full[lane], 2);            // the sum and its scales
+      mbar_init(&acc_empty[lane], kEpiWarps);
     }
-    mbar_init(spare, 1);
-    *abort_flag = 0;
+    if (lane == 0) {
+      mbar_init(spare, 1);
+      mbar_init(joined, kSplit ? (a.split - 1) * kEpiWarps : 1);
+      *abort_flag = 0;
+    }
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) prefetch_tmap(&tmA);
@@ -442,12 +486,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_alloc(holder, 512);
   pdl_wait();
   pdl_trigger();
-  if (warp == 2 && slot_table(a.offsets, a.E, a.S_max, NMAX, offs, prefix)) record_status(a.status, kErrBounds);
+  if (warp == 2 && slot_table<(C8 <= 4 ? 8 : 1)>(a.offsets, a.E, a.S_max, NMAX, offs, prefix)) record_status(a.status, kErrBounds);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *holder;
   const int mt = a.M / 128, nkb = a.K / 128;
+  if constexpr (kSplit) cluster_meet();          // the first block's barrier is set up, and the block is there
+  const int part = kSplit ? (int)(blockIdx.x % a.split) : 0;
+  const int kb0 = kSplit ? nkb * part / a.split : 0, kb1 = kSplit ? nkb * (part + 1) / a.split : nkb;
+  // this block's items (not kept in registers)
+  auto first_item = [&]() { return (int)(kSplit ? blockIdx.x / a.split : blockIdx.x); };
+  auto item_step = [&]() { return (int)(kSplit ? gridDim.x / a.split : gridDim.x); };
   const int total = prefix[a.E] * mt;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_for(bar, parity, abort_flag, a.status); };
   uint32_t issued = 0, issued_par = 0;           // ring places with a load in flight, for the end
@@ -464,10 +514,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int st = 0;
       uint32_t sp = 1;
       bool ok = true;
-      for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+      for (int i = first_item(); i < total && ok; i += item_step()) {
         const Tile8 t = tile_at(i, prefix, offs, a.E, mt, NMAX);
         const int agroup = t.e * (a.M / 32) + t.mt * 4;
-        for (int kb = 0; kb < nkb; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           ok = __all_sync(0xffffffffu, wait(&a_empty[st], sp));
           if (!ok) break;
           note(st, sp ^ 1u);
@@ -486,10 +536,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int st = 0;
       uint32_t sp = 1;
       bool ok = true;
-      for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+      for (int i = first_item(); i < total && ok; i += item_step()) {
         const Tile8 t = tile_at(i, prefix, offs, a.E, mt, NMAX);
         const int rows = (t.n + 31) & ~31;
-        for (int kb = 0; kb < nkb; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           ok = __all_sync(0xffffffffu, wait(&b_empty[st], sp));
           if (!ok) break;
           note(st, sp ^ 1u);
@@ -520,10 +570,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // descriptors differ only in the start address (16-byte units, bits 0..13)
       const uint64_t d0 = smem_desc(smem_u32(sm), 16, 1024, 2);
       const uint32_t b0 = L.b_off >> 4, b16 = L.b_bytes >> 4;
-      for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+      for (int i = first_item(); i < total && ok; i += item_step()) {
         const Tile8 t = tile_at(i, prefix, offs, a.E, mt, NMAX);
         const uint32_t idesc = idesc_f16(128, (t.n + 15) & ~15, 0, 0);   // (e4m3 has f16's code 0)
-        for (int kb = 0; kb < nkb; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           // rows, weight tile and a free slot: a lane waits for each
           uint64_t* bar = lane == 0 ? &b_full[bs] : lane == 1 ? &a_full[as] : &acc_empty[slot];
           ok = __all_sync(0xffffffffu, wait(bar, lane == 0 ? bsp : lane == 1 ? asp : ap));
@@ -555,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- scales
       // Copies run kScaleSlots - 1 blocks ahead of their use, over the ends of items; each lane reads what it copied
       // itself, but for the weight tiles' scales.
-      int li = blockIdx.x, lkb = 0, ls = 0;
+      int li = first_item(), lkb = kb0, ls = 0;
       Tile8 lt = {};
       if (li < total) lt = tile_at(li, prefix, offs, a.E, mt, NMAX);
       auto next_copy = [&]() {
@@ -567,9 +617,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (4 * j < lt.n) copy16(dst + 16 * j, src + 4 * j);
           if (lane == 0) copy4(dst + NMAX * 4, a.wscale + ((size_t)lt.e * mt + lt.mt) * nkb + lkb);
           if (++ls == kScaleSlots) ls = 0;
-          if (++lkb == nkb) {
-            lkb = 0;
-            li += gridDim.x;
+          if (++lkb == kb1) {
+            lkb = kb0;
+            li += item_step();
             if (li < total) lt = tile_at(li, prefix, offs, a.E, mt, NMAX);
           }
         }
@@ -579,9 +629,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int slot = 0, us = 0;
       uint32_t ap = 1;
       bool ok = true;
-      for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+      for (int i = first_item(); i < total && ok; i += item_step()) {
         const int n = tile_at(i, prefix, offs, a.E, mt, NMAX).n;
-        for (int kb = 0; kb < nkb; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           copies_wait<kScaleSlots - 2>();
           __syncwarp();
           const uint8_t* raw = sm + L.raw_off + us * L.raw_bytes;
@@ -617,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int turn = 0;
     // a warp whose wait gives up still meets the others at every item's barrier
-    for (int i = blockIdx.x; i < total; i += gridDim.x, turn ^= 1) {
+    for (int i = first_item(); i < total; i += item_step(), turn ^= 1) {
       const Tile8 t = tile_at(i, prefix, offs, a.E, mt, NMAX);
       const int cw = (t.n + 15) >> 4;            // groups of eight columns of each warp of this tile
       const int col0 = g * cw * 8;
@@ -626,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < C8; ++c)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[c][j] = make_float2(0.f, 0.f);
-      for (int kb = 0; kb < nkb && ok; ++kb) {
+      for (int kb = kb0; kb < kb1 && ok; ++kb) {
         ok = __all_sync(0xffffffffu, wait(&acc_full[slot], ap));
         if (!ok) break;
         tc_fence_after();
@@ -650,6 +700,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++slot == a.nslots) {
           slot = 0;
           ap ^= 1u;
+        }
+      }
+      if constexpr (kSplit) {
+        constexpr int kWords = C8 * 4 * 32 * kEpiWarps;
+        const int tid = (warp - 4) * 32 + lane;
+        if (part > 0) {
+          if (ok) {
+            const uint32_t to = first_block(smem_u32(sm + L.join_off)) + ((part - 1) * kWords + tid) * 8;
+#pragma unroll
+            for (int c = 0; c < C8; ++c)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) store_remote(to + (c * 4 + j) * (32 * kEpiWarps * 8), acc[c][j]);
+            __syncwarp();
+            if (lane == 0) arrive_remote(first_block(smem_u32(joined)));
+          }
+          continue;
+        }
+        if (ok) ok = __all_sync(0xffffffffu, wait_for<true>(joined, 0, abort_flag, a.status));
+        if (ok) {
+          for (int p = 0; p + 1 < a.split; ++p) {
+            const float2* from = reinterpret_cast<const float2*>(sm + L.join_off) + p * kWords + tid;
+#pragma unroll
+            for (int c = 0; c < C8; ++c)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 v = from[(c * 4 + j) * (32 * kEpiWarps)];
+                acc[c][j] = make_float2(acc[c][j].x + v.x, acc[c][j].y + v.y);
+              }
+          }
         }
       }
       const size_t tile0 = (size_t)t.row0 * a.M + t.mt * 128 + 32 * q + 4 * lr;   // this lane's four outputs of a slot
@@ -736,35 +815,63 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  if constexpr (kSplit) cluster_meet();          // no block leaves while another may still write to its shared memory
 }
 
 // Ring lengths: as many runs of rows as fit beside as many weight tiles (at most kMaxStages), the rest for weight tiles.
-bool fp8_rings(int nmax, int E, int smem, int* na, int* nb) {
-  const int fixed = (int)fp8_smem(nmax, 0, 0, E).total, row_bytes = nmax * 128;
+bool fp8_rings(int nmax, int E, int split, int smem, int* na, int* nb) {
+  const int fixed = (int)fp8_smem(nmax, 0, 0, E, split).total, row_bytes = nmax * 128;
   *nb = std::min(kMaxStages, (smem - fixed) / (kABytes + row_bytes));
   *na = std::min(kMaxStages, (smem - fixed - *nb * row_bytes) / kABytes);
   return *nb >= 2;
 }
 
-template <int C8, bool G>
+template <int C8, bool G, bool Z>
 cudaError_t launch_one(const CUtensorMap& A, const RowMaps& B, Fp8Args a, int sms, int smem, cudaStream_t s) {
-  auto kern = fp8_gemm_kernel<C8, G>;
+  auto kern = fp8_gemm_kernel<C8, G, Z>;
   MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
-  if (!fp8_rings(16 * C8, a.E, smem, &a.na, &a.nb)) return cudaErrorInvalidValue;
+  if (!fp8_rings(16 * C8, a.E, a.split, smem, &a.na, &a.nb)) return cudaErrorInvalidValue;
   a.nslots = std::min(kMaxSlots, 512 / (16 * C8));
-  const size_t bytes = std::max<size_t>(fp8_smem(16 * C8, a.na, a.nb, a.E).total, kMinSmem);
-  return launch_k(kern, sms, kThreads, bytes, s, true, A, B, a);
+  const size_t bytes = std::max<size_t>(fp8_smem(16 * C8, a.na, a.nb, a.E, a.split).total, kMinSmem);
+  if (!Z) return launch_k(kern, sms, kThreads, bytes, s, true, A, B, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sms / a.split * a.split);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = a.split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, A, B, (const Fp8Args)a);
+  if (err == cudaSuccess) launch_counter().fetch_add(1, std::memory_order_relaxed);
+  return err;
+}
+
+// Where a short batch's items leave more than half of the SMs idle, clusters of two, four or eight blocks share them
+// (with four blocks of inputs each at least).
+template <int C8, bool G>
+cudaError_t launch_short(const CUtensorMap& A, const RowMaps& B, Fp8Args a, int sms, int smem, cudaStream_t s) {
+  const long long items = (long long)(std::min(a.E, a.S_max) + a.S_max / (16 * C8)) * (a.M / 128);   // at most
+  while (a.split < 8 && items * 2 * a.split <= sms && a.K / 128 >= 8 * a.split) a.split *= 2;
+  if (a.split > 1) return launch_one<C8, G, true>(A, B, a, sms, smem, s);
+  return launch_one<C8, G, false>(A, B, a, sms, smem, s);
 }
 
 template <bool G>
 cudaError_t launch_gemm(int c8, const CUtensorMap& A, const RowMaps& B, const Fp8Args& a, int sms, int smem,
                         cudaStream_t s) {
   switch (c8) {
-    case 2: return launch_one<2, G>(A, B, a, sms, smem, s);
-    case 4: return launch_one<4, G>(A, B, a, sms, smem, s);
-    case 8: return launch_one<8, G>(A, B, a, sms, smem, s);
-    case 10: return launch_one<10, G>(A, B, a, sms, smem, s);
-    case 12: return launch_one<12, G>(A, B, a, sms, smem, s);
+    case 2: return launch_short<2, G>(A, B, a, sms, smem, s);
+    case 4: return launch_one<4, G, false>(A, B, a, sms, smem, s);
+    case 8: return launch_one<8, G, false>(A, B, a, sms, smem, s);
+    case 10: return launch_one<10, G, false>(A, B, a, sms, smem, s);
+    case 12: return launch_one<12, G, false>(A, B, a, sms, smem, s);
   }
   return cudaErrorInvalidValue;
 }
@@ -837,6 +944,7 @@ cudaError_t launch_fp8_ffn(const void* tokens, const int32_t* perm, const int32_
   g.S_max = S_max;
   g.Sp = w.Sp;
   g.status = status;
+  g.split = 1;
   g.wscale = W1s;
   g.xscale = sx;
   g.K = d;

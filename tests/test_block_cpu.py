@@ -208,8 +208,14 @@ def test_no_warp_leaves_a_loop_whose_barrier_others_wait_at():
             continue
         seen += 1
         before = body.split("bar.sync")[0]
-        inner = before.index("for (int kb")           # the loop over the blocks of inputs may end early: it has no barrier
-        before = before.replace(block_behind(before, inner), "")
+        # blocks that hand their sums to another one of the cluster: all warps of the block
+        before = before.replace(block_behind(body, body.index("if (part > 0)")), "")
+        # inner loops may end early: they are over before the barrier
+        for inner in ("for (int kb", "for (int c = 0; c < C8; ++c) {"):
+            while inner in before:
+                at = before.index(inner)
+                end = before.index("{", at) + len(block_behind(before, at)) + 2
+                before = before[:at] + before[end:]
         assert not re.search(r"\b(break|return|continue|goto)\b", before), head
         assert not re.search(r"\bok\b", head), head
     assert seen == 1
@@ -220,4 +226,14 @@ def test_blocks_that_give_up_wait_for_their_copies():
     text = source("fp8.cu")
     end = block_behind(text, text.index("fp8_gemm_kernel("))
     end = end[end.rindex("__syncthreads()"):]
-    assert end.count("mbar_drain") == 3 and "tmem_dealloc" in end
+    # the two rings' loads by the warps that issued them, and the products
+    assert "a_full : b_full" in end and end.count("mbar_drain") == 2 and "tmem_dealloc" in end
+
+
+def test_no_block_of_a_cluster_writes_to_another_that_is_not_there():
+    """Before the first write to another block's shared memory the cluster has met, and it meets again before a block
+    leaves: also where a wait gave up."""
+    kernel = block_behind(source("fp8.cu"), source("fp8.cu").index("fp8_gemm_kernel("))
+    assert kernel.count("cluster_meet()") == 2
+    assert kernel.index("cluster_meet()") < kernel.index("store_remote")
+    assert kernel.rindex("cluster_meet()") > kernel.rindex("tmem_dealloc")

@@ -428,6 +428,13 @@ def test_expert_ffn_fp8(m, rows, d, f, spare):
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("rows", [[1], [0, 3], [9, 0, 0, 20], [32, 33], [1, 0, 1, 0, 1, 2, 1, 1]], ids=str)
+@pytest.mark.parametrize("d,f", [(1024, 128), (1152, 2048), (4096, 1024), (384, 4224)])
+def test_expert_ffn_fp8_short_batches(m, rows, d, f):
+    """Few items with many inputs each: shared by clusters of two, four and eight blocks."""
+    test_expert_ffn_fp8(m, rows, d, f, 2)
+
+
 def test_expert_ffn_fp8_bad_indices(m):
     """Plans that leave their bounds: reported, and nothing outside [0, S_max) is written."""
     g = gen(1)
