@@ -438,10 +438,11 @@ typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
  * Ties go to the lower index.  Order and ties are those of the scores as 64-bit numbers, not of their
  * rounded 32-bit values (without a bias they are ordered by their logits).
  *   tokens, Wg, logits_in, logits_out, dtype, d: as moe_gate_topk's.
- *   bias       nullable [E] float32, added for the choice only (raised for experts that get too few tokens).
+ *   bias       nullable [E] float32, added for the choice only (raised for experts that get too few tokens; -infinity
+ *              for one that is not to be taken while others are left).
  *   token_mask nullable [T] bytes: a token with 0 gets topk_idx = -1, which moe_dispatch drops, and zero
  *              weights; what its row holds has no effect.
- *   scores_out nullable [T, E] float32: s (rows of masked tokens: 0).
+ *   scores_out nullable [T, E] float32: s (rows of masked tokens: 0); not logits_in or logits_out themselves.
  * Scores of logits of -infinity are zero; chosen experts whose scores sum to zero get zero weights.  Logits of
  * NaN or +infinity give unspecified experts (in [0, E)) and weights.
  * Shapes: k <= 16, k <= top_groups E / n_groups, n_groups <= 32 and a divisor of E; otherwise as moe_gate_topk.

@@ -107,6 +107,8 @@ moe_status moe_route(const void* tokens, moe_dtype dtype, const float* Wg, const
     if (!aligned16(tokens) || !aligned16(Wg) || !aligned16(logits_in) || !aligned16(logits_out) || !aligned16(bias) ||
         !aligned16(scores_out) || !aligned16(topk_idx) || !aligned16(topk_w))
       return MOE_ERR_UNSUPPORTED;
+    // the chosen logits are read again after a row's scores are written
+    if (scores_out && (scores_out == logits_in || scores_out == logits_out)) return MOE_ERR_INVALID_ARG;
     cudaStream_t s = as_stream(stream);
     if (!logits_in) MOE_TRY(launch_gate_logits(tokens, dtype == MOE_F16, Wg, T, d, E, logits_out, s));
     const ScoreArgs a{logits_in ? logits_in : logits_out, bias, token_mask, T, E, k, score == MOE_SCORE_SIGMOID,

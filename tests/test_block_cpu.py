@@ -60,7 +60,7 @@ def test_route_refusals(m):
     for bad in (dict(T=-1), dict(E=0), dict(k=0), dict(k=17, E=17 - 1), dict(score=2), dict(G=3), dict(G=0), dict(top=0),
                 dict(G=4, top=5), dict(gt=0), dict(gt=3), dict(scale=NAN), dict(scale=INF), dict(d=0), dict(dt=4),
                 dict(i=None), dict(w=None), dict(li=None), dict(li=None, x=P, Wg=P), dict(li=None, x=P, lo=P),
-                dict(E=16, G=8, top=1, k=3)):
+                dict(E=16, G=8, top=1, k=3), dict(so=P), dict(li=None, x=P, Wg=P, lo=R, so=R)):
         assert route(**bad) == inv, bad
     for bad in (dict(k=17, E=32), dict(E=1025), dict(E=64, G=64, top=64), dict(T=1 << 22, E=1024), dict(li=ODD), dict(i=ODD),
                 dict(b=ODD), dict(w=ODD), dict(so=ODD)):

@@ -172,6 +172,23 @@ def test_route_extremes(m, sigmoid, renorm):
     assert ((i >= 0) & (i < 40)).all()
 
 
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("G,top,gt", [(1, 1, 1), (4, 2, 1), (4, 3, 2)])
+def test_route_with_experts_switched_off(m, sigmoid, G, top, gt):
+    """A bias of -infinity, for whole groups among them: the others are taken first, in their order."""
+    g = gen(12)
+    T, E, k = 50, 48, 6
+    x = randn(g, T, E)
+    bias = randn(g, E, sigma=0.1)
+    bias[::3] = -float("inf")
+    bias[12:24] = -float("inf")
+    idx, w, _ = run_route(m, x, k, sigmoid, bias, None, G, top, gt)
+    want = ref_route(x, k, sigmoid, bias, G, top, gt)
+    assert torch.equal(idx.long(), want) and not torch.isneginf(bias[idx.long()]).any()
+    ww = ref_weights(x, want, sigmoid, True, 1.0)
+    check(w, ww, 70 * U * ww, "topk_w")
+
+
 @pytest.mark.parametrize("T,d,E,dtype", [(1, 128, 8, torch.float16), (70, 100, 24, torch.float32), (600, 256, 64, torch.float16)])
 def test_route_from_tokens(m, T, d, E, dtype):
     """Logits bit for bit those of moe_gate_topk, the rest as with logits_in; logits_in with logits_out copies."""
@@ -795,10 +812,11 @@ def test_block_of_experts(m, T, d, f, E, k):
     check(st["n"], n, 1e-5 * (n.abs() + 1) + 2.0 ** -11 * n.abs(), "n")
 
 
-def test_block_captured_and_eager(m):
+@pytest.mark.parametrize("T,d,f", [(130, 256, 256), (2, 1024, 2048)])
+def test_block_captured_and_eager(m, T, d, f):
     """A captured step with inputs that change between replays, eager calls of another state between them, and two
     states on two streams: the same bits as eager calls one after another."""
-    b = block_inputs(m, 130, 256, 256, 16, 4, 6)
+    b = block_inputs(m, T, d, f, 16, 4, 6)
     st, plain = block_state(m, b), block_state(m, b)
     block_step(m, b, st)                              # (first calls set kernels up outside of a capture)
     torch.cuda.synchronize()
@@ -806,7 +824,7 @@ def test_block_captured_and_eager(m):
     with torch.cuda.graph(graph):
         block_step(m, b, st)
     for seed in (1, 2):
-        b["res"].copy_(randn(gen(seed), 130, 256, dtype=torch.float16))
+        b["res"].copy_(randn(gen(seed), T, d, dtype=torch.float16))
         block_step(m, b, plain)
         graph.replay()
         torch.cuda.synchronize()
