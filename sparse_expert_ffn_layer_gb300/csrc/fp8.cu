@@ -735,9 +735,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (kGelu) {
         // GeLU, the largest magnitude of each slot's 128 columns (four warps), and 8 bits
         uint32_t* am = reinterpret_cast<uint32_t*>(sm + L.amax_off) + turn * (NMAX * 4);
-        // (columns beyond the tile's are taken along: without branches the compiler mixes the groups)
 #pragma unroll
         for (int c = 0; c < C8; ++c) {
+          if (c >= cw) continue;
           uint32_t m0 = 0, m1 = 0;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, o));
             m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, o));
           }
-          if (lr == 0 && c < cw) {
+          if (lr == 0) {
             am[(col0 + c * 8 + lc) * 4 + q] = m0;
             am[(col0 + c * 8 + lc + 1) * 4 + q] = m1;
           }
