@@ -236,7 +236,7 @@ constexpr int kMaxStages = 12;                // of either ring
 constexpr size_t kMinSmem = 116 * 1024;       // one block per SM: each takes all of TMEM
 // Weight tiles and rows have rings of their own: na tiles of 16 KB, nb runs of nmax rows.
 struct Fp8Smem {
-  uint32_t b_off, b_bytes, raw_off, raw_bytes, scale_off, scale_bytes, amax_off, join_off, bars_off, misc_off, total;
+  uint32_t b_off, b_bytes, raw_off, raw_bytes, scale_off, scale_bytes, amax_off, inv_off, join_off, bars_off, misc_off, total;
 };
 __host__ __device__ inline Fp8Smem fp8_smem(int nmax, int na, int nb, int E, int split) {
   Fp8Smem L;
@@ -253,6 +253,8 @@ __host__ __device__ inline Fp8Smem fp8_smem(int nmax, int na, int nb, int E, int
   off += (slots < kMaxSlots ? slots : kMaxSlots) * L.scale_bytes;
   L.amax_off = off;
   off += 2u * (uint32_t)nmax * 16u;           // two items' [column][lane quarter]
+  L.inv_off = off;
+  off += (uint32_t)(kEpiWarps / 2) * (uint32_t)nmax * 4u;   // a warp's columns are half of a tile's
   L.join_off = off;
   off += (uint32_t)(split - 1) * (uint32_t)nmax * 512u;   // the other blocks' sums
   L.bars_off = off;
@@ -407,10 +409,38 @@ __device__ __forceinline__ float2 float2_of(unsigned long long r) {
   return make_float2(__uint_as_float((uint32_t)r), __uint_as_float((uint32_t)(r >> 32)));
 }
 __device__ __forceinline__ float2 pair(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return float2_of(r);
+}
+// The larger magnitude; NaN if either is (as a positive number's bits).
+__device__ __forceinline__ float max_nan(float m, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  return r;
+}
 __device__ __forceinline__ void fma2(float2& d, float2 a, float2 b) {
   unsigned long long r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(d)));
   d = float2_of(r);
+}
+
+// GeLU of two values as gelu_tanh writes it, x / (1 + 2^z) with z = -2 log2(e) sqrt(2 / pi) (x + 0.044715 x^3), by the
+// hardware's exponential (2 ulp and |z| 2^-24) and reciprocal (1 ulp) with subnormals taken as zero, which neither the
+// sum with one nor the quotient notices.  (By the library's functions, which keep them, 128 x 160 values took 5300
+// cycles, not what the two operations need, 2560: 16 a cycle.)
+__device__ __forceinline__ float2 gelu2(float2 x) {
+  const float2 c1 = make_float2(-0.1029432397f, -0.1029432397f), c0 = make_float2(-2.3022081985f, -2.3022081985f);
+  float2 a = c0;
+  fma2(a, mul2(x, x), c1);
+  const float2 z = mul2(x, a);
+  float2 e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(z.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(z.y));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(1.f + e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(1.f + e.y));
+  return mul2(x, r);
 }
 
 // The rows by boxes of 128, 64 and 32 of them.
@@ -738,44 +768,51 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < C8; ++c) {
           if (c >= cw) continue;
-          uint32_t m0 = 0, m1 = 0;
+          float m0 = 0.f, m1 = 0.f;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            float2& v = acc[c][j];
-            v = make_float2(gelu_tanh(v.x), gelu_tanh(v.y));
-            m0 = max(m0, magnitude_bits(v.x));
-            m1 = max(m1, magnitude_bits(v.y));
+            acc[c][j] = gelu2(acc[c][j]);
+            m0 = max_nan(m0, acc[c][j].x);
+            m1 = max_nan(m1, acc[c][j].y);
           }
+          uint32_t b0 = __float_as_uint(m0), b1 = __float_as_uint(m1);
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) {
-            m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-            m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+            b0 = max(b0, __shfl_xor_sync(0xffffffffu, b0, o));
+            b1 = max(b1, __shfl_xor_sync(0xffffffffu, b1, o));
           }
           if (lr == 0) {
-            am[(col0 + c * 8 + lc) * 4 + q] = m0;
-            am[(col0 + c * 8 + lc + 1) * 4 + q] = m1;
+            am[(col0 + c * 8 + lc) * 4 + q] = b0;
+            am[(col0 + c * 8 + lc + 1) * 4 + q] = b1;
           }
         }
         asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
         if (!ok) continue;
+        // a lane makes the scale of a column, for its whole warp
+        float* invs = reinterpret_cast<float*>(sm + L.inv_off) + (warp - 4) * (8 * C8);
+        for (int c = lane; c < 8 * cw; c += 32) {
+          const int col = col0 + c;
+          const uint4 r = *reinterpret_cast<const uint4*>(am + col * 4);
+          float scale, inv;
+          fp8_scale(max(max(r.x, r.y), max(r.z, r.w)), scale, inv);
+          invs[c] = inv;
+          if (q == 0 && col < t.n) a.hscale[(size_t)t.mt * a.Sp + t.sc0 + col] = scale;
+        }
+        __syncwarp();
+        uint8_t* dst = a.h + tile0 + (size_t)(col0 + lc) * a.M;
 #pragma unroll
         for (int c = 0; c < C8; ++c) {
           if (c >= cw) continue;
+          const float2 inv = *reinterpret_cast<const float2*>(invs + c * 8 + lc);
+          float2 v[4];
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const int col = col0 + c * 8 + lc + p;
-            const uint4 r = *reinterpret_cast<const uint4*>(am + col * 4);
-            float scale, inv;
-            fp8_scale(max(max(r.x, r.y), max(r.z, r.w)), scale, inv);
-            if (col < t.n) {
-              if (q == 0 && lr == 0) a.hscale[(size_t)t.mt * a.Sp + t.sc0 + col] = scale;
-              const float2 (&v)[4] = acc[c];
-              *reinterpret_cast<uint32_t*>(a.h + tile0 + (size_t)col * a.M) =
-                  p ? fp8_four(v[0].y * inv, v[1].y * inv, v[2].y * inv, v[3].y * inv)
-                    : fp8_four(v[0].x * inv, v[1].x * inv, v[2].x * inv, v[3].x * inv);
-            }
-          }
+          for (int j = 0; j < 4; ++j) v[j] = mul2(acc[c][j], inv);
+          const int col = col0 + c * 8 + lc;
+          if (col < t.n) *reinterpret_cast<uint32_t*>(dst) = fp8_four(v[0].x, v[1].x, v[2].x, v[3].x);
+          if (col + 1 < t.n) *reinterpret_cast<uint32_t*>(dst + a.M) = fp8_four(v[0].y, v[1].y, v[2].y, v[3].y);
+          dst += 8 * (size_t)a.M;
         }
+        __syncwarp();                            // (the warp's scales are written again with the next item)
       } else {
         if (!ok) continue;
 #pragma unroll

@@ -400,8 +400,9 @@ def ref_ffn8(x, W1, W2, d, f):
     # 128 products of a block in the tensor cores (2 u each addition), the block's scale (2 u) and d / 128 sums
     eu = (2 * 128 + 4 + d / 128) * U * mag
     h = gelu(u)
-    # |gelu'| <= 1.13; gelu's own exponential and quotient: 2 ulp and 1.2 |2 u'| of the exponent each, |2 u'| <= 20
-    eh = 1.13 * eu + 64 * U * h.abs() + 1e-30
+    # |gelu'| <= 1.13; gelu's own steps: three roundings of its exponent z, 3 |z| ln 2 u with |z| <= 29 (beyond that the value
+    # is below 1e-8 of the argument): 60 u, the exponential 2 ulp, a sum, a reciprocal and a product: 8 u
+    eh = 1.13 * eu + 80 * U * h.abs() + 1e-30
     lo, hi = rows8(h - eh), rows8(h + eh)
     q = rows8(h)
     # (lo and hi are taken with the scales of their own rows: a scale at the border moves all its block)
