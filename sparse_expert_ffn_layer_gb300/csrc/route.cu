@@ -7,10 +7,12 @@
 // values whose order matters are nearer than its rounding errors allow is decided again in 64 bits:
 // the experts of a token do not depend on how exp or a sum was rounded.
 //
-// A warp takes a row: its values stay in registers, a round of the selection is two warp-wide reductions over
-// order-preserving integer keys and a pass over the lane's own values.  A lane has V neighbouring columns where a row
-// is 32 V of them (their loads are wide, and groups of whole lanes need no shared memory), else every 32nd.
-// Bound by the rounds' instructions and latencies, not by the 4 E bytes of a row.
+// A warp takes a row, whose values stay in registers as order-preserving integer keys.  The (k + 1)th largest of the
+// lanes' own largest keys is at most the row's (k + 1)th largest: only keys from there on, hardly more than k, are put
+// one to a lane and ranked against each other.  (Rounds of two warp-wide reductions and a pass over a lane's values,
+// which still serve rows of many equal keys, took 1320 instructions a row of 256 experts in groups, k = 8: the integer
+// pipe 68 % busy.)  A lane has V neighbouring columns where a row is 32 V of them (their loads are wide, and groups of
+// whole lanes need no shared memory), else every 32nd.  Bound by instructions, not by the 4 E bytes of a row.
 #include <type_traits>
 
 #include "launch.h"
@@ -118,8 +120,9 @@ __device__ __forceinline__ void scores(F (&x)[V], int sigmoid, F& m, F& sum) {
 
 // The k experts of largest choice; lane j < k gets expert j, lane k the first that is left out.  Says where the order is
 // not certain, because two values whose order matters are within tol (unit + |c|) of each other (tol = 0: not looked
-// at): bit 0 of the experts, bit 1 of the groups.  key: the choices that are left.  taken, floor: how many experts were taken (fewer than k + 1 where
-// no more are in the groups) and the least of their choices.
+// at): bit 0 of the experts, bit 1 of the groups too, or in a way that needs the whole row.  key: the choices of the
+// experts in the groups.  taken, floor: how many experts were taken (fewer than k + 1 where no more are in the groups) and
+// the least of their choices.  sh: 64 words, and E values where groups go through it.
 template <int V, bool kWide, typename F>
 __device__ __forceinline__ int select(F (&c)[V], const ScoreArgs& a, F* sh, int lane, F tol, F unit, int& mine,
                                       typename KeyOf<F>::type (&key)[V], F& floor, int& taken) {
@@ -185,9 +188,62 @@ __device__ __forceinline__ int select(F (&c)[V], const ScoreArgs& a, F* sh, int 
       }
     }
   }
-  // k rounds, and one more for the first expert that is left out
+  // k experts, and one more for the first that is left out
   mine = 0;
   const int rounds = (a.k < a.E && tol > F(0)) ? a.k + 1 : a.k;
+  if constexpr (sizeof(F) == 4) {
+    uint32_t sorted = key[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) sorted = max(sorted, key[v]);
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+      for (int o = size / 2; o > 0; o /= 2) {    // descending over the lanes
+        const uint32_t q = __shfl_xor_sync(0xffffffffu, sorted, o);
+        sorted = ((lane & o) == 0) == ((lane & size) == 0) ? max(sorted, q) : min(sorted, q);
+      }
+    const uint32_t least = max(__shfl_sync(0xffffffffu, sorted, rounds - 1), 1u);
+    uint32_t* near_key = reinterpret_cast<uint32_t*>(sh);
+    int* near_col = reinterpret_cast<int*>(sh) + 32;
+    int n = 0;
+    __syncwarp();
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const bool in = key[v] >= least;
+      const unsigned m = __ballot_sync(0xffffffffu, in);
+      const int at = n + __popc(m & ((1u << lane) - 1u));
+      if (in && at < 32) {
+        near_key[at] = key[v];
+        near_col[at] = col_at<V, kWide>(v, lane);
+      }
+      n += __popc(m);
+    }
+    if (n >= a.k && n <= 32) {
+      __syncwarp();
+      const uint32_t k0 = lane < n ? near_key[lane] : 0u;
+      const int c0 = lane < n ? near_col[lane] : 0x7fffffff;
+      int rank = 0;
+      for (int q = 0; q < n; ++q) {
+        const uint32_t kq = __shfl_sync(0xffffffffu, k0, q);
+        const int cq = __shfl_sync(0xffffffffu, c0, q);
+        rank += (kq > k0 || (kq == k0 && cq < c0)) ? 1 : 0;
+      }
+      __syncwarp();
+      if (lane < n) {
+        near_key[rank] = k0;
+        near_col[rank] = c0;
+      }
+      __syncwarp();
+      taken = min(n, rounds);
+      mine = near_col[min(lane, taken - 1)];
+      if (tol > F(0)) {
+        floor = value_of(near_key[taken - 1]);
+        const float hi = value_of(near_key[min(lane, taken - 1)]), lo = value_of(near_key[min(lane + 1, taken - 1)]);
+        if (__any_sync(0xffffffffu, lane + 1 < taken && hi - lo <= tol * (unit + fabsf(lo)))) unsure |= 1;
+      }
+      return unsure;
+    }
+  }
   F last = F(0);
   taken = 0;
   for (int j = 0; j < rounds; ++j) {
@@ -216,7 +272,7 @@ __device__ __forceinline__ int select(F (&c)[V], const ScoreArgs& a, F* sh, int 
     }
   }
   floor = last;
-  return unsure;
+  return unsure ? unsure | 2 : 0;                // (the keys of those taken are gone)
 }
 
 template <int V, bool kWide>
@@ -258,14 +314,13 @@ __device__ __noinline__ int route_wide(const float* row, const ScoreArgs& a, dou
 
 // The same for sigmoid scores where only the order of the experts near the last one taken is not certain: a lane decides
 // for each expert that was taken, or is within `margin` of the least of these (so that no other can be among the k).
-// False if these are more than 32.  (All columns in 64 bits take a row 3 us, of which a batch waits for the last.)
+// False if these are fewer than k (NaN) or more than 32.  (All columns in 64 bits take a row 3 us, of which a batch waits for the last.)
 template <int V, bool kWide>
-__device__ __forceinline__ bool route_near(const float* row, const ScoreArgs& a, const uint32_t (&key)[V], int taken,
-                                           float floor, float margin, int* sh, int lane, int& mine) {
+__device__ __forceinline__ bool route_near(const float* row, const ScoreArgs& a, const uint32_t (&key)[V], float floor,
+                                           float margin, int* sh, int lane, int& mine) {
   const uint32_t least = key_of(floor - margin);
-  int n = taken;
+  int n = 0;
   __syncwarp();
-  if (lane < n) sh[lane] = mine;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const bool near = key[v] != 0u && key[v] >= least;
@@ -274,7 +329,7 @@ __device__ __forceinline__ bool route_near(const float* row, const ScoreArgs& a,
     if (near && at < 32) sh[at] = col_at<V, kWide>(v, lane);
     n += __popc(m);
   }
-  if (n > 32) return false;
+  if (n < a.k || n > 32) return false;
   __syncwarp();
   const int e = lane < n ? sh[lane] : 0;
   const uint64_t mykey = lane < n ? key_of(sigmoid_of((double)row[e]) + (a.bias ? (double)a.bias[e] : 0.0)) : 0u;
@@ -303,7 +358,7 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 8 : V <= 16 ? 4 : 2) rou
   }
   pdl_wait();
   pdl_trigger();
-  double* sh = shared + (size_t)w * max(a.E, 16);
+  double* sh = shared + (size_t)w * (a.n_groups > 1 && a.top_groups < a.n_groups ? max(a.E, 32) : 32);
   for (int t = blockIdx.x * kWarps + w; t < a.T; t += gridDim.x * kWarps) {
     const float* row = a.logits + (size_t)t * a.E;
     const bool on = !a.mask || a.mask[t];
@@ -347,7 +402,7 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 8 : V <= 16 ? 4 : 2) rou
       const float tol = slack(a.sigmoid, V);
       const int unsure = select<V, kWide, float>(s, a, reinterpret_cast<float*>(sh), lane, tol, unit, mine, key, floor, taken);
       if (unsure && (unsure != 1 || !a.sigmoid || taken < a.k ||
-                     !route_near<V, kWide>(row, a, key, taken, floor, 2.f * tol * (unit + fabsf(floor)), reinterpret_cast<int*>(sh),
+                     !route_near<V, kWide>(row, a, key, floor, 2.f * tol * (unit + fabsf(floor)), reinterpret_cast<int*>(sh),
                                            lane, mine)))
         mine = route_wide<V, kWide>(row, a, sh, lane);
     }
@@ -385,7 +440,8 @@ cudaError_t launch_route(const ScoreArgs& a, cudaStream_t s, bool pdl) {
   MOE_LAUNCH(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   const bool limited = a.n_groups > 1 && a.top_groups < a.n_groups;
   const int direct = !a.bias && !(limited && a.group_top == 2 && a.E > a.n_groups);
-  const size_t smem = limited || !direct ? sizeof(double) * kWarps * std::max(a.E, 16) : 0;   // (at least 32 indices)
+  // 64 words a warp; the values of a row (in 64 bits where that may be needed) where groups go through shared memory
+  const size_t smem = sizeof(double) * kWarps * (limited ? std::max(a.E, 32) : 32);
   const int grid = std::min((a.T + kWarps - 1) / kWarps, 16 * sms);
   auto go = [&](auto v) {
     constexpr int V = decltype(v)::value;
