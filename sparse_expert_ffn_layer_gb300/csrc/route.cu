@@ -118,13 +118,52 @@ __device__ __forceinline__ void scores(F (&x)[V], int sigmoid, F& m, F& sum) {
   for (int v = 0; v < V; ++v) x[v] *= inv;
 }
 
+// The ranks of the groups in 64 bits for sigmoid scores, from the experts that may count: those not surely below their
+// group's group_top-th in 32 bits.  low: what that is for a lane's own group.  False if these are more than 32.
+template <int V, bool kWide>
+__device__ __forceinline__ bool groups_near(const float* row, const ScoreArgs& a, const float (&c)[V], float low, int M,
+                                            int per, int* sh, int lane, int& rank) {
+  int n = 0;
+  __syncwarp();
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = col_at<V, kWide>(v, lane);
+    const float l = __shfl_sync(0xffffffffu, low, min(e / M, a.n_groups - 1) * per);
+    const bool near = e < a.E && c[v] >= l;
+    const unsigned m = __ballot_sync(0xffffffffu, near);
+    const int at = n + __popc(m & ((1u << lane) - 1u));
+    if (near && at < 32) sh[at] = e;
+    n += __popc(m);
+  }
+  if (n > 32) return false;
+  __syncwarp();
+  const int e = lane < n ? sh[lane] : 0, ge = lane < n ? e / M : -1, g = lane / per;
+  const double own = sigmoid_of((double)row[e]) + (a.bias ? (double)a.bias[e] : 0.0);
+  double b1 = -INFINITY, b2 = -INFINITY;
+  for (int q = 0; q < n; ++q) {
+    const double x = __shfl_sync(0xffffffffu, own, q);
+    if (__shfl_sync(0xffffffffu, ge, q) != g) continue;
+    const double lo = x < b1 ? x : b1;
+    b1 = x > b1 ? x : b1;
+    b2 = lo > b2 ? lo : b2;
+  }
+  const uint64_t kv = key_of((a.group_top == 2 && M > 1) ? b1 + b2 : b1);
+  rank = 0;
+  for (int q = 0; q < a.n_groups; ++q) {
+    const uint64_t kw = __shfl_sync(0xffffffffu, (unsigned long long)kv, q * per);
+    rank += (kw > kv || (kw == kv && q < g)) ? 1 : 0;
+  }
+  __syncwarp();
+  return true;
+}
+
 // The k experts of largest choice; lane j < k gets expert j, lane k the first that is left out.  Says where the order is
 // not certain, because two values whose order matters are within tol (unit + |c|) of each other (tol = 0: not looked
 // at): bit 0 of the experts, bit 1 of the groups too, or in a way that needs the whole row.  key: the choices of the
 // experts in the groups.  taken, floor: how many experts were taken (fewer than k + 1 where no more are in the groups) and
 // the least of their choices.  sh: 64 words, and E values where groups go through it.
 template <int V, bool kWide, typename F>
-__device__ __forceinline__ int select(F (&c)[V], const ScoreArgs& a, F* sh, int lane, F tol, F unit, int& mine,
+__device__ __forceinline__ int select(const float* row, F (&c)[V], const ScoreArgs& a, F* sh, int lane, F tol, F unit, int& mine,
                                       typename KeyOf<F>::type (&key)[V], F& floor, int& taken) {
   using K = typename KeyOf<F>::type;
   int unsure = 0;
@@ -173,7 +212,15 @@ __device__ __forceinline__ int select(F (&c)[V], const ScoreArgs& a, F* sh, int 
       const unsigned last = __ballot_sync(0xffffffffu, g < a.n_groups && rank == a.top_groups - 1);
       const unsigned next = __ballot_sync(0xffffffffu, g < a.n_groups && rank == a.top_groups);
       const F in = __shfl_sync(0xffffffffu, value, __ffs(last) - 1), out = __shfl_sync(0xffffffffu, value, __ffs(next) - 1);
-      if (in - out <= F(2) * tol * (unit + (in < F(0) ? -in : in))) unsure |= 2;
+      if (in - out <= F(2) * tol * (unit + (in < F(0) ? -in : in))) {
+        unsure |= 2;
+        if constexpr (sizeof(F) == 4) {
+          const float least = (a.group_top == 2 && M > 1) ? b2 : b1;
+          if (a.sigmoid && groups_near<V, kWide>(row, a, c, least - 2.f * tol * (unit + fabsf(least)), M, per,
+                                                 reinterpret_cast<int*>(sh), lane, rank))
+            unsure = 0;
+        }
+      }
     }
     if (own) {
       if (rank >= a.top_groups)
@@ -308,7 +355,7 @@ __device__ __noinline__ int route_wide(const float* row, const ScoreArgs& a, dou
   uint64_t key[V];
   double floor;
   int taken;
-  select<V, kWide, double>(c, a, sh, lane, 0.0, 0.0, mine, key, floor, taken);
+  select<V, kWide, double>(row, c, a, sh, lane, 0.0, 0.0, mine, key, floor, taken);
   return mine;
 }
 
@@ -391,7 +438,7 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 8 : V <= 16 ? 4 : 2) rou
       uint32_t key[V];
       float floor;
       int taken;
-      select<V, kWide, float>(x, a, reinterpret_cast<float*>(sh), lane, 0.f, 0.f, mine, key, floor, taken);
+      select<V, kWide, float>(row, x, a, reinterpret_cast<float*>(sh), lane, 0.f, 0.f, mine, key, floor, taken);
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) s[v] += bias[v];
@@ -400,7 +447,7 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 8 : V <= 16 ? 4 : 2) rou
       float floor;
       int taken;
       const float tol = slack(a.sigmoid, V);
-      const int unsure = select<V, kWide, float>(s, a, reinterpret_cast<float*>(sh), lane, tol, unit, mine, key, floor, taken);
+      const int unsure = select<V, kWide, float>(row, s, a, reinterpret_cast<float*>(sh), lane, tol, unit, mine, key, floor, taken);
       if (unsure && (unsure != 1 || !a.sigmoid || taken < a.k ||
                      !route_near<V, kWide>(row, a, key, floor, 2.f * tol * (unit + fabsf(floor)), reinterpret_cast<int*>(sh),
                                            lane, mine)))

@@ -151,6 +151,22 @@ def test_route_near_and_exact_ties(m, sigmoid, G, top, gt):
 
 
 @pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("E,G,top,gt", [(256, 8, 4, 2), (256, 8, 3, 1), (60, 4, 2, 2), (15, 3, 1, 2), (96, 32, 7, 2),
+                                        (128, 4, 2, 1), (1024, 16, 5, 2)])
+def test_route_groups_that_hardly_differ(m, sigmoid, E, G, top, gt):
+    """Every group holds the first one's logits in another order, some a rounding apart or equal: 64 bits decide."""
+    g = gen(E + G)
+    T, M, k = 301, E // G, min(5, top * (E // G))
+    x = randn(g, T, 1, M, sigma=2.0).repeat(1, G, 1)
+    x = x.gather(2, torch.rand((T, G, M), generator=g, device="cuda").argsort(2))
+    x = x * (1 + 2.0 ** -23 * torch.randint(-1, 2, (T, G, M), generator=g, device="cuda"))
+    x = x.reshape(T, E).float().contiguous()
+    for bias in (None, torch.full((E,), 0.3, device="cuda"), randn(g, E, sigma=1e-7)):
+        assert torch.equal(run_route(m, x, k, sigmoid, bias, None, G, top, gt)[0].long(),
+                           ref_route(x, k, sigmoid, bias, G, top, gt))
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_route_extremes(m, sigmoid, renorm):
     inf = float("inf")
