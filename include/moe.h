@@ -496,7 +496,8 @@ MOE_API moe_status moe_expert_fp8_workspace_size(int T, int d, int f, int E, int
  * where b runs over blocks of 128 inputs and q brings each block of 128 of a row to e4m3 as moe_fp8_quantize
  * does a weight block (a scale that is a power of two, one rounding of each value).
  *   W1q [E, f, d], W1s [E, f / 128, d / 128], W2q [E, d, f], W2s [E, d / 128, f / 128]: as moe_fp8_quantize
- *   writes them, or with any finite float32 scales.
+ *   writes them (powers of two, which the tensor cores apply themselves where an expert has many slots), or with any
+ *   finite float32 scales.
  *   Everything else as moe_expert_ffn; workspace: moe_expert_fp8_workspace_size bytes, contents need no
  *   initialisation; the device-side status word is in it (moe_status_read).
  *   A token block that holds an infinity or a NaN makes its outputs NaN.

@@ -1,20 +1,25 @@
 // Experts in 8-bit floating point (e4m3) with a scale for each block of 128: the weights' and the rows'
-// quantisers, and the grouped products on the 5th-generation tensor cores (kind::f8f6f4, TMEM, TMA).
+// quantisers, and the grouped products on the 5th-generation tensor cores (kind::f8f6f4 and kind::mxf8f6f4, TMEM, TMA).
 //
 //   y[s, j] = sum_b sx[s, b] sw[j / 128, b] sum_{i in b} x8[s, i] w8[j, i]          (b: blocks of 128 inputs)
 //
 // Scales that this library makes are powers of two, so that bringing a value to 8 bits is one rounding: the
 // quotient is exact, and the same in any precision.  The products take any 32-bit scales.
 //
-// Products: as in the f16 form a weight tile is the MMA's M = 128 operand and a run of one expert's slots its N
-// operand, both with their inputs side by side (K-major).  A stage of the pipeline is one block of 128 inputs:
-// four MMAs whose sum goes to a TMEM slot, from where 16 warps add it, times its scale, to the running sums in
-// their registers (column n of a tile has one scale, a weight tile has one for all its rows).  So the sums over
-// blocks are in 32 bits with every scale applied before them, and a slot is free again as soon as it was read.
-// One more warp multiplies the two scales, so that the 16 do one multiply-add a value.  They read TMEM in the shape
-// in which a lane has two of each eight columns and four rows: with a row of every column a lane, each of the four
-// lane quarters took 128 N bytes of scales from shared memory a block, which with what the MMAs read and the copies
-// write there bound the kernel (N = 160: 1120 cycles a block).
+// Products, in two forms.  In both, as in the f16 form, a weight tile is the MMA's M operand and a run of one expert's slots
+// its N operand, both with their inputs side by side (K-major).
+//
+// Any scales, and short runs: a stage of the pipeline is one block of 128 inputs: four MMAs whose sum goes to a TMEM slot,
+// from where eight warps add it, times its scale, to the running sums in their registers (column n of a tile has one
+// scale, a weight tile has one for all its rows).  So the sums over blocks are in 32 bits with every scale applied before
+// them, and a slot is free again as soon as it was read.  One more warp multiplies the two scales, so that the eight do
+// one multiply-add a value.  They read TMEM in the shape in which a lane has two of each eight columns and four rows: with a
+// row of every column a lane, each of the four lane quarters took 128 N bytes of scales from shared memory a block
+// (N = 160: 1120 cycles a block, now 730).  Bound by these reads and additions: 8 experts of 2048 rows, 8192 x 8192:
+// 2340 us, 1.9 PFLOP/s.
+//
+// Scales that are powers of two, long runs: the tensor cores apply them, and nothing is added outside them (further below;
+// 1330 us for the same, 3.3 PFLOP/s).
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -164,6 +169,8 @@ __device__ __forceinline__ bool slot_table(const int32_t* offsets, int E, int S_
 // Where the scales of expert e's slots begin in a row of scales: a multiple of four, and no run reaches the next
 // (rounded up to four, a run is at least three shorter than its slots; four are added for each expert).
 __device__ __forceinline__ int scale_base(int first_slot, int e) { return ((first_slot + 3) & ~3) + 4 * e; }
+// Where block b's exponent of a place's scale is.
+__device__ __forceinline__ size_t exponent_at(int b, int place, int Sp) { return ((size_t)(b >> 2) * Sp + place) * 4 + (b & 3); }
 int scale_row(int S_max, int E) { return (S_max + 3) / 4 * 4 + 4 * (E + 1); }
 
 // ---------------------------------------------------------------- rows
@@ -173,7 +180,9 @@ constexpr int kRowPart = 8;
 __global__ void __launch_bounds__(256) fp8_rows_kernel(const __half* __restrict__ tokens, const int32_t* __restrict__ perm,
                                                        const int32_t* __restrict__ offsets, int E, int S_max, int T, int d,
                                                        int Sp, uint8_t* __restrict__ Xq, float* __restrict__ sx,
-                                                       int* status) {
+                                                       int* status, const float* __restrict__ s1,
+                                                       const float* __restrict__ s2, long long ns, uint8_t* __restrict__ xexp,
+                                                       int* general) {
   extern __shared__ int32_t offs[];
   pdl_wait();
   pdl_trigger();
@@ -198,7 +207,7 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const __half* __restrict_
       const int mid = (lo + hi) >> 1;
       if (offs[mid] <= s) lo = mid; else hi = mid;
     }
-    float* scale_at = sx + scale_base(offs[lo], lo) + (s - offs[lo]);
+    const int place = scale_base(offs[lo], lo) + (s - offs[lo]);
     uint8_t* dst = Xq + (long long)s * d + l * 8;
 #pragma unroll
     for (int i = 0; i < kRowPart / 2; ++i) {
@@ -216,17 +225,29 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const __half* __restrict_
         *reinterpret_cast<uint2*>(dst + b * 128) =
             make_uint2(fp8_four(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
                        fp8_four(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
-        if (l == 0) scale_at[(long long)b * Sp] = scale;
+        if (l == 0) {
+          sx[(size_t)b * Sp + place] = scale;
+          if (xexp) xexp[exponent_at(b, place, Sp)] = (uint8_t)(__float_as_uint(scale) >> 23);
+        }
       }
     }
   }
   if (bad) record_status(status, kErrBounds);
+  if (general) {                                 // (ns of each; NaN, as the quantiser writes it, has the exponent's form too)
+    bool other = false;
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < 2 * ns; i += gridDim.x * 256ll) {
+      const uint32_t v = __float_as_uint(i < ns ? s1[i] : s2[i - ns]);
+      other |= (v & 0x807fffffu) != 0u && v != 0x7fc00000u;
+      other |= v == 0u || v == 0x7f800000u;
+    }
+    if (__any_sync(0xffffffffu, other) && lane == 0) *general = 1;
+  }
 }
 
 // ---------------------------------------------------------------- products
 // Warps 0 to 3 load the weight tiles, issue the products, multiply the scales and load the rows; eight more add.
-// (One warp for both loads took 600 cycles a block of its own time, and bound the kernel; 16 warps for the sums had
-// too few registers each for two weight tiles.)
+// (One warp for both loads took 600 cycles a block of its own time, and bound the kernel; 16 warps for the sums are no
+// faster: TMEM's reads bound them.)
 constexpr int kEpiWarps = 8;                  // two column groups of the four TMEM lane quarters
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kABytes = 128 * 128;            // a weight tile: 128 outputs, 128 inputs
@@ -273,8 +294,11 @@ struct Fp8Args {
   int split;                   // blocks of a cluster that share an item
   uint8_t* h;                  // first product: [S_max][M], with hscale [M / 128][Sp]
   float* hscale;
+  const uint32_t* xexp;        // the scales' exponents, of four blocks a word: [K / 512][Sp], and of h (by bytes)
+  uint8_t* hexp;
   __half* out;                 // second: [S_max][M]
   int* status;
+  const int* general;          // not null: which of two forms runs (not 0: the one for any scales)
 };
 
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -382,6 +406,60 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
   return ok != 0;
 }
 
+// Pairs of blocks (two neighbours of a cluster, the first one issues): products of 256 weight rows, 128 in each block's
+// shared memory and TMEM, with rows of which each block holds half; loads that complete on the first block's barrier;
+// arrivals on the same barrier of both blocks once the products so far are done.
+__device__ __forceinline__ void mma_mx_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void load_rows_pair(void* smem, const CUtensorMap* m, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(smem)),
+      "l"(m), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void load_weight_tile_pair(void* smem, const CUtensorMap* m, int x, int group, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(smem)),
+      "l"(m), "r"(x), "r"(0), "r"(0), "r"(group), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* holder) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(holder)) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr));
+}
+// 32 lanes of a quarter: a column, or eight, of 32-bit words.
+__device__ __forceinline__ void tmem_st4(uint32_t t, uint32_t w) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%1,%1,%1};" ::"r"(t), "r"(w) : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t (&w)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// An arrival at another block's barrier with no memory to publish but TMEM's, which the fence before it orders.
+__device__ __forceinline__ void arrive_remote_tmem(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // As mbar_wait_bounded; the clock is read only by a wait that is long already.
 template <bool kCluster = false>
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
@@ -443,9 +521,9 @@ __device__ __forceinline__ float2 gelu2(float2 x) {
   return mul2(x, r);
 }
 
-// The rows by boxes of 128, 64 and 32 of them.
+// The rows by boxes of 128, 64 and 32 of them; of long runs, of 24, 48, .. 120.
 struct RowMaps {
-  CUtensorMap box[3];
+  CUtensorMap box[5];
 };
 
 struct Tile8 {
@@ -471,6 +549,85 @@ __device__ __forceinline__ Tile8 tile_at(int i, const int32_t* prefix, const int
   t.sc0 = scale_base(offs[lo], lo) + c * per;
   t.n = min(per, rows - c * per);
   return t;
+}
+
+// What becomes of a warp's sums: acc[c][j] has rows lr + 8 j of the quarter's 32 (four neighbouring outputs) and columns lc and
+// lc + 1 of eight.  kExp: h's scales as exponents.  cw: groups of eight columns of each warp; am: [column][quarter], invs: the warp's columns.
+template <int C8, bool kGelu, bool kExp>
+__device__ __forceinline__ void finish(float2 (&acc)[C8][4], const Tile8& t, const Fp8Args& a, int cw, int col0, int q, int g, int lane,
+                                       uint32_t* am, float* invs, bool ok) {
+  const int lr = lane >> 2, lc = 2 * (lane & 3);
+        const size_t tile0 = (size_t)t.row0 * a.M + t.mt * 128 + 32 * q + 4 * lr;   // this lane's four outputs of a slot
+        if constexpr (kGelu) {
+          // GeLU, the largest magnitude of each slot's 128 columns (four warps), and 8 bits
+  #pragma unroll
+          for (int c = 0; c < C8; ++c) {
+            if (c >= cw) continue;
+            float m0 = 0.f, m1 = 0.f;
+  #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              acc[c][j] = gelu2(acc[c][j]);
+              m0 = max_nan(m0, acc[c][j].x);
+              m1 = max_nan(m1, acc[c][j].y);
+            }
+            uint32_t b0 = __float_as_uint(m0), b1 = __float_as_uint(m1);
+  #pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              b0 = max(b0, __shfl_xor_sync(0xffffffffu, b0, o));
+              b1 = max(b1, __shfl_xor_sync(0xffffffffu, b1, o));
+            }
+            if (lr == 0) {
+              am[(col0 + c * 8 + lc) * 4 + q] = b0;
+              am[(col0 + c * 8 + lc + 1) * 4 + q] = b1;
+            }
+          }
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
+          if (!ok) return;
+          // a lane makes the scale of a column, for its whole warp
+          for (int c = lane; c < 8 * cw; c += 32) {
+            const int col = col0 + c;
+            const uint4 r = *reinterpret_cast<const uint4*>(am + col * 4);
+            float scale, inv;
+            fp8_scale(max(max(r.x, r.y), max(r.z, r.w)), scale, inv);
+            invs[c] = inv;
+            if (q == 0 && col < t.n) {
+              if (kExp) a.hexp[exponent_at(t.mt, t.sc0 + col, a.Sp)] = (uint8_t)(__float_as_uint(scale) >> 23);
+              else a.hscale[(size_t)t.mt * a.Sp + t.sc0 + col] = scale;
+            }
+          }
+          __syncwarp();
+          uint8_t* dst = a.h + tile0 + (size_t)(col0 + lc) * a.M;
+  #pragma unroll
+          for (int c = 0; c < C8; ++c) {
+            if (c >= cw) continue;
+            const float2 inv = *reinterpret_cast<const float2*>(invs + c * 8 + lc);
+            float2 v[4];
+  #pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = mul2(acc[c][j], inv);
+            const int col = col0 + c * 8 + lc;
+            if (col < t.n) *reinterpret_cast<uint32_t*>(dst) = fp8_four(v[0].x, v[1].x, v[2].x, v[3].x);
+            if (col + 1 < t.n) *reinterpret_cast<uint32_t*>(dst + a.M) = fp8_four(v[0].y, v[1].y, v[2].y, v[3].y);
+            dst += 8 * (size_t)a.M;
+          }
+          __syncwarp();                            // (the warp's scales are written again with the next item)
+        } else {
+          if (!ok) return;
+  #pragma unroll
+          for (int c = 0; c < C8; ++c) {
+            if (c >= cw) continue;
+  #pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              const int col = col0 + c * 8 + lc + p;
+              if (col < t.n) {
+                const float2 (&v)[4] = acc[c];
+                const __half2 lo = p ? __floats2half2_rn(v[0].y, v[1].y) : __floats2half2_rn(v[0].x, v[1].x);
+                const __half2 hi = p ? __floats2half2_rn(v[2].y, v[3].y) : __floats2half2_rn(v[2].x, v[3].x);
+                *reinterpret_cast<uint2*>(a.out + tile0 + (size_t)col * a.M) =
+                    make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+              }
+            }
+          }
+        }
 }
 
 // C8: groups of eight columns per warp (a tile has up to 16 C8 rows).  kGelu: first product.  kSplit: a cluster of
@@ -516,6 +673,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_alloc(holder, 512);
   pdl_wait();
   pdl_trigger();
+  if (a.general && *a.general == 0) {            // (the form for scales that are powers of two has run)
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(*holder, 512);
+    return;
+  }
   if (warp == 2 && slot_table<(C8 <= 4 ? 8 : 1)>(a.offsets, a.E, a.S_max, NMAX, offs, prefix)) record_status(a.status, kErrBounds);
   tc_fence_before();
   __syncthreads();
@@ -690,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_up<224>();
     // ------------------------------------------------------------ sums
     const int q = warp & 3, g = (warp - 4) >> 2;
-    const int lr = lane >> 2, lc = 2 * (lane & 3);   // TMEM rows lr + 8 j of the quarter's 32, columns lc, lc + 1 of eight
+    const int lc = 2 * (lane & 3);
     const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
     int slot = 0;
     uint32_t ap = 0;
@@ -761,76 +923,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      const size_t tile0 = (size_t)t.row0 * a.M + t.mt * 128 + 32 * q + 4 * lr;   // this lane's four outputs of a slot
-      if constexpr (kGelu) {
-        // GeLU, the largest magnitude of each slot's 128 columns (four warps), and 8 bits
-        uint32_t* am = reinterpret_cast<uint32_t*>(sm + L.amax_off) + turn * (NMAX * 4);
-#pragma unroll
-        for (int c = 0; c < C8; ++c) {
-          if (c >= cw) continue;
-          float m0 = 0.f, m1 = 0.f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            acc[c][j] = gelu2(acc[c][j]);
-            m0 = max_nan(m0, acc[c][j].x);
-            m1 = max_nan(m1, acc[c][j].y);
-          }
-          uint32_t b0 = __float_as_uint(m0), b1 = __float_as_uint(m1);
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) {
-            b0 = max(b0, __shfl_xor_sync(0xffffffffu, b0, o));
-            b1 = max(b1, __shfl_xor_sync(0xffffffffu, b1, o));
-          }
-          if (lr == 0) {
-            am[(col0 + c * 8 + lc) * 4 + q] = b0;
-            am[(col0 + c * 8 + lc + 1) * 4 + q] = b1;
-          }
-        }
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
-        if (!ok) continue;
-        // a lane makes the scale of a column, for its whole warp
-        float* invs = reinterpret_cast<float*>(sm + L.inv_off) + (warp - 4) * (8 * C8);
-        for (int c = lane; c < 8 * cw; c += 32) {
-          const int col = col0 + c;
-          const uint4 r = *reinterpret_cast<const uint4*>(am + col * 4);
-          float scale, inv;
-          fp8_scale(max(max(r.x, r.y), max(r.z, r.w)), scale, inv);
-          invs[c] = inv;
-          if (q == 0 && col < t.n) a.hscale[(size_t)t.mt * a.Sp + t.sc0 + col] = scale;
-        }
-        __syncwarp();
-        uint8_t* dst = a.h + tile0 + (size_t)(col0 + lc) * a.M;
-#pragma unroll
-        for (int c = 0; c < C8; ++c) {
-          if (c >= cw) continue;
-          const float2 inv = *reinterpret_cast<const float2*>(invs + c * 8 + lc);
-          float2 v[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = mul2(acc[c][j], inv);
-          const int col = col0 + c * 8 + lc;
-          if (col < t.n) *reinterpret_cast<uint32_t*>(dst) = fp8_four(v[0].x, v[1].x, v[2].x, v[3].x);
-          if (col + 1 < t.n) *reinterpret_cast<uint32_t*>(dst + a.M) = fp8_four(v[0].y, v[1].y, v[2].y, v[3].y);
-          dst += 8 * (size_t)a.M;
-        }
-        __syncwarp();                            // (the warp's scales are written again with the next item)
-      } else {
-        if (!ok) continue;
-#pragma unroll
-        for (int c = 0; c < C8; ++c) {
-          if (c >= cw) continue;
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const int col = col0 + c * 8 + lc + p;
-            if (col < t.n) {
-              const float2 (&v)[4] = acc[c];
-              const __half2 lo = p ? __floats2half2_rn(v[0].y, v[1].y) : __floats2half2_rn(v[0].x, v[1].x);
-              const __half2 hi = p ? __floats2half2_rn(v[2].y, v[3].y) : __floats2half2_rn(v[2].x, v[3].x);
-              *reinterpret_cast<uint2*>(a.out + tile0 + (size_t)col * a.M) =
-                  make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-            }
-          }
-        }
-      }
+      float* invs = reinterpret_cast<float*>(sm + L.inv_off) + (warp - 4) * (8 * C8);
+      uint32_t* am = reinterpret_cast<uint32_t*>(sm + L.amax_off) + turn * (NMAX * 4);
+      finish<C8, kGelu, false>(acc, t, a, cw, col0, q, g, lane, am, invs, ok);
     }
   }
   // ------------------------------------------------------------ end
@@ -855,12 +950,321 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (kSplit) cluster_meet();          // no block leaves while another may still write to its shared memory
 }
 
+// ---------------------------------------------------------------- products of long runs, scales that are powers of two
+// The tensor cores apply such scales themselves (kind::mxf8f6f4: a scale for each 32 inputs of a row, as an exponent), so a
+// tile's sum stays in TMEM over all its inputs.  A pair of blocks takes 256 outputs and up to 240 rows: each loads its own
+// weight tile and half of the rows, and has the sums of its 128 outputs in its own TMEM, two items' by turns, which other
+// warps bring out while the next item's products run.
+// Scales lie in TMEM as words, four blocks' exponents each: word (lane l, column i) is row 32 i + l's, in each quarter.
+// Bound by the tensor cores with many inputs (490 cycles a block of 240 rows; their own rate needs 480), by GeLU and the
+// stores with few (2048: 25 % more), by DRAM where an expert has few rows.  What counts a block is what a warp issues:
+// rows in four copies, not one, took 560 cycles and bound the kernel (2340 -> 1610 -> 1400 us with one copy).
+constexpr int kLongRows = 240;
+constexpr int kLongGroups = 3;                // of columns, each for the four warps of the TMEM lane quarters
+constexpr int kLongThreads = 256 + 128 * kLongGroups;   // weight tiles, products, -, rows; four warps for scales; results
+constexpr int kLongBox = 24;                  // rows are loaded by boxes of 24, 48 .. 120: each copy costs its warp 120 cycles
+constexpr uint32_t kLongStage = kABytes + kLongRows / 2 * 128;
+constexpr uint32_t kScaleCols = 2 * kLongRows;   // two sets of 16 columns: four for the weight tile, eight for the rows
+struct LongSmem {
+  uint32_t amax_off, inv_off, bars_off, misc_off, total;
+};
+__host__ __device__ inline LongSmem long_smem(int stages, int E) {
+  LongSmem L;
+  uint32_t off = (uint32_t)stages * kLongStage;
+  L.amax_off = off;
+  off += 2u * kLongRows * 16u;
+  L.inv_off = off;
+  off += 4u * kLongRows * 4u;
+  L.bars_off = off;
+  off += (2u * kMaxStages + 9u) * 8u;
+  L.misc_off = (off + 15u) & ~15u;
+  L.total = L.misc_off + 16u + 8u * (uint32_t)(E + 1) + 1024u;
+  return L;
+}
+
+template <bool kGelu>
+__global__ void __launch_bounds__(kLongThreads, 1)
+    fp8_long_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ RowMaps tmB, const Fp8Args a) {
+  constexpr int C8 = kLongRows / 8 / kLongGroups, CH = 5;   // groups of eight columns per warp
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  const LongSmem L = long_smem(a.na, a.E);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + L.bars_off);
+  uint64_t *empty = full + kMaxStages, *acc_full = empty + kMaxStages, *acc_empty = acc_full + 2, *sc_full = acc_empty + 2,
+           *sc_empty = sc_full + 2, *spare = sc_empty + 2;
+  uint32_t* holder = reinterpret_cast<uint32_t*>(sm + L.misc_off);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L.misc_off + 4);
+  int32_t* prefix = reinterpret_cast<int32_t*>(sm + L.misc_off + 16);
+  int32_t* offs = prefix + a.E + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = blockIdx.x & 1;
+  if (warp == 0) {
+    if (lane < a.na) {
+      mbar_init(&full[lane], 2);                 // (the first block's two loading warps)
+      mbar_init(&empty[lane], 1);
+    }
+    if (lane < 2) {
+      mbar_init(&acc_full[lane], 1);
+      mbar_init(&acc_empty[lane], 8 * kLongGroups);   // both blocks' warps
+      mbar_init(&sc_full[lane], 8);
+      mbar_init(&sc_empty[lane], 1);
+    }
+    if (lane == 0) {
+      mbar_init(spare, 1);
+      *abort_flag = 0;
+    }
+    fence_mbar_init();
+    if (lane == 0) prefetch_tmap(&tmA);
+  }
+  if (warp == 3 && lane < 5) prefetch_tmap(&tmB.box[lane]);
+  pdl_wait();
+  pdl_trigger();
+  if (*a.general) return;                        // (all blocks: the other form runs)
+  if (warp == 1) tmem_alloc_pair(holder);
+  if (warp == 2 && slot_table<1>(a.offsets, a.E, a.S_max, kLongRows, offs, prefix)) record_status(a.status, kErrBounds);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_meet();                                // the other's barriers are set up, and it is there
+  const uint32_t tmem = *holder;
+  const int mt = a.M / 128, nkb = a.K / 128, pairs = gridDim.x / 2, total = prefix[a.E] * (mt / 2);
+  auto item = [&](int i) {
+    Tile8 t = tile_at(i, prefix, offs, a.E, mt / 2, kLongRows);
+    t.mt = 2 * t.mt + part;
+    return t;
+  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(bar, parity, abort_flag, a.status)); };
+  uint32_t issued = 0, issued_par = 0;           // ring places with a load in flight, for the end
+  bool ok = true;
+  if (warp < 8) {
+    regs_down<64>();
+    if (warp == 0 || warp == 3) {
+      // ---------------------------------------------------------- weight tiles, rows
+      // (run by whole warps, and one lane issues: the values stay uniform)
+      int st = 0;
+      uint32_t sp = 1;
+      for (int i = blockIdx.x / 2; i < total && ok; i += pairs) {
+        const Tile8 t = item(i);
+        const int agroup = t.e * (a.M / 32) + t.mt * 4, half = ((t.n + 15) & ~15) / 2, y = t.row0 + part * half,
+                    box = (half - 1) / kLongBox;
+        for (int kb = 0; kb < nkb; ++kb) {
+          ok = wait(&empty[st], sp);
+          if (!ok) break;
+          issued |= 1u << st;
+          issued_par = (issued_par & ~(1u << st)) | (sp ^ 1u) << st;
+          uint8_t* to = sm + st * kLongStage;
+          if (elect_one()) {                     // (what lands before the first block expects it counts all the same)
+            const uint32_t bar = first_block(smem_u32(&full[st]));
+            if (warp == 0) {
+              if (part == 0) mbar_expect_tx(&full[st], 2 * kABytes);
+              load_weight_tile_pair(to, &tmA, kb * 128, agroup, bar);
+            } else {
+              if (part == 0) mbar_expect_tx(&full[st], (uint32_t)(box + 1) * (2 * kLongBox * 128));
+              load_rows_pair(to + kABytes, &tmB.box[box], kb * 128, y, bar);
+            }
+          }
+          if (++st == a.na) {
+            st = 0;
+            sp ^= 1u;
+          }
+        }
+      }
+      for (int n = 0; n < a.na && ok; ++n) {     // the first block's last arrivals here
+        ok = wait(&empty[st], sp);
+        if (++st == a.na) {
+          st = 0;
+          sp ^= 1u;
+        }
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- products
+      int st = 0, set = 0, turn = 0;
+      uint32_t fp = 0, scp = 0, ap = 1;
+      const uint64_t d0 = smem_desc(smem_u32(sm), 16, 1024, 2);
+      for (int i = blockIdx.x / 2; i < total && ok && part == 0; i += pairs) {
+        // e4m3 both, exponents as scales, 256 outputs; which of a word's four is in bits 4 and 29
+        const uint32_t idesc = 1u << 23 | (uint32_t)((item(i).n + 15) >> 4) << 18 | 16u << 24;
+        for (int kb = 0; kb < nkb; ++kb) {
+          const int j = kb & 3;
+          // rows and weight tiles, scales, a free place for the sum: a lane waits for each
+          uint64_t* bar = lane == 1 && j == 0 ? &sc_full[set] : lane == 2 && kb == 0 ? &acc_empty[turn] : &full[st];
+          ok = wait(bar, lane == 1 && j == 0 ? scp : lane == 2 && kb == 0 ? ap : fp);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t ad = d0 + (uint64_t)(st * (kLongStage >> 4)), bd = ad + (kABytes >> 4);
+          const uint32_t id = idesc | (uint32_t)j << 4 | (uint32_t)j << 29, sc = tmem + kScaleCols + 16 * set;
+          const bool last = kb + 1 == nkb, group = j == 3 || last;
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_mx_pair(tmem + turn * kLongRows, ad + 2 * k, bd + 2 * k, id, sc, sc + 4, kb + k ? 1u : 0u);
+            commit_pair(&empty[st]);
+            if (group) commit_pair(&sc_empty[set]);
+            if (last) commit_pair(&acc_full[turn]);
+          }
+          if (++st == a.na) {
+            st = 0;
+            fp ^= 1u;
+          }
+          if (group) {
+            set ^= 1;
+            if (set == 0) scp ^= 1u;
+          }
+        }
+        turn ^= 1;
+        if (turn == 0) ap ^= 1u;
+      }
+    } else if (warp >= 4) {
+      // ---------------------------------------------------------- scales
+      // Loads run kAhead groups of four blocks ahead of their use, over the ends of items.
+      constexpr int kAhead = 3;
+      const uint32_t at = tmem + kScaleCols + ((uint32_t)(32 * (warp - 4)) << 16);
+      int li = blockIdx.x / 2, lkb = 0, left = 0, set = 0;
+      uint32_t sp = 1, w[kAhead] = {}, x[kAhead][8] = {};
+      Tile8 t = {};
+      if (li < total) t = item(li);
+      auto load = [&](uint32_t& w, uint32_t (&x)[8]) {
+        if (li >= total) return;
+        ++left;
+        w = lane < 4 && lkb + lane < nkb
+                ? (__float_as_uint(__ldg(a.wscale + ((size_t)t.e * mt + t.mt) * nkb + lkb + lane)) >> 23) : 0u;
+        const uint32_t* src = a.xexp + (size_t)(lkb / 4) * a.Sp + t.sc0 + lane;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (32 * c + lane < t.n) x[c] = __ldcg(src + 32 * c);
+        lkb += 4;
+        if (lkb >= nkb) {
+          lkb = 0;
+          li += pairs;
+          if (li < total) t = item(li);
+        }
+      };
+#pragma unroll
+      for (int b = 0; b < kAhead; ++b) load(w[b], x[b]);
+      while (left > 0 && ok) {
+#pragma unroll
+        for (int b = 0; b < kAhead; ++b) {
+          if (left == 0 || !ok) break;
+          --left;
+          ok = wait(&sc_empty[set], sp);
+          if (!ok) break;
+          const uint32_t word = __reduce_or_sync(0xffffffffu, (w[b] & 0xffu) << (8 * (lane & 3)));
+          tc_fence_after();
+          tmem_st4(at + 16 * set, word);
+          tmem_st8(at + 16 * set + 4, x[b]);
+          tmem_stored();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (part == 0) mbar_arrive(&sc_full[set]);
+            else arrive_remote_tmem(first_block(smem_u32(&sc_full[set])));
+          }
+          set ^= 1;
+          if (set == 0) sp ^= 1u;
+          load(w[b], x[b]);
+        }
+      }
+      for (int n = 0; n < 2 && ok; ++n) {        // the first block's last arrivals here
+        ok = wait(&sc_empty[set], sp);
+        set ^= 1;
+        if (set == 0) sp ^= 1u;
+      }
+    }
+  } else {
+    regs_up<112>();
+    // ------------------------------------------------------------ results
+    const int q = warp & 3, g = (warp - 8) >> 2;
+    const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
+    int turn = 0;
+    uint32_t ap = 0;
+    // a warp whose wait gives up still meets the others at every item's barrier
+    for (int i = blockIdx.x / 2; i < total; i += pairs) {
+      const Tile8 t = item(i);
+      const int cw = (t.n + 8 * kLongGroups - 1) / (8 * kLongGroups);   // groups of eight columns of each warp of this tile
+      if (ok) ok = wait(&acc_full[turn], ap);
+      tc_fence_after();
+#pragma unroll 1
+      for (int c0 = 0; c0 < cw; c0 += CH) {      // (a few columns at a time, so that the registers hold them)
+        const int col0 = 8 * (g * cw + c0);
+        uint32_t v[2][4 * CH];
+        float2 acc[CH][4];
+        if (ok) {
+          tmem_ld32<CH>(tq + turn * kLongRows + col0, v);
+          tmem_wait<CH>(v);
+          if (c0 + CH >= cw) {                   // read: the place may take the next sum
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (part == 0) mbar_arrive(&acc_empty[turn]);
+              else arrive_remote_tmem(first_block(smem_u32(&acc_empty[turn])));
+            }
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[c][j] = pair(v[j >> 1][4 * c + 2 * (j & 1)], v[j >> 1][4 * c + 2 * (j & 1) + 1]);
+        finish<CH, kGelu, true>(acc, t, a, min(cw - c0, CH), col0, q, g, lane,
+                                reinterpret_cast<uint32_t*>(sm + L.amax_off) + turn * (kLongRows * 4),
+                                reinterpret_cast<float*>(sm + L.inv_off) + (warp - 8) * (8 * C8), ok);
+      }
+      turn ^= 1;
+      if (turn == 0) ap ^= 1u;
+    }
+  }
+  // ------------------------------------------------------------ end
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (*abort_flag) {
+    // what is still in flight lands before its memory is released (bounded)
+    if (part == 0 && warp == 0 && lane == 0)
+      for (int st = 0; st < a.na; ++st)
+        if (issued >> st & 1u) mbar_drain(&full[st], issued_par >> st & 1u);
+    if (part == 0 && warp == 1) {
+      if (elect_one()) commit_pair(spare);       // (the lane that issued the products)
+      __syncwarp();
+      if (lane == 0) mbar_drain(spare, 0);
+    }
+    if (threadIdx.x == 64) {                     // the other block's loads, which this one may not have expected
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 1000000ull) {}
+    }
+  }
+  __syncwarp();
+  cluster_meet();                                // both are done: no arrival or load is on its way to either
+  if (warp == 1) tmem_dealloc_pair(tmem);
+  cluster_meet();
+}
+
 // Ring lengths: as many runs of rows as fit beside as many weight tiles (at most kMaxStages), the rest for weight tiles.
 bool fp8_rings(int nmax, int E, int split, int smem, int* na, int* nb) {
   const int fixed = (int)fp8_smem(nmax, 0, 0, E, split).total, row_bytes = nmax * 128;
   *nb = std::min(kMaxStages, (smem - fixed) / (kABytes + row_bytes));
   *na = std::min(kMaxStages, (smem - fixed - *nb * row_bytes) / kABytes);
   return *nb >= 2;
+}
+
+template <typename Kern>
+cudaError_t launch_cluster(Kern kern, int blocks, int sms, int threads, size_t bytes, cudaStream_t s, const CUtensorMap& A,
+                           const RowMaps& B, const Fp8Args& a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sms / blocks * blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = blocks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, A, B, a);
+  if (err == cudaSuccess) launch_counter().fetch_add(1, std::memory_order_relaxed);
+  return err;
 }
 
 template <int C8, bool G, bool Z>
@@ -871,23 +1275,7 @@ cudaError_t launch_one(const CUtensorMap& A, const RowMaps& B, Fp8Args a, int sm
   a.nslots = std::min(kMaxSlots, 512 / (16 * C8));
   const size_t bytes = std::max<size_t>(fp8_smem(16 * C8, a.na, a.nb, a.E, a.split).total, kMinSmem);
   if (!Z) return launch_k(kern, sms, kThreads, bytes, s, true, A, B, a);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sms / a.split * a.split);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = a.split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, A, B, (const Fp8Args)a);
-  if (err == cudaSuccess) launch_counter().fetch_add(1, std::memory_order_relaxed);
-  return err;
+  return launch_cluster(kern, a.split, sms, kThreads, bytes, s, A, B, a);
 }
 
 // Where a short batch's items leave more than half of the SMs idle, clusters of two, four or eight blocks share them
@@ -913,10 +1301,19 @@ cudaError_t launch_gemm(int c8, const CUtensorMap& A, const RowMaps& B, const Fp
   return cudaErrorInvalidValue;
 }
 
+template <bool G>
+cudaError_t launch_long(const CUtensorMap& A, const RowMaps& B, Fp8Args a, int sms, int smem, cudaStream_t s) {
+  auto kern = fp8_long_kernel<G>;
+  MOE_LAUNCH(ensure_smem_attr(reinterpret_cast<const void*>(kern)));
+  a.na = std::min(kMaxStages, (smem - (int)long_smem(0, a.E).total) / (int)kLongStage);
+  if (a.na < 2) return cudaErrorInvalidValue;
+  return launch_cluster(kern, 2, sms, kLongThreads, std::max<size_t>(long_smem(a.na, a.E).total, kMinSmem), s, A, B, a);
+}
+
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct Fp8Ws {
-  size_t x, sx, h, sh, total;
+  size_t x, sx, h, sh, ex, eh, total;          // ex, eh: exponents of the scales
   int Sp;
 };
 Fp8Ws fp8_ws(int d, int f, int E, int S_max) {
@@ -927,7 +1324,9 @@ Fp8Ws fp8_ws(int d, int f, int E, int S_max) {
   w.sx = w.x + up256(S * d);
   w.h = w.sx + up256((size_t)w.Sp * (d / 128) * 4);
   w.sh = w.h + up256(S * f);
-  w.total = w.sh + up256((size_t)w.Sp * (f / 128) * 4);
+  w.ex = w.sh + up256((size_t)w.Sp * (f / 128) * 4);
+  w.eh = w.ex + up256((size_t)w.Sp * ((d + 511) / 512) * 4);
+  w.total = w.eh + up256((size_t)w.Sp * ((f + 511) / 512) * 4);
   return w;
 }
 
@@ -952,12 +1351,10 @@ cudaError_t launch_fp8_ffn(const void* tokens, const int32_t* perm, const int32_
   MOE_LAUNCH(cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev));
   const Fp8Ws w = fp8_ws(d, f, E, S_max);
   int* status = reinterpret_cast<int*>(ws);
-  MOE_LAUNCH(cudaMemsetAsync(status, 0, sizeof(int), s));
+  int* general = status + 1;
+  MOE_LAUNCH(cudaMemsetAsync(status, 0, 2 * sizeof(int), s));
   uint8_t *x = ws + w.x, *h = ws + w.h;
   float *sx = reinterpret_cast<float*>(ws + w.sx), *sh = reinterpret_cast<float*>(ws + w.sh);
-  MOE_LAUNCH(launch_k(fp8_rows_kernel, (unsigned)std::min<long long>(((long long)S_max * ((d / 128 + kRowPart - 1) / kRowPart) + 7) / 8, 8 * sms), 256,
-                      (E + 1) * sizeof(int32_t), s,
-                      false, static_cast<const __half*>(tokens), perm, offsets, E, S_max, T, d, w.Sp, x, sx, status));
   // Rows per tile.  Slots that are no multiple of the tokens come from a capacity, S_max / E for each expert; otherwise
   // those of an expert that is two standard deviations fuller than the average one.  us of both products: 160 slots
   // each, 128 experts of the 2.4B layer: tiles of 160 rows (three sums in TMEM) 2514, of 192 (two sums) 2810; 160 on
@@ -967,11 +1364,24 @@ cudaError_t launch_fp8_ffn(const void* tokens, const int32_t* perm, const int32_
   const double mean = (double)S_max / E;
   const int rows = (int)std::min<double>(S_max, S_max % T && S_max % E == 0 ? mean : mean + 2.0 * std::sqrt(mean) + 1.0);
   const int c8 = rows <= 32 ? 2 : rows <= 64 ? 4 : rows <= 128 ? 8 : rows <= 160 || rows > 192 ? 10 : 12;
+  // Long runs (from 65 slots on): the form for scales that are powers of two, where the rows' kernel finds no other scale, else
+  // the one for any.  64 experts of 512 rows on average, 2048 x 2048: 460 -> 276 us; 128 experts of 160 rows, 3584 x 14336:
+  // 2390 -> 2182.
+  const bool long_form = c8 >= 8 && d % 256 == 0 && f % 256 == 0;
+  MOE_LAUNCH(launch_k(fp8_rows_kernel, (unsigned)std::min<long long>(((long long)S_max * ((d / 128 + kRowPart - 1) / kRowPart) + 7) / 8, 8 * sms), 256,
+                      (E + 1) * sizeof(int32_t), s,
+                      false, static_cast<const __half*>(tokens), perm, offsets, E, S_max, T, d, w.Sp, x, sx, status,
+                      W1s, W2s, (long long)E * (d / 128) * (f / 128), long_form ? ws + w.ex : nullptr,
+                      long_form ? general : nullptr));
   CUtensorMap A1, A2;
   RowMaps B1, B2;
   bool maps = encode_weight_map(&A1, W1q, d, (uint64_t)E * f) && encode_weight_map(&A2, W2q, f, (uint64_t)E * d);
   for (int i = 0; i < 3; ++i)
     maps = maps && encode_u8_map(&B1.box[i], x, d, S_max, 128, 128 >> i) && encode_u8_map(&B2.box[i], h, f, S_max, 128, 128 >> i);
+  RowMaps L1, L2;
+  for (int i = 0; i < 5 && long_form; ++i)
+    maps = maps && encode_u8_map(&L1.box[i], x, d, S_max, 128, kLongBox * (i + 1)) &&
+           encode_u8_map(&L2.box[i], h, f, S_max, 128, kLongBox * (i + 1));
   if (!maps)
     return cudaErrorInvalidValue;
   Fp8Args g;
@@ -988,12 +1398,18 @@ cudaError_t launch_fp8_ffn(const void* tokens, const int32_t* perm, const int32_
   g.M = f;
   g.h = h;
   g.hscale = sh;
+  g.general = long_form ? general : nullptr;
+  g.xexp = reinterpret_cast<const uint32_t*>(ws + w.ex);
+  g.hexp = ws + w.eh;
+  if (long_form) MOE_LAUNCH(launch_long<true>(A1, L1, g, sms, smem, s));
   MOE_LAUNCH(launch_gemm<true>(c8, A1, B1, g, sms, smem, s));
   g.wscale = W2s;
   g.xscale = sh;
+  g.xexp = reinterpret_cast<const uint32_t*>(ws + w.eh);
   g.K = f;
   g.M = d;
   g.out = static_cast<__half*>(out);
+  if (long_form) MOE_LAUNCH(launch_long<false>(A2, L2, g, sms, smem, s));
   return launch_gemm<false>(c8, A2, B2, g, sms, smem, s);
 }
 

@@ -408,13 +408,14 @@ def gelu(x):
     return torch.nn.functional.gelu(x, approximate="tanh")
 
 
-def ref_ffn8(x, W1, W2, d, f):
+def ref_ffn8(x, W1, W2, d, f, whole=False):
     """Rows of one expert in 64 bits, and how far the 32-bit calculation may be off: what a hidden value may be off by
     moves its 8-bit value where a border is within that."""
     x = rows8(x.double())
     u, mag = x @ W1.t(), x.abs() @ W1.abs().t()
-    # 128 products of a block in the tensor cores (2 u each addition), the block's scale (2 u) and d / 128 sums
-    eu = (2 * 128 + 4 + d / 128) * U * mag
+    # 128 products of a block in the tensor cores (2 u each addition), the block's scale (2 u) and d / 128 sums; whole: all
+    # d in the tensor cores, whose scales are exact
+    eu = (2 * d if whole else 2 * 128 + 4 + d / 128) * U * mag
     h = gelu(u)
     # |gelu'| <= 1.13; gelu's own steps: three roundings of its exponent z, 3 |z| ln 2 u with |z| <= 29 (beyond that the value
     # is below 1e-8 of the argument): 60 u, the exponential 2 ulp, a sum, a reciprocal and a product: 8 u
@@ -424,7 +425,7 @@ def ref_ffn8(x, W1, W2, d, f):
     # (lo and hi are taken with the scales of their own rows: a scale at the border moves all its block)
     move = torch.maximum((hi - q).abs(), (lo - q).abs())
     y = q @ W2.t()
-    tol = move @ W2.abs().t() + (2 * 128 + 4 + f / 128) * U * ((q.abs() + move) @ W2.abs().t())
+    tol = move @ W2.abs().t() + (2 * f if whole else 2 * 128 + 4 + f / 128) * U * ((q.abs() + move) @ W2.abs().t())
     return y, tol
 
 
@@ -436,14 +437,14 @@ LAYOUTS = [[1], [5], [16], [17, 0, 1], [0, 0, 3, 0], [33, 64, 1], [0] * 7 + [2],
 @pytest.mark.parametrize("rows", LAYOUTS, ids=str)
 @pytest.mark.parametrize("d,f", [(128, 128), (256, 640), (640, 256)])
 @pytest.mark.parametrize("spare", [0, 37])
-def test_expert_ffn_fp8(m, rows, d, f, spare):
+def test_expert_ffn_fp8(m, rows, d, f, spare, general=True):
     E, S = len(rows), sum(rows)
     g = gen(S * 3 + E + d)
     T = max(1, S // 2 + 3)
     x = randn(g, T, d, dtype=torch.float16)
     perm = torch.randint(0, T, (S + spare,), generator=g, device="cuda").to(torch.int32)
     offsets = torch.tensor([0] + list(np.cumsum(rows)), dtype=torch.int32, device="cuda")
-    W1, s1 = experts8(m, g, E, d, f, general=True)
+    W1, s1 = experts8(m, g, E, d, f, general=general)
     W2, s2 = experts8(m, g, E, f, d)
     out = torch.full((S + spare + 2, d), 7.5, dtype=torch.float16, device="cuda")
     ws = torch.full((m.moe_expert_fp8_workspace_size(T, d, f, E, S + spare, torch.float16),), 0xA5, dtype=torch.uint8,
@@ -454,7 +455,8 @@ def test_expert_ffn_fp8(m, rows, d, f, spare):
     at = 0
     for e, n in enumerate(rows):
         if n:
-            want, tol = ref_ffn8(x[perm[at:at + n].long()], values8(W1[e], s1[e]), values8(W2[e], s2[e]), d, f)
+            want, tol = ref_ffn8(x[perm[at:at + n].long()], values8(W1[e], s1[e]), values8(W2[e], s2[e]), d, f,
+                                 whole=not general)
             check(out[at:at + n], want, tol + half(torch.float16) * want.abs() + 2.0 ** -25, f"expert {e}")
         at += n
     again = torch.full_like(out, 7.5)
@@ -467,6 +469,46 @@ def test_expert_ffn_fp8(m, rows, d, f, spare):
 def test_expert_ffn_fp8_short_batches(m, rows, d, f):
     """Few items with many inputs each: shared by clusters of two, four and eight blocks."""
     test_expert_ffn_fp8(m, rows, d, f, 2)
+
+
+@pytest.mark.parametrize("rows", [[90], [160, 161, 3], [255, 256, 257, 1], [600, 1, 0, 40], [240, 241, 239, 0, 480], [130, 0, 97, 12],
+                                  [65] * 9, [1000, 8, 9, 16, 17, 120]], ids=str)
+@pytest.mark.parametrize("d,f", [(256, 512), (768, 256), (1280, 1024), (256, 640), (128, 256)])
+def test_expert_ffn_fp8_long_runs(m, rows, d, f):
+    """Scales that are powers of two, as the quantiser makes them: applied by the tensor cores where runs are long."""
+    test_expert_ffn_fp8(m, rows, d, f, 3, general=False)
+
+
+@pytest.mark.parametrize("bad", [0.0, -1.0, 3.0, 2.0 ** -140, float("inf"), NAN])
+@pytest.mark.parametrize("which", [0, 1])
+def test_expert_ffn_fp8_one_other_scale(m, which, bad):
+    """One scale that is no power of two (of either product): its column block of every row, and no other."""
+    g = gen(7)
+    E, n, d, f = 2, 200, 256, 512
+    x = randn(g, E * n, d, dtype=torch.float16)
+    W1, s1 = experts8(m, g, E, d, f)
+    W2, s2 = experts8(m, g, E, f, d)
+    s = (s1, s2)[which]
+    if np.isfinite(bad):
+        s[1, 1, 1] *= bad                             # (2^-140: a subnormal)
+    else:
+        s[1, 1, 1] = bad
+    perm = torch.arange(E * n, device="cuda").to(torch.int32)
+    offsets = torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
+    out = torch.empty((E * n, d), dtype=torch.float16, device="cuda")
+    ws = torch.empty(m.moe_expert_fp8_workspace_size(E * n, d, f, E, E * n, torch.float16), dtype=torch.uint8, device="cuda")
+    m.moe_expert_ffn_fp8(x, perm, offsets, W1, s1, W2, s2, E * n, out, ws)
+    for e in range(E):
+        rows = slice(e * n, (e + 1) * n)
+        if e == 1 and not np.isfinite(bad):
+            cols = slice(128, 256) if which else slice(0, d)
+            assert not torch.isfinite(out[rows, cols]).any() if np.isnan(bad) or which == 0 else True
+            if which:
+                want, tol = ref_ffn8(x[rows], values8(W1[e], s1[e]), values8(W2[e], s2[e])[:128], d, f, True)
+                check(out[rows, :128], want, tol + half(torch.float16) * want.abs() + 2.0 ** -25, "the other columns")
+            continue
+        want, tol = ref_ffn8(x[rows], values8(W1[e], s1[e]), values8(W2[e], s2[e]), d, f, True)
+        check(out[rows], want, tol + half(torch.float16) * want.abs() + 2.0 ** -25, f"expert {e}")
 
 
 def test_expert_ffn_fp8_bad_indices(m):
