@@ -174,14 +174,16 @@ __device__ __forceinline__ size_t exponent_at(int b, int place, int Sp) { return
 int scale_row(int S_max, int E) { return (S_max + 3) / 4 * 4 + 4 * (E + 1); }
 
 // ---------------------------------------------------------------- rows
-// Slot s of an expert: its token's row in 8 bits.  A warp takes eight blocks of 128 columns of a row, 16 lanes each.
+// Slot s of an expert: its token's row in 8 bits.  A warp takes up to eight blocks of 128 columns (by blockIdx.y), 16 lanes
+// each, of neighbouring slots: their tokens come 32 at a time, and their expert is looked for once.  Bound by
+// instructions: 32768 slots x 2048: 42 us with a division, a search and a load of the token for each slot.
 // sx is [d / 128][Sp], a slot's place in it by scale_base.
 constexpr int kRowPart = 8;
-__global__ void __launch_bounds__(256) fp8_rows_kernel(const __half* __restrict__ tokens, const int32_t* __restrict__ perm,
+__global__ void __launch_bounds__(256, 6) fp8_rows_kernel(const __half* __restrict__ tokens, const int32_t* __restrict__ perm,
                                                        const int32_t* __restrict__ offsets, int E, int S_max, int T, int d,
                                                        int Sp, uint8_t* __restrict__ Xq, float* __restrict__ sx,
                                                        int* status, const float* __restrict__ s1,
-                                                       const float* __restrict__ s2, long long ns, uint8_t* __restrict__ xexp,
+                                                       const float* __restrict__ s2, long long ns, uint32_t* __restrict__ xexp,
                                                        int* general) {
   extern __shared__ int32_t offs[];
   pdl_wait();
@@ -189,12 +191,21 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const __half* __restrict_
   if (threadIdx.x < 32 && slot_table<8>(offsets, E, S_max, 1, offs, nullptr)) record_status(status, kErrBounds);
   __syncthreads();
   const int lane = threadIdx.x & 31, l = lane & 15, nb = d / 128, S = offs[E];
-  const int parts = (nb + kRowPart - 1) / kRowPart;
-  const long long units = (long long)S * parts;
+  const int h = lane >> 4, b0 = blockIdx.y * kRowPart + h;
+  const int warps = gridDim.x * 8, w = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int first = (int)((long long)S * w / warps), end = (int)((long long)S * (w + 1) / warps);
   bool bad = false;
-  for (long long u = blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += (long long)gridDim.x * 8) {
-    const int s = (int)(u / parts), b0 = (int)(u - (long long)s * parts) * kRowPart + (lane >> 4);
-    const int t = perm[s];
+  int lo = 0, hi = E;                            // the last e with offs[e] <= s
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (offs[mid] <= first) lo = mid; else hi = mid;
+  }
+  int next = offs[lo + 1], base = scale_base(offs[lo], lo) - offs[lo], tokens_of = 0;
+  uint32_t held[kRowPart / 2] = {};              // the scales of one of up to 16 slots, which leave side by side
+  int place = -1;
+  for (int s = first; s < end; ++s) {
+    if (((s - first) & 31) == 0) tokens_of = s + lane < end ? perm[s + lane] : 0;
+    const int t = __shfl_sync(0xffffffffu, tokens_of, (s - first) & 31);
     const bool in = (unsigned)t < (unsigned)T;
     bad |= !in;
     const __half* src = tokens + (long long)(in ? t : 0) * d + l * 8;
@@ -202,40 +213,52 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const __half* __restrict_
 #pragma unroll
     for (int i = 0; i < kRowPart / 2; ++i)
       r[i] = b0 + 2 * i < nb && in ? *reinterpret_cast<const uint4*>(src + (b0 + 2 * i) * 128) : make_uint4(0u, 0u, 0u, 0u);
-    int lo = 0, hi = E;                         // the last e with offs[e] <= s
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (offs[mid] <= s) lo = mid; else hi = mid;
+    while (s >= next) {                          // (s < offs[E])
+      ++lo;
+      next = offs[lo + 1];
+      base = scale_base(offs[lo], lo) - offs[lo];
     }
-    const int place = scale_base(offs[lo], lo) + (s - offs[lo]);
+    const int turn = (s - first) & 15;
+    if (l == turn) place = base + s;
     uint8_t* dst = Xq + (long long)s * d + l * 8;
 #pragma unroll
     for (int i = 0; i < kRowPart / 2; ++i) {
       const int b = b0 + 2 * i;
+      // the largest magnitude, two at a time as integers: infinity and NaN are above all others
+      uint32_t m = __vmaxu2(__vmaxu2(r[i].x & 0x7fff7fffu, r[i].y & 0x7fff7fffu), __vmaxu2(r[i].z & 0x7fff7fffu, r[i].w & 0x7fff7fffu));
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+      float scale, inv;
+      fp8_scale(__float_as_uint(__half2float(__ushort_as_half((unsigned short)max(m & 0xffffu, m >> 16)))), scale, inv);
       float f[8];
       unpack8(r[i], f);
-      uint32_t m = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, magnitude_bits(f[j]));
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      float scale, inv;
-      fp8_scale(m, scale, inv);
-      if (b < nb) {
+      if (l == turn) held[i] = __float_as_uint(scale);
+      if (b < nb)
         *reinterpret_cast<uint2*>(dst + b * 128) =
             make_uint2(fp8_four(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
                        fp8_four(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
-        if (l == 0) {
-          sx[(size_t)b * Sp + place] = scale;
-          if (xexp) xexp[exponent_at(b, place, Sp)] = (uint8_t)(__float_as_uint(scale) >> 23);
-        }
-      }
     }
+    if (turn < 15 && s + 1 < end) continue;
+#pragma unroll
+    for (int i = 0; i < kRowPart / 2; ++i)
+      if (place >= 0 && b0 + 2 * i < nb) sx[(size_t)(b0 + 2 * i) * Sp + place] = __uint_as_float(held[i]);
+    if (xexp) {                                  // a half has the odd or the even blocks' bytes of two words
+      uint32_t e[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        e[i] = (held[2 * i] >> 23 & 0xffu) << (8 * h) | (held[2 * i + 1] >> 23 & 0xffu) << (16 + 8 * h);
+        e[i] |= __shfl_xor_sync(0xffffffffu, e[i], 16);
+      }
+      const int word = blockIdx.y * (kRowPart / 4) + h;
+      if (place >= 0 && 4 * word < nb) xexp[(size_t)word * Sp + place] = h ? e[1] : e[0];
+    }
+    place = -1;
   }
   if (bad) record_status(status, kErrBounds);
   if (general) {                                 // (ns of each; NaN, as the quantiser writes it, has the exponent's form too)
     bool other = false;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < 2 * ns; i += gridDim.x * 256ll) {
+    const long long at = blockIdx.y * (long long)gridDim.x + blockIdx.x, step = (long long)gridDim.x * gridDim.y * 256;
+    for (long long i = at * 256 + threadIdx.x; i < 2 * ns; i += step) {
       const uint32_t v = __float_as_uint(i < ns ? s1[i] : s2[i - ns]);
       other |= (v & 0x807fffffu) != 0u && v != 0x7fc00000u;
       other |= v == 0u || v == 0x7f800000u;
@@ -1368,11 +1391,13 @@ cudaError_t launch_fp8_ffn(const void* tokens, const int32_t* perm, const int32_
   // the one for any.  64 experts of 512 rows on average, 2048 x 2048: 460 -> 276 us; 128 experts of 160 rows, 3584 x 14336:
   // 2390 -> 2182.
   const bool long_form = c8 >= 8 && d % 256 == 0 && f % 256 == 0;
-  MOE_LAUNCH(launch_k(fp8_rows_kernel, (unsigned)std::min<long long>(((long long)S_max * ((d / 128 + kRowPart - 1) / kRowPart) + 7) / 8, 8 * sms), 256,
+  const int parts = (d / 128 + kRowPart - 1) / kRowPart;
+  const dim3 rows_grid((unsigned)std::max(1, std::min((S_max + 7) / 8, 6 * sms / parts)), (unsigned)parts);
+  MOE_LAUNCH(launch_k(fp8_rows_kernel, rows_grid, 256,
                       (E + 1) * sizeof(int32_t), s,
                       false, static_cast<const __half*>(tokens), perm, offsets, E, S_max, T, d, w.Sp, x, sx, status,
-                      W1s, W2s, (long long)E * (d / 128) * (f / 128), long_form ? ws + w.ex : nullptr,
-                      long_form ? general : nullptr));
+                      W1s, W2s, (long long)E * (d / 128) * (f / 128),
+                      long_form ? reinterpret_cast<uint32_t*>(ws + w.ex) : nullptr, long_form ? general : nullptr));
   CUtensorMap A1, A2;
   RowMaps B1, B2;
   bool maps = encode_weight_map(&A1, W1q, d, (uint64_t)E * f) && encode_weight_map(&A2, W2q, f, (uint64_t)E * d);

@@ -199,35 +199,48 @@ def test_no_warp_leaves_a_loop_whose_barrier_others_wait_at():
     """A bounded wait may give up in one warp and not in the next.  Around each barrier of several warps, each warp goes
     round as often as the others, whatever its waits say."""
     text = source("fp8.cu")
-    kernel = block_behind(text, text.index("fp8_gemm_kernel("))
-    seen = 0
-    for mt in re.finditer(r"\bfor \(", kernel):
-        head = kernel[mt.start():kernel.index("{", mt.start())]
-        body = block_behind(kernel, mt.start())
-        if "bar.sync" not in body:
-            continue
-        seen += 1
-        before = body.split("bar.sync")[0]
-        # blocks that hand their sums to another one of the cluster: all warps of the block
-        before = before.replace(block_behind(body, body.index("if (part > 0)")), "")
-        # inner loops may end early: they are over before the barrier
-        for inner in ("for (int kb", "for (int c = 0; c < C8; ++c) {"):
+
+    def without(before, heads):                       # inner loops may end early: they are over before the barrier
+        for inner in heads:
             while inner in before:
                 at = before.index(inner)
                 end = before.index("{", at) + len(block_behind(before, at)) + 2
                 before = before[:at] + before[end:]
-        assert not re.search(r"\b(break|return|continue|goto)\b", before), head
-        assert not re.search(r"\bok\b", head), head
-    assert seen == 1
+        return before
+
+    results = block_behind(text, text.index("void finish("))
+    assert results.count("bar.sync") == 1
+    before = without(results.split("bar.sync")[0], ("for (int c = 0; c < C8; ++c) {",))
+    assert not re.search(r"\b(break|return|continue|goto)\b", before)
+    for name in ("fp8_gemm_kernel(", "fp8_long_kernel("):
+        kernel = block_behind(text, text.index(name))
+        assert "bar.sync" not in kernel
+        seen = 0
+        for mt in re.finditer(r"\bfor \(", kernel):
+            head = kernel[mt.start():kernel.index("{", mt.start())]
+            body = block_behind(kernel, mt.start())
+            if "finish<" not in body:
+                continue
+            seen += 1
+            before = body.split("finish<")[0]
+            # blocks that hand their sums to another one of the cluster: all warps of the block
+            if "if (part > 0)" in body:
+                before = before.replace(block_behind(body, body.index("if (part > 0)")), "")
+            before = without(before, ("for (int kb",))
+            assert not re.search(r"\b(break|return|continue|goto)\b", before), head
+            assert not re.search(r"\bok\b", head), head
+        assert seen == (1 if name == "fp8_gemm_kernel(" else 2)   # items, and their parts
 
 
 def test_blocks_that_give_up_wait_for_their_copies():
     """The block's shared memory may be another's a moment after its end."""
     text = source("fp8.cu")
-    end = block_behind(text, text.index("fp8_gemm_kernel("))
-    end = end[end.rindex("__syncthreads()"):]
-    # the two rings' loads by the warps that issued them, and the products
-    assert "a_full : b_full" in end and end.count("mbar_drain") == 2 and "tmem_dealloc" in end
+    for name, rings in (("fp8_gemm_kernel(", "a_full : b_full"), ("fp8_long_kernel(", "&full[st]")):
+        end = block_behind(text, text.index(name))
+        end = end[end.rindex("__syncthreads()"):]
+        # the rings' loads by the warps that issued them, and the products
+        assert rings in end and end.count("mbar_drain") == 2 and "tmem_dealloc" in end
+        assert end.rindex("mbar_drain") < end.index("tmem_dealloc")
 
 
 def test_no_block_of_a_cluster_writes_to_another_that_is_not_there():
@@ -237,3 +250,10 @@ def test_no_block_of_a_cluster_writes_to_another_that_is_not_there():
     assert kernel.count("cluster_meet()") == 2
     assert kernel.index("cluster_meet()") < kernel.index("store_remote")
     assert kernel.rindex("cluster_meet()") > kernel.rindex("tmem_dealloc")
+    kernel = block_behind(source("fp8.cu"), source("fp8.cu").index("fp8_long_kernel("))
+    first = kernel.index("cluster_meet()")
+    assert first < min(kernel.index(w) for w in ("load_rows_pair", "commit_pair", "arrive_remote_tmem"))
+    last = kernel.rindex("__syncthreads()")
+    assert kernel.index("cluster_meet()", last) < kernel.index("tmem_dealloc_pair") < kernel.rindex("cluster_meet()")
+    # the warps that wait for arrivals of the other block see the last of them before they end
+    assert "n < a.na && ok" in kernel and "n < 2 && ok" in kernel
