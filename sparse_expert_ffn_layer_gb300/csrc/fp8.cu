@@ -175,8 +175,9 @@ int scale_row(int S_max, int E) { return (S_max + 3) / 4 * 4 + 4 * (E + 1); }
 
 // ---------------------------------------------------------------- rows
 // Slot s of an expert: its token's row in 8 bits.  A warp takes up to eight blocks of 128 columns (by blockIdx.y), 16 lanes
-// each, of neighbouring slots: their tokens come 32 at a time, and their expert is looked for once.  Bound by
-// instructions: 32768 slots x 2048: 42 us with a division, a search and a load of the token for each slot.
+// each, of neighbouring slots: their tokens come 32 at a time, their expert is looked for once, and the scales of 16 slots
+// leave together: 32768 slots x 2048: 30 us cold (42 with a division, a search and a load of the token for each slot, and
+// its scales as words and bytes of their own).
 // sx is [d / 128][Sp], a slot's place in it by scale_base.
 constexpr int kRowPart = 8;
 __global__ void __launch_bounds__(256, 6) fp8_rows_kernel(const __half* __restrict__ tokens, const int32_t* __restrict__ perm,
@@ -1387,10 +1388,12 @@ cudaError_t launch_fp8_ffn(const void* tokens, const int32_t* perm, const int32_
   const double mean = (double)S_max / E;
   const int rows = (int)std::min<double>(S_max, S_max % T && S_max % E == 0 ? mean : mean + 2.0 * std::sqrt(mean) + 1.0);
   const int c8 = rows <= 32 ? 2 : rows <= 64 ? 4 : rows <= 128 ? 8 : rows <= 160 || rows > 192 ? 10 : 12;
-  // Long runs (from 65 slots on): the form for scales that are powers of two, where the rows' kernel finds no other scale, else
-  // the one for any.  64 experts of 512 rows on average, 2048 x 2048: 460 -> 276 us; 128 experts of 160 rows, 3584 x 14336:
-  // 2390 -> 2182.
-  const bool long_form = c8 >= 8 && d % 256 == 0 && f % 256 == 0;
+  // Long runs (from 65 slots on) with enough to do: the form for scales that are powers of two, where the rows' kernel finds no
+  // other scale, else the one for any; the one that does not run takes 3 us of each product.  us without and with it, S d f
+  // in 10^9: 64 experts of 512 rows, 2048 x 2048 (137): 460, 268; 128 of 160, 3584 x 14336 (1050): 2390, 2150; 64 of 70,
+  // 2048 x 2048 (19): 133, 126; 1 of 4096, 1024 x 4096 (17): 80, 59; 8 of 128, 4096 x 4096 (17): 81, 81; 4 of 128, 1024 x 1024
+  // (0.5): 28, 33; 4 of 256, 256 x 256 (0.07): 23, 30.
+  const bool long_form = c8 >= 8 && d % 256 == 0 && f % 256 == 0 && (double)S_max * d * f >= 8e9;
   const int parts = (d / 128 + kRowPart - 1) / kRowPart;
   const dim3 rows_grid((unsigned)std::max(1, std::min((S_max + 7) / 8, 6 * sms / parts)), (unsigned)parts);
   MOE_LAUNCH(launch_k(fp8_rows_kernel, rows_grid, 256,

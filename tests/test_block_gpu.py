@@ -471,9 +471,11 @@ def test_expert_ffn_fp8_short_batches(m, rows, d, f):
     test_expert_ffn_fp8(m, rows, d, f, 2)
 
 
-@pytest.mark.parametrize("rows", [[90], [160, 161, 3], [255, 256, 257, 1], [600, 1, 0, 40], [240, 241, 239, 0, 480], [130, 0, 97, 12],
-                                  [65] * 9, [1000, 8, 9, 16, 17, 120]], ids=str)
-@pytest.mark.parametrize("d,f", [(256, 512), (768, 256), (1280, 1024), (256, 640), (128, 256)])
+@pytest.mark.parametrize("rows,d,f", [([90], 256, 512), ([160, 161, 3], 768, 256), ([65] * 9, 1280, 1024),
+                                      ([160, 161, 3], 4352, 6400), ([255, 256, 257, 1], 2304, 5120), ([600, 1, 0, 40], 4352, 3328),
+                                      ([240, 241, 239, 0, 480], 1280, 6400), ([1000, 8, 9, 16, 17, 120], 2304, 3328),
+                                      ([500, 0, 0, 333], 3328, 3200), ([65] * 33, 2048, 2048), ([3000, 700], 256, 9216),
+                                      ([2999, 701, 0], 9216, 256)], ids=str)
 def test_expert_ffn_fp8_long_runs(m, rows, d, f):
     """Scales that are powers of two, as the quantiser makes them: applied by the tensor cores where runs are long."""
     test_expert_ffn_fp8(m, rows, d, f, 3, general=False)
@@ -484,7 +486,7 @@ def test_expert_ffn_fp8_long_runs(m, rows, d, f):
 def test_expert_ffn_fp8_one_other_scale(m, which, bad):
     """One scale that is no power of two (of either product): its column block of every row, and no other."""
     g = gen(7)
-    E, n, d, f = 2, 200, 256, 512
+    E, n, d, f = 2, 300, 3328, 4608
     x = randn(g, E * n, d, dtype=torch.float16)
     W1, s1 = experts8(m, g, E, d, f)
     W2, s2 = experts8(m, g, E, f, d)
