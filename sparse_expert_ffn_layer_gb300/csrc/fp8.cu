@@ -980,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // weight tile and half of the rows, and has the sums of its 128 outputs in its own TMEM, two items' by turns, which other
 // warps bring out while the next item's products run.
 // Scales lie in TMEM as words, four blocks' exponents each: word (lane l, column i) is row 32 i + l's, in each quarter.
-// Bound by the tensor cores with many inputs (490 cycles a block of 240 rows; their own rate needs 480), by GeLU and the
+// Bound by the tensor cores with many inputs (490 cycles a block of 240 rows; their nominal rate is 480), by GeLU and the
 // stores with few (2048: 25 % more), by DRAM where an expert has few rows.  What counts a block is what a warp issues:
 // rows in four copies, not one, took 560 cycles and bound the kernel (2340 -> 1610 -> 1400 us with one copy).
 constexpr int kLongRows = 240;

@@ -873,7 +873,7 @@ def test_block_of_experts(m, T, d, f, E, k):
     check(st["n"], n, 1e-5 * (n.abs() + 1) + 2.0 ** -11 * n.abs(), "n")
 
 
-@pytest.mark.parametrize("T,d,f", [(130, 256, 256), (2, 1024, 2048)])
+@pytest.mark.parametrize("T,d,f", [(130, 256, 256), (2, 1024, 2048), (1500, 1024, 4096)])
 def test_block_captured_and_eager(m, T, d, f):
     """A captured step with inputs that change between replays, eager calls of another state between them, and two
     states on two streams: the same bits as eager calls one after another."""
