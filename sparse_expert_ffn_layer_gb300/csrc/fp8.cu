@@ -579,79 +579,79 @@ __device__ __forceinline__ Tile8 tile_at(int i, const int32_t* prefix, const int
 // lc + 1 of eight.  kExp: h's scales as exponents.  cw: groups of eight columns of each warp; am: [column][quarter], invs: the warp's columns.
 template <int C8, bool kGelu, bool kExp>
 __device__ __forceinline__ void finish(float2 (&acc)[C8][4], const Tile8& t, const Fp8Args& a, int cw, int col0, int q, int g, int lane,
-                                       uint32_t* am, float* invs, bool ok) {
+                                 uint32_t* am, float* invs, bool ok) {
   const int lr = lane >> 2, lc = 2 * (lane & 3);
-        const size_t tile0 = (size_t)t.row0 * a.M + t.mt * 128 + 32 * q + 4 * lr;   // this lane's four outputs of a slot
-        if constexpr (kGelu) {
-          // GeLU, the largest magnitude of each slot's 128 columns (four warps), and 8 bits
-  #pragma unroll
-          for (int c = 0; c < C8; ++c) {
-            if (c >= cw) continue;
-            float m0 = 0.f, m1 = 0.f;
-  #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              acc[c][j] = gelu2(acc[c][j]);
-              m0 = max_nan(m0, acc[c][j].x);
-              m1 = max_nan(m1, acc[c][j].y);
-            }
-            uint32_t b0 = __float_as_uint(m0), b1 = __float_as_uint(m1);
-  #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-              b0 = max(b0, __shfl_xor_sync(0xffffffffu, b0, o));
-              b1 = max(b1, __shfl_xor_sync(0xffffffffu, b1, o));
-            }
-            if (lr == 0) {
-              am[(col0 + c * 8 + lc) * 4 + q] = b0;
-              am[(col0 + c * 8 + lc + 1) * 4 + q] = b1;
-            }
-          }
-          asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
-          if (!ok) return;
-          // a lane makes the scale of a column, for its whole warp
-          for (int c = lane; c < 8 * cw; c += 32) {
-            const int col = col0 + c;
-            const uint4 r = *reinterpret_cast<const uint4*>(am + col * 4);
-            float scale, inv;
-            fp8_scale(max(max(r.x, r.y), max(r.z, r.w)), scale, inv);
-            invs[c] = inv;
-            if (q == 0 && col < t.n) {
-              if (kExp) a.hexp[exponent_at(t.mt, t.sc0 + col, a.Sp)] = (uint8_t)(__float_as_uint(scale) >> 23);
-              else a.hscale[(size_t)t.mt * a.Sp + t.sc0 + col] = scale;
-            }
-          }
-          __syncwarp();
-          uint8_t* dst = a.h + tile0 + (size_t)(col0 + lc) * a.M;
-  #pragma unroll
-          for (int c = 0; c < C8; ++c) {
-            if (c >= cw) continue;
-            const float2 inv = *reinterpret_cast<const float2*>(invs + c * 8 + lc);
-            float2 v[4];
-  #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = mul2(acc[c][j], inv);
-            const int col = col0 + c * 8 + lc;
-            if (col < t.n) *reinterpret_cast<uint32_t*>(dst) = fp8_four(v[0].x, v[1].x, v[2].x, v[3].x);
-            if (col + 1 < t.n) *reinterpret_cast<uint32_t*>(dst + a.M) = fp8_four(v[0].y, v[1].y, v[2].y, v[3].y);
-            dst += 8 * (size_t)a.M;
-          }
-          __syncwarp();                            // (the warp's scales are written again with the next item)
-        } else {
-          if (!ok) return;
-  #pragma unroll
-          for (int c = 0; c < C8; ++c) {
-            if (c >= cw) continue;
-  #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              const int col = col0 + c * 8 + lc + p;
-              if (col < t.n) {
-                const float2 (&v)[4] = acc[c];
-                const __half2 lo = p ? __floats2half2_rn(v[0].y, v[1].y) : __floats2half2_rn(v[0].x, v[1].x);
-                const __half2 hi = p ? __floats2half2_rn(v[2].y, v[3].y) : __floats2half2_rn(v[2].x, v[3].x);
-                *reinterpret_cast<uint2*>(a.out + tile0 + (size_t)col * a.M) =
-                    make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-              }
-            }
-          }
+  const size_t tile0 = (size_t)t.row0 * a.M + t.mt * 128 + 32 * q + 4 * lr;   // this lane's four outputs of a slot
+  if constexpr (kGelu) {
+    // GeLU, the largest magnitude of each slot's 128 columns (four warps), and 8 bits
+#pragma unroll
+    for (int c = 0; c < C8; ++c) {
+      if (c >= cw) continue;
+      float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[c][j] = gelu2(acc[c][j]);
+        m0 = max_nan(m0, acc[c][j].x);
+        m1 = max_nan(m1, acc[c][j].y);
+      }
+      uint32_t b0 = __float_as_uint(m0), b1 = __float_as_uint(m1);
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        b0 = max(b0, __shfl_xor_sync(0xffffffffu, b0, o));
+        b1 = max(b1, __shfl_xor_sync(0xffffffffu, b1, o));
+      }
+      if (lr == 0) {
+        am[(col0 + c * 8 + lc) * 4 + q] = b0;
+        am[(col0 + c * 8 + lc + 1) * 4 + q] = b1;
+      }
+    }
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
+    if (!ok) return;
+    // a lane makes the scale of a column, for its whole warp
+    for (int c = lane; c < 8 * cw; c += 32) {
+      const int col = col0 + c;
+      const uint4 r = *reinterpret_cast<const uint4*>(am + col * 4);
+      float scale, inv;
+      fp8_scale(max(max(r.x, r.y), max(r.z, r.w)), scale, inv);
+      invs[c] = inv;
+      if (q == 0 && col < t.n) {
+        if (kExp) a.hexp[exponent_at(t.mt, t.sc0 + col, a.Sp)] = (uint8_t)(__float_as_uint(scale) >> 23);
+        else a.hscale[(size_t)t.mt * a.Sp + t.sc0 + col] = scale;
+      }
+    }
+    __syncwarp();
+    uint8_t* dst = a.h + tile0 + (size_t)(col0 + lc) * a.M;
+#pragma unroll
+    for (int c = 0; c < C8; ++c) {
+      if (c >= cw) continue;
+      const float2 inv = *reinterpret_cast<const float2*>(invs + c * 8 + lc);
+      float2 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = mul2(acc[c][j], inv);
+      const int col = col0 + c * 8 + lc;
+      if (col < t.n) *reinterpret_cast<uint32_t*>(dst) = fp8_four(v[0].x, v[1].x, v[2].x, v[3].x);
+      if (col + 1 < t.n) *reinterpret_cast<uint32_t*>(dst + a.M) = fp8_four(v[0].y, v[1].y, v[2].y, v[3].y);
+      dst += 8 * (size_t)a.M;
+    }
+    __syncwarp();                            // (the warp's scales are written again with the next item)
+  } else {
+    if (!ok) return;
+#pragma unroll
+    for (int c = 0; c < C8; ++c) {
+      if (c >= cw) continue;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int col = col0 + c * 8 + lc + p;
+        if (col < t.n) {
+          const float2 (&v)[4] = acc[c];
+          const __half2 lo = p ? __floats2half2_rn(v[0].y, v[1].y) : __floats2half2_rn(v[0].x, v[1].x);
+          const __half2 hi = p ? __floats2half2_rn(v[2].y, v[3].y) : __floats2half2_rn(v[2].x, v[3].x);
+          *reinterpret_cast<uint2*>(a.out + tile0 + (size_t)col * a.M) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
         }
+      }
+    }
+  }
 }
 
 // C8: groups of eight columns per warp (a tile has up to 16 C8 rows).  kGelu: first product.  kSplit: a cluster of
