@@ -280,6 +280,27 @@ def test_route_gradient(m, T, E, k, sigmoid, renorm, parts):
     check(dl, want, 128 * U * mag + 2.0 ** -47 * mag.sum(1, keepdim=True) + 1e-37, "dlogits")
 
 
+@pytest.mark.parametrize("T,E,k", [(5, 1, 1), (40, 3, 3), (300, 128, 8), (21, 600, 16)])
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_gradient_of_an_expert_named_twice(m, T, E, k, sigmoid, renorm):
+    """Plans of the caller's own: each mention carries its gradient."""
+    g = gen(T * 3 + E)
+    d = 128
+    x, dw, ds = randn(g, T, E, sigma=2.0), randn(g, T, k), randn(g, T, E)
+    idx = torch.randint(0, min(E, 3), (T, k), generator=g, device="cuda").to(torch.int32)
+    want, mag = ref_route_grad(x, idx, None, dw, ds, sigmoid, renorm, 1.5)
+    tol = 128 * U * mag + 2.0 ** -47 * mag.sum(1, keepdim=True) + 1e-37
+    tokens, Wg = randn(g, T, d, dtype=torch.float16), randn(g, d, E, sigma=0.1)
+    ws = torch.zeros(m.moe_gate_backward_workspace_size(T, d, E, torch.float16), dtype=torch.uint8, device="cuda")
+    for deep in (False, True):
+        dl = torch.full((T, E), NAN, device="cuda")
+        more = dict(tokens=tokens, Wg=Wg, dWg=torch.empty((d, E), device="cuda"), dtokens=torch.empty_like(tokens),
+                    workspace=ws) if deep else {}
+        m.moe_route_backward(x, idx, dl, dtopk_w=dw, dscores=ds, score=int(sigmoid), renormalize=renorm, scale=1.5, **more)
+        check(dl, want, tol, f"dlogits, deep {deep}")
+
+
 @pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_route_gradient_against_differences(m, sigmoid, renorm):
