@@ -5,7 +5,7 @@
 // A team of WPR warps takes a token's row: thread i of the team has the 16-byte pieces i, i + 32 WPR, ..., NV
 // of them, in registers from the first load to the last store, so that every row crosses DRAM once.  Bound by
 // DRAM, (k + 3) rows a token forward and 2 k + 4 backward, and by how many rows an SM has in work: forward 16384 x 3584,
-// k = 2: 113 us, 5.0 TB/s; backward 230 us, 3.9 TB/s (the time of a row's loads, sums and stores one after another).
+// k = 2: 117 us, 4.8 TB/s; backward 230 us, 3.9 TB/s (the time of a row's loads, sums and stores one after another).
 #include "launch.h"
 
 namespace moe {
@@ -175,6 +175,11 @@ __device__ __forceinline__ void block_sum(const NormArgs& a, size_t t, int tl, f
   }
 }
 
+// A row asks for the one that is this far behind it, on its way to L2, while its own norm is worked on: four for each SM.
+// Rows of 3584, k = 2: 121 us without, 117.5 with (twice as far the same, three times 132); of 2048, k = 4, shared: 53.1, 50.3
+// (52.3, 55.2); of 1024, k = 8: 165, 159 (165, 164).  Before its own rows are summed: 116, 48.6, 167.
+constexpr int kRowsAhead = 4 * 152;
+
 template <typename T, int WPR, int NV>
 __global__ void __launch_bounds__(32 * kBlockWarps<WPR>, (NV * Piece<T>::N <= 16 ? 32 : 16) / kBlockWarps<WPR>)
     block_norm_kernel(const NormArgs a) {
@@ -188,6 +193,10 @@ __global__ void __launch_bounds__(32 * kBlockWarps<WPR>, (NV * Piece<T>::N <= 16
   Team<WPR> tm{red[team], team, tl, 0};
   const int pieces = a.d / N;
   const uint4* res = row_of<T>(a.residual, t, a.d);
+  const size_t u = t + kRowsAhead;
+  const bool more = u < (size_t)a.T;
+  int next_slot = -1;
+  if (more && (tl & 31) < a.k) next_slot = a.slot_of[u * a.k + (tl & 31)];
   uint4 r[NV];
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
@@ -229,6 +238,14 @@ __global__ void __launch_bounds__(32 * kBlockWarps<WPR>, (NV * Piece<T>::N <= 16
         s = fma2(y[n][i], y[n][i], s);
       }
       if (a.hidden_out) out_of<T>(a.hidden_out, t, a.d)[p] = Piece<T>::pack(y[n]);
+    }
+  }
+  if (more) {
+    fetch_row<WPR, NV>(row_of<T>(a.residual, u, a.d), pieces, tl);
+    if (a.shared) fetch_row<WPR, NV>(row_of<T>(a.shared, u, a.d), pieces, tl);
+    for (int j = 0; j < a.k; ++j) {
+      const int s = __shfl_sync(0xffffffffu, next_slot, j);
+      if ((unsigned)s < (unsigned)a.S_max) fetch_row<WPR, NV>(row_of<T>(a.expert_out, s, a.d), pieces, tl);
     }
   }
   if (!a.normed_out && !a.rstd_next) return;
