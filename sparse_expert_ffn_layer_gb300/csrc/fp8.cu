@@ -176,20 +176,24 @@ int scale_row(int S_max, int E) { return (S_max + 3) / 4 * 4 + 4 * (E + 1); }
 // ---------------------------------------------------------------- rows
 // Slot s of an expert: its token's row in 8 bits.  A warp takes up to eight blocks of 128 columns (by blockIdx.y), 16 lanes
 // each, of neighbouring slots: their tokens come 32 at a time, their expert is looked for once, and the scales of 16 slots
-// leave together: 32768 slots x 2048: 30 us cold (42 with a division, a search and a load of the token for each slot, and
+// leave together.  It clears the status word, so a block says in a word of its own whether a slot's token was out of range,
+// for the first product to report (a memset before this kernel took 2 us).  32768 slots x 2048: 30 us cold (42 with a division, a search and a load of the token for each slot, and
 // its scales as words and bytes of their own).
 // sx is [d / 128][Sp], a slot's place in it by scale_base.
 constexpr int kRowPart = 8;
+constexpr int kMaxRowBlocks = 1024;
 __global__ void __launch_bounds__(256, 6) fp8_rows_kernel(const __half* __restrict__ tokens, const int32_t* __restrict__ perm,
                                                        const int32_t* __restrict__ offsets, int E, int S_max, int T, int d,
                                                        int Sp, uint8_t* __restrict__ Xq, float* __restrict__ sx,
                                                        int* status, const float* __restrict__ s1,
-                                                       const float* __restrict__ s2, long long ns, uint32_t* __restrict__ xexp,
+                                                       const float* __restrict__ s2, long long ns, uint32_t* __restrict__ xexp, int* __restrict__ bad_rows,
                                                        int* general) {
   extern __shared__ int32_t offs[];
   pdl_wait();
   pdl_trigger();
-  if (threadIdx.x < 32 && slot_table<8>(offsets, E, S_max, 1, offs, nullptr)) record_status(status, kErrBounds);
+  const int block = blockIdx.y * gridDim.x + blockIdx.x;
+  if (block == 0 && threadIdx.x == 0) *status = 0;
+  if (threadIdx.x < 32) slot_table<8>(offsets, E, S_max, 1, offs, nullptr);   // (what is wrong there, the products report)
   __syncthreads();
   const int lane = threadIdx.x & 31, l = lane & 15, nb = d / 128, S = offs[E];
   const int h = lane >> 4, b0 = blockIdx.y * kRowPart + h;
@@ -255,10 +259,11 @@ __global__ void __launch_bounds__(256, 6) fp8_rows_kernel(const __half* __restri
     }
     place = -1;
   }
-  if (bad) record_status(status, kErrBounds);
+  const int any = __syncthreads_or(bad);
+  if (threadIdx.x == 0) bad_rows[block] = any;
   if (general) {                                 // (ns of each; NaN, as the quantiser writes it, has the exponent's form too)
     bool other = false;
-    const long long at = blockIdx.y * (long long)gridDim.x + blockIdx.x, step = (long long)gridDim.x * gridDim.y * 256;
+    const long long at = block, step = (long long)gridDim.x * gridDim.y * 256;
     for (long long i = at * 256 + threadIdx.x; i < 2 * ns; i += step) {
       const uint32_t v = __float_as_uint(i < ns ? s1[i] : s2[i - ns]);
       other |= (v & 0x807fffffu) != 0u && v != 0x7fc00000u;
@@ -322,6 +327,8 @@ struct Fp8Args {
   uint8_t* hexp;
   __half* out;                 // second: [S_max][M]
   int* status;
+  const int* bad_rows;         // of the rows' blocks; first product
+  int row_blocks;
   const int* general;          // not null: which of two forms runs (not 0: the one for any scales)
 };
 
@@ -702,6 +709,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc(*holder, 512);
     return;
   }
+  if (kGelu && blockIdx.x == 0 && warp == 3) {
+    int bad = 0;
+    for (int i = lane; i < a.row_blocks; i += 32) bad |= a.bad_rows[i];
+    if (bad) record_status(a.status, kErrBounds);
+  }
   if (warp == 2 && slot_table<(C8 <= 4 ? 8 : 1)>(a.offsets, a.E, a.S_max, NMAX, offs, prefix)) record_status(a.status, kErrBounds);
   tc_fence_before();
   __syncthreads();
@@ -1044,6 +1056,11 @@ __global__ void __launch_bounds__(kLongThreads, 1)
   pdl_trigger();
   if (*a.general) return;                        // (all blocks: the other form runs)
   if (warp == 1) tmem_alloc_pair(holder);
+  if (kGelu && blockIdx.x == 0 && warp == 3) {
+    int bad = 0;
+    for (int i = lane; i < a.row_blocks; i += 32) bad |= a.bad_rows[i];
+    if (bad) record_status(a.status, kErrBounds);
+  }
   if (warp == 2 && slot_table<1>(a.offsets, a.E, a.S_max, kLongRows, offs, prefix)) record_status(a.status, kErrBounds);
   tc_fence_before();
   __syncthreads();
@@ -1337,14 +1354,15 @@ cudaError_t launch_long(const CUtensorMap& A, const RowMaps& B, Fp8Args a, int s
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct Fp8Ws {
-  size_t x, sx, h, sh, ex, eh, total;          // ex, eh: exponents of the scales
+  size_t bad, x, sx, h, sh, ex, eh, total;     // ex, eh: exponents of the scales
   int Sp;
 };
 Fp8Ws fp8_ws(int d, int f, int E, int S_max) {
   Fp8Ws w;
   const size_t S = std::max(S_max, 1);
   w.Sp = scale_row((int)S, E);
-  w.x = 256;                                    // the status word
+  w.bad = 256;                                  // behind the status word
+  w.x = w.bad + kMaxRowBlocks * 4;
   w.sx = w.x + up256(S * d);
   w.h = w.sx + up256((size_t)w.Sp * (d / 128) * 4);
   w.sh = w.h + up256(S * f);
@@ -1376,7 +1394,6 @@ cudaError_t launch_fp8_ffn(const void* tokens, const int32_t* perm, const int32_
   const Fp8Ws w = fp8_ws(d, f, E, S_max);
   int* status = reinterpret_cast<int*>(ws);
   int* general = status + 1;
-  MOE_LAUNCH(cudaMemsetAsync(status, 0, 2 * sizeof(int), s));
   uint8_t *x = ws + w.x, *h = ws + w.h;
   float *sx = reinterpret_cast<float*>(ws + w.sx), *sh = reinterpret_cast<float*>(ws + w.sh);
   // Rows per tile.  Slots that are no multiple of the tokens come from a capacity, S_max / E for each expert; otherwise
@@ -1395,12 +1412,14 @@ cudaError_t launch_fp8_ffn(const void* tokens, const int32_t* perm, const int32_
   // (0.5): 28, 33; 4 of 256, 256 x 256 (0.07): 23, 30.
   const bool long_form = c8 >= 8 && d % 256 == 0 && f % 256 == 0 && (double)S_max * d * f >= 8e9;
   const int parts = (d / 128 + kRowPart - 1) / kRowPart;
-  const dim3 rows_grid((unsigned)std::max(1, std::min((S_max + 7) / 8, 6 * sms / parts)), (unsigned)parts);
+  const dim3 rows_grid((unsigned)std::max(1, std::min((S_max + 7) / 8, std::min(6 * sms, kMaxRowBlocks) / parts)), (unsigned)parts);
+  int* bad_rows = reinterpret_cast<int*>(ws + w.bad);
+  if (long_form) MOE_LAUNCH(cudaMemsetAsync(general, 0, sizeof(int), s));
   MOE_LAUNCH(launch_k(fp8_rows_kernel, rows_grid, 256,
                       (E + 1) * sizeof(int32_t), s,
                       false, static_cast<const __half*>(tokens), perm, offsets, E, S_max, T, d, w.Sp, x, sx, status,
                       W1s, W2s, (long long)E * (d / 128) * (f / 128),
-                      long_form ? reinterpret_cast<uint32_t*>(ws + w.ex) : nullptr, long_form ? general : nullptr));
+                      long_form ? reinterpret_cast<uint32_t*>(ws + w.ex) : nullptr, bad_rows, long_form ? general : nullptr));
   CUtensorMap A1, A2;
   RowMaps B1, B2;
   bool maps = encode_weight_map(&A1, W1q, d, (uint64_t)E * f) && encode_weight_map(&A2, W2q, f, (uint64_t)E * d);
@@ -1420,6 +1439,8 @@ cudaError_t launch_fp8_ffn(const void* tokens, const int32_t* perm, const int32_
   g.Sp = w.Sp;
   g.status = status;
   g.split = 1;
+  g.bad_rows = bad_rows;
+  g.row_blocks = (int)(rows_grid.x * rows_grid.y);
   g.wscale = W1s;
   g.xscale = sx;
   g.K = d;
