@@ -177,8 +177,8 @@ int scale_row(int S_max, int E) { return (S_max + 3) / 4 * 4 + 4 * (E + 1); }
 // Slot s of an expert: its token's row in 8 bits.  A warp takes up to eight blocks of 128 columns (by blockIdx.y), 16 lanes
 // each, of neighbouring slots: their tokens come 32 at a time, their expert is looked for once, and the scales of 16 slots
 // leave together.  It clears the status word, so a block says in a word of its own whether a slot's token was out of range,
-// for the first product to report (a memset before this kernel took 2 us).  32768 slots x 2048: 30 us cold (42 with a division, a search and a load of the token for each slot, and
-// its scales as words and bytes of their own).
+// for the first product to report (a memset before this kernel took 3 us).  32768 slots x 2048: 30 us cold (42 with a
+// division, a search and a load of the token for each slot, and its scales as words and bytes of their own).
 // sx is [d / 128][Sp], a slot's place in it by scale_base.
 constexpr int kRowPart = 8;
 constexpr int kMaxRowBlocks = 1024;
@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(256, 6) fp8_rows_kernel(const __half* __restri
                                                        const int32_t* __restrict__ offsets, int E, int S_max, int T, int d,
                                                        int Sp, uint8_t* __restrict__ Xq, float* __restrict__ sx,
                                                        int* status, const float* __restrict__ s1,
-                                                       const float* __restrict__ s2, long long ns, uint32_t* __restrict__ xexp, int* __restrict__ bad_rows,
+                                                       const float* __restrict__ s2, long long ns, uint32_t* __restrict__ xexp,
+                                                       int* __restrict__ bad_rows,
                                                        int* general) {
   extern __shared__ int32_t offs[];
   pdl_wait();
@@ -230,7 +231,8 @@ __global__ void __launch_bounds__(256, 6) fp8_rows_kernel(const __half* __restri
     for (int i = 0; i < kRowPart / 2; ++i) {
       const int b = b0 + 2 * i;
       // the largest magnitude, two at a time as integers: infinity and NaN are above all others
-      uint32_t m = __vmaxu2(__vmaxu2(r[i].x & 0x7fff7fffu, r[i].y & 0x7fff7fffu), __vmaxu2(r[i].z & 0x7fff7fffu, r[i].w & 0x7fff7fffu));
+      uint32_t m = __vmaxu2(__vmaxu2(r[i].x & 0x7fff7fffu, r[i].y & 0x7fff7fffu),
+                            __vmaxu2(r[i].z & 0x7fff7fffu, r[i].w & 0x7fff7fffu));
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
       float scale, inv;
@@ -583,10 +585,11 @@ __device__ __forceinline__ Tile8 tile_at(int i, const int32_t* prefix, const int
 }
 
 // What becomes of a warp's sums: acc[c][j] has rows lr + 8 j of the quarter's 32 (four neighbouring outputs) and columns lc and
-// lc + 1 of eight.  kExp: h's scales as exponents.  cw: groups of eight columns of each warp; am: [column][quarter], invs: the warp's columns.
+// lc + 1 of eight.  kExp: h's scales as exponents.  cw: groups of eight columns of each warp; am: [column][quarter], invs: the
+// warp's columns.
 template <int C8, bool kGelu, bool kExp>
-__device__ __forceinline__ void finish(float2 (&acc)[C8][4], const Tile8& t, const Fp8Args& a, int cw, int col0, int q, int g, int lane,
-                                 uint32_t* am, float* invs, bool ok) {
+__device__ __forceinline__ void finish(float2 (&acc)[C8][4], const Tile8& t, const Fp8Args& a, int cw, int col0, int q,
+                                       int g, int lane, uint32_t* am, float* invs, bool ok) {
   const int lr = lane >> 2, lc = 2 * (lane & 3);
   const size_t tile0 = (size_t)t.row0 * a.M + t.mt * 128 + 32 * q + 4 * lr;   // this lane's four outputs of a slot
   if constexpr (kGelu) {

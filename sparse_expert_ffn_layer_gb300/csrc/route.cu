@@ -362,7 +362,8 @@ __device__ __noinline__ int route_wide(const float* row, const ScoreArgs& a, dou
 
 // The same for sigmoid scores where only the order of the experts near the last one taken is not certain: a lane decides
 // for each expert that was taken, or is within `margin` of the least of these (so that no other can be among the k).
-// False if these are fewer than k (NaN) or more than 32.  (All columns in 64 bits take a row 3 us, of which a batch waits for the last.)
+// False if these are fewer than k (NaN) or more than 32.  (All columns in 64 bits take a row 3 us, of which a batch waits
+// for the last.)
 template <int V, bool kWide>
 __device__ __forceinline__ bool route_near(const float* row, const ScoreArgs& a, const uint32_t (&key)[V], float floor,
                                            float margin, int* sh, int lane, int& mine) {
