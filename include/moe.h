@@ -490,7 +490,8 @@ MOE_API moe_status moe_expert_fp8_workspace_size(int T, int d, int f, int E, int
                                                  size_t* bytes);
 
 /*
- * moe_expert_ffn with weights and products in 8 bits, sums in float32:
+ * moe_expert_ffn with weights and products in 8 bits, sums in float32 (the tensor cores', whose additions cut off,
+ * over at most 1024 inputs, and those added with rounding):
  *   x8, sx = q(tokens[perm[s], :]),   u[s, j] = sum_b sx[s, b] W1s[e, j / 128, b] sum_{i in b} x8[s, i] W1q[e, j, i],
  *   h8, sh = q(GeLU_tanh(u[s, :])),   expert_out[s, j] = the same sum over h8, sh, W2q [E, d, f], W2s,
  * where b runs over blocks of 128 inputs and q brings each block of 128 of a row to e4m3 as moe_fp8_quantize

@@ -18,8 +18,8 @@
 // (N = 160: 1120 cycles a block, now 730).  Bound by these reads and additions: 8 experts of 2048 rows, 8192 x 8192:
 // 2340 us, 1.9 PFLOP/s.
 //
-// Scales that are powers of two, long runs: the tensor cores apply them, and nothing is added outside them (further below;
-// 1330 us for the same, 3.3 PFLOP/s).
+// Scales that are powers of two, long runs: the tensor cores apply them, and a sum leaves them every eight blocks at the
+// latest (further below; 1340 us for the same, 3.3 PFLOP/s).
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -531,6 +531,11 @@ __device__ __forceinline__ float max_nan(float m, float v) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
   return r;
 }
+__device__ __forceinline__ void add2(float2& d, float2 a) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(d)), "l"(bits2(a)));
+  d = float2_of(r);
+}
 __device__ __forceinline__ void fma2(float2& d, float2 a, float2 b) {
   unsigned long long r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(d)));
@@ -991,9 +996,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- products of long runs, scales that are powers of two
 // The tensor cores apply such scales themselves (kind::mxf8f6f4: a scale for each 32 inputs of a row, as an exponent), so a
-// tile's sum stays in TMEM over all its inputs.  A pair of blocks takes 256 outputs and up to 240 rows: each loads its own
-// weight tile and half of the rows, and has the sums of its 128 outputs in its own TMEM, two items' by turns, which other
-// warps bring out while the next item's products run.
+// tile's sum stays in TMEM over many blocks.  But their additions cut off what does not fit 24 bits, always towards zero:
+// over all of 16384 inputs a sum of one sign lost 395 u (u = 2^-24; now 33), and hidden values next to the border of two 8-bit ones
+// took the other more often than with sums that are rounded.  So a sum leaves TMEM after kLongSum blocks, for registers
+// where it is added with rounding.  Outputs' distance from those of exact sums (rounded to f16 too), 2.4B top-2 layer
+// at T = 16384: 1.4e-4 with all blocks in TMEM, 0.85e-4 with eight at a time (the register form 0.8e-4, sums by 32-bit matrix
+// products 0.9e-4), 0.82e-4 with four; us: 2240, 2270, 2360; 64 experts of 512 rows, 2048 x 2048: 287, 292, 319 (six: 308).
+// A pair of blocks takes 256 outputs and up to 240 rows: each loads its own weight tile and half of the rows, and has the
+// sums of its 128 outputs in its own TMEM, in two places by turns: eight blocks' products run while the sum before is read,
+// and 16 while the end of an item is worked on.
 // Scales lie in TMEM as words, four blocks' exponents each: word (lane l, column i) is row 32 i + l's, in each quarter.
 // Bound by the tensor cores with many inputs (490 cycles a block of 240 rows; their nominal rate is 480), by GeLU and the
 // stores with few (2048: 25 % more), by DRAM where an expert has few rows.  What counts a block is what a warp issues:
@@ -1003,6 +1014,7 @@ constexpr int kLongGroups = 3;                // of columns, each for the four w
 constexpr int kLongThreads = 256 + 128 * kLongGroups;   // weight tiles, products, -, rows; four warps for scales; results
 constexpr int kLongBox = 24;                  // rows are loaded by boxes of 24, 48 .. 120: each copy costs its warp 120 cycles
 constexpr uint32_t kLongStage = kABytes + kLongRows / 2 * 128;
+constexpr int kLongSum = 8;                   // blocks of 128 inputs, at most, whose sum stays in the tensor cores
 constexpr uint32_t kScaleCols = 2 * kLongRows;   // two sets of 16 columns: four for the weight tile, eight for the rows
 struct LongSmem {
   uint32_t amax_off, inv_off, bars_off, misc_off, total;
@@ -1024,7 +1036,7 @@ __host__ __device__ inline LongSmem long_smem(int stages, int E) {
 template <bool kGelu>
 __global__ void __launch_bounds__(kLongThreads, 1)
     fp8_long_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ RowMaps tmB, const Fp8Args a) {
-  constexpr int C8 = kLongRows / 8 / kLongGroups, CH = 5;   // groups of eight columns per warp
+  constexpr int C8 = kLongRows / 8 / kLongGroups, CH = 2;   // groups of eight columns per warp, and of one load
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const LongSmem L = long_smem(a.na, a.E);
@@ -1071,6 +1083,7 @@ __global__ void __launch_bounds__(kLongThreads, 1)
   cluster_meet();                                // the other's barriers are set up, and it is there
   const uint32_t tmem = *holder;
   const int mt = a.M / 128, nkb = a.K / 128, pairs = gridDim.x / 2, total = prefix[a.E] * (mt / 2);
+  const int segs = (nkb + kLongSum - 1) / kLongSum;   // sums of an item, of about as many blocks each
   auto item = [&](int i) {
     Tile8 t = tile_at(i, prefix, offs, a.E, mt / 2, kLongRows);
     t.mt = 2 * t.mt + part;
@@ -1080,7 +1093,7 @@ __global__ void __launch_bounds__(kLongThreads, 1)
   uint32_t issued = 0, issued_par = 0;           // ring places with a load in flight, for the end
   bool ok = true;
   if (warp < 8) {
-    regs_down<64>();
+    regs_down<56>();
     if (warp == 0 || warp == 3) {
       // ---------------------------------------------------------- weight tiles, rows
       // (run by whole warps, and one lane issues: the values stay uniform)
@@ -1127,40 +1140,43 @@ __global__ void __launch_bounds__(kLongThreads, 1)
       for (int i = blockIdx.x / 2; i < total && ok && part == 0; i += pairs) {
         // e4m3 both, exponents as scales, 256 outputs; which of a word's four is in bits 4 and 29
         const uint32_t idesc = 1u << 23 | (uint32_t)((item(i).n + 15) >> 4) << 18 | 16u << 24;
-        for (int kb = 0; kb < nkb; ++kb) {
-          const int j = kb & 3;
-          // rows and weight tiles, scales, a free place for the sum: a lane waits for each
-          uint64_t* bar = lane == 1 && j == 0 ? &sc_full[set] : lane == 2 && kb == 0 ? &acc_empty[turn] : &full[st];
-          ok = wait(bar, lane == 1 && j == 0 ? scp : lane == 2 && kb == 0 ? ap : fp);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t ad = d0 + (uint64_t)(st * (kLongStage >> 4)), bd = ad + (kABytes >> 4);
-          const uint32_t id = idesc | (uint32_t)j << 4 | (uint32_t)j << 29, sc = tmem + kScaleCols + 16 * set;
-          const bool last = kb + 1 == nkb, group = j == 3 || last;
-          if (elect_one()) {
+        for (int sg = 0, first = 0, end; sg < segs && ok; ++sg, first = end) {
+          end = nkb * (sg + 1) / segs;
+          for (int kb = first; kb < end; ++kb) {
+            const int j = kb & 3;
+            // rows and weight tiles, scales, a free place for the sum: a lane waits for each
+            uint64_t* bar = lane == 1 && j == 0 ? &sc_full[set] : lane == 2 && kb == first ? &acc_empty[turn] : &full[st];
+            ok = wait(bar, lane == 1 && j == 0 ? scp : lane == 2 && kb == first ? ap : fp);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t ad = d0 + (uint64_t)(st * (kLongStage >> 4)), bd = ad + (kABytes >> 4);
+            const uint32_t id = idesc | (uint32_t)j << 4 | (uint32_t)j << 29, sc = tmem + kScaleCols + 16 * set;
+            const bool group = j == 3 || kb + 1 == nkb;
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_mx_pair(tmem + turn * kLongRows, ad + 2 * k, bd + 2 * k, id, sc, sc + 4, kb + k ? 1u : 0u);
-            commit_pair(&empty[st]);
-            if (group) commit_pair(&sc_empty[set]);
-            if (last) commit_pair(&acc_full[turn]);
+              for (int k = 0; k < 4; ++k)
+                mma_mx_pair(tmem + turn * kLongRows, ad + 2 * k, bd + 2 * k, id, sc, sc + 4, kb - first + k ? 1u : 0u);
+              commit_pair(&empty[st]);
+              if (group) commit_pair(&sc_empty[set]);
+              if (kb + 1 == end) commit_pair(&acc_full[turn]);
+            }
+            if (++st == a.na) {
+              st = 0;
+              fp ^= 1u;
+            }
+            if (group) {
+              set ^= 1;
+              if (set == 0) scp ^= 1u;
+            }
           }
-          if (++st == a.na) {
-            st = 0;
-            fp ^= 1u;
-          }
-          if (group) {
-            set ^= 1;
-            if (set == 0) scp ^= 1u;
-          }
+          turn ^= 1;
+          if (turn == 0) ap ^= 1u;
         }
-        turn ^= 1;
-        if (turn == 0) ap ^= 1u;
       }
     } else if (warp >= 4) {
       // ---------------------------------------------------------- scales
       // Loads run kAhead groups of four blocks ahead of their use, over the ends of items.
-      constexpr int kAhead = 3;
+      constexpr int kAhead = 2;
       const uint32_t at = tmem + kScaleCols + ((uint32_t)(32 * (warp - 4)) << 16);
       int li = blockIdx.x / 2, lkb = 0, left = 0, set = 0;
       uint32_t sp = 1, w[kAhead] = {}, x[kAhead][8] = {};
@@ -1220,39 +1236,47 @@ __global__ void __launch_bounds__(kLongThreads, 1)
     const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
     int turn = 0;
     uint32_t ap = 0;
+    bool odd = false;
     // a warp whose wait gives up still meets the others at every item's barrier
     for (int i = blockIdx.x / 2; i < total; i += pairs) {
       const Tile8 t = item(i);
       const int cw = (t.n + 8 * kLongGroups - 1) / (8 * kLongGroups);   // groups of eight columns of each warp of this tile
-      if (ok) ok = wait(&acc_full[turn], ap);
-      tc_fence_after();
-#pragma unroll 1
-      for (int c0 = 0; c0 < cw; c0 += CH) {      // (a few columns at a time, so that the registers hold them)
-        const int col0 = 8 * (g * cw + c0);
-        uint32_t v[2][4 * CH];
-        float2 acc[CH][4];
-        if (ok) {
-          tmem_ld32<CH>(tq + turn * kLongRows + col0, v);
+      const int col0 = 8 * g * cw;
+      float2 acc[C8][4];
+#pragma unroll
+      for (int c = 0; c < C8; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[c][j] = make_float2(0.f, 0.f);
+      for (int sg = 0; sg < segs && ok; ++sg) {
+        ok = wait(&acc_full[turn], ap);
+        if (!ok) break;
+        tc_fence_after();
+        // (what is loaded beyond the tile's columns stays within the place, and is not used)
+#pragma unroll
+        for (int c = 0; c < C8; c += CH) {
+          if (c >= cw) continue;
+          uint32_t v[2][4 * CH];
+          tmem_ld32<CH>(tq + turn * kLongRows + col0 + 8 * c, v);
           tmem_wait<CH>(v);
-          if (c0 + CH >= cw) {                   // read: the place may take the next sum
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if (part == 0) mbar_arrive(&acc_empty[turn]);
-              else arrive_remote_tmem(first_block(smem_u32(&acc_empty[turn])));
-            }
-          }
+#pragma unroll
+          for (int h = 0; h < CH; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              add2(acc[c + h][j], pair(v[j >> 1][4 * h + 2 * (j & 1)], v[j >> 1][4 * h + 2 * (j & 1) + 1]));
         }
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[c][j] = pair(v[j >> 1][4 * c + 2 * (j & 1)], v[j >> 1][4 * c + 2 * (j & 1) + 1]);
-        finish<CH, kGelu, true>(acc, t, a, min(cw - c0, CH), col0, q, g, lane,
-                                reinterpret_cast<uint32_t*>(sm + L.amax_off) + turn * (kLongRows * 4),
-                                reinterpret_cast<float*>(sm + L.inv_off) + (warp - 8) * (8 * C8), ok);
+        tc_fence_before();                       // read: the place may take the next sum
+        __syncwarp();
+        if (lane == 0) {
+          if (part == 0) mbar_arrive(&acc_empty[turn]);
+          else arrive_remote_tmem(first_block(smem_u32(&acc_empty[turn])));
+        }
+        turn ^= 1;
+        if (turn == 0) ap ^= 1u;
       }
-      turn ^= 1;
-      if (turn == 0) ap ^= 1u;
+      finish<C8, kGelu, true>(acc, t, a, cw, col0, q, g, lane,
+                              reinterpret_cast<uint32_t*>(sm + L.amax_off) + (odd ? kLongRows * 4 : 0),
+                              reinterpret_cast<float*>(sm + L.inv_off) + (warp - 8) * (8 * C8), ok);
+      odd = !odd;
     }
   }
   // ------------------------------------------------------------ end
