@@ -439,7 +439,8 @@ typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
  * rounded 32-bit values (without a bias they are ordered by their logits).
  *   tokens, Wg, logits_in, logits_out, dtype, d: as moe_gate_topk's.
  *   bias       nullable [E] float32, added for the choice only (raised for experts that get too few tokens; -infinity
- *              for one that is not to be taken while others are left).
+ *              for one that is not to be taken while others are left; +infinity for one that is to be taken before
+ *              others, whose group's value it makes infinite whatever the second largest c is).
  *   token_mask nullable [T] bytes: a token with 0 gets topk_idx = -1, which moe_dispatch drops, and zero
  *              weights; what its row holds has no effect.
  *   scores_out nullable [T, E] float32: s (rows of masked tokens: 0); not logits_in or logits_out themselves.

@@ -119,6 +119,10 @@ __device__ __forceinline__ void scores(F (&x)[V], int sigmoid, F& m, F& sum) {
   for (int v = 0; v < V; ++v) x[v] *= inv;
 }
 
+// A group's value from its two largest choices: an infinite one decides it alone (a second one of -infinity would make NaN).
+template <typename F>
+__device__ __forceinline__ F group_value(F b1, F b2, bool two) { return two && b1 < F(INFINITY) ? b1 + b2 : b1; }
+
 // The ranks of the groups in 64 bits for sigmoid scores, from the experts that may count: those not surely below their
 // group's group_top-th in 32 bits.  low: what that is for a lane's own group.  False if these are more than 32.
 template <int V, bool kWide>
@@ -148,7 +152,7 @@ __device__ __forceinline__ bool groups_near(const float* row, const ScoreArgs& a
     b1 = x > b1 ? x : b1;
     b2 = lo > b2 ? lo : b2;
   }
-  const uint64_t kv = key_of((a.group_top == 2 && M > 1) ? b1 + b2 : b1);
+  const uint64_t kv = key_of(group_value(b1, b2, a.group_top == 2 && M > 1));
   rank = 0;
   for (int q = 0; q < a.n_groups; ++q) {
     const uint64_t kw = __shfl_sync(0xffffffffu, (unsigned long long)kv, q * per);
@@ -201,7 +205,7 @@ __device__ __forceinline__ int select(const float* row, F (&c)[V], const ScoreAr
       take(q1);
       b2 = q2 > b2 ? q2 : b2;
     }
-    const F value = (a.group_top == 2 && M > 1) ? b1 + b2 : b1;
+    const F value = group_value(b1, b2, a.group_top == 2 && M > 1);
     const K kv = key_of(value);
     int rank = 0;
     for (int q = 0; q < a.n_groups; ++q) {
@@ -213,12 +217,13 @@ __device__ __forceinline__ int select(const float* row, F (&c)[V], const ScoreAr
       const unsigned last = __ballot_sync(0xffffffffu, g < a.n_groups && rank == a.top_groups - 1);
       const unsigned next = __ballot_sync(0xffffffffu, g < a.n_groups && rank == a.top_groups);
       const F in = __shfl_sync(0xffffffffu, value, __ffs(last) - 1), out = __shfl_sync(0xffffffffu, value, __ffs(next) - 1);
-      if (in - out <= F(2) * tol * (unit + (in < F(0) ? -in : in))) {
+      // (an infinite choice is before any other, however large the bound would be)
+      if (in < F(INFINITY) && in - out <= F(2) * tol * (unit + (in < F(0) ? -in : in))) {
         unsure |= 2;
         if constexpr (sizeof(F) == 4) {
           const float least = (a.group_top == 2 && M > 1) ? b2 : b1;
-          if (a.sigmoid && groups_near<V, kWide>(row, a, c, least - 2.f * tol * (unit + fabsf(least)), M, per,
-                                                 reinterpret_cast<int*>(sh), lane, rank))
+          const float low = isinf(least) ? least : least - 2.f * tol * (unit + fabsf(least));
+          if (a.sigmoid && groups_near<V, kWide>(row, a, c, low, M, per, reinterpret_cast<int*>(sh), lane, rank))
             unsure = 0;
         }
       }
