@@ -75,8 +75,8 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, i
 // pass over 262144 x 128 logits (31 us instead of 28).  A row of -inf only has p = 0 and lse = 0 (it
 // adds nothing to either loss); NaN and +inf give NaN as the formula does.
 template <int LANES, int N>
-__device__ __forceinline__ float exp_row(float (&x)[N], float& inv) {
-  float m = x[0];
+__device__ __forceinline__ float exp_row(float (&x)[N], float& inv, float& m) {
+  m = x[0];
 #pragma unroll
   for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
   m = group_max<LANES>(m);
@@ -91,6 +91,11 @@ __device__ __forceinline__ float exp_row(float (&x)[N], float& inv) {
   const bool empty = s == 0.f;
   inv = empty ? 0.f : 1.f / s;
   return empty ? 0.f : m + logf(s);
+}
+template <int LANES, int N>
+__device__ __forceinline__ float exp_row(float (&x)[N], float& inv) {
+  float m;
+  return exp_row<LANES>(x, inv, m);
 }
 template <int LANES, int N>
 __device__ __forceinline__ float softmax_row(float (&x)[N]) {
@@ -446,8 +451,12 @@ __device__ __forceinline__ void row_gradient(const RouteDlArgs& d, int64_t t, bo
   constexpr int V = VEC * J;
   constexpr int KL = LANES >= kRouteMaxK ? 1 : kRouteMaxK / LANES;   // chosen experts per lane of the row
   const bool whole = route_row_read(d);
-  float lse = 0.f;
-  if (whole && !d.how.sigmoid) lse = softmax_row<LANES>(x);           // x is s now
+  float m = 0.f, inv_sum = 0.f;
+  if (whole && !d.how.sigmoid) {
+    exp_row<LANES>(x, inv_sum, m);
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] *= inv_sum;                       // x is s now
+  }
   // this lane's share of the chosen experts
   int idx[KL];
   float xs[KL], g[KL], u[KL];
@@ -477,7 +486,8 @@ __device__ __forceinline__ void row_gradient(const RouteDlArgs& d, int64_t t, bo
       const float low = fminf(xs[q], 0.f) - (d.how.renorm ? top : 0.f);
       v = xs[q] == -INFINITY ? 0.f : expf(low) / (1.f + expf(-fabsf(xs[q])));
     } else {
-      v = xs[q] == -INFINITY ? 0.f : expf(xs[q] - (d.how.renorm ? top : lse));
+      // (by the row's maximum and sum, as moe_route has it: the logarithm of the sum next to a large maximum loses bits)
+      v = xs[q] == -INFINITY ? 0.f : expf(xs[q] - (d.how.renorm ? top : m)) * (d.how.renorm ? 1.f : inv_sum);
     }
     u[q] = v;
     su += v;

@@ -64,3 +64,20 @@ def test_an_expert_that_is_always_taken_in_a_group_of_none_other(m, sigmoid, E):
     off = torch.arange(E, device="cuda")[None, :] // M != best
     rest = other.masked_fill(off, -INF).sort(dim=1, descending=True, stable=True).indices[:, :k - 1]
     assert (idx[:, 0] == M + 5).all() and torch.equal(idx[:, 1:].long(), rest)
+
+
+@pytest.mark.parametrize("T,E,k", [(64, 16, 4), (200, 64, 6), (33, 250, 16), (40, 600, 8)])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("offset", [-1000.0, 200.0, 1000.0, 10000.0])
+def test_gradient_with_an_offset_of_all_logits(m, T, E, k, renorm, offset):
+    """The softmax does not know of it: nothing may be lost by it."""
+    g = gen(T + E)
+    x = randn(g, T, E, sigma=2.0) + offset
+    idx = torch.rand((T, E), generator=g, device="cuda").argsort(1)[:, :k].to(torch.int32).contiguous()
+    dw, ds = randn(g, T, k), randn(g, T, E)
+    for parts in (dict(dtopk_w=dw), dict(dtopk_w=dw, dscores=ds)):
+        dl = torch.full((T, E), float("nan"), device="cuda")
+        m.moe_route_backward(x, idx, dl, renormalize=renorm, scale=1.5, **parts)
+        want, mag = ref_route_grad(x, idx, None, dw, parts.get("dscores"), False, renorm, 1.5)
+        # as in test_route_gradient
+        check(dl, want, 128 * U * mag + 2.0 ** -47 * mag.sum(1, keepdim=True) + 1e-37, "dlogits")
