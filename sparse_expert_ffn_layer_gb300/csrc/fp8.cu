@@ -997,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------- products of long runs, scales that are powers of two
 // The tensor cores apply such scales themselves (kind::mxf8f6f4: a scale for each 32 inputs of a row, as an exponent), so a
 // tile's sum stays in TMEM over many blocks.  But their additions cut off what does not fit 24 bits, always towards zero:
-// over all of 16384 inputs a sum of one sign lost 395 u (u = 2^-24; now 33), and hidden values next to the border of two 8-bit ones
+// over all of 16384 inputs a sum of one sign lost 395 u (u = 2^-24; now at most 37), and hidden values next to the border of two 8-bit ones
 // took the other more often than with sums that are rounded.  So a sum leaves TMEM after kLongSum blocks, for registers
 // where it is added with rounding.  Outputs' distance from those of exact sums (rounded to f16 too), 2.4B top-2 layer
 // at T = 16384: 1.4e-4 with all blocks in TMEM, 0.85e-4 with eight at a time (the register form 0.8e-4, sums by 32-bit matrix
@@ -1036,7 +1036,7 @@ __host__ __device__ inline LongSmem long_smem(int stages, int E) {
 template <bool kGelu>
 __global__ void __launch_bounds__(kLongThreads, 1)
     fp8_long_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ RowMaps tmB, const Fp8Args a) {
-  constexpr int C8 = kLongRows / 8 / kLongGroups, CH = 2;   // groups of eight columns per warp, and of one load
+  constexpr int C8 = kLongRows / 8 / kLongGroups, CH = 2, CF = 5;   // groups of eight columns: per warp, of a load, finished at once
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const LongSmem L = long_smem(a.na, a.E);
@@ -1247,7 +1247,7 @@ __global__ void __launch_bounds__(kLongThreads, 1)
       for (int c = 0; c < C8; ++c)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[c][j] = make_float2(0.f, 0.f);
-      for (int sg = 0; sg < segs && ok; ++sg) {
+      for (int kb = 0, sg = 0; kb < nkb && ok; kb = nkb * ++sg / segs) {   // (kb: a sum's first block)
         ok = wait(&acc_full[turn], ap);
         if (!ok) break;
         tc_fence_after();
@@ -1273,9 +1273,12 @@ __global__ void __launch_bounds__(kLongThreads, 1)
         turn ^= 1;
         if (turn == 0) ap ^= 1u;
       }
-      finish<C8, kGelu, true>(acc, t, a, cw, col0, q, g, lane,
-                              reinterpret_cast<uint32_t*>(sm + L.amax_off) + (odd ? kLongRows * 4 : 0),
-                              reinterpret_cast<float*>(sm + L.inv_off) + (warp - 8) * (8 * C8), ok);
+#pragma unroll
+      for (int c = 0; c < C8; c += CF) {
+        finish<CF, kGelu, true>(reinterpret_cast<float2 (&)[CF][4]>(acc[c]), t, a, min(max(cw - c, 0), CF), col0 + 8 * c, q, g,
+                                lane, reinterpret_cast<uint32_t*>(sm + L.amax_off) + (odd ? kLongRows * 4 : 0),
+                                reinterpret_cast<float*>(sm + L.inv_off) + (warp - 8) * (8 * C8), ok);
+      }
       odd = !odd;
     }
   }
