@@ -424,6 +424,8 @@ MOE_API moe_status moe_adapter_backward(const void* dout, const void* tokens, co
  *   moe_expert_ffn, moe_block_norm (the sum over a token's experts, the block's end and the next norm),
  * and moe_block_norm_backward and moe_route_backward for training the router, norms and gates.  An empty batch
  * (T = 0) is valid for each: outputs with a row per token have none, sums over the batch are written as zeros.
+ * An output that shares memory with an input of the call (one that is read), with another output or with the workspace:
+ * MOE_ERR_INVALID_ARG, but where it says that the two may be the same.
  * Deterministic: equal calls give equal bits.  All sums are in float32 or wider.
  */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
@@ -437,13 +439,13 @@ typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
  *   topk_w[t, j]   = scale s[e_j], divided by sum_j s[e_j] when renormalize is not 0.
  * Ties go to the lower index.  Order and ties are those of the scores as 64-bit numbers, not of their
  * rounded 32-bit values (without a bias they are ordered by their logits).
- *   tokens, Wg, logits_in, logits_out, dtype, d: as moe_gate_topk's.
+ *   tokens, Wg, logits_in, logits_out, dtype, d: as moe_gate_topk's; logits_out may be logits_in.
  *   bias       nullable [E] float32, added for the choice only (raised for experts that get too few tokens; -infinity
  *              for one that is not to be taken while others are left; +infinity for one that is to be taken before
  *              others, whose group's value it makes infinite whatever the second largest c is).
  *   token_mask nullable [T] bytes: a token with 0 gets topk_idx = -1, which moe_dispatch drops, and zero
  *              weights; what its row holds has no effect.
- *   scores_out nullable [T, E] float32: s (rows of masked tokens: 0); not logits_in or logits_out themselves.
+ *   scores_out nullable [T, E] float32: s (rows of masked tokens: 0).
  * Scores of logits of -infinity are zero; chosen experts whose scores sum to zero get zero weights.  Logits of
  * NaN or +infinity give unspecified experts (in [0, E)) and weights.
  * Shapes: k <= 16, k <= top_groups E / n_groups, n_groups <= 32 and a divisor of E; otherwise as moe_gate_topk.
@@ -501,7 +503,7 @@ MOE_API moe_status moe_expert_fp8_workspace_size(int T, int d, int f, int E, int
  *   writes them (powers of two, which the tensor cores apply themselves where an expert has many slots), or with any
  *   finite float32 scales.
  *   Everything else as moe_expert_ffn; workspace: moe_expert_fp8_workspace_size bytes, contents need no
- *   initialisation; the device-side status word is in it (moe_status_read).
+ *   initialisation; the device-side status word is in it (moe_status_read).  expert_out may be tokens.
  *   A token block that holds an infinity or a NaN makes its outputs NaN.
  * Shapes: MOE_F16 (tokens and expert_out), d and f multiples of 128.  MOE_F32: MOE_ERR_UNSUPPORTED.
  */
@@ -523,7 +525,6 @@ MOE_API moe_status moe_expert_ffn_fp8(const void* tokens, const int32_t* perm, c
  *   residual [T, d]; hidden_out may be residual itself.  post_w, gate, next_w nullable [d] float32; normed_out
  *   nullable (with next_w: a norm whose weights are NULL does not exist), not NULL together with hidden_out.
  *   rstd_post, rstd_next nullable [T] float32: 1 / sqrt(mean + eps) of the two norms, for the backward pass.
- *   No output overlaps an input otherwise.
  * Shapes: k <= 16, d a multiple of 8 (MOE_F16) or 4 (MOE_F32), at most 16384; T <= 2^30.
  */
 MOE_API moe_status moe_block_norm(const void* residual, const void* expert_out, const int32_t* slot_of,
@@ -547,7 +548,7 @@ MOE_API moe_status moe_block_norm_workspace_size(int T, int d, int k, moe_dtype 
  *   hidden, rstd_next and next_w are read with dnormed only; rstd_post with post_w only.
  *   dresidual, dexpert_out, dshared [like their values, `dtype`], dtopk_w [T, k], dpost_w, dgate, dnext_w [d]
  *   (float32): each nullable, not all.  dgate needs gate, dpost_w post_w, dnext_w dnormed, dtopk_w and dexpert_out
- *   expert_out.  dresidual may be dhidden itself; no output overlaps an input otherwise.
+ *   expert_out.  dresidual may be dhidden itself.
  *   workspace: moe_block_norm_workspace_size bytes (NULL without dpost_w, dgate and dnext_w).
  * With k = 1, post_w and no shared, dtopk_w is what rounding leaves of a sum that is zero but for eps: the norm
  * does not change with the weight.

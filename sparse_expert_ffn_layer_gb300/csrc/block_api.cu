@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 
 #include "../../include/moe.h"
 #include "launch.h"
@@ -39,6 +40,7 @@ moe_status guarded(F f) noexcept {
 }
 
 bool dtype_ok(moe_dtype t) { return t == MOE_F16 || t == MOE_F32; }
+size_t elem_bytes(moe_dtype t) { return t == MOE_F16 ? 2 : 4; }
 int lane_elems(moe_dtype t) { return t == MOE_F16 ? 8 : 4; }     // elements of 16 bytes
 
 moe_status check_route(int T, int E, int k, moe_score score) {
@@ -65,6 +67,26 @@ moe_status check_norm(int T, int d, int k, moe_dtype dtype) {
 bool experts_ok(const void* expert_out, const int32_t* slot_of, const float* topk_w, int k, int S_max) {
   if (k == 0) return !expert_out && !slot_of && !topk_w;
   return slot_of && topk_w && (expert_out || S_max == 0);
+}
+
+// Memory of an argument, and whether an output shares some with an input or with another output: blocks write while others
+// still read, and a sum may be written before its factor is read.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool shared_memory(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x && y && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+bool overlap(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+  for (auto o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Span& i : inputs)
+      if (shared_memory(*o, i)) return true;
+    for (auto q = o + 1; q != outputs.end(); ++q)
+      if (shared_memory(*o, *q)) return true;
+  }
+  return false;
 }
 
 // An empty call launches nothing that would write the status word: it is cleared here, in a workspace that is
@@ -107,8 +129,11 @@ moe_status moe_route(const void* tokens, moe_dtype dtype, const float* Wg, const
     if (!aligned16(tokens) || !aligned16(Wg) || !aligned16(logits_in) || !aligned16(logits_out) || !aligned16(bias) ||
         !aligned16(scores_out) || !aligned16(topk_idx) || !aligned16(topk_w))
       return MOE_ERR_UNSUPPORTED;
-    // the chosen logits are read again after a row's scores are written
-    if (scores_out && (scores_out == logits_in || scores_out == logits_out)) return MOE_ERR_INVALID_ARG;
+    const size_t te = (size_t)T * E * 4, tk = (size_t)T * k * 4;
+    if (overlap({{logits_out == logits_in ? nullptr : logits_out, te}, {scores_out, te}, {topk_idx, tk}, {topk_w, tk}},
+                {{logits_in ? nullptr : tokens, (size_t)T * d * elem_bytes(dtype)},
+                 {logits_in ? nullptr : Wg, (size_t)d * E * 4}, {logits_in, te}, {bias, (size_t)E * 4}, {token_mask, (size_t)T}}))
+      return MOE_ERR_INVALID_ARG;
     cudaStream_t s = as_stream(stream);
     if (!logits_in) MOE_TRY(launch_gate_logits(tokens, dtype == MOE_F16, Wg, T, d, E, logits_out, s));
     const ScoreArgs a{logits_in ? logits_in : logits_out, bias, token_mask, T, E, k, score == MOE_SCORE_SIGMOID,
@@ -142,14 +167,19 @@ moe_status moe_route_backward(const float* logits, const int32_t* topk_idx, cons
         !aligned16(tokens) || !aligned16(Wg) || !aligned16(dlogits) || !aligned16(dWg) || !aligned16(dtokens_in) ||
         !aligned16(dtokens) || !aligned16(workspace))
       return MOE_ERR_UNSUPPORTED;
+    size_t need = 0;
     if (deep) {
-      size_t need = 0;
       st = moe_gate_backward_workspace_size(T, d, E, dtype, &need);
       if (st != MOE_OK) return st;
       if (!workspace || ws_bytes < need) return MOE_ERR_WORKSPACE;
     }
-    if (dlogits == logits || dlogits == dscores) return MOE_ERR_INVALID_ARG;   // written while read
-    if (dtokens && dWg && dtokens == tokens) return MOE_ERR_INVALID_ARG;
+    const size_t te = (size_t)T * E * 4, tk = (size_t)T * k * 4, de = (size_t)d * E * 4;
+    const size_t td = deep ? (size_t)T * d * elem_bytes(dtype) : 0;
+    if (overlap({{dlogits, te}, {dWg, de}, {dtokens, td}, {deep ? workspace : nullptr, need}},
+                {{logits, te}, {topk_idx, tk}, {dtopk_w, tk}, {dscores, te}, {token_mask, (size_t)T},
+                 {dWg ? tokens : nullptr, td}, {dtokens ? Wg : nullptr, de},
+                 {dtokens_in == dtokens ? nullptr : dtokens_in, td}}))
+      return MOE_ERR_INVALID_ARG;
     const int f16 = dtype == MOE_F16;
     uint8_t* ws = static_cast<uint8_t*>(workspace) + kAlign;
     int* status = deep ? static_cast<int*>(workspace) : nullptr;
@@ -177,7 +207,8 @@ moe_status moe_fp8_quantize(const void* W, moe_dtype dtype, int E, int K, int N,
     if (K % 128 || N % 128 || K > kMaxCols || N > kMaxCols) return MOE_ERR_UNSUPPORTED;
     if ((long long)E * (K / 128) * (N / 128) > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
     if (!aligned16(W) || !aligned16(Wq) || !aligned4(scales)) return MOE_ERR_UNSUPPORTED;
-    if (static_cast<const void*>(Wq) == W) return MOE_ERR_INVALID_ARG;         // written while read
+    const size_t n = (size_t)E * K * N;
+    if (overlap({{Wq, n}, {scales, n / 16384 * 4}}, {{W, n * elem_bytes(dtype)}})) return MOE_ERR_INVALID_ARG;
     MOE_TRY(launch_fp8_weights(W, dtype == MOE_F16, E, K, N, Wq, scales, as_stream(stream)));
     return MOE_OK;
   });
@@ -203,7 +234,14 @@ moe_status moe_expert_ffn_fp8(const void* tokens, const int32_t* perm, const int
     if (!aligned16(tokens) || !aligned4(perm) || !aligned4(offsets) || !aligned16(W1q) || !aligned4(W1s) ||
         !aligned16(W2q) || !aligned4(W2s) || !aligned16(expert_out) || !aligned16(workspace))
       return MOE_ERR_UNSUPPORTED;
-    if (!workspace || ws_bytes < fp8_ffn_bytes(d, f, E, S_max)) return MOE_ERR_WORKSPACE;
+    const size_t need = fp8_ffn_bytes(d, f, E, S_max), w = (size_t)E * d * f;
+    if (!workspace || ws_bytes < need) return MOE_ERR_WORKSPACE;
+    // (expert_out may be tokens: these are in the workspace, in 8 bits, before the first row of it is written)
+    if (overlap({{workspace, need}, {expert_out, (size_t)S_max * d * 2}},
+                {{perm, (size_t)S_max * 4}, {offsets, (size_t)(E + 1) * 4}, {W1q, w}, {W1s, w / 16384 * 4}, {W2q, w},
+                 {W2s, w / 16384 * 4}}) ||
+        overlap({{workspace, need}}, {{tokens, (size_t)T * d * 2}}))
+      return MOE_ERR_INVALID_ARG;
     MOE_TRY(launch_fp8_ffn(tokens, perm, offsets, W1q, W1s, W2q, W2s, T, d, f, E, S_max, expert_out,
                            static_cast<uint8_t*>(workspace), as_stream(stream)));
     return MOE_OK;
@@ -230,9 +268,11 @@ moe_status moe_block_norm(const void* residual, const void* expert_out, const in
         !aligned16(shared) || !aligned16(post_w) || !aligned16(gate) || !aligned16(next_w) ||
         !aligned16(hidden_out) || !aligned16(normed_out) || !aligned4(rstd_post) || !aligned4(rstd_next))
       return MOE_ERR_UNSUPPORTED;
-    for (const void* o : {(const void*)hidden_out, (const void*)normed_out})
-      if (o && (o == expert_out || o == shared)) return MOE_ERR_INVALID_ARG;    // written while read
-    if (normed_out && (normed_out == residual || normed_out == hidden_out)) return MOE_ERR_INVALID_ARG;
+    const size_t el = elem_bytes(dtype), row = (size_t)d * 4, td = (size_t)T * d * el, t4 = (size_t)T * 4;
+    if (overlap({{hidden_out, td}, {normed_out, td}, {rstd_post, t4}, {rstd_next, t4}},
+                {{residual == hidden_out ? nullptr : residual, td}, {expert_out, (size_t)S_max * d * el},
+                 {slot_of, t4 * k}, {topk_w, t4 * k}, {shared, td}, {post_w, row}, {gate, row}, {next_w, row}}))
+      return MOE_ERR_INVALID_ARG;
     const NormArgs a{residual, expert_out, slot_of, topk_w, shared, post_w, gate, next_w, alpha, eps, T, d, k, S_max,
                      with_block, hidden_out, normed_out, rstd_post, rstd_next};
     MOE_TRY(launch_block_norm(a, dtype == MOE_F16, as_stream(stream)));
@@ -283,13 +323,16 @@ moe_status moe_block_norm_backward(const void* dhidden, const void* dnormed, con
       return MOE_ERR_UNSUPPORTED;
     const bool f16 = dtype == MOE_F16;
     if (sums && (!workspace || ws_bytes < norm_bytes(T, d, f16))) return MOE_ERR_WORKSPACE;
-    // Written while read: dresidual may take dhidden's place and nothing else; a slot's row is read by its own
-    // token before it is written, but a slot that is named twice would be read after.
-    for (const void* o : {(const void*)dresidual, (const void*)dexpert_out, (const void*)dshared})
-      if (o && (o == dnormed || o == hidden || o == expert_out || o == shared || (o == dhidden && o != dresidual)))
-        return MOE_ERR_INVALID_ARG;
-    if (dresidual && (dresidual == dshared || dresidual == dexpert_out)) return MOE_ERR_INVALID_ARG;
-    if (dshared && dshared == dexpert_out) return MOE_ERR_INVALID_ARG;
+    // (dresidual may be dhidden: a row is read before it is written, by the same threads)
+    const size_t el = elem_bytes(dtype), row = (size_t)d * 4, td = (size_t)T * d * el, t4 = (size_t)T * 4;
+    const size_t sd = (size_t)S_max * d * el;
+    if (overlap({{dresidual, td}, {dexpert_out, sd}, {dtopk_w, t4 * k}, {dshared, td}, {dpost_w, row}, {dgate, row},
+                 {dnext_w, row}, {sums ? workspace : nullptr, norm_bytes(T, d, f16)}},
+                {{dhidden == dresidual ? nullptr : dhidden, td}, {dnormed, td}, {dnormed ? hidden : nullptr, td},
+                 {dnormed ? rstd_next : nullptr, t4}, {dnormed ? next_w : nullptr, row}, {expert_out, sd},
+                 {slot_of, t4 * k}, {topk_w, t4 * k}, {shared, td}, {post_w, row}, {post_w ? rstd_post : nullptr, t4},
+                 {gate, row}}))
+      return MOE_ERR_INVALID_ARG;
     NormArgs a;
     memset(&a, 0, sizeof(a));
     a.expert_out = expert_out;
