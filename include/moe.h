@@ -504,6 +504,8 @@ MOE_API moe_status moe_expert_fp8_workspace_size(int T, int d, int f, int E, int
  *   finite float32 scales.
  *   Everything else as moe_expert_ffn; workspace: moe_expert_fp8_workspace_size bytes, contents need no
  *   initialisation; the device-side status word is in it (moe_status_read).  expert_out may be tokens.
+ *   Slots before offsets[0] belong to no expert (the plan may be a slice of a larger one): neither perm nor
+ *   expert_out is looked at there.
  *   A token block that holds an infinity or a NaN makes its outputs NaN.
  * Shapes: MOE_F16 (tokens and expert_out), d and f multiples of 128.  MOE_F32: MOE_ERR_UNSUPPORTED.
  */

@@ -196,10 +196,11 @@ __global__ void __launch_bounds__(256, 6) fp8_rows_kernel(const __half* __restri
   if (block == 0 && threadIdx.x == 0) *status = 0;
   if (threadIdx.x < 32) slot_table<8>(offsets, E, S_max, 1, offs, nullptr);   // (what is wrong there, the products report)
   __syncthreads();
-  const int lane = threadIdx.x & 31, l = lane & 15, nb = d / 128, S = offs[E];
+  // (slots before offsets[0] belong to no expert: a plan may be a slice of a larger one)
+  const int lane = threadIdx.x & 31, l = lane & 15, nb = d / 128, S0 = offs[0], S = offs[E] - S0;
   const int h = lane >> 4, b0 = blockIdx.y * kRowPart + h;
   const int warps = gridDim.x * 8, w = blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int first = (int)((long long)S * w / warps), end = (int)((long long)S * (w + 1) / warps);
+  const int first = S0 + (int)((long long)S * w / warps), end = S0 + (int)((long long)S * (w + 1) / warps);
   bool bad = false;
   int lo = 0, hi = E;                            // the last e with offs[e] <= s
   while (hi - lo > 1) {

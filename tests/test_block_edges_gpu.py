@@ -74,3 +74,83 @@ def test_gradients_over_their_weights_are_refused(m):
         m.moe_route_backward(li, idx, torch.empty_like(li), dtopk_w=randn(g, T, 1), tokens=y, Wg=Wg, dWg=Wg,
                              dtokens=torch.empty_like(y), workspace=ws)
     assert e.value.code == m.MOE_ERR_INVALID_ARG
+
+
+def layer8(m, g, T, d, f, E, S):
+    """An input, experts and a workspace; run(perm, offsets) gives the outputs (rows that nothing wrote: 7.5) and status."""
+    x = randn(g, T, d, dtype=F16)
+    (W1, s1), (W2, s2) = experts8(m, g, E, d, f), experts8(m, g, E, f, d)
+
+    def run(perm, offsets):
+        size = m.moe_expert_fp8_workspace_size(T, d, f, E, S, F16)
+        ws = torch.full((size + 256,), 0x5A, dtype=torch.uint8, device="cuda")
+        out = torch.full((S + 3, d), 7.5, dtype=F16, device="cuda")
+        n0 = m.get_lib().moe_kernel_launches()
+        m.moe_expert_ffn_fp8(x, perm, torch.tensor(offsets, dtype=torch.int32, device="cuda"), W1, s1, W2, s2, S, out, ws[:size])
+        launches = m.get_lib().moe_kernel_launches() - n0
+        status = m.moe_status_read(ws[:size])
+        assert (ws[size:] == 0x5A).all() and (out[S:] == 7.5).all()
+        return out[:S], status, launches
+    return run
+
+
+# short runs with clusters, tiles of 32 and of more rows; long runs: each product in two forms of which one returns at once
+SHAPES = [(60, 1024, 512, 3, 40, 3), (300, 256, 384, 3, 290, 3), (700, 2048, 2048, 3, 2100, 5)]
+
+
+@pytest.mark.parametrize("T,d,f,E,S,launches", SHAPES)
+@pytest.mark.parametrize("start", [1, 13, 38])
+def test_experts_in_8_bits_of_a_plan_that_starts_late(m, T, d, f, E, S, launches, start):
+    """A slice of a larger plan: what stands before its first slot is not looked at, and the rows are those of the plan
+    without the gap."""
+    g = gen(start)
+    run = layer8(m, g, T, d, f, E, S)
+    n = S - 38
+    cut = [0, n // 3, n // 3 + 1, n]
+    tokens = torch.randint(0, T, (n,), generator=g, device="cuda").to(torch.int32)
+    perm0 = torch.full((S,), -1, dtype=torch.int32, device="cuda")
+    perm0[:n] = tokens
+    want, status, took = run(perm0, cut)
+    assert status == m.MOE_OK and took == launches
+    perm = torch.full((S,), T + 9, dtype=torch.int32, device="cuda")
+    perm[start:start + n] = tokens
+    out, status, _ = run(perm, [start + c for c in cut])
+    assert status == m.MOE_OK
+    assert torch.equal(out[start:start + n], want[:n])
+    assert (out[:start] == 7.5).all() and (out[start + n:] == 7.5).all()
+    # as moe_expert_ffn has it
+    W1, W2 = randn(g, E, d, f, sigma=0.05, dtype=F16), randn(g, E, f, d, sigma=0.05, dtype=F16)
+    x = randn(g, T, d, dtype=F16)
+    ws = torch.empty(512 + S * f * 2, dtype=torch.uint8, device="cuda")
+    m.moe_expert_ffn(x, perm, torch.tensor([start + c for c in cut], dtype=torch.int32, device="cuda"), W1, W2, S,
+                     out.contiguous(), ws)
+    assert m.moe_status_read(ws) == m.MOE_OK
+
+
+@pytest.mark.parametrize("T,d,f,E,S,launches", SHAPES)
+def test_experts_in_8_bits_of_plans_that_leave_their_bounds(m, T, d, f, E, S, launches):
+    """Offsets that fall, exceed S_max or are negative are clamped, tokens out of range give rows of zeros, both are
+    reported; everything else is as in the plan that this amounts to."""
+    g = gen(S)
+    run = layer8(m, g, T, d, f, E, S)
+    perm = torch.randint(0, T, (S,), generator=g, device="cuda").to(torch.int32)
+    a, b = S // 3, S // 3 * 2
+    for given, clamped in (([0, a, b, S + 900], [0, a, b, S]), ([0, b, a, S], [0, b, b, S]), ([-7, a, b, S], [0, a, b, S]),
+                           ([0, a, 2 ** 31 - 1, S], [0, a, S, S]), ([S + 5, 0, a, b], [S, S, S, S]),
+                           ([0, a, -2 ** 31, b], [0, a, a, b])):
+        want, status, took = run(perm, clamped)
+        assert status == m.MOE_OK and took == launches
+        out, status, _ = run(perm, given)
+        assert status == m.MOE_ERR_DEVICE_BOUNDS, given
+        assert torch.equal(out, want), given
+    want, _, _ = run(perm, [0, a, b, S])
+    for at, token in ((0, T), (a, -1), (S - 1, 2 ** 31 - 1), (b + 3, -2 ** 31)):
+        bad = perm.clone()
+        bad[at] = token
+        out, status, _ = run(bad, [0, a, b, S])
+        assert status == m.MOE_ERR_DEVICE_BOUNDS
+        assert (out[at] == 0).all()
+        rest = torch.arange(S, device="cuda") != at
+        assert torch.equal(out[rest], want[rest])
+        # the next call sets the word anew
+        assert run(perm, [0, a, b, S])[1] == m.MOE_OK
