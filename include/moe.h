@@ -34,8 +34,8 @@
  *     recorded in the workspace's status word and read with moe_status_read.
  *   - No call throws across this boundary; all are safe to call from any host thread as
  *     long as concurrent calls use different workspaces and outputs.
- *   - T = 0 (an empty batch) is valid: the call enqueues nothing and returns MOE_OK (the
- *     training calls clear what is summed over the batch, and their status word).
+ *   - T = 0 (an empty batch) is valid: the call enqueues nothing and returns MOE_OK (the training calls
+ *     and those of a block clear what is summed over the batch, and their status word).
  *
  * Supported shapes: E <= 1024, k in {1, 2} (moe_dispatch, moe_dispatch_sharded, moe_route and
  * moe_block_norm: up to 16), k <= E.  MOE_F16 (tensor-core path): d, f and
@@ -221,7 +221,8 @@ MOE_API moe_status moe_layer_forward(const void* tokens, const float* Wg, const 
  * moe_expert_ffn / moe_expert_ffn_fp8 / moe_layer_forward / moe_adapter_forward / moe_adapter_backward call, or
  * moe_gate_topk_backward / moe_route_backward call with dWg or dtokens, on this workspace (MOE_OK, MOE_ERR_TIMEOUT
  * or MOE_ERR_DEVICE_BOUNDS), or MOE_ERR_CUDA if the synchronisation or the read failed.  Each of
- * those calls sets the word anew (of the empty ones the training calls; the others enqueue nothing).
+ * those calls sets the word anew (of the empty ones the training calls, moe_expert_ffn_fp8 and
+ * moe_route_backward; the others enqueue nothing).
  */
 MOE_API moe_status moe_status_read(const void* workspace, moe_stream_t stream);
 
@@ -345,7 +346,7 @@ MOE_API moe_status moe_gate_topk_backward(const float* logits, const int32_t* to
  *   names are left as they were.  dexpert_out nullable (then topk_w is not read), dtopk_w
  *   nullable (then expert_out is not read); not both.  residual_in's gradient is dout itself.
  *   dexpert_out does not overlap dout, nor expert_out.
- *   A slot that two assignments name (moe_dispatch names none twice) gets one of their rows.
+ *   Of a slot that two assignments name (moe_dispatch names none twice) each element is one of theirs.
  * Shapes: T <= 2^30, d <= 2^20.
  */
 MOE_API moe_status moe_combine_backward(const void* dout, const void* expert_out,
@@ -438,7 +439,8 @@ typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
  *   topk_idx[t, :] = the k experts of largest c among them, in descending order,
  *   topk_w[t, j]   = scale s[e_j], divided by sum_j s[e_j] when renormalize is not 0.
  * Ties go to the lower index.  Order and ties are those of the scores as 64-bit numbers, not of their
- * rounded 32-bit values (without a bias they are ordered by their logits).
+ * rounded 32-bit values; without a bias, and where no two c are added for a group, those of the logits
+ * (two sigmoid scores of 1 - 2^-60 are equal in 64 bits, their logits need not be).
  *   tokens, Wg, logits_in, logits_out, dtype, d: as moe_gate_topk's; logits_out may be logits_in.
  *   bias       nullable [E] float32, added for the choice only (raised for experts that get too few tokens; -infinity
  *              for one that is not to be taken while others are left; +infinity for one that is to be taken before
@@ -482,7 +484,7 @@ MOE_API moe_status moe_route_backward(const float* logits, const int32_t* topk_i
  *   W [E, K, N] in `dtype` (the layout of W1 and W2); Wq [E, N, K], one byte a value: each output's K weights
  *   side by side; scales [E, N / 128, K / 128] float32 (a block of zeros: 1).
  *   A block that holds an infinity or a NaN gets scale NaN and Wq NaN.
- * Shapes: K, N multiples of 128, E K N < 2^43.  T plays no part here; E = 0 is an error.
+ * Shapes: K, N multiples of 128, at most 2^20; at most 2^31 - 1 blocks.  T plays no part here; E = 0 is an error.
  */
 MOE_API moe_status moe_fp8_quantize(const void* W, moe_dtype dtype, int E, int K, int N, uint8_t* Wq,
                                     float* scales, moe_stream_t stream);
@@ -546,7 +548,7 @@ MOE_API moe_status moe_block_norm_workspace_size(int T, int d, int k, moe_dtype 
  *   dshared = dy,   dexpert_out[s, :] = topk_w[t,j] dy,   dtopk_w[t,j] = sum_i dy_i expert_out[s, i],
  *   dnext_w = sum_t rn dnormed . h,   dgate = sum_t alpha dh . z0 (z0: z before its gate),   dpost_w = sum_t rp dz . y,
  * for every assignment with s = slot_of[t, j] in [0, S_max) (dtopk_w of the others: 0; slots that no assignment
- * names are left as they were; a slot that two name gets one of their rows).
+ * names are left as they were; of a slot that two name each element is one of theirs, which one is not said).
  *   hidden, rstd_next and next_w are read with dnormed only; rstd_post with post_w only.
  *   dresidual, dexpert_out, dshared [like their values, `dtype`], dtopk_w [T, k], dpost_w, dgate, dnext_w [d]
  *   (float32): each nullable, not all.  dgate needs gate, dpost_w post_w, dnext_w dnormed, dtopk_w and dexpert_out

@@ -1298,7 +1298,9 @@ __global__ void __launch_bounds__(kLongThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_drain(spare, 0);
     }
-    if (threadIdx.x == 64) {                     // the other block's loads, which this one may not have expected
+    // The other block's loads, which this one may not have expected: microseconds each, the last of them asked for before
+    // the wait of kDefaultWaitNs that gave up; a pause all the same.
+    if (threadIdx.x == 64) {
       const uint64_t t0 = globaltimer_ns();
       while (globaltimer_ns() - t0 < 1000000ull) {}
     }

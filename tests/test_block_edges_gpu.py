@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from test_block_gpu import experts8, gen, norm_inputs, randn
+from test_block_gpu import check, experts8, gen, half, norm_inputs, randn, ref_ffn8, rows8, values8
 
 pytestmark = pytest.mark.gpu
 F16 = torch.float16
@@ -154,3 +154,65 @@ def test_experts_in_8_bits_of_plans_that_leave_their_bounds(m, T, d, f, E, S, la
         assert torch.equal(out[rest], want[rest])
         # the next call sets the word anew
         assert run(perm, [0, a, b, S])[1] == m.MOE_OK
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_a_slot_that_two_tokens_name(m, dtype):
+    """Each element of its gradient is one of theirs; the other slots and gradients do not notice."""
+    g = gen(6)
+    T, d, k = 64, 2048, 2
+    slot, rows, w = norm_inputs(g, T, d, k, dtype, drop=0.0)
+    dh = randn(g, T, d, dtype=dtype)
+    a, b = int(slot[10, 0]), int(slot[50, 1])
+    one, two = slot.clone(), slot.clone()
+    one[50, 1], two[50, 1] = -1, a
+    got = {}
+    for name, s in (("one", one), ("two", two)):
+        dy, dw = torch.full_like(rows, 7.5), torch.empty((T, k), device="cuda")
+        m.moe_block_norm_backward(dh, expert_out=rows, slot_of=s, topk_w=w, dexpert_out=dy, dtopk_w=dw)
+        got[name] = dy, dw
+    (y1, w1), (y2, w2) = got["one"], got["two"]
+    other = torch.arange(rows.shape[0], device="cuda") != a
+    assert torch.equal(y1[other], y2[other]) and (y2[b] == 7.5).all()
+    theirs = (w[50, 1].double() * dh[50].double()).to(dtype)
+    assert ((y2[a] == y1[a]) | (y2[a] == theirs)).all()
+    same = torch.ones_like(w, dtype=torch.bool)
+    same[50, 1] = False
+    assert torch.equal(w1[same], w2[same]) and float(w2[50, 1]) != 0.0
+
+
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("factor", [0.0, -1.0, 3.0, 2.0 ** -140, float("inf"), -float("inf")])
+def test_one_scale_that_is_no_power_of_two(m, which, factor):
+    """Long runs, in the form for any scales and to its tolerance; an infinite scale makes its columns infinite with the
+    sign of the block's sum."""
+    g = gen(17)
+    E, n, d, f = 2, 300, 3328, 4608
+    x = randn(g, E * n, d, dtype=F16)
+    (W1, s1), (W2, s2) = experts8(m, g, E, d, f), experts8(m, g, E, f, d)
+    s = (s1, s2)[which]
+    s[1, 1, 1] = s[1, 1, 1] * factor if abs(factor) < 1e30 else factor
+    perm, off = torch.arange(E * n, device="cuda").to(torch.int32), torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
+    out = torch.empty((E * n, d), dtype=F16, device="cuda")
+    ws = torch.empty(m.moe_expert_fp8_workspace_size(E * n, d, f, E, E * n, F16), dtype=torch.uint8, device="cuda")
+    m.moe_expert_ffn_fp8(x, perm, off, W1, s1, W2, s2, E * n, out, ws)
+    assert m.moe_status_read(ws) == m.MOE_OK
+    for e in range(E):
+        rows, cols = slice(e * n, (e + 1) * n), torch.ones(d, dtype=torch.bool, device="cuda")
+        w1, w2 = values8(W1[e], s1[e]), values8(W2[e], s2[e])
+        if e == 1 and abs(factor) > 1e30:
+            if which == 0:                            # GeLU(-infinity) is NaN in its formula: all of each row
+                assert not torch.isfinite(out[rows]).any()
+                continue
+            cols[128:256] = False
+            got = out[rows, 128:256].float()
+            h = rows8(torch.nn.functional.gelu(rows8(x[rows].double()) @ values8(W1[e], s1[e]).t(), approximate="tanh"))
+            sign = h[:, 128:256] @ W2[e, 128:256, 128:256].double().t()
+            # (a sum that is near zero may have either sign, or be zero: 0 times infinity is NaN)
+            clear = sign.abs() > 0.05 * (h[:, 128:256].abs() @ W2[e, 128:256, 128:256].double().abs().t())
+            assert clear.float().mean() > 0.5 and not torch.isfinite(got).any()
+            assert torch.equal(got[clear], (torch.sign(sign[clear]) * factor).float())
+            w2 = w2.clone()
+            w2[128:256] = 0.0
+        want, tol = ref_ffn8(x[rows], w1, w2, d, f)
+        check(out[rows][:, cols], want[:, cols], (tol + half(F16) * want.abs() + 2.0 ** -25)[:, cols], f"expert {e}")

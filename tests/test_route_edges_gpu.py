@@ -81,3 +81,13 @@ def test_gradient_with_an_offset_of_all_logits(m, T, E, k, renorm, offset):
         want, mag = ref_route_grad(x, idx, None, dw, parts.get("dscores"), False, renorm, 1.5)
         # as in test_route_gradient
         check(dl, want, 128 * U * mag + 2.0 ** -47 * mag.sum(1, keepdim=True) + 1e-37, "dlogits")
+
+
+def test_order_of_scores_that_are_one(m):
+    """Logits whose sigmoid is one in 64 bits: by the logits, or by the index where choices are added for groups."""
+    x = torch.full((3, 16), -1.0, device="cuda")
+    x[:, 2], x[:, 3], x[:, 9] = 40.0, 50.0, 45.0
+    assert (run_route(m, x, 3, True)[0].long() == torch.tensor([3, 9, 2], device="cuda")).all()
+    assert (run_route(m, x, 3, True, G=4, top=2, gt=1)[0].long() == torch.tensor([3, 9, 2], device="cuda")).all()
+    assert (run_route(m, x, 3, True, G=4, top=2, gt=2)[0].long() == torch.tensor([2, 3, 9], device="cuda")).all()
+    assert (run_route(m, x, 3, True, bias=torch.zeros(16, device="cuda"))[0].long() == torch.tensor([2, 3, 9], device="cuda")).all()
