@@ -1440,9 +1440,11 @@ cudaError_t launch_fp8_ffn(const void* tokens, const int32_t* perm, const int32_
   const int c8 = rows <= 32 ? 2 : rows <= 64 ? 4 : rows <= 128 ? 8 : rows <= 160 || rows > 192 ? 10 : 12;
   // Long runs (from 65 slots on) with enough to do: the form for scales that are powers of two, where the rows' kernel finds no
   // other scale, else the one for any; the one that does not run takes 3 us of each product.  us without and with it, S d f
-  // in 10^9: 64 experts of 512 rows, 2048 x 2048 (137): 460, 268; 128 of 160, 3584 x 14336 (1050): 2390, 2150; 64 of 70,
-  // 2048 x 2048 (19): 133, 126; 1 of 4096, 1024 x 4096 (17): 80, 59; 8 of 128, 4096 x 4096 (17): 81, 81; 4 of 128, 1024 x 1024
-  // (0.5): 28, 33; 4 of 256, 256 x 256 (0.07): 23, 30.
+  // in 10^9: 64 experts of 512 rows, 2048 x 2048 (137): 483, 295; 128 of 160, 3584 x 14336 (1050): 2840, 2270; 64 of 70,
+  // 2048 x 2048 (19): 130, 125 to 130; 1 of 4096, 1024 x 4096 (17): 78, 58; 8 of 128, 4096 x 4096 (17): 79, 81.  About the border
+  // (8.6): 1 of 2048, 2048 x 2048: 49, 41; 32 of 256, 1024 x 1024: 62, 62; 16 of 128, 2048 x 2048: 52, 56.  Below it: 16 of 256,
+  // 1024 x 1024 (4.3): 35, 41; 8 of 128 and 1 of 1024, 2048 x 2048 (4.3): 31, 37 both; 4 of 128, 2048 x 2048 (2.1): 29, 35;
+  // 8 of 128, 1024 x 1024 (1.1): 23, 32; 4 of 256, 256 x 256 (0.07): 17, 27.
   const bool long_form = c8 >= 8 && d % 256 == 0 && f % 256 == 0 && (double)S_max * d * f >= 8e9;
   const int parts = (d / 128 + kRowPart - 1) / kRowPart;
   const dim3 rows_grid((unsigned)std::max(1, std::min((S_max + 7) / 8, std::min(6 * sms, kMaxRowBlocks) / parts)), (unsigned)parts);
