@@ -5,7 +5,7 @@
 // A team of WPR warps takes a token's row: thread i of the team has the 16-byte pieces i, i + 32 WPR, ..., NV
 // of them, in registers from the first load to the last store, so that every row crosses DRAM once.  Bound by
 // DRAM, (k + 3) rows a token forward and 2 k + 4 backward, and by how many rows an SM has in work: forward 16384 x 3584,
-// k = 2: 117 us, 4.8 TB/s; backward 230 us, 3.9 TB/s (the time of a row's loads, sums and stores one after another).
+// k = 2: 116 us, 5.1 TB/s; backward 248 us, 3.8 TB/s (the time of a row's loads, sums and stores one after another).
 #include "launch.h"
 
 namespace moe {
@@ -76,8 +76,11 @@ struct Team {
   float* red;
   int id, tl, turn;
   __device__ __forceinline__ void meet() const {
-    if (WPR > 1) asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "n"(32 * WPR) : "memory");
-    else __syncwarp();
+    // (A block has one or two such teams.  With the barrier's number in a register a block takes all 16, and an SM held four
+    // blocks: 16384 x 1024, k = 2: 49 us instead of 35, the gradient 114 instead of 77.)
+    if (WPR == 1) __syncwarp();
+    else if (id == 0) asm volatile("bar.sync 1, %0;" ::"n"(32 * WPR) : "memory");
+    else asm volatile("bar.sync 2, %0;" ::"n"(32 * WPR) : "memory");
   }
   __device__ __forceinline__ float sum(float2 two) {
     float v = two.x + two.y;
@@ -176,8 +179,9 @@ __device__ __forceinline__ void block_sum(const NormArgs& a, size_t t, int tl, f
 }
 
 // A row asks for the one that is this far behind it, on its way to L2, while its own norm is worked on: four for each SM.
-// Rows of 3584, k = 2: 121 us without, 117.5 with (twice as far the same, three times 132); of 2048, k = 4, shared: 53.1, 50.3
-// (52.3, 55.2); of 1024, k = 8: 165, 159 (165, 164).  Before its own rows are summed: 116, 48.6, 167.
+// us without, with four and with eight for each: rows of 3584, k = 2: 124, 116, 118; of 2048, k = 4, shared: 52, 48.5, 50; of
+// 4096, k = 2, shared: 79, 72, 80; of 2048, k = 2: 62, 62, 57; of 1024, k = 8: 119, 120, 114; f32, of 4096, k = 2: 74, 67, 88;
+// of 8192: 71, 81, 78.
 constexpr int kRowsAhead = 4 * 152;
 
 template <typename T, int WPR, int NV>
@@ -270,13 +274,19 @@ __global__ void __launch_bounds__(32 * kBlockWarps<WPR>, (NV * Piece<T>::N <= 16
 // warps, 2048 columns, k = 4: 192 us, not 115), and leave once, as one partial row per team and sum; norm_join_kernel adds
 // these in order.  Up to eight columns are kept in registers.  There are two sums: with G = sum_t rp dh . y,
 //   dgate = alpha post_w . G,   dpost_w = alpha gate . G,        and   dnext_w = sum_t rn dnormed . h.
-constexpr int kBackWarps = 24;                   // of a row pass on an SM (16: 107 and 284 us for 8191 x 2048, k = 4, and
-                                                 // 16384 x 3584, k = 2; 24: 104, 230; 32, 64 registers: 114, 218)
+//
+// Warps of a row pass on an SM: 24, and of rows that take 16 warps two teams where a thread has two pieces of a row (with 64
+// registers; four pieces need more).  us with 16, 24, 32: f16, 512 columns, k = 4: 125, 125, 146; 1024, k = 2: 85, 77, 81;
+// 1024, k = 8: 376, 364, 391; 2048, k = 4: 127, 125, 138; 2048, k = 2: 147, 127, 128; 3584: 296, 248, 234; 4096: 175, 159, 169;
+// f32, 1024: 70, 60, 63; 2048: 221, 219, 228.  One team or two of 16 warps: f16, 8192: 189, 155; f32, 4096: 146, 117; f32, 8192
+// (four pieces): 150, 174.
+template <int WPR, int NV>
+constexpr int kBackWarps = WPR < 16 ? 24 : NV == 2 ? 32 : 16;
 template <typename T, int NV>
 constexpr bool kSumsInSmem = NV * Piece<T>::N > 8;
 
 template <typename T, int WPR, int NV>
-__global__ void __launch_bounds__(32 * kBlockWarps<WPR>, (NV * Piece<T>::N <= 16 ? kBackWarps : 16) / kBlockWarps<WPR>)
+__global__ void __launch_bounds__(32 * kBlockWarps<WPR>, kBackWarps<WPR, NV> / kBlockWarps<WPR>)
     block_norm_backward_kernel(const NormArgs a, const NormGrads b, int teams) {
   constexpr int N = Piece<T>::N, H = N / 2, TPB = kBlockWarps<WPR> / WPR;
   constexpr bool kSmem = kSumsInSmem<T, NV>;
@@ -535,8 +545,9 @@ cudaError_t with_team(int d, F f) {
 
 // Teams of the backward pass: kBackWarps for each of 152 SMs, fewer where the sums of more would not fit shared memory.
 int norm_teams(int T, int d, bool f16) {
-  const int w = warps_for(d, f16), per_sm = std::max(1, std::min(kBackWarps / w, 200 * 1024 / (8 * d)));
-  return std::min(T, 152 * per_sm);
+  const int w = warps_for(d, f16), pieces = d / (f16 ? 8 : 4);
+  const int warps = w < 16 ? kBackWarps<1, 1> : pieces <= 1024 ? kBackWarps<16, 2> : kBackWarps<16, 4>;
+  return std::min(T, 152 * std::max(1, std::min(warps / w, 200 * 1024 / (8 * d))));
 }
 
 cudaError_t launch_block_norm(const NormArgs& a, bool f16, cudaStream_t s) {

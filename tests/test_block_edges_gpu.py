@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import test_block_gpu
 from test_block_gpu import check, experts8, gen, half, norm_inputs, randn, ref_ffn8, rows8, values8
 
 pytestmark = pytest.mark.gpu
@@ -216,3 +217,10 @@ def test_one_scale_that_is_no_power_of_two(m, which, factor):
             w2[128:256] = 0.0
         want, tol = ref_ffn8(x[rows], w1, w2, d, f)
         check(out[rows][:, cols], want[:, cols], (tol + half(F16) * want.abs() + 2.0 ** -25)[:, cols], f"expert {e}")
+
+
+@pytest.mark.parametrize("T,d,k,dtype", [(2500, 1024, 2, F16), (700, 4104, 1, F16), (700, 8192, 2, F16), (500, 8200, 1, F16),
+                                         (700, 2560, 2, torch.float32), (500, 4100, 1, torch.float32), (900, 520, 3, torch.float32)])
+def test_gradients_where_each_team_has_several_rows(m, T, d, k, dtype):
+    """Every width of a team, two of them to a block, and sums over tokens of more rows than there are teams."""
+    test_block_gpu.test_block_norm_gradient(m, T, d, k, dtype, "spg", "hn")
