@@ -12,8 +12,9 @@
 // one to a lane and ranked against each other.  (Rounds of two warp-wide reductions and a pass over a lane's values,
 // which still serve rows of many equal keys, took 1320 instructions a row of 256 experts in groups, k = 8: the integer
 // pipe 68 % busy.)  A lane has V neighbouring columns where a row is 32 V of them (their loads are wide, and groups of
-// whole lanes need no shared memory), else every 32nd.  Bound by instructions, not by the 4 E bytes of a row: 16384 rows
-// of 256, k = 8: 19 us by the logits alone, 23 with a bias, 29 with a bias and groups (rounds: 22, 28, 42).
+// whole lanes need no shared memory), else every 32nd.  Bound by a warp's chain of dependent
+// shuffles and ranks (no pipe above half, half of the warps resident), not by the 4 E bytes of a row: 16384 rows of 256,
+// k = 8: 19 us by the logits alone, 23 with a bias, 27 with a bias and groups, cold (rounds: 22, 28, 42).
 #include <type_traits>
 
 #include "launch.h"
